@@ -413,6 +413,47 @@ ssm_status_t ssm_scan_bwd_initial_state(const float* dt, const float* A, const v
                                         ssm_dtype_t dtype, ssm_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------
+ * ssm_norm_fwd / ssm_norm_bwd -- RMS or layer norm of rows of channels with an optional SiLU
+ * gate: the norm between a layer's scan and its output projection (gate before or after), or
+ * a plain pre-norm (z NULL).  Per row and group of m = channels / ngroups channels:
+ *     u = x silu(z) (gate before the norm) or x
+ *     n = (u - mean) / sqrt(mean((u - mean)^2) + eps),   mean = 0 for SSM_NORM_RMS
+ *     out = n w + b, times silu(z) when norm_before_gate
+ * Statistics and sums in fp32; outputs rounded once.  The backward recomputes the statistics
+ * from x and z (nothing is kept from the forward) and gives, from dout = dL/d(out), dx, dz and
+ * the sums over the rows dweight, dbias (fixed summation order: deterministic).
+ *
+ *   x, z, dout, out, dx, dz  rows of `channels` consecutive elements, dtype; row r at
+ *                  p + r * p_row elements (z may be a channel range of a wider projection);
+ *                  input rows may repeat (p_row >= 0), output rows may not (p_row >= channels)
+ *   z              or NULL (no gate; then dz and norm_before_gate are ignored)
+ *   weight, bias   [channels] fp32, or NULL (= 1, = 0)
+ *   dz             or NULL (not written)
+ *   dweight, dbias [channels] fp32, or NULL (not written)
+ *   workspace      ssm_norm_bwd_workspace_size bytes, 4-byte aligned (partial sums; not needed
+ *                  when dweight and dbias are both NULL)
+ * channels / ngroups <= 16384; eps >= 0.  Outputs must not overlap inputs.  rows = 0: out, dx
+ * and dz have no elements, dweight = dbias = 0.  Rows whose pointers and strides are 16-byte
+ * multiples (and channels / ngroups a multiple of 8) use 16-byte accesses, others element
+ * accesses; the results agree to rounding.
+ * ------------------------------------------------------------------------------------- */
+enum { SSM_NORM_RMS = 0, SSM_NORM_LAYER = 1 };
+typedef int32_t ssm_norm_t;
+ssm_status_t ssm_norm_fwd(const void* x, int64_t x_row, const void* z, int64_t z_row,
+                          const float* weight, const float* bias, void* out, int64_t out_row,
+                          int64_t rows, int64_t channels, int64_t ngroups, float eps,
+                          ssm_norm_t kind, int32_t norm_before_gate, ssm_dtype_t dtype,
+                          ssm_stream_t stream);
+size_t ssm_norm_bwd_workspace_size(int64_t rows, int64_t channels, int64_t ngroups);
+ssm_status_t ssm_norm_bwd(const void* x, int64_t x_row, const void* z, int64_t z_row,
+                          const void* dout, int64_t dout_row, const float* weight,
+                          const float* bias, void* dx, int64_t dx_row, void* dz, int64_t dz_row,
+                          float* dweight, float* dbias, void* workspace, size_t workspace_bytes,
+                          int64_t rows, int64_t channels, int64_t ngroups, float eps,
+                          ssm_norm_t kind, int32_t norm_before_gate, ssm_dtype_t dtype,
+                          ssm_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
  * Initial-state distributions for training ([LG] Sec. 2.6: the four interventions -- Random
  * Noise, Fitted Noise, State Passing, TBTT -- and the Fitted Noise update, Eqs. (5)-(6)).
  * Random numbers: Philox4x64-10 (Salmon, Moraes, Dror, Shaw, "Parallel random numbers: as

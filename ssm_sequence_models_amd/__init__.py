@@ -102,6 +102,13 @@ def _load():
     lib.ssm_initial_state_noise.argtypes = [fp, i64, i64, i64, i64, fp, fp, ctypes.c_float, u64,
                                             u64, vp]
     lib.ssm_state_reset.argtypes = [vp, vp, vp, i64, i64, ctypes.c_double, u64, u64, vp]
+    cf, sz = ctypes.c_float, ctypes.c_size_t
+    lib.ssm_norm_fwd.argtypes = [vp, i64, vp, i64, fp, fp, vp, i64, i64, i64, i64, cf, ci, ci, ci,
+                                 vp]
+    lib.ssm_norm_bwd_workspace_size.restype = sz
+    lib.ssm_norm_bwd_workspace_size.argtypes = [i64, i64, i64]
+    lib.ssm_norm_bwd.argtypes = [vp, i64, vp, i64, vp, i64, fp, fp, vp, i64, vp, i64, fp, fp, vp,
+                                 sz, i64, i64, i64, cf, ci, ci, ci, vp]
     lib.ssm_stream_copy.argtypes = [vp, vp, i64, vp]
     lib.ssm_timing_enable.argtypes = [ci]
     lib.ssm_timing_read.argtypes = [ctypes.POINTER(ctypes.c_double),
@@ -109,7 +116,8 @@ def _load():
     for f in ("ssm_conv1d_fwd", "ssm_conv1d_update", "ssm_scan_fwd", "ssm_conv_scan_fwd",
               "ssm_conv_scan_fwd_noalloc", "ssm_step", "ssm_decode_step", "ssm_conv1d_bwd", "ssm_scan_bwd_initial_state",
               "ssm_conv_scan_fwd_pooled", "ssm_state_stats_update", "ssm_scan_fwd_vector_decay",
-              "ssm_initial_state_noise", "ssm_state_reset", "ssm_stream_copy",
+              "ssm_initial_state_noise", "ssm_state_reset", "ssm_stream_copy", "ssm_norm_fwd",
+              "ssm_norm_bwd",
               "ssm_timing_enable", "ssm_timing_read"):
         getattr(lib, f).restype = ci
     return lib
@@ -154,6 +162,35 @@ def _need(t, name, dtype=None, shape=None, contiguous=True):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _need_device(ref, **tensors):
+    """Every given tensor lives on ref's device (the call is made on that device's current
+    stream)."""
+    for name, t in tensors.items():
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{name} must be on {ref.device}, got {t.device}")
+
+
+def _rows(t, name, channels):
+    """(rows, row stride) of t [..., channels]: its last dimension consecutive, the leading
+    ones at one stride."""
+    if t.dim() < 1 or t.shape[-1] != channels:
+        raise ValueError(f"{name} must have {channels} channels, got shape {tuple(t.shape)}")
+    if t.is_contiguous():
+        return t.numel() // channels, channels
+    if channels > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have consecutive channels")
+    rows, row = 1, None
+    for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if row is None:
+            row = s
+        elif s != row * rows:
+            raise ValueError(f"{name} must have its rows at one stride")
+        rows *= n
+    return rows, channels if row is None else row
 
 
 def workspace_size(batch, seqlen, nheads, headdim, ngroups, dstate, dtype=torch.bfloat16) -> int:
@@ -589,6 +626,82 @@ def decode_step(x_new, conv_state, conv_weight, conv_bias, dt, A, ssm_state, nhe
         _ptr(state_indices), _ptr(conv_out), _ptr(y), bsz, n_new, H, P, G, N, K, state_len,
         n_cslots, ssm_state.shape[0], _dtype_code(x_new), ACT[activation], _stream()))
     return y
+
+
+NORM = {"rms": 0, "layer": 1}
+
+
+def _norm_args(x, weight, bias, z, kind, ngroups):
+    """Checks shared by norm_fwd and norm_bwd; returns (channels, rows, x_row, z_row)."""
+    if kind not in NORM:
+        raise ValueError(f"kind must be one of {sorted(NORM)}, got {kind!r}")
+    if x.dim() < 1:
+        raise ValueError("x must be [..., channels]")
+    C = x.shape[-1]
+    if ngroups < 1 or C < 1 or C % ngroups != 0:
+        raise ValueError(f"channels {C} must be a positive multiple of ngroups {ngroups}")
+    _need(x, "x", contiguous=False)
+    _need(weight, "weight", torch.float32, (C,))
+    _need(bias, "bias", torch.float32, (C,))
+    _need(z, "z", x.dtype, x.shape, contiguous=False)
+    _need_device(x, weight=weight, bias=bias, z=z)
+    rows, x_row = _rows(x, "x", C)
+    return C, rows, x_row, 0 if z is None else _rows(z, "z", C)[1]
+
+
+def norm_fwd(x, weight=None, bias=None, z=None, eps=1e-5, kind="rms", ngroups=1,
+             norm_before_gate=False, out=None):
+    """RMS (kind "rms") or layer (kind "layer") norm of x [..., channels] over ngroups groups of
+    channels, times weight [channels] fp32, plus bias; z [..., channels] gates with silu(z),
+    before the norm or (norm_before_gate) after it.  x, z and out: consecutive channels, rows at
+    any one stride.  Returns out [..., channels] (x's dtype)."""
+    C, rows, x_row, z_row = _norm_args(x, weight, bias, z, kind, ngroups)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _need(out, "out", x.dtype, x.shape, contiguous=False)
+    _need_device(x, out=out)
+    with torch.cuda.device(x.device):
+        _check("ssm_norm_fwd", _lib.ssm_norm_fwd(
+            _ptr(x), x_row, _ptr(z), z_row, _ptr(weight), _ptr(bias), _ptr(out),
+            _rows(out, "out", C)[1], rows, C, ngroups, eps, NORM[kind], int(norm_before_gate),
+            _dtype_code(x), _stream()))
+    return out
+
+
+def norm_bwd_workspace_size(rows, channels, ngroups=1) -> int:
+    return int(_lib.ssm_norm_bwd_workspace_size(rows, channels, ngroups))
+
+
+def norm_bwd(x, weight, dout, bias=None, z=None, eps=1e-5, kind="rms", ngroups=1,
+             norm_before_gate=False, dx=None, dz=None, dweight=None, dbias=None, workspace=None):
+    """Backward of norm_fwd from dout [..., channels]: the statistics are recomputed from x and
+    z.  Returns (dx, dz or None without z, dweight [channels] fp32, dbias [channels] fp32 or
+    None without bias)."""
+    C, rows, x_row, z_row = _norm_args(x, weight, bias, z, kind, ngroups)
+    _need(dout, "dout", x.dtype, x.shape, contiguous=False)
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if z is None and dz is not None:
+        raise ValueError("dz given without z")
+    if z is not None and dz is None:
+        dz = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if dweight is None:
+        dweight = torch.empty(C, dtype=torch.float32, device=x.device)
+    if bias is not None and dbias is None:
+        dbias = torch.empty(C, dtype=torch.float32, device=x.device)
+    _need(dx, "dx", x.dtype, x.shape, contiguous=False)
+    _need(dz, "dz", x.dtype, x.shape, contiguous=False)
+    _need(dweight, "dweight", torch.float32, (C,))
+    _need(dbias, "dbias", torch.float32, (C,))
+    _need_device(x, dout=dout, dx=dx, dz=dz, dweight=dweight, dbias=dbias, workspace=workspace)
+    ws, wsb = _workspace(workspace, norm_bwd_workspace_size(rows, C, ngroups), x.device)
+    with torch.cuda.device(x.device):
+        _check("ssm_norm_bwd", _lib.ssm_norm_bwd(
+            _ptr(x), x_row, _ptr(z), z_row, _ptr(dout), _rows(dout, "dout", C)[1], _ptr(weight),
+            _ptr(bias), _ptr(dx), _rows(dx, "dx", C)[1], _ptr(dz),
+            0 if dz is None else _rows(dz, "dz", C)[1], _ptr(dweight), _ptr(dbias), _ptr(ws), wsb,
+            rows, C, ngroups, eps, NORM[kind], int(norm_before_gate), _dtype_code(x), _stream()))
+    return dx, dz, dweight, dbias
 
 
 def stream_copy(src, dst):

@@ -882,6 +882,136 @@ ssm_status_t ssm_scan_bwd_initial_state(const float* dt, const float* A, const v
 }
 
 namespace {
+
+ssm_status_t check_norm_dims(const char* fn, int64_t rows, int64_t channels, int64_t ngroups,
+                             float eps, int32_t kind, int dtype) {
+    if (!valid_dtype(dtype)) return fail(SSM_ERR_INVALID_ARG, std::string(fn) + ": bad dtype");
+    if (kind != SSM_NORM_RMS && kind != SSM_NORM_LAYER)
+        return fail(SSM_ERR_INVALID_ARG, std::string(fn) + ": bad norm kind");
+    if (rows < 0 || channels < 1 || ngroups < 1 || channels % ngroups != 0)
+        return fail(SSM_ERR_INVALID_ARG, std::string(fn) + ": need rows >= 0 and channels a positive multiple of ngroups");
+    if (!(eps >= 0.0f)) return fail(SSM_ERR_INVALID_ARG, std::string(fn) + ": eps must be >= 0");
+    if (channels / ngroups > 16384)
+        return fail(SSM_ERR_UNSUPPORTED, std::string(fn) + ": channels / ngroups must be <= 16384");
+    if (ngroups > 0x7FFFFFFF || channels > (int64_t{1} << 36))
+        return fail(SSM_ERR_UNSUPPORTED, std::string(fn) + ": too many channels");
+    return SSM_OK;
+}
+ssm_status_t check_row(const char* fn, const char* name, const void* p, int64_t row, int64_t rows,
+                       int64_t least) {
+    if (p == nullptr || rows <= 1 || row >= least) return SSM_OK;
+    return fail(SSM_ERR_INVALID_ARG, std::string(fn) + ": " + name + " row stride below " + std::to_string(least));
+}
+
+}  // namespace
+
+ssm_status_t ssm_norm_fwd(const void* x, int64_t x_row, const void* z, int64_t z_row,
+                          const float* weight, const float* bias, void* out, int64_t out_row,
+                          int64_t rows, int64_t channels, int64_t ngroups, float eps,
+                          ssm_norm_t kind, int32_t norm_before_gate, ssm_dtype_t dtype,
+                          ssm_stream_t stream) {
+    const char* fn = "ssm_norm_fwd";
+    ssm_status_t st = check_norm_dims(fn, rows, channels, ngroups, eps, kind, dtype);
+    if (st != SSM_OK) return st;
+    const size_t es = esize(dtype);
+    const bool work = rows > 0;
+    st = check_ptrs(fn, {{"x", x, work, es},
+                         {"z", z, false, es},
+                         {"weight", weight, false, 4},
+                         {"bias", bias, false, 4},
+                         {"out", out, work, es}});
+    if (st == SSM_OK) st = check_row(fn, "x", x, x_row, rows, 0);
+    if (st == SSM_OK) st = check_row(fn, "z", z, z_row, rows, 0);
+    if (st == SSM_OK) st = check_row(fn, "out", out, out_row, rows, channels);
+    if (st != SSM_OK) return st;
+    if (!work) return ok();
+    ssm::NormCall c{};
+    c.x = x;
+    c.x_row = x_row;
+    c.z = z;
+    c.z_row = z_row;
+    c.w = weight;
+    c.b = bias;
+    c.out = out;
+    c.out_row = out_row;
+    c.rows = rows;
+    c.channels = channels;
+    c.groups = ngroups;
+    c.eps = eps;
+    c.layer = kind == SSM_NORM_LAYER;
+    c.gate_after = norm_before_gate != 0;
+    c.dtype = dtype;
+    return hip_status(ssm::launch_norm_fwd(c, reinterpret_cast<hipStream_t>(stream)), fn);
+}
+
+size_t ssm_norm_bwd_workspace_size(int64_t rows, int64_t channels, int64_t ngroups) {
+    if (rows <= 0 || channels < 1 || ngroups < 1 || channels % ngroups != 0) return 0;
+    return static_cast<size_t>(2 * ssm::norm_partial_rows(rows, channels, ngroups) * channels) * 4;
+}
+
+ssm_status_t ssm_norm_bwd(const void* x, int64_t x_row, const void* z, int64_t z_row,
+                          const void* dout, int64_t dout_row, const float* weight,
+                          const float* bias, void* dx, int64_t dx_row, void* dz, int64_t dz_row,
+                          float* dweight, float* dbias, void* workspace, size_t workspace_bytes,
+                          int64_t rows, int64_t channels, int64_t ngroups, float eps,
+                          ssm_norm_t kind, int32_t norm_before_gate, ssm_dtype_t dtype,
+                          ssm_stream_t stream) {
+    const char* fn = "ssm_norm_bwd";
+    ssm_status_t st = check_norm_dims(fn, rows, channels, ngroups, eps, kind, dtype);
+    if (st != SSM_OK) return st;
+    const size_t es = esize(dtype);
+    const bool work = rows > 0;
+    if (z == nullptr) dz = nullptr;
+    st = check_ptrs(fn, {{"x", x, work, es},
+                         {"z", z, false, es},
+                         {"dout", dout, work, es},
+                         {"weight", weight, false, 4},
+                         {"bias", bias, false, 4},
+                         {"dx", dx, work, es},
+                         {"dz", dz, false, es},
+                         {"dweight", dweight, false, 4},
+                         {"dbias", dbias, false, 4},
+                         {"workspace", workspace, false, 4}});
+    if (st == SSM_OK) st = check_row(fn, "x", x, x_row, rows, 0);
+    if (st == SSM_OK) st = check_row(fn, "z", z, z_row, rows, 0);
+    if (st == SSM_OK) st = check_row(fn, "dout", dout, dout_row, rows, 0);
+    if (st == SSM_OK) st = check_row(fn, "dx", dx, dx_row, rows, channels);
+    if (st == SSM_OK) st = check_row(fn, "dz", dz, dz_row, rows, channels);
+    if (st != SSM_OK) return st;
+    if (work && (dweight || dbias)) {
+        const size_t need = ssm_norm_bwd_workspace_size(rows, channels, ngroups);
+        if (workspace == nullptr || workspace_bytes < need)
+            return fail(SSM_ERR_WORKSPACE, "ssm_norm_bwd: workspace missing or smaller than "
+                                           "ssm_norm_bwd_workspace_size");
+    }
+    if (!work && !dweight && !dbias) return ok();
+    ssm::NormCall c{};
+    c.x = x;
+    c.x_row = x_row;
+    c.z = z;
+    c.z_row = z_row;
+    c.dout = dout;
+    c.dout_row = dout_row;
+    c.w = weight;
+    c.b = bias;
+    c.dx = dx;
+    c.dx_row = dx_row;
+    c.dz = dz;
+    c.dz_row = dz_row;
+    c.dw = dweight;
+    c.db = dbias;
+    c.workspace = workspace;
+    c.rows = rows;
+    c.channels = channels;
+    c.groups = ngroups;
+    c.eps = eps;
+    c.layer = kind == SSM_NORM_LAYER;
+    c.gate_after = norm_before_gate != 0;
+    c.dtype = dtype;
+    return hip_status(ssm::launch_norm_bwd(c, reinterpret_cast<hipStream_t>(stream)), fn);
+}
+
+namespace {
 ssm_status_t check_state_dims(const char* fn, int64_t batch, int64_t nheads, int64_t headdim,
                               int64_t dstate) {
     if (batch < 0) return fail(SSM_ERR_INVALID_ARG, std::string(fn) + ": negative batch");

@@ -236,6 +236,28 @@ hipError_t launch_scan_bwd_h0(const float* dt, const float* A, const void* Cm,
                               int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim,
                               int64_t ngroups, int64_t dstate, ssm_dtype_t dtype,
                               hipStream_t stream);
+// RMS / layer norm with a SiLU gate; rows of `channels` elements at the given row strides
+struct NormCall {
+    const void* x;
+    const void* z;     // NULL: no gate
+    const void* dout;
+    const float* w;    // NULL: ones
+    const float* b;    // NULL: zeros
+    void* out;
+    void* dx;
+    void* dz;          // NULL: not written
+    float* dw;         // NULL: not written
+    float* db;         // NULL: not written
+    void* workspace;   // 2 x norm_partial_rows x channels floats when dw or db is asked for
+    int64_t x_row, z_row, dout_row, out_row, dx_row, dz_row;
+    int64_t rows, channels, groups;
+    float eps;
+    bool layer, gate_after;
+    ssm_dtype_t dtype;
+};
+int64_t norm_partial_rows(int64_t rows, int64_t channels, int64_t groups);
+hipError_t launch_norm_fwd(const NormCall& c, hipStream_t stream);
+hipError_t launch_norm_bwd(const NormCall& c, hipStream_t stream);
 hipError_t launch_pool_gather(const void* conv_pool, const float* ssm_pool, const int32_t* indices,
                               const int32_t* seqlens, void* conv_hist, float* ssm_init,
                               int64_t batch, int64_t C, int64_t K, int64_t state_len,

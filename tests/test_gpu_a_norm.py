@@ -1,0 +1,218 @@
+"""GPU parity of ssm_norm_fwd / ssm_norm_bwd against the plain form in 64 bits.
+
+Bounds: every output is rounded once to its type (half a step of it), after fp32 arithmetic.
+A value of the forward passes at most a dozen fp32 roundings besides the reductions: SiLU by
+the hardware exp and reciprocal (below (7 + 3|z|) half-steps), products, the square root and
+division, and a reduction as a tree over at most 16 register values, 6 lane steps and 16
+waves, two of them (mean and squares), below 2 (16 + 6 + 16) half-steps in all; together
+below 128 half-steps of the magnitudes that make the value up.  dw and db add the rows of one
+thread one after the other: rows more half-steps.
+"""
+import itertools
+
+import pytest
+import torch
+
+from train_ref import U, assert_bound, half_step, norm64
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+K_ARITH = 128 * U
+
+
+def _inputs(rows, C, gate, bias, dtype, seed, shift=0.0):
+    g = torch.Generator().manual_seed(seed)
+    x = (torch.randn(rows, C, generator=g) + shift).to(dtype)
+    w = 1.0 + 0.25 * torch.randn(C, generator=g)
+    b = 0.5 * torch.randn(C, generator=g) if bias else None
+    z = (2.0 * torch.randn(rows, C, generator=g)).to(dtype) if gate != "none" else None
+    d = torch.randn(rows, C, generator=g).to(dtype)
+    return x, w, b, z, d
+
+
+def _check(got, ref, name, dtype, extra=0):
+    h = half_step(dtype)
+    bound = h * ref[name].abs() + (K_ARITH + extra * U) * (1 + h) * ref[name + "_mag"] + 1e-30
+    assert_bound(got, ref[name], bound, name)
+
+
+def _run(x, w, b, z, d, kind, groups, gate, eps=1e-5, dev=None):
+    import ssm_sequence_models_amd as ssm
+    c = lambda t: None if t is None else t.to("cuda")  # noqa: E731
+    how = dict(bias=c(b), z=dev if dev is not None else c(z), eps=eps, kind=kind, ngroups=groups,
+               norm_before_gate=gate == "after")
+    out = ssm.norm_fwd(c(x), c(w), **how)
+    dx, dz, dw, db = ssm.norm_bwd(c(x), c(w), c(d), **how)
+    torch.cuda.synchronize()
+    ref = norm64(x, w, b, z, eps, kind, groups, gate == "after", d)
+    dt = x.dtype
+    _check(out, ref, "out", dt)
+    _check(dx, ref, "dx", dt)
+    if gate != "none":
+        _check(dz, ref, "dz", dt)
+    else:
+        assert dz is None
+    _check(dw, ref, "dw", F32, extra=x.shape[0])
+    if b is not None:
+        _check(db, ref, "db", F32, extra=x.shape[0])
+    else:
+        assert db is None
+
+
+# one width on each side of every change of layout, vector (multiples of 8) and element access
+WIDTHS = [1, 7, 8, 64, 511, 512, 513, 520, 1537, 2048, 2056, 2049, 4096, 4104, 8192, 8200, 8193, 16384]
+
+
+@pytest.mark.parametrize("C", WIDTHS)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_widths(C, dtype):
+    for i, (kind, gate) in enumerate(itertools.product(["rms", "layer"], ["none", "before", "after"])):
+        x, w, b, z, d = _inputs(5, C, gate, i % 2 == 0, dtype, seed=C + i)
+        _run(x, w, b, z, d, kind, 1, gate)
+
+
+@pytest.mark.parametrize("rows", [1, 2, 3, 4, 5, 255, 1030, 4100])
+@pytest.mark.parametrize("C,groups", [(24, 3), (1024, 2), (560, 1)])
+def test_rows_and_groups(rows, C, groups):
+    for gate, kind in (("before", "rms"), ("after", "layer")):
+        x, w, b, z, d = _inputs(rows, C, gate, True, BF16, seed=rows + C)
+        _run(x, w, b, z, d, kind, groups, gate)
+
+
+def test_many_groups():
+    x, w, b, z, d = _inputs(3, 1100 * 4, "before", False, F32, seed=3)
+    _run(x, w, b, z, d, "rms", 1100, "before")
+
+
+def test_large_mean():
+    """Rows far from zero: the layer norm's two steps keep the deviation."""
+    x, w, b, z, d = _inputs(9, 768, "none", True, F32, seed=5, shift=1000.0)
+    _run(x, w, b, z, d, "layer", 1, "none")
+
+
+def test_extreme_gates():
+    """SiLU at gates where exp(-z) overflows or vanishes is 0 or z, its derivative 0 or 1."""
+    x, w, b, z, d = _inputs(6, 256, "after", True, F32, seed=6)
+    z[0], z[1], z[2], z[3] = -200.0, 200.0, 0.0, -88.7
+    _run(x, w, b, z, d, "rms", 1, "after")
+    _run(x, w, b, z, d, "rms", 1, "before", eps=1e-3)
+
+
+def test_zero_rows_of_values():
+    """A row of zeros: n = 0 / sqrt(eps)."""
+    x, w, b, z, d = _inputs(4, 96, "none", True, BF16, seed=7)
+    x[1] = 0
+    _run(x, w, b, z, d, "layer", 2, "none")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("off,pad", [(0, 64), (8, 24), (3, 17), (1, 0)])
+def test_strided_rows(dtype, off, pad):
+    """z as a channel range of a wider projection (aligned and odd offsets and strides), x as
+    every second row, outputs into ranges of wider rows; what lies beside them stays."""
+    import ssm_sequence_models_amd as ssm
+    rows, C = 37, 264
+    x, w, b, z, d = _inputs(rows, C, "before", True, dtype, seed=off + pad)
+    wide = torch.full((rows, off + C + pad), 7.0, dtype=dtype)
+    wide[:, off:off + C] = z
+    xw = torch.zeros(rows, 2, C, dtype=dtype)
+    xw[:, 0] = x
+    xg, zg = xw.cuda()[:, 0], wide.cuda()[:, off:off + C]
+    ref = norm64(x, w, b, z, 1e-5, "rms", 3, False, d)
+    buf = {k: torch.full((rows, off + C + pad), 5.0, dtype=dtype, device="cuda") for k in ("out", "dx", "dz")}
+    v = {k: t[:, off:off + C] for k, t in buf.items()}
+    how = dict(bias=b.cuda(), z=zg, kind="rms", ngroups=3)
+    ssm.norm_fwd(xg, w.cuda(), out=v["out"], **how)
+    ssm.norm_bwd(xg, w.cuda(), d.cuda(), dx=v["dx"], dz=v["dz"], **how)
+    torch.cuda.synchronize()
+    for k in v:
+        _check(v[k], ref, k, dtype)
+        keep = torch.ones(off + C + pad, dtype=torch.bool)
+        keep[off:off + C] = False
+        assert (buf[k].cpu()[:, keep] == 5.0).all(), f"{k}: wrote beside its rows"
+
+
+def test_leading_dimensions_and_repeated_rows():
+    """[b, t, C] inputs, a broadcast (stride 0) gate row, no weight."""
+    import ssm_sequence_models_amd as ssm
+    x, _, _, z, d = _inputs(12, 128, "after", False, F32, seed=11)
+    zr = z[:1].cuda().expand(12, 128)
+    out = ssm.norm_fwd(x.cuda().view(3, 4, 128), z=zr.reshape(3, 4, 128),
+                       norm_before_gate=True)
+    rep = ssm.norm_fwd(x.cuda(), z=zr, norm_before_gate=True)
+    ref = norm64(x, None, None, z[:1].expand(12, 128), 1e-5, "rms", 1, True)
+    _check(out.view(12, 128), ref, "out", F32)
+    assert torch.equal(out.view(12, 128), rep)
+
+
+def test_no_rows():
+    import ssm_sequence_models_amd as ssm
+    x = torch.empty(0, 32, device="cuda")
+    w = torch.ones(32, device="cuda")
+    assert ssm.norm_fwd(x, w).shape == (0, 32)
+    dx, dz, dw, db = ssm.norm_bwd(x, w, x, bias=w)
+    torch.cuda.synchronize()
+    assert dx.shape == (0, 32) and float(dw.abs().max()) == 0 and float(db.abs().max()) == 0
+
+
+def test_gradient_against_differences():
+    """<gradient, v> against the central difference of the 64-bit loss along v.  The third
+    derivative along v leaves h^2 / 6 times it (h = 1e-4: below 1e-6 of these O(1) losses)."""
+    import ssm_sequence_models_amd as ssm
+    for kind, gate in itertools.product(["rms", "layer"], ["before", "after"]):
+        x, w, b, z, d = _inputs(6, 40, gate, True, F32, seed=21)
+        how = dict(kind=kind, ngroups=2, norm_before_gate=gate == "after")
+        dx, dz, dw, db = ssm.norm_bwd(x.cuda(), w.cuda(), d.cuda(), bias=b.cuda(), z=z.cuda(), **how)
+        g = torch.Generator().manual_seed(5)
+        for t, grad, i in ((x, dx, 0), (w, dw, 1), (b, db, 2), (z, dz, 3)):
+            v = torch.randn(t.shape, generator=g, dtype=torch.float64)
+
+            def loss(e):
+                args = [q.double() for q in (x, w, b, z)]
+                args[i] = args[i] + e * v
+                return float((norm64(*args, 1e-5, kind, 2, gate == "after")["out"] * d.double()).sum())
+            h = 1e-4
+            diff = (loss(h) - loss(-h)) / (2 * h)
+            dot = float((grad.cpu().double() * v).sum())
+            scale = float((grad.cpu().double() * v).abs().sum())
+            assert abs(diff - dot) <= 1e-5 * scale + 1e-5, (kind, gate, i, diff, dot)
+
+
+def test_deterministic_and_graph_replay():
+    """The same bits from every run, and from every replay of a captured graph with eager calls
+    between the replays."""
+    import ssm_sequence_models_amd as ssm
+    x, w, b, z, d = (t.cuda() for t in _inputs(300, 1024, "before", True, BF16, seed=31))
+    how = dict(bias=b, z=z, kind="layer", ngroups=2)
+    want = (ssm.norm_fwd(x, w, **how), *ssm.norm_bwd(x, w, d, **how))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        ssm.norm_bwd(x, w, d, **how)
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = (ssm.norm_fwd(x, w, **how), *ssm.norm_bwd(x, w, d, **how))
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        eager = ssm.norm_bwd(x, w, d, **how)
+        torch.cuda.synchronize()
+        for a, c in zip(got, want):
+            assert torch.equal(a, c)
+        for a, c in zip(eager, want[1:]):
+            assert torch.equal(a, c)
+
+
+def test_another_stream():
+    import ssm_sequence_models_amd as ssm
+    x, w, b, z, d = (t.cuda() for t in _inputs(64, 512, "before", True, F32, seed=41))
+    want = ssm.norm_bwd(x, w, d, bias=b, z=z)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        got = ssm.norm_bwd(x, w, d, bias=b, z=z)
+    s.synchronize()
+    for a, c in zip(got, want):
+        assert torch.equal(a, c)

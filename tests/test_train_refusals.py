@@ -1,0 +1,109 @@
+"""Refusals of the training operators, on the CPU: status codes of the C entry points for
+arguments that fail their host-side checks (no call reaches a launch), and the 64-bit plain
+forms against differences."""
+import ctypes
+
+import pytest
+import torch
+
+from train_ref import norm64
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import ssm_sequence_models_amd as s
+    return s._lib
+
+
+P = ctypes.c_void_p(256)
+ODD = ctypes.c_void_p(257)
+F = ctypes.c_float
+
+
+def _norm_fwd(lib, x=P, x_row=64, z=None, z_row=64, w=P, b=None, out=P, out_row=64, rows=2, C=64,
+              g=1, eps=1e-5, kind=0, after=0, dtype=1):
+    return lib.ssm_norm_fwd(x, x_row, z, z_row, w, b, out, out_row, rows, C, g, F(eps), kind, after,
+                            dtype, None)
+
+
+def _norm_bwd(lib, x=P, x_row=64, z=None, z_row=64, d=P, d_row=64, w=P, b=None, dx=P, dx_row=64,
+              dz=None, dz_row=64, dw=P, db=None, ws=P, wsb=1 << 30, rows=2, C=64, g=1, eps=1e-5,
+              kind=0, after=0, dtype=1):
+    return lib.ssm_norm_bwd(x, x_row, z, z_row, d, d_row, w, b, dx, dx_row, dz, dz_row, dw, db, ws,
+                            wsb, rows, C, g, F(eps), kind, after, dtype, None)
+
+
+@pytest.mark.parametrize("call", [_norm_fwd, _norm_bwd])
+def test_norm_refusals(lib, call):
+    for status, how in ((1, dict(dtype=7)), (1, dict(kind=2)), (1, dict(kind=-1)), (1, dict(rows=-1)),
+                        (1, dict(C=0)), (1, dict(g=0)), (1, dict(g=3)), (1, dict(eps=-1.0)),
+                        (1, dict(eps=float("nan"))), (2, dict(C=16392)), (1, dict(x=None)),
+                        (3, dict(x=ODD)), (3, dict(w=ODD)), (3, dict(z=ODD)), (1, dict(x_row=-64)),
+                        (1, dict(z=P, z_row=-1))):
+        assert call(lib, **how) == status, how
+        assert lib.ssm_last_error()
+    # a group of 16384 is the largest; rows = 0 is a no-op that needs no pointers
+    if call is _norm_fwd:
+        assert call(lib, out=None) == 1
+        assert call(lib, out_row=63) == 1
+        assert call(lib, x=None, out=None, rows=0) == 0
+    else:
+        assert call(lib, dx=None) == 1
+        assert call(lib, d=None) == 1
+        assert call(lib, dx_row=63) == 1
+        assert call(lib, z=P, dz=P, dz_row=63) == 1
+        assert call(lib, ws=None) == 4
+        assert call(lib, wsb=16) == 4
+        assert call(lib, x=None, d=None, dx=None, dw=None, rows=0) == 0
+
+
+def test_norm_workspace_size(lib):
+    import ssm_sequence_models_amd as s
+    # 1024 blocks over the groups, four rows a block up to 512 channels a group, one above
+    assert s.norm_bwd_workspace_size(32768, 4096, 1) == 2 * 1024 * 4096 * 4
+    assert s.norm_bwd_workspace_size(32768, 4096, 8) == 2 * 128 * 4096 * 4
+    assert s.norm_bwd_workspace_size(10, 4096, 1) == 2 * 10 * 4096 * 4
+    assert s.norm_bwd_workspace_size(10, 64, 1) == 2 * 3 * 64 * 4
+    assert s.norm_bwd_workspace_size(0, 64, 1) == 0
+
+
+def test_norm_binding_refusals():
+    import ssm_sequence_models_amd as ssm
+    x = torch.zeros(4, 8)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        ssm.norm_fwd(x)
+    with pytest.raises(ValueError, match="kind"):
+        ssm.norm_fwd(x, kind="batch")
+    with pytest.raises(ValueError, match="ngroups"):
+        ssm.norm_fwd(x, ngroups=3)
+    # the row view: one stride for all leading dimensions, consecutive channels
+    assert ssm._rows(torch.zeros(3, 4, 8), "x", 8) == (12, 8)
+    assert ssm._rows(torch.zeros(3, 4, 20)[:, :, 2:10], "x", 8) == (12, 20)
+    assert ssm._rows(torch.zeros(6, 4, 8)[::2, :1], "x", 8) == (3, 64)
+    assert ssm._rows(torch.zeros(1, 8).expand(5, 8), "x", 8) == (5, 0)
+    assert ssm._rows(torch.zeros(0, 8), "x", 8)[0] == 0
+    assert ssm._rows(torch.zeros(8), "x", 8) == (1, 8)
+    with pytest.raises(ValueError, match="one stride"):
+        ssm._rows(torch.zeros(3, 5, 8)[:, :4], "x", 8)
+    with pytest.raises(ValueError, match="consecutive"):
+        ssm._rows(torch.zeros(8, 4).t(), "x", 8)
+    with pytest.raises(ValueError, match="channels"):
+        ssm._rows(torch.zeros(4, 9), "x", 8)
+
+
+def test_norm64_against_differences():
+    g = torch.Generator().manual_seed(2)
+    rnd = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)  # noqa: E731
+    for kind in ("rms", "layer"):
+        for after in (False, True):
+            a = [rnd(3, 12), 1 + 0.2 * rnd(12), rnd(12), rnd(3, 12)]
+            d = rnd(3, 12)
+            r = norm64(*a, 1e-4, kind, 3, after, d)
+            for i, name in enumerate(("dx", "dw", "db", "dz")):
+                v = rnd(*a[i].shape)
+                f = []
+                for e in (1e-5, -1e-5):
+                    q = list(a)
+                    q[i] = a[i] + e * v
+                    f.append(float((norm64(*q, 1e-4, kind, 3, after)["out"] * d).sum()))
+                assert abs((f[0] - f[1]) / 2e-5 - float((r[name] * v).sum())) < 1e-6
