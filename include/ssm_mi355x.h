@@ -413,6 +413,61 @@ ssm_status_t ssm_scan_bwd_initial_state(const float* dt, const float* A, const v
                                         ssm_dtype_t dtype, ssm_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------
+ * The per-channel gated recurrence: [LG] Sec. 2.1 Eq. (1) with a state of one value per
+ * channel (A_t = diag(a_t), B = C = 1), for layers whose gates are data-dependent and whose
+ * recurrence has no state dimension.  Per row b and channel c
+ *     h_t = a_t h_{t-1} + i_t x_t,   y_t = h_t,   h_{-1} = initial_state (zeros when NULL)
+ *   SSM_GATE_LOG:      a_t = exp(gate_t), i_t = 1         (gate <= 0 for a contraction)
+ *   SSM_GATE_SIGMOID:  a_t = sigmoid(gate_t), i_t = 1 - a_t
+ * seq_idx: the state restarts from zero where seq_idx[b,t] != seq_idx[b,t-1] (a_t counts as 0
+ * there, i_t does not change); a NaN or infinity of one sequence does not reach the next.
+ *
+ *   x, gate, dy, y, dx, dgate   tokens of `channels` consecutive elements, dtype; token t of
+ *                  row b at p + (b * seqlen + t) * p_row elements (inputs p_row >= 0, outputs
+ *                  p_row >= channels)
+ *   initial_state, final_state, dfinal_state, dinitial_state   [batch, channels] fp32, or NULL
+ *                  (zeros / not written)
+ *   seq_idx        [batch, seqlen] int32, or NULL
+ *   workspace      ..._workspace_size bytes, 4-byte aligned (NULL if 0): the joins of rows cut
+ *                  into segments and, backward, the state before every 128th token
+ * States and sums in fp32; outputs rounded once; deterministic.
+ *
+ * ssm_gated_scan_fwd   final_state may alias initial_state.  seqlen = 0: final = initial.
+ * ssm_gated_scan_bwd   from dy and dfinal_state, with E_t the gradient token t hands to
+ *     h_{t-1}:  D_t = dy_t + E_{t+1},  E_t = a_t D_t,  E_L = dfinal_state,  dx_t = i_t D_t,
+ *     dinitial_state = E_0,  dgate_t = D_t a_t h_{t-1} (log form) or
+ *     a_t (1 - a_t) D_t (h_{t-1} - x_t) (sigmoid form; h_{t-1} = 0 at a start).
+ *     Outputs must not overlap inputs (dinitial_state == dfinal_state is refused).
+ *     seqlen = 0: dinitial_state = dfinal_state (or zeros).
+ * ssm_gated_scan_step  n_new >= 1 tokens a request on pool slot s = state_indices[b] (b when
+ *     NULL): state [n_slots, channels] fp32, in / out.  A row whose slot is outside
+ *     [0, n_slots) is skipped: its y is zero-filled, the pool is not touched.  Two rows on one
+ *     slot: undefined.  x, gate and y: token t of row b at p + (b * n_new + t) * p_row.
+ * ------------------------------------------------------------------------------------- */
+enum { SSM_GATE_LOG = 0, SSM_GATE_SIGMOID = 1 };
+typedef int32_t ssm_gate_t;
+size_t ssm_gated_scan_fwd_workspace_size(int64_t batch, int64_t seqlen, int64_t channels);
+ssm_status_t ssm_gated_scan_fwd(const void* x, int64_t x_row, const void* gate, int64_t gate_row,
+                                const float* initial_state, float* final_state,
+                                const int32_t* seq_idx, void* y, int64_t y_row, int64_t batch,
+                                int64_t seqlen, int64_t channels, ssm_gate_t form,
+                                ssm_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                                ssm_stream_t stream);
+size_t ssm_gated_scan_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t channels);
+ssm_status_t ssm_gated_scan_bwd(const void* x, int64_t x_row, const void* gate, int64_t gate_row,
+                                const void* dy, int64_t dy_row, const float* initial_state,
+                                const float* dfinal_state, const int32_t* seq_idx, void* dx,
+                                int64_t dx_row, void* dgate, int64_t dgate_row,
+                                float* dinitial_state, int64_t batch, int64_t seqlen,
+                                int64_t channels, ssm_gate_t form, ssm_dtype_t dtype,
+                                void* workspace, size_t workspace_bytes, ssm_stream_t stream);
+ssm_status_t ssm_gated_scan_step(const void* x, int64_t x_row, const void* gate, int64_t gate_row,
+                                 float* state, const int32_t* state_indices, void* y,
+                                 int64_t y_row, int64_t batch, int64_t n_new, int64_t channels,
+                                 int64_t n_slots, ssm_gate_t form, ssm_dtype_t dtype,
+                                 ssm_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
  * ssm_norm_fwd / ssm_norm_bwd -- RMS or layer norm of rows of channels with an optional SiLU
  * gate: the norm between a layer's scan and its output projection (gate before or after), or
  * a plain pre-norm (z NULL).  Per row and group of m = channels / ngroups channels:

@@ -109,6 +109,16 @@ def _load():
     lib.ssm_norm_bwd_workspace_size.argtypes = [i64, i64, i64]
     lib.ssm_norm_bwd.argtypes = [vp, i64, vp, i64, vp, i64, fp, fp, vp, i64, vp, i64, fp, fp, vp,
                                  sz, i64, i64, i64, cf, ci, ci, ci, vp]
+    lib.ssm_gated_scan_fwd_workspace_size.restype = sz
+    lib.ssm_gated_scan_fwd_workspace_size.argtypes = [i64, i64, i64]
+    lib.ssm_gated_scan_fwd.argtypes = [vp, i64, vp, i64, fp, fp, i32p, vp, i64, i64, i64, i64, ci,
+                                       ci, vp, sz, vp]
+    lib.ssm_gated_scan_bwd_workspace_size.restype = sz
+    lib.ssm_gated_scan_bwd_workspace_size.argtypes = [i64, i64, i64]
+    lib.ssm_gated_scan_bwd.argtypes = [vp, i64, vp, i64, vp, i64, fp, fp, i32p, vp, i64, vp, i64,
+                                       fp, i64, i64, i64, ci, ci, vp, sz, vp]
+    lib.ssm_gated_scan_step.argtypes = [vp, i64, vp, i64, fp, i32p, vp, i64, i64, i64, i64, i64,
+                                        ci, ci, vp]
     lib.ssm_stream_copy.argtypes = [vp, vp, i64, vp]
     lib.ssm_timing_enable.argtypes = [ci]
     lib.ssm_timing_read.argtypes = [ctypes.POINTER(ctypes.c_double),
@@ -117,7 +127,7 @@ def _load():
               "ssm_conv_scan_fwd_noalloc", "ssm_step", "ssm_decode_step", "ssm_conv1d_bwd", "ssm_scan_bwd_initial_state",
               "ssm_conv_scan_fwd_pooled", "ssm_state_stats_update", "ssm_scan_fwd_vector_decay",
               "ssm_initial_state_noise", "ssm_state_reset", "ssm_stream_copy", "ssm_norm_fwd",
-              "ssm_norm_bwd",
+              "ssm_norm_bwd", "ssm_gated_scan_fwd", "ssm_gated_scan_bwd", "ssm_gated_scan_step",
               "ssm_timing_enable", "ssm_timing_read"):
         getattr(lib, f).restype = ci
     return lib
@@ -625,6 +635,111 @@ def decode_step(x_new, conv_state, conv_weight, conv_bias, dt, A, ssm_state, nhe
         _ptr(conv_state_indices), _ptr(cache_seqlens), _ptr(dt), _ptr(A), _ptr(ssm_state),
         _ptr(state_indices), _ptr(conv_out), _ptr(y), bsz, n_new, H, P, G, N, K, state_len,
         n_cslots, ssm_state.shape[0], _dtype_code(x_new), ACT[activation], _stream()))
+    return y
+
+
+GATE = {"log": 0, "sigmoid": 1}
+
+
+def _gated_args(x, gate, form):
+    """Checks shared by the gated scans; returns (batch, tokens, channels, x_row, gate_row)."""
+    if form not in GATE:
+        raise ValueError(f"form must be one of {sorted(GATE)}, got {form!r}")
+    if x.dim() != 3:
+        raise ValueError(f"x must be [batch, tokens, channels], got shape {tuple(x.shape)}")
+    B, L, C = x.shape
+    if C < 1:
+        raise ValueError("x must have at least one channel")
+    _need(x, "x", contiguous=False)
+    _need(gate, "gate", x.dtype, x.shape, contiguous=False)
+    _need_device(x, gate=gate)
+    return B, L, C, _rows(x, "x", C)[1], _rows(gate, "gate", C)[1]
+
+
+def gated_scan_fwd_workspace_size(batch, seqlen, channels) -> int:
+    return int(_lib.ssm_gated_scan_fwd_workspace_size(batch, seqlen, channels))
+
+
+def gated_scan_bwd_workspace_size(batch, seqlen, channels) -> int:
+    return int(_lib.ssm_gated_scan_bwd_workspace_size(batch, seqlen, channels))
+
+
+def gated_scan_fwd(x, gate, form="sigmoid", initial_state=None, seq_idx=None,
+                   return_final_state=True, final_state=None, y=None, workspace=None):
+    """The per-channel gated recurrence h_t = a_t h_{t-1} + i_t x_t (length-generalization notes
+    Sec. 2.1 Eq. (1), a state of one value per channel): a = exp(gate), i = 1 (form "log") or
+    a = sigmoid(gate), i = 1 - a (form "sigmoid").  x, gate [b, L, C] (consecutive channels,
+    tokens at any one stride); initial_state [b, C] fp32 (may be the same tensor as
+    final_state); seq_idx [b, L] int32.  Returns (y [b, L, C], final_state or None)."""
+    B, L, C, x_row, gate_row = _gated_args(x, gate, form)
+    _need(initial_state, "initial_state", torch.float32, (B, C))
+    _need(seq_idx, "seq_idx", torch.int32, (B, L))
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _need(y, "y", x.dtype, x.shape, contiguous=False)
+    if final_state is None and return_final_state:
+        final_state = torch.empty((B, C), dtype=torch.float32, device=x.device)
+    _need(final_state, "final_state", torch.float32, (B, C))
+    _need_device(x, initial_state=initial_state, seq_idx=seq_idx, y=y, final_state=final_state,
+                 workspace=workspace)
+    ws, wsb = _workspace(workspace, gated_scan_fwd_workspace_size(B, L, C), x.device)
+    with torch.cuda.device(x.device):
+        _check("ssm_gated_scan_fwd", _lib.ssm_gated_scan_fwd(
+            _ptr(x), x_row, _ptr(gate), gate_row, _ptr(initial_state), _ptr(final_state),
+            _ptr(seq_idx), _ptr(y), _rows(y, "y", C)[1], B, L, C, GATE[form], _dtype_code(x),
+            _ptr(ws), wsb, _stream()))
+    return y, final_state
+
+
+def gated_scan_bwd(x, gate, dy, form="sigmoid", initial_state=None, dfinal_state=None,
+                   seq_idx=None, dx=None, dgate=None, dinitial_state=None, workspace=None):
+    """Backward of gated_scan_fwd from dy [b, L, C] and dfinal_state [b, C] fp32 (None = zero).
+    Returns (dx, dgate [b, L, C], dinitial_state [b, C] fp32)."""
+    B, L, C, x_row, gate_row = _gated_args(x, gate, form)
+    _need(dy, "dy", x.dtype, x.shape, contiguous=False)
+    _need(initial_state, "initial_state", torch.float32, (B, C))
+    _need(dfinal_state, "dfinal_state", torch.float32, (B, C))
+    _need(seq_idx, "seq_idx", torch.int32, (B, L))
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if dgate is None:
+        dgate = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if dinitial_state is None:
+        dinitial_state = torch.empty((B, C), dtype=torch.float32, device=x.device)
+    _need(dx, "dx", x.dtype, x.shape, contiguous=False)
+    _need(dgate, "dgate", x.dtype, x.shape, contiguous=False)
+    _need(dinitial_state, "dinitial_state", torch.float32, (B, C))
+    _need_device(x, dy=dy, initial_state=initial_state, dfinal_state=dfinal_state, seq_idx=seq_idx,
+                 dx=dx, dgate=dgate, dinitial_state=dinitial_state, workspace=workspace)
+    ws, wsb = _workspace(workspace, gated_scan_bwd_workspace_size(B, L, C), x.device)
+    with torch.cuda.device(x.device):
+        _check("ssm_gated_scan_bwd", _lib.ssm_gated_scan_bwd(
+            _ptr(x), x_row, _ptr(gate), gate_row, _ptr(dy), _rows(dy, "dy", C)[1],
+            _ptr(initial_state), _ptr(dfinal_state), _ptr(seq_idx), _ptr(dx),
+            _rows(dx, "dx", C)[1], _ptr(dgate), _rows(dgate, "dgate", C)[1],
+            _ptr(dinitial_state), B, L, C, GATE[form], _dtype_code(x), _ptr(ws), wsb, _stream()))
+    return dx, dgate, dinitial_state
+
+
+def gated_scan_step(x, gate, state, form="sigmoid", state_indices=None, y=None):
+    """Decode update of a pool of gated_scan states: x, gate [b, n_new, C], state [n_slots, C]
+    fp32 (updated in place), state_indices [b] int32 (None: row b uses slot b).  Returns y
+    [b, n_new, C]."""
+    B, T, C, x_row, gate_row = _gated_args(x, gate, form)
+    if state.dim() != 2 or state.shape[1] != C:
+        raise ValueError(f"state must be [n_slots, {C}], got shape {tuple(state.shape)}")
+    _need(state, "state", torch.float32)
+    _need(state_indices, "state_indices", torch.int32, (B,))
+    if DEBUG_CHECKS:
+        check_distinct_slots(state_indices, state.shape[0], "state_indices")
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _need(y, "y", x.dtype, x.shape, contiguous=False)
+    _need_device(x, state=state, state_indices=state_indices, y=y)
+    with torch.cuda.device(x.device):
+        _check("ssm_gated_scan_step", _lib.ssm_gated_scan_step(
+            _ptr(x), x_row, _ptr(gate), gate_row, _ptr(state), _ptr(state_indices), _ptr(y),
+            _rows(y, "y", C)[1], B, T, C, state.shape[0], GATE[form], _dtype_code(x), _stream()))
     return y
 
 

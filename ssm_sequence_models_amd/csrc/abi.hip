@@ -1012,6 +1012,193 @@ ssm_status_t ssm_norm_bwd(const void* x, int64_t x_row, const void* z, int64_t z
 }
 
 namespace {
+
+ssm_status_t check_gscan_dims(const char* fn, int64_t batch, int64_t seqlen, int64_t channels,
+                              int32_t form, int dtype) {
+    if (!valid_dtype(dtype)) return fail(SSM_ERR_INVALID_ARG, std::string(fn) + ": bad dtype");
+    if (form != SSM_GATE_LOG && form != SSM_GATE_SIGMOID)
+        return fail(SSM_ERR_INVALID_ARG, std::string(fn) + ": bad gate form");
+    if (batch < 0 || seqlen < 0 || channels < 1)
+        return fail(SSM_ERR_INVALID_ARG, std::string(fn) + ": need batch >= 0, tokens >= 0, channels >= 1");
+    // sizes whose products below could leave 63 bits, or their grid 31
+    const int64_t most = int64_t{1} << 31;
+    if (batch >= most || seqlen >= most || channels >= most ||
+        (batch > 0 && (channels + 63) / 64 > most / batch))
+        return fail(SSM_ERR_UNSUPPORTED, std::string(fn) + ": batch, tokens or channels too large");
+    return SSM_OK;
+}
+
+}  // namespace
+
+size_t ssm_gated_scan_fwd_workspace_size(int64_t batch, int64_t seqlen, int64_t channels) {
+    if (batch <= 0 || seqlen <= 0 || channels < 1) return 0;
+    return ssm::gscan_workspace_bytes(batch, seqlen, channels, false);
+}
+
+size_t ssm_gated_scan_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t channels) {
+    if (batch <= 0 || seqlen <= 0 || channels < 1) return 0;
+    return ssm::gscan_workspace_bytes(batch, seqlen, channels, true);
+}
+
+ssm_status_t ssm_gated_scan_fwd(const void* x, int64_t x_row, const void* gate, int64_t gate_row,
+                                const float* initial_state, float* final_state,
+                                const int32_t* seq_idx, void* y, int64_t y_row, int64_t batch,
+                                int64_t seqlen, int64_t channels, ssm_gate_t form,
+                                ssm_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                                ssm_stream_t stream) {
+    const char* fn = "ssm_gated_scan_fwd";
+    ssm_status_t st = check_gscan_dims(fn, batch, seqlen, channels, form, dtype);
+    if (st != SSM_OK) return st;
+    const size_t es = esize(dtype);
+    const bool work = batch > 0 && seqlen > 0;
+    const int64_t rows = batch * seqlen;
+    st = check_ptrs(fn, {{"x", x, work, es},
+                         {"gate", gate, work, es},
+                         {"initial_state", initial_state, false, 4},
+                         {"final_state", final_state, false, 4},
+                         {"seq_idx", seq_idx, false, 4},
+                         {"y", y, work, es},
+                         {"workspace", workspace, false, 4}});
+    if (st == SSM_OK) st = check_row(fn, "x", x, x_row, rows, 0);
+    if (st == SSM_OK) st = check_row(fn, "gate", gate, gate_row, rows, 0);
+    if (st == SSM_OK) st = check_row(fn, "y", y, y_row, rows, channels);
+    if (st != SSM_OK) return st;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    if (batch == 0) return ok();
+    if (seqlen == 0)
+        return hip_status(ssm::launch_copy_or_zero_f32(final_state, initial_state, batch * channels, s), fn);
+    if (ssm::gscan_blocks(batch, seqlen, channels) > 0x7FFFFFFF)
+        return fail(SSM_ERR_UNSUPPORTED, std::string(fn) + ": too many rows and channels");
+    const size_t need = ssm_gated_scan_fwd_workspace_size(batch, seqlen, channels);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need))
+        return fail(SSM_ERR_WORKSPACE, std::string(fn) + ": workspace missing or smaller than "
+                                       "ssm_gated_scan_fwd_workspace_size");
+    ssm::GscanCall c{};
+    c.x = x;
+    c.x_row = x_row;
+    c.gate = gate;
+    c.gate_row = gate_row;
+    c.y = y;
+    c.y_row = y_row;
+    c.h0 = initial_state;
+    c.final_state = final_state;
+    c.seq = seq_idx;
+    c.workspace = workspace;
+    c.B = batch;
+    c.L = seqlen;
+    c.C = channels;
+    c.sigmoid = form == SSM_GATE_SIGMOID;
+    c.dtype = dtype;
+    return hip_status(ssm::launch_gscan_fwd(c, s), fn);
+}
+
+ssm_status_t ssm_gated_scan_bwd(const void* x, int64_t x_row, const void* gate, int64_t gate_row,
+                                const void* dy, int64_t dy_row, const float* initial_state,
+                                const float* dfinal_state, const int32_t* seq_idx, void* dx,
+                                int64_t dx_row, void* dgate, int64_t dgate_row,
+                                float* dinitial_state, int64_t batch, int64_t seqlen,
+                                int64_t channels, ssm_gate_t form, ssm_dtype_t dtype,
+                                void* workspace, size_t workspace_bytes, ssm_stream_t stream) {
+    const char* fn = "ssm_gated_scan_bwd";
+    ssm_status_t st = check_gscan_dims(fn, batch, seqlen, channels, form, dtype);
+    if (st != SSM_OK) return st;
+    const size_t es = esize(dtype);
+    const bool work = batch > 0 && seqlen > 0;
+    const int64_t rows = batch * seqlen;
+    st = check_ptrs(fn, {{"x", x, work, es},
+                         {"gate", gate, work, es},
+                         {"dy", dy, work, es},
+                         {"initial_state", initial_state, false, 4},
+                         {"dfinal_state", dfinal_state, false, 4},
+                         {"seq_idx", seq_idx, false, 4},
+                         {"dx", dx, work, es},
+                         {"dgate", dgate, work, es},
+                         {"dinitial_state", dinitial_state, false, 4},
+                         {"workspace", workspace, false, 4}});
+    if (st == SSM_OK) st = check_row(fn, "x", x, x_row, rows, 0);
+    if (st == SSM_OK) st = check_row(fn, "gate", gate, gate_row, rows, 0);
+    if (st == SSM_OK) st = check_row(fn, "dy", dy, dy_row, rows, 0);
+    if (st == SSM_OK) st = check_row(fn, "dx", dx, dx_row, rows, channels);
+    if (st == SSM_OK) st = check_row(fn, "dgate", dgate, dgate_row, rows, channels);
+    if (st != SSM_OK) return st;
+    if (dinitial_state != nullptr && dinitial_state == dfinal_state)
+        return fail(SSM_ERR_INVALID_ARG, std::string(fn) + ": dinitial_state must not be dfinal_state");
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    if (batch == 0) return ok();
+    if (seqlen == 0)
+        return hip_status(ssm::launch_copy_or_zero_f32(dinitial_state, dfinal_state, batch * channels, s), fn);
+    if (ssm::gscan_blocks(batch, seqlen, channels) > 0x7FFFFFFF)
+        return fail(SSM_ERR_UNSUPPORTED, std::string(fn) + ": too many rows and channels");
+    const size_t need = ssm_gated_scan_bwd_workspace_size(batch, seqlen, channels);
+    if (workspace == nullptr || workspace_bytes < need)
+        return fail(SSM_ERR_WORKSPACE, std::string(fn) + ": workspace missing or smaller than "
+                                       "ssm_gated_scan_bwd_workspace_size");
+    ssm::GscanCall c{};
+    c.x = x;
+    c.x_row = x_row;
+    c.gate = gate;
+    c.gate_row = gate_row;
+    c.dy = dy;
+    c.dy_row = dy_row;
+    c.dx = dx;
+    c.dx_row = dx_row;
+    c.dgate = dgate;
+    c.dgate_row = dgate_row;
+    c.h0 = initial_state;
+    c.dhT = dfinal_state;
+    c.dh0 = dinitial_state;
+    c.seq = seq_idx;
+    c.workspace = workspace;
+    c.B = batch;
+    c.L = seqlen;
+    c.C = channels;
+    c.sigmoid = form == SSM_GATE_SIGMOID;
+    c.dtype = dtype;
+    return hip_status(ssm::launch_gscan_bwd(c, s), fn);
+}
+
+ssm_status_t ssm_gated_scan_step(const void* x, int64_t x_row, const void* gate, int64_t gate_row,
+                                 float* state, const int32_t* state_indices, void* y,
+                                 int64_t y_row, int64_t batch, int64_t n_new, int64_t channels,
+                                 int64_t n_slots, ssm_gate_t form, ssm_dtype_t dtype,
+                                 ssm_stream_t stream) {
+    const char* fn = "ssm_gated_scan_step";
+    ssm_status_t st = check_gscan_dims(fn, batch, n_new, channels, form, dtype);
+    if (st != SSM_OK) return st;
+    if (n_slots < 1) return fail(SSM_ERR_INVALID_ARG, std::string(fn) + ": n_slots must be >= 1");
+    const size_t es = esize(dtype);
+    const bool work = batch > 0 && n_new > 0;
+    const int64_t rows = batch * n_new;
+    st = check_ptrs(fn, {{"x", x, work, es},
+                         {"gate", gate, work, es},
+                         {"state", state, work, 4},
+                         {"state_indices", state_indices, false, 4},
+                         {"y", y, work, es}});
+    if (st == SSM_OK) st = check_row(fn, "x", x, x_row, rows, 0);
+    if (st == SSM_OK) st = check_row(fn, "gate", gate, gate_row, rows, 0);
+    if (st == SSM_OK) st = check_row(fn, "y", y, y_row, rows, channels);
+    if (st != SSM_OK) return st;
+    if (!work) return ok();
+    if ((batch * channels + 255) / 256 > 0x7FFFFFFF)
+        return fail(SSM_ERR_UNSUPPORTED, std::string(fn) + ": too many rows and channels");
+    ssm::GscanCall c{};
+    c.x = x;
+    c.x_row = x_row;
+    c.gate = gate;
+    c.gate_row = gate_row;
+    c.y = y;
+    c.y_row = y_row;
+    c.B = batch;
+    c.L = n_new;
+    c.C = channels;
+    c.sigmoid = form == SSM_GATE_SIGMOID;
+    c.dtype = dtype;
+    return hip_status(ssm::launch_gscan_step(c, state, state_indices, n_slots,
+                                             reinterpret_cast<hipStream_t>(stream)),
+                      fn);
+}
+
+namespace {
 ssm_status_t check_state_dims(const char* fn, int64_t batch, int64_t nheads, int64_t headdim,
                               int64_t dstate) {
     if (batch < 0) return fail(SSM_ERR_INVALID_ARG, std::string(fn) + ": negative batch");

@@ -258,6 +258,31 @@ struct NormCall {
 int64_t norm_partial_rows(int64_t rows, int64_t channels, int64_t groups);
 hipError_t launch_norm_fwd(const NormCall& c, hipStream_t stream);
 hipError_t launch_norm_bwd(const NormCall& c, hipStream_t stream);
+// the per-channel gated recurrence; token rows of C elements at the given strides
+struct GscanCall {
+    const void* x;
+    const void* gate;
+    const void* dy;
+    void* y;
+    void* dx;
+    void* dgate;
+    int64_t x_row, gate_row, dy_row, y_row, dx_row, dgate_row;
+    const float* h0;      // [B, C] or NULL
+    const float* dhT;     // [B, C] or NULL
+    float* final_state;   // [B, C] or NULL
+    float* dh0;           // [B, C] or NULL
+    const int32_t* seq;   // [B, L] or NULL
+    void* workspace;      // gscan_workspace_bytes
+    int64_t B, L, C;
+    bool sigmoid;
+    ssm_dtype_t dtype;
+};
+int64_t gscan_blocks(int64_t B, int64_t L, int64_t C);
+size_t gscan_workspace_bytes(int64_t B, int64_t L, int64_t C, bool bwd);
+hipError_t launch_gscan_fwd(const GscanCall& c, hipStream_t stream);
+hipError_t launch_gscan_bwd(const GscanCall& c, hipStream_t stream);
+hipError_t launch_gscan_step(const GscanCall& c, float* pool, const int32_t* slots,
+                             int64_t n_slots, hipStream_t stream);
 hipError_t launch_pool_gather(const void* conv_pool, const float* ssm_pool, const int32_t* indices,
                               const int32_t* seqlens, void* conv_hist, float* ssm_init,
                               int64_t batch, int64_t C, int64_t K, int64_t state_len,

@@ -107,3 +107,60 @@ def test_norm64_against_differences():
                     q[i] = a[i] + e * v
                     f.append(float((norm64(*q, 1e-4, kind, 3, after)["out"] * d).sum()))
                 assert abs((f[0] - f[1]) / 2e-5 - float((r[name] * v).sum())) < 1e-6
+
+
+def _gfwd(lib, x=P, xr=64, g=P, gr=64, h0=None, f=None, seq=None, y=P, yr=64, B=2, L=4, C=64, form=1,
+          dtype=1, ws=P, wsb=1 << 30):
+    return lib.ssm_gated_scan_fwd(x, xr, g, gr, h0, f, seq, y, yr, B, L, C, form, dtype, ws, wsb, None)
+
+
+def _gbwd(lib, x=P, xr=64, g=P, gr=64, d=P, dr=64, h0=None, f=None, seq=None, y=P, yr=64, dg=P,
+          dgr=64, dh0=None, B=2, L=4, C=64, form=1, dtype=1, ws=P, wsb=1 << 30):
+    return lib.ssm_gated_scan_bwd(x, xr, g, gr, d, dr, h0, f, seq, y, yr, dg, dgr, dh0, B, L, C, form,
+                                  dtype, ws, wsb, None)
+
+
+def _gstep(lib, x=P, xr=64, g=P, gr=64, state=P, idx=None, y=P, yr=64, B=2, L=4, C=64, n=4, form=1,
+           dtype=1):
+    return lib.ssm_gated_scan_step(x, xr, g, gr, state, idx, y, yr, B, L, C, n, form, dtype, None)
+
+
+@pytest.mark.parametrize("call", [_gfwd, _gbwd, _gstep])
+def test_gated_scan_refusals(lib, call):
+    for status, how in ((1, dict(dtype=2)), (1, dict(form=2)), (1, dict(form=-1)), (1, dict(B=-1)),
+                        (1, dict(L=-1)), (1, dict(C=0)), (2, dict(C=1 << 31, xr=1 << 31, yr=1 << 31)),
+                        (2, dict(B=1 << 31)), (1, dict(x=None)), (1, dict(g=None)), (1, dict(y=None)),
+                        (3, dict(x=ODD)), (3, dict(y=ODD)), (1, dict(xr=-1)), (1, dict(gr=-1)),
+                        (1, dict(yr=63))):
+        assert call(lib, **how) == status, how
+        assert lib.ssm_last_error()
+    assert call(lib, B=0, x=None, g=None, y=None) == 0
+
+
+def test_gated_scan_workspace(lib):
+    import ssm_sequence_models_amd as s
+    # 256 blocks already: no cut; else segments of at least four 128-token tiles, three floats a
+    # segment and channel; backward two floats a tile and channel more
+    assert s.gated_scan_fwd_workspace_size(4, 8192, 4096) == 0
+    assert s.gated_scan_bwd_workspace_size(4, 8192, 4096) == 4 * 64 * 2 * 4096 * 4
+    assert s.gated_scan_fwd_workspace_size(1, 1023, 64) == 2 * 3 * 64 * 4
+    assert s.gated_scan_fwd_workspace_size(1, 896, 64) == 0
+    assert s.gated_scan_fwd_workspace_size(0, 5, 5) == 0
+    assert _gfwd(lib, B=1, L=2000, ws=None) == 4
+    assert _gfwd(lib, B=1, L=2000, wsb=16) == 4
+    assert _gbwd(lib, ws=None) == 4
+    assert _gbwd(lib, wsb=16) == 4
+    assert _gbwd(lib, f=P, dh0=P) == 1
+    assert _gstep(lib, n=0) == 1
+    assert _gstep(lib, state=None) == 1
+
+
+def test_gated_scan_binding_refusals():
+    import ssm_sequence_models_amd as ssm
+    x = torch.zeros(1, 4, 8)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        ssm.gated_scan_fwd(x, x)
+    with pytest.raises(ValueError, match="form"):
+        ssm.gated_scan_bwd(x, x, x, form="tanh")
+    with pytest.raises(ValueError, match="batch, tokens, channels"):
+        ssm.gated_scan_step(x[0], x[0], x[0])

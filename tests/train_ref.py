@@ -70,3 +70,74 @@ def norm64(x, w, b, z, eps, kind, ngroups, after, dout=None):
     r.update(dw=(dp * n).sum(0), dw_mag=(dp.abs() * nk2 * zmag).sum(0), db=dp.sum(0),
              db_mag=(dp.abs() * zmag).sum(0))
     return r
+
+
+# ---------------------------------------------------------------------------------------
+# per-channel gated recurrence
+# ---------------------------------------------------------------------------------------
+def starts_of(seq, B, L):
+    """[B, L] bool: tokens that start a packed sequence (never token 0)."""
+    m = torch.zeros(B, L, dtype=torch.bool)
+    if seq is not None:
+        m[:, 1:] = seq[:, 1:] != seq[:, :-1]
+    return m
+
+
+def gated64(x, gate, form, h0=None, seq=None, dy=None, dhT=None):
+    """y, final and, with dy, dx, dgate, dh0 token by token; `*_err`: a bound of the fp32 error
+    of each before its rounding to the output type, by the same recurrence: a token multiplies
+    what it passes on and adds its own, each with k half-steps (k = 24 + 4 |gate|: the exp of a
+    rounded argument, reciprocal, product and sum, and the joins of spans, whose products add
+    fewer roundings than the tokens they span)."""
+    B, L, C = x.shape
+    x, g = x.double(), gate.double()
+    log = form == "log"
+    ag = torch.exp(g) if log else torch.sigmoid(g)
+    i = torch.ones_like(g) if log else torch.sigmoid(-g)
+    st = starts_of(seq, B, L)[..., None]
+    a = ag.masked_fill(st, 0.0)
+    u = i * x
+    k = (24 + 4 * g.abs().clamp(max=200.0)) * U
+    h = torch.zeros(B, C, dtype=torch.float64) if h0 is None else h0.double()
+    mag, err = h.abs(), torch.zeros_like(h)
+    hs, before, berr, bmag, es = (torch.empty_like(x) for _ in range(5))
+    for t in range(L):
+        s = st[:, t]
+        before[:, t], berr[:, t], bmag[:, t] = (v.masked_fill(s, 0.0) for v in (h, err, mag))
+        keep = a[:, t]
+        # a start keeps nothing, whatever the state (also NaN or inf) was
+        h = torch.where(s, torch.zeros_like(h), keep * h) + u[:, t]
+        err = torch.where(s, torch.zeros_like(h), keep * err + k[:, t] * keep * mag) + k[:, t] * u[:, t].abs()
+        mag = torch.where(s, torch.zeros_like(h), keep * mag) + u[:, t].abs()
+        hs[:, t], es[:, t] = h, err + 1e-30
+    r = dict(y=hs, y_err=es, final=h, final_err=err + 1e-30)
+    if dy is None:
+        return r
+    dy = dy.double()
+    E = torch.zeros(B, C, dtype=torch.float64) if dhT is None else dhT.double()
+    Eerr, Emag = torch.zeros_like(E), E.abs()
+    dx, dgate, dxe, dge = (torch.empty_like(x) for _ in range(4))
+    for t in range(L - 1, -1, -1):
+        kt = k[:, t]
+        D, De, Dm = E + dy[:, t], Eerr + U * (Emag + dy[:, t].abs()), Emag + dy[:, t].abs()
+        dx[:, t] = D * i[:, t]
+        dxe[:, t] = i[:, t] * (De + kt * Dm) + 1e-30
+        dl = D * a[:, t] * before[:, t]
+        le = a[:, t] * (De * before[:, t].abs() + Dm * berr[:, t] + kt * Dm * bmag[:, t])
+        if log:
+            dgate[:, t], dge[:, t] = dl, le + 1e-30
+        else:
+            w = i[:, t] * ag[:, t] * x[:, t].abs()
+            dgate[:, t] = i[:, t] * dl - D * x[:, t] * i[:, t] * ag[:, t]
+            dge[:, t] = i[:, t] * (le + kt * a[:, t] * Dm * bmag[:, t]) + w * (De + kt * Dm) + 1e-30
+        s = st[:, t]
+        E = torch.where(s, torch.zeros_like(D), a[:, t] * D)
+        Eerr = torch.where(s, torch.zeros_like(D), a[:, t] * De + kt * a[:, t] * Dm)
+        Emag = torch.where(s, torch.zeros_like(D), a[:, t] * Dm)
+    r.update(dx=dx, dx_err=dxe, dgate=dgate, dgate_err=dge, dh0=E, dh0_err=Eerr + 1e-30)
+    return r
+
+
+def check_err(got, ref, name, dtype):
+    h = half_step(dtype)
+    assert_bound(got, ref[name], h * ref[name].abs() + (1 + h) * ref[name + "_err"], name)
