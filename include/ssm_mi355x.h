@@ -413,6 +413,43 @@ ssm_status_t ssm_scan_bwd_initial_state(const float* dt, const float* A, const v
                                         ssm_dtype_t dtype, ssm_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------
+ * ssm_scan_bwd -- the complete backward of ssm_scan_fwd.  [LG] Sec. 2.1 Eq. (1), Sec. 2.5
+ * Eq. (4): with a_t = exp(dt_t A_h) (0 where a packed sequence starts), state h_t and
+ * g_t = dL/dh_t, per head h of group g
+ *     g_t = dy_t C_t^T + a_{t+1} g_{t+1},  beyond the last token dfinal_state
+ *     dx_t = dt_t g_t B_t,   ddt_t = x_t . (g_t B_t) + A_h q_t,   dA_h = sum_{b,t} dt_t q_t,
+ *     q_t = <g_t, a_t h_{t-1}>,   dinitial_state = a_0 g_0,
+ *     dB_t = sum_{heads of g} dt_t g_t^T x_t,   dC_t = sum_{heads of g} h_t^T dy_t
+ * (h_t is recomputed from the inputs; nothing is kept from the forward).  Chunked training
+ * (Sec. 2.6): chunk B's dinitial_state, passed as chunk A's dfinal_state, gives the whole
+ * sequence's gradients; dA adds up.
+ *
+ *   x, dt, A, Bm, Cm, initial_state, seq_idx   as ssm_scan_fwd
+ *   dy               [batch, seqlen, nheads, headdim]   dtype: dL/dy
+ *   dfinal_state     [batch, nheads, headdim, dstate]   fp32, or NULL (= 0)
+ *   dx               [batch, seqlen, nheads, headdim]   dtype
+ *   ddt              [batch, seqlen, nheads]            fp32
+ *   dA               [nheads]                           fp32 (summed over the batch)
+ *   dB, dC           [batch, seqlen, ngroups, dstate]   dtype
+ *   dinitial_state   [batch, nheads, headdim, dstate]   fp32, or NULL (not written)
+ *   workspace        ssm_scan_bwd_workspace_size bytes, 256-byte aligned
+ * headdim and dstate as ssm_scan_fwd takes them (dstate 4 * 2^k <= 256, headdim * dstate <=
+ * 32768); dt * A finite.  Sums and states in fp32 (sums of log decays in double); outputs
+ * rounded once; deterministic.  Outputs must not overlap inputs (dinitial_state ==
+ * dfinal_state is refused).  Non-finite inputs may spread over the 64-token chunk they are in.
+ * seqlen = 0: dinitial_state = dfinal_state (or zeros), dA = 0.  batch = 0: dA = 0.
+ * ------------------------------------------------------------------------------------- */
+size_t ssm_scan_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim,
+                                   int64_t ngroups, int64_t dstate, ssm_dtype_t dtype);
+ssm_status_t ssm_scan_bwd(const void* x, const float* dt, const float* A, const void* Bm,
+                          const void* Cm, const void* dy, const float* initial_state,
+                          const float* dfinal_state, const int32_t* seq_idx, void* dx, float* ddt,
+                          float* dA, void* dB, void* dC, float* dinitial_state, int64_t batch,
+                          int64_t seqlen, int64_t nheads, int64_t headdim, int64_t ngroups,
+                          int64_t dstate, ssm_dtype_t dtype, void* workspace,
+                          size_t workspace_bytes, ssm_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
  * The per-channel gated recurrence: [LG] Sec. 2.1 Eq. (1) with a state of one value per
  * channel (A_t = diag(a_t), B = C = 1), for layers whose gates are data-dependent and whose
  * recurrence has no state dimension.  Per row b and channel c

@@ -109,6 +109,10 @@ def _load():
     lib.ssm_norm_bwd_workspace_size.argtypes = [i64, i64, i64]
     lib.ssm_norm_bwd.argtypes = [vp, i64, vp, i64, vp, i64, fp, fp, vp, i64, vp, i64, fp, fp, vp,
                                  sz, i64, i64, i64, cf, ci, ci, ci, vp]
+    lib.ssm_scan_bwd_workspace_size.restype = sz
+    lib.ssm_scan_bwd_workspace_size.argtypes = [i64, i64, i64, i64, i64, i64, ci]
+    lib.ssm_scan_bwd.argtypes = [vp, fp, fp, vp, vp, vp, fp, fp, i32p, vp, fp, fp, vp, vp, fp, i64,
+                                 i64, i64, i64, i64, i64, ci, vp, sz, vp]
     lib.ssm_gated_scan_fwd_workspace_size.restype = sz
     lib.ssm_gated_scan_fwd_workspace_size.argtypes = [i64, i64, i64]
     lib.ssm_gated_scan_fwd.argtypes = [vp, i64, vp, i64, fp, fp, i32p, vp, i64, i64, i64, i64, ci,
@@ -127,7 +131,7 @@ def _load():
               "ssm_conv_scan_fwd_noalloc", "ssm_step", "ssm_decode_step", "ssm_conv1d_bwd", "ssm_scan_bwd_initial_state",
               "ssm_conv_scan_fwd_pooled", "ssm_state_stats_update", "ssm_scan_fwd_vector_decay",
               "ssm_initial_state_noise", "ssm_state_reset", "ssm_stream_copy", "ssm_norm_fwd",
-              "ssm_norm_bwd", "ssm_gated_scan_fwd", "ssm_gated_scan_bwd", "ssm_gated_scan_step",
+              "ssm_norm_bwd", "ssm_scan_bwd", "ssm_gated_scan_fwd", "ssm_gated_scan_bwd", "ssm_gated_scan_step",
               "ssm_timing_enable", "ssm_timing_read"):
         getattr(lib, f).restype = ci
     return lib
@@ -636,6 +640,61 @@ def decode_step(x_new, conv_state, conv_weight, conv_bias, dt, A, ssm_state, nhe
         _ptr(state_indices), _ptr(conv_out), _ptr(y), bsz, n_new, H, P, G, N, K, state_len,
         n_cslots, ssm_state.shape[0], _dtype_code(x_new), ACT[activation], _stream()))
     return y
+
+
+def scan_bwd_workspace_size(batch, seqlen, nheads, headdim, ngroups, dstate,
+                            dtype=torch.bfloat16) -> int:
+    code = SSM_BF16 if dtype == torch.bfloat16 else SSM_F32
+    return int(_lib.ssm_scan_bwd_workspace_size(batch, seqlen, nheads, headdim, ngroups, dstate,
+                                                code))
+
+
+def scan_bwd(x, dt, A, B, C, dy, initial_state=None, dfinal_state=None, seq_idx=None, dx=None,
+             ddt=None, dA=None, dB=None, dC=None, dinitial_state=None, workspace=None):
+    """The complete backward of scan_fwd (length-generalization notes Sec. 2.1 Eq. (1), Sec. 2.5
+    Eq. (4)) from dy [b, L, H, P] and dfinal_state [b, H, P, N] fp32 (None = zero); the other
+    inputs as scan_fwd's.  Returns (dx [b, L, H, P], ddt [b, L, H] fp32, dA [H] fp32, dB, dC
+    [b, L, G, N], dinitial_state [b, H, P, N] fp32)."""
+    bsz, L, H, P = x.shape
+    G, N = B.shape[2], B.shape[3]
+    dev = x.device
+    _need(x, "x")
+    _need(dt, "dt", torch.float32, (bsz, L, H))
+    _need(A, "A", torch.float32, (H,))
+    _need(B, "B", x.dtype, (bsz, L, G, N))
+    _need(C, "C", x.dtype, (bsz, L, G, N))
+    _need(dy, "dy", x.dtype, (bsz, L, H, P))
+    _need(initial_state, "initial_state", torch.float32, (bsz, H, P, N))
+    _need(dfinal_state, "dfinal_state", torch.float32, (bsz, H, P, N))
+    _need(seq_idx, "seq_idx", torch.int32, (bsz, L))
+    if dx is None:
+        dx = torch.empty_like(x)
+    if ddt is None:
+        ddt = torch.empty_like(dt)
+    if dA is None:
+        dA = torch.empty_like(A)
+    if dB is None:
+        dB = torch.empty_like(B)
+    if dC is None:
+        dC = torch.empty_like(C)
+    if dinitial_state is None:
+        dinitial_state = torch.empty((bsz, H, P, N), dtype=torch.float32, device=dev)
+    _need(dx, "dx", x.dtype, (bsz, L, H, P))
+    _need(ddt, "ddt", torch.float32, (bsz, L, H))
+    _need(dA, "dA", torch.float32, (H,))
+    _need(dB, "dB", x.dtype, (bsz, L, G, N))
+    _need(dC, "dC", x.dtype, (bsz, L, G, N))
+    _need(dinitial_state, "dinitial_state", torch.float32, (bsz, H, P, N))
+    _need_device(x, dt=dt, A=A, B=B, C=C, dy=dy, initial_state=initial_state,
+                 dfinal_state=dfinal_state, seq_idx=seq_idx, dx=dx, ddt=ddt, dA=dA, dB=dB, dC=dC,
+                 dinitial_state=dinitial_state, workspace=workspace)
+    ws, wsb = _workspace(workspace, scan_bwd_workspace_size(bsz, L, H, P, G, N, x.dtype), dev)
+    with torch.cuda.device(dev):
+        _check("ssm_scan_bwd", _lib.ssm_scan_bwd(
+            _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(dy), _ptr(initial_state),
+            _ptr(dfinal_state), _ptr(seq_idx), _ptr(dx), _ptr(ddt), _ptr(dA), _ptr(dB), _ptr(dC),
+            _ptr(dinitial_state), bsz, L, H, P, G, N, _dtype_code(x), _ptr(ws), wsb, _stream()))
+    return dx, ddt, dA, dB, dC, dinitial_state
 
 
 GATE = {"log": 0, "sigmoid": 1}

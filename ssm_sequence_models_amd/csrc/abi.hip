@@ -1011,6 +1011,88 @@ ssm_status_t ssm_norm_bwd(const void* x, int64_t x_row, const void* z, int64_t z
     return hip_status(ssm::launch_norm_bwd(c, reinterpret_cast<hipStream_t>(stream)), fn);
 }
 
+size_t ssm_scan_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim,
+                                   int64_t ngroups, int64_t dstate, ssm_dtype_t dtype) {
+    if (batch <= 0 || seqlen <= 0 || nheads < 1 || headdim < 1 || ngroups < 1 || dstate < 1 ||
+        nheads % ngroups != 0 || !valid_dtype(dtype) || !ssm::recurrent_supported(headdim, dstate))
+        return 0;
+    return ssm::scan_bwd_workspace_bytes(batch, seqlen, nheads, headdim, ngroups, dstate, dtype);
+}
+
+ssm_status_t ssm_scan_bwd(const void* x, const float* dt, const float* A, const void* Bm,
+                          const void* Cm, const void* dy, const float* initial_state,
+                          const float* dfinal_state, const int32_t* seq_idx, void* dx, float* ddt,
+                          float* dA, void* dB, void* dC, float* dinitial_state, int64_t batch,
+                          int64_t seqlen, int64_t nheads, int64_t headdim, int64_t ngroups,
+                          int64_t dstate, ssm_dtype_t dtype, void* workspace,
+                          size_t workspace_bytes, ssm_stream_t stream) {
+    const char* fn = "ssm_scan_bwd";
+    ssm_status_t st = check_scan_dims(fn, batch, seqlen, nheads, headdim, ngroups, dstate, dtype);
+    if (st != SSM_OK) return st;
+    if (!ssm::recurrent_supported(headdim, dstate))
+        return fail(SSM_ERR_UNSUPPORTED, "ssm_scan_bwd: headdim and dstate must be sizes that ssm_scan_fwd takes (dstate 4 * 2^k <= 256, headdim*dstate <= 32768)");
+    const int64_t most = int64_t{1} << 31;
+    if (batch >= most || seqlen >= most || nheads >= most ||
+        (batch > 0 && seqlen > 0 && nheads > (most << 20) / batch / seqlen))
+        return fail(SSM_ERR_UNSUPPORTED, "ssm_scan_bwd: batch, seqlen or nheads too large");
+    const size_t es = esize(dtype);
+    const bool work = batch > 0 && seqlen > 0;
+    st = check_ptrs(fn, {{"x", x, work, es},
+                         {"dt", dt, work, 4},
+                         {"A", A, work, 4},
+                         {"Bm", Bm, work, es},
+                         {"Cm", Cm, work, es},
+                         {"dy", dy, work, es},
+                         {"initial_state", initial_state, false, 16},
+                         {"dfinal_state", dfinal_state, false, 16},
+                         {"seq_idx", seq_idx, false, 4},
+                         {"dx", dx, work, es},
+                         {"ddt", ddt, work, 4},
+                         {"dA", dA, true, 4},
+                         {"dB", dB, work, es},
+                         {"dC", dC, work, es},
+                         {"dinitial_state", dinitial_state, false, 16}});
+    if (st != SSM_OK) return st;
+    if (dinitial_state != nullptr && dinitial_state == dfinal_state)
+        return fail(SSM_ERR_INVALID_ARG, "ssm_scan_bwd: dinitial_state must not be dfinal_state");
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    if (!work)
+        return hip_status(ssm::launch_scan_bwd_empty(dfinal_state, dinitial_state, dA,
+                                                     batch * nheads * headdim * dstate, nheads, s),
+                          fn);
+    if (ssm::scan_bwd_blocks(batch, seqlen, nheads, headdim, ngroups, dstate) > 0x7FFFFFFF)
+        return fail(SSM_ERR_UNSUPPORTED, "ssm_scan_bwd: tensors too large for one call");
+    const size_t need = ssm_scan_bwd_workspace_size(batch, seqlen, nheads, headdim, ngroups, dstate, dtype);
+    if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 256))
+        return fail(SSM_ERR_WORKSPACE, "ssm_scan_bwd: workspace must be >= " + std::to_string(need) +
+                                           " bytes, 256-byte aligned");
+    ssm::ScanBwdArgs a{};
+    a.x = x;
+    a.dt = dt;
+    a.A = A;
+    a.Bm = Bm;
+    a.C = Cm;
+    a.dy = dy;
+    a.h0 = initial_state;
+    a.dhT = dfinal_state;
+    a.seq = seq_idx;
+    a.dx = dx;
+    a.ddt = ddt;
+    a.dA = dA;
+    a.dB = dB;
+    a.dC = dC;
+    a.dh0 = dinitial_state;
+    a.x_row = a.dy_row = a.dx_row = nheads * headdim;
+    a.b_row = a.c_row = a.db_row = a.dc_row = ngroups * dstate;
+    a.B = batch;
+    a.L = seqlen;
+    a.H = nheads;
+    a.P = headdim;
+    a.G = ngroups;
+    a.N = dstate;
+    return hip_status(ssm::launch_scan_bwd(a, workspace, dtype, s), fn);
+}
+
 namespace {
 
 ssm_status_t check_gscan_dims(const char* fn, int64_t batch, int64_t seqlen, int64_t channels,

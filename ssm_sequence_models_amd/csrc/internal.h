@@ -283,6 +283,41 @@ hipError_t launch_gscan_fwd(const GscanCall& c, hipStream_t stream);
 hipError_t launch_gscan_bwd(const GscanCall& c, hipStream_t stream);
 hipError_t launch_gscan_step(const GscanCall& c, float* pool, const int32_t* slots,
                              int64_t n_slots, hipStream_t stream);
+// the scan's complete backward; token rows of x, dy, dx (H*P elements) and B, C, dB, dC (G*N)
+// at the given strides
+struct ScanBwdArgs {
+    const void* x;
+    const float* dt;   // [B, L, H]
+    const float* A;    // [H]
+    const void* Bm;
+    const void* C;
+    const void* dy;
+    const float* h0;   // [B, H, P, N] or NULL
+    const float* dhT;  // [B, H, P, N] or NULL
+    const int32_t* seq;
+    void* dx;
+    float* ddt;
+    float* dA;
+    void* dB;
+    void* dC;
+    float* dh0;        // [B, H, P, N] or NULL
+    int64_t x_row, dy_row, b_row, c_row, dx_row, db_row, dc_row;
+    int64_t B, L, H, P, G, N;
+    // set by launch_scan_bwd
+    int64_t chunks;
+    double* dA_part;   // [B, chunks, H]
+    float* through;    // [B, H, chunks]
+    float* states;     // [B, H, chunks, P, N]: the state before each chunk
+    float* grads;      // [B, H, chunks, P, N]: the gradient of the state after it
+    float* dB_head;    // [B, L, H, N]
+    float* dC_head;
+};
+size_t scan_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N,
+                                ssm_dtype_t dtype);
+int64_t scan_bwd_blocks(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N);
+hipError_t launch_scan_bwd(ScanBwdArgs a, void* workspace, ssm_dtype_t dtype, hipStream_t stream);
+hipError_t launch_scan_bwd_empty(const float* dhT, float* dh0, float* dA, int64_t n, int64_t H,
+                                 hipStream_t stream);
 hipError_t launch_pool_gather(const void* conv_pool, const float* ssm_pool, const int32_t* indices,
                               const int32_t* seqlens, void* conv_hist, float* ssm_init,
                               int64_t batch, int64_t C, int64_t K, int64_t state_len,

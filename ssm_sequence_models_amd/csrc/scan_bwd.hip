@@ -1,0 +1,460 @@
+// scan_bwd.hip -- the complete backward of the selective scan (ssm_scan_bwd), general shapes.
+//
+// Forward (length-generalization reading notes, Sec. 2.1 Eq. (1), Sec. 2.5 Eq. (4)), per head:
+//     h_t = a_t h_{t-1} + dt_t x_t B_t^T,  y_t = h_t C_t,  a_t = exp(dt_t A),
+// a_t counting as 0 where a packed sequence starts.  With g_t = dL/dh_t,
+//     g_t = dy_t C_t^T + a_{t+1} g_{t+1},  g past the end = d(final state),
+//     dx_t = dt_t g_t B_t,  dB_t = dt_t g_t^T x_t,  dC_t = h_t^T dy_t  (summed over the group's heads),
+//     ddt_t = x_t . (g_t B_t) + A q_t,  dA = sum_t dt_t q_t,  q_t = <g_t, a_t h_{t-1}> = dL/d log a_t.
+//
+// Chunked: tokens in chunks of Q = 64, L_ts = a_{s+1} .. a_t for s <= t of one sequence (else
+// 0), S the state before the chunk, G the gradient of the state after it, f_t = a_first .. a_t
+// (from the chunk's start), e_s = a_{s+1} .. a_last (to its end), both 0 across a start:
+//     S' = f_last S + sum_s (dt_s e_s x_s) B_s^T        (the next chunk's S)
+//     G' = f_last G + sum_t (f_t dy_t) C_t^T            (the previous chunk's G)
+//     dx_s = dt_s ( sum_t L_ts (C_t.B_s) dy_t  +  e_s G B_s )
+//     dC_t = sum_s L_ts dt_s (dy_t.x_s) B_s  +  f_t S^T dy_t
+//     dB_s = dt_s ( sum_t L_ts (dy_t.x_s) C_t  +  e_s G^T x_s )
+// and q_t is the sum of every product whose factor spans t: with
+//     W_ts = L_ts (C_t.B_s) (dy_t.x_s) dt_s,  u_t = f_t dy_t.(S C_t),  v_s = dt_s e_s x_s.(G B_s),
+// each W_ts counts for s < tau <= t, u_t for tau <= t, v_s for tau > s, f_last <G, S> for all,
+// so q is the sum from the chunk's end back of
+//     sum_{s<t} W_ts - sum_{t'>t} W_t't + u_t - v_t  (+ sum_s v_s + f_last <G, S> at the last).
+// The part of ddt that does not pass through a_t is sum_t W_ts / dt_s + v_s / dt_s, formed
+// without the division.
+//
+// Decays: log a_t is summed in double over the chunk and each factor is the exponential of a
+// difference of two sums, so its relative error stays near 2^-24 however fast the decay.
+// log a below -1024 (a = 0 in fp32 by far) counts as -1024: the sums keep what follows.
+//
+// This file: any headdim and dstate that the forward takes, fp32 or bf16 activations, products
+// on the fp32 matrix instruction (16 x 16 x 4).  Three steps: the chunks' own shares of S and G
+// (one block a chunk and head), their sums along the row (one thread a state element), the
+// gradients (one block a chunk and head; dB and dC a head, which a last kernel adds over the
+// heads of a group in order, with the chunks' dA).
+#include "internal.h"
+
+namespace ssm {
+namespace {
+
+constexpr int kQ = 64;
+
+typedef float f4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ f4 mfma4(const f4& a, const f4& b, f4 c) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
+    return c;
+}
+
+// The chunk's decays, by the block's first wavefront (lane = token).
+struct ChunkDecay {
+    double cs[kQ];   // sum of log a over the chunk's tokens 0 .. t
+    int starts[kQ];  // sequence starts among tokens 0 .. t
+    float f[kQ];     // f_t
+    float e[kQ];     // e_t
+    float dt[kQ];    // dt_t (0 past the row's end)
+    float through;   // f_last
+};
+
+__device__ __forceinline__ void chunk_decay(ChunkDecay& cd, const float* dt, int64_t dt_stride,
+                                            float A, const int32_t* seq, int64_t t0, int nv) {
+    const int t = threadIdx.x;
+    if (t < kQ) {
+        const float d = t < nv ? dt[t * dt_stride] : 0.0f;
+        double s = static_cast<double>(d) * static_cast<double>(A);
+        if (s < -1024.0) s = -1024.0;
+        int r = 0;
+        if (seq && t < nv && t0 + t > 0) r = seq[t0 + t] != seq[t0 + t - 1];
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const double so = __shfl_up(s, o);
+            const int ro = __shfl_up(r, o);
+            if (t >= o) {
+                s += so;
+                r += ro;
+            }
+        }
+        const double end = __shfl(s, 63);
+        const int rend = __shfl(r, 63);
+        cd.cs[t] = s;
+        cd.starts[t] = r;
+        cd.f[t] = r == 0 ? __expf(static_cast<float>(s)) : 0.0f;
+        cd.e[t] = r == rend ? __expf(static_cast<float>(end - s)) : 0.0f;
+        cd.dt[t] = d;
+        if (t == 63) cd.through = r == 0 ? __expf(static_cast<float>(s)) : 0.0f;
+    }
+    __syncthreads();
+}
+
+// block -> (row, head, chunk)
+struct Where {
+    int64_t b, h, c, g, t0;
+    int nv;
+};
+__device__ __forceinline__ Where where(const ScanBwdArgs& a, int64_t blk) {
+    Where w;
+    w.c = blk % a.chunks;
+    w.h = blk / a.chunks % a.H;
+    w.b = blk / a.chunks / a.H;
+    w.g = w.h / (a.H / a.G);
+    w.t0 = w.c * kQ;
+    w.nv = a.L - w.t0 < kQ ? static_cast<int>(a.L - w.t0) : kQ;
+    return w;
+}
+
+// A row-major view [tokens][cols] of the chunk's tokens: zeros outside.
+template <class S>
+struct View {
+    const typename S::T* p;
+    int64_t row;
+    int rows, cols;
+    __device__ __forceinline__ float at(int r, int c) const {
+        return r < rows && c < cols ? S::load(p, r * row + c) : 0.0f;
+    }
+    // operand with the contraction along the row: row r, columns k .. k + 3
+    __device__ __forceinline__ f4 along(int r, int k) const {
+        return f4{at(r, k), at(r, k + 1), at(r, k + 2), at(r, k + 3)};
+    }
+    // operand with the contraction over the rows: rows k .. k + 3 of column c
+    __device__ __forceinline__ f4 down(int k, int c) const {
+        return f4{at(k, c), at(k + 1, c), at(k + 2, c), at(k + 3, c)};
+    }
+};
+
+// ---------------------------------------------------------------------------------------
+// each chunk's share of the next S (blockIdx.y = 0) and of the previous G (blockIdx.y = 1)
+// ---------------------------------------------------------------------------------------
+template <class S>
+__global__ void __launch_bounds__(256) sb_local_kernel(ScanBwdArgs a) {
+    __shared__ ChunkDecay cd;
+    const Where w = where(a, blockIdx.x);
+    const bool rev = blockIdx.y != 0;
+    chunk_decay(cd, a.dt + (w.b * a.L + w.t0) * a.H + w.h, a.H, a.A[w.h],
+                a.seq ? a.seq + w.b * a.L : nullptr, w.t0, w.nv);
+    using T = typename S::T;
+    const int64_t tok = w.b * a.L + w.t0;
+    const int P = static_cast<int>(a.P), N = static_cast<int>(a.N);
+    const View<S> xv{static_cast<const T*>(rev ? a.dy : a.x) + tok * (rev ? a.dy_row : a.x_row) + w.h * P,
+                     rev ? a.dy_row : a.x_row, w.nv, P};
+    const View<S> bv{static_cast<const T*>(rev ? a.C : a.Bm) + tok * (rev ? a.c_row : a.b_row) + w.g * N,
+                     rev ? a.c_row : a.b_row, w.nv, N};
+    float* out = (rev ? a.grads : a.states) + ((w.b * a.H + w.h) * a.chunks + w.c) * a.P * a.N;
+    const int lane = threadIdx.x & 63, li = lane & 15, g4 = lane >> 4;
+    const int np = (P + 15) / 16, nn = (N + 15) / 16;
+    for (int tile = threadIdx.x >> 6; tile < np * nn; tile += 4) {
+        const int p0 = tile / nn * 16, n0 = tile % nn * 16;
+        f4 acc{0, 0, 0, 0};
+        for (int k = 0; k < kQ; k += 16) {
+            f4 x = xv.down(k + 4 * g4, p0 + li);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int t = k + 4 * g4 + j;
+                x[j] *= rev ? cd.f[t] : cd.dt[t] * cd.e[t];
+            }
+            acc = mfma4(x, bv.down(k + 4 * g4, n0 + li), acc);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int p = p0 + 4 * g4 + e, n = n0 + li;
+            if (p < P && n < N) out[p * N + n] = acc[e];
+        }
+    }
+}
+
+// f_last of every chunk
+__global__ void __launch_bounds__(64) sb_through_kernel(ScanBwdArgs a) {
+    __shared__ ChunkDecay cd;
+    const Where w = where(a, blockIdx.x);
+    chunk_decay(cd, a.dt + (w.b * a.L + w.t0) * a.H + w.h, a.H, a.A[w.h],
+                a.seq ? a.seq + w.b * a.L : nullptr, w.t0, w.nv);
+    if (threadIdx.x == 0) a.through[(w.b * a.H + w.h) * a.chunks + w.c] = cd.through;
+}
+
+// Sums along the row, in place: the share of chunk c becomes the state before it (blockIdx.y =
+// 0), or the gradient of the state after it (1, which also gives the initial state's).  A
+// chunk that holds a start takes nothing over, whatever the state was.
+__global__ void __launch_bounds__(256) sb_pass_kernel(ScanBwdArgs a) {
+    const int64_t PN = a.P * a.N, per = (PN + 255) / 256;
+    const int64_t bh = blockIdx.x / per, i = blockIdx.x % per * 256 + threadIdx.x;
+    if (i >= PN) return;
+    const bool rev = blockIdx.y != 0;
+    float* s = (rev ? a.grads : a.states) + bh * a.chunks * PN + i;
+    const float* f = a.through + bh * a.chunks;
+    const float* from = rev ? a.dhT : a.h0;
+    float v = from ? from[bh * PN + i] : 0.0f;
+    for (int64_t j = 0; j < a.chunks; ++j) {
+        const int64_t c = rev ? a.chunks - 1 - j : j;
+        const float own = s[c * PN], th = f[c];
+        s[c * PN] = v;
+        v = th == 0.0f ? own : th * v + own;
+    }
+    if (rev && a.dh0) a.dh0[bh * PN + i] = v;
+}
+
+// ---------------------------------------------------------------------------------------
+// gradients of one chunk and head
+// ---------------------------------------------------------------------------------------
+template <class S>
+__global__ void __launch_bounds__(256) sb_grad_kernel(ScanBwdArgs a) {
+    __shared__ ChunkDecay cd;
+    __shared__ float pair[kQ][kQ + 1];  // [t][s] L_ts (C_t.B_s)
+    __shared__ float lw[kQ][kQ + 1];    // [t][s] L_ts (dy_t.x_s) dt_s
+    __shared__ float rowp[4][kQ];       // sums over the s of one 16-column tile, s < t, of W
+    __shared__ float colp[4][2][kQ];    // sums over the t of one 16-row tile: t > s of W; t >= s of W / dt_s
+    __shared__ float uu[kQ], vv[kQ];    // u_t, v_s / dt_s
+    __shared__ float gs[4];
+    const Where w = where(a, blockIdx.x);
+    chunk_decay(cd, a.dt + (w.b * a.L + w.t0) * a.H + w.h, a.H, a.A[w.h],
+                a.seq ? a.seq + w.b * a.L : nullptr, w.t0, w.nv);
+    using T = typename S::T;
+    const int64_t tok = w.b * a.L + w.t0;
+    const int P = static_cast<int>(a.P), N = static_cast<int>(a.N);
+    const View<S> xv{static_cast<const T*>(a.x) + tok * a.x_row + w.h * P, a.x_row, w.nv, P};
+    const View<S> dyv{static_cast<const T*>(a.dy) + tok * a.dy_row + w.h * P, a.dy_row, w.nv, P};
+    const View<S> bv{static_cast<const T*>(a.Bm) + tok * a.b_row + w.g * N, a.b_row, w.nv, N};
+    const View<S> cv{static_cast<const T*>(a.C) + tok * a.c_row + w.g * N, a.c_row, w.nv, N};
+    const int64_t at = ((w.b * a.H + w.h) * a.chunks + w.c) * a.P * a.N;
+    const View<F32> sv{a.states + at, N, P, N}, gv{a.grads + at, N, P, N};
+    const int lane = threadIdx.x & 63, li = lane & 15, g4 = lane >> 4, wave = threadIdx.x >> 6;
+
+    // pairs s <= t: the ten 16 x 16 tiles on and below the diagonal
+    for (int tile = wave; tile < 10; tile += 4) {
+        const int ti = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3;
+        const int si = tile - ti * (ti + 1) / 2;
+        f4 cb{0, 0, 0, 0}, yx{0, 0, 0, 0};
+        for (int k = 0; k < N; k += 16)
+            cb = mfma4(cv.along(16 * ti + li, k + 4 * g4), bv.along(16 * si + li, k + 4 * g4), cb);
+        for (int k = 0; k < P; k += 16)
+            yx = mfma4(dyv.along(16 * ti + li, k + 4 * g4), xv.along(16 * si + li, k + 4 * g4), yx);
+        const int s = 16 * si + li;
+        const double css = cd.cs[s];
+        const int rs = cd.starts[s];
+        const float dts = cd.dt[s];
+        float below = 0.0f, all = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int t = 16 * ti + 4 * g4 + e;
+            const bool in = t >= s && cd.starts[t] == rs;
+            const float l = in ? __expf(static_cast<float>(cd.cs[t] - css)) : 0.0f;
+            const float pv = in ? l * cb[e] : 0.0f, yv = in ? l * yx[e] * dts : 0.0f;
+            pair[t][s] = pv;
+            lw[t][s] = yv;
+            const float w0 = in ? pv * yx[e] : 0.0f;
+            all += w0;
+            float row = t > s ? w0 * dts : 0.0f;
+            below += row;
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) row += __shfl_xor(row, o);
+            if (li == 0) rowp[si][t] = row;
+        }
+        below += __shfl_xor(below, 16);
+        below += __shfl_xor(below, 32);
+        all += __shfl_xor(all, 16);
+        all += __shfl_xor(all, 32);
+        if (g4 == 0) {
+            colp[ti][0][s] = below;
+            colp[ti][1][s] = all;
+        }
+    }
+    // <G, S>
+    {
+        float d = 0.0f;
+        for (int i = threadIdx.x; i < P * N; i += 256) d += sv.p[i] * gv.p[i];
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) d += __shfl_xor(d, o);
+        if (lane == 0) gs[wave] = d;
+    }
+    __syncthreads();
+
+    // this wavefront's 16 tokens r0 .. r0 + 15 of every output
+    const int r0 = 16 * wave;
+    T* dxo = static_cast<T*>(a.dx) + tok * a.dx_row + w.h * P;
+    float v[4] = {0, 0, 0, 0}, u[4] = {0, 0, 0, 0};
+    for (int p0 = 0; p0 < P; p0 += 16) {
+        f4 in{0, 0, 0, 0}, out{0, 0, 0, 0};
+        for (int k = r0; k < kQ; k += 16) {
+            const int t = k + 4 * g4;
+            in = mfma4(f4{pair[t][r0 + li], pair[t + 1][r0 + li], pair[t + 2][r0 + li], pair[t + 3][r0 + li]},
+                       dyv.down(t, p0 + li), in);
+        }
+        for (int k = 0; k < N; k += 16)
+            out = mfma4(bv.along(r0 + li, k + 4 * g4), gv.along(p0 + li, k + 4 * g4), out);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int s = r0 + 4 * g4 + e, p = p0 + li;
+            const float o = cd.e[s] == 0.0f ? 0.0f : cd.e[s] * out[e];
+            v[e] += xv.at(s, p) * o;
+            if (s < w.nv && p < P) S::store(dxo, s * a.dx_row + p, cd.dt[s] * (in[e] + o));
+        }
+    }
+    const int64_t ho = (tok * a.H + w.h) * N;  // [row][token][head][N]
+    for (int n0 = 0; n0 < N; n0 += 16) {
+        f4 in{0, 0, 0, 0}, out{0, 0, 0, 0}, bin{0, 0, 0, 0}, bout{0, 0, 0, 0};
+        for (int k = 0; k < r0 + 16; k += 16) {
+            const int s = k + 4 * g4;
+            in = mfma4(f4{lw[r0 + li][s], lw[r0 + li][s + 1], lw[r0 + li][s + 2], lw[r0 + li][s + 3]},
+                       bv.down(s, n0 + li), in);
+        }
+        for (int k = r0; k < kQ; k += 16) {
+            const int t = k + 4 * g4;
+            bin = mfma4(f4{lw[t][r0 + li], lw[t + 1][r0 + li], lw[t + 2][r0 + li], lw[t + 3][r0 + li]},
+                        cv.down(t, n0 + li), bin);
+        }
+        for (int k = 0; k < P; k += 16) {
+            out = mfma4(dyv.along(r0 + li, k + 4 * g4), sv.down(k + 4 * g4, n0 + li), out);
+            bout = mfma4(xv.along(r0 + li, k + 4 * g4), gv.down(k + 4 * g4, n0 + li), bout);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int t = r0 + 4 * g4 + e, n = n0 + li;
+            const float o = cd.f[t] == 0.0f ? 0.0f : cd.f[t] * out[e];
+            const float bo = cd.e[t] == 0.0f ? 0.0f : cd.e[t] * cd.dt[t] * bout[e];
+            u[e] += cv.at(t, n) * o;
+            if (t < w.nv && n < N) {
+                a.dC_head[ho + t * a.H * N + n] = in[e] + o;
+                a.dB_head[ho + t * a.H * N + n] = bin[e] + bo;
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) {
+            u[e] += __shfl_xor(u[e], o);
+            v[e] += __shfl_xor(v[e], o);
+        }
+        if (li == 0) {
+            uu[r0 + 4 * g4 + e] = u[e];
+            vv[r0 + 4 * g4 + e] = v[e];
+        }
+    }
+    __syncthreads();
+
+    // q, ddt and the chunk's share of dA (lane = token)
+    if (wave != 0) return;
+    const int t = lane;
+    float row = 0.0f, below = 0.0f, all = 0.0f;
+    for (int i = 0; i <= t / 16; ++i) row += rowp[i][t];
+    for (int i = t / 16; i < 4; ++i) {
+        below += colp[i][0][t];
+        all += colp[i][1][t];
+    }
+    const double vd = static_cast<double>(vv[t]) * cd.dt[t];
+    double q = static_cast<double>(row) - below + uu[t] - vd, vsum = vd;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) vsum += __shfl_xor(vsum, o);
+    if (t == 63) {
+        const float dot = (gs[0] + gs[1]) + (gs[2] + gs[3]);
+        q += vsum + (cd.through == 0.0f ? 0.0 : static_cast<double>(cd.through) * dot);
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const double qo = __shfl_down(q, o);
+        if (t + o < 64) q += qo;
+    }
+    const bool start = cd.starts[t] != (t > 0 ? cd.starts[t - 1] : 0);
+    if (start) q = 0.0;
+    if (t < w.nv)
+        a.ddt[(tok + t) * a.H + w.h] = static_cast<float>(q * a.A[w.h] + (static_cast<double>(all) + vv[t]));
+    double da = t < w.nv ? q * cd.dt[t] : 0.0;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) da += __shfl_xor(da, o);
+    if (t == 0) a.dA_part[(w.b * a.chunks + w.c) * a.H + w.h] = da;
+}
+
+// dB, dC: the heads of a group added in order, rounded once
+template <class S>
+__global__ void __launch_bounds__(256) sb_heads_kernel(ScanBwdArgs a) {
+    using T = typename S::T;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t GN = a.G * a.N;
+    if (i >= a.B * a.L * GN) return;
+    const int64_t k = a.H / a.G, tok = i / GN, g = i % GN / a.N, n = i % a.N;
+    const float* p = (blockIdx.y ? a.dC_head : a.dB_head) + (tok * a.H + g * k) * a.N + n;
+    float s = 0.0f;
+    for (int64_t j = 0; j < k; ++j) s += p[j * a.N];
+    if (blockIdx.y) S::store(static_cast<T*>(a.dC) + tok * a.dc_row, g * a.N + n, s);
+    else S::store(static_cast<T*>(a.dB) + tok * a.db_row, g * a.N + n, s);
+}
+
+// dA: the chunks' shares in a fixed order, in double; one block a head
+__global__ void __launch_bounds__(256) sb_dA_kernel(ScanBwdArgs a) {
+    __shared__ double sum[4];
+    double s = 0.0;
+    for (int64_t i = threadIdx.x; i < a.B * a.chunks; i += 256) s += a.dA_part[i * a.H + blockIdx.x];
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o);
+    if ((threadIdx.x & 63) == 0) sum[threadIdx.x >> 6] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) a.dA[blockIdx.x] = static_cast<float>((sum[0] + sum[1]) + (sum[2] + sum[3]));
+}
+
+template <class S>
+hipError_t launch_general(const ScanBwdArgs& a, hipStream_t s) {
+    const uint32_t bhc = static_cast<uint32_t>(a.B * a.H * a.chunks);
+    sb_through_kernel<<<bhc, 64, 0, s>>>(a);
+    sb_local_kernel<S><<<dim3(bhc, 2), 256, 0, s>>>(a);
+    sb_pass_kernel<<<dim3(static_cast<uint32_t>(a.B * a.H * ((a.P * a.N + 255) / 256)), 2), 256, 0, s>>>(a);
+    sb_grad_kernel<S><<<bhc, 256, 0, s>>>(a);
+    sb_heads_kernel<S><<<dim3(static_cast<uint32_t>((a.B * a.L * a.G * a.N + 255) / 256), 2), 256, 0, s>>>(a);
+    sb_dA_kernel<<<static_cast<uint32_t>(a.H), 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+size_t r256(size_t n) { return (n + 255) / 256 * 256; }
+
+// places the workspace's parts; returns its size
+size_t lay_out(ScanBwdArgs& a, uint8_t* base) {
+    size_t at = 0;
+    auto part = [&](auto*& p, size_t n) {
+        p = reinterpret_cast<std::remove_reference_t<decltype(p)>>(base + at);
+        at += r256(n * sizeof(*p));
+    };
+    const size_t bh = static_cast<size_t>(a.B * a.H), bhc = bh * a.chunks;
+    part(a.dA_part, bhc);
+    part(a.through, bhc);
+    part(a.states, bhc * a.P * a.N);
+    part(a.grads, bhc * a.P * a.N);
+    part(a.dB_head, bh * a.L * a.N);
+    part(a.dC_head, bh * a.L * a.N);
+    return at;
+}
+
+}  // namespace
+
+size_t scan_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N,
+                                ssm_dtype_t) {
+    ScanBwdArgs a{};
+    a.B = B; a.L = L; a.H = H; a.P = P; a.G = G; a.N = N;
+    a.chunks = (L + kQ - 1) / kQ;
+    return lay_out(a, nullptr);
+}
+
+// blocks of the largest launch, against the grid's limit
+int64_t scan_bwd_blocks(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N) {
+    const int64_t a = B * H * ((L + kQ - 1) / kQ), b = B * H * ((P * N + 255) / 256);
+    const int64_t c = (B * L * G * N + 255) / 256;
+    return a > b ? (a > c ? a : c) : (b > c ? b : c);
+}
+
+hipError_t launch_scan_bwd(ScanBwdArgs a, void* workspace, ssm_dtype_t dtype, hipStream_t s) {
+    a.chunks = (a.L + kQ - 1) / kQ;
+    lay_out(a, static_cast<uint8_t*>(workspace));
+    return dtype == SSM_BF16 ? launch_general<BF16>(a, s) : launch_general<F32>(a, s);
+}
+
+// no tokens: the initial state's gradient is the final state's, dA = 0
+__global__ void sb_empty_kernel(const float* dhT, float* dh0, float* dA, int64_t n, int64_t H) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i < H) dA[i] = 0.0f;
+    if (dh0 && i < n) dh0[i] = dhT ? dhT[i] : 0.0f;
+}
+hipError_t launch_scan_bwd_empty(const float* dhT, float* dh0, float* dA, int64_t n, int64_t H,
+                                 hipStream_t s) {
+    const int64_t m = n > H ? n : H;
+    sb_empty_kernel<<<static_cast<uint32_t>((m + 255) / 256), 256, 0, s>>>(dhT, dh0, dA, n, H);
+    return hipGetLastError();
+}
+
+}  // namespace ssm

@@ -164,3 +164,65 @@ def test_gated_scan_binding_refusals():
         ssm.gated_scan_bwd(x, x, x, form="tanh")
     with pytest.raises(ValueError, match="batch, tokens, channels"):
         ssm.gated_scan_step(x[0], x[0], x[0])
+
+
+def _sbwd(lib, x=P, dt=P, A=P, B=P, C=P, dy=P, h0=None, f=None, seq=None, dx=P, ddt=P, dA=P, dB=P,
+          dC=P, dh0=None, b=2, L=100, H=4, hd=64, G=1, N=128, dtype=1, ws=P, wsb=1 << 40):
+    return lib.ssm_scan_bwd(x, dt, A, B, C, dy, h0, f, seq, dx, ddt, dA, dB, dC, dh0, b, L, H, hd, G, N,
+                            dtype, ws, wsb, None)
+
+
+def test_scan_bwd_refusals(lib):
+    for status, how in ((1, dict(dtype=5)), (1, dict(b=-1)), (1, dict(L=-1)), (1, dict(H=0)), (1, dict(G=3)),
+                        (2, dict(N=6)), (2, dict(hd=512, N=128)), (2, dict(b=1 << 31)), (2, dict(L=1 << 40)),
+                        (2, dict(b=1 << 25, L=1 << 25)), (1, dict(x=None)), (1, dict(dy=None)),
+                        (1, dict(dA=None)), (1, dict(dx=None)), (1, dict(ddt=None)), (1, dict(dB=None)),
+                        (3, dict(x=ODD)), (3, dict(h0=ctypes.c_void_p(264))), (1, dict(f=P, dh0=P)),
+                        (4, dict(ws=None)), (4, dict(wsb=1000)), (4, dict(ws=ctypes.c_void_p(128)))):
+        assert _sbwd(lib, **how) == status, how
+        assert lib.ssm_last_error()
+
+
+def test_scan_bwd_workspace(lib):
+    import ssm_sequence_models_amd as s
+    for dims in ((1, 64, 1, 4, 1, 4), (4, 8192, 64, 64, 1, 128), (1, 131072, 48, 64, 1, 128)):
+        assert s.scan_bwd_workspace_size(*dims) > 0
+    assert s.scan_bwd_workspace_size(0, 64, 1, 4, 1, 4) == 0
+    assert s.scan_bwd_workspace_size(1, 64, 3, 4, 2, 4) == 0
+    assert s.scan_bwd_workspace_size(1, 64, 1, 4, 1, 6) == 0
+
+
+def test_scan_bwd_binding_refusals():
+    import ssm_sequence_models_amd as ssm
+    x, dt, A, B = torch.zeros(1, 4, 2, 8), torch.zeros(1, 4, 2), torch.zeros(2), torch.zeros(1, 4, 1, 8)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        ssm.scan_bwd(x, dt, A, B, B, x)
+
+
+def test_gated64_and_scan64_against_torch():
+    """The plain forms' gradients against torch's differentiation of the plain forward."""
+    from train_ref import gated64, scan_bwd64, scan_loss64
+    g = torch.Generator().manual_seed(4)
+    r = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)  # noqa: E731
+    seq = torch.tensor([[0, 0, 1, 1, 1, 0, 0, 2, 2, 2, 2, 2]], dtype=torch.int32)
+    i = dict(x=r(1, 12, 4, 3), dt=r(1, 12, 4).abs(), A=-r(4).abs(), Bm=r(1, 12, 2, 4), Cm=r(1, 12, 2, 4),
+             dy=r(1, 12, 4, 3), h0=r(1, 4, 3, 4), dhT=r(1, 4, 3, 4), seq=seq)
+    ref = scan_bwd64(**i)
+    leaf = {k: v.clone().requires_grad_() if k not in ("dy", "dhT", "seq") else v for k, v in i.items()}
+    scan_loss64(**leaf).backward()
+    for name, k in (("dx", "x"), ("ddt", "dt"), ("dA", "A"), ("dB", "Bm"), ("dC", "Cm"), ("dh0", "h0")):
+        assert torch.allclose(leaf[k].grad, ref[name], rtol=1e-10, atol=1e-12), name
+    for form in ("log", "sigmoid"):
+        x, gate, dy, h0, dhT = r(1, 12, 3), r(1, 12, 3) * 0.5, r(1, 12, 3), r(1, 3), r(1, 3)
+        ref = gated64(x, gate, form, h0, seq, dy, dhT)
+        xs, gs, hs = (v.clone().requires_grad_() for v in (x, gate, h0))
+        h, loss = hs, 0.0
+        for t in range(12):
+            a = torch.exp(gs[:, t]) if form == "log" else torch.sigmoid(gs[:, t])
+            u = xs[:, t] * (1.0 if form == "log" else 1 - a)
+            start = t > 0 and int(seq[0, t]) != int(seq[0, t - 1])
+            h = u if start else a * h + u
+            loss = loss + (h * dy[:, t]).sum()
+        (loss + (h * dhT).sum()).backward()
+        for name, v in (("dx", xs), ("dgate", gs), ("dh0", hs)):
+            assert torch.allclose(v.grad, ref[name], rtol=1e-10, atol=1e-12), (form, name)

@@ -141,3 +141,82 @@ def gated64(x, gate, form, h0=None, seq=None, dy=None, dhT=None):
 def check_err(got, ref, name, dtype):
     h = half_step(dtype)
     assert_bound(got, ref[name], h * ref[name].abs() + (1 + h) * ref[name + "_err"], name)
+
+
+# ---------------------------------------------------------------------------------------
+# the scan's backward
+# ---------------------------------------------------------------------------------------
+def _scan_tokens(x, dt, a, Bh, Ch, dy, h0, dhT):
+    """States h_t, gradients g_t [B, L, H, P, N] and the gradient handed to h_{-1}, token by
+    token (all float64; a [B, L, H] with 0 at the starts)."""
+    B, L, H, P = x.shape
+    N = Bh.shape[-1]
+    h = h0
+    hs, gs = (torch.empty(B, L, H, P, N, dtype=torch.float64) for _ in range(2))
+    prev = torch.empty_like(hs)
+    for t in range(L):
+        prev[:, t] = h
+        h = a[:, t, :, None, None] * h + (dt[:, t, :, None] * x[:, t])[..., None] * Bh[:, t, :, None, :]
+        hs[:, t] = h
+    g = dhT
+    for t in range(L - 1, -1, -1):
+        gs[:, t] = g + dy[:, t, :, :, None] * Ch[:, t, :, None, :]
+        g = a[:, t, :, None, None] * gs[:, t]
+    return hs, prev, gs, g
+
+
+def scan_bwd64(x, dt, A, Bm, Cm, dy, h0=None, dhT=None, seq=None):
+    """dx, ddt, dA, dB, dC, dh0 from the definition, token by token, and for each the magnitude
+    its fp32 error scales with (`*_mag`).  The magnitudes come from the same recurrences over
+    absolute values; q = dL/d log a is formed from sums over a 64-token chunk that cancel, so
+    its magnitude is what the whole chunk adds up."""
+    B, L, H, P = x.shape
+    G, N = Bm.shape[2:]
+    k = H // G
+    x, dt, A, dy = x.double(), dt.double(), A.double(), dy.double()
+    Bh, Ch = (v.double().repeat_interleave(k, 2) for v in (Bm, Cm))
+    z = torch.zeros(B, H, P, N, dtype=torch.float64)
+    h0 = z if h0 is None else h0.double()
+    dhT = z if dhT is None else dhT.double()
+    st = starts_of(seq, B, L)
+    a = torch.exp(dt * A).masked_fill(st[..., None], 0.0)
+
+    def grads(x, dt, Bh, Ch, dy, h0, dhT):
+        hs, prev, gs, g = _scan_tokens(x, dt, a, Bh, Ch, dy, h0, dhT)
+        gB = (gs * Bh[..., None, :]).sum(-1)
+        q = a * (gs * prev).sum((-1, -2))
+        group = lambda v: v.view(B, L, G, k, N).sum(3)  # noqa: E731
+        r = dict(dx=dt[..., None] * gB, direct=(x * gB).sum(-1), q=q, dh0=g,
+                 dB=group(((dt[..., None] * x)[..., None] * gs).sum(3)),
+                 dC=group((dy[..., None] * hs).sum(3)))
+        r["Y"] = (dy * (hs * Ch[..., None, :]).sum(-1)).sum(-1)
+        r["through"] = q  # <g_t, a_t h_{t-1}> bounds what passes through the chunk
+        return r
+    r = grads(x, dt, Bh, Ch, dy, h0, dhT)
+    m = grads(x.abs(), dt.abs(), Bh.abs(), Ch.abs(), dy.abs(), h0.abs(), dhT.abs())
+    r["ddt"] = r["direct"] + A * r["q"]
+    r["dA"] = (dt * r["q"]).sum((0, 1))
+    each = m["Y"] + 2 * m["direct"] * dt.abs() + m["q"]
+    qm = torch.empty_like(each)
+    for t0 in range(0, L, 64):
+        qm[:, t0:t0 + 64] = each[:, t0:t0 + 64].sum(1, keepdim=True)
+    out = {n: r[n] for n in ("dx", "ddt", "dA", "dB", "dC", "dh0")}
+    for n in ("dx", "dB", "dC", "dh0"):
+        out[n + "_mag"] = m[n]
+    out["ddt_mag"] = m["direct"] + A.abs() * qm
+    out["dA_mag"] = (dt.abs() * qm).sum((0, 1))
+    return out
+
+
+def scan_loss64(x, dt, A, Bm, Cm, dy, h0, dhT, seq):
+    """sum(y dy) + sum(final dfinal), differentiable by torch, token by token in float64."""
+    B, L, H, P = x.shape
+    k = H // Bm.shape[2]
+    Bh, Ch = Bm.repeat_interleave(k, 2), Cm.repeat_interleave(k, 2)
+    st = starts_of(seq, B, L)
+    h, loss = h0, 0.0
+    for t in range(L):
+        a = torch.exp(dt[:, t] * A).masked_fill(st[:, t, None], 0.0)
+        h = a[..., None, None] * h + (dt[:, t, :, None] * x[:, t])[..., None] * Bh[:, t, :, None, :]
+        loss = loss + ((h * Ch[:, t, :, None, :]).sum(-1) * dy[:, t]).sum()
+    return loss + (h * dhT).sum()
