@@ -309,13 +309,22 @@ struct ScanBwdArgs {
     float* through;    // [B, H, chunks]
     float* states;     // [B, H, chunks, P, N]: the state before each chunk
     float* grads;      // [B, H, chunks, P, N]: the gradient of the state after it
-    float* dB_head;    // [B, L, H, N]
+    float* dB_head;    // [B, L, H, N]; on the matrix cores [splits, B, L, G, N]
     float* dC_head;
+    // matrix cores only
+    float* decay;      // [B, H, chunks, 5, 128]: sums of log2 a (hi, lo), f, e, dt
+    int32_t* starts;   // [B, chunks, 128]: sequence starts so far in the chunk
+    int64_t splits, split_heads;  // ranges of a group's heads a chunk, heads in each
 };
 size_t scan_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N,
                                 ssm_dtype_t dtype);
 int64_t scan_bwd_blocks(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N);
 hipError_t launch_scan_bwd(ScanBwdArgs a, void* workspace, ssm_dtype_t dtype, hipStream_t stream);
+// bf16, headdim 64, dstate 64 or 128
+bool scan_bwd_mfma_supported(int64_t P, int64_t N, ssm_dtype_t dtype);
+size_t scan_bwd_mfma_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N);
+hipError_t launch_scan_bwd_mfma(ScanBwdArgs a, void* workspace, hipStream_t stream);
+hipError_t launch_scan_bwd_dA(const ScanBwdArgs& a, hipStream_t stream);  // dA from dA_part
 hipError_t launch_scan_bwd_empty(const float* dhT, float* dh0, float* dA, int64_t n, int64_t H,
                                  hipStream_t stream);
 hipError_t launch_pool_gather(const void* conv_pool, const float* ssm_pool, const int32_t* indices,

@@ -398,8 +398,8 @@ hipError_t launch_general(const ScanBwdArgs& a, hipStream_t s) {
     sb_pass_kernel<<<dim3(static_cast<uint32_t>(a.B * a.H * ((a.P * a.N + 255) / 256)), 2), 256, 0, s>>>(a);
     sb_grad_kernel<S><<<bhc, 256, 0, s>>>(a);
     sb_heads_kernel<S><<<dim3(static_cast<uint32_t>((a.B * a.L * a.G * a.N + 255) / 256), 2), 256, 0, s>>>(a);
-    sb_dA_kernel<<<static_cast<uint32_t>(a.H), 256, 0, s>>>(a);
-    return hipGetLastError();
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? launch_scan_bwd_dA(a, s) : e;
 }
 
 size_t r256(size_t n) { return (n + 255) / 256 * 256; }
@@ -423,8 +423,14 @@ size_t lay_out(ScanBwdArgs& a, uint8_t* base) {
 
 }  // namespace
 
+hipError_t launch_scan_bwd_dA(const ScanBwdArgs& a, hipStream_t s) {
+    sb_dA_kernel<<<static_cast<uint32_t>(a.H), 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
 size_t scan_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N,
-                                ssm_dtype_t) {
+                                ssm_dtype_t dtype) {
+    if (scan_bwd_mfma_supported(P, N, dtype)) return scan_bwd_mfma_workspace_bytes(B, L, H, P, G, N);
     ScanBwdArgs a{};
     a.B = B; a.L = L; a.H = H; a.P = P; a.G = G; a.N = N;
     a.chunks = (L + kQ - 1) / kQ;
@@ -439,6 +445,7 @@ int64_t scan_bwd_blocks(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, i
 }
 
 hipError_t launch_scan_bwd(ScanBwdArgs a, void* workspace, ssm_dtype_t dtype, hipStream_t s) {
+    if (scan_bwd_mfma_supported(a.P, a.N, dtype)) return launch_scan_bwd_mfma(a, workspace, s);
     a.chunks = (a.L + kQ - 1) / kQ;
     lay_out(a, static_cast<uint8_t*>(workspace));
     return dtype == SSM_BF16 ? launch_general<BF16>(a, s) : launch_general<F32>(a, s);

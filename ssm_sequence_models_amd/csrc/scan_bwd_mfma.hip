@@ -1,0 +1,826 @@
+// scan_bwd_mfma.hip -- the complete backward of the selective scan on the bf16 matrix cores:
+// bf16 activations, headdim 64, dstate 64 or 128 (the formulas stand in scan_bwd.hip).
+//
+// Chunks of Q = 128 tokens: the states before the chunks and the gradients after them are 8 N
+// bytes a channel and chunk, written once and read once, and are the larger part of the
+// traffic; twice the chunk halves them and costs only more pairs within the chunk.
+//
+//   sbf_decay   one pass over dt: for each head and chunk the sums of log2 a in double, kept as
+//               hi + lo floats, f_t, e_t, dt_t and f_last
+//   sbf_states  S and G, one block a row, head and direction walking over the chunks with the
+//               state in accumulators (or, where those are too few blocks, one block a chunk,
+//               joined along the row by sbf_pass)
+//   sbf_grad    one block a chunk, group and range of its heads: everything else.  B and C stay
+//               in LDS and C B^T in registers for all heads; the sums over heads of
+//               L dt (dy x^T), from which dB and dC take their pairs, stay in registers as
+//               well, and dB and dC in accumulators: they are summed over the heads without
+//               traffic.  Ranges of heads are joined by sbf_join (in order).
+//
+// Operands: x, dy, B and C are exact in bf16.  The fp32 operands S and G and the scaled x and dy
+// of sbf_states are taken in three bf16 parts (24 bits, nothing lost: ddt and dA are fp32
+// outputs formed from the same products); where only bf16 outputs depend on an operand (the
+// pairs of dx, G of dx, the pairs of dB and dC) two parts do (2^-17 of the operand).
+//
+// Layouts of the 16 x 16 x 32 instruction: A lane (row li, k 8 g4 ..), B lane (column li, k
+// 8 g4 ..), result lane (column li, rows 4 g4 ..), li = lane % 16, g4 = lane / 16.  A result
+// whose rows are the next product's contraction is that product's operand as it stands, with
+// k running 4 g4 + e over one 16-row tile and 16 + 4 g4 + e over the next ("token order"
+// below); the transposing LDS read (4 rows of 16 columns a 16-lane group) gives the other
+// operand in the same order.  So pairs never pass through LDS.
+#include "internal.h"
+
+namespace ssm {
+namespace {
+
+constexpr int kFQ = 128;
+constexpr int kFP = 64;
+
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u4any __attribute__((ext_vector_type(4), aligned(2)));  // any bf16 address
+typedef uint32_t u2any __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ f4 mfma(bf8 a, bf8 b, f4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// v = sum of its parts in bf16, each the rounded rest: PARTS = 3 leaves nothing of 24 bits
+template <int PARTS>
+__device__ __forceinline__ void split(const float (&v)[8], bf8 (&part)[PARTS]) {
+    u4 w[PARTS];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a = v[2 * i], b = v[2 * i + 1];
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) {
+            const uint32_t q = pack_bf16x2(a, b);
+            w[k][i] = q;
+            if (k + 1 < PARTS) {
+                a -= __uint_as_float(q << 16);
+                b -= __uint_as_float(q & 0xFFFF0000u);
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) part[k] = __builtin_bit_cast(bf8, w[k]);
+}
+
+// LDS tiles of bf16: rows of RB bytes in 16-byte pieces, the piece index XORed with sw(row), so
+// that 8 rows' equal pieces (operand reads along rows) and 4 rows' neighbouring pairs of pieces
+// (transposing reads) fall into different banks.
+__device__ __forceinline__ int sw(int row) { return ((row & 3) << 1) | ((row >> 2) & 1); }
+template <int RB>
+__device__ __forceinline__ int piece(int row, int q) { return row * RB + ((q ^ sw(row)) << 4); }
+
+template <class T>
+__device__ __forceinline__ T lds(const uint8_t* p) { return *reinterpret_cast<const T*>(p); }
+
+// operand read along rows: row r0 + li, k = 32 kk + 8 g4 ..
+template <int RB>
+__device__ __forceinline__ bf8 along(const uint8_t* tile, int lane_off, int r0, int kk) {
+    return lds<bf8>(tile + r0 * RB + (lane_off ^ (kk << 6)));
+}
+template <int RB>
+__device__ __forceinline__ int along_off(int li, int g4) { return piece<RB>(li, g4); }
+
+__device__ __forceinline__ s4 tr_read(const uint8_t* p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) s4*)const_cast<uint8_t*>(p));
+}
+// lane offset of a transposing read of rows r .. r + 3 (r = 4 x group) and columns 0 .. 15
+template <int RB>
+__device__ __forceinline__ int down_off(int r, int li) {
+    const int row = r + (li >> 2);
+    return piece<RB>(row, (li & 3) >> 1) + 8 * (li & 1);
+}
+__device__ __forceinline__ bf8 join(s4 a, s4 b) {
+    const u2 x = __builtin_bit_cast(u2, a), y = __builtin_bit_cast(u2, b);
+    return __builtin_bit_cast(bf8, u4{x[0], x[1], y[0], y[1]});
+}
+// operand read down rows in token order: rows r0 + 4 g4 .. and r0 + 16 + 4 g4 .. (r0 = 32 x), of
+// columns 16 c ..
+template <int RB>
+__device__ __forceinline__ bf8 down(const uint8_t* tile, int lane_off, int r0, int c) {
+    const uint8_t* p = tile + r0 * RB + (lane_off ^ (c << 5));
+    return join(tr_read(p), tr_read(p + 16 * RB));
+}
+
+__device__ __forceinline__ float lane_sum16(float v) {  // over the 16 lanes that share g4
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xf, 0xf, true));   // i ^ 1
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xf, 0xf, true));   // i ^ 2
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xf, 0xf, true));  // half mirror
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 0xf, 0xf, true));  // mirror
+    return v;
+}
+__device__ __forceinline__ float group_sum4(float v) {  // over the four lanes that share li
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+
+// ---------------------------------------------------------------------------------------
+// decays
+// ---------------------------------------------------------------------------------------
+// Block: one row, chunk and 16 heads; dt is turned over in LDS, then a wavefront does four heads,
+// two tokens a lane.
+__global__ void __launch_bounds__(256) sbf_decay_kernel(ScanBwdArgs a) {
+    __shared__ float dts[16][kFQ + 1];
+    const int64_t hb = (a.H + 15) / 16;
+    const int64_t h0 = blockIdx.x % hb * 16, c = blockIdx.x / hb % a.chunks, b = blockIdx.x / hb / a.chunks;
+    const int64_t t0 = c * kFQ;
+    const int nv = a.L - t0 < kFQ ? static_cast<int>(a.L - t0) : kFQ;
+    for (int i = threadIdx.x; i < 16 * kFQ; i += 256) {
+        const int h = i & 15, t = i >> 4;
+        dts[h][t] = t < nv && h0 + h < a.H ? a.dt[(b * a.L + t0 + t) * a.H + h0 + h] : 0.0f;
+    }
+    __syncthreads();
+    const int lane = threadIdx.x & 63;
+    const int32_t* seq = a.seq ? a.seq + b * a.L + t0 : nullptr;
+    int start[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int t = lane + 64 * k;
+        if (seq && t < nv && t0 + t > 0) start[k] = seq[t] != seq[t - 1];
+    }
+    int r0 = start[0], r1 = start[1];
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int u0 = __shfl_up(r0, o), u1 = __shfl_up(r1, o);
+        if (lane >= o) {
+            r0 += u0;
+            r1 += u1;
+        }
+    }
+    r1 += __shfl(r0, 63);
+    const int rend = __shfl(r1, 63);
+    if (h0 == 0 && threadIdx.x < 64) {
+        a.starts[(b * a.chunks + c) * kFQ + lane] = r0;
+        a.starts[(b * a.chunks + c) * kFQ + 64 + lane] = r1;
+    }
+    for (int j = 0; j < 4; ++j) {
+        const int h = (threadIdx.x >> 6) + 4 * j;
+        if (h0 + h >= a.H) break;
+        const double A2 = static_cast<double>(a.A[h0 + h]) * 1.4426950408889634;
+        const float d0 = dts[h][lane], d1 = dts[h][64 + lane];
+        double s0 = d0 * A2, s1 = d1 * A2;
+        // a = 0 in fp32 by far: the sums keep what follows
+        if (s0 < -1500.0) s0 = -1500.0;
+        if (s1 < -1500.0) s1 = -1500.0;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const double u0 = __shfl_up(s0, o), u1 = __shfl_up(s1, o);
+            if (lane >= o) {
+                s0 += u0;
+                s1 += u1;
+            }
+        }
+        s1 += __shfl(s0, 63);
+        const double end = __shfl(s1, 63);
+        const int64_t bh = b * a.H + h0 + h;
+        float* rec = a.decay + (bh * a.chunks + c) * 5 * kFQ;
+        auto put = [&](int t, double s, int r, float d) {
+            const float hi = static_cast<float>(s);
+            rec[t] = hi;
+            rec[kFQ + t] = static_cast<float>(s - hi);
+            rec[2 * kFQ + t] = r == 0 ? __builtin_amdgcn_exp2f(hi) : 0.0f;
+            rec[3 * kFQ + t] = r == rend ? __builtin_amdgcn_exp2f(static_cast<float>(end - s)) : 0.0f;
+            rec[4 * kFQ + t] = d;
+        };
+        put(lane, s0, r0, d0);
+        put(64 + lane, s1, r1, d1);
+        if (lane == 63) a.through[bh * a.chunks + c] = r1 == 0 ? __builtin_amdgcn_exp2f(static_cast<float>(s1)) : 0.0f;
+    }
+}
+
+// ---------------------------------------------------------------------------------------
+// states before the chunks (forward) and gradients after them (reverse)
+// ---------------------------------------------------------------------------------------
+// Block: row, head, direction; wavefront w holds channels 16 w .. of the state as result tiles
+// [p][n].  Stored [n][p]: four channels a lane, and the order sbf_grad's operands have.
+// SEQ: the chunks in turn; else one chunk's own share.
+template <int N, bool SEQ>
+__global__ void __launch_bounds__(256) sbf_states_kernel(ScanBwdArgs a) {
+    constexpr int NT = N / 16, RB = 2 * N, BP = N / 8;  // n tiles, row bytes and pieces of B
+    constexpr int BL = kFQ * BP / 256, XL = kFQ * 8 / 256;
+    __shared__ __attribute__((aligned(16))) uint8_t sb[kFQ * RB];
+    __shared__ __attribute__((aligned(16))) uint8_t sx[kFQ * 128];
+    __shared__ __attribute__((aligned(16))) float scale[kFQ];
+    const bool rev = blockIdx.y != 0;
+    const int64_t per = SEQ ? 1 : a.chunks;
+    const int64_t bh = blockIdx.x / per, b = bh / a.H, h = bh % a.H, g = h / (a.H / a.G);
+    const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g4 = lane >> 4, w = tid >> 6;
+    const uint16_t* xs = static_cast<const uint16_t*>(rev ? a.dy : a.x) + b * a.L * (rev ? a.dy_row : a.x_row) + h * kFP;
+    const uint16_t* bs = static_cast<const uint16_t*>(rev ? a.C : a.Bm) + b * a.L * (rev ? a.c_row : a.b_row) + g * N;
+    const int64_t x_row = rev ? a.dy_row : a.x_row, b_row = rev ? a.c_row : a.b_row;
+    float* out = (rev ? a.grads : a.states) + bh * a.chunks * N * kFP;
+
+    u4 rb[BL], rx[XL];
+    float rs = 0.0f;
+    auto load = [&](int64_t c) __attribute__((always_inline)) {
+        const int64_t t0 = c * kFQ;
+#pragma unroll
+        for (int i = 0; i < XL; ++i) {
+            const int q = tid + 256 * i, row = q >> 3;
+            rx[i] = u4{0, 0, 0, 0};
+            if (t0 + row < a.L) rx[i] = *reinterpret_cast<const u4any*>(xs + (t0 + row) * x_row + 8 * (q & 7));
+        }
+#pragma unroll
+        for (int i = 0; i < BL; ++i) {
+            const int q = tid + 256 * i, row = q / BP;
+            rb[i] = u4{0, 0, 0, 0};
+            if (t0 + row < a.L) rb[i] = *reinterpret_cast<const u4any*>(bs + (t0 + row) * b_row + 8 * (q % BP));
+        }
+        if (tid < kFQ) {
+            const float* rec = a.decay + (bh * a.chunks + c) * 5 * kFQ + tid;
+            rs = rev ? rec[2 * kFQ] : rec[3 * kFQ] * rec[4 * kFQ];
+        }
+    };
+    const int64_t steps = SEQ ? a.chunks : 1;
+    const int64_t c0 = SEQ ? (rev ? a.chunks - 1 : 0) : blockIdx.x % per, dc = rev ? -1 : 1;
+    load(c0);
+    f4 acc[NT];
+    const float* from = SEQ ? (rev ? a.dhT : a.h0) : nullptr;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            acc[n][e] = from ? from[(bh * kFP + 16 * w + 4 * g4 + e) * N + 16 * n + li] : 0.0f;
+    const int xo = down_off<128>(4 * g4, li) ^ (w << 5), bo = down_off<RB>(4 * g4, li);
+    for (int64_t i = 0; i < steps; ++i) {
+        const int64_t c = c0 + i * dc;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < XL; ++j) {
+            const int q = tid + 256 * j;
+            *reinterpret_cast<u4*>(sx + piece<128>(q >> 3, q & 7)) = rx[j];
+        }
+#pragma unroll
+        for (int j = 0; j < BL; ++j) {
+            const int q = tid + 256 * j;
+            *reinterpret_cast<u4*>(sb + piece<RB>(q / BP, q % BP)) = rb[j];
+        }
+        if (tid < kFQ) scale[tid] = rs;
+        __syncthreads();
+        if (i + 1 < steps) load(c + dc);
+        if (SEQ) {
+            float* o = out + c * N * kFP + 16 * w + 4 * g4;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) *reinterpret_cast<f4*>(o + (16 * n + li) * kFP) = acc[n];
+            const float th = a.through[bh * a.chunks + c];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[n][e] = th == 0.0f ? 0.0f : acc[n][e] * th;
+        }
+#pragma unroll
+        for (int k = 0; k < kFQ / 32; ++k) {
+            const u4 raw = __builtin_bit_cast(u4, down<128>(sx, xo, 32 * k, 0));
+            const f4 s0 = *reinterpret_cast<const f4*>(scale + 32 * k + 4 * g4);
+            const f4 s1 = *reinterpret_cast<const f4*>(scale + 32 * k + 16 + 4 * g4);
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[2 * e] = __uint_as_float(raw[e] << 16) * (e < 2 ? s0[2 * e] : s1[2 * e - 4]);
+                v[2 * e + 1] = __uint_as_float(raw[e] & 0xFFFF0000u) * (e < 2 ? s0[2 * e + 1] : s1[2 * e - 3]);
+            }
+            bf8 p[3];
+            split(v, p);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const bf8 q = down<RB>(sb, bo, 32 * k, n);
+#pragma unroll
+                for (int j = 2; j >= 0; --j) acc[n] = mfma(p[j], q, acc[n]);
+            }
+        }
+        if (!SEQ) {
+            float* o = out + c * N * kFP + 16 * w + 4 * g4;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) *reinterpret_cast<f4*>(o + (16 * n + li) * kFP) = acc[n];
+        }
+    }
+    if (SEQ && rev && a.dh0) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a.dh0[(bh * kFP + 16 * w + 4 * g4 + e) * N + 16 * n + li] = acc[n][e];
+    }
+}
+
+// The chunks' shares summed along the row, in place (states stored [n][p], the caller's [p][n])
+__global__ void __launch_bounds__(256) sbf_pass_kernel(ScanBwdArgs a) {
+    const int64_t PN = kFP * a.N, per = PN / 256;
+    const int64_t bh = blockIdx.x / per, i = blockIdx.x % per * 256 + threadIdx.x;
+    const int64_t j = (i % kFP) * a.N + i / kFP;
+    const bool rev = blockIdx.y != 0;
+    float* s = (rev ? a.grads : a.states) + bh * a.chunks * PN + i;
+    const float* f = a.through + bh * a.chunks;
+    const float* from = rev ? a.dhT : a.h0;
+    float v = from ? from[bh * PN + j] : 0.0f;
+    for (int64_t k0 = 0; k0 < a.chunks; k0 += 8) {
+        float own[8], th[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int64_t m = k0 + k < a.chunks ? k0 + k : a.chunks - 1;
+            const int64_t c = rev ? a.chunks - 1 - m : m;
+            own[k] = s[c * PN];
+            th[k] = f[c];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (k0 + k >= a.chunks) break;
+            const int64_t c = rev ? a.chunks - 1 - (k0 + k) : k0 + k;
+            s[c * PN] = v;
+            v = th[k] == 0.0f ? own[k] : th[k] * v + own[k];
+        }
+    }
+    if (rev && a.dh0) a.dh0[bh * PN + j] = v;
+}
+
+// ---------------------------------------------------------------------------------------
+// gradients
+// ---------------------------------------------------------------------------------------
+template <int N>
+struct GradLds {
+    static constexpr int B = 0;                        // [128 s][N] bf16
+    static constexpr int C = B + kFQ * N * 2;          // [128 t][N] bf16
+    static constexpr int X = C + kFQ * N * 2;          // [128 s][64] bf16
+    static constexpr int DY = X + kFQ * 128;           // [128 t][64] bf16
+    static constexpr int G = DY + kFQ * 128;           // two parts of [N][64] bf16
+    static constexpr int LW = X;                       // at the end: two parts of [128 t][128 s] bf16
+    static constexpr int ROW = (G + 2 * N * 128 > LW + 2 * kFQ * 256 ? G + 2 * N * 128 : LW + 2 * kFQ * 256);
+    // per parity of the head:
+    //   row sums of W by s tile [8][128], col sums [2][128], u by n tile [8][128], v [8][128],
+    //   decays [5][128], <G, S> by wavefront [8]
+    static constexpr int HEAD = (8 + 2 + 8 + 8 + 5) * kFQ * 4 + 32;
+    static constexpr int START = ROW + 2 * HEAD;       // [128] int
+    static constexpr int TOTAL = START + kFQ * 4;
+};
+static_assert(GradLds<128>::TOTAL <= 160 * 1024, "LDS");
+
+struct HeadPart {
+    float *row, *col, *u, *v, *dec, *gs;
+};
+__device__ __forceinline__ HeadPart head_part(uint8_t* sm, int base) {
+    float* p = reinterpret_cast<float*>(sm + base);
+    return HeadPart{p, p + 8 * kFQ, p + 10 * kFQ, p + 18 * kFQ, p + 26 * kFQ, p + 31 * kFQ};
+}
+
+// q, ddt and the chunk's share of dA for one head, by one wavefront (tokens lane and 64 + lane)
+template <int NT>
+__device__ __forceinline__ void head_end(const ScanBwdArgs& a, const HeadPart& p, const int* starts,
+                                         int64_t b, int64_t c, int64_t h, int nv, int lane) {
+    double q[2], vd[2];
+    float direct[2], dts[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int t = lane + 64 * k;
+        float row = 0.0f, u = 0.0f, v = 0.0f;
+        for (int i = 0; i <= t / 16; ++i) row += p.row[i * kFQ + t];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            u += p.u[i * kFQ + t];
+            v += p.v[i * kFQ + t];
+        }
+        const float below = p.col[t], all = p.col[kFQ + t];
+        dts[k] = p.dec[4 * kFQ + t];
+        vd[k] = static_cast<double>(v) * dts[k];
+        q[k] = static_cast<double>(row) - static_cast<double>(below) * dts[k] + u - vd[k];
+        direct[k] = all + v;
+    }
+    double vsum = vd[0] + vd[1];
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) vsum += __shfl_xor(vsum, o);
+    const float th = a.through[(b * a.H + h) * a.chunks + c];
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) dot += p.gs[i];
+    if (lane == 63) q[1] += vsum + (th == 0.0f ? 0.0 : static_cast<double>(th) * dot);
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const double u0 = __shfl_down(q[0], o), u1 = __shfl_down(q[1], o);
+        if (lane + o < 64) {
+            q[0] += u0;
+            q[1] += u1;
+        }
+    }
+    q[0] += __shfl(q[1], 0);
+    const double A = a.A[h];
+    double da = 0.0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int t = lane + 64 * k;
+        if (starts[t] != (t > 0 ? starts[t - 1] : 0)) q[k] = 0.0;  // a start takes nothing over
+        if (t < nv) {
+            a.ddt[(b * a.L + c * kFQ + t) * a.H + h] = static_cast<float>(q[k] * A + direct[k]);
+            da += q[k] * dts[k];
+        }
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) da += __shfl_xor(da, o);
+    if (lane == 0) a.dA_part[(b * a.chunks + c) * a.H + h] = da;
+}
+
+template <int N>
+__global__ void __launch_bounds__(512) sbf_grad_kernel(ScanBwdArgs a) {
+    using O = GradLds<N>;
+    constexpr int NT = N / 16, RB = 2 * N, BP = N / 8;
+    constexpr int TT = NT;       // t tiles a wavefront does for dB and dC: all 8, or half of them
+    constexpr int PL = N * 128;  // bytes of one part of G
+    __shared__ __attribute__((aligned(16))) uint8_t sm[O::TOTAL];
+    const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g4 = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t hs = blockIdx.x % a.splits, g = blockIdx.x / a.splits % a.G;
+    const int64_t c = blockIdx.x / a.splits / a.G % a.chunks, b = blockIdx.x / a.splits / a.G / a.chunks;
+    const int64_t k_heads = a.H / a.G;
+    const int64_t hfirst = g * k_heads + hs * a.split_heads;
+    const int64_t hend = hs * a.split_heads + a.split_heads < k_heads ? hfirst + a.split_heads : (g + 1) * k_heads;
+    const int64_t t0 = c * kFQ, tok = b * a.L + t0;
+    const int nv = a.L - t0 < kFQ ? static_cast<int>(a.L - t0) : kFQ;
+    const int nt = wave % NT, th0 = NT == 8 ? 0 : (wave / NT) * TT;  // n tile and first t tile for dB, dC
+    const int st = wave < 4 ? wave : 11 - wave;  // s tile for the pairs: 9 tiles a SIMD (waves w, w + 4)
+    int* starts = reinterpret_cast<int*>(sm + O::START);
+
+    const uint16_t* xg = static_cast<const uint16_t*>(a.x) + tok * a.x_row;
+    const uint16_t* dyg = static_cast<const uint16_t*>(a.dy) + tok * a.dy_row;
+    u4 rx[2], rdy[2];
+    f4 rS[4], rG[4];
+    float rd[2];
+    auto load = [&](int64_t h) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int q = tid + 512 * i, row = q >> 3;
+            rx[i] = rdy[i] = u4{0, 0, 0, 0};
+            if (row < nv) {
+                rx[i] = *reinterpret_cast<const u4any*>(xg + row * a.x_row + h * kFP + 8 * (q & 7));
+                rdy[i] = *reinterpret_cast<const u4any*>(dyg + row * a.dy_row + h * kFP + 8 * (q & 7));
+            }
+        }
+        const int64_t at = ((b * a.H + h) * a.chunks + c) * N * kFP + (16 * nt + li) * kFP + 8 * g4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            rS[i] = *reinterpret_cast<const f4*>(a.states + at + 32 * (i >> 1) + 4 * (i & 1));
+            rG[i] = *reinterpret_cast<const f4*>(a.grads + at + 32 * (i >> 1) + 4 * (i & 1));
+        }
+        const float* rec = a.decay + ((b * a.H + h) * a.chunks + c) * 5 * kFQ;
+        rd[0] = rec[tid];
+        if (tid < kFQ) rd[1] = rec[4 * kFQ + tid];
+    };
+    load(hfirst);
+    {
+        const uint16_t* bg = static_cast<const uint16_t*>(a.Bm) + tok * a.b_row + g * N;
+        const uint16_t* cg = static_cast<const uint16_t*>(a.C) + tok * a.c_row + g * N;
+        for (int q = tid; q < kFQ * BP; q += 512) {
+            const int row = q / BP;
+            u4 v{0, 0, 0, 0}, u{0, 0, 0, 0};
+            if (row < nv) {
+                v = *reinterpret_cast<const u4any*>(bg + row * a.b_row + 8 * (q % BP));
+                u = *reinterpret_cast<const u4any*>(cg + row * a.c_row + 8 * (q % BP));
+            }
+            *reinterpret_cast<u4*>(sm + O::B + piece<RB>(row, q % BP)) = v;
+            *reinterpret_cast<u4*>(sm + O::C + piece<RB>(row, q % BP)) = u;
+        }
+        if (tid < kFQ) starts[tid] = a.starts[(b * a.chunks + c) * kFQ + tid];
+    }
+    __syncthreads();
+    const bool masked = starts[kFQ - 1] != 0;
+    const int ao = along_off<RB>(li, g4), xo = along_off<128>(li, g4);
+    const int yo = down_off<128>(4 * g4, li);
+    const int go0 = down_off<128>(8 * g4, li), go1 = down_off<128>(8 * g4 + 4, li);
+
+    // C B^T for the pairs of this wavefront's s tile, t tiles st .. 7
+    f4 cb[8], lw[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        cb[j] = lw[j] = f4{0, 0, 0, 0};
+        if (j >= st) {
+#pragma unroll
+            for (int kk = 0; kk < N / 32; ++kk)
+                cb[j] = mfma(along<RB>(sm + O::C, ao, 16 * j, kk), along<RB>(sm + O::B, ao, 16 * st, kk), cb[j]);
+        }
+    }
+    f4 accC[TT], accB[TT];
+#pragma unroll
+    for (int j = 0; j < TT; ++j) accC[j] = accB[j] = f4{0, 0, 0, 0};
+
+    const int s = 16 * st + li;
+    const int rs = starts[s];
+    for (int64_t h = hfirst; h < hend; ++h) {
+        const int par = static_cast<int>(h - hfirst) & 1;
+        const HeadPart hp = head_part(sm, O::ROW + par * O::HEAD);
+        // operands from the loaded states
+        bf8 Sp[2][3], Gp[2][3];
+        {
+            float dot = 0.0f;
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                float vs[8], vg[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    vs[e] = rS[2 * kk + (e >> 2)][e & 3];
+                    vg[e] = rG[2 * kk + (e >> 2)][e & 3];
+                    dot += vs[e] * vg[e];
+                }
+                split(vs, Sp[kk]);
+                split(vg, Gp[kk]);
+            }
+            dot = group_sum4(lane_sum16(dot));
+            if (lane == 0 && wave < NT) hp.gs[wave] = dot;
+        }
+        __syncthreads();  // the previous head's x, dy and G have been read
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int q = tid + 512 * i, o = piece<128>(q >> 3, q & 7);
+            *reinterpret_cast<u4*>(sm + O::X + o) = rx[i];
+            *reinterpret_cast<u4*>(sm + O::DY + o) = rdy[i];
+        }
+        if (wave < NT) {
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    *reinterpret_cast<bf8*>(sm + O::G + k * PL + piece<128>(16 * nt + li, 4 * kk + g4)) = Gp[kk][k];
+        }
+        hp.dec[tid] = rd[0];
+        if (tid < kFQ) hp.dec[4 * kFQ + tid] = rd[1];
+        __syncthreads();
+        if (h > hfirst && wave == static_cast<int>((h - 1 - hfirst) & 7))
+            head_end<NT>(a, head_part(sm, O::ROW + (par ^ 1) * O::HEAD), starts, b, c, h - 1, nv, lane);
+
+        // ---- dy against S and x: dC, u, the pairs ----
+        f4 dxa[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) dxa[p] = f4{0, 0, 0, 0};
+        const bf8 xf0 = along<128>(sm + O::X, xo, 16 * st, 0), xf1 = along<128>(sm + O::X, xo, 16 * st, 1);
+        const float hs_ = hp.dec[s], ls_ = hp.dec[kFQ + s], dts = hp.dec[4 * kFQ + s];
+        float below = 0.0f, diag = 0.0f;
+        u4 pw[2];  // two parts of the pairs of two t tiles, in token order
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const bf8 d0 = along<128>(sm + O::DY, xo, 16 * j, 0), d1 = along<128>(sm + O::DY, xo, 16 * j, 1);
+            if (j >= th0 && j < th0 + TT) {
+                f4 o{0, 0, 0, 0};
+#pragma unroll
+                for (int k = 2; k >= 0; --k) {
+                    o = mfma(Sp[0][k], d0, o);
+                    o = mfma(Sp[1][k], d1, o);
+                }
+                const int t = 16 * j + li;
+                const float ft = hp.dec[2 * kFQ + t];
+                const u2 cw = lds<u2>(sm + O::C + piece<RB>(t, 2 * nt + (g4 >> 1)) + 8 * (g4 & 1));
+                float u = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (masked && ft == 0.0f) o[e] = 0.0f;
+                    u += __uint_as_float(e & 1 ? cw[e >> 1] & 0xFFFF0000u : cw[e >> 1] << 16) * o[e];
+                    if (NT == 8) accC[j][e] += ft * o[e];
+                    else accC[j & 3][e] += ft * o[e];
+                }
+                u = group_sum4(u) * ft;
+                if (g4 == 0) hp.u[nt * kFQ + t] = u;
+            }
+            if (j >= st) {
+                f4 yx = mfma(d0, xf0, f4{0, 0, 0, 0});
+                yx = mfma(d1, xf1, yx);
+                const f4 ht = *reinterpret_cast<const f4*>(hp.dec + 16 * j + 4 * g4);
+                const f4 lt = *reinterpret_cast<const f4*>(hp.dec + kFQ + 16 * j + 4 * g4);
+                float pv[4], row[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float l = __builtin_amdgcn_exp2f((ht[e] - hs_) + (lt[e] - ls_));
+                    const int t = 4 * g4 + e;  // within the tile
+                    if (j == st && t < li) l = 0.0f;
+                    if (masked && starts[16 * j + t] != rs) l = 0.0f;
+                    pv[e] = l * cb[j][e];
+                    lw[j][e] += l * yx[e] * dts;
+                    float w = pv[e] * yx[e];
+                    if (j == st && t == li) {
+                        diag = w;
+                        w = 0.0f;
+                    }
+                    below += w;
+                    row[e] = lane_sum16(w * dts);
+                }
+                if (li < 4) hp.row[st * kFQ + 16 * j + 4 * g4 + li] = li == 0 ? row[0] : li == 1 ? row[1] : li == 2 ? row[2] : row[3];
+                // two parts, into this tile's half of the operand
+                const uint32_t q0 = pack_bf16x2(pv[0], pv[1]), q1 = pack_bf16x2(pv[2], pv[3]);
+                pw[0][2 * (j & 1)] = q0;
+                pw[0][2 * (j & 1) + 1] = q1;
+                pw[1][2 * (j & 1)] = pack_bf16x2(pv[0] - __uint_as_float(q0 << 16), pv[1] - __uint_as_float(q0 & 0xFFFF0000u));
+                pw[1][2 * (j & 1) + 1] = pack_bf16x2(pv[2] - __uint_as_float(q1 << 16), pv[3] - __uint_as_float(q1 & 0xFFFF0000u));
+            } else {
+                pw[0][2 * (j & 1)] = pw[0][2 * (j & 1) + 1] = pw[1][2 * (j & 1)] = pw[1][2 * (j & 1) + 1] = 0;
+            }
+            if ((j & 1) && j >= st) {
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const bf8 y = down<128>(sm + O::DY, yo, 16 * (j - 1), p);
+                    dxa[p] = mfma(y, __builtin_bit_cast(bf8, pw[1]), dxa[p]);
+                    dxa[p] = mfma(y, __builtin_bit_cast(bf8, pw[0]), dxa[p]);
+                }
+            }
+        }
+        below = group_sum4(below);
+        diag = group_sum4(diag);
+        if (g4 == 0) {
+            hp.col[s] = below;
+            hp.col[kFQ + s] = below + diag;
+        }
+        if (h + 1 < hend) load(h + 1);
+
+        // ---- x against G: dB, v ----
+#pragma unroll
+        for (int jj = 0; jj < TT; ++jj) {
+            const int j = th0 + jj;
+            const bf8 x0 = along<128>(sm + O::X, xo, 16 * j, 0), x1 = along<128>(sm + O::X, xo, 16 * j, 1);
+            f4 o{0, 0, 0, 0};
+#pragma unroll
+            for (int k = 2; k >= 0; --k) {
+                o = mfma(Gp[0][k], x0, o);
+                o = mfma(Gp[1][k], x1, o);
+            }
+            const int t = 16 * j + li;
+            const float es = hp.dec[3 * kFQ + t], ed = es * hp.dec[4 * kFQ + t];
+            const u2 bw = lds<u2>(sm + O::B + piece<RB>(t, 2 * nt + (g4 >> 1)) + 8 * (g4 & 1));
+            float v = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (masked && es == 0.0f) o[e] = 0.0f;
+                v += __uint_as_float(e & 1 ? bw[e >> 1] & 0xFFFF0000u : bw[e >> 1] << 16) * o[e];
+                accB[jj][e] += ed * o[e];
+            }
+            v = group_sum4(v) * es;
+            if (g4 == 0) hp.v[nt * kFQ + t] = v;
+        }
+
+        // ---- dx: G B, then with the pairs ----
+        const float es = hp.dec[3 * kFQ + s];
+        uint16_t* dxo = static_cast<uint16_t*>(a.dx) + (tok + s) * a.dx_row + h * kFP + 4 * g4;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            f4 o{0, 0, 0, 0};
+#pragma unroll
+            for (int kk = 0; kk < N / 32; ++kk) {
+                const bf8 bf = along<RB>(sm + O::B, ao, 16 * st, kk);
+#pragma unroll
+                for (int k = 1; k >= 0; --k) {
+                    const uint8_t* pl = sm + O::G + k * PL + 32 * kk * 128;
+                    o = mfma(join(tr_read(pl + (go0 ^ (p << 5))), tr_read(pl + (go1 ^ (p << 5)))), bf, o);
+                }
+            }
+            f4 r;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) r[e] = dts * (dxa[p][e] + (masked && es == 0.0f ? 0.0f : es * o[e]));
+            if (s < nv) *reinterpret_cast<u2any*>(dxo + 16 * p) = u2{pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3])};
+        }
+    }
+    __syncthreads();
+    if (wave == static_cast<int>((hend - 1 - hfirst) & 7))
+        head_end<NT>(a, head_part(sm, O::ROW + (static_cast<int>(hend - 1 - hfirst) & 1) * O::HEAD), starts, b, c,
+                     hend - 1, nv, lane);
+
+    // ---- the heads' summed pairs: two parts of [t][s] in LDS (zero above the diagonal) ----
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float v = j >= st ? lw[j][e] : 0.0f;
+            const int t = 16 * j + 4 * g4 + e;
+            const uint16_t hi = f32_to_bf16(v), lo = f32_to_bf16(v - bf16_to_f32(hi));
+            const int o = piece<256>(t, s >> 3) + 2 * (s & 7);
+            *reinterpret_cast<uint16_t*>(sm + O::LW + o) = hi;
+            *reinterpret_cast<uint16_t*>(sm + O::LW + kFQ * 256 + o) = lo;
+        }
+    __syncthreads();
+    const int bo = down_off<RB>(4 * g4, li) ^ (nt << 5);       // B^T, C^T: rows of n tile nt
+    const int b0 = down_off<RB>(8 * g4, li) ^ (nt << 5), b1 = down_off<RB>(8 * g4 + 4, li) ^ (nt << 5);
+    const int lo_ = along_off<256>(li, g4), ld = down_off<256>(4 * g4, li);
+#pragma unroll
+    for (int jj = 0; jj < TT; ++jj) {
+        const int j = th0 + jj;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (2 * k <= j) {  // dC of t tile j: s tiles 2 k, 2 k + 1
+                const uint8_t* p = sm + O::B + 32 * k * RB;
+                const bf8 f = join(tr_read(p + b0), tr_read(p + b1));
+                accC[jj] = mfma(f, along<256>(sm + O::LW + kFQ * 256, lo_, 16 * j, k), accC[jj]);
+                accC[jj] = mfma(f, along<256>(sm + O::LW, lo_, 16 * j, k), accC[jj]);
+            }
+            if (2 * k + 1 >= j) {  // dB of s tile j: t tiles 2 k, 2 k + 1
+                const bf8 f = down<RB>(sm + O::C, bo, 32 * k, 0);
+                accB[jj] = mfma(f, down<256>(sm + O::LW + kFQ * 256, ld, 32 * k, j), accB[jj]);
+                accB[jj] = mfma(f, down<256>(sm + O::LW, ld, 32 * k, j), accB[jj]);
+            }
+        }
+        const int t = 16 * j + li;
+        if (t < nv) {
+            const int64_t col = g * N + 16 * nt + 4 * g4;
+            if (a.splits == 1) {
+                *reinterpret_cast<u2any*>(static_cast<uint16_t*>(a.dC) + (tok + t) * a.dc_row + col) =
+                    u2{pack_bf16x2(accC[jj][0], accC[jj][1]), pack_bf16x2(accC[jj][2], accC[jj][3])};
+                *reinterpret_cast<u2any*>(static_cast<uint16_t*>(a.dB) + (tok + t) * a.db_row + col) =
+                    u2{pack_bf16x2(accB[jj][0], accB[jj][1]), pack_bf16x2(accB[jj][2], accB[jj][3])};
+            } else {
+                const int64_t at = (hs * a.B * a.L + tok + t) * a.G * N + col;
+                *reinterpret_cast<f4*>(a.dC_head + at) = accC[jj];
+                *reinterpret_cast<f4*>(a.dB_head + at) = accB[jj];
+            }
+        }
+    }
+}
+
+// dB, dC of several ranges of heads, added in order and rounded once (blockIdx.y: dB, dC)
+__global__ void __launch_bounds__(256) sbf_join_kernel(ScanBwdArgs a) {
+    const int64_t GN = a.G * a.N, n = a.B * a.L * GN;
+    const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+    if (i >= n) return;
+    const float* p = (blockIdx.y ? a.dC_head : a.dB_head) + i;
+    f4 s = *reinterpret_cast<const f4*>(p);
+    for (int64_t j = 1; j < a.splits; ++j) s += *reinterpret_cast<const f4*>(p + j * n);
+    uint16_t* o = blockIdx.y ? static_cast<uint16_t*>(a.dC) + i / GN * a.dc_row
+                             : static_cast<uint16_t*>(a.dB) + i / GN * a.db_row;
+    *reinterpret_cast<u2any*>(o + i % GN) = u2{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
+}
+
+size_t r256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Ranges of heads a chunk and group: one block runs on a unit at a time (LDS), so the time is
+// the rounds of blocks over the 256 units times what a block does: its heads, and about two
+// heads' worth of B, C and the pairs' end.
+void cut_heads(ScanBwdArgs& a) {
+    const int64_t blocks = a.B * a.chunks * a.G, k = a.H / a.G;
+    int64_t best = -1;
+    for (int64_t n = 1; n <= k && n <= 256; ++n) {
+        const int64_t heads = (k + n - 1) / n;
+        if ((k + heads - 1) / heads != n) continue;
+        const int64_t cost = (blocks * n + 255) / 256 * (heads + 2);
+        if (best < 0 || cost < best) {
+            best = cost;
+            a.splits = n;
+            a.split_heads = heads;
+        }
+    }
+}
+
+size_t lay_out(ScanBwdArgs& a, uint8_t* base) {
+    size_t at = 0;
+    auto part = [&](auto*& p, size_t n) {
+        p = reinterpret_cast<std::remove_reference_t<decltype(p)>>(base + at);
+        at += r256(n * sizeof(*p));
+    };
+    const size_t bhc = static_cast<size_t>(a.B * a.H * a.chunks);
+    part(a.dA_part, bhc);
+    part(a.through, bhc);
+    part(a.decay, bhc * 5 * kFQ);
+    part(a.starts, static_cast<size_t>(a.B * a.chunks) * kFQ);
+    part(a.states, bhc * a.P * a.N);
+    part(a.grads, bhc * a.P * a.N);
+    const size_t heads = a.splits > 1 ? static_cast<size_t>(a.splits * a.B * a.L * a.G * a.N) : 0;
+    part(a.dB_head, heads);
+    part(a.dC_head, heads);
+    return at;
+}
+
+void set_up(ScanBwdArgs& a) {
+    a.chunks = (a.L + kFQ - 1) / kFQ;
+    cut_heads(a);
+}
+
+template <int N>
+hipError_t launch_typed(const ScanBwdArgs& a, hipStream_t s) {
+    const int64_t bh = a.B * a.H;
+    sbf_decay_kernel<<<static_cast<uint32_t>(a.B * a.chunks * ((a.H + 15) / 16)), 256, 0, s>>>(a);
+    if (2 * bh >= 256 || a.chunks == 1) {
+        sbf_states_kernel<N, true><<<dim3(static_cast<uint32_t>(bh), 2), 256, 0, s>>>(a);
+    } else {
+        sbf_states_kernel<N, false><<<dim3(static_cast<uint32_t>(bh * a.chunks), 2), 256, 0, s>>>(a);
+        sbf_pass_kernel<<<dim3(static_cast<uint32_t>(bh * (kFP * N / 256)), 2), 256, 0, s>>>(a);
+    }
+    sbf_grad_kernel<N><<<static_cast<uint32_t>(a.B * a.chunks * a.G * a.splits), 512, 0, s>>>(a);
+    if (a.splits > 1)
+        sbf_join_kernel<<<dim3(static_cast<uint32_t>((a.B * a.L * a.G * N / 4 + 255) / 256), 2), 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+bool scan_bwd_mfma_supported(int64_t P, int64_t N, ssm_dtype_t dtype) {
+    return dtype == SSM_BF16 && P == kFP && (N == 64 || N == 128);
+}
+
+size_t scan_bwd_mfma_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N) {
+    ScanBwdArgs a{};
+    a.B = B; a.L = L; a.H = H; a.P = P; a.G = G; a.N = N;
+    set_up(a);
+    return lay_out(a, nullptr);
+}
+
+hipError_t launch_scan_bwd_mfma(ScanBwdArgs a, void* workspace, hipStream_t s) {
+    set_up(a);
+    lay_out(a, static_cast<uint8_t*>(workspace));
+    const hipError_t e = a.N == 128 ? launch_typed<128>(a, s) : launch_typed<64>(a, s);
+    return e == hipSuccess ? launch_scan_bwd_dA(a, s) : e;
+}
+
+}  // namespace ssm

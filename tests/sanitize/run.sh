@@ -15,7 +15,7 @@ RT=$("$CLANG" -print-file-name=libclang_rt.asan-x86_64.so)
 SAN="-Xarch_host -fsanitize=address -Xarch_host -fsanitize=undefined -Xarch_host -fno-omit-frame-pointer -Xarch_host -fno-sanitize-recover=all"
 echo "== host-sanitized HIP library -> $OUT"
 objs=(); pids=()
-for src in abi bwd conv gscan init_state norm pool recurrent scan_bwd ssd vchunk vdecay; do
+for src in abi bwd conv gscan init_state norm pool recurrent scan_bwd scan_bwd_mfma ssd vchunk vdecay; do
   $HIPCC -O1 -g -std=c++17 -fPIC --offload-arch=gfx950 -Xclang -target-feature -Xclang -packed-fp32-ops \
     $SAN -c "$ROOT/ssm_sequence_models_amd/csrc/$src.hip" -o "$OUT/$src.o" &
   objs+=("$OUT/$src.o"); pids+=($!)
