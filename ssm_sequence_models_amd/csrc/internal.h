@@ -315,7 +315,14 @@ struct ScanBwdArgs {
     float* decay;      // [B, H, chunks, 5, 128]: sums of log2 a (hi, lo), f, e, dt
     int32_t* starts;   // [B, chunks, 128]: sequence starts so far in the chunk
     int64_t splits, split_heads;  // ranges of a group's heads a chunk, heads in each
+    float* sums;       // [B, H, chunks, kSums * Q + kSumTail], Q the chunk's tokens
 };
+// Sums over pairs of tokens that ddt and dA are formed from (W, u, v as in scan_bwd.hip), each an
+// array over the chunk's tokens: u; v / dt; row sums of W over s < t, in earlier 16-token tiles
+// and in t's own; column sums of W / dt_s over t > s, in later tiles and in s's own; W_tt / dt_t.
+// Behind them the row sums' sums by tile, [t tile][s tile] in eights, then <G, S>.
+enum { kSumU, kSumV, kSumRowOff, kSumRowDiag, kSumColOff, kSumColDiag, kSumDiag, kSums };
+constexpr int kSumTail = 128;
 size_t scan_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N,
                                 ssm_dtype_t dtype);
 int64_t scan_bwd_blocks(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N);
@@ -324,7 +331,8 @@ hipError_t launch_scan_bwd(ScanBwdArgs a, void* workspace, ssm_dtype_t dtype, hi
 bool scan_bwd_mfma_supported(int64_t P, int64_t N, ssm_dtype_t dtype);
 size_t scan_bwd_mfma_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N);
 hipError_t launch_scan_bwd_mfma(ScanBwdArgs a, void* workspace, hipStream_t stream);
-hipError_t launch_scan_bwd_dA(const ScanBwdArgs& a, hipStream_t stream);  // dA from dA_part
+// ddt and dA from the sums of chunks of 64 or 128 tokens
+hipError_t launch_scan_bwd_ddt(const ScanBwdArgs& a, int tokens, hipStream_t stream);
 hipError_t launch_scan_bwd_empty(const float* dhT, float* dh0, float* dA, int64_t n, int64_t H,
                                  hipStream_t stream);
 hipError_t launch_pool_gather(const void* conv_pool, const float* ssm_pool, const int32_t* indices,

@@ -17,15 +17,18 @@
 //     dB_s = dt_s ( sum_t L_ts (dy_t.x_s) C_t  +  e_s G^T x_s )
 // and q_t is the sum of every product whose factor spans t: with
 //     W_ts = L_ts (C_t.B_s) (dy_t.x_s) dt_s,  u_t = f_t dy_t.(S C_t),  v_s = dt_s e_s x_s.(G B_s),
-// each W_ts counts for s < tau <= t, u_t for tau <= t, v_s for tau > s, f_last <G, S> for all,
-// so q is the sum from the chunk's end back of
-//     sum_{s<t} W_ts - sum_{t'>t} W_t't + u_t - v_t  (+ sum_s v_s + f_last <G, S> at the last).
-// The part of ddt that does not pass through a_t is sum_t W_ts / dt_s + v_s / dt_s, formed
-// without the division.
+//     q_tau = sum_{s < tau <= t} W_ts + sum_{t >= tau} u_t + sum_{s < tau} v_s + f_last <G, S>.
+// The W that span tau are not taken as the difference of all row sums and column sums from tau
+// on: those are far larger where the decay is fast, and dA, a sum over the whole batch, would
+// keep their rounding errors.  With 16-token tiles they are the row sums over earlier tiles
+// from tau to its tile's end, the column sums over later tiles from its tile's start to tau, the
+// tile pairs around its tile, all sums of what spans tau only, and the difference within the
+// one tile.  The part of ddt that does not pass through a_t is sum_t W_ts / dt_s + v_s / dt_s,
+// formed without the division.
 //
 // Decays: log a_t is summed in double over the chunk and each factor is the exponential of a
 // difference of two sums, so its relative error stays near 2^-24 however fast the decay.
-// log a below -1024 (a = 0 in fp32 by far) counts as -1024: the sums keep what follows.
+// log2 a below -1500 (a = 0 in fp32 by far) counts as -1500: the sums keep what follows.
 //
 // This file: any headdim and dstate that the forward takes, fp32 or bf16 activations, products
 // on the fp32 matrix instruction (16 x 16 x 4).  Three steps: the chunks' own shares of S and G
@@ -49,7 +52,7 @@ __device__ __forceinline__ f4 mfma4(const f4& a, const f4& b, f4 c) {
 
 // The chunk's decays, by the block's first wavefront (lane = token).
 struct ChunkDecay {
-    double cs[kQ];   // sum of log a over the chunk's tokens 0 .. t
+    double cs[kQ];   // sum of log2 a over the chunk's tokens 0 .. t
     int starts[kQ];  // sequence starts among tokens 0 .. t
     float f[kQ];     // f_t
     float e[kQ];     // e_t
@@ -62,8 +65,8 @@ __device__ __forceinline__ void chunk_decay(ChunkDecay& cd, const float* dt, int
     const int t = threadIdx.x;
     if (t < kQ) {
         const float d = t < nv ? dt[t * dt_stride] : 0.0f;
-        double s = static_cast<double>(d) * static_cast<double>(A);
-        if (s < -1024.0) s = -1024.0;
+        double s = static_cast<double>(d) * (static_cast<double>(A) * 1.4426950408889634);
+        if (s < -1500.0) s = -1500.0;
         int r = 0;
         if (seq && t < nv && t0 + t > 0) r = seq[t0 + t] != seq[t0 + t - 1];
 #pragma unroll
@@ -79,10 +82,10 @@ __device__ __forceinline__ void chunk_decay(ChunkDecay& cd, const float* dt, int
         const int rend = __shfl(r, 63);
         cd.cs[t] = s;
         cd.starts[t] = r;
-        cd.f[t] = r == 0 ? __expf(static_cast<float>(s)) : 0.0f;
-        cd.e[t] = r == rend ? __expf(static_cast<float>(end - s)) : 0.0f;
+        cd.f[t] = r == 0 ? __builtin_amdgcn_exp2f(static_cast<float>(s)) : 0.0f;
+        cd.e[t] = r == rend ? __builtin_amdgcn_exp2f(static_cast<float>(end - s)) : 0.0f;
         cd.dt[t] = d;
-        if (t == 63) cd.through = r == 0 ? __expf(static_cast<float>(s)) : 0.0f;
+        if (t == 63) cd.through = cd.f[63];
     }
     __syncthreads();
 }
@@ -201,7 +204,8 @@ __global__ void __launch_bounds__(256) sb_grad_kernel(ScanBwdArgs a) {
     __shared__ float pair[kQ][kQ + 1];  // [t][s] L_ts (C_t.B_s)
     __shared__ float lw[kQ][kQ + 1];    // [t][s] L_ts (dy_t.x_s) dt_s
     __shared__ float rowp[4][kQ];       // sums over the s of one 16-column tile, s < t, of W
-    __shared__ float colp[4][2][kQ];    // sums over the t of one 16-row tile: t > s of W; t >= s of W / dt_s
+    __shared__ float colp[4][kQ];       // sums over the t of one 16-row tile, t > s, of W / dt_s
+    __shared__ float diag[kQ];          // W_ss / dt_s
     __shared__ float uu[kQ], vv[kQ];    // u_t, v_s / dt_s
     __shared__ float gs[4];
     const Where w = where(a, blockIdx.x);
@@ -231,31 +235,26 @@ __global__ void __launch_bounds__(256) sb_grad_kernel(ScanBwdArgs a) {
         const double css = cd.cs[s];
         const int rs = cd.starts[s];
         const float dts = cd.dt[s];
-        float below = 0.0f, all = 0.0f;
+        float below = 0.0f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int t = 16 * ti + 4 * g4 + e;
             const bool in = t >= s && cd.starts[t] == rs;
-            const float l = in ? __expf(static_cast<float>(cd.cs[t] - css)) : 0.0f;
+            const float l = in ? __builtin_amdgcn_exp2f(static_cast<float>(cd.cs[t] - css)) : 0.0f;
             const float pv = in ? l * cb[e] : 0.0f, yv = in ? l * yx[e] * dts : 0.0f;
             pair[t][s] = pv;
             lw[t][s] = yv;
             const float w0 = in ? pv * yx[e] : 0.0f;
-            all += w0;
+            if (t == s) diag[s] = w0;
+            else below += w0;
             float row = t > s ? w0 * dts : 0.0f;
-            below += row;
 #pragma unroll
             for (int o = 1; o < 16; o <<= 1) row += __shfl_xor(row, o);
             if (li == 0) rowp[si][t] = row;
         }
         below += __shfl_xor(below, 16);
         below += __shfl_xor(below, 32);
-        all += __shfl_xor(all, 16);
-        all += __shfl_xor(all, 32);
-        if (g4 == 0) {
-            colp[ti][0][s] = below;
-            colp[ti][1][s] = all;
-        }
+        if (g4 == 0) colp[ti][s] = below;
     }
     // <G, S>
     {
@@ -331,36 +330,105 @@ __global__ void __launch_bounds__(256) sb_grad_kernel(ScanBwdArgs a) {
     }
     __syncthreads();
 
-    // q, ddt and the chunk's share of dA (lane = token)
+    // the sums that ddt and dA are formed from (lane = token)
     if (wave != 0) return;
-    const int t = lane;
-    float row = 0.0f, below = 0.0f, all = 0.0f;
-    for (int i = 0; i <= t / 16; ++i) row += rowp[i][t];
-    for (int i = t / 16; i < 4; ++i) {
-        below += colp[i][0][t];
-        all += colp[i][1][t];
-    }
-    const double vd = static_cast<double>(vv[t]) * cd.dt[t];
-    double q = static_cast<double>(row) - below + uu[t] - vd, vsum = vd;
+    const int t = lane, j = t / 16;
+    float* out = a.sums + ((w.b * a.H + w.h) * a.chunks + w.c) * (kSums * kQ + kSumTail);
+    float row = 0.0f, below = 0.0f;
+    for (int i = 0; i < j; ++i) row += rowp[i][t];
+    for (int i = j + 1; i < 4; ++i) below += colp[i][t];
+    out[kSumU * kQ + t] = uu[t];
+    out[kSumV * kQ + t] = vv[t];
+    out[kSumRowOff * kQ + t] = row;
+    out[kSumRowDiag * kQ + t] = rowp[j][t];
+    out[kSumColOff * kQ + t] = below;
+    out[kSumColDiag * kQ + t] = colp[j][t];
+    out[kSumDiag * kQ + t] = diag[t];
+    float tile = 0.0f;  // [t tile][s tile] in eights
+    if (t < 32 && (t & 7) < (t >> 3))
+        for (int i = 0; i < 16; ++i) tile += rowp[t & 7][16 * (t >> 3) + i];
+    out[kSums * kQ + t] = tile;
+    if (t == 0) out[kSums * kQ + 64] = (gs[0] + gs[1]) + (gs[2] + gs[3]);
+}
+
+// sums along aligned spans of LEN lanes: from the lane to the span's end, and before the lane
+template <int LEN>
+__device__ __forceinline__ double from_lane(double v, int lane) {
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) vsum += __shfl_xor(vsum, o);
-    if (t == 63) {
-        const float dot = (gs[0] + gs[1]) + (gs[2] + gs[3]);
-        q += vsum + (cd.through == 0.0f ? 0.0 : static_cast<double>(cd.through) * dot);
+    for (int o = 1; o < LEN; o <<= 1) {
+        const double u = __shfl_down(v, o);
+        if ((lane & (LEN - 1)) + o < LEN) v += u;
     }
+    return v;
+}
+template <int LEN>
+__device__ __forceinline__ double before_lane(double v, int lane) {
+    const double own = v;
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const double qo = __shfl_down(q, o);
-        if (t + o < 64) q += qo;
+    for (int o = 1; o < LEN; o <<= 1) {
+        const double u = __shfl_up(v, o);
+        if ((lane & (LEN - 1)) >= o) v += u;
     }
-    const bool start = cd.starts[t] != (t > 0 ? cd.starts[t - 1] : 0);
-    if (start) q = 0.0;
-    if (t < w.nv)
-        a.ddt[(tok + t) * a.H + w.h] = static_cast<float>(q * a.A[w.h] + (static_cast<double>(all) + vv[t]));
-    double da = t < w.nv ? q * cd.dt[t] : 0.0;
+    return v - own;
+}
+
+// q, ddt and a chunk's share of dA: one wavefront a chunk and head, Q / 64 tokens a lane; a
+// block takes 16 heads of one row and chunk (its stores of ddt are 64-byte runs).
+template <int Q>
+__global__ void __launch_bounds__(1024) sb_ddt_kernel(ScanBwdArgs a) {
+    constexpr int K = Q / 64;
+    const int64_t hb = (a.H + 15) / 16;
+    const int64_t h = blockIdx.x % hb * 16 + (threadIdx.x >> 6), c = blockIdx.x / hb % a.chunks;
+    const int64_t b = blockIdx.x / hb / a.chunks;
+    if (h >= a.H) return;
+    const int lane = threadIdx.x & 63;
+    const int64_t at = (b * a.H + h) * a.chunks + c, t0 = c * Q;
+    const float* in = a.sums + at * (kSums * Q + kSumTail);
+    const float th = a.through[at];
+    const double pass = th == 0.0f ? 0.0 : static_cast<double>(th) * in[kSums * Q + 64];
+    double q[K], u[K], v[K];
+    float direct[K], dts[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int t = lane + 64 * k, j = t >> 4;
+        dts[k] = t0 + t < a.L ? a.dt[(b * a.L + t0 + t) * a.H + h] : 0.0f;
+        const float coff = in[kSumColOff * Q + t], cdiag = in[kSumColDiag * Q + t], vt = in[kSumV * Q + t];
+        direct[k] = ((coff + cdiag) + in[kSumDiag * Q + t]) + vt;
+        u[k] = in[kSumU * Q + t];
+        v[k] = static_cast<double>(vt) * dts[k];
+        q[k] = from_lane<16>(in[kSumRowOff * Q + t], lane) + before_lane<16>(static_cast<double>(coff) * dts[k], lane);
+        q[k] += from_lane<16>(static_cast<double>(in[kSumRowDiag * Q + t]) - static_cast<double>(cdiag) * dts[k], lane);
+        for (int j2 = j + 1; j2 < Q / 16; ++j2)
+            for (int i = 0; i < j; ++i) q[k] += in[kSums * Q + 8 * j2 + i];
+    }
+    double after = 0.0;
+#pragma unroll
+    for (int k = K - 1; k >= 0; --k) {
+        const double s = from_lane<64>(u[k], lane);
+        q[k] += s + after;
+        after += __shfl(s, 0);
+    }
+    double before = 0.0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const double s = before_lane<64>(v[k], lane);
+        q[k] += s + before;
+        before += __shfl(s + v[k], 63);
+    }
+    const double A = a.A[h];
+    double da = 0.0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int64_t t = t0 + lane + 64 * k;
+        if (t >= a.L) continue;
+        q[k] += pass;
+        if (a.seq && t > 0 && a.seq[b * a.L + t] != a.seq[b * a.L + t - 1]) q[k] = 0.0;  // a start takes nothing over
+        a.ddt[(b * a.L + t) * a.H + h] = static_cast<float>(q[k] * A + direct[k]);
+        da += q[k] * dts[k];
+    }
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) da += __shfl_xor(da, o);
-    if (t == 0) a.dA_part[(w.b * a.chunks + w.c) * a.H + w.h] = da;
+    if (lane == 0) a.dA_part[(b * a.chunks + c) * a.H + h] = da;
 }
 
 // dB, dC: the heads of a group added in order, rounded once
@@ -399,7 +467,7 @@ hipError_t launch_general(const ScanBwdArgs& a, hipStream_t s) {
     sb_grad_kernel<S><<<bhc, 256, 0, s>>>(a);
     sb_heads_kernel<S><<<dim3(static_cast<uint32_t>((a.B * a.L * a.G * a.N + 255) / 256), 2), 256, 0, s>>>(a);
     const hipError_t e = hipGetLastError();
-    return e == hipSuccess ? launch_scan_bwd_dA(a, s) : e;
+    return e == hipSuccess ? launch_scan_bwd_ddt(a, kQ, s) : e;
 }
 
 size_t r256(size_t n) { return (n + 255) / 256 * 256; }
@@ -414,6 +482,7 @@ size_t lay_out(ScanBwdArgs& a, uint8_t* base) {
     const size_t bh = static_cast<size_t>(a.B * a.H), bhc = bh * a.chunks;
     part(a.dA_part, bhc);
     part(a.through, bhc);
+    part(a.sums, bhc * (kSums * kQ + kSumTail));
     part(a.states, bhc * a.P * a.N);
     part(a.grads, bhc * a.P * a.N);
     part(a.dB_head, bh * a.L * a.N);
@@ -423,7 +492,10 @@ size_t lay_out(ScanBwdArgs& a, uint8_t* base) {
 
 }  // namespace
 
-hipError_t launch_scan_bwd_dA(const ScanBwdArgs& a, hipStream_t s) {
+hipError_t launch_scan_bwd_ddt(const ScanBwdArgs& a, int tokens, hipStream_t s) {
+    const uint32_t grid = static_cast<uint32_t>(a.B * a.chunks * ((a.H + 15) / 16));
+    if (tokens == 128) sb_ddt_kernel<128><<<grid, 1024, 0, s>>>(a);
+    else sb_ddt_kernel<64><<<grid, 1024, 0, s>>>(a);
     sb_dA_kernel<<<static_cast<uint32_t>(a.H), 256, 0, s>>>(a);
     return hipGetLastError();
 }

@@ -350,76 +350,57 @@ struct GradLds {
     static constexpr int G = DY + kFQ * 128;           // two parts of [N][64] bf16
     static constexpr int LW = X;                       // at the end: two parts of [128 t][128 s] bf16
     static constexpr int ROW = (G + 2 * N * 128 > LW + 2 * kFQ * 256 ? G + 2 * N * 128 : LW + 2 * kFQ * 256);
-    // per parity of the head:
-    //   row sums of W by s tile [8][128], col sums [2][128], u by n tile [8][128], v [8][128],
-    //   decays [5][128], <G, S> by wavefront [8]
-    static constexpr int HEAD = (8 + 2 + 8 + 8 + 5) * kFQ * 4 + 32;
+    // per parity of the head: row sums of W by s tile [8][128], u by n tile [8][128], v [8][128],
+    // decays [5][128], <G, S> by wavefront [8]
+    static constexpr int U = 8 * kFQ * 4, V = 16 * kFQ * 4, DEC = 24 * kFQ * 4, DOT = 29 * kFQ * 4;
+    static constexpr int HEAD = DOT + 32;
     static constexpr int START = ROW + 2 * HEAD;       // [128] int
     static constexpr int TOTAL = START + kFQ * 4;
 };
 static_assert(GradLds<128>::TOTAL <= 160 * 1024, "LDS");
 
-struct HeadPart {
-    float *row, *col, *u, *v, *dec, *gs;
-};
-__device__ __forceinline__ HeadPart head_part(uint8_t* sm, int base) {
-    float* p = reinterpret_cast<float*>(sm + base);
-    return HeadPart{p, p + 8 * kFQ, p + 10 * kFQ, p + 18 * kFQ, p + 26 * kFQ, p + 31 * kFQ};
+// Joins one head's sums over wavefronts and writes them out for sb_ddt_kernel: threads 0-127 u,
+// 128-255 v, 256-383 the row sums, 384-447 the row sums' sums by tile, 448 <G, S>.
+template <int N>
+__device__ __forceinline__ void head_sums(const uint8_t* sm, int hb, float* out, int tid) {
+    using O = GradLds<N>;
+    const int t = tid & 127, which = tid >> 7;
+    const float* row = reinterpret_cast<const float*>(sm + hb);
+    if (which < 2) {
+        const float* p = reinterpret_cast<const float*>(sm + hb + (which ? O::V : O::U)) + t;
+        float v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N / 16; ++i) v += p[i * kFQ];
+        out[(which ? kSumV : kSumU) * kFQ + t] = v;
+    } else if (which == 2) {
+        float off = 0.0f;
+        const int j = t >> 4;
+        for (int i = 0; i < j; ++i) off += row[i * kFQ + t];
+        out[kSumRowOff * kFQ + t] = off;
+        out[kSumRowDiag * kFQ + t] = row[j * kFQ + t];
+    } else if (t < 64) {
+        const int j = t >> 3, i = t & 7;
+        float r = 0.0f;
+        if (i < j) {
+            const f4* p = reinterpret_cast<const f4*>(row + i * kFQ + 16 * j);
+            const f4 q = (p[0] + p[1]) + (p[2] + p[3]);
+            r = (q[0] + q[1]) + (q[2] + q[3]);
+        }
+        out[kSums * kFQ + t] = r;
+    } else if (t == 64) {
+        const float* p = reinterpret_cast<const float*>(sm + hb + O::DOT);
+        float d = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N / 16; ++i) d += p[i];
+        out[kSums * kFQ + 64] = d;
+    }
 }
 
-// q, ddt and the chunk's share of dA for one head, by one wavefront (tokens lane and 64 + lane)
-template <int NT>
-__device__ __forceinline__ void head_end(const ScanBwdArgs& a, const HeadPart& p, const int* starts,
-                                         int64_t b, int64_t c, int64_t h, int nv, int lane) {
-    double q[2], vd[2];
-    float direct[2], dts[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int t = lane + 64 * k;
-        float row = 0.0f, u = 0.0f, v = 0.0f;
-        for (int i = 0; i <= t / 16; ++i) row += p.row[i * kFQ + t];
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            u += p.u[i * kFQ + t];
-            v += p.v[i * kFQ + t];
-        }
-        const float below = p.col[t], all = p.col[kFQ + t];
-        dts[k] = p.dec[4 * kFQ + t];
-        vd[k] = static_cast<double>(v) * dts[k];
-        q[k] = static_cast<double>(row) - static_cast<double>(below) * dts[k] + u - vd[k];
-        direct[k] = all + v;
-    }
-    double vsum = vd[0] + vd[1];
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) vsum += __shfl_xor(vsum, o);
-    const float th = a.through[(b * a.H + h) * a.chunks + c];
-    float dot = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NT; ++i) dot += p.gs[i];
-    if (lane == 63) q[1] += vsum + (th == 0.0f ? 0.0 : static_cast<double>(th) * dot);
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const double u0 = __shfl_down(q[0], o), u1 = __shfl_down(q[1], o);
-        if (lane + o < 64) {
-            q[0] += u0;
-            q[1] += u1;
-        }
-    }
-    q[0] += __shfl(q[1], 0);
-    const double A = a.A[h];
-    double da = 0.0;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int t = lane + 64 * k;
-        if (starts[t] != (t > 0 ? starts[t - 1] : 0)) q[k] = 0.0;  // a start takes nothing over
-        if (t < nv) {
-            a.ddt[(b * a.L + c * kFQ + t) * a.H + h] = static_cast<float>(q[k] * A + direct[k]);
-            da += q[k] * dts[k];
-        }
-    }
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) da += __shfl_xor(da, o);
-    if (lane == 0) a.dA_part[(b * a.chunks + c) * a.H + h] = da;
+// Makes an offset opaque: what is derived from it is computed where it is used instead of being
+// kept in registers over the whole loop over the heads.
+__device__ __forceinline__ int here(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
 }
 
 template <int N>
@@ -428,6 +409,7 @@ __global__ void __launch_bounds__(512) sbf_grad_kernel(ScanBwdArgs a) {
     constexpr int NT = N / 16, RB = 2 * N, BP = N / 8;
     constexpr int TT = NT;       // t tiles a wavefront does for dB and dC: all 8, or half of them
     constexpr int PL = N * 128;  // bytes of one part of G
+    constexpr int LR = kFQ * 4;  // bytes of one float a token
     __shared__ __attribute__((aligned(16))) uint8_t sm[O::TOTAL];
     const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g4 = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -442,26 +424,33 @@ __global__ void __launch_bounds__(512) sbf_grad_kernel(ScanBwdArgs a) {
     const int st = wave < 4 ? wave : 11 - wave;  // s tile for the pairs: 9 tiles a SIMD (waves w, w + 4)
     int* starts = reinterpret_cast<int*>(sm + O::START);
 
-    const uint16_t* xg = static_cast<const uint16_t*>(a.x) + tok * a.x_row;
-    const uint16_t* dyg = static_cast<const uint16_t*>(a.dy) + tok * a.dy_row;
+    // loads of one head: uniform bases that move with the head, 32-bit lane offsets that do not
+    // (128 token rows are under 2^32 bytes)
+    const int row = tid >> 3;  // and row + 64
+    const uint32_t vx = static_cast<uint32_t>(row * a.x_row * 2 + 16 * (tid & 7));
+    const uint32_t vdy = static_cast<uint32_t>(row * a.dy_row * 2 + 16 * (tid & 7));
+    const uint32_t vs = static_cast<uint32_t>((16 * nt + li) * (kFP * 4) + 32 * g4);
     u4 rx[2], rdy[2];
     f4 rS[4], rG[4];
     float rd[2];
     auto load = [&](int64_t h) __attribute__((always_inline)) {
+        const char* xb = reinterpret_cast<const char*>(static_cast<const uint16_t*>(a.x) + tok * a.x_row + h * kFP);
+        const char* db = reinterpret_cast<const char*>(static_cast<const uint16_t*>(a.dy) + tok * a.dy_row + h * kFP);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int q = tid + 512 * i, row = q >> 3;
             rx[i] = rdy[i] = u4{0, 0, 0, 0};
-            if (row < nv) {
-                rx[i] = *reinterpret_cast<const u4any*>(xg + row * a.x_row + h * kFP + 8 * (q & 7));
-                rdy[i] = *reinterpret_cast<const u4any*>(dyg + row * a.dy_row + h * kFP + 8 * (q & 7));
+            if (row + 64 * i < nv) {
+                rx[i] = *reinterpret_cast<const u4any*>(xb + i * 128 * a.x_row + vx);
+                rdy[i] = *reinterpret_cast<const u4any*>(db + i * 128 * a.dy_row + vdy);
             }
         }
-        const int64_t at = ((b * a.H + h) * a.chunks + c) * N * kFP + (16 * nt + li) * kFP + 8 * g4;
+        const int64_t at = ((b * a.H + h) * a.chunks + c) * N * kFP;
+        const char* sp = reinterpret_cast<const char*>(a.states + at);
+        const char* gp = reinterpret_cast<const char*>(a.grads + at);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            rS[i] = *reinterpret_cast<const f4*>(a.states + at + 32 * (i >> 1) + 4 * (i & 1));
-            rG[i] = *reinterpret_cast<const f4*>(a.grads + at + 32 * (i >> 1) + 4 * (i & 1));
+            rS[i] = *reinterpret_cast<const f4*>(sp + 128 * (i >> 1) + 16 * (i & 1) + vs);
+            rG[i] = *reinterpret_cast<const f4*>(gp + 128 * (i >> 1) + 16 * (i & 1) + vs);
         }
         const float* rec = a.decay + ((b * a.H + h) * a.chunks + c) * 5 * kFQ;
         rd[0] = rec[tid];
@@ -472,137 +461,169 @@ __global__ void __launch_bounds__(512) sbf_grad_kernel(ScanBwdArgs a) {
         const uint16_t* bg = static_cast<const uint16_t*>(a.Bm) + tok * a.b_row + g * N;
         const uint16_t* cg = static_cast<const uint16_t*>(a.C) + tok * a.c_row + g * N;
         for (int q = tid; q < kFQ * BP; q += 512) {
-            const int row = q / BP;
+            const int r = q / BP;
             u4 v{0, 0, 0, 0}, u{0, 0, 0, 0};
-            if (row < nv) {
-                v = *reinterpret_cast<const u4any*>(bg + row * a.b_row + 8 * (q % BP));
-                u = *reinterpret_cast<const u4any*>(cg + row * a.c_row + 8 * (q % BP));
+            if (r < nv) {
+                v = *reinterpret_cast<const u4any*>(bg + r * a.b_row + 8 * (q % BP));
+                u = *reinterpret_cast<const u4any*>(cg + r * a.c_row + 8 * (q % BP));
             }
-            *reinterpret_cast<u4*>(sm + O::B + piece<RB>(row, q % BP)) = v;
-            *reinterpret_cast<u4*>(sm + O::C + piece<RB>(row, q % BP)) = u;
+            *reinterpret_cast<u4*>(sm + O::B + piece<RB>(r, q % BP)) = v;
+            *reinterpret_cast<u4*>(sm + O::C + piece<RB>(r, q % BP)) = u;
         }
         if (tid < kFQ) starts[tid] = a.starts[(b * a.chunks + c) * kFQ + tid];
     }
     __syncthreads();
-    const bool masked = starts[kFQ - 1] != 0;
-    const int ao = along_off<RB>(li, g4), xo = along_off<128>(li, g4);
-    const int yo = down_off<128>(4 * g4, li);
-    const int go0 = down_off<128>(8 * g4, li), go1 = down_off<128>(8 * g4 + 4, li);
+    const int any_start = __builtin_amdgcn_readfirstlane(starts[kFQ - 1]);
+    const int s = 16 * st + li;
+    const int rs = starts[s];
 
-    // C B^T for the pairs of this wavefront's s tile, t tiles st .. 7
-    f4 cb[8], lw[8];
+    f4 lw[8];  // sums over the heads of L dt (dy x^T), tiles of s tile st
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        cb[j] = lw[j] = f4{0, 0, 0, 0};
-        if (j >= st) {
-#pragma unroll
-            for (int kk = 0; kk < N / 32; ++kk)
-                cb[j] = mfma(along<RB>(sm + O::C, ao, 16 * j, kk), along<RB>(sm + O::B, ao, 16 * st, kk), cb[j]);
-        }
-    }
+    for (int j = 0; j < 8; ++j) lw[j] = f4{0, 0, 0, 0};
     f4 accC[TT], accB[TT];
 #pragma unroll
     for (int j = 0; j < TT; ++j) accC[j] = accB[j] = f4{0, 0, 0, 0};
 
-    const int s = 16 * st + li;
-    const int rs = starts[s];
+    const int64_t sum_step = a.chunks * (kSums * kFQ + kSumTail);
+    float* sums = a.sums + ((b * a.H + hfirst) * a.chunks + c) * (kSums * kFQ + kSumTail);
     for (int64_t h = hfirst; h < hend; ++h) {
         const int par = static_cast<int>(h - hfirst) & 1;
-        const HeadPart hp = head_part(sm, O::ROW + par * O::HEAD);
-        // operands from the loaded states
-        bf8 Sp[2][3], Gp[2][3];
+        const int hb = O::ROW + par * O::HEAD;  // this head's part of LDS
+        int m = any_start;
+        asm volatile("" : "+s"(m));  // one copy of the loop, not one for each case
+        const bool masked = m != 0;
+        // operands from the loaded states: S in registers, G in LDS (its third part, which dx does
+        // without, in registers)
+        bf8 Sp[2][3], Glo[2];
         {
             float dot = 0.0f;
+            bf8 Gp[2][3];
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
-                float vs[8], vg[8];
+                float v1[8], v2[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    vs[e] = rS[2 * kk + (e >> 2)][e & 3];
-                    vg[e] = rG[2 * kk + (e >> 2)][e & 3];
-                    dot += vs[e] * vg[e];
+                    v1[e] = rS[2 * kk + (e >> 2)][e & 3];
+                    v2[e] = rG[2 * kk + (e >> 2)][e & 3];
+                    dot += v1[e] * v2[e];
                 }
-                split(vs, Sp[kk]);
-                split(vg, Gp[kk]);
+                split(v1, Sp[kk]);
+                split(v2, Gp[kk]);
+                Glo[kk] = Gp[kk][2];
+                rG[2 * kk] = __builtin_bit_cast(f4, Gp[kk][0]);
+                rG[2 * kk + 1] = __builtin_bit_cast(f4, Gp[kk][1]);
             }
             dot = group_sum4(lane_sum16(dot));
-            if (lane == 0 && wave < NT) hp.gs[wave] = dot;
+            if (lane == 0 && wave < NT) *reinterpret_cast<float*>(sm + hb + O::DOT + 4 * nt) = dot;
         }
         __syncthreads();  // the previous head's x, dy and G have been read
+        {
+            const int o = here(piece<128>(row, tid & 7));  // rows row and row + 64 share the swizzle
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int q = tid + 512 * i, o = piece<128>(q >> 3, q & 7);
-            *reinterpret_cast<u4*>(sm + O::X + o) = rx[i];
-            *reinterpret_cast<u4*>(sm + O::DY + o) = rdy[i];
+            for (int i = 0; i < 2; ++i) {
+                *reinterpret_cast<u4*>(sm + o + O::X + i * 64 * 128) = rx[i];
+                *reinterpret_cast<u4*>(sm + o + O::DY + i * 64 * 128) = rdy[i];
+            }
+            if (wave < NT) {
+                const int q = here(O::G + 16 * nt * 128 + along_off<128>(li, g4));
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) *reinterpret_cast<f4*>(sm + k * PL + (q ^ (kk << 6))) = rG[2 * kk + k];
+            }
+            float* dec = reinterpret_cast<float*>(sm + hb + O::DEC);
+            dec[tid] = rd[0];
+            if (tid < kFQ) dec[4 * kFQ + tid] = rd[1];
         }
-        if (wave < NT) {
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    *reinterpret_cast<bf8*>(sm + O::G + k * PL + piece<128>(16 * nt + li, 4 * kk + g4)) = Gp[kk][k];
-        }
-        hp.dec[tid] = rd[0];
-        if (tid < kFQ) hp.dec[4 * kFQ + tid] = rd[1];
         __syncthreads();
-        if (h > hfirst && wave == static_cast<int>((h - 1 - hfirst) & 7))
-            head_end<NT>(a, head_part(sm, O::ROW + (par ^ 1) * O::HEAD), starts, b, c, h - 1, nv, lane);
+        if (h > hfirst) head_sums<N>(sm, O::ROW + (par ^ 1) * O::HEAD, sums - sum_step, tid);
 
-        // ---- dy against S and x: dC, u, the pairs ----
+        // LDS offsets of this head's reads
+        const int ao = here(along_off<RB>(li, g4));                      // B, C along rows
+        const int bst = here(along_off<RB>(li, g4) + 16 * st * RB);      // B, rows of s tile st
+        const int xo = here(O::X + along_off<128>(li, g4));              // x, dy along rows
+        const int yo = here(O::DY + down_off<128>(4 * g4, li));          // dy down rows
+        const int cw = here(piece<RB>(li, 2 * nt + (g4 >> 1)) + 8 * (g4 & 1));  // C, B elements (n 4 g4 .., t li)
+        const int tl = here(hb + O::DEC + 4 * li);                       // decays of token li of a tile
+        const int t4 = here(hb + O::DEC + 16 * g4);                      // decays of tokens 4 g4 ..
+        const int ut = here(hb + O::U + nt * LR + 4 * li);               // u, v of n tile nt
+        const int rt = here(hb + st * LR + 16 * g4 + 4 * (li & 3));      // row sums
+
+        // ---- dy against S: dC, u ----
+#pragma unroll
+        for (int jj = 0; jj < TT; ++jj) {
+            const int j = th0 + jj;
+            const bf8 d0 = lds<bf8>(sm + xo + (O::DY - O::X) + 16 * j * 128);
+            const bf8 d1 = lds<bf8>(sm + (xo ^ 64) + (O::DY - O::X) + 16 * j * 128);
+            f4 o{0, 0, 0, 0};
+#pragma unroll
+            for (int k = 2; k >= 0; --k) {
+                o = mfma(Sp[0][k], d0, o);
+                o = mfma(Sp[1][k], d1, o);
+            }
+            const float ft = lds<float>(sm + tl + 2 * LR + 64 * j);
+            const u2 cv = lds<u2>(sm + cw + O::C + 16 * j * RB);
+            if (masked) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] = ft == 0.0f ? 0.0f : o[e];
+            }
+            float u = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                u += __uint_as_float(e & 1 ? cv[e >> 1] & 0xFFFF0000u : cv[e >> 1] << 16) * o[e];
+                accC[jj][e] += ft * o[e];
+            }
+            u = group_sum4(u) * ft;
+            if (g4 == 0) *reinterpret_cast<float*>(sm + ut + 64 * j) = u;
+        }
+
+        // ---- pairs s <= t of s tile st: W's sums, the pairs' part of dx ----
         f4 dxa[4];
 #pragma unroll
         for (int p = 0; p < 4; ++p) dxa[p] = f4{0, 0, 0, 0};
-        const bf8 xf0 = along<128>(sm + O::X, xo, 16 * st, 0), xf1 = along<128>(sm + O::X, xo, 16 * st, 1);
-        const float hs_ = hp.dec[s], ls_ = hp.dec[kFQ + s], dts = hp.dec[4 * kFQ + s];
-        float below = 0.0f, diag = 0.0f;
+        const bf8 xf0 = lds<bf8>(sm + xo + 16 * st * 128), xf1 = lds<bf8>(sm + (xo ^ 64) + 16 * st * 128);
+        const float hi_s = lds<float>(sm + tl + 64 * st), lo_s = lds<float>(sm + tl + LR + 64 * st);
+        const float dts = lds<float>(sm + tl + 4 * LR + 64 * st);
+        float below = 0.0f, bdiag = 0.0f, diag = 0.0f;  // column sums of W / dt_s
         u4 pw[2];  // two parts of the pairs of two t tiles, in token order
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const bf8 d0 = along<128>(sm + O::DY, xo, 16 * j, 0), d1 = along<128>(sm + O::DY, xo, 16 * j, 1);
-            if (j >= th0 && j < th0 + TT) {
-                f4 o{0, 0, 0, 0};
-#pragma unroll
-                for (int k = 2; k >= 0; --k) {
-                    o = mfma(Sp[0][k], d0, o);
-                    o = mfma(Sp[1][k], d1, o);
-                }
-                const int t = 16 * j + li;
-                const float ft = hp.dec[2 * kFQ + t];
-                const u2 cw = lds<u2>(sm + O::C + piece<RB>(t, 2 * nt + (g4 >> 1)) + 8 * (g4 & 1));
-                float u = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (masked && ft == 0.0f) o[e] = 0.0f;
-                    u += __uint_as_float(e & 1 ? cw[e >> 1] & 0xFFFF0000u : cw[e >> 1] << 16) * o[e];
-                    if (NT == 8) accC[j][e] += ft * o[e];
-                    else accC[j & 3][e] += ft * o[e];
-                }
-                u = group_sum4(u) * ft;
-                if (g4 == 0) hp.u[nt * kFQ + t] = u;
-            }
             if (j >= st) {
-                f4 yx = mfma(d0, xf0, f4{0, 0, 0, 0});
-                yx = mfma(d1, xf1, yx);
-                const f4 ht = *reinterpret_cast<const f4*>(hp.dec + 16 * j + 4 * g4);
-                const f4 lt = *reinterpret_cast<const f4*>(hp.dec + kFQ + 16 * j + 4 * g4);
-                float pv[4], row[4];
+                f4 yx = mfma(lds<bf8>(sm + xo + (O::DY - O::X) + 16 * j * 128), xf0, f4{0, 0, 0, 0});
+                yx = mfma(lds<bf8>(sm + (xo ^ 64) + (O::DY - O::X) + 16 * j * 128), xf1, yx);
+                f4 cb{0, 0, 0, 0};
+#pragma unroll
+                for (int kk = 0; kk < N / 32; ++kk)
+                    cb = mfma(lds<bf8>(sm + (ao ^ (kk << 6)) + O::C + 16 * j * RB), lds<bf8>(sm + (bst ^ (kk << 6))), cb);
+                const f4 ht = lds<f4>(sm + t4 + 64 * j), lt = lds<f4>(sm + t4 + LR + 64 * j);
+                f4 l;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) l[e] = __builtin_amdgcn_exp2f((ht[e] - hi_s) + (lt[e] - lo_s));
+                if (masked) {
+                    const int4 r = *reinterpret_cast<const int4*>(starts + 16 * j + 4 * g4);
+                    l = f4{r.x == rs ? l[0] : 0.0f, r.y == rs ? l[1] : 0.0f, r.z == rs ? l[2] : 0.0f, r.w == rs ? l[3] : 0.0f};
+                }
+                float dw[4] = {0, 0, 0, 0};  // products of a token with itself
+                if (j == st) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (4 * g4 + e < li) l[e] = 0.0f;
+                        dw[e] = 4 * g4 + e == li ? cb[e] * yx[e] : 0.0f;
+                        diag += dw[e];
+                    }
+                }
+                float pv[4], rw[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    float l = __builtin_amdgcn_exp2f((ht[e] - hs_) + (lt[e] - ls_));
-                    const int t = 4 * g4 + e;  // within the tile
-                    if (j == st && t < li) l = 0.0f;
-                    if (masked && starts[16 * j + t] != rs) l = 0.0f;
-                    pv[e] = l * cb[j][e];
-                    lw[j][e] += l * yx[e] * dts;
-                    float w = pv[e] * yx[e];
-                    if (j == st && t == li) {
-                        diag = w;
-                        w = 0.0f;
-                    }
-                    below += w;
-                    row[e] = lane_sum16(w * dts);
+                    pv[e] = l[e] * cb[e];
+                    lw[j][e] += l[e] * yx[e] * dts;
+                    const float w = pv[e] * yx[e] - dw[e];  // l = 1 on the diagonal: exactly 0 there
+                    if (j == st) bdiag += w;
+                    else below += w;
+                    rw[e] = lane_sum16(w * dts);
                 }
-                if (li < 4) hp.row[st * kFQ + 16 * j + 4 * g4 + li] = li == 0 ? row[0] : li == 1 ? row[1] : li == 2 ? row[2] : row[3];
+                const float r01 = li & 1 ? rw[1] : rw[0], r23 = li & 1 ? rw[3] : rw[2];
+                if (li < 4) *reinterpret_cast<float*>(sm + rt + 64 * j) = li & 2 ? r23 : r01;
                 // two parts, into this tile's half of the operand
                 const uint32_t q0 = pack_bf16x2(pv[0], pv[1]), q1 = pack_bf16x2(pv[2], pv[3]);
                 pw[0][2 * (j & 1)] = q0;
@@ -615,70 +636,91 @@ __global__ void __launch_bounds__(512) sbf_grad_kernel(ScanBwdArgs a) {
             if ((j & 1) && j >= st) {
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
-                    const bf8 y = down<128>(sm + O::DY, yo, 16 * (j - 1), p);
+                    const uint8_t* q = sm + (yo ^ (p << 5)) + 16 * (j - 1) * 128;
+                    const bf8 y = join(tr_read(q), tr_read(q + 16 * 128));
                     dxa[p] = mfma(y, __builtin_bit_cast(bf8, pw[1]), dxa[p]);
                     dxa[p] = mfma(y, __builtin_bit_cast(bf8, pw[0]), dxa[p]);
                 }
             }
         }
         below = group_sum4(below);
+        bdiag = group_sum4(bdiag);
         diag = group_sum4(diag);
-        if (g4 == 0) {
-            hp.col[s] = below;
-            hp.col[kFQ + s] = below + diag;
+        if (g4 < 3) {  // kSumColOff, kSumColDiag, kSumDiag
+            const float v = g4 == 0 ? below : g4 == 1 ? bdiag : diag;
+            sums[(kSumColOff + g4) * kFQ + s] = v;
         }
+        sums += sum_step;
         if (h + 1 < hend) load(h + 1);
 
         // ---- x against G: dB, v ----
+        bf8 Gp[2][3];
+        {
+            const int q = here(O::G + 16 * nt * 128 + along_off<128>(li, g4));
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                Gp[kk][0] = lds<bf8>(sm + (q ^ (kk << 6)));
+                Gp[kk][1] = lds<bf8>(sm + PL + (q ^ (kk << 6)));
+                Gp[kk][2] = Glo[kk];
+            }
+        }
 #pragma unroll
         for (int jj = 0; jj < TT; ++jj) {
             const int j = th0 + jj;
-            const bf8 x0 = along<128>(sm + O::X, xo, 16 * j, 0), x1 = along<128>(sm + O::X, xo, 16 * j, 1);
+            const bf8 x0 = lds<bf8>(sm + xo + 16 * j * 128), x1 = lds<bf8>(sm + (xo ^ 64) + 16 * j * 128);
             f4 o{0, 0, 0, 0};
 #pragma unroll
             for (int k = 2; k >= 0; --k) {
                 o = mfma(Gp[0][k], x0, o);
                 o = mfma(Gp[1][k], x1, o);
             }
-            const int t = 16 * j + li;
-            const float es = hp.dec[3 * kFQ + t], ed = es * hp.dec[4 * kFQ + t];
-            const u2 bw = lds<u2>(sm + O::B + piece<RB>(t, 2 * nt + (g4 >> 1)) + 8 * (g4 & 1));
+            const float es = lds<float>(sm + tl + 3 * LR + 64 * j), ed = es * lds<float>(sm + tl + 4 * LR + 64 * j);
+            const u2 bv = lds<u2>(sm + cw + O::B + 16 * j * RB);
+            if (masked) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] = es == 0.0f ? 0.0f : o[e];
+            }
             float v = 0.0f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                if (masked && es == 0.0f) o[e] = 0.0f;
-                v += __uint_as_float(e & 1 ? bw[e >> 1] & 0xFFFF0000u : bw[e >> 1] << 16) * o[e];
+                v += __uint_as_float(e & 1 ? bv[e >> 1] & 0xFFFF0000u : bv[e >> 1] << 16) * o[e];
                 accB[jj][e] += ed * o[e];
             }
             v = group_sum4(v) * es;
-            if (g4 == 0) hp.v[nt * kFQ + t] = v;
+            if (g4 == 0) *reinterpret_cast<float*>(sm + ut + (O::V - O::U) + 64 * j) = v;
         }
 
         // ---- dx: G B, then with the pairs ----
-        const float es = hp.dec[3 * kFQ + s];
-        uint16_t* dxo = static_cast<uint16_t*>(a.dx) + (tok + s) * a.dx_row + h * kFP + 4 * g4;
+        const float es = lds<float>(sm + tl + 3 * LR + 64 * st);
+        const int go0 = here(O::G + down_off<128>(8 * g4, li)), go1 = here(O::G + down_off<128>(8 * g4 + 4, li));
+        f4 gb[4];
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            f4 o{0, 0, 0, 0};
+        for (int p = 0; p < 4; ++p) gb[p] = f4{0, 0, 0, 0};
 #pragma unroll
-            for (int kk = 0; kk < N / 32; ++kk) {
-                const bf8 bf = along<RB>(sm + O::B, ao, 16 * st, kk);
+        for (int kk = 0; kk < N / 32; ++kk) {
+            const bf8 bf = lds<bf8>(sm + (bst ^ (kk << 6)));
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
 #pragma unroll
                 for (int k = 1; k >= 0; --k) {
-                    const uint8_t* pl = sm + O::G + k * PL + 32 * kk * 128;
-                    o = mfma(join(tr_read(pl + (go0 ^ (p << 5))), tr_read(pl + (go1 ^ (p << 5)))), bf, o);
+                    const int o = k * PL + 32 * kk * 128;
+                    gb[p] = mfma(join(tr_read(sm + (go0 ^ (p << 5)) + o), tr_read(sm + (go1 ^ (p << 5)) + o)), bf, gb[p]);
                 }
-            }
-            f4 r;
+        }
+        char* dxo = reinterpret_cast<char*>(static_cast<uint16_t*>(a.dx) + tok * a.dx_row + h * kFP);
+        const uint32_t vdx = here(static_cast<int>(s * a.dx_row * 2 + 8 * g4));
+        if (s < nv) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) r[e] = dts * (dxa[p][e] + (masked && es == 0.0f ? 0.0f : es * o[e]));
-            if (s < nv) *reinterpret_cast<u2any*>(dxo + 16 * p) = u2{pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3])};
+            for (int p = 0; p < 4; ++p) {
+                f4 r;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) r[e] = dts * (dxa[p][e] + (es == 0.0f ? 0.0f : es * gb[p][e]));
+                *reinterpret_cast<u2any*>(dxo + vdx + 32 * p) = u2{pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3])};
+            }
         }
     }
     __syncthreads();
-    if (wave == static_cast<int>((hend - 1 - hfirst) & 7))
-        head_end<NT>(a, head_part(sm, O::ROW + (static_cast<int>(hend - 1 - hfirst) & 1) * O::HEAD), starts, b, c,
-                     hend - 1, nv, lane);
+    head_sums<N>(sm, O::ROW + (static_cast<int>(hend - 1 - hfirst) & 1) * O::HEAD, sums - sum_step, tid);
 
     // ---- the heads' summed pairs: two parts of [t][s] in LDS (zero above the diagonal) ----
 #pragma unroll
@@ -693,8 +735,8 @@ __global__ void __launch_bounds__(512) sbf_grad_kernel(ScanBwdArgs a) {
             *reinterpret_cast<uint16_t*>(sm + O::LW + kFQ * 256 + o) = lo;
         }
     __syncthreads();
-    const int bo = down_off<RB>(4 * g4, li) ^ (nt << 5);       // B^T, C^T: rows of n tile nt
-    const int b0 = down_off<RB>(8 * g4, li) ^ (nt << 5), b1 = down_off<RB>(8 * g4 + 4, li) ^ (nt << 5);
+    const int bo = down_off<RB>(4 * g4, li) ^ (nt << 5);       // C^T: rows of n tile nt
+    const int b0 = down_off<RB>(8 * g4, li) ^ (nt << 5), b1 = down_off<RB>(8 * g4 + 4, li) ^ (nt << 5);  // B^T
     const int lo_ = along_off<256>(li, g4), ld = down_off<256>(4 * g4, li);
 #pragma unroll
     for (int jj = 0; jj < TT; ++jj) {
@@ -774,6 +816,7 @@ size_t lay_out(ScanBwdArgs& a, uint8_t* base) {
     part(a.through, bhc);
     part(a.decay, bhc * 5 * kFQ);
     part(a.starts, static_cast<size_t>(a.B * a.chunks) * kFQ);
+    part(a.sums, bhc * (kSums * kFQ + kSumTail));
     part(a.states, bhc * a.P * a.N);
     part(a.grads, bhc * a.P * a.N);
     const size_t heads = a.splits > 1 ? static_cast<size_t>(a.splits * a.B * a.L * a.G * a.N) : 0;
@@ -820,7 +863,7 @@ hipError_t launch_scan_bwd_mfma(ScanBwdArgs a, void* workspace, hipStream_t s) {
     set_up(a);
     lay_out(a, static_cast<uint8_t*>(workspace));
     const hipError_t e = a.N == 128 ? launch_typed<128>(a, s) : launch_typed<64>(a, s);
-    return e == hipSuccess ? launch_scan_bwd_dA(a, s) : e;
+    return e == hipSuccess ? launch_scan_bwd_ddt(a, kFQ, s) : e;
 }
 
 }  // namespace ssm
