@@ -436,7 +436,8 @@ ssm_status_t ssm_scan_bwd_initial_state(const float* dt, const float* A, const v
  * headdim and dstate as ssm_scan_fwd takes them (dstate 4 * 2^k <= 256, headdim * dstate <=
  * 32768); dt * A finite.  Sums and states in fp32 (sums of log decays in double); outputs
  * rounded once; deterministic.  Outputs must not overlap inputs (dinitial_state ==
- * dfinal_state is refused).  Non-finite inputs may spread over the 64-token chunk they are in.
+ * dfinal_state is refused).  A non-finite value may reach every token of the 128-token chunks
+ * (of the row, from its start) that its sequence reaches, other sequences' among them.
  * seqlen = 0: dinitial_state = dfinal_state (or zeros), dA = 0.  batch = 0: dA = 0.
  * ------------------------------------------------------------------------------------- */
 size_t ssm_scan_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim,

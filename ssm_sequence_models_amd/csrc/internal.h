@@ -315,14 +315,18 @@ struct ScanBwdArgs {
     float* decay;      // [B, H, chunks, 5, 128]: sums of log2 a (hi, lo), f, e, dt
     int32_t* starts;   // [B, chunks, 128]: sequence starts so far in the chunk
     int64_t splits, split_heads;  // ranges of a group's heads a chunk, heads in each
+    int64_t dc_splits, dc_heads;  // the same for dC's part from before the chunk
+    float* anchor;     // [B, H, ceil(chunks / kAnchor)]: f_last <G, S> of the last chunk of each
     float* sums;       // [B, H, chunks, kSums * Q + kSumTail], Q the chunk's tokens
 };
 // Sums over pairs of tokens that ddt and dA are formed from (W, u, v as in scan_bwd.hip), each an
 // array over the chunk's tokens: u; v / dt; row sums of W over s < t, in earlier 16-token tiles
 // and in t's own; column sums of W / dt_s over t > s, in later tiles and in s's own; W_tt / dt_t.
-// Behind them the row sums' sums by tile, [t tile][s tile] in eights, then <G, S>.
+// Behind them the row sums' sums by tile, [t tile][s tile] in eights, then <G, S> (64-token chunks)
+// or the parts of |S|^2 and |G|^2 by 16 state dimensions, in eights (128).
 enum { kSumU, kSumV, kSumRowOff, kSumRowDiag, kSumColOff, kSumColDiag, kSumDiag, kSums };
 constexpr int kSumTail = 128;
+constexpr int kAnchor = 8;
 size_t scan_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N,
                                 ssm_dtype_t dtype);
 int64_t scan_bwd_blocks(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N);

@@ -10,11 +10,19 @@
 //   sbf_states  S and G, one block a row, head and direction walking over the chunks with the
 //               state in accumulators (or, where those are too few blocks, one block a chunk,
 //               joined along the row by sbf_pass)
-//   sbf_grad    one block a chunk, group and range of its heads: everything else.  B and C stay
-//               in LDS and C B^T in registers for all heads; the sums over heads of
-//               L dt (dy x^T), from which dB and dC take their pairs, stay in registers as
-//               well, and dB and dC in accumulators: they are summed over the heads without
-//               traffic.  Ranges of heads are joined by sbf_join (in order).
+//   sbf_dc      one block a chunk, group and range of its heads: dy against S, dC's part from
+//               before the chunk in accumulators over the heads, and u
+//   sbf_grad    one block a chunk, group and range of its heads: everything else.  B and the
+//               pairs' C B^T stay in LDS for all heads; the sums over heads of L dt (dy x^T),
+//               from which dB and dC take their pairs, stay in registers, and dB in accumulators:
+//               the heads are summed without traffic.  Ranges of heads are joined by sbf_join.
+//   sbf_anchor  f_last <G, S> of every eighth chunk; sb_ddt has the others from
+//               f<G, S> of c = f<G, S> of c + 1 + sum of u of c + 1 - sum of v of c
+//               (both sides plus sum of v are <G_c, S_{c+1}>), so S and G are not read a second
+//               time; the rounding errors of eight chunks at most add up, and where f <G, S> is
+//               far below u and v, |G| |S| f bounds it and with it the error
+// One kernel for dC and the rest together read S, G and dy once, but held 300 registers a lane:
+// at two wavefronts a SIMD (LDS) it spilled, and took 2318 us where the two take 0 us.
 //
 // Operands: x, dy, B and C are exact in bf16.  The fp32 operands S and G and the scaled x and dy
 // of sbf_states are taken in three bf16 parts (24 bits, nothing lost: ddt and dA are fp32
@@ -118,6 +126,40 @@ __device__ __forceinline__ float lane_sum16(float v) {  // over the 16 lanes tha
 __device__ __forceinline__ float group_sum4(float v) {  // over the four lanes that share li
     v += __shfl_xor(v, 16);
     return v + __shfl_xor(v, 32);
+}
+
+// Sums over the four lanes that share li, of four values at once: rows of 16 lanes 0, 1, 2, 3 of
+// the result hold the sums of a, c, b, d.
+__device__ __forceinline__ float group_sums(float a, float b, float c, float d) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(c), __float_as_uint(d), false, false);
+    const float ab = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+    const float cd = __uint_as_float(q[0]) + __uint_as_float(q[1]);
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(ab), __float_as_uint(cd), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ int group_of_row(int row) { return row == 1 ? 2 : row == 2 ? 1 : row; }
+// Sums over the 16 lanes that share g4, of four values at once: lane li holds that of v[li % 4].
+__device__ __forceinline__ float row_sums(const float (&v)[4], int li) {
+    const float k01 = li & 1 ? v[1] : v[0], s01 = li & 1 ? v[0] : v[1];
+    const float k23 = li & 1 ? v[3] : v[2], s23 = li & 1 ? v[2] : v[3];
+    const float a = k01 + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(s01), 0xB1, 0xf, 0xf, true));
+    const float b = k23 + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(s23), 0xB1, 0xf, 0xf, true));
+    const float k = li & 2 ? b : a, o = li & 2 ? a : b;
+    float r = k + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(o), 0x4E, 0xf, 0xf, true));
+    r += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(r), 0x124, 0xf, 0xf, true));         // rotated by 4
+    return r + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(r), 0x128, 0xf, 0xf, true));   // by 8
+}
+// Makes an offset opaque: what is derived from it is computed where it is used instead of being
+// kept in registers over the whole loop over the heads.
+__device__ __forceinline__ int here(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+// keeps a sum where it is computed (moved to the loop's end it would keep its terms in registers)
+__device__ __forceinline__ void settle(f4& v) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) asm volatile("" : "+v"(v[e]));
 }
 
 // ---------------------------------------------------------------------------------------
@@ -344,41 +386,40 @@ __global__ void __launch_bounds__(256) sbf_pass_kernel(ScanBwdArgs a) {
 template <int N>
 struct GradLds {
     static constexpr int B = 0;                        // [128 s][N] bf16
-    static constexpr int C = B + kFQ * N * 2;          // [128 t][N] bf16
-    static constexpr int X = C + kFQ * N * 2;          // [128 s][64] bf16
+    static constexpr int CB = B + kFQ * N * 2;         // C B^T, 36 tiles as results lie (at first and last: C)
+    static constexpr int X = CB + 36 * 1024;           // [128 s][64] bf16
     static constexpr int DY = X + kFQ * 128;           // [128 t][64] bf16
     static constexpr int G = DY + kFQ * 128;           // two parts of [N][64] bf16
     static constexpr int LW = X;                       // at the end: two parts of [128 t][128 s] bf16
     static constexpr int ROW = (G + 2 * N * 128 > LW + 2 * kFQ * 256 ? G + 2 * N * 128 : LW + 2 * kFQ * 256);
-    // per parity of the head: row sums of W by s tile [8][128], u by n tile [8][128], v [8][128],
-    // decays [5][128], <G, S> by wavefront [8]
-    static constexpr int U = 8 * kFQ * 4, V = 16 * kFQ * 4, DEC = 24 * kFQ * 4, DOT = 29 * kFQ * 4;
-    static constexpr int HEAD = DOT + 32;
+    // per parity of the head: row sums of W by s tile [8][128], v by n tile [8][128], decays [5][128]
+    static constexpr int V = 8 * kFQ * 4, DEC = 16 * kFQ * 4;
+    static constexpr int HEAD = DEC + 5 * kFQ * 4;
     static constexpr int START = ROW + 2 * HEAD;       // [128] int
     static constexpr int TOTAL = START + kFQ * 4;
 };
 static_assert(GradLds<128>::TOTAL <= 160 * 1024, "LDS");
 
-// Joins one head's sums over wavefronts and writes them out for sb_ddt_kernel: threads 0-127 u,
-// 128-255 v, 256-383 the row sums, 384-447 the row sums' sums by tile, 448 <G, S>.
+// Joins one head's sums over wavefronts and writes them out for the ddt kernel: threads 0-127 v,
+// 128-255 the row sums, 256-319 the row sums' sums by tile.
 template <int N>
 __device__ __forceinline__ void head_sums(const uint8_t* sm, int hb, float* out, int tid) {
     using O = GradLds<N>;
     const int t = tid & 127, which = tid >> 7;
     const float* row = reinterpret_cast<const float*>(sm + hb);
-    if (which < 2) {
-        const float* p = reinterpret_cast<const float*>(sm + hb + (which ? O::V : O::U)) + t;
+    if (which == 0) {
+        const float* p = reinterpret_cast<const float*>(sm + hb + O::V) + t;
         float v = 0.0f;
 #pragma unroll
         for (int i = 0; i < N / 16; ++i) v += p[i * kFQ];
-        out[(which ? kSumV : kSumU) * kFQ + t] = v;
-    } else if (which == 2) {
+        out[kSumV * kFQ + t] = v;
+    } else if (which == 1) {
         float off = 0.0f;
         const int j = t >> 4;
         for (int i = 0; i < j; ++i) off += row[i * kFQ + t];
         out[kSumRowOff * kFQ + t] = off;
         out[kSumRowDiag * kFQ + t] = row[j * kFQ + t];
-    } else if (t < 64) {
+    } else if (which == 2 && t < 64) {
         const int j = t >> 3, i = t & 7;
         float r = 0.0f;
         if (i < j) {
@@ -387,20 +428,152 @@ __device__ __forceinline__ void head_sums(const uint8_t* sm, int hb, float* out,
             r = (q[0] + q[1]) + (q[2] + q[3]);
         }
         out[kSums * kFQ + t] = r;
-    } else if (t == 64) {
-        const float* p = reinterpret_cast<const float*>(sm + hb + O::DOT);
-        float d = 0.0f;
-#pragma unroll
-        for (int i = 0; i < N / 16; ++i) d += p[i];
-        out[kSums * kFQ + 64] = d;
     }
 }
 
-// Makes an offset opaque: what is derived from it is computed where it is used instead of being
-// kept in registers over the whole loop over the heads.
-__device__ __forceinline__ int here(int v) {
-    asm volatile("" : "+v"(v));
-    return v;
+// dC from before the chunk, summed over the heads of a range, and u
+template <int N>
+__global__ void __launch_bounds__(512, 4) sbf_dc_kernel(ScanBwdArgs a) {
+    constexpr int NT = N / 16, RB = 2 * N, BP = N / 8;
+    constexpr int TT = NT;  // t tiles a wavefront does: all 8, or half of them
+    __shared__ __attribute__((aligned(16))) uint8_t sc[kFQ * RB];
+    __shared__ __attribute__((aligned(16))) uint8_t sdy[2][kFQ * 128];
+    __shared__ float su[2][8][kFQ];
+    __shared__ float sf[2][kFQ];
+    const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g4 = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t hs = blockIdx.x % a.dc_splits, g = blockIdx.x / a.dc_splits % a.G;
+    const int64_t c = blockIdx.x / a.dc_splits / a.G % a.chunks, b = blockIdx.x / a.dc_splits / a.G / a.chunks;
+    const int64_t k_heads = a.H / a.G;
+    const int64_t hfirst = g * k_heads + hs * a.dc_heads;
+    const int64_t hend = hs * a.dc_heads + a.dc_heads < k_heads ? hfirst + a.dc_heads : (g + 1) * k_heads;
+    const int64_t t0 = c * kFQ, tok = b * a.L + t0;
+    const int nv = a.L - t0 < kFQ ? static_cast<int>(a.L - t0) : kFQ;
+    const int nt = wave % NT, th0 = NT == 8 ? 0 : (wave / NT) * TT;
+    const int row = tid >> 3;
+    const uint32_t vdy = static_cast<uint32_t>(row * a.dy_row * 2 + 16 * (tid & 7));
+    const uint32_t vs = static_cast<uint32_t>((16 * nt + li) * (kFP * 4) + 32 * g4);
+    u4 rdy[2];
+    f4 rS[4];
+    float rf = 0.0f;
+    auto load = [&](int64_t h) __attribute__((always_inline)) {
+        const char* db = reinterpret_cast<const char*>(static_cast<const uint16_t*>(a.dy) + tok * a.dy_row + h * kFP);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            rdy[i] = u4{0, 0, 0, 0};
+            if (row + 64 * i < nv) rdy[i] = *reinterpret_cast<const u4any*>(db + i * 128 * a.dy_row + vdy);
+        }
+        const char* sp = reinterpret_cast<const char*>(a.states + ((b * a.H + h) * a.chunks + c) * N * kFP);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) rS[i] = *reinterpret_cast<const f4*>(sp + 128 * (i >> 1) + 16 * (i & 1) + vs);
+        if (tid < kFQ) rf = a.decay[(((b * a.H + h) * a.chunks + c) * 5 + 2) * kFQ + tid];
+    };
+    load(hfirst);
+    {
+        const uint16_t* cg = static_cast<const uint16_t*>(a.C) + tok * a.c_row + g * N;
+        for (int q = tid; q < kFQ * BP; q += 512) {
+            const int r = q / BP;
+            u4 u{0, 0, 0, 0};
+            if (r < nv) u = *reinterpret_cast<const u4any*>(cg + r * a.c_row + 8 * (q % BP));
+            *reinterpret_cast<u4*>(sc + piece<RB>(r, q % BP)) = u;
+        }
+    }
+    f4 acc[TT];
+#pragma unroll
+    for (int j = 0; j < TT; ++j) acc[j] = f4{0, 0, 0, 0};
+    const int64_t sum_step = a.chunks * (kSums * kFQ + kSumTail);
+    float* sums = a.sums + ((b * a.H + hfirst) * a.chunks + c) * (kSums * kFQ + kSumTail) + kSumU * kFQ;
+    auto put_u = [&](int par) __attribute__((always_inline)) {  // of the head before
+        if (tid < kFQ) {
+            float u = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) u += su[par][i][tid];
+            (sums - sum_step)[tid] = u;
+        }
+    };
+    const int xo = along_off<128>(li, g4) + 16 * th0 * 128;
+    const int cw = piece<RB>(li, 2 * nt + (g4 >> 1)) + 8 * (g4 & 1) + 16 * th0 * RB;
+    for (int64_t h = hfirst; h < hend; ++h) {
+        const int par = static_cast<int>(h - hfirst) & 1;
+        bf8 Sp[2][3];
+        float norm = 0.0f;
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                v[e] = rS[2 * kk + (e >> 2)][e & 3];
+                norm += v[e] * v[e];
+            }
+            split(v, Sp[kk]);
+        }
+        norm = group_sum4(lane_sum16(norm));
+        if (lane == 0 && wave < NT) sums[(kSums - kSumU) * kFQ + 64 + nt] = norm;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) *reinterpret_cast<u4*>(sdy[par] + piece<128>(row, tid & 7) + i * 64 * 128) = rdy[i];
+        if (tid < kFQ) sf[par][tid] = rf;
+        // one barrier a head: what is written above was last read two heads ago
+        __syncthreads();
+        if (h > hfirst) put_u(par ^ 1);
+        if (h + 1 < hend) load(h + 1);
+        const uint8_t* dp = sdy[par] + here(xo);
+        const uint8_t* dq = sdy[par] + here(xo ^ 64);
+        const uint8_t* fp = reinterpret_cast<const uint8_t*>(sf[par]) + here(64 * th0 + 4 * li);
+        float* up = su[par][nt] + here(16 * (th0 + group_of_row(g4)) + li);
+        float u[4];
+#pragma unroll
+        for (int jj = 0; jj < TT; ++jj) {
+            const bf8 d0 = lds<bf8>(dp + 16 * jj * 128), d1 = lds<bf8>(dq + 16 * jj * 128);
+            f4 o{0, 0, 0, 0};
+#pragma unroll
+            for (int k = 2; k >= 0; --k) {
+                o = mfma(Sp[0][k], d0, o);
+                o = mfma(Sp[1][k], d1, o);
+            }
+            const float ft = lds<float>(fp + 64 * jj);
+            const u2 cv = lds<u2>(sc + cw + 16 * jj * RB);
+            float w = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                w += __uint_as_float(e & 1 ? cv[e >> 1] & 0xFFFF0000u : cv[e >> 1] << 16) * o[e];
+                acc[jj][e] += ft * o[e];
+            }
+            settle(acc[jj]);
+            u[jj & 3] = w * ft;
+            if ((jj & 3) == 3) up[16 * (jj - 3)] = group_sums(u[0], u[1], u[2], u[3]);
+        }
+        sums += sum_step;
+    }
+    __syncthreads();
+    put_u(static_cast<int>(hend - 1 - hfirst) & 1);
+#pragma unroll
+    for (int jj = 0; jj < TT; ++jj) {
+        const int t = 16 * (th0 + jj) + li;
+        if (t < nv)
+            *reinterpret_cast<f4*>(a.dC_head + (hs * a.B * a.L + tok + t) * a.G * N + g * N + 16 * nt + 4 * g4) = acc[jj];
+    }
+}
+
+// f_last <G, S> of the last chunk of every kAnchor (one block each)
+__global__ void __launch_bounds__(256) sbf_anchor_kernel(ScanBwdArgs a) {
+    __shared__ float sum[4];
+    const int64_t n = (a.chunks + kAnchor - 1) / kAnchor;
+    const int64_t bh = blockIdx.x / n, i = blockIdx.x % n;
+    const int64_t c = (i + 1) * kAnchor < a.chunks ? (i + 1) * kAnchor - 1 : a.chunks - 1;
+    const int64_t at = bh * a.chunks + c, PN = a.P * a.N;
+    const float th = a.through[at];
+    float d = 0.0f;
+    if (th != 0.0f)
+        for (int64_t k = threadIdx.x * 4; k < PN; k += 1024) {
+            const f4 x = *reinterpret_cast<const f4*>(a.states + at * PN + k);
+            const f4 y = *reinterpret_cast<const f4*>(a.grads + at * PN + k);
+            d += (x[0] * y[0] + x[1] * y[1]) + (x[2] * y[2] + x[3] * y[3]);
+        }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) d += __shfl_xor(d, o);
+    if ((threadIdx.x & 63) == 0) sum[threadIdx.x >> 6] = d;
+    __syncthreads();
+    if (threadIdx.x == 0) a.anchor[bh * n + i] = th * ((sum[0] + sum[1]) + (sum[2] + sum[3]));
 }
 
 template <int N>
@@ -431,7 +604,7 @@ __global__ void __launch_bounds__(512) sbf_grad_kernel(ScanBwdArgs a) {
     const uint32_t vdy = static_cast<uint32_t>(row * a.dy_row * 2 + 16 * (tid & 7));
     const uint32_t vs = static_cast<uint32_t>((16 * nt + li) * (kFP * 4) + 32 * g4);
     u4 rx[2], rdy[2];
-    f4 rS[4], rG[4];
+    f4 rG[4];
     float rd[2];
     auto load = [&](int64_t h) __attribute__((always_inline)) {
         const char* xb = reinterpret_cast<const char*>(static_cast<const uint16_t*>(a.x) + tok * a.x_row + h * kFP);
@@ -445,13 +618,9 @@ __global__ void __launch_bounds__(512) sbf_grad_kernel(ScanBwdArgs a) {
             }
         }
         const int64_t at = ((b * a.H + h) * a.chunks + c) * N * kFP;
-        const char* sp = reinterpret_cast<const char*>(a.states + at);
         const char* gp = reinterpret_cast<const char*>(a.grads + at);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            rS[i] = *reinterpret_cast<const f4*>(sp + 128 * (i >> 1) + 16 * (i & 1) + vs);
-            rG[i] = *reinterpret_cast<const f4*>(gp + 128 * (i >> 1) + 16 * (i & 1) + vs);
-        }
+        for (int i = 0; i < 4; ++i) rG[i] = *reinterpret_cast<const f4*>(gp + 128 * (i >> 1) + 16 * (i & 1) + vs);
         const float* rec = a.decay + ((b * a.H + h) * a.chunks + c) * 5 * kFQ;
         rd[0] = rec[tid];
         if (tid < kFQ) rd[1] = rec[4 * kFQ + tid];
@@ -468,7 +637,7 @@ __global__ void __launch_bounds__(512) sbf_grad_kernel(ScanBwdArgs a) {
                 u = *reinterpret_cast<const u4any*>(cg + r * a.c_row + 8 * (q % BP));
             }
             *reinterpret_cast<u4*>(sm + O::B + piece<RB>(r, q % BP)) = v;
-            *reinterpret_cast<u4*>(sm + O::C + piece<RB>(r, q % BP)) = u;
+            *reinterpret_cast<u4*>(sm + O::CB + piece<RB>(r, q % BP)) = u;
         }
         if (tid < kFQ) starts[tid] = a.starts[(b * a.chunks + c) * kFQ + tid];
     }
@@ -477,12 +646,31 @@ __global__ void __launch_bounds__(512) sbf_grad_kernel(ScanBwdArgs a) {
     const int s = 16 * st + li;
     const int rs = starts[s];
 
+    // C B^T of this wavefront's s tile and t tiles st .. 7, then in place of C
+    const int cbt = O::CB + (st * (17 - st) / 2) * 1024 - st * 1024 + 16 * lane;  // tile of t tile j at + 1024 j
+    {
+        f4 cb[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            cb[j] = f4{0, 0, 0, 0};
+            if (j >= st) {
+#pragma unroll
+                for (int kk = 0; kk < N / 32; ++kk)
+                    cb[j] = mfma(lds<bf8>(sm + O::CB + 16 * j * RB + (along_off<RB>(li, g4) ^ (kk << 6))),
+                                 lds<bf8>(sm + O::B + 16 * st * RB + (along_off<RB>(li, g4) ^ (kk << 6))), cb[j]);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j >= st) *reinterpret_cast<f4*>(sm + cbt + 1024 * j) = cb[j];
+    }
     f4 lw[8];  // sums over the heads of L dt (dy x^T), tiles of s tile st
 #pragma unroll
     for (int j = 0; j < 8; ++j) lw[j] = f4{0, 0, 0, 0};
-    f4 accC[TT], accB[TT];
+    f4 accB[TT];
 #pragma unroll
-    for (int j = 0; j < TT; ++j) accC[j] = accB[j] = f4{0, 0, 0, 0};
+    for (int j = 0; j < TT; ++j) accB[j] = f4{0, 0, 0, 0};
 
     const int64_t sum_step = a.chunks * (kSums * kFQ + kSumTail);
     float* sums = a.sums + ((b * a.H + hfirst) * a.chunks + c) * (kSums * kFQ + kSumTail);
@@ -492,30 +680,25 @@ __global__ void __launch_bounds__(512) sbf_grad_kernel(ScanBwdArgs a) {
         int m = any_start;
         asm volatile("" : "+s"(m));  // one copy of the loop, not one for each case
         const bool masked = m != 0;
-        // operands from the loaded states: S in registers, G in LDS (its third part, which dx does
-        // without, in registers)
-        bf8 Sp[2][3], Glo[2];
-        {
-            float dot = 0.0f;
-            bf8 Gp[2][3];
+        // G's parts: two in LDS, the third (which dx does without) in registers
+        bf8 Glo[2];
+        float norm = 0.0f;
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                float v1[8], v2[8];
+        for (int kk = 0; kk < 2; ++kk) {
+            float v[8];
+            bf8 p[3];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    v1[e] = rS[2 * kk + (e >> 2)][e & 3];
-                    v2[e] = rG[2 * kk + (e >> 2)][e & 3];
-                    dot += v1[e] * v2[e];
-                }
-                split(v1, Sp[kk]);
-                split(v2, Gp[kk]);
-                Glo[kk] = Gp[kk][2];
-                rG[2 * kk] = __builtin_bit_cast(f4, Gp[kk][0]);
-                rG[2 * kk + 1] = __builtin_bit_cast(f4, Gp[kk][1]);
+            for (int e = 0; e < 8; ++e) {
+                v[e] = rG[2 * kk + (e >> 2)][e & 3];
+                norm += v[e] * v[e];
             }
-            dot = group_sum4(lane_sum16(dot));
-            if (lane == 0 && wave < NT) *reinterpret_cast<float*>(sm + hb + O::DOT + 4 * nt) = dot;
+            split(v, p);
+            rG[2 * kk] = __builtin_bit_cast(f4, p[0]);
+            rG[2 * kk + 1] = __builtin_bit_cast(f4, p[1]);
+            Glo[kk] = p[2];
         }
+        norm = group_sum4(lane_sum16(norm));
+        if (lane == 0 && wave < NT) sums[kSums * kFQ + 72 + nt] = norm;
         __syncthreads();  // the previous head's x, dy and G have been read
         {
             const int o = here(piece<128>(row, tid & 7));  // rows row and row + 64 share the swizzle
@@ -539,43 +722,15 @@ __global__ void __launch_bounds__(512) sbf_grad_kernel(ScanBwdArgs a) {
         if (h > hfirst) head_sums<N>(sm, O::ROW + (par ^ 1) * O::HEAD, sums - sum_step, tid);
 
         // LDS offsets of this head's reads
-        const int ao = here(along_off<RB>(li, g4));                      // B, C along rows
         const int bst = here(along_off<RB>(li, g4) + 16 * st * RB);      // B, rows of s tile st
         const int xo = here(O::X + along_off<128>(li, g4));              // x, dy along rows
         const int yo = here(O::DY + down_off<128>(4 * g4, li));          // dy down rows
-        const int cw = here(piece<RB>(li, 2 * nt + (g4 >> 1)) + 8 * (g4 & 1));  // C, B elements (n 4 g4 .., t li)
+        const int cw = here(piece<RB>(li, 2 * nt + (g4 >> 1)) + 8 * (g4 & 1));  // B elements (n 4 g4 .., s li)
         const int tl = here(hb + O::DEC + 4 * li);                       // decays of token li of a tile
         const int t4 = here(hb + O::DEC + 16 * g4);                      // decays of tokens 4 g4 ..
-        const int ut = here(hb + O::U + nt * LR + 4 * li);               // u, v of n tile nt
+        const int vt = here(hb + O::V + nt * LR + 64 * group_of_row(g4) + 4 * li);  // v of n tile nt, four s tiles
+        const int ct = here(cbt);                                        // C B^T
         const int rt = here(hb + st * LR + 16 * g4 + 4 * (li & 3));      // row sums
-
-        // ---- dy against S: dC, u ----
-#pragma unroll
-        for (int jj = 0; jj < TT; ++jj) {
-            const int j = th0 + jj;
-            const bf8 d0 = lds<bf8>(sm + xo + (O::DY - O::X) + 16 * j * 128);
-            const bf8 d1 = lds<bf8>(sm + (xo ^ 64) + (O::DY - O::X) + 16 * j * 128);
-            f4 o{0, 0, 0, 0};
-#pragma unroll
-            for (int k = 2; k >= 0; --k) {
-                o = mfma(Sp[0][k], d0, o);
-                o = mfma(Sp[1][k], d1, o);
-            }
-            const float ft = lds<float>(sm + tl + 2 * LR + 64 * j);
-            const u2 cv = lds<u2>(sm + cw + O::C + 16 * j * RB);
-            if (masked) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[e] = ft == 0.0f ? 0.0f : o[e];
-            }
-            float u = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                u += __uint_as_float(e & 1 ? cv[e >> 1] & 0xFFFF0000u : cv[e >> 1] << 16) * o[e];
-                accC[jj][e] += ft * o[e];
-            }
-            u = group_sum4(u) * ft;
-            if (g4 == 0) *reinterpret_cast<float*>(sm + ut + 64 * j) = u;
-        }
 
         // ---- pairs s <= t of s tile st: W's sums, the pairs' part of dx ----
         f4 dxa[4];
@@ -591,10 +746,7 @@ __global__ void __launch_bounds__(512) sbf_grad_kernel(ScanBwdArgs a) {
             if (j >= st) {
                 f4 yx = mfma(lds<bf8>(sm + xo + (O::DY - O::X) + 16 * j * 128), xf0, f4{0, 0, 0, 0});
                 yx = mfma(lds<bf8>(sm + (xo ^ 64) + (O::DY - O::X) + 16 * j * 128), xf1, yx);
-                f4 cb{0, 0, 0, 0};
-#pragma unroll
-                for (int kk = 0; kk < N / 32; ++kk)
-                    cb = mfma(lds<bf8>(sm + (ao ^ (kk << 6)) + O::C + 16 * j * RB), lds<bf8>(sm + (bst ^ (kk << 6))), cb);
+                const f4 cb = lds<f4>(sm + ct + 1024 * j);
                 const f4 ht = lds<f4>(sm + t4 + 64 * j), lt = lds<f4>(sm + t4 + LR + 64 * j);
                 f4 l;
 #pragma unroll
@@ -620,10 +772,10 @@ __global__ void __launch_bounds__(512) sbf_grad_kernel(ScanBwdArgs a) {
                     const float w = pv[e] * yx[e] - dw[e];  // l = 1 on the diagonal: exactly 0 there
                     if (j == st) bdiag += w;
                     else below += w;
-                    rw[e] = lane_sum16(w * dts);
+                    rw[e] = w * dts;
                 }
-                const float r01 = li & 1 ? rw[1] : rw[0], r23 = li & 1 ? rw[3] : rw[2];
-                if (li < 4) *reinterpret_cast<float*>(sm + rt + 64 * j) = li & 2 ? r23 : r01;
+                settle(lw[j]);
+                *reinterpret_cast<float*>(sm + rt + 64 * j) = row_sums(rw, li);  // the same from four lanes
                 // two parts, into this tile's half of the operand
                 const uint32_t q0 = pack_bf16x2(pv[0], pv[1]), q1 = pack_bf16x2(pv[2], pv[3]);
                 pw[0][2 * (j & 1)] = q0;
@@ -643,17 +795,15 @@ __global__ void __launch_bounds__(512) sbf_grad_kernel(ScanBwdArgs a) {
                 }
             }
         }
-        below = group_sum4(below);
-        bdiag = group_sum4(bdiag);
-        diag = group_sum4(diag);
-        if (g4 < 3) {  // kSumColOff, kSumColDiag, kSumDiag
-            const float v = g4 == 0 ? below : g4 == 1 ? bdiag : diag;
-            sums[(kSumColOff + g4) * kFQ + s] = v;
+        {  // rows of lanes 0, 1, 2: kSumColOff, kSumColDiag, kSumDiag
+            const float v = group_sums(below, diag, bdiag, 0.0f);
+            if (g4 < 3) sums[(kSumColOff + g4) * kFQ + s] = v;
         }
         sums += sum_step;
         if (h + 1 < hend) load(h + 1);
 
         // ---- x against G: dB, v ----
+        float v[4];
         bf8 Gp[2][3];
         {
             const int q = here(O::G + 16 * nt * 128 + along_off<128>(li, g4));
@@ -676,18 +826,15 @@ __global__ void __launch_bounds__(512) sbf_grad_kernel(ScanBwdArgs a) {
             }
             const float es = lds<float>(sm + tl + 3 * LR + 64 * j), ed = es * lds<float>(sm + tl + 4 * LR + 64 * j);
             const u2 bv = lds<u2>(sm + cw + O::B + 16 * j * RB);
-            if (masked) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[e] = es == 0.0f ? 0.0f : o[e];
-            }
-            float v = 0.0f;
+            float w = 0.0f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                v += __uint_as_float(e & 1 ? bv[e >> 1] & 0xFFFF0000u : bv[e >> 1] << 16) * o[e];
+                w += __uint_as_float(e & 1 ? bv[e >> 1] & 0xFFFF0000u : bv[e >> 1] << 16) * o[e];
                 accB[jj][e] += ed * o[e];
             }
-            v = group_sum4(v) * es;
-            if (g4 == 0) *reinterpret_cast<float*>(sm + ut + (O::V - O::U) + 64 * j) = v;
+            settle(accB[jj]);
+            v[jj & 3] = w * es;
+            if ((jj & 3) == 3) *reinterpret_cast<float*>(sm + vt + 64 * (j - 3)) = group_sums(v[0], v[1], v[2], v[3]);
         }
 
         // ---- dx: G B, then with the pairs ----
@@ -714,7 +861,7 @@ __global__ void __launch_bounds__(512) sbf_grad_kernel(ScanBwdArgs a) {
             for (int p = 0; p < 4; ++p) {
                 f4 r;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) r[e] = dts * (dxa[p][e] + (es == 0.0f ? 0.0f : es * gb[p][e]));
+                for (int e = 0; e < 4; ++e) r[e] = dts * (dxa[p][e] + es * gb[p][e]);
                 *reinterpret_cast<u2any*>(dxo + vdx + 32 * p) = u2{pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3])};
             }
         }
@@ -722,7 +869,7 @@ __global__ void __launch_bounds__(512) sbf_grad_kernel(ScanBwdArgs a) {
     __syncthreads();
     head_sums<N>(sm, O::ROW + (static_cast<int>(hend - 1 - hfirst) & 1) * O::HEAD, sums - sum_step, tid);
 
-    // ---- the heads' summed pairs: two parts of [t][s] in LDS (zero above the diagonal) ----
+    // ---- the heads' summed pairs: two parts of [t][s] in LDS (zero above the diagonal); C again ----
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -734,6 +881,15 @@ __global__ void __launch_bounds__(512) sbf_grad_kernel(ScanBwdArgs a) {
             *reinterpret_cast<uint16_t*>(sm + O::LW + o) = hi;
             *reinterpret_cast<uint16_t*>(sm + O::LW + kFQ * 256 + o) = lo;
         }
+    {
+        const uint16_t* cg = static_cast<const uint16_t*>(a.C) + tok * a.c_row + g * N;
+        for (int q = tid; q < kFQ * BP; q += 512) {
+            const int r = q / BP;
+            u4 u{0, 0, 0, 0};
+            if (r < nv) u = *reinterpret_cast<const u4any*>(cg + r * a.c_row + 8 * (q % BP));
+            *reinterpret_cast<u4*>(sm + O::CB + piece<RB>(r, q % BP)) = u;
+        }
+    }
     __syncthreads();
     const int bo = down_off<RB>(4 * g4, li) ^ (nt << 5);       // C^T: rows of n tile nt
     const int b0 = down_off<RB>(8 * g4, li) ^ (nt << 5), b1 = down_off<RB>(8 * g4 + 4, li) ^ (nt << 5);  // B^T
@@ -741,32 +897,35 @@ __global__ void __launch_bounds__(512) sbf_grad_kernel(ScanBwdArgs a) {
 #pragma unroll
     for (int jj = 0; jj < TT; ++jj) {
         const int j = th0 + jj;
+        const int t = 16 * j + li;
+        const int64_t col = g * N + 16 * nt + 4 * g4, slab = a.B * a.L * a.G * N;
+        const int64_t at = (tok + t) * a.G * N + col;
+        f4 accC{0, 0, 0, 0};
+        if (a.splits == 1 && t < nv)  // sbf_dc's part
+            for (int64_t i = 0; i < a.dc_splits; ++i) accC += *reinterpret_cast<const f4*>(a.dC_head + i * slab + at);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             if (2 * k <= j) {  // dC of t tile j: s tiles 2 k, 2 k + 1
                 const uint8_t* p = sm + O::B + 32 * k * RB;
                 const bf8 f = join(tr_read(p + b0), tr_read(p + b1));
-                accC[jj] = mfma(f, along<256>(sm + O::LW + kFQ * 256, lo_, 16 * j, k), accC[jj]);
-                accC[jj] = mfma(f, along<256>(sm + O::LW, lo_, 16 * j, k), accC[jj]);
+                accC = mfma(f, along<256>(sm + O::LW + kFQ * 256, lo_, 16 * j, k), accC);
+                accC = mfma(f, along<256>(sm + O::LW, lo_, 16 * j, k), accC);
             }
             if (2 * k + 1 >= j) {  // dB of s tile j: t tiles 2 k, 2 k + 1
-                const bf8 f = down<RB>(sm + O::C, bo, 32 * k, 0);
+                const bf8 f = down<RB>(sm + O::CB, bo, 32 * k, 0);
                 accB[jj] = mfma(f, down<256>(sm + O::LW + kFQ * 256, ld, 32 * k, j), accB[jj]);
                 accB[jj] = mfma(f, down<256>(sm + O::LW, ld, 32 * k, j), accB[jj]);
             }
         }
-        const int t = 16 * j + li;
         if (t < nv) {
-            const int64_t col = g * N + 16 * nt + 4 * g4;
             if (a.splits == 1) {
                 *reinterpret_cast<u2any*>(static_cast<uint16_t*>(a.dC) + (tok + t) * a.dc_row + col) =
-                    u2{pack_bf16x2(accC[jj][0], accC[jj][1]), pack_bf16x2(accC[jj][2], accC[jj][3])};
+                    u2{pack_bf16x2(accC[0], accC[1]), pack_bf16x2(accC[2], accC[3])};
                 *reinterpret_cast<u2any*>(static_cast<uint16_t*>(a.dB) + (tok + t) * a.db_row + col) =
                     u2{pack_bf16x2(accB[jj][0], accB[jj][1]), pack_bf16x2(accB[jj][2], accB[jj][3])};
             } else {
-                const int64_t at = (hs * a.B * a.L + tok + t) * a.G * N + col;
-                *reinterpret_cast<f4*>(a.dC_head + at) = accC[jj];
-                *reinterpret_cast<f4*>(a.dB_head + at) = accB[jj];
+                *reinterpret_cast<f4*>(a.dC_head + (a.dc_splits + hs) * slab + at) = accC;
+                *reinterpret_cast<f4*>(a.dB_head + hs * slab + at) = accB[jj];
             }
         }
     }
@@ -779,7 +938,8 @@ __global__ void __launch_bounds__(256) sbf_join_kernel(ScanBwdArgs a) {
     if (i >= n) return;
     const float* p = (blockIdx.y ? a.dC_head : a.dB_head) + i;
     f4 s = *reinterpret_cast<const f4*>(p);
-    for (int64_t j = 1; j < a.splits; ++j) s += *reinterpret_cast<const f4*>(p + j * n);
+    const int64_t slabs = a.splits + (blockIdx.y ? a.dc_splits : 0);
+    for (int64_t j = 1; j < slabs; ++j) s += *reinterpret_cast<const f4*>(p + j * n);
     uint16_t* o = blockIdx.y ? static_cast<uint16_t*>(a.dC) + i / GN * a.dc_row
                              : static_cast<uint16_t*>(a.dB) + i / GN * a.db_row;
     *reinterpret_cast<u2any*>(o + i % GN) = u2{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
@@ -803,6 +963,10 @@ void cut_heads(ScanBwdArgs& a) {
             a.split_heads = heads;
         }
     }
+    // sbf_dc: two blocks run on a unit
+    const int64_t n = blocks >= 512 ? 1 : (512 + blocks - 1) / blocks < k ? (512 + blocks - 1) / blocks : k;
+    a.dc_heads = (k + n - 1) / n;
+    a.dc_splits = (k + a.dc_heads - 1) / a.dc_heads;
 }
 
 size_t lay_out(ScanBwdArgs& a, uint8_t* base) {
@@ -819,9 +983,10 @@ size_t lay_out(ScanBwdArgs& a, uint8_t* base) {
     part(a.sums, bhc * (kSums * kFQ + kSumTail));
     part(a.states, bhc * a.P * a.N);
     part(a.grads, bhc * a.P * a.N);
-    const size_t heads = a.splits > 1 ? static_cast<size_t>(a.splits * a.B * a.L * a.G * a.N) : 0;
-    part(a.dB_head, heads);
-    part(a.dC_head, heads);
+    part(a.anchor, static_cast<size_t>(a.B * a.H * ((a.chunks + kAnchor - 1) / kAnchor)));
+    const size_t slab = static_cast<size_t>(a.B * a.L * a.G * a.N), slabs = a.splits > 1 ? a.splits : 0;
+    part(a.dB_head, slabs * slab);
+    part(a.dC_head, (slabs + a.dc_splits) * slab);
     return at;
 }
 
@@ -840,6 +1005,8 @@ hipError_t launch_typed(const ScanBwdArgs& a, hipStream_t s) {
         sbf_states_kernel<N, false><<<dim3(static_cast<uint32_t>(bh * a.chunks), 2), 256, 0, s>>>(a);
         sbf_pass_kernel<<<dim3(static_cast<uint32_t>(bh * (kFP * N / 256)), 2), 256, 0, s>>>(a);
     }
+    sbf_anchor_kernel<<<static_cast<uint32_t>(bh * ((a.chunks + kAnchor - 1) / kAnchor)), 256, 0, s>>>(a);
+    sbf_dc_kernel<N><<<static_cast<uint32_t>(a.B * a.chunks * a.G * a.dc_splits), 512, 0, s>>>(a);
     sbf_grad_kernel<N><<<static_cast<uint32_t>(a.B * a.chunks * a.G * a.splits), 512, 0, s>>>(a);
     if (a.splits > 1)
         sbf_join_kernel<<<dim3(static_cast<uint32_t>((a.B * a.L * a.G * N / 4 + 255) / 256), 2), 256, 0, s>>>(a);
