@@ -77,11 +77,17 @@ __device__ __forceinline__ void split(const float (&v)[8], bf8 (&part)[PARTS]) {
 }
 
 // LDS tiles of bf16: rows of RB bytes in 16-byte pieces, the piece index XORed with sw(row), so
-// that 8 rows' equal pieces (operand reads along rows) and 4 rows' neighbouring pairs of pieces
-// (transposing reads) fall into different banks.
-__device__ __forceinline__ int sw(int row) { return ((row & 3) << 1) | ((row >> 2) & 1); }
+// that over the 64 banks (256 bytes) fall apart: the equal pieces of 16 rows (operand reads along
+// rows), and the neighbouring pairs of pieces of the 8 rows that two 16-lane groups of a
+// transposing read take (0-7 and 8-15 in token order, 0-3 with 8-11 and 4-7 with 12-15 else).
 template <int RB>
-__device__ __forceinline__ int piece(int row, int q) { return row * RB + ((q ^ sw(row)) << 4); }
+__device__ __forceinline__ int sw(int row) {
+    const int b0 = row & 1, b1 = (row >> 1) & 1, b2 = (row >> 2) & 1, b3 = (row >> 3) & 1;
+    if (RB == 128) return b1 << 2 | (b2 ^ b3) << 1 | b3;  // neighbouring rows lie 128 bytes apart
+    return b0 << 3 | b1 << 2 | (b2 ^ b3) << 1 | b3;
+}
+template <int RB>
+__device__ __forceinline__ int piece(int row, int q) { return row * RB + ((q ^ sw<RB>(row)) << 4); }
 
 template <class T>
 __device__ __forceinline__ T lds(const uint8_t* p) { return *reinterpret_cast<const T*>(p); }
