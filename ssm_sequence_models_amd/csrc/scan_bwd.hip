@@ -372,30 +372,30 @@ __device__ __forceinline__ double before_lane(double v, int lane) {
     return v - own;
 }
 
-// q, ddt and a chunk's share of dA: one wavefront a head and (64-token chunks) chunk, or (128)
-// kAnchor chunks from the last of them back, Q / 64 tokens a lane; a block takes 16 heads of one
-// row and chunk (its stores of ddt are 64-byte runs).
+// q, ddt and a chunk's share of dA: one wavefront a head and chunk, Q / 64 tokens a lane; a block
+// takes kAnchor chunks of two heads (the chunks that share an f <G, S>).  Blocks of one row and
+// chunk range follow each other at the distance of all ranges: on one XCD where that is a
+// multiple of 8, so that their stores of ddt meet in its L2.
 template <int Q>
-__global__ void __launch_bounds__(1024) sb_ddt_kernel(ScanBwdArgs a) {
-    constexpr int K = Q / 64, PER = Q == 64 ? 1 : kAnchor;
-    const int64_t hb = (a.H + 15) / 16, groups = (a.chunks + PER - 1) / PER;
-    const int64_t h = blockIdx.x % hb * 16 + (threadIdx.x >> 6), group = blockIdx.x / hb % groups;
-    const int64_t b = blockIdx.x / hb / groups;
-    if (h >= a.H) return;
-    const int lane = threadIdx.x & 63;
-    const double A = a.A[h];
-    const int64_t last = (group + 1) * PER < a.chunks ? (group + 1) * PER - 1 : a.chunks - 1;
-    double pass = 0.0, after_u = 0.0;  // f_last <G, S> and sum of u of the chunk behind
-    for (int64_t c = last; c >= group * PER; --c) {
-        const int64_t at = (b * a.H + h) * a.chunks + c, t0 = c * Q;
-        const float* in = a.sums + at * (kSums * Q + kSumTail);
-        const float th = a.through[at];
-        double q[K], u[K], v[K];
-        float direct[K], dts[K];
+__global__ void __launch_bounds__(128 * kAnchor) sb_ddt_kernel(ScanBwdArgs a) {
+    constexpr int K = Q / 64;
+    __shared__ double usum[2][kAnchor], vsum[2][kAnchor];
+    const int64_t ranges = (a.chunks + kAnchor - 1) / kAnchor, br = a.B * ranges;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, hw = wave / kAnchor, ci = wave % kAnchor;
+    const int64_t h = blockIdx.x / br * 2 + hw, b = blockIdx.x % br / ranges, range = blockIdx.x % ranges;
+    const int64_t c = range * kAnchor + ci, t0 = c * Q;
+    const int64_t last = (range + 1) * kAnchor < a.chunks ? (range + 1) * kAnchor - 1 : a.chunks - 1;
+    const bool on = h < a.H && c < a.chunks;
+    const int64_t at = on ? (b * a.H + h) * a.chunks + c : 0;
+    const float* in = a.sums + at * (kSums * Q + kSumTail);
+    double q[K], after = 0.0, before = 0.0;
+    float direct[K], dts[K];
+    if (on) {
+        double u[K], v[K];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int t = lane + 64 * k, j = t >> 4;
-            dts[k] = t0 + t < a.L ? a.dt[(b * a.L + t0 + t) * a.H + h] : 0.0f;
+            dts[k] = t0 + t < a.L ? (Q == 128 ? a.decay[(at * 5 + 4) * Q + t] : a.dt[(b * a.L + t0 + t) * a.H + h]) : 0.0f;
             const float coff = in[kSumColOff * Q + t], cdiag = in[kSumColDiag * Q + t], vt = in[kSumV * Q + t];
             direct[k] = ((coff + cdiag) + in[kSumDiag * Q + t]) + vt;
             u[k] = in[kSumU * Q + t];
@@ -405,50 +405,65 @@ __global__ void __launch_bounds__(1024) sb_ddt_kernel(ScanBwdArgs a) {
             for (int j2 = j + 1; j2 < Q / 16; ++j2)
                 for (int i = 0; i < j; ++i) q[k] += in[kSums * Q + 8 * j2 + i];
         }
-        double after = 0.0;
 #pragma unroll
         for (int k = K - 1; k >= 0; --k) {
             const double s = from_lane<64>(u[k], lane);
             q[k] += s + after;
             after += __shfl(s, 0);
         }
-        double before = 0.0;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const double s = before_lane<64>(v[k], lane);
             q[k] += s + before;
             before += __shfl(s + v[k], 63);
         }
-        // what passes through the whole chunk (nothing across a start or a decay to 0)
-        if (th == 0.0f) pass = 0.0;
-        else if (Q == 64) pass = static_cast<double>(th) * in[kSums * Q + 64];
-        else if (c == last) pass = a.anchor[(b * a.H + h) * groups + group];
-        else {
+        if (lane == 0) {
+            usum[hw][ci] = after;
+            vsum[hw][ci] = before;
+        }
+    }
+    __syncthreads();
+    if (!on) return;
+    // f_last <G, S> of this chunk: from the range's last chunk back (nothing across a start or a
+    // decay to 0)
+    double pass = 0.0;
+    for (int64_t d = Q == 64 ? c : last; d >= c; --d) {
+        const int64_t da = at + d - c;
+        const float th = a.through[da];
+        const float* tail = a.sums + da * (kSums * Q + kSumTail) + kSums * Q;
+        if (th == 0.0f) {
+            pass = 0.0;
+        } else if (Q == 64) {
+            pass = static_cast<double>(th) * tail[64];
+        } else if (d == last) {
+            pass = a.anchor[(b * a.H + h) * ranges + range];
+        } else {
             float ns = 0.0f, ng = 0.0f;
             for (int i = 0; i < a.N / 16; ++i) {
-                ns += in[kSums * Q + 64 + i];
-                ng += in[kSums * Q + 72 + i];
+                ns += tail[64 + i];
+                ng += tail[72 + i];
             }
             const double most = 1.00001 * th * sqrt(static_cast<double>(ns)) * sqrt(static_cast<double>(ng));
-            pass += after_u - before;
+            const int64_t k = d - range * kAnchor;
+            pass += usum[hw][k + 1] - vsum[hw][k];
             if (pass > most) pass = most;
             if (pass < -most) pass = -most;
         }
-        after_u = after;
-        double da = 0.0;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int64_t t = t0 + lane + 64 * k;
-            if (t >= a.L) continue;
-            q[k] += pass;
-            if (a.seq && t > 0 && a.seq[b * a.L + t] != a.seq[b * a.L + t - 1]) q[k] = 0.0;  // a start takes nothing over
-            a.ddt[(b * a.L + t) * a.H + h] = static_cast<float>(q[k] * A + direct[k]);
-            da += q[k] * dts[k];
-        }
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) da += __shfl_xor(da, o);
-        if (lane == 0) a.dA_part[(b * a.chunks + c) * a.H + h] = da;
     }
+    const double A = a.A[h];
+    double da = 0.0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int64_t t = t0 + lane + 64 * k;
+        if (t >= a.L) continue;
+        q[k] += pass;
+        if (a.seq && t > 0 && a.seq[b * a.L + t] != a.seq[b * a.L + t - 1]) q[k] = 0.0;  // a start takes nothing over
+        a.ddt[(b * a.L + t) * a.H + h] = static_cast<float>(q[k] * A + direct[k]);
+        da += q[k] * dts[k];
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) da += __shfl_xor(da, o);
+    if (lane == 0) a.dA_part[(b * a.chunks + c) * a.H + h] = da;
 }
 
 // dB, dC: the heads of a group added in order, rounded once
@@ -513,8 +528,7 @@ size_t lay_out(ScanBwdArgs& a, uint8_t* base) {
 }  // namespace
 
 hipError_t launch_scan_bwd_ddt(const ScanBwdArgs& a, int tokens, hipStream_t s) {
-    const int64_t groups = tokens == 128 ? (a.chunks + kAnchor - 1) / kAnchor : a.chunks;
-    const uint32_t grid = static_cast<uint32_t>(a.B * groups * ((a.H + 15) / 16));
+    const uint32_t grid = static_cast<uint32_t>(a.B * ((a.chunks + kAnchor - 1) / kAnchor) * ((a.H + 1) / 2));
     if (tokens == 128) sb_ddt_kernel<128><<<grid, 1024, 0, s>>>(a);
     else sb_ddt_kernel<64><<<grid, 1024, 0, s>>>(a);
     sb_dA_kernel<<<static_cast<uint32_t>(a.H), 256, 0, s>>>(a);

@@ -246,39 +246,46 @@ __global__ void __launch_bounds__(256) sbf_decay_kernel(ScanBwdArgs a) {
 // states before the chunks (forward) and gradients after them (reverse)
 // ---------------------------------------------------------------------------------------
 // Block: row, head, direction; wavefront w holds channels 16 w .. of the state as result tiles
-// [p][n].  Stored [n][p]: four channels a lane, and the order sbf_grad's operands have.
+// [p][n].  Stored as the tiles lie, [n tile][p tile][lane][4]: a store is 1024 consecutive bytes, and
+// the gradient kernels' operands (a state dimension, eight channels) are two 16-byte pieces of it.
 // SEQ: the chunks in turn; else one chunk's own share.
 template <int N, bool SEQ>
-__global__ void __launch_bounds__(256) sbf_states_kernel(ScanBwdArgs a) {
-    constexpr int NT = N / 16, RB = 2 * N, BP = N / 8;  // n tiles, row bytes and pieces of B
-    constexpr int BL = kFQ * BP / 256, XL = kFQ * 8 / 256;
+__global__ void __launch_bounds__(256, 2) sbf_states_kernel(ScanBwdArgs a) {
+    constexpr int TH = 256, NT = N / 16, RB = 2 * N, BP = N / 8;  // n tiles, row bytes and pieces of B
+    constexpr int BL = kFQ * BP / TH, XL = kFQ * 8 / TH, XR = TH / 8, BR = TH / BP;  // loads a thread, rows apart
     __shared__ __attribute__((aligned(16))) uint8_t sb[kFQ * RB];
     __shared__ __attribute__((aligned(16))) uint8_t sx[kFQ * 128];
     __shared__ __attribute__((aligned(16))) float scale[kFQ];
     const bool rev = blockIdx.y != 0;
     const int64_t per = SEQ ? 1 : a.chunks;
     const int64_t bh = blockIdx.x / per, b = bh / a.H, h = bh % a.H, g = h / (a.H / a.G);
-    const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g4 = lane >> 4, w = tid >> 6;
-    const uint16_t* xs = static_cast<const uint16_t*>(rev ? a.dy : a.x) + b * a.L * (rev ? a.dy_row : a.x_row) + h * kFP;
-    const uint16_t* bs = static_cast<const uint16_t*>(rev ? a.C : a.Bm) + b * a.L * (rev ? a.c_row : a.b_row) + g * N;
+    const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g4 = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t x_row = rev ? a.dy_row : a.x_row, b_row = rev ? a.c_row : a.b_row;
+    const uint16_t* xs = static_cast<const uint16_t*>(rev ? a.dy : a.x) + b * a.L * x_row + h * kFP;
+    const uint16_t* bs = static_cast<const uint16_t*>(rev ? a.C : a.Bm) + b * a.L * b_row + g * N;
     float* out = (rev ? a.grads : a.states) + bh * a.chunks * N * kFP;
+    // lane offsets of the loads and of the stores, the same for every chunk
+    const uint32_t vx = static_cast<uint32_t>((tid >> 3) * x_row * 2 + 16 * (tid & 7));
+    const uint32_t vb = static_cast<uint32_t>((tid / BP) * b_row * 2 + 16 * (tid % BP));
+    const uint32_t vo = static_cast<uint32_t>(w * 1024 + lane * 16);
 
     u4 rb[BL], rx[XL];
     float rs = 0.0f;
     auto load = [&](int64_t c) __attribute__((always_inline)) {
         const int64_t t0 = c * kFQ;
+        const int nv = a.L - t0 < kFQ ? static_cast<int>(a.L - t0) : kFQ;
+        const char* xp = reinterpret_cast<const char*>(xs + t0 * x_row);
+        const char* bp = reinterpret_cast<const char*>(bs + t0 * b_row);
 #pragma unroll
         for (int i = 0; i < XL; ++i) {
-            const int q = tid + 256 * i, row = q >> 3;
             rx[i] = u4{0, 0, 0, 0};
-            if (t0 + row < a.L) rx[i] = *reinterpret_cast<const u4any*>(xs + (t0 + row) * x_row + 8 * (q & 7));
+            if ((tid >> 3) + XR * i < nv) rx[i] = *reinterpret_cast<const u4any*>(xp + i * (2 * XR) * x_row + vx);
         }
 #pragma unroll
         for (int i = 0; i < BL; ++i) {
-            const int q = tid + 256 * i, row = q / BP;
             rb[i] = u4{0, 0, 0, 0};
-            if (t0 + row < a.L) rb[i] = *reinterpret_cast<const u4any*>(bs + (t0 + row) * b_row + 8 * (q % BP));
+            if (tid / BP + BR * i < nv) rb[i] = *reinterpret_cast<const u4any*>(bp + i * (2 * BR) * b_row + vb);
         }
         if (tid < kFQ) {
             const float* rec = a.decay + (bh * a.chunks + c) * 5 * kFQ + tid;
@@ -295,38 +302,44 @@ __global__ void __launch_bounds__(256) sbf_states_kernel(ScanBwdArgs a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             acc[n][e] = from ? from[(bh * kFP + 16 * w + 4 * g4 + e) * N + 16 * n + li] : 0.0f;
+    auto store = [&](int64_t c) __attribute__((always_inline)) {
+        char* o = reinterpret_cast<char*>(out + c * N * kFP);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            __builtin_nontemporal_store(acc[n], reinterpret_cast<f4*>(o + vo + n * 4096));
+    };
     const int xo = down_off<128>(4 * g4, li) ^ (w << 5), bo = down_off<RB>(4 * g4, li);
     for (int64_t i = 0; i < steps; ++i) {
         const int64_t c = c0 + i * dc;
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < XL; ++j) {
-            const int q = tid + 256 * j;
-            *reinterpret_cast<u4*>(sx + piece<128>(q >> 3, q & 7)) = rx[j];
-        }
+        for (int j = 0; j < XL; ++j)
+            *reinterpret_cast<u4*>(sx + piece<128>(tid >> 3, tid & 7) + j * XR * 128) = rx[j];
 #pragma unroll
-        for (int j = 0; j < BL; ++j) {
-            const int q = tid + 256 * j;
-            *reinterpret_cast<u4*>(sb + piece<RB>(q / BP, q % BP)) = rb[j];
-        }
+        for (int j = 0; j < BL; ++j)
+            *reinterpret_cast<u4*>(sb + piece<RB>(tid / BP, tid % BP) + j * BR * RB) = rb[j];
         if (tid < kFQ) scale[tid] = rs;
         __syncthreads();
         if (i + 1 < steps) load(c + dc);
         if (SEQ) {
-            float* o = out + c * N * kFP + 16 * w + 4 * g4;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) *reinterpret_cast<f4*>(o + (16 * n + li) * kFP) = acc[n];
+            store(c);
             const float th = a.through[bh * a.chunks + c];
+            if (th == 0.0f) {  // nothing passes a start, whatever the state was
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n) acc[n] = f4{0, 0, 0, 0};
+            } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[n][e] = th == 0.0f ? 0.0f : acc[n][e] * th;
+                for (int n = 0; n < NT; ++n) acc[n] *= th;
+            }
         }
 #pragma unroll
         for (int k = 0; k < kFQ / 32; ++k) {
             const u4 raw = __builtin_bit_cast(u4, down<128>(sx, xo, 32 * k, 0));
             const f4 s0 = *reinterpret_cast<const f4*>(scale + 32 * k + 4 * g4);
             const f4 s1 = *reinterpret_cast<const f4*>(scale + 32 * k + 16 + 4 * g4);
+            bf8 q[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) q[n] = down<RB>(sb, bo, 32 * k, n);
             float v[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -336,17 +349,11 @@ __global__ void __launch_bounds__(256) sbf_states_kernel(ScanBwdArgs a) {
             bf8 p[3];
             split(v, p);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const bf8 q = down<RB>(sb, bo, 32 * k, n);
+            for (int j = 2; j >= 0; --j)
 #pragma unroll
-                for (int j = 2; j >= 0; --j) acc[n] = mfma(p[j], q, acc[n]);
-            }
+                for (int n = 0; n < NT; ++n) acc[n] = mfma(p[j], q[n], acc[n]);
         }
-        if (!SEQ) {
-            float* o = out + c * N * kFP + 16 * w + 4 * g4;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) *reinterpret_cast<f4*>(o + (16 * n + li) * kFP) = acc[n];
-        }
+        if (!SEQ) store(c);
     }
     if (SEQ && rev && a.dh0) {
 #pragma unroll
@@ -356,11 +363,11 @@ __global__ void __launch_bounds__(256) sbf_states_kernel(ScanBwdArgs a) {
     }
 }
 
-// The chunks' shares summed along the row, in place (states stored [n][p], the caller's [p][n])
+// The chunks' shares summed along the row, in place (states stored as tiles, the caller's [p][n])
 __global__ void __launch_bounds__(256) sbf_pass_kernel(ScanBwdArgs a) {
     const int64_t PN = kFP * a.N, per = PN / 256;
     const int64_t bh = blockIdx.x / per, i = blockIdx.x % per * 256 + threadIdx.x;
-    const int64_t j = (i % kFP) * a.N + i / kFP;
+    const int64_t j = (16 * (i / 256 % 4) + 4 * (i / 64 % 4) + i % 4) * a.N + 16 * (i / 1024) + i / 4 % 16;
     const bool rev = blockIdx.y != 0;
     float* s = (rev ? a.grads : a.states) + bh * a.chunks * PN + i;
     const float* f = a.through + bh * a.chunks;
@@ -458,7 +465,7 @@ __global__ void __launch_bounds__(512, 4) sbf_dc_kernel(ScanBwdArgs a) {
     const int nt = wave % NT, th0 = NT == 8 ? 0 : (wave / NT) * TT;
     const int row = tid >> 3;
     const uint32_t vdy = static_cast<uint32_t>(row * a.dy_row * 2 + 16 * (tid & 7));
-    const uint32_t vs = static_cast<uint32_t>((16 * nt + li) * (kFP * 4) + 32 * g4);
+    const uint32_t vs = static_cast<uint32_t>(nt * 4096 + (g4 >> 1) * 1024 + (g4 & 1) * 512 + li * 16);
     u4 rdy[2];
     f4 rS[4];
     float rf = 0.0f;
@@ -471,7 +478,7 @@ __global__ void __launch_bounds__(512, 4) sbf_dc_kernel(ScanBwdArgs a) {
         }
         const char* sp = reinterpret_cast<const char*>(a.states + ((b * a.H + h) * a.chunks + c) * N * kFP);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) rS[i] = *reinterpret_cast<const f4*>(sp + 128 * (i >> 1) + 16 * (i & 1) + vs);
+        for (int i = 0; i < 4; ++i) rS[i] = __builtin_nontemporal_load(reinterpret_cast<const f4*>(sp + 2048 * (i >> 1) + 256 * (i & 1) + vs));
         if (tid < kFQ) rf = a.decay[(((b * a.H + h) * a.chunks + c) * 5 + 2) * kFQ + tid];
     };
     load(hfirst);
@@ -608,7 +615,7 @@ __global__ void __launch_bounds__(512) sbf_grad_kernel(ScanBwdArgs a) {
     const int row = tid >> 3;  // and row + 64
     const uint32_t vx = static_cast<uint32_t>(row * a.x_row * 2 + 16 * (tid & 7));
     const uint32_t vdy = static_cast<uint32_t>(row * a.dy_row * 2 + 16 * (tid & 7));
-    const uint32_t vs = static_cast<uint32_t>((16 * nt + li) * (kFP * 4) + 32 * g4);
+    const uint32_t vs = static_cast<uint32_t>(nt * 4096 + (g4 >> 1) * 1024 + (g4 & 1) * 512 + li * 16);
     u4 rx[2], rdy[2];
     f4 rG[4];
     float rd[2];
@@ -626,7 +633,7 @@ __global__ void __launch_bounds__(512) sbf_grad_kernel(ScanBwdArgs a) {
         const int64_t at = ((b * a.H + h) * a.chunks + c) * N * kFP;
         const char* gp = reinterpret_cast<const char*>(a.grads + at);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) rG[i] = *reinterpret_cast<const f4*>(gp + 128 * (i >> 1) + 16 * (i & 1) + vs);
+        for (int i = 0; i < 4; ++i) rG[i] = __builtin_nontemporal_load(reinterpret_cast<const f4*>(gp + 2048 * (i >> 1) + 256 * (i & 1) + vs));
         const float* rec = a.decay + ((b * a.H + h) * a.chunks + c) * 5 * kFQ;
         rd[0] = rec[tid];
         if (tid < kFQ) rd[1] = rec[4 * kFQ + tid];
