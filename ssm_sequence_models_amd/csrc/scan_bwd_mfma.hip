@@ -35,6 +35,8 @@
 // k running 4 g4 + e over one 16-row tile and 16 + 4 g4 + e over the next ("token order"
 // below); the transposing LDS read (4 rows of 16 columns a 16-lane group) gives the other
 // operand in the same order.  So pairs never pass through LDS.
+#include <type_traits>
+
 #include "internal.h"
 
 namespace ssm {
@@ -678,9 +680,9 @@ __global__ void __launch_bounds__(512) sbf_grad_kernel(ScanBwdArgs a) {
         for (int j = 0; j < 8; ++j)
             if (j >= st) *reinterpret_cast<f4*>(sm + cbt + 1024 * j) = cb[j];
     }
-    f4 lw[8];  // sums over the heads of L dt (dy x^T), tiles of s tile st
-#pragma unroll
-    for (int j = 0; j < 8; ++j) lw[j] = f4{0, 0, 0, 0};
+    // sums over the heads of L dt (dy x^T) with s tile st: the two t tiles that hold the diagonal,
+    // and tiles 2 m, 2 m + 1 behind them
+    f4 lwd[2] = {}, lw[3][2] = {};
     f4 accB[TT];
 #pragma unroll
     for (int j = 0; j < TT; ++j) accB[j] = f4{0, 0, 0, 0};
@@ -753,61 +755,79 @@ __global__ void __launch_bounds__(512) sbf_grad_kernel(ScanBwdArgs a) {
         const float hi_s = lds<float>(sm + tl + 64 * st), lo_s = lds<float>(sm + tl + LR + 64 * st);
         const float dts = lds<float>(sm + tl + 4 * LR + 64 * st);
         float below = 0.0f, bdiag = 0.0f, diag = 0.0f;  // column sums of W / dt_s
-        u4 pw[2];  // two parts of the pairs of two t tiles, in token order
+        // two t tiles at a time (one operand of dx), from token r0; FIRST: the two that hold the
+        // diagonal (where st is odd, the first of them lies above it and gives nothing)
+        auto step = [&](int r0, f4 (&sum)[2], auto first) __attribute__((always_inline)) {
+            constexpr bool FIRST = decltype(first)::value;
+            const uint8_t* dp = sm + xo + (O::DY - O::X) + r0 * 128;
+            const uint8_t* dq = sm + (xo ^ 64) + (O::DY - O::X) + r0 * 128;
+            f4 yx[2], cb[2], l[2];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (j >= st) {
-                f4 yx = mfma(lds<bf8>(sm + xo + (O::DY - O::X) + 16 * j * 128), xf0, f4{0, 0, 0, 0});
-                yx = mfma(lds<bf8>(sm + (xo ^ 64) + (O::DY - O::X) + 16 * j * 128), xf1, yx);
-                const f4 cb = lds<f4>(sm + ct + 1024 * j);
-                const f4 ht = lds<f4>(sm + t4 + 64 * j), lt = lds<f4>(sm + t4 + LR + 64 * j);
-                f4 l;
+            for (int i = 0; i < 2; ++i) {
+                yx[i] = mfma(lds<bf8>(dp + i * 2048), xf0, f4{0, 0, 0, 0});
+                cb[i] = lds<f4>(sm + ct + 64 * r0 + 1024 * i);
+                const f4 ht = lds<f4>(sm + t4 + 4 * r0 + 64 * i), lt = lds<f4>(sm + t4 + LR + 4 * r0 + 64 * i);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) l[e] = __builtin_amdgcn_exp2f((ht[e] - hi_s) + (lt[e] - lo_s));
+                for (int e = 0; e < 4; ++e) l[i][e] = (ht[e] - hi_s) + (lt[e] - lo_s);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) yx[i] = mfma(lds<bf8>(dq + i * 2048), xf1, yx[i]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) l[i][e] = __builtin_amdgcn_exp2f(l[i][e]);
                 if (masked) {
-                    const int4 r = *reinterpret_cast<const int4*>(starts + 16 * j + 4 * g4);
-                    l = f4{r.x == rs ? l[0] : 0.0f, r.y == rs ? l[1] : 0.0f, r.z == rs ? l[2] : 0.0f, r.w == rs ? l[3] : 0.0f};
+                    const int4 r = *reinterpret_cast<const int4*>(starts + r0 + 16 * i + 4 * g4);
+                    l[i] = f4{r.x == rs ? l[i][0] : 0.0f, r.y == rs ? l[i][1] : 0.0f, r.z == rs ? l[i][2] : 0.0f,
+                              r.w == rs ? l[i][3] : 0.0f};
                 }
-                float dw[4] = {0, 0, 0, 0};  // products of a token with itself
-                if (j == st) {
+            }
+            u4 pw[2];  // two parts of the pairs, in token order
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (4 * g4 + e < li) l[e] = 0.0f;
-                        dw[e] = 4 * g4 + e == li ? cb[e] * yx[e] : 0.0f;
-                        diag += dw[e];
-                    }
-                }
+            for (int i = 0; i < 2; ++i) {
+                const bool own = FIRST && (st & 1) == i;  // the tile on the diagonal
                 float pv[4], rw[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    pv[e] = l[e] * cb[e];
-                    lw[j][e] += l[e] * yx[e] * dts;
-                    const float w = pv[e] * yx[e] - dw[e];  // l = 1 on the diagonal: exactly 0 there
-                    if (j == st) bdiag += w;
-                    else below += w;
+                    const int after = r0 + 16 * i + 4 * g4 + e - s;  // t - s
+                    if (FIRST) l[i][e] = after >= 0 ? l[i][e] : 0.0f;
+                    pv[e] = l[i][e] * cb[i][e];
+                    if (FIRST) pv[e] = after >= 0 ? pv[e] : 0.0f;  // what stands above the diagonal is another tile's
+                    sum[i][e] += l[i][e] * yx[i][e] * dts;
+                    float w = pv[e] * yx[i][e];
+                    if (FIRST) {
+                        diag += after == 0 ? w : 0.0f;
+                        w = after == 0 ? 0.0f : w;
+                        bdiag += own ? w : 0.0f;
+                        below += own ? 0.0f : w;
+                    } else {
+                        below += w;
+                    }
                     rw[e] = w * dts;
                 }
-                settle(lw[j]);
-                *reinterpret_cast<float*>(sm + rt + 64 * j) = row_sums(rw, li);  // the same from four lanes
-                // two parts, into this tile's half of the operand
+                settle(sum[i]);
+                *reinterpret_cast<float*>(sm + rt + 4 * r0 + 64 * i) = row_sums(rw, li);  // the same from four lanes
                 const uint32_t q0 = pack_bf16x2(pv[0], pv[1]), q1 = pack_bf16x2(pv[2], pv[3]);
-                pw[0][2 * (j & 1)] = q0;
-                pw[0][2 * (j & 1) + 1] = q1;
-                pw[1][2 * (j & 1)] = pack_bf16x2(pv[0] - __uint_as_float(q0 << 16), pv[1] - __uint_as_float(q0 & 0xFFFF0000u));
-                pw[1][2 * (j & 1) + 1] = pack_bf16x2(pv[2] - __uint_as_float(q1 << 16), pv[3] - __uint_as_float(q1 & 0xFFFF0000u));
-            } else {
-                pw[0][2 * (j & 1)] = pw[0][2 * (j & 1) + 1] = pw[1][2 * (j & 1)] = pw[1][2 * (j & 1) + 1] = 0;
+                pw[0][2 * i] = q0;
+                pw[0][2 * i + 1] = q1;
+                pw[1][2 * i] = pack_bf16x2(pv[0] - __uint_as_float(q0 << 16), pv[1] - __uint_as_float(q0 & 0xFFFF0000u));
+                pw[1][2 * i + 1] = pack_bf16x2(pv[2] - __uint_as_float(q1 << 16), pv[3] - __uint_as_float(q1 & 0xFFFF0000u));
             }
-            if ((j & 1) && j >= st) {
+            bf8 y[4];
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    const uint8_t* q = sm + (yo ^ (p << 5)) + 16 * (j - 1) * 128;
-                    const bf8 y = join(tr_read(q), tr_read(q + 16 * 128));
-                    dxa[p] = mfma(y, __builtin_bit_cast(bf8, pw[1]), dxa[p]);
-                    dxa[p] = mfma(y, __builtin_bit_cast(bf8, pw[0]), dxa[p]);
-                }
+            for (int p = 0; p < 4; ++p) {
+                const uint8_t* q = sm + (yo ^ (p << 5)) + r0 * 128;
+                y[p] = join(tr_read(q), tr_read(q + 16 * 128));
             }
-        }
+#pragma unroll
+            for (int k = 1; k >= 0; --k)
+#pragma unroll
+                for (int p = 0; p < 4; ++p) dxa[p] = mfma(y[p], __builtin_bit_cast(bf8, pw[k]), dxa[p]);
+        };
+        step(32 * (st >> 1), lwd, std::true_type{});
+#pragma unroll
+        for (int m = 1; m < 4; ++m)
+            if (m > (st >> 1)) step(32 * m, lw[m - 1], std::false_type{});
         {  // rows of lanes 0, 1, 2: kSumColOff, kSumColDiag, kSumDiag
             const float v = group_sums(below, diag, bdiag, 0.0f);
             if (g4 < 3) sums[(kSumColOff + g4) * kFQ + s] = v;
@@ -827,16 +847,26 @@ __global__ void __launch_bounds__(512) sbf_grad_kernel(ScanBwdArgs a) {
                 Gp[kk][2] = Glo[kk];
             }
         }
+        f4 oo[2];
 #pragma unroll
         for (int jj = 0; jj < TT; ++jj) {
             const int j = th0 + jj;
-            const bf8 x0 = lds<bf8>(sm + xo + 16 * j * 128), x1 = lds<bf8>(sm + (xo ^ 64) + 16 * j * 128);
-            f4 o{0, 0, 0, 0};
+            if ((jj & 1) == 0) {  // two tiles' products side by side
+                bf8 xx[2][2];
 #pragma unroll
-            for (int k = 2; k >= 0; --k) {
-                o = mfma(Gp[0][k], x0, o);
-                o = mfma(Gp[1][k], x1, o);
+                for (int i = 0; i < 2; ++i) {
+                    xx[i][0] = lds<bf8>(sm + xo + 16 * (j + i) * 128);
+                    xx[i][1] = lds<bf8>(sm + (xo ^ 64) + 16 * (j + i) * 128);
+                    oo[i] = f4{0, 0, 0, 0};
+                }
+#pragma unroll
+                for (int k = 2; k >= 0; --k)
+#pragma unroll
+                    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) oo[i] = mfma(Gp[kk][k], xx[i][kk], oo[i]);
             }
+            const f4 o = oo[jj & 1];
             const float es = lds<float>(sm + tl + 3 * LR + 64 * j), ed = es * lds<float>(sm + tl + 4 * LR + 64 * j);
             const u2 bv = lds<u2>(sm + cw + O::B + 16 * j * RB);
             float w = 0.0f;
@@ -887,7 +917,7 @@ __global__ void __launch_bounds__(512) sbf_grad_kernel(ScanBwdArgs a) {
     for (int j = 0; j < 8; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float v = j >= st ? lw[j][e] : 0.0f;
+            const float v = j >> 1 == st >> 1 ? lwd[j & 1][e] : j > st ? lw[(j >> 1) > 0 ? (j >> 1) - 1 : 0][j & 1][e] : 0.0f;
             const int t = 16 * j + 4 * g4 + e;
             const uint16_t hi = f32_to_bf16(v), lo = f32_to_bf16(v - bf16_to_f32(hi));
             const int o = piece<256>(t, s >> 3) + 2 * (s & 7);
