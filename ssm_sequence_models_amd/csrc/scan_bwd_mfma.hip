@@ -22,7 +22,8 @@
 //               time; the rounding errors of eight chunks at most add up, and where f <G, S> is
 //               far below u and v, |G| |S| f bounds it and with it the error
 // One kernel for dC and the rest together read S, G and dy once, but held 300 registers a lane:
-// at two wavefronts a SIMD (LDS) it spilled, and took 2318 us where the two take 0 us.
+// at two wavefronts a SIMD (LDS) it spilled, and took 2318 us at 4 x 8192 tokens x 64 heads,
+// dstate 128, where the two take 168 + 486 us.
 //
 // Operands: x, dy, B and C are exact in bf16.  The fp32 operands S and G and the scaled x and dy
 // of sbf_states are taken in three bf16 parts (24 bits, nothing lost: ddt and dA are fp32
@@ -165,6 +166,7 @@ __device__ __forceinline__ int here(int v) {
     return v;
 }
 // keeps a sum where it is computed (moved to the loop's end it would keep its terms in registers)
+__device__ __forceinline__ void settle(float& v) { asm volatile("" : "+v"(v)); }
 __device__ __forceinline__ void settle(f4& v) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) asm volatile("" : "+v"(v[e]));
@@ -554,6 +556,7 @@ __global__ void __launch_bounds__(512, 4) sbf_dc_kernel(ScanBwdArgs a) {
                 acc[jj][e] += ft * o[e];
             }
             settle(acc[jj]);
+            settle(w);
             u[jj & 3] = w * ft;
             if ((jj & 3) == 3) up[16 * (jj - 3)] = group_sums(u[0], u[1], u[2], u[3]);
         }
@@ -591,385 +594,391 @@ __global__ void __launch_bounds__(256) sbf_anchor_kernel(ScanBwdArgs a) {
     if (threadIdx.x == 0) a.anchor[bh * n + i] = th * ((sum[0] + sum[1]) + (sum[2] + sum[3]));
 }
 
+// 16 wavefronts, four a SIMD, in two roles that meet at the two barriers of a head and otherwise
+// run beside each other:
+//   0-7   s tile st (1, 2, .. and 7, 6, .. on one SIMD: nine pair tiles each): the pairs, W's sums, dx
+//   8-15  n tile nt: G's parts, dB from behind the chunk and v; the head before's sums
+// LDS holds one block a CU, so the roles are what hides one's LDS waits behind the other's
+// products: as eight wavefronts that did both in turn it took 541 us where this takes 486 (227
+// and 190 us at one row of 32768 tokens, 24 heads, dstate 64).  The t tiles are taken in pairs
+// from an even one on, so that the bodies a wavefront may start in are few and keep within 128
+// registers: from any one on they were 8, with 51 spilled registers where these spill 28
+// outside the pairs, and 510 us.
 template <int N>
-__global__ void __launch_bounds__(512) sbf_grad_kernel(ScanBwdArgs a) {
+__global__ void __launch_bounds__(1024) sbf_grad_kernel(ScanBwdArgs a) {
     using O = GradLds<N>;
     constexpr int NT = N / 16, RB = 2 * N, BP = N / 8;
-    constexpr int TT = NT;       // t tiles a wavefront does for dB and dC: all 8, or half of them
+    constexpr int TT = NT;       // s tiles a wavefront does for dB: all 8, or half of them
     constexpr int PL = N * 128;  // bytes of one part of G
     constexpr int LR = kFQ * 4;  // bytes of one float a token
     __shared__ __attribute__((aligned(16))) uint8_t sm[O::TOTAL];
-    const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g4 = lane >> 4;
+    const int tid = threadIdx.x & 511, lane = tid & 63, li = lane & 15, g4 = lane >> 4;
+    const bool pairs = __builtin_amdgcn_readfirstlane(threadIdx.x >> 9) == 0;  // the role
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t hs = blockIdx.x % a.splits, g = blockIdx.x / a.splits % a.G;
     const int64_t c = blockIdx.x / a.splits / a.G % a.chunks, b = blockIdx.x / a.splits / a.G / a.chunks;
     const int64_t k_heads = a.H / a.G;
     const int64_t hfirst = g * k_heads + hs * a.split_heads;
-    const int64_t hend = hs * a.split_heads + a.split_heads < k_heads ? hfirst + a.split_heads : (g + 1) * k_heads;
+    const int heads = static_cast<int>(hs * a.split_heads + a.split_heads < k_heads ? a.split_heads : k_heads - hs * a.split_heads);
     const int64_t t0 = c * kFQ, tok = b * a.L + t0;
     const int nv = a.L - t0 < kFQ ? static_cast<int>(a.L - t0) : kFQ;
-    const int nt = wave % NT, th0 = NT == 8 ? 0 : (wave / NT) * TT;  // n tile and first t tile for dB, dC
-    const int st = wave < 4 ? wave : 11 - wave;  // s tile for the pairs: 9 tiles a SIMD (waves w, w + 4)
+    const int nt = wave % NT, th0 = NT == 8 ? 0 : (wave / NT) * TT;  // n tile and first s tile for dB
+    const int st = wave < 4 ? wave : 11 - wave;
     int* starts = reinterpret_cast<int*>(sm + O::START);
 
     // loads of one head: uniform bases that move with the head, 32-bit lane offsets that do not
-    // (128 token rows are under 2^32 bytes)
-    const int row = tid >> 3;  // and row + 64
-    const uint32_t vx = static_cast<uint32_t>(row * a.x_row * 2 + 16 * (tid & 7));
-    const uint32_t vdy = static_cast<uint32_t>(row * a.dy_row * 2 + 16 * (tid & 7));
-    const uint32_t vs = static_cast<uint32_t>(nt * 4096 + (g4 >> 1) * 1024 + (g4 & 1) * 512 + li * 16);
-    u4 rx[2], rdy[2];
-    f4 rG[4];
-    float rd[2];
-    auto load = [&](int64_t h) __attribute__((always_inline)) {
-        const char* xb = reinterpret_cast<const char*>(static_cast<const uint16_t*>(a.x) + tok * a.x_row + h * kFP);
-        const char* db = reinterpret_cast<const char*>(static_cast<const uint16_t*>(a.dy) + tok * a.dy_row + h * kFP);
+    // (128 token rows are under 2^32 bytes).  The pairs' role stages dy, the other x, G and decays.
+    const int64_t xrow = pairs ? a.dy_row : a.x_row;
+    const char* xb = reinterpret_cast<const char*>(static_cast<const uint16_t*>(pairs ? a.dy : a.x) + tok * xrow + hfirst * kFP);
+    const int xpart = pairs ? O::DY : O::X;
+    u4 rx[2];
+    auto load_x = [&]() __attribute__((always_inline)) {
+        const int id = here(tid), row = id >> 3;  // and row + 64
+        const uint32_t vx = static_cast<uint32_t>(row) * static_cast<uint32_t>(xrow * 2) + 16 * (id & 7);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            rx[i] = rdy[i] = u4{0, 0, 0, 0};
-            if (row + 64 * i < nv) {
-                rx[i] = *reinterpret_cast<const u4any*>(xb + i * 128 * a.x_row + vx);
-                rdy[i] = *reinterpret_cast<const u4any*>(db + i * 128 * a.dy_row + vdy);
-            }
+            rx[i] = u4{0, 0, 0, 0};
+            if (row + 64 * i < nv) rx[i] = *reinterpret_cast<const u4any*>(xb + i * 128 * xrow + vx);
         }
-        const int64_t at = ((b * a.H + h) * a.chunks + c) * N * kFP;
-        const char* gp = reinterpret_cast<const char*>(a.grads + at);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) rG[i] = __builtin_nontemporal_load(reinterpret_cast<const f4*>(gp + 2048 * (i >> 1) + 256 * (i & 1) + vs));
-        const float* rec = a.decay + ((b * a.H + h) * a.chunks + c) * 5 * kFQ;
-        rd[0] = rec[tid];
-        if (tid < kFQ) rd[1] = rec[4 * kFQ + tid];
+        xb += kFP * 2;
     };
-    load(hfirst);
+    auto stage_x = [&]() __attribute__((always_inline)) {  // rows row and row + 64 share the swizzle
+        const int id = here(tid), xpiece = xpart + piece<128>(id >> 3, id & 7);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) *reinterpret_cast<u4*>(sm + xpiece + i * 64 * 128) = rx[i];
+    };
     {
-        const uint16_t* bg = static_cast<const uint16_t*>(a.Bm) + tok * a.b_row + g * N;
-        const uint16_t* cg = static_cast<const uint16_t*>(a.C) + tok * a.c_row + g * N;
+        const uint16_t* bg = static_cast<const uint16_t*>(pairs ? a.Bm : a.C) + tok * (pairs ? a.b_row : a.c_row) + g * N;
+        const int64_t brow = pairs ? a.b_row : a.c_row;
         for (int q = tid; q < kFQ * BP; q += 512) {
             const int r = q / BP;
-            u4 v{0, 0, 0, 0}, u{0, 0, 0, 0};
-            if (r < nv) {
-                v = *reinterpret_cast<const u4any*>(bg + r * a.b_row + 8 * (q % BP));
-                u = *reinterpret_cast<const u4any*>(cg + r * a.c_row + 8 * (q % BP));
-            }
-            *reinterpret_cast<u4*>(sm + O::B + piece<RB>(r, q % BP)) = v;
-            *reinterpret_cast<u4*>(sm + O::CB + piece<RB>(r, q % BP)) = u;
+            u4 v{0, 0, 0, 0};
+            if (r < nv) v = *reinterpret_cast<const u4any*>(bg + r * brow + 8 * (q % BP));
+            *reinterpret_cast<u4*>(sm + (pairs ? O::B : O::CB) + piece<RB>(r, q % BP)) = v;
         }
-        if (tid < kFQ) starts[tid] = a.starts[(b * a.chunks + c) * kFQ + tid];
+        if (threadIdx.x < kFQ) starts[threadIdx.x] = a.starts[(b * a.chunks + c) * kFQ + threadIdx.x];
     }
-    __syncthreads();
-    const int any_start = __builtin_amdgcn_readfirstlane(starts[kFQ - 1]);
-    const int s = 16 * st + li;
-    const int rs = starts[s];
-
-    // C B^T of this wavefront's s tile and t tiles st .. 7, then in place of C
-    const int cbt = O::CB + (st * (17 - st) / 2) * 1024 - st * 1024 + 16 * lane;  // tile of t tile j at + 1024 j
-    {
-        f4 cb[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            cb[j] = f4{0, 0, 0, 0};
-            if (j >= st) {
-#pragma unroll
-                for (int kk = 0; kk < N / 32; ++kk)
-                    cb[j] = mfma(lds<bf8>(sm + O::CB + 16 * j * RB + (along_off<RB>(li, g4) ^ (kk << 6))),
-                                 lds<bf8>(sm + O::B + 16 * st * RB + (along_off<RB>(li, g4) ^ (kk << 6))), cb[j]);
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j >= st) *reinterpret_cast<f4*>(sm + cbt + 1024 * j) = cb[j];
-    }
-    // sums over the heads of L dt (dy x^T) with s tile st: the two t tiles that hold the diagonal,
-    // and tiles 2 m, 2 m + 1 behind them
-    f4 lwd[2] = {}, lw[3][2] = {};
-    f4 accB[TT];
-#pragma unroll
-    for (int j = 0; j < TT; ++j) accB[j] = f4{0, 0, 0, 0};
-
     const int64_t sum_step = a.chunks * (kSums * kFQ + kSumTail);
     float* sums = a.sums + ((b * a.H + hfirst) * a.chunks + c) * (kSums * kFQ + kSumTail);
-    for (int64_t h = hfirst; h < hend; ++h) {
-        const int par = static_cast<int>(h - hfirst) & 1;
-        const int hb = O::ROW + par * O::HEAD;  // this head's part of LDS
-        int m = any_start;
-        asm volatile("" : "+s"(m));  // one copy of the loop, not one for each case
-        const bool masked = m != 0;
-        // G's parts: two in LDS, the third (which dx does without) in registers
-        bf8 Glo[2];
-        float norm = 0.0f;
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            float v[8];
-            bf8 p[3];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                v[e] = rG[2 * kk + (e >> 2)][e & 3];
-                norm += v[e] * v[e];
-            }
-            split(v, p);
-            rG[2 * kk] = __builtin_bit_cast(f4, p[0]);
-            rG[2 * kk + 1] = __builtin_bit_cast(f4, p[1]);
-            Glo[kk] = p[2];
-        }
-        norm = group_sum4(lane_sum16(norm));
-        if (lane == 0 && wave < NT) sums[kSums * kFQ + 72 + nt] = norm;
-        __syncthreads();  // the previous head's x, dy and G have been read
+    __syncthreads();
+
+    if (pairs) {
+        const bool masked = __builtin_amdgcn_readfirstlane(starts[kFQ - 1]) != 0;
+        // C B^T of this wavefront's s tile and t tiles st .. 7, then in place of C
+        const int cbt = O::CB + (st * (17 - st) / 2) * 1024 - st * 1024;  // t tile j at + 1024 j
         {
-            const int o = here(piece<128>(row, tid & 7));  // rows row and row + 64 share the swizzle
+            f4 cb[8];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                *reinterpret_cast<u4*>(sm + o + O::X + i * 64 * 128) = rx[i];
-                *reinterpret_cast<u4*>(sm + o + O::DY + i * 64 * 128) = rdy[i];
-            }
-            if (wave < NT) {
-                const int q = here(O::G + 16 * nt * 128 + along_off<128>(li, g4));
+            for (int j = 0; j < 8; ++j) {
+                cb[j] = f4{0, 0, 0, 0};
+                if (j >= st) {
 #pragma unroll
-                for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) *reinterpret_cast<f4*>(sm + k * PL + (q ^ (kk << 6))) = rG[2 * kk + k];
-            }
-            float* dec = reinterpret_cast<float*>(sm + hb + O::DEC);
-            dec[tid] = rd[0];
-            if (tid < kFQ) dec[4 * kFQ + tid] = rd[1];
-        }
-        __syncthreads();
-        if (h > hfirst) head_sums<N>(sm, O::ROW + (par ^ 1) * O::HEAD, sums - sum_step, tid);
-
-        // LDS offsets of this head's reads
-        const int bst = here(along_off<RB>(li, g4) + 16 * st * RB);      // B, rows of s tile st
-        const int xo = here(O::X + along_off<128>(li, g4));              // x, dy along rows
-        const int yo = here(O::DY + down_off<128>(4 * g4, li));          // dy down rows
-        const int cw = here(piece<RB>(li, 2 * nt + (g4 >> 1)) + 8 * (g4 & 1));  // B elements (n 4 g4 .., s li)
-        const int tl = here(hb + O::DEC + 4 * li);                       // decays of token li of a tile
-        const int t4 = here(hb + O::DEC + 16 * g4);                      // decays of tokens 4 g4 ..
-        const int vt = here(hb + O::V + nt * LR + 64 * group_of_row(g4) + 4 * li);  // v of n tile nt, four s tiles
-        const int ct = here(cbt);                                        // C B^T
-        const int rt = here(hb + st * LR + 16 * g4 + 4 * (li & 3));      // row sums
-
-        // ---- pairs s <= t of s tile st: W's sums, the pairs' part of dx ----
-        f4 dxa[4];
-#pragma unroll
-        for (int p = 0; p < 4; ++p) dxa[p] = f4{0, 0, 0, 0};
-        const bf8 xf0 = lds<bf8>(sm + xo + 16 * st * 128), xf1 = lds<bf8>(sm + (xo ^ 64) + 16 * st * 128);
-        const float hi_s = lds<float>(sm + tl + 64 * st), lo_s = lds<float>(sm + tl + LR + 64 * st);
-        const float dts = lds<float>(sm + tl + 4 * LR + 64 * st);
-        float below = 0.0f, bdiag = 0.0f, diag = 0.0f;  // column sums of W / dt_s
-        // two t tiles at a time (one operand of dx), from token r0; FIRST: the two that hold the
-        // diagonal (where st is odd, the first of them lies above it and gives nothing)
-        auto step = [&](int r0, f4 (&sum)[2], auto first) __attribute__((always_inline)) {
-            constexpr bool FIRST = decltype(first)::value;
-            const uint8_t* dp = sm + xo + (O::DY - O::X) + r0 * 128;
-            const uint8_t* dq = sm + (xo ^ 64) + (O::DY - O::X) + r0 * 128;
-            f4 yx[2], cb[2], l[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                yx[i] = mfma(lds<bf8>(dp + i * 2048), xf0, f4{0, 0, 0, 0});
-                cb[i] = lds<f4>(sm + ct + 64 * r0 + 1024 * i);
-                const f4 ht = lds<f4>(sm + t4 + 4 * r0 + 64 * i), lt = lds<f4>(sm + t4 + LR + 4 * r0 + 64 * i);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) l[i][e] = (ht[e] - hi_s) + (lt[e] - lo_s);
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) yx[i] = mfma(lds<bf8>(dq + i * 2048), xf1, yx[i]);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) l[i][e] = __builtin_amdgcn_exp2f(l[i][e]);
-                if (masked) {
-                    const int4 r = *reinterpret_cast<const int4*>(starts + r0 + 16 * i + 4 * g4);
-                    l[i] = f4{r.x == rs ? l[i][0] : 0.0f, r.y == rs ? l[i][1] : 0.0f, r.z == rs ? l[i][2] : 0.0f,
-                              r.w == rs ? l[i][3] : 0.0f};
+                    for (int kk = 0; kk < N / 32; ++kk)
+                        cb[j] = mfma(lds<bf8>(sm + O::CB + 16 * j * RB + (along_off<RB>(li, g4) ^ (kk << 6))),
+                                     lds<bf8>(sm + O::B + 16 * st * RB + (along_off<RB>(li, g4) ^ (kk << 6))), cb[j]);
                 }
             }
-            u4 pw[2];  // two parts of the pairs, in token order
+            __syncthreads();
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const bool own = FIRST && (st & 1) == i;  // the tile on the diagonal
+            for (int j = 0; j < 8; ++j)
+                if (j >= st) *reinterpret_cast<f4*>(sm + cbt + 16 * lane + 1024 * j) = cb[j];
+        }
+        load_x();
+        // sums over the heads of L dt (dy x^T) with s tile st: the even t tile and its neighbour that
+        // hold the diagonal, and tiles 2 m, 2 m + 1 behind them
+        f4 lwd[2] = {}, lw[3][2] = {};
+        char* dxp = reinterpret_cast<char*>(static_cast<uint16_t*>(a.dx) + tok * a.dx_row + hfirst * kFP);
+        for (int h = 0; h < heads; ++h) {
+            const int hb = O::ROW + (h & 1) * O::HEAD;  // this head's part of LDS
+            __syncthreads();  // the previous head's x, dy and G have been read
+            stage_x();
+            __syncthreads();
+            // all that depends on the lane is computed anew for each head: registers are short
+            const int ln = here(lane), li = ln & 15, g4 = ln >> 4, s = 16 * st + li;
+            const int rs = masked ? starts[s] : 0;
+            // LDS offsets of this head's reads
+            const int xo = here(O::X + along_off<128>(li, g4));              // x, dy along rows
+            const int yo = here(O::DY + down_off<128>(4 * g4, li));          // dy down rows
+            const int tl = here(hb + O::DEC + 4 * li);                       // decays of token li of a tile
+            const int t4 = here(hb + O::DEC + 16 * g4);                      // decays of tokens 4 g4 ..
+            const int rt = here(hb + st * LR + 16 * g4 + 4 * (li & 3));      // row sums
+            const int ct = here(cbt + 16 * ln);                              // C B^T
+
+            // ---- pairs s <= t: W's sums, the pairs' part of dx ----
+            f4 dxa[4] = {};
+            const float hi_s = lds<float>(sm + tl + 64 * st), lo_s = lds<float>(sm + tl + LR + 64 * st);
+            const float dts = lds<float>(sm + tl + 4 * LR + 64 * st);
+            float below = 0.0f, bdiag = 0.0f, diag = 0.0f;  // column sums of W / dt_s
+            u4 pw[2];  // two parts of the pairs of two t tiles, in token order
+            // the pairs of t tile j with s tile st, in half i of that operand
+            auto tile = [&](int j, int i, f4& sum, auto on_diagonal) __attribute__((always_inline)) {
+                constexpr bool DIAG = decltype(on_diagonal)::value;
+                const uint8_t* dp = sm + xo + (O::DY - O::X) + j * 2048;
+                const uint8_t* dq = sm + (xo ^ 64) + (O::DY - O::X) + j * 2048;
+                f4 yx = mfma(lds<bf8>(dp), lds<bf8>(sm + xo + 2048 * st), f4{0, 0, 0, 0});
+                yx = mfma(lds<bf8>(dq), lds<bf8>(sm + (xo ^ 64) + 2048 * st), yx);
+                const f4 ht = lds<f4>(sm + t4 + 64 * j), lt = lds<f4>(sm + t4 + LR + 64 * j);
+                f4 l;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) l[e] = __builtin_amdgcn_exp2f((ht[e] - hi_s) + (lt[e] - lo_s));
+                if (masked) {
+                    const int4 r = *reinterpret_cast<const int4*>(starts + 16 * j + 4 * g4);
+                    l = f4{r.x == rs ? l[0] : 0.0f, r.y == rs ? l[1] : 0.0f, r.z == rs ? l[2] : 0.0f, r.w == rs ? l[3] : 0.0f};
+                }
+                const f4 cb = lds<f4>(sm + ct + 1024 * j);
+                const int d = li - 4 * g4;  // t - s = e - d on the diagonal
                 float pv[4], rw[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int after = r0 + 16 * i + 4 * g4 + e - s;  // t - s
-                    if (FIRST) l[i][e] = after >= 0 ? l[i][e] : 0.0f;
-                    pv[e] = l[i][e] * cb[i][e];
-                    if (FIRST) pv[e] = after >= 0 ? pv[e] : 0.0f;  // what stands above the diagonal is another tile's
-                    sum[i][e] += l[i][e] * yx[i][e] * dts;
-                    float w = pv[e] * yx[i][e];
-                    if (FIRST) {
-                        diag += after == 0 ? w : 0.0f;
-                        w = after == 0 ? 0.0f : w;
-                        bdiag += own ? w : 0.0f;
-                        below += own ? 0.0f : w;
+                    if (DIAG) l[e] = e >= d ? l[e] : 0.0f;
+                    pv[e] = l[e] * cb[e];
+                    const float yd = yx[e] * dts;
+                    sum[e] += l[e] * yd;
+                    rw[e] = pv[e] * yd;
+                    if (DIAG) {
+                        const float w = pv[e] * yx[e];
+                        diag += e == d ? w : 0.0f;
+                        bdiag += e == d ? 0.0f : w;
+                        rw[e] = e == d ? 0.0f : rw[e];
                     } else {
-                        below += w;
+                        below += pv[e] * yx[e];
                     }
-                    rw[e] = w * dts;
                 }
-                settle(sum[i]);
-                *reinterpret_cast<float*>(sm + rt + 4 * r0 + 64 * i) = row_sums(rw, li);  // the same from four lanes
+                settle(sum);
+                *reinterpret_cast<float*>(sm + rt + 64 * j) = row_sums(rw, li);  // the same from four lanes
                 const uint32_t q0 = pack_bf16x2(pv[0], pv[1]), q1 = pack_bf16x2(pv[2], pv[3]);
                 pw[0][2 * i] = q0;
                 pw[0][2 * i + 1] = q1;
                 pw[1][2 * i] = pack_bf16x2(pv[0] - __uint_as_float(q0 << 16), pv[1] - __uint_as_float(q0 & 0xFFFF0000u));
                 pw[1][2 * i + 1] = pack_bf16x2(pv[2] - __uint_as_float(q1 << 16), pv[3] - __uint_as_float(q1 & 0xFFFF0000u));
-            }
-            bf8 y[4];
+                __builtin_amdgcn_sched_barrier(0);  // the registers of one tile at a time
+            };
+            // their part of dx, from t tile j on (even)
+            auto to_dx = [&](int j) __attribute__((always_inline)) {
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                const uint8_t* q = sm + (yo ^ (p << 5)) + r0 * 128;
-                y[p] = join(tr_read(q), tr_read(q + 16 * 128));
-            }
+                for (int p0 = 0; p0 < 4; p0 += 2) {
+                    bf8 y[2];
 #pragma unroll
-            for (int k = 1; k >= 0; --k)
+                    for (int p = 0; p < 2; ++p) {
+                        const uint8_t* q = sm + (yo ^ ((p0 + p) << 5)) + j * 2048;
+                        y[p] = join(tr_read(q), tr_read(q + 16 * 128));
+                    }
 #pragma unroll
-                for (int p = 0; p < 4; ++p) dxa[p] = mfma(y[p], __builtin_bit_cast(bf8, pw[k]), dxa[p]);
-        };
-        step(32 * (st >> 1), lwd, std::true_type{});
+                    for (int k = 1; k >= 0; --k)
 #pragma unroll
-        for (int m = 1; m < 4; ++m)
-            if (m > (st >> 1)) step(32 * m, lw[m - 1], std::false_type{});
-        {  // rows of lanes 0, 1, 2: kSumColOff, kSumColDiag, kSumDiag
-            const float v = group_sums(below, diag, bdiag, 0.0f);
-            if (g4 < 3) sums[(kSumColOff + g4) * kFQ + s] = v;
-        }
-        sums += sum_step;
-        if (h + 1 < hend) load(h + 1);
-
-        // ---- x against G: dB, v ----
-        float v[4];
-        bf8 Gp[2][3];
-        {
-            const int q = here(O::G + 16 * nt * 128 + along_off<128>(li, g4));
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                Gp[kk][0] = lds<bf8>(sm + (q ^ (kk << 6)));
-                Gp[kk][1] = lds<bf8>(sm + PL + (q ^ (kk << 6)));
-                Gp[kk][2] = Glo[kk];
-            }
-        }
-        f4 oo[2];
-#pragma unroll
-        for (int jj = 0; jj < TT; ++jj) {
-            const int j = th0 + jj;
-            if ((jj & 1) == 0) {  // two tiles' products side by side
-                bf8 xx[2][2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    xx[i][0] = lds<bf8>(sm + xo + 16 * (j + i) * 128);
-                    xx[i][1] = lds<bf8>(sm + (xo ^ 64) + 16 * (j + i) * 128);
-                    oo[i] = f4{0, 0, 0, 0};
+                        for (int p = 0; p < 2; ++p) dxa[p0 + p] = mfma(y[p], __builtin_bit_cast(bf8, pw[k]), dxa[p0 + p]);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-#pragma unroll
-                for (int k = 2; k >= 0; --k)
-#pragma unroll
-                    for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) oo[i] = mfma(Gp[kk][k], xx[i][kk], oo[i]);
+            };
+            if (st & 1) {
+                pw[0] = pw[1] = u4{0, 0, 0, 0};
+            } else {
+                tile(st, 0, lwd[0], std::true_type{});
             }
-            const f4 o = oo[jj & 1];
-            const float es = lds<float>(sm + tl + 3 * LR + 64 * j), ed = es * lds<float>(sm + tl + 4 * LR + 64 * j);
-            const u2 bv = lds<u2>(sm + cw + O::B + 16 * j * RB);
-            float w = 0.0f;
+            if (st & 1) tile(st, 1, lwd[1], std::true_type{});
+            else tile(st + 1, 1, lwd[1], std::false_type{});
+            to_dx(st & 6);
+#pragma unroll
+            for (int m = 1; m < 4; ++m)
+                if (m > (st >> 1)) {
+                    tile(2 * m, 0, lw[m - 1][0], std::false_type{});
+                    tile(2 * m + 1, 1, lw[m - 1][1], std::false_type{});
+                    to_dx(2 * m);
+                }
+            if (h + 1 < heads) load_x();
+            {  // rows of lanes 0, 1, 2: kSumColOff, kSumColDiag, kSumDiag
+                const float v = group_sums(below, diag, bdiag, 0.0f);
+                if (g4 < 3) sums[(kSumColOff + g4) * kFQ + s] = v;
+            }
+            sums += sum_step;
+
+            // ---- dx: G B, then with the pairs ----
+            const float es = lds<float>(sm + tl + 3 * LR + 64 * st);
+            const int bst = here(along_off<RB>(li, g4) + 16 * st * RB);  // B, rows of s tile st
+            const int go0 = here(O::G + down_off<128>(8 * g4, li)), go1 = here(O::G + down_off<128>(8 * g4 + 4, li));
+            f4 gb[4] = {};
+#pragma unroll
+            for (int kk = 0; kk < N / 32; ++kk) {
+                const bf8 bf = lds<bf8>(sm + (bst ^ (kk << 6)));
+#pragma unroll
+                for (int k = 1; k >= 0; --k)
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        const int o = k * PL + 32 * kk * 128;
+                        gb[p] = mfma(join(tr_read(sm + (go0 ^ (p << 5)) + o), tr_read(sm + (go1 ^ (p << 5)) + o)), bf, gb[p]);
+                    }
+            }
+            const uint32_t vdx = static_cast<uint32_t>(s) * static_cast<uint32_t>(a.dx_row * 2) + 8 * g4;
+            if (s < nv) {
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    f4 r;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) r[e] = dts * (dxa[p][e] + es * gb[p][e]);
+                    *reinterpret_cast<u2any*>(dxp + vdx + 32 * p) = u2{pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3])};
+                }
+            }
+            dxp += kFP * 2;
+        }
+        __syncthreads();
+        // ---- the heads' summed pairs: two parts of [t][s] in LDS (zero above the diagonal) ----
+        const int s = 16 * st + li;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                w += __uint_as_float(e & 1 ? bv[e >> 1] & 0xFFFF0000u : bv[e >> 1] << 16) * o[e];
-                accB[jj][e] += ed * o[e];
+                const float v = j >> 1 == st >> 1 ? lwd[j & 1][e] : j > st ? lw[(j >> 1) > 0 ? (j >> 1) - 1 : 0][j & 1][e] : 0.0f;
+                const int t = 16 * j + 4 * g4 + e;
+                const uint16_t hi = f32_to_bf16(v), lo = f32_to_bf16(v - bf16_to_f32(hi));
+                const int o = piece<256>(t, s >> 3) + 2 * (s & 7);
+                *reinterpret_cast<uint16_t*>(sm + O::LW + o) = hi;
+                *reinterpret_cast<uint16_t*>(sm + O::LW + kFQ * 256 + o) = lo;
             }
-            settle(accB[jj]);
-            v[jj & 3] = w * es;
-            if ((jj & 3) == 3) *reinterpret_cast<float*>(sm + vt + 64 * (j - 3)) = group_sums(v[0], v[1], v[2], v[3]);
-        }
-
-        // ---- dx: G B, then with the pairs ----
-        const float es = lds<float>(sm + tl + 3 * LR + 64 * st);
-        const int go0 = here(O::G + down_off<128>(8 * g4, li)), go1 = here(O::G + down_off<128>(8 * g4 + 4, li));
-        f4 gb[4];
+        __syncthreads();
+        // ---- dC of n tile nt: sbf_dc's part (where this block alone has the pairs), then the pairs ----
+        const int b0 = down_off<RB>(8 * g4, li) ^ (nt << 5), b1 = down_off<RB>(8 * g4 + 4, li) ^ (nt << 5);
+        const int lo_ = along_off<256>(li, g4);
 #pragma unroll
-        for (int p = 0; p < 4; ++p) gb[p] = f4{0, 0, 0, 0};
+        for (int jj = 0; jj < TT; ++jj) {
+            const int j = th0 + jj, t = 16 * j + li;
+            const int64_t col = g * N + 16 * nt + 4 * g4, slab = a.B * a.L * a.G * N;
+            const int64_t at = (tok + t) * a.G * N + col;
+            f4 acc{0, 0, 0, 0};
+            if (a.splits == 1 && t < nv)
+                for (int64_t i = 0; i < a.dc_splits; ++i) acc += *reinterpret_cast<const f4*>(a.dC_head + i * slab + at);
 #pragma unroll
-        for (int kk = 0; kk < N / 32; ++kk) {
-            const bf8 bf = lds<bf8>(sm + (bst ^ (kk << 6)));
-#pragma unroll
-            for (int p = 0; p < 4; ++p)
-#pragma unroll
-                for (int k = 1; k >= 0; --k) {
-                    const int o = k * PL + 32 * kk * 128;
-                    gb[p] = mfma(join(tr_read(sm + (go0 ^ (p << 5)) + o), tr_read(sm + (go1 ^ (p << 5)) + o)), bf, gb[p]);
+            for (int k = 0; k < 4; ++k)
+                if (2 * k <= j) {  // s tiles 2 k, 2 k + 1
+                    const uint8_t* p = sm + O::B + 32 * k * RB;
+                    const bf8 f = join(tr_read(p + b0), tr_read(p + b1));
+                    acc = mfma(f, along<256>(sm + O::LW + kFQ * 256, lo_, 16 * j, k), acc);
+                    acc = mfma(f, along<256>(sm + O::LW, lo_, 16 * j, k), acc);
                 }
-        }
-        char* dxo = reinterpret_cast<char*>(static_cast<uint16_t*>(a.dx) + tok * a.dx_row + h * kFP);
-        const uint32_t vdx = here(static_cast<int>(s * a.dx_row * 2 + 8 * g4));
-        if (s < nv) {
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                f4 r;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) r[e] = dts * (dxa[p][e] + es * gb[p][e]);
-                *reinterpret_cast<u2any*>(dxo + vdx + 32 * p) = u2{pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3])};
-            }
-        }
-    }
-    __syncthreads();
-    head_sums<N>(sm, O::ROW + (static_cast<int>(hend - 1 - hfirst) & 1) * O::HEAD, sums - sum_step, tid);
-
-    // ---- the heads' summed pairs: two parts of [t][s] in LDS (zero above the diagonal); C again ----
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float v = j >> 1 == st >> 1 ? lwd[j & 1][e] : j > st ? lw[(j >> 1) > 0 ? (j >> 1) - 1 : 0][j & 1][e] : 0.0f;
-            const int t = 16 * j + 4 * g4 + e;
-            const uint16_t hi = f32_to_bf16(v), lo = f32_to_bf16(v - bf16_to_f32(hi));
-            const int o = piece<256>(t, s >> 3) + 2 * (s & 7);
-            *reinterpret_cast<uint16_t*>(sm + O::LW + o) = hi;
-            *reinterpret_cast<uint16_t*>(sm + O::LW + kFQ * 256 + o) = lo;
-        }
-    {
-        const uint16_t* cg = static_cast<const uint16_t*>(a.C) + tok * a.c_row + g * N;
-        for (int q = tid; q < kFQ * BP; q += 512) {
-            const int r = q / BP;
-            u4 u{0, 0, 0, 0};
-            if (r < nv) u = *reinterpret_cast<const u4any*>(cg + r * a.c_row + 8 * (q % BP));
-            *reinterpret_cast<u4*>(sm + O::CB + piece<RB>(r, q % BP)) = u;
-        }
-    }
-    __syncthreads();
-    const int bo = down_off<RB>(4 * g4, li) ^ (nt << 5);       // C^T: rows of n tile nt
-    const int b0 = down_off<RB>(8 * g4, li) ^ (nt << 5), b1 = down_off<RB>(8 * g4 + 4, li) ^ (nt << 5);  // B^T
-    const int lo_ = along_off<256>(li, g4), ld = down_off<256>(4 * g4, li);
-#pragma unroll
-    for (int jj = 0; jj < TT; ++jj) {
-        const int j = th0 + jj;
-        const int t = 16 * j + li;
-        const int64_t col = g * N + 16 * nt + 4 * g4, slab = a.B * a.L * a.G * N;
-        const int64_t at = (tok + t) * a.G * N + col;
-        f4 accC{0, 0, 0, 0};
-        if (a.splits == 1 && t < nv)  // sbf_dc's part
-            for (int64_t i = 0; i < a.dc_splits; ++i) accC += *reinterpret_cast<const f4*>(a.dC_head + i * slab + at);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (2 * k <= j) {  // dC of t tile j: s tiles 2 k, 2 k + 1
-                const uint8_t* p = sm + O::B + 32 * k * RB;
-                const bf8 f = join(tr_read(p + b0), tr_read(p + b1));
-                accC = mfma(f, along<256>(sm + O::LW + kFQ * 256, lo_, 16 * j, k), accC);
-                accC = mfma(f, along<256>(sm + O::LW, lo_, 16 * j, k), accC);
-            }
-            if (2 * k + 1 >= j) {  // dB of s tile j: t tiles 2 k, 2 k + 1
-                const bf8 f = down<RB>(sm + O::CB, bo, 32 * k, 0);
-                accB[jj] = mfma(f, down<256>(sm + O::LW + kFQ * 256, ld, 32 * k, j), accB[jj]);
-                accB[jj] = mfma(f, down<256>(sm + O::LW, ld, 32 * k, j), accB[jj]);
-            }
-        }
-        if (t < nv) {
-            if (a.splits == 1) {
+            if (t >= nv) continue;
+            if (a.splits == 1)
                 *reinterpret_cast<u2any*>(static_cast<uint16_t*>(a.dC) + (tok + t) * a.dc_row + col) =
-                    u2{pack_bf16x2(accC[0], accC[1]), pack_bf16x2(accC[2], accC[3])};
-                *reinterpret_cast<u2any*>(static_cast<uint16_t*>(a.dB) + (tok + t) * a.db_row + col) =
-                    u2{pack_bf16x2(accB[jj][0], accB[jj][1]), pack_bf16x2(accB[jj][2], accB[jj][3])};
-            } else {
-                *reinterpret_cast<f4*>(a.dC_head + (a.dc_splits + hs) * slab + at) = accC;
-                *reinterpret_cast<f4*>(a.dB_head + hs * slab + at) = accB[jj];
+                    u2{pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3])};
+            else
+                *reinterpret_cast<f4*>(a.dC_head + (a.dc_splits + hs) * slab + at) = acc;
+        }
+    } else {
+        const char* gp = reinterpret_cast<const char*>(a.grads + ((b * a.H + hfirst) * a.chunks + c) * N * kFP);
+        const float* rec = a.decay + ((b * a.H + hfirst) * a.chunks + c) * 5 * kFQ;
+        f4 rG[4];
+        float rd[2];
+        auto load_g = [&]() __attribute__((always_inline)) {
+            const int ln = here(lane);
+            const uint32_t vs = static_cast<uint32_t>(nt * 4096 + (ln >> 5) * 1024 + (ln >> 4 & 1) * 512 + (ln & 15) * 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                rG[i] = __builtin_nontemporal_load(reinterpret_cast<const f4*>(gp + 2048 * (i >> 1) + 256 * (i & 1) + vs));
+            gp += a.chunks * N * kFP * 4;
+            const int id = here(tid);
+            rd[0] = rec[id];
+            if (id < kFQ) rd[1] = rec[4 * kFQ + id];
+            rec += a.chunks * 5 * kFQ;
+        };
+        load_g();
+        load_x();
+        __syncthreads();  // the other role's of C B^T
+        f4 acc[TT] = {};
+        for (int h = 0; h < heads; ++h) {
+            const int hb = O::ROW + (h & 1) * O::HEAD;
+            const int id = here(tid), ln = id & 63, li = ln & 15, g4 = ln >> 4;
+            bf8 Gp[2][3];
+            float norm = 0.0f;
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    v[e] = rG[2 * kk + (e >> 2)][e & 3];
+                    norm += v[e] * v[e];
+                }
+                split(v, Gp[kk]);
             }
+            norm = group_sum4(lane_sum16(norm));
+            if (ln == 0 && wave < NT) sums[kSums * kFQ + 72 + nt] = norm;
+            __syncthreads();  // the previous head's x, dy and G have been read
+            stage_x();
+            if (wave < NT) {
+                const int q = here(O::G + 16 * nt * 128 + along_off<128>(li, g4));
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) *reinterpret_cast<bf8*>(sm + k * PL + (q ^ (kk << 6))) = Gp[kk][k];
+            }
+            {
+                float* dec = reinterpret_cast<float*>(sm + hb + O::DEC);
+                dec[id] = rd[0];
+                if (id < kFQ) dec[4 * kFQ + id] = rd[1];
+            }
+            __syncthreads();
+            if (h + 1 < heads) load_x();
+            if (h > 0) head_sums<N>(sm, O::ROW + ((h & 1) ^ 1) * O::HEAD, sums - sum_step, here(id));
+            sums += sum_step;
+            const int xo = here(O::X + along_off<128>(li, g4));                      // x along rows
+            const int cw = here(piece<RB>(li, 2 * nt + (g4 >> 1)) + 8 * (g4 & 1));   // B elements (n 4 g4 .., s li)
+            const int tl = here(hb + O::DEC + 4 * li);                               // decays of token li of a tile
+            const int vt = here(hb + O::V + nt * LR + 64 * group_of_row(g4) + 4 * li);  // v of n tile nt, four s tiles
+            float v[4];
+#pragma unroll
+            for (int jj = 0; jj < TT; ++jj) {
+                const int j = th0 + jj;
+                const bf8 x0 = lds<bf8>(sm + xo + 16 * j * 128), x1 = lds<bf8>(sm + (xo ^ 64) + 16 * j * 128);
+                f4 o{0, 0, 0, 0};
+#pragma unroll
+                for (int k = 2; k >= 0; --k) {
+                    o = mfma(Gp[0][k], x0, o);
+                    o = mfma(Gp[1][k], x1, o);
+                }
+                const float es = lds<float>(sm + tl + 3 * LR + 64 * j), ed = es * lds<float>(sm + tl + 4 * LR + 64 * j);
+                const u2 bv = lds<u2>(sm + cw + O::B + 16 * j * RB);
+                float w = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    w += __uint_as_float(e & 1 ? bv[e >> 1] & 0xFFFF0000u : bv[e >> 1] << 16) * o[e];
+                    acc[jj][e] += ed * o[e];
+                }
+                settle(acc[jj]);
+                settle(w);
+                if (jj == TT / 2 - 1 && h + 1 < heads) load_g();
+                v[jj & 3] = w * es;
+                if ((jj & 3) == 3) *reinterpret_cast<float*>(sm + vt + 64 * (j - 3)) = group_sums(v[0], v[1], v[2], v[3]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        __syncthreads();
+        head_sums<N>(sm, O::ROW + ((heads - 1) & 1) * O::HEAD, sums - sum_step, tid);
+        {  // C again, in place of C B^T
+            const uint16_t* cg = static_cast<const uint16_t*>(a.C) + tok * a.c_row + g * N;
+            for (int q = tid; q < kFQ * BP; q += 512) {
+                const int r = q / BP;
+                u4 u{0, 0, 0, 0};
+                if (r < nv) u = *reinterpret_cast<const u4any*>(cg + r * a.c_row + 8 * (q % BP));
+                *reinterpret_cast<u4*>(sm + O::CB + piece<RB>(r, q % BP)) = u;
+            }
+        }
+        __syncthreads();
+        // ---- dB of n tile nt: the pairs ----
+        const int bo = down_off<RB>(4 * g4, li) ^ (nt << 5), ld = down_off<256>(4 * g4, li);
+#pragma unroll
+        for (int jj = 0; jj < TT; ++jj) {
+            const int j = th0 + jj, t = 16 * j + li;
+            const int64_t col = g * N + 16 * nt + 4 * g4;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (2 * k + 1 >= j) {  // t tiles 2 k, 2 k + 1
+                    const bf8 f = down<RB>(sm + O::CB, bo, 32 * k, 0);
+                    acc[jj] = mfma(f, down<256>(sm + O::LW + kFQ * 256, ld, 32 * k, j), acc[jj]);
+                    acc[jj] = mfma(f, down<256>(sm + O::LW, ld, 32 * k, j), acc[jj]);
+                }
+            if (t >= nv) continue;
+            if (a.splits == 1)
+                *reinterpret_cast<u2any*>(static_cast<uint16_t*>(a.dB) + (tok + t) * a.db_row + col) =
+                    u2{pack_bf16x2(acc[jj][0], acc[jj][1]), pack_bf16x2(acc[jj][2], acc[jj][3])};
+            else
+                *reinterpret_cast<f4*>(a.dB_head + ((hs * a.B * a.L + tok + t) * a.G) * N + col) = acc[jj];
         }
     }
 }
@@ -1050,7 +1059,7 @@ hipError_t launch_typed(const ScanBwdArgs& a, hipStream_t s) {
     }
     sbf_anchor_kernel<<<static_cast<uint32_t>(bh * ((a.chunks + kAnchor - 1) / kAnchor)), 256, 0, s>>>(a);
     sbf_dc_kernel<N><<<static_cast<uint32_t>(a.B * a.chunks * a.G * a.dc_splits), 512, 0, s>>>(a);
-    sbf_grad_kernel<N><<<static_cast<uint32_t>(a.B * a.chunks * a.G * a.splits), 512, 0, s>>>(a);
+    sbf_grad_kernel<N><<<static_cast<uint32_t>(a.B * a.chunks * a.G * a.splits), 1024, 0, s>>>(a);
     if (a.splits > 1)
         sbf_join_kernel<<<dim3(static_cast<uint32_t>((a.B * a.L * a.G * N / 4 + 255) / 256), 2), 256, 0, s>>>(a);
     return hipGetLastError();
