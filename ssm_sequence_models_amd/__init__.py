@@ -13,6 +13,7 @@ cache_seqlens, conv_state_indices, seq_idx, and the backward with state gradient
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -162,7 +163,16 @@ def _ptr(t):
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    # the current stream's handle without a Stream object around it (2.9 us of a 15 us call)
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+
+
+_CURRENT = contextlib.nullcontext()
+
+
+def _on(device):
+    """The device of a call's tensors made the current one; nothing to do where it is already."""
+    return _CURRENT if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def _need(t, name, dtype=None, shape=None, contiguous=True):
@@ -488,10 +498,12 @@ def scan_fwd(x, dt, A, B, C, initial_state=None, seq_idx=None, return_final_stat
 def conv_scan_fwd(xBC, conv_weight, conv_bias, dt, A, nheads, headdim, ngroups, dstate,
                   conv_initial_state=None, initial_state=None, seq_idx=None,
                   activation="silu", return_final_states=True, conv_final_state=None,
-                  final_state=None, y=None, workspace=None):
+                  final_state=None, y=None, workspace=None, norm=None):
     """The fused prefill.  xBC [b, L, H*P + 2*G*N] (x | B | C channels); conv_weight
     [C_conv, K] fp32; conv_bias [C_conv]; dt [b, L, H]; A [H]; conv states [b, C_conv, K-1];
-    SSM states [b, H, P, N] fp32.  Returns (y [b, L, H, P], conv_final_state, final_state)."""
+    SSM states [b, H, P, N] fp32.  Returns (y [b, L, H, P], conv_final_state, final_state); with
+    norm (a dict of norm_fwd's keyword arguments) y normed and gated over its H*P channels,
+    [b, L, H*P], in y's place."""
     bsz, L, Cc = xBC.shape
     H, P, G, N = nheads, headdim, ngroups, dstate
     if Cc != H * P + 2 * G * N:
@@ -516,12 +528,13 @@ def conv_scan_fwd(xBC, conv_weight, conv_bias, dt, A, nheads, headdim, ngroups, 
     _need(conv_final_state, "conv_final_state", xBC.dtype, (bsz, Cc, K - 1))
     _need(final_state, "final_state", torch.float32, (bsz, H, P, N))
     ws, nbytes = _workspace(workspace, workspace_size(bsz, L, H, P, G, N, xBC.dtype), xBC.device)
+    normed = None if norm is None else _norm_plan(y.view(bsz, L, H * P), **norm)[1]
     _check("ssm_conv_scan_fwd", _lib.ssm_conv_scan_fwd(
         _ptr(xBC), _ptr(conv_weight), _ptr(conv_bias), _ptr(conv_initial_state),
         _ptr(conv_final_state), _ptr(dt), _ptr(A), _ptr(initial_state), _ptr(final_state),
         _ptr(seq_idx), _ptr(y), bsz, L, H, P, G, N, K, _dtype_code(xBC), ACT[activation], _ptr(ws),
         nbytes, _stream()))
-    return y, conv_final_state, final_state
+    return y if normed is None else normed(), conv_final_state, final_state
 
 
 def noalloc_scratch_bytes() -> int:
@@ -601,11 +614,12 @@ def step(x, dt, A, B, C, state, state_indices=None, y=None, nheads=None, ngroups
 
 def decode_step(x_new, conv_state, conv_weight, conv_bias, dt, A, ssm_state, nheads, headdim,
                 ngroups, dstate, conv_state_indices=None, cache_seqlens=None,
-                state_indices=None, activation="silu", conv_out=None, y=None):
+                state_indices=None, activation="silu", conv_out=None, y=None, norm=None):
     """One decode step on the pools (ssm_decode_step): the conv update over x_new
     [b, C_conv, n_new], then the SSM step reading the x | B | C channel ranges of its output.
     Both pools update in place; cache_seqlens is not advanced.  state_indices defaults to
-    conv_state_indices.  Returns y [b, n_new, H, P]."""
+    conv_state_indices.  Returns y [b, n_new, H, P], or with norm (a dict of norm_fwd's keyword
+    arguments) y normed and gated over its H*P channels, [b, n_new, H*P]."""
     bsz, C, n_new = x_new.shape
     H, P, G, N = nheads, headdim, ngroups, dstate
     if C != H * P + 2 * G * N:
@@ -634,12 +648,13 @@ def decode_step(x_new, conv_state, conv_weight, conv_bias, dt, A, ssm_state, nhe
     if y is None:
         y = torch.empty((bsz, n_new, H, P), dtype=x_new.dtype, device=x_new.device)
     _need(y, "y", x_new.dtype, (bsz, n_new, H, P))
+    normed = None if norm is None else _norm_plan(y.view(bsz, n_new, H * P), **norm)[1]
     _check("ssm_decode_step", _lib.ssm_decode_step(
         _ptr(x_new), _ptr(conv_state), _ptr(conv_weight), _ptr(conv_bias),
         _ptr(conv_state_indices), _ptr(cache_seqlens), _ptr(dt), _ptr(A), _ptr(ssm_state),
         _ptr(state_indices), _ptr(conv_out), _ptr(y), bsz, n_new, H, P, G, N, K, state_len,
         n_cslots, ssm_state.shape[0], _dtype_code(x_new), ACT[activation], _stream()))
-    return y
+    return y if normed is None else normed()
 
 
 def scan_bwd_workspace_size(batch, seqlen, nheads, headdim, ngroups, dstate,
@@ -689,7 +704,7 @@ def scan_bwd(x, dt, A, B, C, dy, initial_state=None, dfinal_state=None, seq_idx=
                  dfinal_state=dfinal_state, seq_idx=seq_idx, dx=dx, ddt=ddt, dA=dA, dB=dB, dC=dC,
                  dinitial_state=dinitial_state, workspace=workspace)
     ws, wsb = _workspace(workspace, scan_bwd_workspace_size(bsz, L, H, P, G, N, x.dtype), dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check("ssm_scan_bwd", _lib.ssm_scan_bwd(
             _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(dy), _ptr(initial_state),
             _ptr(dfinal_state), _ptr(seq_idx), _ptr(dx), _ptr(ddt), _ptr(dA), _ptr(dB), _ptr(dC),
@@ -734,7 +749,7 @@ def gated_scan_fwd(x, gate, form="sigmoid", initial_state=None, seq_idx=None,
     _need(initial_state, "initial_state", torch.float32, (B, C))
     _need(seq_idx, "seq_idx", torch.int32, (B, L))
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
     _need(y, "y", x.dtype, x.shape, contiguous=False)
     if final_state is None and return_final_state:
         final_state = torch.empty((B, C), dtype=torch.float32, device=x.device)
@@ -742,7 +757,7 @@ def gated_scan_fwd(x, gate, form="sigmoid", initial_state=None, seq_idx=None,
     _need_device(x, initial_state=initial_state, seq_idx=seq_idx, y=y, final_state=final_state,
                  workspace=workspace)
     ws, wsb = _workspace(workspace, gated_scan_fwd_workspace_size(B, L, C), x.device)
-    with torch.cuda.device(x.device):
+    with _on(x.device):
         _check("ssm_gated_scan_fwd", _lib.ssm_gated_scan_fwd(
             _ptr(x), x_row, _ptr(gate), gate_row, _ptr(initial_state), _ptr(final_state),
             _ptr(seq_idx), _ptr(y), _rows(y, "y", C)[1], B, L, C, GATE[form], _dtype_code(x),
@@ -760,9 +775,9 @@ def gated_scan_bwd(x, gate, dy, form="sigmoid", initial_state=None, dfinal_state
     _need(dfinal_state, "dfinal_state", torch.float32, (B, C))
     _need(seq_idx, "seq_idx", torch.int32, (B, L))
     if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dx = torch.empty_like(x, memory_format=torch.contiguous_format)
     if dgate is None:
-        dgate = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dgate = torch.empty_like(x, memory_format=torch.contiguous_format)
     if dinitial_state is None:
         dinitial_state = torch.empty((B, C), dtype=torch.float32, device=x.device)
     _need(dx, "dx", x.dtype, x.shape, contiguous=False)
@@ -771,7 +786,7 @@ def gated_scan_bwd(x, gate, dy, form="sigmoid", initial_state=None, dfinal_state
     _need_device(x, dy=dy, initial_state=initial_state, dfinal_state=dfinal_state, seq_idx=seq_idx,
                  dx=dx, dgate=dgate, dinitial_state=dinitial_state, workspace=workspace)
     ws, wsb = _workspace(workspace, gated_scan_bwd_workspace_size(B, L, C), x.device)
-    with torch.cuda.device(x.device):
+    with _on(x.device):
         _check("ssm_gated_scan_bwd", _lib.ssm_gated_scan_bwd(
             _ptr(x), x_row, _ptr(gate), gate_row, _ptr(dy), _rows(dy, "dy", C)[1],
             _ptr(initial_state), _ptr(dfinal_state), _ptr(seq_idx), _ptr(dx),
@@ -792,10 +807,10 @@ def gated_scan_step(x, gate, state, form="sigmoid", state_indices=None, y=None):
     if DEBUG_CHECKS:
         check_distinct_slots(state_indices, state.shape[0], "state_indices")
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
     _need(y, "y", x.dtype, x.shape, contiguous=False)
     _need_device(x, state=state, state_indices=state_indices, y=y)
-    with torch.cuda.device(x.device):
+    with _on(x.device):
         _check("ssm_gated_scan_step", _lib.ssm_gated_scan_step(
             _ptr(x), x_row, _ptr(gate), gate_row, _ptr(state), _ptr(state_indices), _ptr(y),
             _rows(y, "y", C)[1], B, T, C, state.shape[0], GATE[form], _dtype_code(x), _stream()))
@@ -818,9 +833,27 @@ def _norm_args(x, weight, bias, z, kind, ngroups):
     _need(weight, "weight", torch.float32, (C,))
     _need(bias, "bias", torch.float32, (C,))
     _need(z, "z", x.dtype, x.shape, contiguous=False)
-    _need_device(x, weight=weight, bias=bias, z=z)
     rows, x_row = _rows(x, "x", C)
     return C, rows, x_row, 0 if z is None else _rows(z, "z", C)[1]
+
+
+def _norm_plan(x, weight=None, bias=None, z=None, eps=1e-5, kind="rms", ngroups=1,
+               norm_before_gate=False, out=None):
+    """norm_fwd checked and its output allocated, not run: (out, the call)."""
+    C, rows, x_row, z_row = _norm_args(x, weight, bias, z, kind, ngroups)
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    _need(out, "out", x.dtype, x.shape, contiguous=False)
+    _need_device(x, weight=weight, bias=bias, z=z, out=out)
+    args = (_ptr(x), x_row, _ptr(z), z_row, _ptr(weight), _ptr(bias), _ptr(out),
+            _rows(out, "out", C)[1], rows, C, ngroups, eps, NORM[kind], int(norm_before_gate),
+            _dtype_code(x))
+
+    def run():
+        with _on(x.device):
+            _check("ssm_norm_fwd", _lib.ssm_norm_fwd(*args, _stream()))
+        return out
+    return out, run
 
 
 def norm_fwd(x, weight=None, bias=None, z=None, eps=1e-5, kind="rms", ngroups=1,
@@ -829,17 +862,7 @@ def norm_fwd(x, weight=None, bias=None, z=None, eps=1e-5, kind="rms", ngroups=1,
     channels, times weight [channels] fp32, plus bias; z [..., channels] gates with silu(z),
     before the norm or (norm_before_gate) after it.  x, z and out: consecutive channels, rows at
     any one stride.  Returns out [..., channels] (x's dtype)."""
-    C, rows, x_row, z_row = _norm_args(x, weight, bias, z, kind, ngroups)
-    if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _need(out, "out", x.dtype, x.shape, contiguous=False)
-    _need_device(x, out=out)
-    with torch.cuda.device(x.device):
-        _check("ssm_norm_fwd", _lib.ssm_norm_fwd(
-            _ptr(x), x_row, _ptr(z), z_row, _ptr(weight), _ptr(bias), _ptr(out),
-            _rows(out, "out", C)[1], rows, C, ngroups, eps, NORM[kind], int(norm_before_gate),
-            _dtype_code(x), _stream()))
-    return out
+    return _norm_plan(x, weight, bias, z, eps, kind, ngroups, norm_before_gate, out)[1]()
 
 
 def norm_bwd_workspace_size(rows, channels, ngroups=1) -> int:
@@ -854,11 +877,11 @@ def norm_bwd(x, weight, dout, bias=None, z=None, eps=1e-5, kind="rms", ngroups=1
     C, rows, x_row, z_row = _norm_args(x, weight, bias, z, kind, ngroups)
     _need(dout, "dout", x.dtype, x.shape, contiguous=False)
     if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dx = torch.empty_like(x, memory_format=torch.contiguous_format)
     if z is None and dz is not None:
         raise ValueError("dz given without z")
     if z is not None and dz is None:
-        dz = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dz = torch.empty_like(x, memory_format=torch.contiguous_format)
     if dweight is None:
         dweight = torch.empty(C, dtype=torch.float32, device=x.device)
     if bias is not None and dbias is None:
@@ -867,9 +890,9 @@ def norm_bwd(x, weight, dout, bias=None, z=None, eps=1e-5, kind="rms", ngroups=1
     _need(dz, "dz", x.dtype, x.shape, contiguous=False)
     _need(dweight, "dweight", torch.float32, (C,))
     _need(dbias, "dbias", torch.float32, (C,))
-    _need_device(x, dout=dout, dx=dx, dz=dz, dweight=dweight, dbias=dbias, workspace=workspace)
+    _need_device(x, weight=weight, bias=bias, z=z, dout=dout, dx=dx, dz=dz, dweight=dweight, dbias=dbias, workspace=workspace)
     ws, wsb = _workspace(workspace, norm_bwd_workspace_size(rows, C, ngroups), x.device)
-    with torch.cuda.device(x.device):
+    with _on(x.device):
         _check("ssm_norm_bwd", _lib.ssm_norm_bwd(
             _ptr(x), x_row, _ptr(z), z_row, _ptr(dout), _rows(dout, "dout", C)[1], _ptr(weight),
             _ptr(bias), _ptr(dx), _rows(dx, "dx", C)[1], _ptr(dz),
