@@ -322,9 +322,13 @@ struct ScanBwdArgs {
 // Sums over pairs of tokens that ddt and dA are formed from (W, u, v as in scan_bwd.hip), each an
 // array over the chunk's tokens: u; v / dt; row sums of W over s < t, in earlier 16-token tiles
 // and in t's own; column sums of W / dt_s over t > s, in later tiles and in s's own; W_tt / dt_t.
-// Behind them the row sums' sums by tile, [t tile][s tile] in eights, then <G, S> (64-token chunks)
-// or the parts of |S|^2 and |G|^2 by 16 state dimensions, in eights (128).
-enum { kSumU, kSumV, kSumRowOff, kSumRowDiag, kSumColOff, kSumColDiag, kSumDiag, kSums };
+// Behind them the row sums' sums by tile, [t tile][s tile] in eights, then the parts of |S|^2 and
+// |G|^2 by 16 state dimensions, in eights.
+// Chunks of 64 tokens: u; v / dt; the W that span t; all column sums; W_tt / dt_t; the rests of
+// u and of the spanning W, which are kept as two floats each, and behind them those of v / dt and
+// both parts of f_last <G, S>.
+enum { kSumU, kSumV, kSumRowOff, kSumRowDiag, kSumColOff, kSumColDiag, kSumDiag, kSums,
+       kSumSpan = kSumRowOff, kSumSpanLow = kSumRowDiag, kSumULow = kSumColDiag };
 constexpr int kSumTail = 128;
 constexpr int kAnchor = 8;
 size_t scan_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N,

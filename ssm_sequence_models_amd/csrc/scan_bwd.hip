@@ -195,6 +195,27 @@ __global__ void __launch_bounds__(256) sb_pass_kernel(ScanBwdArgs a) {
     if (rev && a.dh0) a.dh0[bh * PN + i] = v;
 }
 
+// sums along aligned spans of LEN lanes: from the lane to the span's end, and before the lane
+template <int LEN>
+__device__ __forceinline__ double from_lane(double v, int lane) {
+#pragma unroll
+    for (int o = 1; o < LEN; o <<= 1) {
+        const double u = __shfl_down(v, o);
+        if ((lane & (LEN - 1)) + o < LEN) v += u;
+    }
+    return v;
+}
+template <int LEN>
+__device__ __forceinline__ double before_lane(double v, int lane) {
+    const double own = v;
+#pragma unroll
+    for (int o = 1; o < LEN; o <<= 1) {
+        const double u = __shfl_up(v, o);
+        if ((lane & (LEN - 1)) >= o) v += u;
+    }
+    return v - own;
+}
+
 // ---------------------------------------------------------------------------------------
 // gradients of one chunk and head
 // ---------------------------------------------------------------------------------------
@@ -203,11 +224,13 @@ __global__ void __launch_bounds__(256) sb_grad_kernel(ScanBwdArgs a) {
     __shared__ ChunkDecay cd;
     __shared__ float pair[kQ][kQ + 1];  // [t][s] L_ts (C_t.B_s)
     __shared__ float lw[kQ][kQ + 1];    // [t][s] L_ts (dy_t.x_s) dt_s
-    __shared__ float rowp[4][kQ];       // sums over the s of one 16-column tile, s < t, of W
-    __shared__ float colp[4][kQ];       // sums over the t of one 16-row tile, t > s, of W / dt_s
+    // in double, formed from the fp32 dot products without another rounding: the part of q_t within
+    // its tile is a difference of these, and dA, a sum over all tokens, may cancel further
+    __shared__ double rowp[4][kQ];      // sums over the s of one 16-column tile, s < t, of W
+    __shared__ double colp[4][kQ];      // sums over the t of one 16-row tile, t > s, of W / dt_s
     __shared__ float diag[kQ];          // W_ss / dt_s
-    __shared__ float uu[kQ], vv[kQ];    // u_t, v_s / dt_s
-    __shared__ float gs[4];
+    __shared__ double uu[kQ], vv[kQ];   // u_t, v_s / dt_s
+    __shared__ double gs[4];
     const Where w = where(a, blockIdx.x);
     chunk_decay(cd, a.dt + (w.b * a.L + w.t0) * a.H + w.h, a.H, a.A[w.h],
                 a.seq ? a.seq + w.b * a.L : nullptr, w.t0, w.nv);
@@ -235,19 +258,20 @@ __global__ void __launch_bounds__(256) sb_grad_kernel(ScanBwdArgs a) {
         const double css = cd.cs[s];
         const int rs = cd.starts[s];
         const float dts = cd.dt[s];
-        float below = 0.0f;
+        double below = 0.0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int t = 16 * ti + 4 * g4 + e;
             const bool in = t >= s && cd.starts[t] == rs;
-            const float l = in ? static_cast<float>(exp2(cd.cs[t] - css)) : 0.0f;
+            const double ld = in ? exp2(cd.cs[t] - css) : 0.0;
+            const float l = static_cast<float>(ld);
             const float pv = in ? l * cb[e] : 0.0f, yv = in ? l * yx[e] * dts : 0.0f;
             pair[t][s] = pv;
             lw[t][s] = yv;
-            const float w0 = in ? pv * yx[e] : 0.0f;
-            if (t == s) diag[s] = w0;
+            const double w0 = in ? ld * (static_cast<double>(cb[e]) * yx[e]) : 0.0;
+            if (t == s) diag[s] = static_cast<float>(w0);
             else below += w0;
-            float row = t > s ? w0 * dts : 0.0f;
+            double row = t > s ? w0 * dts : 0.0;
 #pragma unroll
             for (int o = 1; o < 16; o <<= 1) row += __shfl_xor(row, o);
             if (li == 0) rowp[si][t] = row;
@@ -258,8 +282,8 @@ __global__ void __launch_bounds__(256) sb_grad_kernel(ScanBwdArgs a) {
     }
     // <G, S>
     {
-        float d = 0.0f;
-        for (int i = threadIdx.x; i < P * N; i += 256) d += sv.p[i] * gv.p[i];
+        double d = 0.0;
+        for (int i = threadIdx.x; i < P * N; i += 256) d += static_cast<double>(sv.p[i]) * gv.p[i];
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) d += __shfl_xor(d, o);
         if (lane == 0) gs[wave] = d;
@@ -269,7 +293,7 @@ __global__ void __launch_bounds__(256) sb_grad_kernel(ScanBwdArgs a) {
     // this wavefront's 16 tokens r0 .. r0 + 15 of every output
     const int r0 = 16 * wave;
     T* dxo = static_cast<T*>(a.dx) + tok * a.dx_row + w.h * P;
-    float v[4] = {0, 0, 0, 0}, u[4] = {0, 0, 0, 0};
+    double v[4] = {0, 0, 0, 0}, u[4] = {0, 0, 0, 0};  // without e and f
     for (int p0 = 0; p0 < P; p0 += 16) {
         f4 in{0, 0, 0, 0}, out{0, 0, 0, 0};
         for (int k = r0; k < kQ; k += 16) {
@@ -283,7 +307,7 @@ __global__ void __launch_bounds__(256) sb_grad_kernel(ScanBwdArgs a) {
         for (int e = 0; e < 4; ++e) {
             const int s = r0 + 4 * g4 + e, p = p0 + li;
             const float o = cd.e[s] == 0.0f ? 0.0f : cd.e[s] * out[e];
-            v[e] += xv.at(s, p) * o;
+            if (o != 0.0f) v[e] += static_cast<double>(xv.at(s, p)) * out[e];
             if (s < w.nv && p < P) S::store(dxo, s * a.dx_row + p, cd.dt[s] * (in[e] + o));
         }
     }
@@ -309,7 +333,7 @@ __global__ void __launch_bounds__(256) sb_grad_kernel(ScanBwdArgs a) {
             const int t = r0 + 4 * g4 + e, n = n0 + li;
             const float o = cd.f[t] == 0.0f ? 0.0f : cd.f[t] * out[e];
             const float bo = cd.e[t] == 0.0f ? 0.0f : cd.e[t] * cd.dt[t] * bout[e];
-            u[e] += cv.at(t, n) * o;
+            if (o != 0.0f) u[e] += static_cast<double>(cv.at(t, n)) * out[e];
             if (t < w.nv && n < N) {
                 a.dC_head[ho + t * a.H * N + n] = in[e] + o;
                 a.dB_head[ho + t * a.H * N + n] = bin[e] + bo;
@@ -324,8 +348,9 @@ __global__ void __launch_bounds__(256) sb_grad_kernel(ScanBwdArgs a) {
             v[e] += __shfl_xor(v[e], o);
         }
         if (li == 0) {
-            uu[r0 + 4 * g4 + e] = u[e];
-            vv[r0 + 4 * g4 + e] = v[e];
+            const int t = r0 + 4 * g4 + e;
+            uu[t] = cd.f[t] == 0.0f ? 0.0 : u[e] * exp2(cd.cs[t]);
+            vv[t] = cd.e[t] == 0.0f ? 0.0 : v[e] * exp2(cd.cs[kQ - 1] - cd.cs[t]);
         }
     }
     __syncthreads();
@@ -334,42 +359,29 @@ __global__ void __launch_bounds__(256) sb_grad_kernel(ScanBwdArgs a) {
     if (wave != 0) return;
     const int t = lane, j = t / 16;
     float* out = a.sums + ((w.b * a.H + w.h) * a.chunks + w.c) * (kSums * kQ + kSumTail);
-    float row = 0.0f, below = 0.0f;
+    double row = 0.0, below = 0.0;
     for (int i = 0; i < j; ++i) row += rowp[i][t];
     for (int i = j + 1; i < 4; ++i) below += colp[i][t];
-    out[kSumU * kQ + t] = uu[t];
-    out[kSumV * kQ + t] = vv[t];
-    out[kSumRowOff * kQ + t] = row;
-    out[kSumRowDiag * kQ + t] = rowp[j][t];
-    out[kSumColOff * kQ + t] = below;
-    out[kSumColDiag * kQ + t] = colp[j][t];
+    // the W that span t: rows from t to its tile's end over earlier tiles, columns of its tile
+    // before t under later tiles, the pairs within its tile, and the tile pairs around it
+    const double dts = cd.dt[t];
+    double q = from_lane<16>(row, t) + before_lane<16>(below * dts, t);
+    q += from_lane<16>(rowp[j][t] - colp[j][t] * dts, t);
+    for (int tj = j + 1; tj < 4; ++tj)
+        for (int i = 0; i < 16 * j; ++i) q += rowp[i >> 4][16 * tj + (i & 15)];
+    // each as the sum of two floats
+    auto both = [](float* hi, float* lo, double v) {
+        *hi = static_cast<float>(v);
+        *lo = static_cast<float>(v - *hi);
+    };
+    both(out + kSumU * kQ + t, out + kSumULow * kQ + t, uu[t]);
+    both(out + kSumV * kQ + t, out + kSums * kQ + t, vv[t]);
+    both(out + kSumSpan * kQ + t, out + kSumSpanLow * kQ + t, q);
+    out[kSumColOff * kQ + t] = static_cast<float>(below + colp[j][t]);
     out[kSumDiag * kQ + t] = diag[t];
-    float tile = 0.0f;  // [t tile][s tile] in eights
-    if (t < 32 && (t & 7) < (t >> 3))
-        for (int i = 0; i < 16; ++i) tile += rowp[t & 7][16 * (t >> 3) + i];
-    out[kSums * kQ + t] = tile;
-    if (t == 0) out[kSums * kQ + 64] = (gs[0] + gs[1]) + (gs[2] + gs[3]);
-}
-
-// sums along aligned spans of LEN lanes: from the lane to the span's end, and before the lane
-template <int LEN>
-__device__ __forceinline__ double from_lane(double v, int lane) {
-#pragma unroll
-    for (int o = 1; o < LEN; o <<= 1) {
-        const double u = __shfl_down(v, o);
-        if ((lane & (LEN - 1)) + o < LEN) v += u;
-    }
-    return v;
-}
-template <int LEN>
-__device__ __forceinline__ double before_lane(double v, int lane) {
-    const double own = v;
-#pragma unroll
-    for (int o = 1; o < LEN; o <<= 1) {
-        const double u = __shfl_up(v, o);
-        if ((lane & (LEN - 1)) >= o) v += u;
-    }
-    return v - own;
+    if (t == 0)
+        both(out + kSums * kQ + 64, out + kSums * kQ + 65,
+             cd.through == 0.0f ? 0.0 : exp2(cd.cs[kQ - 1]) * ((gs[0] + gs[1]) + (gs[2] + gs[3])));
 }
 
 // q, ddt and a chunk's share of dA: one wavefront a head and chunk, Q / 64 tokens a lane; a block
@@ -396,10 +408,18 @@ __global__ void __launch_bounds__(128 * kAnchor) sb_ddt_kernel(ScanBwdArgs a) {
         for (int k = 0; k < K; ++k) {
             const int t = lane + 64 * k, j = t >> 4;
             dts[k] = t0 + t < a.L ? (Q == 128 ? a.decay[(at * 5 + 4) * Q + t] : a.dt[(b * a.L + t0 + t) * a.H + h]) : 0.0f;
-            const float coff = in[kSumColOff * Q + t], cdiag = in[kSumColDiag * Q + t], vt = in[kSumV * Q + t];
-            direct[k] = ((coff + cdiag) + in[kSumDiag * Q + t]) + vt;
+            const float coff = in[kSumColOff * Q + t], vt = in[kSumV * Q + t];
             u[k] = in[kSumU * Q + t];
             v[k] = static_cast<double>(vt) * dts[k];
+            if constexpr (Q == kQ) {  // the span's W are summed already; two floats each
+                direct[k] = (coff + in[kSumDiag * Q + t]) + vt;
+                u[k] += in[kSumULow * Q + t];
+                v[k] += static_cast<double>(in[kSums * Q + t]) * dts[k];
+                q[k] = static_cast<double>(in[kSumSpan * Q + t]) + in[kSumSpanLow * Q + t];
+                continue;
+            }
+            const float cdiag = in[kSumColDiag * Q + t];
+            direct[k] = ((coff + cdiag) + in[kSumDiag * Q + t]) + vt;
             q[k] = from_lane<16>(in[kSumRowOff * Q + t], lane) + before_lane<16>(static_cast<double>(coff) * dts[k], lane);
             q[k] += from_lane<16>(static_cast<double>(in[kSumRowDiag * Q + t]) - static_cast<double>(cdiag) * dts[k], lane);
             for (int j2 = j + 1; j2 < Q / 16; ++j2)
@@ -434,7 +454,7 @@ __global__ void __launch_bounds__(128 * kAnchor) sb_ddt_kernel(ScanBwdArgs a) {
         if (th == 0.0f) {
             pass = 0.0;
         } else if (Q == 64) {
-            pass = static_cast<double>(th) * tail[64];
+            pass = static_cast<double>(tail[64]) + tail[65];
         } else if (d == last) {
             pass = a.anchor[(b * a.H + h) * ranges + range];
         } else {
