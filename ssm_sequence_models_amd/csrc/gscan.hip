@@ -11,23 +11,30 @@
 //
 // Bound by memory, so the recurrence is cut along the row to keep the GPU full, and joined
 // again on chip: h over a span of tokens is A h_in + H (Sec. 2.5 Eq. (4): A the product of its
-// decays, H its own tokens' share).  A block takes 64 channels (one a lane) of one row and
-// walks over tiles of 128 tokens, 8 wavefronts of 16 tokens each: every wavefront forms its
-// (A, H), and (A, E) backward, from registers, the 8 spans are joined through LDS, and a
-// second walk over the registers applies the state that comes in.  So a tile is read once.
-// The next tile's loads are issued before the current one is worked on.  4 x 8192 tokens x 4096
-// channels, bf16, sigmoid form, packed: 200 us (0.80 GB, 4.0 TB/s), 158 us with all loads from
-// one tile: the instructions (nine a token and lane for the gates alone, two of them at a
-// quarter of the rate) bound it as much as the traffic.  16 wavefronts of 8 tokens join twice
-// the spans for the same tokens: 221 us.
+// decays, H its own tokens' share).  A block takes 64 channels of one row and walks over tiles
+// of 128 tokens, 8 wavefronts of 16 tokens each; a lane has two channels of half the tokens, so
+// that a load or store moves a pair.  Every wavefront forms its (A, H), and (A, E) backward,
+// from registers (the halves against each other with the half-swap of lanes, one channel a
+// lane), the 8 spans are joined through LDS, and a second walk over the registers applies the
+// state that comes in.  So a tile is read once.
+//
+// The next tile's loads are issued before the current one is worked on, and its stores are not
+// waited for.  That holds as long as the loop has one path: where loads or stores were under a
+// branch (a row's last tile, lanes past the last channel), the waits behind it were those of
+// the path with the fewest, and 16-bit loads kept the load return path busy for 82 % of the
+// time.  So tiles that end within the row have a loop of their own, and lanes past the last
+// channel repeat the last pair.  4 x 8192 tokens x 4096 channels, bf16, sigmoid form, packed:
+// forward 173 us (0.80 GB, 4.7 TB/s; one channel a lane 200; 16 wavefronts of 8 tokens, which
+// join twice the spans, 221), backward 149 + 269 us (0.56 + 1.36 GB; one channel a lane
+// 161 + 326).  The instructions bound it as much: nine a token and channel for the gates alone,
+// two of them at a quarter of the rate.
 //
 // Rows and channels too few to fill the GPU (under kFill blocks) are cut into segments of
 // tiles: a first kernel joins each segment to one (A, H), which reads the inputs once more,
 // and each block of the second folds the segments before (and behind) its own.  One row of
-// 65573 tokens x 333 channels, fp32, log form: 37 + 69 us.
+// 65573 tokens x 333 channels, fp32, log form: 37 + 71 us.
 // The backward needs h before each tile: its first kernel walks forward and stores (A, H) from
-// the segment's start to each tile's (8 bytes a channel and 128 tokens).  At the size above
-// 161 + 326 us (0.56 + 1.36 GB).
+// the segment's start to each tile's (8 bytes a channel and 128 tokens).
 //
 // A span that holds a sequence start passes nothing on; it is marked by A = -1 (a product of
 // decays is never negative) and folded by a select, so a NaN or infinity of one sequence does
@@ -40,7 +47,8 @@ namespace ssm {
 namespace {
 
 constexpr int kGW = 8;              // wavefronts a block
-constexpr int kGT = 16;             // tokens a wavefront and tile
+constexpr int kGL = 8;              // tokens a lane and tile
+constexpr int kGT = 2 * kGL;        // tokens a wavefront and tile
 constexpr int kGTile = kGW * kGT;   // 128
 constexpr int kGThreads = 64 * kGW;
 
@@ -55,6 +63,7 @@ struct GArgs {
     int64_t tiles, nseg, seg_tiles;
     float* seg;   // [B][nseg][3][C]: A, H, E of each segment (forward: the initial state in segment 0's E)
     float* ckpt;  // [B][tiles][2][C]: A, H from the segment's start to the tile's
+    bool pairs;   // two channels and the lanes' 32-bit offsets serve whole tiles
 };
 
 // decay a and input factor i of a gate: e = exp(-g), a = 1 / (1 + e) and i = e a keep both to full
@@ -82,19 +91,41 @@ __device__ __forceinline__ float fold_mark(float A, float P) {
     return MARKS && (P < 0.0f || A < 0.0f) ? -1.0f : P * A;
 }
 
-// a wavefront's tokens of one tile, as loaded; token i is row tok0 + i of the row b.  SEQ: the rows
-// are packed
+// two consecutive channels of a token, at any element's alignment
+template <class S>
+struct Two;
+template <>
+struct Two<BF16> {
+    typedef uint32_t R;
+    typedef uint32_t M __attribute__((aligned(2)));
+    __device__ __forceinline__ static float get(R r, int k) { return __uint_as_float(k ? r & 0xFFFF0000u : r << 16); }
+    __device__ __forceinline__ static R of(uint16_t lo, uint16_t hi) { return lo | static_cast<uint32_t>(hi) << 16; }
+    __device__ __forceinline__ static R round(float lo, float hi) { return pack_bf16x2(lo, hi); }
+};
+template <>
+struct Two<F32> {
+    typedef float R __attribute__((ext_vector_type(2)));
+    typedef float M __attribute__((ext_vector_type(2), aligned(4)));
+    __device__ __forceinline__ static float get(R r, int k) { return r[k]; }
+    __device__ __forceinline__ static R of(float lo, float hi) { return R{lo, hi}; }
+    __device__ __forceinline__ static R round(float lo, float hi) { return R{lo, hi}; }
+};
+
+// a lane's tokens of one tile, as loaded.  SEQ: the rows are packed
 template <class S, bool DY, bool SEQ>
 struct GRaw {
     static constexpr bool kSeq = SEQ;
-    typename S::T x[kGT], g[kGT], d[DY ? kGT : 1];
-    int32_t id;  // lane j: sequence id of token tok0 - 1 + j
+    typename Two<S>::R x[kGL], g[kGL], d[DY ? kGL : 1];
+    int32_t id;  // lane j: sequence id of the token before the wavefront's token j
 };
 
+// A lane's place: channels c0, c0 + 1 of the tokens 8 half .. 8 half + 7 of a wavefront's 16, and
+// one channel, c, of all that is joined over spans.  Past the last pair lanes take the last two
+// channels once more (of one channel, that one twice): the same values to the same places.
 struct GPos {
-    int64_t b, c;
-    int lane, wave;
-    bool live;  // the lane's channel exists
+    int64_t b, c, c0;
+    int lane, wave, half;
+    bool live;  // no other lane has channel c
 };
 
 // A 32-bit lane offset that stays one: added to a uniform base it is part of the access (left to
@@ -103,41 +134,71 @@ __device__ __forceinline__ uint32_t here(uint32_t v) {
     asm volatile("" : "+v"(v));
     return v;
 }
-template <class T>
-__device__ __forceinline__ T g_at(const char* token, uint32_t lane_bytes) {
-    return *reinterpret_cast<const T*>(token + lane_bytes);
-}
-template <class S, bool DY, bool SEQ>
-__device__ __forceinline__ void g_load(const GArgs& a, const GPos& p, int64_t tile, GRaw<S, DY, SEQ>& r) {
+// byte offset of a lane's first token and channel from the wavefront's first token
+template <class S>
+__device__ __forceinline__ uint32_t g_offset(const GPos& p, int64_t row) {
     using T = typename S::T;
+    return (static_cast<uint32_t>(p.half * kGL) * static_cast<uint32_t>(row) + static_cast<uint32_t>(p.c0)) * sizeof(T);
+}
+
+template <class S>
+__device__ __forceinline__ void g_rows(const void* base, int64_t token, int64_t row, uint32_t off, typename Two<S>::R (&v)[kGL]) {
+    const char* q = reinterpret_cast<const char*>(static_cast<const typename S::T*>(base) + token * row);
+    off = here(off);
+#pragma unroll
+    for (int i = 0; i < kGL; ++i) {
+        v[i] = *reinterpret_cast<const typename Two<S>::M*>(q + off);
+        q += row * sizeof(typename S::T);
+    }
+}
+// The same element by element, tokens past the row's end replaced by its last (read and not
+// used): the last tile of a row, one channel, or rows too far apart
+template <class S>
+__device__ __forceinline__ void g_rows_any(const GArgs& a, const GPos& p, const void* base, int64_t t0, int64_t row,
+                                           typename Two<S>::R (&v)[kGL]) {
+    using T = typename S::T;
+    const int64_t second = p.c0 + 1 < a.C ? 1 : 0;
+    int64_t t = t0 + here(p.half * kGL);
+    if (t >= a.L) t = a.L - 1;
+    const T* q = static_cast<const T*>(base) + (p.b * a.L + t) * row + p.c0;
+#pragma unroll
+    for (int i = 0; i < kGL; ++i) {
+        v[i] = Two<S>::of(q[0], q[second]);
+        if (t + 1 < a.L) {
+            ++t;
+            q += row;
+        }
+    }
+}
+
+// FULL: the tile ends within the row, and pairs serve it
+template <bool FULL, class S, bool DY, bool SEQ>
+__device__ __forceinline__ void g_load(const GArgs& a, const GPos& p, int64_t tile, GRaw<S, DY, SEQ>& r) {
     const int64_t t0 = tile * kGTile + p.wave * kGT, row0 = p.b * a.L;
-    const uint32_t lb = here(static_cast<uint32_t>(p.c) * static_cast<uint32_t>(sizeof(T)));
-    // tokens past the row's end: its last one, read and not used
-    const int64_t from = row0 + (t0 < a.L ? t0 : a.L - 1);
-    // tokens of this wavefront behind its first
-    const int left = a.L - 1 - t0 < kGT ? (a.L - 1 > t0 ? static_cast<int>(a.L - 1 - t0) : 0) : kGT;
-    const char* x = reinterpret_cast<const char*>(static_cast<const T*>(a.x) + from * a.x_row);
-    const char* g = reinterpret_cast<const char*>(static_cast<const T*>(a.gate) + from * a.gate_row);
-    const char* d = DY ? reinterpret_cast<const char*>(static_cast<const T*>(a.dy) + from * a.dy_row) : nullptr;
     // in the order of their use: a wait for one load is a wait for those before it
     if constexpr (SEQ) {
         int64_t t = t0 - 1 + p.lane;
         t = t < 0 ? 0 : t < a.L ? t : a.L - 1;
         r.id = a.seq[row0 + t];
     }
-    auto rows = [&](const char* p, int64_t step, typename S::T (&v)[kGT]) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < kGT; ++i) {
-            v[i] = g_at<T>(p, lb);
-            p += step & -static_cast<int64_t>(i < left);
-        }
-    };
-    rows(g, sizeof(T) * a.gate_row, r.g);
-    rows(x, sizeof(T) * a.x_row, r.x);
-    if constexpr (DY) rows(d, sizeof(T) * a.dy_row, r.d);
+    if constexpr (FULL) {
+        g_rows<S>(a.gate, row0 + t0, a.gate_row, g_offset<S>(p, a.gate_row), r.g);
+        g_rows<S>(a.x, row0 + t0, a.x_row, g_offset<S>(p, a.x_row), r.x);
+        if constexpr (DY) g_rows<S>(a.dy, row0 + t0, a.dy_row, g_offset<S>(p, a.dy_row), r.d);
+    } else {
+        g_rows_any<S>(a, p, a.gate, t0, a.gate_row, r.g);
+        g_rows_any<S>(a, p, a.x, t0, a.x_row, r.x);
+        if constexpr (DY) g_rows_any<S>(a, p, a.dy, t0, a.dy_row, r.d);
+    }
 }
 
-// bit i: token i starts a sequence (token 0 of the row never does)
+// the first tile that g_load<true> does not serve, from `first` on
+__device__ __forceinline__ int64_t g_full(const GArgs& a, int64_t first, int64_t last) {
+    const int64_t n = a.pairs ? a.L / kGTile : 0;
+    return n < first ? first : n < last ? n : last;
+}
+
+// bit i: the wavefront's token i starts a sequence (token 0 of the row never does)
 template <class R>
 __device__ __forceinline__ uint32_t g_starts(const GArgs& a, const GPos& p, int64_t tile, const R& r) {
     if constexpr (!R::kSeq) return 0;
@@ -147,6 +208,7 @@ __device__ __forceinline__ uint32_t g_starts(const GArgs& a, const GPos& p, int6
     return static_cast<uint32_t>(m >> 1);
 }
 
+// tokens of the wavefront that the row has
 __device__ __forceinline__ int g_valid(const GArgs& a, const GPos& p, int64_t tile) {
     const int64_t n = a.L - (tile * kGTile + p.wave * kGT);
     return n < 0 ? 0 : n < kGT ? static_cast<int>(n) : kGT;
@@ -155,12 +217,14 @@ __device__ __forceinline__ int g_valid(const GArgs& a, const GPos& p, int64_t ti
 __device__ __forceinline__ GPos g_pos(const GArgs& a, int64_t row_group) {
     GPos p;
     p.lane = threadIdx.x & 63;
+    p.half = p.lane >> 5;
     p.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t groups = (a.C + 63) / 64;
     p.b = row_group / groups;
-    const int64_t c = (row_group % groups) * 64 + p.lane;
-    p.live = c < a.C;
-    p.c = p.live ? c : a.C - 1;
+    const int64_t c = (row_group % groups) * 64 + 2 * (p.lane & 31);
+    p.live = c + 1 < a.C || (c + 1 == a.C && p.half == 1);
+    p.c0 = c + 1 < a.C ? c : a.C > 1 ? a.C - 2 : 0;
+    p.c = a.C > 1 ? p.c0 + p.half : 0;
     return p;
 }
 
@@ -198,67 +262,131 @@ __device__ __forceinline__ float fold_segments(const GArgs& a, const GPos& p, fl
     return v;
 }
 
-// decays and input factors of the tile's tokens in this wavefront: past the row's end a = 1, i = 0
-template <class S, bool SIG, class R>
-__device__ __forceinline__ void g_gates(const R& r, int nv, float (&av)[kGT], float (&in)[kGT]) {
+// The lane's tokens of a tile: st, nv of its half of the wavefront's 16
+template <class S>
+struct GTile {
+    float av[kGL][2], in[kGL][2], uv[kGL][2];  // decays, input factors, inputs: past the end 1, 0, 0
+    uint32_t st;
+    int nv;
+    bool plain;  // all 16 tokens valid, none a start (uniform)
+};
+template <bool FULL, class S, bool SIG, class R>
+__device__ __forceinline__ void g_terms(const GArgs& a, const GPos& p, int64_t tile, const R& r, GTile<S>& q) {
+    const uint32_t st = g_starts(a, p, tile, r);
+    const int nv = FULL ? kGT : g_valid(a, p, tile);
+    q.plain = st == 0 && nv == kGT;
+    q.st = st >> (kGL * p.half) & ((1u << kGL) - 1);
+    q.nv = nv - kGL * p.half;
 #pragma unroll
-    for (int i = 0; i < kGT; ++i) gates<SIG>(S::load(r.g, i), av[i], in[i]);
-    if (nv < kGT) {
+    for (int i = 0; i < kGL; ++i)
 #pragma unroll
-        for (int i = 0; i < kGT; ++i)
-            if (i >= nv) {
-                av[i] = 1.0f;
-                in[i] = 0.0f;
+        for (int k = 0; k < 2; ++k) {
+            gates<SIG>(Two<S>::get(r.g[i], k), q.av[i][k], q.in[i][k]);
+            q.uv[i][k] = q.in[i][k] * Two<S>::get(r.x[i], k);
+        }
+    if (!FULL && nv < kGT) {
+#pragma unroll
+        for (int i = 0; i < kGL; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                q.av[i][k] = i < q.nv ? q.av[i][k] : 1.0f;
+                q.in[i][k] = i < q.nv ? q.in[i][k] : 0.0f;
+                q.uv[i][k] = i < q.nv ? q.uv[i][k] : 0.0f;
             }
     }
 }
-// inputs i x (x is finite or not: past the end 0)
-template <class S, class R>
-__device__ __forceinline__ void g_inputs(const R& r, int nv, const float (&in)[kGT], float (&uv)[kGT]) {
-#pragma unroll
-    for (int i = 0; i < kGT; ++i) uv[i] = in[i] * S::load(r.x, i);
-    if (nv < kGT) {
-#pragma unroll
-        for (int i = 0; i < kGT; ++i)
-            if (i >= nv) uv[i] = 0.0f;
-    }
+
+// Two channels of one half of the tokens against one channel of both halves: of a lane's values
+// v0, v1 of its two channels, the lower half of the wavefront takes the first channel's of both
+// halves, the upper the second's; the same step leads back.
+__device__ __forceinline__ void g_swap(float& v0, float& v1) {
+    const auto w = __builtin_amdgcn_permlane32_swap(__float_as_uint(v0), __float_as_uint(v1), false, false);
+    v0 = __uint_as_float(w[0]);
+    v1 = __uint_as_float(w[1]);
 }
 
-// (A, H) of the wavefront's tokens
-__device__ __forceinline__ float2 g_span(const float (&av)[kGT], const float (&uv)[kGT], uint32_t st) {
-    float A = av[0], H = uv[0];
-    if (st == 0) {
+// (A, H) of the two halves of the wavefront's tokens, of the lane's one channel
+template <class S>
+__device__ __forceinline__ void g_spans(const GTile<S>& q, float (&A)[2], float (&H)[2]) {
+    if (q.plain) {
 #pragma unroll
-        for (int i = 1; i < kGT; ++i) {
-            H = av[i] * H + uv[i];
-            A *= av[i];
+        for (int k = 0; k < 2; ++k) {
+            A[k] = q.av[0][k];
+            H[k] = q.uv[0][k];
+#pragma unroll
+            for (int i = 1; i < kGL; ++i) {
+                H[k] = q.av[i][k] * H[k] + q.uv[i][k];
+                A[k] *= q.av[i][k];
+            }
         }
     } else {
 #pragma unroll
-        for (int i = 1; i < kGT; ++i) H = (st >> i) & 1 ? uv[i] : av[i] * H + uv[i];
-        A = -1.0f;
-    }
-    return make_float2(A, H);
-}
-
-// E that the wavefront's tokens hand to the token before them, with E = 0 behind them
-template <class S, class R>
-__device__ __forceinline__ float g_back(const R& r, int nv, const float (&av)[kGT], uint32_t st) {
-    float e = 0.0f;
-    if (st == 0 && nv == kGT) {
+        for (int k = 0; k < 2; ++k) {
+            A[k] = 1.0f;
+            H[k] = 0.0f;
 #pragma unroll
-        for (int i = kGT - 1; i >= 0; --i) e = av[i] * (S::load(r.d, i) + e);
-    } else {
-#pragma unroll
-        for (int i = kGT - 1; i >= 0; --i) {
-            const float d = (i < nv ? S::load(r.d, i) : 0.0f) + e;
-            e = (st >> i) & 1 ? 0.0f : av[i] * d;
+            for (int i = 0; i < kGL; ++i) {
+                H[k] = (q.st >> i) & 1 ? q.uv[i][k] : q.av[i][k] * H[k] + q.uv[i][k];
+                A[k] *= q.av[i][k];
+            }
+            if (q.st) A[k] = -1.0f;
         }
     }
-    return e;
+    g_swap(A[0], A[1]);
+    g_swap(H[0], H[1]);
 }
 
-// whether any span of the tile is marked (uniform); A as stored by the 16 wavefronts
+// E that the two halves hand to the token before them, with E = 0 behind them
+template <class S, class R>
+__device__ __forceinline__ void g_backs(const R& r, const GTile<S>& q, float (&E)[2]) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        float e = 0.0f;
+        if (q.plain) {
+#pragma unroll
+            for (int i = kGL - 1; i >= 0; --i) e = q.av[i][k] * (Two<S>::get(r.d[i], k) + e);
+        } else {
+#pragma unroll
+            for (int i = kGL - 1; i >= 0; --i) {
+                const float d = (i < q.nv ? Two<S>::get(r.d[i], k) : 0.0f) + e;
+                e = (q.st >> i) & 1 ? 0.0f : q.av[i][k] * d;
+            }
+        }
+        E[k] = e;
+    }
+    g_swap(E[0], E[1]);
+}
+
+// the wavefront's (A, H) from its halves'
+template <bool SEQ>
+__device__ __forceinline__ float2 g_wave(const float (&A)[2], const float (&H)[2]) {
+    return make_float2(fold_mark<SEQ>(A[1], A[0]), fold<SEQ>(A[1], H[1], H[0]));
+}
+
+// stores the lane's tokens; FULL as for the loads
+template <bool FULL, class S>
+__device__ __forceinline__ void g_put(const GArgs& a, const GPos& p, void* base, int64_t tile, int64_t row, int nv,
+                                      const float (&v)[kGL][2]) {
+    using T = typename S::T;
+    const int64_t t0 = p.b * a.L + tile * kGTile + p.wave * kGT;
+    if constexpr (FULL) {
+        char* q = reinterpret_cast<char*>(static_cast<T*>(base) + t0 * row);
+        const uint32_t off = here(g_offset<S>(p, row));
+#pragma unroll
+        for (int i = 0; i < kGL; ++i, q += row * sizeof(T))
+            *reinterpret_cast<typename Two<S>::M*>(q + off) = Two<S>::round(v[i][0], v[i][1]);
+    } else {
+        T* q = static_cast<T*>(base) + (t0 + here(p.half * kGL)) * row + p.c0;
+#pragma unroll
+        for (int i = 0; i < kGL; ++i, q += row)
+            if (i < nv) {
+                S::store(q, 0, v[i][0]);
+                if (p.c0 + 1 < a.C) S::store(q, 1, v[i][1]);
+            }
+    }
+}
+
+// whether any span of the tile is marked (uniform); A as stored by the wavefronts
 template <bool SEQ>
 __device__ __forceinline__ bool g_marked(const float2 (&s)[kGW][64], int lane) {
     return SEQ && __ballot(s[lane % kGW][0].x < 0.0f) != 0;
@@ -276,8 +404,9 @@ __global__ void __launch_bounds__(kGThreads) gscan_fwd_kernel(GArgs a) {
     const GPos p = g_pos(a, blockIdx.x / nseg);
     const int64_t first = seg * a.seg_tiles;
     const int64_t last = first + a.seg_tiles < a.tiles ? first + a.seg_tiles : a.tiles;
-    GRaw<S, false, SEQ> cur;
-    g_load(a, p, first, cur);
+    const int64_t full = g_full(a, first, last);
+    GRaw<S, false, SEQ> cur, other;
+    if (full > first) g_load<true>(a, p, first, cur);
     float carry = 0.0f, P = 1.0f;
     if (AGG) {
         // final_state may be initial_state itself: the second kernel, whose last segment writes
@@ -292,50 +421,57 @@ __global__ void __launch_bounds__(kGThreads) gscan_fwd_kernel(GArgs a) {
         // wavefront 0 stores the final state
         asm volatile("" : "+v"(carry));
     }
-    auto step = [&](int64_t tile, const GRaw<S, false, SEQ>& cur, GRaw<S, false, SEQ>& nxt) __attribute__((always_inline)) {
-        g_load(a, p, tile + 1 < last ? tile + 1 : tile, nxt);
-        const int nv = g_valid(a, p, tile);
-        const uint32_t st = g_starts(a, p, tile, cur);
-        float av[kGT], uv[kGT];
-        g_gates<S, SIG>(cur, nv, av, uv);
-        g_inputs<S>(cur, nv, uv, uv);
+    auto step = [&](int64_t tile, const GRaw<S, false, SEQ>& cur, auto whole) __attribute__((always_inline)) {
+        constexpr bool FULL = decltype(whole)::value;
+        GTile<S> q;
+        g_terms<FULL, S, SIG>(a, p, tile, cur, q);
+        float A[2], H[2];
+        g_spans(q, A, H);
         float2(*s2)[64] = sp[tile & 1];
-        s2[p.wave][p.lane] = g_span(av, uv, st);
+        s2[p.wave][p.lane] = g_wave<SEQ>(A, H);
         __syncthreads();
-        float h = carry;
+        float h[2] = {carry, carry};  // before each half
         auto join = [&](auto marks) __attribute__((always_inline)) {
             constexpr bool M = decltype(marks)::value;
 #pragma unroll
             for (int w = 0; w < kGW; ++w) {
-                if (w == p.wave) h = carry;
+                if (w == p.wave) h[0] = carry;
                 const float2 s = s2[w][p.lane];
                 carry = fold<M>(s.x, s.y, carry);
                 if (AGG) P = fold_mark<M>(s.x, P);
             }
+            h[1] = fold<M>(A[0], H[0], h[0]);
         };
         if (g_marked<SEQ>(sp[tile & 1], p.lane) || (SEQ && AGG && P < 0.0f)) join(std::true_type{});
         else join(std::false_type{});
-        if (!AGG) {
-            using T = typename S::T;
-            char* y = reinterpret_cast<char*>(static_cast<T*>(a.y) + (p.b * a.L + tile * kGTile + p.wave * kGT) * a.y_row);
-            const uint32_t lb = here(static_cast<uint32_t>(p.c) * static_cast<uint32_t>(sizeof(T)));
-            auto out = [&](auto plain) __attribute__((always_inline)) {
-                constexpr bool PLAIN = decltype(plain)::value;  // all tokens valid, none a start
+        if constexpr (!AGG) {
+            g_swap(h[0], h[1]);
+            float hv[kGL][2];
+            if (q.plain) {
 #pragma unroll
-                for (int i = 0; i < kGT; ++i) {
-                    h = !PLAIN && (st >> i) & 1 ? uv[i] : av[i] * h + uv[i];
-                    if ((PLAIN || i < nv) && p.live) S::store(reinterpret_cast<T*>(y + lb), 0, h);
-                    y += a.y_row * sizeof(T);
-                }
-            };
-            if (st == 0 && nv == kGT) out(std::true_type{});
-            else out(std::false_type{});
+                for (int i = 0; i < kGL; ++i)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) hv[i][k] = h[k] = q.av[i][k] * h[k] + q.uv[i][k];
+            } else {
+#pragma unroll
+                for (int i = 0; i < kGL; ++i)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        hv[i][k] = h[k] = (q.st >> i) & 1 ? q.uv[i][k] : q.av[i][k] * h[k] + q.uv[i][k];
+            }
+            g_put<FULL, S>(a, p, a.y, tile, a.y_row, q.nv, hv);
         }
     };
-    GRaw<S, false, SEQ> other;
-    for (int64_t tile = first; tile < last; tile += 2) {
-        step(tile, cur, other);
-        if (tile + 1 < last) step(tile + 1, other, cur);
+    for (int64_t tile = first; tile < full; tile += 2) {
+        g_load<true>(a, p, tile + 1 < full ? tile + 1 : tile, other);
+        step(tile, cur, std::true_type{});
+        if (tile + 1 == full) break;
+        g_load<true>(a, p, tile + 2 < full ? tile + 2 : tile + 1, cur);
+        step(tile + 1, other, std::true_type{});
+    }
+    for (int64_t tile = full; tile < last; ++tile) {
+        g_load<false>(a, p, tile, cur);
+        step(tile, cur, std::false_type{});
     }
     if (p.wave != 0 || !p.live) return;
     if (AGG) {
@@ -360,24 +496,28 @@ __global__ void __launch_bounds__(kGThreads) gscan_bwd_states_kernel(GArgs a) {
     const GPos p = g_pos(a, blockIdx.x / a.nseg);
     const int64_t first = seg * a.seg_tiles;
     const int64_t last = first + a.seg_tiles < a.tiles ? first + a.seg_tiles : a.tiles;
-    GRaw<S, SEG, SEQ> cur;
-    g_load(a, p, first, cur);
+    const int64_t full = g_full(a, first, last);
+    GRaw<S, SEG, SEQ> cur, other;
+    if (full > first) g_load<true>(a, p, first, cur);
     float H = 0.0f, P = 1.0f, E = 0.0f;
-    auto step = [&](int64_t tile, const GRaw<S, SEG, SEQ>& cur, GRaw<S, SEG, SEQ>& nxt) __attribute__((always_inline)) {
-        g_load(a, p, tile + 1 < last ? tile + 1 : tile, nxt);
+    auto step = [&](int64_t tile, const GRaw<S, SEG, SEQ>& cur, auto whole) __attribute__((always_inline)) {
+        constexpr bool FULL = decltype(whole)::value;
+        GTile<S> q;
+        g_terms<FULL, S, SIG>(a, p, tile, cur, q);
         if (p.wave == 0 && p.live) {
             float* o = a.ckpt + (p.b * a.tiles + tile) * 2 * a.C + p.c;
             o[0] = P;
             o[a.C] = H;
         }
-        const int nv = g_valid(a, p, tile);
-        const uint32_t st = g_starts(a, p, tile, cur);
-        float av[kGT], uv[kGT];
-        g_gates<S, SIG>(cur, nv, av, uv);
-        g_inputs<S>(cur, nv, uv, uv);
+        float As[2], Hs[2];
+        g_spans(q, As, Hs);
         float2(*s2)[64] = sp[tile & 1];
-        s2[p.wave][p.lane] = g_span(av, uv, st);
-        if constexpr (SEG) se[tile & 1][p.wave][p.lane] = g_back<S>(cur, nv, av, st);
+        s2[p.wave][p.lane] = g_wave<SEQ>(As, Hs);
+        if constexpr (SEG) {
+            float Es[2];
+            g_backs<S>(cur, q, Es);
+            se[tile & 1][p.wave][p.lane] = fold<SEQ>(As[0], Es[0], Es[1]);
+        }
         __syncthreads();
         auto join = [&](auto marks) __attribute__((always_inline)) {
             constexpr bool M = decltype(marks)::value;
@@ -392,10 +532,16 @@ __global__ void __launch_bounds__(kGThreads) gscan_bwd_states_kernel(GArgs a) {
         if (g_marked<SEQ>(sp[tile & 1], p.lane) || (SEQ && P < 0.0f)) join(std::true_type{});
         else join(std::false_type{});
     };
-    GRaw<S, SEG, SEQ> other;
-    for (int64_t tile = first; tile < last; tile += 2) {
-        step(tile, cur, other);
-        if (tile + 1 < last) step(tile + 1, other, cur);
+    for (int64_t tile = first; tile < full; tile += 2) {
+        g_load<true>(a, p, tile + 1 < full ? tile + 1 : tile, other);
+        step(tile, cur, std::true_type{});
+        if (tile + 1 == full) break;
+        g_load<true>(a, p, tile + 2 < full ? tile + 2 : tile + 1, cur);
+        step(tile + 1, other, std::true_type{});
+    }
+    for (int64_t tile = full; tile < last; ++tile) {
+        g_load<false>(a, p, tile, cur);
+        step(tile, cur, std::false_type{});
     }
     if constexpr (SEG) {
         if (p.wave != 0 || !p.live) return;
@@ -415,8 +561,9 @@ __global__ void __launch_bounds__(kGThreads) gscan_bwd_kernel(GArgs a) {
     const GPos p = g_pos(a, blockIdx.x / a.nseg);
     const int64_t first = seg * a.seg_tiles;
     const int64_t last = first + a.seg_tiles < a.tiles ? first + a.seg_tiles : a.tiles;
-    GRaw<S, true, SEQ> cur;
-    g_load(a, p, last - 1, cur);
+    const int64_t full = g_full(a, first, last);
+    GRaw<S, true, SEQ> cur, other;
+    if (full > first && full == last) g_load<true>(a, p, full - 1, cur);
     float hseg = a.h0 ? a.h0[p.b * a.C + p.c] : 0.0f;
     float carry = a.dhT ? a.dhT[p.b * a.C + p.c] : 0.0f;
     if (a.nseg > 1) {
@@ -425,79 +572,93 @@ __global__ void __launch_bounds__(kGThreads) gscan_bwd_kernel(GArgs a) {
         __syncthreads();
     }
     using T = typename S::T;
-    auto step = [&](int64_t tile, const GRaw<S, true, SEQ>& cur, GRaw<S, true, SEQ>& nxt) __attribute__((always_inline)) {
+    // (A, H) of the segment's tokens before the tile
+    auto before_tile = [&](int64_t tile) __attribute__((always_inline)) {
         const float* ck = a.ckpt + (p.b * a.tiles + tile) * 2 * a.C + p.c;
-        const float cA = ck[0], cH = ck[a.C];
-        g_load(a, p, tile > first ? tile - 1 : tile, nxt);
-        const int nv = g_valid(a, p, tile);
-        const uint32_t st = g_starts(a, p, tile, cur);
-        float av[kGT], in[kGT], uv[kGT];
-        g_gates<S, SIG>(cur, nv, av, in);
-        g_inputs<S>(cur, nv, in, uv);
+        return make_float2(ck[0], ck[a.C]);
+    };
+    auto step = [&](int64_t tile, const GRaw<S, true, SEQ>& cur, float2 ck, auto whole) __attribute__((always_inline)) {
+        constexpr bool FULL = decltype(whole)::value;
+        GTile<S> q;
+        g_terms<FULL, S, SIG>(a, p, tile, cur, q);
+        float As[2], Hs[2], Es[2];
+        g_spans(q, As, Hs);
+        g_backs<S>(cur, q, Es);
         float2(*s2)[64] = sp[tile & 1];
         float(*s1)[64] = se[tile & 1];
-        s2[p.wave][p.lane] = g_span(av, uv, st);
-        s1[p.wave][p.lane] = g_back<S>(cur, nv, av, st);
+        s2[p.wave][p.lane] = g_wave<SEQ>(As, Hs);
+        s1[p.wave][p.lane] = fold<SEQ>(As[0], Es[0], Es[1]);
         __syncthreads();
-        float h = fold<true>(cA, cH, hseg), E = 0.0f;
+        float h[2] = {fold<true>(ck.x, ck.y, hseg), 0.0f}, E[2];  // before and behind each half
         auto join = [&](auto marks) __attribute__((always_inline)) {
             constexpr bool M = decltype(marks)::value;
-            // all 16 spans are read at once: a branch around those that do not count would wait
-            // for one LDS read after the other
-            float A[kGW], t = h;
+            // all spans are read at once: a branch around those that do not count would wait for
+            // one LDS read after the other
+            float A[kGW], t = h[0];
 #pragma unroll
             for (int w = 0; w < kGW; ++w) {
                 const float2 s = s2[w][p.lane];
                 A[w] = s.x;
-                if (w == p.wave) h = t;
+                if (w == p.wave) h[0] = t;
                 t = fold<M>(s.x, s.y, t);
             }
+            E[1] = carry;
 #pragma unroll
             for (int w = kGW - 1; w >= 0; --w) {
-                if (w == p.wave) E = carry;
+                if (w == p.wave) E[1] = carry;
                 carry = fold<M>(A[w], s1[w][p.lane], carry);
             }
+            h[1] = fold<M>(As[0], Hs[0], h[0]);
+            E[0] = fold<M>(As[1], Es[1], E[1]);
         };
         if (g_marked<SEQ>(sp[tile & 1], p.lane)) join(std::true_type{});
         else join(std::false_type{});
-        const int64_t t0 = p.b * a.L + tile * kGTile + p.wave * kGT;
-        char* dx = reinterpret_cast<char*>(static_cast<T*>(a.dx) + t0 * a.dx_row);
-        char* dg = reinterpret_cast<char*>(static_cast<T*>(a.dgate) + t0 * a.dgate_row);
-        const uint32_t lb = here(static_cast<uint32_t>(p.c) * static_cast<uint32_t>(sizeof(T)));
-        auto out = [&](auto plain) __attribute__((always_inline)) {
-            constexpr bool PLAIN = decltype(plain)::value;  // all tokens valid, none a start
-            float before[kGT];                              // h_{t-1}, 0 at a start
+        g_swap(h[0], h[1]);
+        g_swap(E[0], E[1]);
+        float dx[kGL][2], dg[kGL][2];
+        auto grads = [&](auto starts) __attribute__((always_inline)) {
+            constexpr bool ST = decltype(starts)::value;
+            float before[kGL][2];  // h_{t-1}, not used at a start
 #pragma unroll
-            for (int i = 0; i < kGT; ++i) {
-                const bool s = !PLAIN && (st >> i) & 1;
-                before[i] = s ? 0.0f : h;
-                h = s ? uv[i] : av[i] * h + uv[i];
-            }
+            for (int i = 0; i < kGL; ++i)
 #pragma unroll
-            for (int i = kGT - 1; i >= 0; --i) {
-                if (PLAIN || i < nv) {
-                    const bool s = !PLAIN && (st >> i) & 1;
-                    const float D = S::load(cur.d, i) + E, aD = av[i] * D;
-                    float dlog = s ? 0.0f : aD * before[i], dxv = D;
-                    if constexpr (SIG) {
-                        dxv = D * in[i];
-                        dlog = in[i] * dlog - aD * uv[i];
-                    }
-                    if (p.live) {
-                        S::store(reinterpret_cast<T*>(dx + i * a.dx_row * sizeof(T) + lb), 0, dxv);
-                        S::store(reinterpret_cast<T*>(dg + i * a.dgate_row * sizeof(T) + lb), 0, dlog);
-                    }
-                    E = s ? 0.0f : aD;
+                for (int k = 0; k < 2; ++k) {
+                    before[i][k] = h[k];
+                    h[k] = ST && (q.st >> i) & 1 ? q.uv[i][k] : q.av[i][k] * h[k] + q.uv[i][k];
                 }
-            }
+#pragma unroll
+            for (int i = kGL - 1; i >= 0; --i)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const bool start = ST && (q.st >> i) & 1, off = !FULL && i >= q.nv;
+                    const float D = (off ? 0.0f : Two<S>::get(cur.d[i], k)) + E[k], aD = q.av[i][k] * D;
+                    dx[i][k] = D;
+                    dg[i][k] = start ? 0.0f : aD * before[i][k];
+                    if constexpr (SIG) {
+                        dx[i][k] = D * q.in[i][k];
+                        dg[i][k] = q.in[i][k] * dg[i][k] - aD * q.uv[i][k];
+                    }
+                    E[k] = start ? 0.0f : aD;
+                }
         };
-        if (st == 0 && nv == kGT) out(std::true_type{});
-        else out(std::false_type{});
+        if (SEQ && !q.plain) grads(std::true_type{});
+        else grads(std::false_type{});
+        g_put<FULL, S>(a, p, a.dx, tile, a.dx_row, q.nv, dx);
+        g_put<FULL, S>(a, p, a.dgate, tile, a.dgate_row, q.nv, dg);
     };
-    GRaw<S, true, SEQ> other;
-    for (int64_t tile = last - 1; tile >= first; tile -= 2) {
-        step(tile, cur, other);
-        if (tile > first) step(tile - 1, other, cur);
+    for (int64_t tile = last - 1; tile >= full; --tile) {
+        g_load<false>(a, p, tile, cur);
+        step(tile, cur, before_tile(tile), std::false_type{});
+    }
+    if (full > first && full < last) g_load<true>(a, p, full - 1, cur);
+    for (int64_t tile = full - 1; tile >= first; tile -= 2) {
+        float2 ck = before_tile(tile);
+        g_load<true>(a, p, tile > first ? tile - 1 : tile, other);
+        step(tile, cur, ck, std::true_type{});
+        if (tile == first) break;
+        ck = before_tile(tile - 1);
+        g_load<true>(a, p, tile - 1 > first ? tile - 2 : tile - 1, cur);
+        step(tile - 1, other, ck, std::true_type{});
     }
     if (seg == 0 && p.wave == 0 && p.live && a.dh0) a.dh0[p.b * a.C + p.c] = carry;
 }
@@ -548,7 +709,9 @@ __global__ void __launch_bounds__(256) gscan_step_kernel(GArgs a, float* pool, c
 }
 
 // Cut along the row: as many segments as bring the grid to kFill blocks, none of fewer than
-// kLeast tiles.
+// kLeast tiles.  The size above in 256 blocks takes 198 us forward and 325 + 161 backward; cut
+// once more, for 512, the first kernel's second reading costs more than it gives (346 + 249
+// backward; the long row 72 + 40 us against 66 + 37).  kLeast 2 or 8 measured as 4.
 constexpr int64_t kFill = 256, kLeast = 4;
 void g_cut(GArgs& a) {
     const int64_t blocks = a.B * ((a.C + 63) / 64);
@@ -567,6 +730,11 @@ GArgs g_args(const GscanCall& c) {
     a.dx_row = c.dx_row; a.dgate_row = c.dgate_row;
     a.h0 = c.h0; a.dhT = c.dhT; a.final_state = c.final_state; a.dh0 = c.dh0; a.seq = c.seq;
     a.B = c.B; a.L = c.L; a.C = c.C;
+    // a lane's tokens start up to 8 rows behind the wavefront's first: 2^31 bytes of 4-byte
+    // elements at 2^26 a row
+    a.pairs = c.C > 1;
+    for (const int64_t row : {a.x_row, a.gate_row, a.dy_row, a.y_row, a.dx_row, a.dgate_row})
+        if (row >= int64_t{1} << 26) a.pairs = false;
     return a;
 }
 
