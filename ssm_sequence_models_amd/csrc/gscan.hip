@@ -709,14 +709,22 @@ __global__ void __launch_bounds__(256) gscan_step_kernel(GArgs a, float* pool, c
 }
 
 // Cut along the row: as many segments as bring the grid to kFill blocks, none of fewer than
-// kLeast tiles.  The size above in 256 blocks takes 198 us forward and 325 + 161 backward; cut
-// once more, for 512, the first kernel's second reading costs more than it gives (346 + 249
-// backward; the long row 72 + 40 us against 66 + 37).  kLeast 2 or 8 measured as 4.
-constexpr int64_t kFill = 256, kLeast = 4;
-void g_cut(GArgs& a) {
+// kLeast tiles.  The forward's first kernel reads everything once more, so it is cut only where
+// fewer than kFill / 2 blocks would run, and on more than kWhole tiles; the backward needs two
+// walks in any case.  bf16, sigmoid form, forward / backward in us, cut to 256 blocks against
+// other numbers:
+//   1 x 8192 x 4096   53 / 98     to 128 blocks: 80 / 138
+//   2 x 8192 x 4096  115 / 220    left at 128 blocks: 110 / 278
+//   8 x 2048 x 1024   29 / 47     left at 128 blocks: 23 / 60
+//   4 x 8192 x 4096  171 / 398    (256 blocks as it is) cut to 512: 237 / 473
+//   1 x 4096 x 1024   19 / 24     segments of 8 tiles: 25 / 37
+//   1 x 1024 x 1024   20 / 22     one segment of 8 tiles: 15 / 31
+constexpr int64_t kFill = 256, kLeast = 4, kWhole = 8;
+void g_cut(GArgs& a, bool bwd) {
     const int64_t blocks = a.B * ((a.C + 63) / 64);
     a.tiles = (a.L + kGTile - 1) / kGTile;
     int64_t want = (kFill + blocks - 1) / blocks;
+    if (!bwd && (2 * blocks >= kFill || a.tiles <= kWhole)) want = 1;
     const int64_t most = a.tiles / kLeast > 1 ? a.tiles / kLeast : 1;
     if (want > most) want = most;
     a.seg_tiles = (a.tiles + want - 1) / want;
@@ -782,21 +790,21 @@ hipError_t step_typed(const GArgs& a, float* pool, const int32_t* slots, int64_t
 int64_t gscan_blocks(int64_t B, int64_t L, int64_t C) {
     GArgs a{};
     a.B = B; a.L = L; a.C = C;
-    g_cut(a);
+    g_cut(a, true);  // the forward has at most as many segments
     return B * ((C + 63) / 64) * a.nseg;
 }
 
 size_t gscan_workspace_bytes(int64_t B, int64_t L, int64_t C, bool bwd) {
     GArgs a{};
     a.B = B; a.L = L; a.C = C;
-    g_cut(a);
+    g_cut(a, bwd);
     const int64_t seg = a.nseg > 1 ? B * a.nseg * 3 * C : 0;
     return static_cast<size_t>(seg + (bwd ? B * a.tiles * 2 * C : 0)) * 4;
 }
 
 hipError_t launch_gscan_fwd(const GscanCall& c, hipStream_t s) {
     GArgs a = g_args(c);
-    g_cut(a);
+    g_cut(a, false);
     a.seg = static_cast<float*>(c.workspace);
     return g_dispatch(c, [&](auto S, auto sig, auto seq) {
         return fwd_typed<decltype(S), decltype(sig)::value, decltype(seq)::value>(a, s);
@@ -805,7 +813,7 @@ hipError_t launch_gscan_fwd(const GscanCall& c, hipStream_t s) {
 
 hipError_t launch_gscan_bwd(const GscanCall& c, hipStream_t s) {
     GArgs a = g_args(c);
-    g_cut(a);
+    g_cut(a, true);
     a.ckpt = static_cast<float*>(c.workspace);
     a.seg = a.ckpt + a.B * a.tiles * 2 * a.C;
     return g_dispatch(c, [&](auto S, auto sig, auto seq) {

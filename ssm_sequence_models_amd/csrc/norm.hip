@@ -9,7 +9,7 @@
 // Both directions are bound by memory: every element is read once and written once, so a team
 // of threads keeps its row's piece in registers from the load to the store, and the statistics
 // (two steps for the layer norm: the mean, then the centred squares) are reductions over
-// registers.  A team is one wavefront for m <= 512 (four teams a block, no barrier) and one
+// registers.  A team is one wavefront for m <= 1024 (four teams a block, no barrier) and one
 // block above.  A team keeps its group and its columns while it walks over rows, so the
 // weights are read once and the sums of dw and db stay in registers; each block writes one
 // partial row, and a second kernel adds the partial rows in a fixed order in double
@@ -61,13 +61,20 @@ __device__ __forceinline__ float sigmoidf(float z) {
     return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
 }
 
-// VEC consecutive elements; 16-byte accesses for VEC = 8 (the host has checked alignment)
-template <class S, int VEC>
-__device__ __forceinline__ void load_vec(const typename S::T* p, float (&v)[VEC]) {
-    if constexpr (VEC == 1) {
-        v[0] = S::load(p, 0);
+// Eight consecutive elements, 16 bytes an access at any element's alignment.  TAIL: of the last
+// eight of a group only n exist; the others are 0 and not stored.
+constexpr int kVec = 8;
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+
+template <class S, bool TAIL>
+__device__ __forceinline__ void load_vec(const typename S::T* p, float (&v)[kVec], int n) {
+    if (TAIL && n < kVec) {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+            if (i < n) v[i] = S::load(p, i);
     } else if constexpr (S::kBytes == 2) {
-        const u32x4_t q = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p));
+        const u32x4_t q = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             v[2 * i] = __uint_as_float(q[i] << 16);
@@ -76,33 +83,35 @@ __device__ __forceinline__ void load_vec(const typename S::T* p, float (&v)[VEC]
     } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const f32x4_t q = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(p) + h);
+            const f32x4_t q = __builtin_nontemporal_load(reinterpret_cast<const f32x4_any*>(p) + h);
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[4 * h + i] = q[i];
         }
     }
 }
-template <class S, int VEC>
-__device__ __forceinline__ void store_vec(typename S::T* p, const float (&v)[VEC]) {
-    if constexpr (VEC == 1) {
-        S::store(p, 0, v[0]);
+template <class S, bool TAIL>
+__device__ __forceinline__ void store_vec(typename S::T* p, const float (&v)[kVec], int n) {
+    if (TAIL && n < kVec) {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+            if (i < n) S::store(p, i, v[i]);
     } else if constexpr (S::kBytes == 2) {
         u32x4_t q;
 #pragma unroll
         for (int i = 0; i < 4; ++i) q[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-        __builtin_nontemporal_store(q, reinterpret_cast<u32x4_t*>(p));
+        __builtin_nontemporal_store(q, reinterpret_cast<u32x4_any*>(p));
     } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
             __builtin_nontemporal_store(f32x4_t{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]},
-                                        reinterpret_cast<f32x4_t*>(p) + h);
+                                        reinterpret_cast<f32x4_any*>(p) + h);
     }
 }
 
 enum { kGateNone = 0, kGateBefore = 1, kGateAfter = 2 };
 
-// Thread `tid` of a team of TPR holds, for j < NV, the VEC columns from (j TPR + tid) VEC.
-template <class S, int VEC, int NV, int TPR, int GATE>
+// Thread `tid` of a team of TPR holds, for j < NV, the 8 columns from 8 (j TPR + tid).
+template <class S, bool TAIL, int NV, int TPR, int GATE>
 __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_fwd_kernel(NormArgs a) {
     using T = typename S::T;
     __shared__ float red[3][16];
@@ -111,13 +120,13 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_fwd_kernel(NormArg
     const int64_t g = blockIdx.x % a.groups, blk = blockIdx.x / a.groups;
     const int m = a.m;
     const int64_t c0 = g * m;
-    float w[NV][VEC], b[NV][VEC];
+    float w[NV][kVec], b[NV][kVec];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int c = (j * TPR + tid) * VEC;
+        const int c = (j * TPR + tid) * kVec;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const bool in = c < m;
+        for (int e = 0; e < kVec; ++e) {
+            const bool in = c + (TAIL ? e : 0) < m;
             w[j][e] = in ? (a.w ? a.w[c0 + c + e] : 1.0f) : 0.0f;
             b[j][e] = in && a.b ? a.b[c0 + c + e] : 0.0f;
         }
@@ -127,22 +136,22 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_fwd_kernel(NormArg
     for (int64_t r = blk * TEAMS + team; r < a.rows; r += a.nb * TEAMS) {
         const T* xr = static_cast<const T*>(a.x) + r * a.x_row + c0;
         const T* zr = GATE != kGateNone ? static_cast<const T*>(a.z) + r * a.z_row + c0 : nullptr;
-        float u[NV][VEC], z[NV][VEC];
+        float u[NV][kVec], z[NV][kVec];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * TPR + tid) * VEC;
+            const int c = (j * TPR + tid) * kVec;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) u[j][e] = z[j][e] = 0.0f;
+            for (int e = 0; e < kVec; ++e) u[j][e] = z[j][e] = 0.0f;
             if (c < m) {
-                load_vec<S, VEC>(xr + c, u[j]);
-                if constexpr (GATE != kGateNone) load_vec<S, VEC>(zr + c, z[j]);
+                load_vec<S, TAIL>(xr + c, u[j], m - c);
+                if constexpr (GATE != kGateNone) load_vec<S, TAIL>(zr + c, z[j], m - c);
             }
         }
         float mean = 0.0f, q = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
+            for (int e = 0; e < kVec; ++e) {
                 if constexpr (GATE == kGateBefore) u[j][e] *= z[j][e] * sigmoidf(z[j][e]);
                 mean += u[j][e];
             }
@@ -155,8 +164,8 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_fwd_kernel(NormArg
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float d = (j * TPR + tid) * VEC < m ? u[j][e] - mean : 0.0f;
+            for (int e = 0; e < kVec; ++e) {
+                const float d = (j * TPR + tid) * kVec + (TAIL ? e : 0) < m ? u[j][e] - mean : 0.0f;
                 u[j][e] = d;
                 q += d * d;
             }
@@ -166,35 +175,35 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_fwd_kernel(NormArg
         T* out = static_cast<T*>(a.out) + r * a.out_row + c0;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * TPR + tid) * VEC;
-            float o[VEC];
+            const int c = (j * TPR + tid) * kVec;
+            float o[kVec];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
+            for (int e = 0; e < kVec; ++e) {
                 o[e] = u[j][e] * rstd * w[j][e] + b[j][e];
                 if constexpr (GATE == kGateAfter) o[e] *= z[j][e] * sigmoidf(z[j][e]);
             }
-            if (c < m) store_vec<S, VEC>(out + c, o);
+            if (c < m) store_vec<S, TAIL>(out + c, o, m - c);
         }
     }
 }
 
-template <class S, int VEC, int NV, int TPR, int GATE>
+template <class S, bool TAIL, int NV, int TPR, int GATE>
 __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_bwd_kernel(NormArgs a) {
     using T = typename S::T;
     __shared__ float red[3][16];
     constexpr int TEAMS = TPR == 64 ? 4 : 1;
-    __shared__ float join[TEAMS == 4 ? 4 : 1][TEAMS == 4 ? 64 * VEC * NV : 1];
+    __shared__ float join[TEAMS == 4 ? 4 : 1][TEAMS == 4 ? 64 * kVec * NV : 1];
     const int tid = threadIdx.x % TPR, team = threadIdx.x / TPR;
     const int64_t g = blockIdx.x % a.groups, blk = blockIdx.x / a.groups;
     const int m = a.m;
     const int64_t c0 = g * m;
-    float w[NV][VEC], b[NV][VEC], dw[NV][VEC], db[NV][VEC];
+    float w[NV][kVec], b[NV][kVec], dw[NV][kVec], db[NV][kVec];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int c = (j * TPR + tid) * VEC;
+        const int c = (j * TPR + tid) * kVec;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const bool in = c < m;
+        for (int e = 0; e < kVec; ++e) {
+            const bool in = c + (TAIL ? e : 0) < m;
             w[j][e] = in ? (a.w ? a.w[c0 + c + e] : 1.0f) : 0.0f;
             b[j][e] = GATE == kGateAfter && in && a.b ? a.b[c0 + c + e] : 0.0f;
             dw[j][e] = db[j][e] = 0.0f;
@@ -206,23 +215,23 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_bwd_kernel(NormArg
         const T* xr = static_cast<const T*>(a.x) + r * a.x_row + c0;
         const T* zr = GATE != kGateNone ? static_cast<const T*>(a.z) + r * a.z_row + c0 : nullptr;
         const T* dr = static_cast<const T*>(a.dout) + r * a.dout_row + c0;
-        float x[NV][VEC], z[NV][VEC], d[NV][VEC], n[NV][VEC];
+        float x[NV][kVec], z[NV][kVec], d[NV][kVec], n[NV][kVec];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * TPR + tid) * VEC;
+            const int c = (j * TPR + tid) * kVec;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) x[j][e] = z[j][e] = d[j][e] = 0.0f;
+            for (int e = 0; e < kVec; ++e) x[j][e] = z[j][e] = d[j][e] = 0.0f;
             if (c < m) {
-                load_vec<S, VEC>(xr + c, x[j]);
-                if constexpr (GATE != kGateNone) load_vec<S, VEC>(zr + c, z[j]);
-                load_vec<S, VEC>(dr + c, d[j]);
+                load_vec<S, TAIL>(xr + c, x[j], m - c);
+                if constexpr (GATE != kGateNone) load_vec<S, TAIL>(zr + c, z[j], m - c);
+                load_vec<S, TAIL>(dr + c, d[j], m - c);
             }
         }
         float mean = 0.0f, q = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
+            for (int e = 0; e < kVec; ++e) {
                 n[j][e] = x[j][e];
                 if constexpr (GATE == kGateBefore) n[j][e] *= z[j][e] * sigmoidf(z[j][e]);
                 mean += n[j][e];
@@ -236,8 +245,8 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_bwd_kernel(NormArg
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float v = (j * TPR + tid) * VEC < m ? n[j][e] - mean : 0.0f;
+            for (int e = 0; e < kVec; ++e) {
+                const float v = (j * TPR + tid) * kVec + (TAIL ? e : 0) < m ? n[j][e] - mean : 0.0f;
                 n[j][e] = v;
                 q += v * v;
             }
@@ -248,9 +257,9 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_bwd_kernel(NormArg
         float c1 = 0.0f, c2 = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            float dzv[VEC];
+            float dzv[kVec];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
+            for (int e = 0; e < kVec; ++e) {
                 n[j][e] *= rstd;
                 float dp = d[j][e];
                 if constexpr (GATE == kGateAfter) {
@@ -266,8 +275,8 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_bwd_kernel(NormArg
                 c2 += d[j][e];
             }
             if constexpr (GATE == kGateAfter) {
-                const int c = (j * TPR + tid) * VEC;
-                if (c < m && a.want_dz) store_vec<S, VEC>(dzr + c, dzv);
+                const int c = (j * TPR + tid) * kVec;
+                if (c < m && a.want_dz) store_vec<S, TAIL>(dzr + c, dzv, m - c);
             }
         }
         c1 = team_sum<TPR>(c1, red, slot) * inv_m;
@@ -281,10 +290,10 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_bwd_kernel(NormArg
         T* dxr = static_cast<T*>(a.dx) + r * a.dx_row + c0;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * TPR + tid) * VEC;
-            float dxv[VEC], dzv[VEC];
+            const int c = (j * TPR + tid) * kVec;
+            float dxv[kVec], dzv[kVec];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
+            for (int e = 0; e < kVec; ++e) {
                 const float du = rstd * (d[j][e] - n[j][e] * c1 - c2);
                 dxv[e] = du;
                 if constexpr (GATE == kGateBefore) {
@@ -294,9 +303,9 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_bwd_kernel(NormArg
                 }
             }
             if (c < m) {
-                store_vec<S, VEC>(dxr + c, dxv);
+                store_vec<S, TAIL>(dxr + c, dxv, m - c);
                 if constexpr (GATE == kGateBefore)
-                    if (a.want_dz) store_vec<S, VEC>(dzr + c, dzv);
+                    if (a.want_dz) store_vec<S, TAIL>(dzr + c, dzv, m - c);
             }
         }
     }
@@ -309,18 +318,19 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_bwd_kernel(NormArg
 #pragma unroll
             for (int j = 0; j < NV; ++j)
 #pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    join[team][(j * 64 + tid) * VEC + e] = k == 0 ? dw[j][e] : db[j][e];
+                for (int e = 0; e < kVec; ++e)
+                    join[team][(j * 64 + tid) * kVec + e] = k == 0 ? dw[j][e] : db[j][e];
             __syncthreads();
             for (int c = threadIdx.x; c < m; c += 256)
                 out[c] = (join[0][c] + join[1][c]) + (join[2][c] + join[3][c]);
         } else {
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const int c = (j * TPR + tid) * VEC;
+                const int c = (j * TPR + tid) * kVec;
                 if (c < m) {
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) out[c + e] = k == 0 ? dw[j][e] : db[j][e];
+                    for (int e = 0; e < kVec; ++e)
+                        if (!TAIL || c + e < m) out[c + e] = k == 0 ? dw[j][e] : db[j][e];
                 }
             }
         }
@@ -356,21 +366,22 @@ __global__ void norm_zero_kernel(float* dw, float* db, int64_t n) {
     if (db) db[i] = 0.0f;
 }
 
-// blocks a group: enough to fill the GPU (1024 blocks of 256 threads; four wavefront teams a
-// block for m <= 512), never more than there are rows for
+// Blocks a group: 1024 in all (four wavefront teams a block for m <= 1024), never more than
+// there are rows for.  At the size above with m = 512, forward / backward: 142 / 257 us; 512
+// blocks 173 / 269, 2048 blocks 153 / 251 (m = 4096: 146 / 260, 185 / 258, 147 / 267).
 int64_t norm_blocks(int64_t rows, int64_t m, int64_t groups) {
-    const int64_t per = m <= 512 ? 4 : 1;
+    const int64_t per = m <= 1024 ? 4 : 1;
     const int64_t need = (rows + per - 1) / per;
     const int64_t most = groups >= 1024 ? 1 : 1024 / groups;
     return need < most ? need : most;
 }
 
-template <class S, int VEC, int NV, int TPR>
+template <class S, bool TAIL, int NV, int TPR>
 void launch_one(const NormArgs& a, int gate, bool bwd, hipStream_t s) {
     const dim3 grid(static_cast<uint32_t>(a.nb * a.groups)), block(TPR > 256 ? TPR : 256);
 #define SSM_NORM(G)                                                                    \
-    (bwd ? norm_bwd_kernel<S, VEC, NV, TPR, G><<<grid, block, 0, s>>>(a)               \
-         : norm_fwd_kernel<S, VEC, NV, TPR, G><<<grid, block, 0, s>>>(a))
+    (bwd ? norm_bwd_kernel<S, TAIL, NV, TPR, G><<<grid, block, 0, s>>>(a)               \
+         : norm_fwd_kernel<S, TAIL, NV, TPR, G><<<grid, block, 0, s>>>(a))
     if (gate == kGateNone)
         SSM_NORM(kGateNone);
     else if (gate == kGateBefore)
@@ -380,26 +391,27 @@ void launch_one(const NormArgs& a, int gate, bool bwd, hipStream_t s) {
 #undef SSM_NORM
 }
 
-template <class S>
-void launch_typed(const NormArgs& a, int gate, bool bwd, bool vec, hipStream_t s) {
+// Teams by the group's width m, bf16 with a gate at 32768 rows x 4096 channels (16384 x 8192),
+// forward / backward in us (the same bytes: the floor is 130 / 217):
+//   m = 512   one wavefront, one vector a lane 142 / 257    four wavefronts 344 / 546
+//   m = 1024  one wavefront, two vectors 138 / 251          four wavefronts, half idle, 205 / 312
+//   m = 4096  four wavefronts, two vectors 146 / 260        eight, one vector 149 / 235
+//   m = 8192  16 wavefronts, one vector 138 / 279           eight, two vectors 151 / 350
+template <class S, bool TAIL>
+void launch_typed(const NormArgs& a, int gate, bool bwd, hipStream_t s) {
     const int m = a.m;
-    if (vec) {
-        if (m <= 512) launch_one<S, 8, 1, 64>(a, gate, bwd, s);
-        else if (m <= 2048) launch_one<S, 8, 1, 256>(a, gate, bwd, s);
-        else if (m <= 4096) launch_one<S, 8, 2, 256>(a, gate, bwd, s);
-        else if (m <= 8192) launch_one<S, 8, 2, 512>(a, gate, bwd, s);
-        else launch_one<S, 8, 2, 1024>(a, gate, bwd, s);
-    } else {
-        if (m <= 512) launch_one<S, 1, 8, 64>(a, gate, bwd, s);
-        else if (m <= 2048) launch_one<S, 1, 8, 256>(a, gate, bwd, s);
-        else if (m <= 8192) launch_one<S, 1, 16, 512>(a, gate, bwd, s);
-        else launch_one<S, 1, 16, 1024>(a, gate, bwd, s);
-    }
+    if (m <= 512) launch_one<S, TAIL, 1, 64>(a, gate, bwd, s);
+    else if (m <= 1024) launch_one<S, TAIL, 2, 64>(a, gate, bwd, s);
+    else if (m <= 2048) launch_one<S, TAIL, 1, 256>(a, gate, bwd, s);
+    else if (m <= 4096 && !bwd) launch_one<S, TAIL, 2, 256>(a, gate, bwd, s);
+    else if (m <= 4096) launch_one<S, TAIL, 1, 512>(a, gate, bwd, s);
+    else if (m <= 8192) launch_one<S, TAIL, 1, 1024>(a, gate, bwd, s);
+    else launch_one<S, TAIL, 2, 1024>(a, gate, bwd, s);
 }
-
-// 8-element accesses: 16-byte aligned rows (bf16: row strides of 8 elements, fp32: of 4)
-bool vec_ok(const void* p, int64_t row, int es) {
-    return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && row * es % 16 == 0);
+void launch_norm(const NormArgs& a, ssm_dtype_t dtype, int gate, bool bwd, hipStream_t s) {
+    const bool tail = a.m % kVec != 0;
+    if (dtype == SSM_BF16) tail ? launch_typed<BF16, true>(a, gate, bwd, s) : launch_typed<BF16, false>(a, gate, bwd, s);
+    else tail ? launch_typed<F32, true>(a, gate, bwd, s) : launch_typed<F32, false>(a, gate, bwd, s);
 }
 
 }  // namespace
@@ -416,12 +428,8 @@ hipError_t launch_norm_fwd(const NormCall& c, hipStream_t s) {
     a.m = static_cast<int>(c.channels / c.groups);
     a.nb = norm_blocks(c.rows, a.m, c.groups);
     a.eps = c.eps; a.layer = c.layer;
-    const int es = c.dtype == SSM_BF16 ? 2 : 4;
-    const bool vec = a.m % 8 == 0 && vec_ok(c.x, c.x_row, es) && vec_ok(c.z, c.z_row, es) &&
-                     vec_ok(c.out, c.out_row, es);
     const int gate = c.z == nullptr ? kGateNone : c.gate_after ? kGateAfter : kGateBefore;
-    if (c.dtype == SSM_BF16) launch_typed<BF16>(a, gate, false, vec, s);
-    else launch_typed<F32>(a, gate, false, vec, s);
+    launch_norm(a, c.dtype, gate, false, s);
     return hipGetLastError();
 }
 
@@ -441,13 +449,8 @@ hipError_t launch_norm_bwd(const NormCall& c, hipStream_t s) {
     a.want_dz = c.dz != nullptr;
     a.want_db = c.db != nullptr;
     a.part = c.dw || c.db ? static_cast<float*>(c.workspace) : nullptr;
-    const int es = c.dtype == SSM_BF16 ? 2 : 4;
-    const bool vec = a.m % 8 == 0 && vec_ok(c.x, c.x_row, es) && vec_ok(c.z, c.z_row, es) &&
-                     vec_ok(c.dout, c.dout_row, es) && vec_ok(c.dx, c.dx_row, es) &&
-                     vec_ok(c.dz, c.dz_row, es);
     const int gate = c.z == nullptr ? kGateNone : c.gate_after ? kGateAfter : kGateBefore;
-    if (c.dtype == SSM_BF16) launch_typed<BF16>(a, gate, true, vec, s);
-    else launch_typed<F32>(a, gate, true, vec, s);
+    launch_norm(a, c.dtype, gate, true, s);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.part == nullptr) return e;
     const dim3 grid(static_cast<uint32_t>((c.channels + 63) / 64), c.db ? 2 : 1);

@@ -1001,7 +1001,8 @@ size_t r256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Ranges of heads a chunk and group: one block runs on a unit at a time (LDS), so the time is
 // the rounds of blocks over the 256 units times what a block does: its heads, and about two
-// heads' worth of B, C and the pairs' end.
+// heads' worth of B, C and the pairs' end.  Against one range, dstate 128: 1 x 8192 x 64 heads
+// 406 for 625 us, 2 x 8192 x 48 581 for 689, 2 x 2048 x 64 190 for 480.
 void cut_heads(ScanBwdArgs& a) {
     const int64_t blocks = a.B * a.chunks * a.G, k = a.H / a.G;
     int64_t best = -1;
@@ -1051,7 +1052,11 @@ template <int N>
 hipError_t launch_typed(const ScanBwdArgs& a, hipStream_t s) {
     const int64_t bh = a.B * a.H;
     sbf_decay_kernel<<<static_cast<uint32_t>(a.B * a.chunks * ((a.H + 15) / 16)), 256, 0, s>>>(a);
-    if (2 * bh >= 256 || a.chunks == 1) {
+    // Walking over the chunks reads nothing twice but runs 2 B H blocks; else one block a chunk
+    // and a pass over their shares (us of the whole call, walking / by chunk, dstate 128):
+    // 4 x 8192 x 64 heads 1074 / 1462; 2 x 8192 x 48 525 / 582; 1 x 8192 x 64 419 / 404;
+    // 1 x 8192 x 32 320 / 233; 1 x 32768 x 24, dstate 64, 806 / 383
+    if (2 * bh >= 192 || a.chunks == 1) {
         sbf_states_kernel<N, true><<<dim3(static_cast<uint32_t>(bh), 2), 256, 0, s>>>(a);
     } else {
         sbf_states_kernel<N, false><<<dim3(static_cast<uint32_t>(bh * a.chunks), 2), 256, 0, s>>>(a);
