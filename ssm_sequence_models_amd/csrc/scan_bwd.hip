@@ -106,18 +106,38 @@ __device__ __forceinline__ Where where(const ScanBwdArgs& a, int64_t blk) {
     return w;
 }
 
-// A row-major view [tokens][cols] of the chunk's tokens: zeros outside.
-template <class S>
+// four consecutive elements at any element's alignment
+__device__ __forceinline__ f4 load4(const float* p) {
+    typedef float f4any __attribute__((ext_vector_type(4), aligned(4)));
+    return *reinterpret_cast<const f4any*>(p);
+}
+__device__ __forceinline__ f4 load4(const uint16_t* p) {
+    typedef uint32_t u2any __attribute__((ext_vector_type(2), aligned(2)));
+    const u2any q = *reinterpret_cast<const u2any*>(p);
+    return f4{__uint_as_float(q[0] << 16), __uint_as_float(q[0] & 0xFFFF0000u),
+              __uint_as_float(q[1] << 16), __uint_as_float(q[1] & 0xFFFF0000u)};
+}
+
+// A row-major view [tokens][cols] of the chunk's tokens: zeros outside.  What lies outside is read
+// from the last row and column instead and replaced, so no load is under a branch and waits for
+// another.  W: cols is a multiple of 16, only rows can lie outside.
+template <class S, bool W>
 struct View {
     const typename S::T* p;
     int64_t row;
     int rows, cols;
     __device__ __forceinline__ float at(int r, int c) const {
-        return r < rows && c < cols ? S::load(p, r * row + c) : 0.0f;
+        const float v = S::load(p, (r < rows ? r : rows - 1) * row + (W || c < cols ? c : cols - 1));
+        return r < rows && (W || c < cols) ? v : 0.0f;
     }
     // operand with the contraction along the row: row r, columns k .. k + 3
     __device__ __forceinline__ f4 along(int r, int k) const {
-        return f4{at(r, k), at(r, k + 1), at(r, k + 2), at(r, k + 3)};
+        if constexpr (W) {
+            const f4 v = load4(p + (r < rows ? r : rows - 1) * row + k);
+            return r < rows ? v : f4{0, 0, 0, 0};
+        } else {
+            return f4{at(r, k), at(r, k + 1), at(r, k + 2), at(r, k + 3)};
+        }
     }
     // operand with the contraction over the rows: rows k .. k + 3 of column c
     __device__ __forceinline__ f4 down(int k, int c) const {
@@ -128,7 +148,7 @@ struct View {
 // ---------------------------------------------------------------------------------------
 // each chunk's share of the next S (blockIdx.y = 0) and of the previous G (blockIdx.y = 1)
 // ---------------------------------------------------------------------------------------
-template <class S>
+template <class S, bool W>
 __global__ void __launch_bounds__(256) sb_local_kernel(ScanBwdArgs a) {
     __shared__ ChunkDecay cd;
     const Where w = where(a, blockIdx.x);
@@ -138,9 +158,9 @@ __global__ void __launch_bounds__(256) sb_local_kernel(ScanBwdArgs a) {
     using T = typename S::T;
     const int64_t tok = w.b * a.L + w.t0;
     const int P = static_cast<int>(a.P), N = static_cast<int>(a.N);
-    const View<S> xv{static_cast<const T*>(rev ? a.dy : a.x) + tok * (rev ? a.dy_row : a.x_row) + w.h * P,
+    const View<S, W> xv{static_cast<const T*>(rev ? a.dy : a.x) + tok * (rev ? a.dy_row : a.x_row) + w.h * P,
                      rev ? a.dy_row : a.x_row, w.nv, P};
-    const View<S> bv{static_cast<const T*>(rev ? a.C : a.Bm) + tok * (rev ? a.c_row : a.b_row) + w.g * N,
+    const View<S, W> bv{static_cast<const T*>(rev ? a.C : a.Bm) + tok * (rev ? a.c_row : a.b_row) + w.g * N,
                      rev ? a.c_row : a.b_row, w.nv, N};
     float* out = (rev ? a.grads : a.states) + ((w.b * a.H + w.h) * a.chunks + w.c) * a.P * a.N;
     const int lane = threadIdx.x & 63, li = lane & 15, g4 = lane >> 4;
@@ -219,7 +239,7 @@ __device__ __forceinline__ double before_lane(double v, int lane) {
 // ---------------------------------------------------------------------------------------
 // gradients of one chunk and head
 // ---------------------------------------------------------------------------------------
-template <class S>
+template <class S, bool W>
 __global__ void __launch_bounds__(256) sb_grad_kernel(ScanBwdArgs a) {
     __shared__ ChunkDecay cd;
     __shared__ float pair[kQ][kQ + 1];  // [t][s] L_ts (C_t.B_s)
@@ -237,12 +257,12 @@ __global__ void __launch_bounds__(256) sb_grad_kernel(ScanBwdArgs a) {
     using T = typename S::T;
     const int64_t tok = w.b * a.L + w.t0;
     const int P = static_cast<int>(a.P), N = static_cast<int>(a.N);
-    const View<S> xv{static_cast<const T*>(a.x) + tok * a.x_row + w.h * P, a.x_row, w.nv, P};
-    const View<S> dyv{static_cast<const T*>(a.dy) + tok * a.dy_row + w.h * P, a.dy_row, w.nv, P};
-    const View<S> bv{static_cast<const T*>(a.Bm) + tok * a.b_row + w.g * N, a.b_row, w.nv, N};
-    const View<S> cv{static_cast<const T*>(a.C) + tok * a.c_row + w.g * N, a.c_row, w.nv, N};
+    const View<S, W> xv{static_cast<const T*>(a.x) + tok * a.x_row + w.h * P, a.x_row, w.nv, P};
+    const View<S, W> dyv{static_cast<const T*>(a.dy) + tok * a.dy_row + w.h * P, a.dy_row, w.nv, P};
+    const View<S, W> bv{static_cast<const T*>(a.Bm) + tok * a.b_row + w.g * N, a.b_row, w.nv, N};
+    const View<S, W> cv{static_cast<const T*>(a.C) + tok * a.c_row + w.g * N, a.c_row, w.nv, N};
     const int64_t at = ((w.b * a.H + w.h) * a.chunks + w.c) * a.P * a.N;
-    const View<F32> sv{a.states + at, N, P, N}, gv{a.grads + at, N, P, N};
+    const View<F32, W> sv{a.states + at, N, P, N}, gv{a.grads + at, N, P, N};
     const int lane = threadIdx.x & 63, li = lane & 15, g4 = lane >> 4, wave = threadIdx.x >> 6;
 
     // pairs s <= t: the ten 16 x 16 tiles on and below the diagonal
@@ -517,9 +537,12 @@ template <class S>
 hipError_t launch_general(const ScanBwdArgs& a, hipStream_t s) {
     const uint32_t bhc = static_cast<uint32_t>(a.B * a.H * a.chunks);
     sb_through_kernel<<<bhc, 64, 0, s>>>(a);
-    sb_local_kernel<S><<<dim3(bhc, 2), 256, 0, s>>>(a);
+    const bool whole = a.P % 16 == 0 && a.N % 16 == 0;
+    if (whole) sb_local_kernel<S, true><<<dim3(bhc, 2), 256, 0, s>>>(a);
+    else sb_local_kernel<S, false><<<dim3(bhc, 2), 256, 0, s>>>(a);
     sb_pass_kernel<<<dim3(static_cast<uint32_t>(a.B * a.H * ((a.P * a.N + 255) / 256)), 2), 256, 0, s>>>(a);
-    sb_grad_kernel<S><<<bhc, 256, 0, s>>>(a);
+    if (whole) sb_grad_kernel<S, true><<<bhc, 256, 0, s>>>(a);
+    else sb_grad_kernel<S, false><<<bhc, 256, 0, s>>>(a);
     sb_heads_kernel<S><<<dim3(static_cast<uint32_t>((a.B * a.L * a.G * a.N + 255) / 256), 2), 256, 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     return e == hipSuccess ? launch_scan_bwd_ddt(a, kQ, s) : e;
