@@ -34,7 +34,15 @@
 // on the fp32 matrix instruction (16 x 16 x 4).  Three steps: the chunks' own shares of S and G
 // (one block a chunk and head), their sums along the row (one thread a state element), the
 // gradients (one block a chunk and head; dB and dC a head, which a last kernel adds over the
-// heads of a group in order, with the chunks' dA).
+// heads of a group in order, with the chunks' dA).  4 x 8192 tokens x 64 heads x 64 x 128, fp32:
+// 1.33 + 0.96 + 5.92 ms and 0.6 ms for the rest, about 190 GFLOP of products at 33 TFLOP/s of the
+// 153 that a large fp32 matrix product reaches: bound by the operands' loads, one to four for
+// four products.  One head of 64 tokens x 4 x 4: 35 us in six launches, the dependent steps of
+// one block (17 us in the gradients).
+//
+// dA is one number a head: what it is summed from (the pairs' sums, u, v, <G, S>) is formed in
+// double from the fp32 dot products and kept as two floats, so that what cancels in it is the
+// dot products' rounding alone.
 #include "internal.h"
 
 namespace ssm {
@@ -120,20 +128,20 @@ __device__ __forceinline__ f4 load4(const uint16_t* p) {
 
 // A row-major view [tokens][cols] of the chunk's tokens: zeros outside.  What lies outside is read
 // from the last row and column instead and replaced, so no load is under a branch and waits for
-// another.  W: cols is a multiple of 16, only rows can lie outside.
+// another.  W: cols is a multiple of 16, so four consecutive columns are inside or outside.
 template <class S, bool W>
 struct View {
     const typename S::T* p;
     int64_t row;
     int rows, cols;
     __device__ __forceinline__ float at(int r, int c) const {
-        const float v = S::load(p, (r < rows ? r : rows - 1) * row + (W || c < cols ? c : cols - 1));
-        return r < rows && (W || c < cols) ? v : 0.0f;
+        const float v = S::load(p, (r < rows ? r : rows - 1) * row + (c < cols ? c : cols - 1));
+        return r < rows && c < cols ? v : 0.0f;
     }
     // operand with the contraction along the row: row r, columns k .. k + 3
     __device__ __forceinline__ f4 along(int r, int k) const {
         if constexpr (W) {
-            const f4 v = load4(p + (r < rows ? r : rows - 1) * row + k);
+            const f4 v = load4(p + (r < rows ? r : rows - 1) * row + k);  // k < cols: called for 16 at a time
             return r < rows ? v : f4{0, 0, 0, 0};
         } else {
             return f4{at(r, k), at(r, k + 1), at(r, k + 2), at(r, k + 3)};
@@ -164,34 +172,41 @@ __global__ void __launch_bounds__(256) sb_local_kernel(ScanBwdArgs a) {
                      rev ? a.c_row : a.b_row, w.nv, N};
     float* out = (rev ? a.grads : a.states) + ((w.b * a.H + w.h) * a.chunks + w.c) * a.P * a.N;
     const int lane = threadIdx.x & 63, li = lane & 15, g4 = lane >> 4;
-    const int np = (P + 15) / 16, nn = (N + 15) / 16;
+    if (!rev && threadIdx.x == 0) a.through[(w.b * a.H + w.h) * a.chunks + w.c] = cd.through;
+    // A wavefront takes kLP x kLN tiles at a time: an operand serves all tiles of its row or column
+    // (4 x 8192 x 64 heads x 64 x 128, fp32: 1337 us, one tile at a time 2570; narrow heads have
+    // too few tiles, 2048 x 16 x 24 x 16: 13 and 8 us).
+    constexpr int kLP = W ? 2 : 1, kLN = W ? 4 : 1;
+    const int np = (P + 16 * kLP - 1) / (16 * kLP), nn = (N + 16 * kLN - 1) / (16 * kLN);
     for (int tile = threadIdx.x >> 6; tile < np * nn; tile += 4) {
-        const int p0 = tile / nn * 16, n0 = tile % nn * 16;
-        f4 acc{0, 0, 0, 0};
+        const int p0 = tile / nn * 16 * kLP, n0 = tile % nn * 16 * kLN;
+        f4 acc[kLP][kLN] = {};
         for (int k = 0; k < kQ; k += 16) {
-            f4 x = xv.down(k + 4 * g4, p0 + li);
+            f4 x[kLP], y[kLN], scale;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int t = k + 4 * g4 + j;
-                x[j] *= rev ? cd.f[t] : cd.dt[t] * cd.e[t];
+                scale[j] = rev ? cd.f[t] : cd.dt[t] * cd.e[t];
             }
-            acc = mfma4(x, bv.down(k + 4 * g4, n0 + li), acc);
+#pragma unroll
+            for (int i = 0; i < kLP; ++i) x[i] = xv.down(k + 4 * g4, p0 + 16 * i + li) * scale;
+#pragma unroll
+            for (int i = 0; i < kLN; ++i) y[i] = bv.down(k + 4 * g4, n0 + 16 * i + li);
+#pragma unroll
+            for (int i = 0; i < kLP; ++i)
+#pragma unroll
+                for (int h = 0; h < kLN; ++h) acc[i][h] = mfma4(x[i], y[h], acc[i][h]);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int p = p0 + 4 * g4 + e, n = n0 + li;
-            if (p < P && n < N) out[p * N + n] = acc[e];
-        }
+        for (int i = 0; i < kLP; ++i)
+#pragma unroll
+            for (int h = 0; h < kLN; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int p = p0 + 16 * i + 4 * g4 + e, n = n0 + 16 * h + li;
+                    if (p < P && n < N) out[p * N + n] = acc[i][h][e];
+                }
     }
-}
-
-// f_last of every chunk
-__global__ void __launch_bounds__(64) sb_through_kernel(ScanBwdArgs a) {
-    __shared__ ChunkDecay cd;
-    const Where w = where(a, blockIdx.x);
-    chunk_decay(cd, a.dt + (w.b * a.L + w.t0) * a.H + w.h, a.H, a.A[w.h],
-                a.seq ? a.seq + w.b * a.L : nullptr, w.t0, w.nv);
-    if (threadIdx.x == 0) a.through[(w.b * a.H + w.h) * a.chunks + w.c] = cd.through;
 }
 
 // Sums along the row, in place: the share of chunk c becomes the state before it (blockIdx.y =
@@ -240,7 +255,7 @@ __device__ __forceinline__ double before_lane(double v, int lane) {
 // gradients of one chunk and head
 // ---------------------------------------------------------------------------------------
 template <class S, bool W>
-__global__ void __launch_bounds__(256) sb_grad_kernel(ScanBwdArgs a) {
+__global__ void __launch_bounds__(512) sb_grad_kernel(ScanBwdArgs a) {
     __shared__ ChunkDecay cd;
     __shared__ float pair[kQ][kQ + 1];  // [t][s] L_ts (C_t.B_s)
     __shared__ float lw[kQ][kQ + 1];    // [t][s] L_ts (dy_t.x_s) dt_s
@@ -249,8 +264,8 @@ __global__ void __launch_bounds__(256) sb_grad_kernel(ScanBwdArgs a) {
     __shared__ double rowp[4][kQ];      // sums over the s of one 16-column tile, s < t, of W
     __shared__ double colp[4][kQ];      // sums over the t of one 16-row tile, t > s, of W / dt_s
     __shared__ float diag[kQ];          // W_ss / dt_s
-    __shared__ double uu[kQ], vv[kQ];   // u_t, v_s / dt_s
-    __shared__ double gs[4];
+    __shared__ double uu[2][kQ], vv[2][kQ];  // u_t, v_s / dt_s, by the columns' share
+    __shared__ double gs[8];
     const Where w = where(a, blockIdx.x);
     chunk_decay(cd, a.dt + (w.b * a.L + w.t0) * a.H + w.h, a.H, a.A[w.h],
                 a.seq ? a.seq + w.b * a.L : nullptr, w.t0, w.nv);
@@ -266,7 +281,7 @@ __global__ void __launch_bounds__(256) sb_grad_kernel(ScanBwdArgs a) {
     const int lane = threadIdx.x & 63, li = lane & 15, g4 = lane >> 4, wave = threadIdx.x >> 6;
 
     // pairs s <= t: the ten 16 x 16 tiles on and below the diagonal
-    for (int tile = wave; tile < 10; tile += 4) {
+    for (int tile = wave; tile < 10; tile += 8) {
         const int ti = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3;
         const int si = tile - ti * (ti + 1) / 2;
         f4 cb{0, 0, 0, 0}, yx{0, 0, 0, 0};
@@ -303,18 +318,18 @@ __global__ void __launch_bounds__(256) sb_grad_kernel(ScanBwdArgs a) {
     // <G, S>
     {
         double d = 0.0;
-        for (int i = threadIdx.x; i < P * N; i += 256) d += static_cast<double>(sv.p[i]) * gv.p[i];
+        for (int i = threadIdx.x; i < P * N; i += 512) d += static_cast<double>(sv.p[i]) * gv.p[i];
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) d += __shfl_xor(d, o);
         if (lane == 0) gs[wave] = d;
     }
     __syncthreads();
 
-    // this wavefront's 16 tokens r0 .. r0 + 15 of every output
-    const int r0 = 16 * wave;
+    // this wavefront's 16 tokens r0 .. r0 + 15 of every output, every other 16 columns of them
+    const int r0 = 16 * (wave & 3), part = wave >> 2;
     T* dxo = static_cast<T*>(a.dx) + tok * a.dx_row + w.h * P;
     double v[4] = {0, 0, 0, 0}, u[4] = {0, 0, 0, 0};  // without e and f
-    for (int p0 = 0; p0 < P; p0 += 16) {
+    for (int p0 = 16 * part; p0 < P; p0 += 32) {
         f4 in{0, 0, 0, 0}, out{0, 0, 0, 0};
         for (int k = r0; k < kQ; k += 16) {
             const int t = k + 4 * g4;
@@ -332,7 +347,7 @@ __global__ void __launch_bounds__(256) sb_grad_kernel(ScanBwdArgs a) {
         }
     }
     const int64_t ho = (tok * a.H + w.h) * N;  // [row][token][head][N]
-    for (int n0 = 0; n0 < N; n0 += 16) {
+    for (int n0 = 16 * part; n0 < N; n0 += 32) {
         f4 in{0, 0, 0, 0}, out{0, 0, 0, 0}, bin{0, 0, 0, 0}, bout{0, 0, 0, 0};
         for (int k = 0; k < r0 + 16; k += 16) {
             const int s = k + 4 * g4;
@@ -369,8 +384,8 @@ __global__ void __launch_bounds__(256) sb_grad_kernel(ScanBwdArgs a) {
         }
         if (li == 0) {
             const int t = r0 + 4 * g4 + e;
-            uu[t] = cd.f[t] == 0.0f ? 0.0 : u[e] * exp2(cd.cs[t]);
-            vv[t] = cd.e[t] == 0.0f ? 0.0 : v[e] * exp2(cd.cs[kQ - 1] - cd.cs[t]);
+            uu[part][t] = cd.f[t] == 0.0f ? 0.0 : u[e] * exp2(cd.cs[t]);
+            vv[part][t] = cd.e[t] == 0.0f ? 0.0 : v[e] * exp2(cd.cs[kQ - 1] - cd.cs[t]);
         }
     }
     __syncthreads();
@@ -394,14 +409,14 @@ __global__ void __launch_bounds__(256) sb_grad_kernel(ScanBwdArgs a) {
         *hi = static_cast<float>(v);
         *lo = static_cast<float>(v - *hi);
     };
-    both(out + kSumU * kQ + t, out + kSumULow * kQ + t, uu[t]);
-    both(out + kSumV * kQ + t, out + kSums * kQ + t, vv[t]);
+    both(out + kSumU * kQ + t, out + kSumULow * kQ + t, uu[0][t] + uu[1][t]);
+    both(out + kSumV * kQ + t, out + kSums * kQ + t, vv[0][t] + vv[1][t]);
     both(out + kSumSpan * kQ + t, out + kSumSpanLow * kQ + t, q);
     out[kSumColOff * kQ + t] = static_cast<float>(below + colp[j][t]);
     out[kSumDiag * kQ + t] = diag[t];
     if (t == 0)
         both(out + kSums * kQ + 64, out + kSums * kQ + 65,
-             cd.through == 0.0f ? 0.0 : exp2(cd.cs[kQ - 1]) * ((gs[0] + gs[1]) + (gs[2] + gs[3])));
+             cd.through == 0.0f ? 0.0 : exp2(cd.cs[kQ - 1]) * (((gs[0] + gs[1]) + (gs[2] + gs[3])) + ((gs[4] + gs[5]) + (gs[6] + gs[7]))));
 }
 
 // q, ddt and a chunk's share of dA: one wavefront a head and chunk, Q / 64 tokens a lane; a block
@@ -536,13 +551,12 @@ __global__ void __launch_bounds__(256) sb_dA_kernel(ScanBwdArgs a) {
 template <class S>
 hipError_t launch_general(const ScanBwdArgs& a, hipStream_t s) {
     const uint32_t bhc = static_cast<uint32_t>(a.B * a.H * a.chunks);
-    sb_through_kernel<<<bhc, 64, 0, s>>>(a);
     const bool whole = a.P % 16 == 0 && a.N % 16 == 0;
     if (whole) sb_local_kernel<S, true><<<dim3(bhc, 2), 256, 0, s>>>(a);
     else sb_local_kernel<S, false><<<dim3(bhc, 2), 256, 0, s>>>(a);
     sb_pass_kernel<<<dim3(static_cast<uint32_t>(a.B * a.H * ((a.P * a.N + 255) / 256)), 2), 256, 0, s>>>(a);
-    if (whole) sb_grad_kernel<S, true><<<bhc, 256, 0, s>>>(a);
-    else sb_grad_kernel<S, false><<<bhc, 256, 0, s>>>(a);
+    if (whole) sb_grad_kernel<S, true><<<bhc, 512, 0, s>>>(a);
+    else sb_grad_kernel<S, false><<<bhc, 512, 0, s>>>(a);
     sb_heads_kernel<S><<<dim3(static_cast<uint32_t>((a.B * a.L * a.G * a.N + 255) / 256), 2), 256, 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     return e == hipSuccess ? launch_scan_bwd_ddt(a, kQ, s) : e;
