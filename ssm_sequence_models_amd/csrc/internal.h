@@ -320,8 +320,8 @@ struct ScanBwdArgs {
     float* sums;       // [B, H, chunks, kSums * Q + kSumTail], Q the chunk's tokens
 };
 // Sums over pairs of tokens that ddt and dA are formed from (W, u, v as in scan_bwd.hip), each an
-// array over the chunk's tokens: u; v / dt; row sums of W over s < t, in earlier 16-token tiles
-// and in t's own; column sums of W / dt_s over t > s, in later tiles and in s's own; W_tt / dt_t.
+// array over the chunk's tokens: u; v / dt; row sums of W over s < t in earlier 16-token tiles;
+// the W of t's own tile that span t; column sums of W / dt_s over t > s, in later tiles and in s's own; W_tt / dt_t.
 // Behind them the row sums' sums by tile, [t tile][s tile] in eights, then the parts of |S|^2 and
 // |G|^2 by 16 state dimensions, in eights.
 // Chunks of 64 tokens: u; v / dt; the W that span t; all column sums; W_tt / dt_t; the rests of

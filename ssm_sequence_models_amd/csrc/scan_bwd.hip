@@ -22,8 +22,8 @@
 // on: those are far larger where the decay is fast, and dA, a sum over the whole batch, would
 // keep their rounding errors.  With 16-token tiles they are the row sums over earlier tiles
 // from tau to its tile's end, the column sums over later tiles from its tile's start to tau, the
-// tile pairs around its tile, all sums of what spans tau only, and the difference within the
-// one tile.  The part of ddt that does not pass through a_t is sum_t W_ts / dt_s + v_s / dt_s,
+// tile pairs around its tile, all sums of what spans tau only, and the pairs within the one tile
+// (here as a difference in double, on the bf16 matrix cores summed directly).  The part of ddt that does not pass through a_t is sum_t W_ts / dt_s + v_s / dt_s,
 // formed without the division.
 //
 // Decays: log a_t is summed in double over the chunk and each factor is the exponential of a
@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(128 * kAnchor) sb_ddt_kernel(ScanBwdArgs a) {
             const float cdiag = in[kSumColDiag * Q + t];
             direct[k] = ((coff + cdiag) + in[kSumDiag * Q + t]) + vt;
             q[k] = from_lane<16>(in[kSumRowOff * Q + t], lane) + before_lane<16>(static_cast<double>(coff) * dts[k], lane);
-            q[k] += from_lane<16>(static_cast<double>(in[kSumRowDiag * Q + t]) - static_cast<double>(cdiag) * dts[k], lane);
+            q[k] += in[kSumRowDiag * Q + t];
             for (int j2 = j + 1; j2 < Q / 16; ++j2)
                 for (int i = 0; i < j; ++i) q[k] += in[kSums * Q + 8 * j2 + i];
         }

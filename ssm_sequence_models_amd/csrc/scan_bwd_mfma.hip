@@ -148,6 +148,24 @@ __device__ __forceinline__ float group_sums(float a, float b, float c, float d) 
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 __device__ __forceinline__ int group_of_row(int row) { return row == 1 ? 2 : row == 2 ? 1 : row; }
+// Of the tile's W on rows 4 g4 + e, column li (0 on and above the diagonal): the column's sums
+// from row 4 g4 + e on where that lies below the diagonal.  Summed over the columns they are the W
+// that span a token, without a difference of row and column sums: that kept the rounding of every
+// pair for all 16 tokens, eight times what dA of a fast head is made of.
+__device__ __forceinline__ void spanning(float (&w)[4], int li, int g4) {
+    const int d = li - 4 * g4;
+    w[2] += w[3];
+    w[1] += w[2];
+    w[0] += w[1];
+    const uint32_t t = __float_as_uint(w[0]);
+    const auto p = __builtin_amdgcn_permlane16_swap(t, t, false, false);  // rows 0 0 2 2 and 1 1 3 3
+    const float even = __uint_as_float(p[0]), odd = __uint_as_float(p[1]);
+    const uint32_t two = __float_as_uint(even + odd);
+    const auto q = __builtin_amdgcn_permlane32_swap(two, two, false, false);
+    const float later = (g4 & 1 ? 0.0f : odd) + (g4 & 2 ? 0.0f : __uint_as_float(q[1]));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = e > d ? w[e] + later : 0.0f;
+}
 // Sums over the 16 lanes that share g4, of four values at once: lane li holds that of v[li % 4].
 __device__ __forceinline__ float row_sums(const float (&v)[4], int li) {
     const float k01 = li & 1 ? v[1] : v[0], s01 = li & 1 ? v[0] : v[1];
@@ -745,6 +763,7 @@ __global__ void __launch_bounds__(1024) sbf_grad_kernel(ScanBwdArgs a) {
                     }
                 }
                 settle(sum);
+                if (DIAG) spanning(rw, li, g4);
                 *reinterpret_cast<float*>(sm + rt + 64 * j) = row_sums(rw, li);  // the same from four lanes
                 const uint32_t q0 = pack_bf16x2(pv[0], pv[1]), q1 = pack_bf16x2(pv[2], pv[3]);
                 pw[0][2 * i] = q0;
