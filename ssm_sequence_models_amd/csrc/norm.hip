@@ -61,21 +61,38 @@ __device__ __forceinline__ float sigmoidf(float z) {
     return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
 }
 
-// Eight consecutive elements, 16 bytes an access at any element's alignment.  TAIL: of the last
-// eight of a group only n exist; the others are 0 and not stored.  Nothing is used twice, so
-// accesses are non-temporal, but for fp32 at odd widths, where neighbours share lines
-// (32768 x 4097, gate: 344 -> 309 us forward, 720 -> 589 backward; bf16 at that width 289 / 558
-// non-temporal, 313 / 602 not, element by element 816 / 1297).
+// A thread's columns: eight consecutive ones, 16 bytes an access at any element's alignment.
+// TAIL: the width is no multiple of eight, and the thread whose eight would pass the end takes the
+// last eight instead.  Those it shares with the thread before it are computed twice and stored
+// twice, the same values, and counted once; no access is under a branch of its own (an element at
+// a time for the last few took 26 us for 1027 x 1537 fp32 backward).  Widths below eight go element
+// by element.  Nothing is used twice, so
+// accesses are non-temporal, but for fp32 at odd widths, where neighbours share lines (32768 x
+// 4097 with a gate, forward: 309 us, non-temporal 344).  bf16, 32768 x 4097, forward / backward:
+// 227 / 546 us; element by element throughout 816 / 1297.
 constexpr int kVec = 8;
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 
+template <bool TAIL>
+struct Cols {
+    int at;     // first column
+    int own;    // columns at + own .. are this thread's to count
+    int width;  // the group's
+    __device__ __forceinline__ Cols(int c, int m) : at(c), own(0), width(m) {
+        if (TAIL && c + kVec > m && c < m) {
+            at = m < kVec ? 0 : m - kVec;
+            own = c - at;
+        }
+    }
+    __device__ __forceinline__ bool counts(int e) const { return TAIL ? e >= own && at + e < width : at < width; }
+};
+
 template <class S, bool TAIL>
-__device__ __forceinline__ void load_vec(const typename S::T* p, float (&v)[kVec], int n) {
-    if (TAIL && n < kVec) {
+__device__ __forceinline__ void load_vec(const typename S::T* p, float (&v)[kVec], int m) {
+    if (TAIL && m < kVec) {
 #pragma unroll
-        for (int i = 0; i < kVec; ++i)
-            if (i < n) v[i] = S::load(p, i);
+        for (int i = 0; i < kVec; ++i) v[i] = i < m ? S::load(p, i < m ? i : 0) : 0.0f;
     } else if constexpr (S::kBytes == 2) {
         const u32x4_t q = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p));
 #pragma unroll
@@ -94,11 +111,11 @@ __device__ __forceinline__ void load_vec(const typename S::T* p, float (&v)[kVec
     }
 }
 template <class S, bool TAIL>
-__device__ __forceinline__ void store_vec(typename S::T* p, const float (&v)[kVec], int n) {
-    if (TAIL && n < kVec) {
+__device__ __forceinline__ void store_vec(typename S::T* p, const float (&v)[kVec], int m) {
+    if (TAIL && m < kVec) {
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
-            if (i < n) S::store(p, i, v[i]);
+            if (i < m) S::store(p, i, v[i]);
     } else if constexpr (S::kBytes == 2) {
         u32x4_t q;
 #pragma unroll
@@ -130,12 +147,12 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_fwd_kernel(NormArg
     float w[NV][kVec], b[NV][kVec];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int c = (j * TPR + tid) * kVec;
+        const Cols<TAIL> c((j * TPR + tid) * kVec, m);
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
-            const bool in = c + (TAIL ? e : 0) < m;
-            w[j][e] = in ? (a.w ? a.w[c0 + c + e] : 1.0f) : 0.0f;
-            b[j][e] = in && a.b ? a.b[c0 + c + e] : 0.0f;
+            const bool in = c.at + (TAIL ? e : 0) < m;
+            w[j][e] = in ? (a.w ? a.w[c0 + c.at + e] : 1.0f) : 0.0f;
+            b[j][e] = in && a.b ? a.b[c0 + c.at + e] : 0.0f;
         }
     }
     const float inv_m = 1.0f / static_cast<float>(m);
@@ -146,22 +163,24 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_fwd_kernel(NormArg
         float u[NV][kVec], z[NV][kVec];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * TPR + tid) * kVec;
+            const Cols<TAIL> c((j * TPR + tid) * kVec, m);
 #pragma unroll
             for (int e = 0; e < kVec; ++e) u[j][e] = z[j][e] = 0.0f;
-            if (c < m) {
-                load_vec<S, TAIL>(xr + c, u[j], m - c);
-                if constexpr (GATE != kGateNone) load_vec<S, TAIL>(zr + c, z[j], m - c);
+            if (c.at < m) {
+                load_vec<S, TAIL>(xr + c.at, u[j], m);
+                if constexpr (GATE != kGateNone) load_vec<S, TAIL>(zr + c.at, z[j], m);
             }
         }
         float mean = 0.0f, q = 0.0f;
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j) {
+            const Cols<TAIL> c((j * TPR + tid) * kVec, m);
 #pragma unroll
             for (int e = 0; e < kVec; ++e) {
                 if constexpr (GATE == kGateBefore) u[j][e] *= z[j][e] * sigmoidf(z[j][e]);
-                mean += u[j][e];
+                mean += !TAIL || c.counts(e) ? u[j][e] : 0.0f;
             }
+        }
         if (a.layer) {
             mean = team_sum<TPR>(mean, red, slot) * inv_m;
             slot = slot == 2 ? 0 : slot + 1;
@@ -169,27 +188,29 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_fwd_kernel(NormArg
             mean = 0.0f;
         }
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j) {
+            const Cols<TAIL> c((j * TPR + tid) * kVec, m);
 #pragma unroll
             for (int e = 0; e < kVec; ++e) {
-                const float d = (j * TPR + tid) * kVec + (TAIL ? e : 0) < m ? u[j][e] - mean : 0.0f;
+                const float d = c.at < m ? u[j][e] - mean : 0.0f;
                 u[j][e] = d;
-                q += d * d;
+                q += !TAIL || c.counts(e) ? d * d : 0.0f;
             }
+        }
         q = team_sum<TPR>(q, red, slot) * inv_m;
         slot = slot == 2 ? 0 : slot + 1;
         const float rstd = 1.0f / sqrtf(q + a.eps);
         T* out = static_cast<T*>(a.out) + r * a.out_row + c0;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * TPR + tid) * kVec;
+            const Cols<TAIL> c((j * TPR + tid) * kVec, m);
             float o[kVec];
 #pragma unroll
             for (int e = 0; e < kVec; ++e) {
                 o[e] = u[j][e] * rstd * w[j][e] + b[j][e];
                 if constexpr (GATE == kGateAfter) o[e] *= z[j][e] * sigmoidf(z[j][e]);
             }
-            if (c < m) store_vec<S, TAIL>(out + c, o, m - c);
+            if (c.at < m) store_vec<S, TAIL>(out + c.at, o, m);
         }
     }
 }
@@ -207,12 +228,12 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_bwd_kernel(NormArg
     float w[NV][kVec], b[NV][kVec], dw[NV][kVec], db[NV][kVec];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int c = (j * TPR + tid) * kVec;
+        const Cols<TAIL> c((j * TPR + tid) * kVec, m);
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
-            const bool in = c + (TAIL ? e : 0) < m;
-            w[j][e] = in ? (a.w ? a.w[c0 + c + e] : 1.0f) : 0.0f;
-            b[j][e] = GATE == kGateAfter && in && a.b ? a.b[c0 + c + e] : 0.0f;
+            const bool in = c.at + (TAIL ? e : 0) < m;
+            w[j][e] = in ? (a.w ? a.w[c0 + c.at + e] : 1.0f) : 0.0f;
+            b[j][e] = GATE == kGateAfter && in && a.b ? a.b[c0 + c.at + e] : 0.0f;
             dw[j][e] = db[j][e] = 0.0f;
         }
     }
@@ -225,24 +246,26 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_bwd_kernel(NormArg
         float x[NV][kVec], z[NV][kVec], d[NV][kVec], n[NV][kVec];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * TPR + tid) * kVec;
+            const Cols<TAIL> c((j * TPR + tid) * kVec, m);
 #pragma unroll
             for (int e = 0; e < kVec; ++e) x[j][e] = z[j][e] = d[j][e] = 0.0f;
-            if (c < m) {
-                load_vec<S, TAIL>(xr + c, x[j], m - c);
-                if constexpr (GATE != kGateNone) load_vec<S, TAIL>(zr + c, z[j], m - c);
-                load_vec<S, TAIL>(dr + c, d[j], m - c);
+            if (c.at < m) {
+                load_vec<S, TAIL>(xr + c.at, x[j], m);
+                if constexpr (GATE != kGateNone) load_vec<S, TAIL>(zr + c.at, z[j], m);
+                load_vec<S, TAIL>(dr + c.at, d[j], m);
             }
         }
         float mean = 0.0f, q = 0.0f;
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j) {
+            const Cols<TAIL> c((j * TPR + tid) * kVec, m);
 #pragma unroll
             for (int e = 0; e < kVec; ++e) {
                 n[j][e] = x[j][e];
                 if constexpr (GATE == kGateBefore) n[j][e] *= z[j][e] * sigmoidf(z[j][e]);
-                mean += n[j][e];
+                mean += !TAIL || c.counts(e) ? n[j][e] : 0.0f;
             }
+        }
         if (a.layer) {
             mean = team_sum<TPR>(mean, red, slot) * inv_m;
             slot = slot == 2 ? 0 : slot + 1;
@@ -250,13 +273,15 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_bwd_kernel(NormArg
             mean = 0.0f;
         }
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j) {
+            const Cols<TAIL> c((j * TPR + tid) * kVec, m);
 #pragma unroll
             for (int e = 0; e < kVec; ++e) {
-                const float v = (j * TPR + tid) * kVec + (TAIL ? e : 0) < m ? n[j][e] - mean : 0.0f;
+                const float v = c.at < m ? n[j][e] - mean : 0.0f;
                 n[j][e] = v;
-                q += v * v;
+                q += !TAIL || c.counts(e) ? v * v : 0.0f;
             }
+        }
         q = team_sum<TPR>(q, red, slot) * inv_m;
         slot = slot == 2 ? 0 : slot + 1;
         const float rstd = 1.0f / sqrtf(q + a.eps);
@@ -264,6 +289,7 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_bwd_kernel(NormArg
         float c1 = 0.0f, c2 = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
+            const Cols<TAIL> c((j * TPR + tid) * kVec, m);
             float dzv[kVec];
 #pragma unroll
             for (int e = 0; e < kVec; ++e) {
@@ -278,12 +304,11 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_bwd_kernel(NormArg
                 dw[j][e] += dp * n[j][e];
                 db[j][e] += dp;
                 d[j][e] = dp * w[j][e];
-                c1 += d[j][e] * n[j][e];
-                c2 += d[j][e];
+                c1 += !TAIL || c.counts(e) ? d[j][e] * n[j][e] : 0.0f;
+                c2 += !TAIL || c.counts(e) ? d[j][e] : 0.0f;
             }
             if constexpr (GATE == kGateAfter) {
-                const int c = (j * TPR + tid) * kVec;
-                if (c < m && a.want_dz) store_vec<S, TAIL>(dzr + c, dzv, m - c);
+                if (c.at < m && a.want_dz) store_vec<S, TAIL>(dzr + c.at, dzv, m);
             }
         }
         c1 = team_sum<TPR>(c1, red, slot) * inv_m;
@@ -297,7 +322,7 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_bwd_kernel(NormArg
         T* dxr = static_cast<T*>(a.dx) + r * a.dx_row + c0;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * TPR + tid) * kVec;
+            const Cols<TAIL> c((j * TPR + tid) * kVec, m);
             float dxv[kVec], dzv[kVec];
 #pragma unroll
             for (int e = 0; e < kVec; ++e) {
@@ -309,10 +334,10 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_bwd_kernel(NormArg
                     dzv[e] = du * x[j][e] * (sg * (1.0f + z[j][e] * (1.0f - sg)));
                 }
             }
-            if (c < m) {
-                store_vec<S, TAIL>(dxr + c, dxv, m - c);
+            if (c.at < m) {
+                store_vec<S, TAIL>(dxr + c.at, dxv, m);
                 if constexpr (GATE == kGateBefore)
-                    if (a.want_dz) store_vec<S, TAIL>(dzr + c, dzv, m - c);
+                    if (a.want_dz) store_vec<S, TAIL>(dzr + c.at, dzv, m);
             }
         }
     }
@@ -323,21 +348,23 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) norm_bwd_kernel(NormArg
         if constexpr (TEAMS == 4) {
             if (k > 0) __syncthreads();
 #pragma unroll
-            for (int j = 0; j < NV; ++j)
+            for (int j = 0; j < NV; ++j) {
+                const Cols<TAIL> c((j * 64 + tid) * kVec, m);
 #pragma unroll
                 for (int e = 0; e < kVec; ++e)
-                    join[team][(j * 64 + tid) * kVec + e] = k == 0 ? dw[j][e] : db[j][e];
+                    if (c.counts(e)) join[team][c.at + e] = k == 0 ? dw[j][e] : db[j][e];
+            }
             __syncthreads();
             for (int c = threadIdx.x; c < m; c += 256)
                 out[c] = (join[0][c] + join[1][c]) + (join[2][c] + join[3][c]);
         } else {
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const int c = (j * TPR + tid) * kVec;
-                if (c < m) {
+                const Cols<TAIL> c((j * TPR + tid) * kVec, m);
+                if (c.at < m) {
 #pragma unroll
                     for (int e = 0; e < kVec; ++e)
-                        if (!TAIL || c + e < m) out[c + e] = k == 0 ? dw[j][e] : db[j][e];
+                        if (c.counts(e)) out[c.at + e] = k == 0 ? dw[j][e] : db[j][e];
                 }
             }
         }
@@ -374,10 +401,11 @@ __global__ void norm_zero_kernel(float* dw, float* db, int64_t n) {
 }
 
 // Blocks a group: 1024 in all (four wavefront teams a block for m <= 1024), never more than
-// there are rows for.  At the size above with m = 512, forward / backward: 142 / 257 us; 512
+// there are rows for; backward, four rows a team, since every block writes a partial row
+// (2048 x 4096 bf16 33 -> 26 us, 4096 x 1024 30 -> 20; 512 rows the same).  At the size above with m = 512, forward / backward: 142 / 257 us; 512
 // blocks 173 / 269, 2048 blocks 153 / 251 (m = 4096: 146 / 260, 185 / 258, 147 / 267).
-int64_t norm_blocks(int64_t rows, int64_t m, int64_t groups) {
-    const int64_t per = m <= 1024 ? 4 : 1;
+int64_t norm_blocks(int64_t rows, int64_t m, int64_t groups, bool bwd) {
+    const int64_t per = (m <= 1024 ? 4 : 1) * (bwd ? 4 : 1);
     const int64_t need = (rows + per - 1) / per;
     const int64_t most = groups >= 1024 ? 1 : 1024 / groups;
     return need < most ? need : most;
@@ -424,7 +452,7 @@ void launch_norm(const NormArgs& a, ssm_dtype_t dtype, int gate, bool bwd, hipSt
 }  // namespace
 
 int64_t norm_partial_rows(int64_t rows, int64_t channels, int64_t groups) {
-    return norm_blocks(rows, channels / groups, groups);
+    return norm_blocks(rows, channels / groups, groups, true);
 }
 
 hipError_t launch_norm_fwd(const NormCall& c, hipStream_t s) {
@@ -433,7 +461,7 @@ hipError_t launch_norm_fwd(const NormCall& c, hipStream_t s) {
     a.x_row = c.x_row; a.z_row = c.z_row; a.out_row = c.out_row;
     a.rows = c.rows; a.groups = c.groups;
     a.m = static_cast<int>(c.channels / c.groups);
-    a.nb = norm_blocks(c.rows, a.m, c.groups);
+    a.nb = norm_blocks(c.rows, a.m, c.groups, false);
     a.eps = c.eps; a.layer = c.layer;
     const int gate = c.z == nullptr ? kGateNone : c.gate_after ? kGateAfter : kGateBefore;
     launch_norm(a, c.dtype, gate, false, s);
@@ -451,7 +479,7 @@ hipError_t launch_norm_bwd(const NormCall& c, hipStream_t s) {
     a.dx_row = c.dx_row; a.dz_row = c.dz_row;
     a.rows = c.rows; a.groups = c.groups;
     a.m = static_cast<int>(c.channels / c.groups);
-    a.nb = norm_blocks(c.rows, a.m, c.groups);
+    a.nb = norm_blocks(c.rows, a.m, c.groups, true);
     a.eps = c.eps; a.layer = c.layer;
     a.want_dz = c.dz != nullptr;
     a.want_db = c.db != nullptr;
