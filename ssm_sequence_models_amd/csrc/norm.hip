@@ -64,12 +64,11 @@ __device__ __forceinline__ float sigmoidf(float z) {
 // A thread's columns: eight consecutive ones, 16 bytes an access at any element's alignment.
 // TAIL: the width is no multiple of eight, and the thread whose eight would pass the end takes the
 // last eight instead.  Those it shares with the thread before it are computed twice and stored
-// twice, the same values, and counted once; no access is under a branch of its own (an element at
-// a time for the last few took 26 us for 1027 x 1537 fp32 backward).  Widths below eight go element
-// by element.  Nothing is used twice, so
-// accesses are non-temporal, but for fp32 at odd widths, where neighbours share lines (32768 x
-// 4097 with a gate, forward: 309 us, non-temporal 344).  bf16, 32768 x 4097, forward / backward:
-// 227 / 546 us; element by element throughout 816 / 1297.
+// twice, the same values, and counted once, so that no access is under a branch of its own (bf16
+// with a gate, 32768 x 2047, forward / backward: 89 / 152 us; the last few element by element
+// 176 / 347; 32768 x 4097: 227 / 546, all element by element 816 / 1297).  Widths below eight go
+// element by element.  Accesses are non-temporal, since nothing is used twice, but for fp32 at odd
+// widths, where neighbours share lines (32768 x 4097 forward: 309 us, non-temporal 344).
 constexpr int kVec = 8;
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));

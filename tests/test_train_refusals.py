@@ -59,11 +59,13 @@ def test_norm_refusals(lib, call):
 
 def test_norm_workspace_size(lib):
     import ssm_sequence_models_amd as s
-    # 1024 blocks over the groups, four rows a block up to 512 channels a group, one above
+    # 1024 blocks over the groups, of at least four rows a team; four teams a block up to 1024
+    # channels a group, one above
     assert s.norm_bwd_workspace_size(32768, 4096, 1) == 2 * 1024 * 4096 * 4
     assert s.norm_bwd_workspace_size(32768, 4096, 8) == 2 * 128 * 4096 * 4
-    assert s.norm_bwd_workspace_size(10, 4096, 1) == 2 * 10 * 4096 * 4
-    assert s.norm_bwd_workspace_size(10, 64, 1) == 2 * 3 * 64 * 4
+    assert s.norm_bwd_workspace_size(10, 4096, 1) == 2 * 3 * 4096 * 4
+    assert s.norm_bwd_workspace_size(10, 64, 1) == 2 * 1 * 64 * 4
+    assert s.norm_bwd_workspace_size(33, 1024, 1) == 2 * 3 * 1024 * 4
     assert s.norm_bwd_workspace_size(0, 64, 1) == 0
 
 
@@ -139,12 +141,14 @@ def test_gated_scan_refusals(lib, call):
 
 def test_gated_scan_workspace(lib):
     import ssm_sequence_models_amd as s
-    # 256 blocks already: no cut; else segments of at least four 128-token tiles, three floats a
-    # segment and channel; backward two floats a tile and channel more
+    # 256 blocks already (forward 128, or eight 128-token tiles): no cut; else segments of at least
+    # four tiles, three floats a segment and channel; backward two floats a tile and channel more
     assert s.gated_scan_fwd_workspace_size(4, 8192, 4096) == 0
     assert s.gated_scan_bwd_workspace_size(4, 8192, 4096) == 4 * 64 * 2 * 4096 * 4
-    assert s.gated_scan_fwd_workspace_size(1, 1023, 64) == 2 * 3 * 64 * 4
-    assert s.gated_scan_fwd_workspace_size(1, 896, 64) == 0
+    assert s.gated_scan_fwd_workspace_size(2, 8192, 4096) == 0
+    assert s.gated_scan_fwd_workspace_size(1, 1025, 64) == 2 * 3 * 64 * 4
+    assert s.gated_scan_fwd_workspace_size(1, 1024, 64) == 0
+    assert s.gated_scan_bwd_workspace_size(1, 1023, 64) == (2 * 3 + 8 * 2) * 64 * 4
     assert s.gated_scan_fwd_workspace_size(0, 5, 5) == 0
     assert _gfwd(lib, B=1, L=2000, ws=None) == 4
     assert _gfwd(lib, B=1, L=2000, wsb=16) == 4
