@@ -526,9 +526,8 @@ ssm_status_t ssm_gated_scan_step(const void* x, int64_t x_row, const void* gate,
  *   workspace      ssm_norm_bwd_workspace_size bytes, 4-byte aligned (partial sums; not needed
  *                  when dweight and dbias are both NULL)
  * channels / ngroups <= 16384; eps >= 0.  Outputs must not overlap inputs.  rows = 0: out, dx
- * and dz have no elements, dweight = dbias = 0.  Rows whose pointers and strides are 16-byte
- * multiples (and channels / ngroups a multiple of 8) use 16-byte accesses, others element
- * accesses; the results agree to rounding.
+ * and dz have no elements, dweight = dbias = 0.  Pointers and strides may be any number of
+ * elements; multiples of 16 bytes are the fastest.
  * ------------------------------------------------------------------------------------- */
 enum { SSM_NORM_RMS = 0, SSM_NORM_LAYER = 1 };
 typedef int32_t ssm_norm_t;

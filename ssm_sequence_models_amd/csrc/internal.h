@@ -336,7 +336,7 @@ size_t scan_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t P, int6
 int64_t scan_bwd_blocks(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N);
 hipError_t launch_scan_bwd(ScanBwdArgs a, void* workspace, ssm_dtype_t dtype, hipStream_t stream);
 // bf16, headdim 64, dstate 64 or 128
-bool scan_bwd_mfma_supported(int64_t P, int64_t N, ssm_dtype_t dtype);
+bool scan_bwd_mfma_supported(int64_t H, int64_t P, int64_t G, int64_t N, ssm_dtype_t dtype);
 size_t scan_bwd_mfma_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N);
 hipError_t launch_scan_bwd_mfma(ScanBwdArgs a, void* workspace, hipStream_t stream);
 // ddt and dA from the sums of chunks of 64 or 128 tokens

@@ -594,7 +594,7 @@ hipError_t launch_scan_bwd_ddt(const ScanBwdArgs& a, int tokens, hipStream_t s) 
 
 size_t scan_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N,
                                 ssm_dtype_t dtype) {
-    if (scan_bwd_mfma_supported(P, N, dtype)) return scan_bwd_mfma_workspace_bytes(B, L, H, P, G, N);
+    if (scan_bwd_mfma_supported(H, P, G, N, dtype)) return scan_bwd_mfma_workspace_bytes(B, L, H, P, G, N);
     ScanBwdArgs a{};
     a.B = B; a.L = L; a.H = H; a.P = P; a.G = G; a.N = N;
     a.chunks = (L + kQ - 1) / kQ;
@@ -609,7 +609,7 @@ int64_t scan_bwd_blocks(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, i
 }
 
 hipError_t launch_scan_bwd(ScanBwdArgs a, void* workspace, ssm_dtype_t dtype, hipStream_t s) {
-    if (scan_bwd_mfma_supported(a.P, a.N, dtype)) return launch_scan_bwd_mfma(a, workspace, s);
+    if (scan_bwd_mfma_supported(a.H, a.P, a.G, a.N, dtype)) return launch_scan_bwd_mfma(a, workspace, s);
     a.chunks = (a.L + kQ - 1) / kQ;
     lay_out(a, static_cast<uint8_t*>(workspace));
     return dtype == SSM_BF16 ? launch_general<BF16>(a, s) : launch_general<F32>(a, s);

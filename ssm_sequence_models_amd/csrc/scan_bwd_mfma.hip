@@ -1091,8 +1091,10 @@ hipError_t launch_typed(const ScanBwdArgs& a, hipStream_t s) {
 
 }  // namespace
 
-bool scan_bwd_mfma_supported(int64_t P, int64_t N, ssm_dtype_t dtype) {
-    return dtype == SSM_BF16 && P == kFP && (N == 64 || N == 128);
+// 128 rows of tokens within 2^32 bytes: the lanes' offsets into a chunk have 32 bits
+bool scan_bwd_mfma_supported(int64_t H, int64_t P, int64_t G, int64_t N, ssm_dtype_t dtype) {
+    const int64_t most = int64_t{1} << 23;
+    return dtype == SSM_BF16 && P == kFP && (N == 64 || N == 128) && H <= most / P && G <= most / N;
 }
 
 size_t scan_bwd_mfma_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N) {

@@ -71,6 +71,15 @@ def test_widths(C, dtype):
         _run(x, w, b, z, d, kind, 1, gate)
 
 
+@pytest.mark.parametrize("C", [2, 9, 15, 1023, 1024, 1025, 2047, 4097, 8191])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_widths_beside_a_vector(C, dtype):
+    """A last vector that overlaps the one before it, beside every change of team."""
+    for gate, kind, groups in (("before", "rms", 1), ("after", "layer", 1), ("none", "layer", 3)):
+        x, w, b, z, d = _inputs(9, C * groups if C < 5000 else C, gate, True, dtype, seed=C)
+        _run(x, w, b, z, d, kind, groups if C < 5000 else 1, gate)
+
+
 @pytest.mark.parametrize("rows", [1, 2, 3, 4, 5, 255, 1030, 4100])
 @pytest.mark.parametrize("C,groups", [(24, 3), (1024, 2), (560, 1)])
 def test_rows_and_groups(rows, C, groups):

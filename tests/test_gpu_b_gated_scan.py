@@ -203,6 +203,25 @@ def test_chunks_continue():
         check_err(t, ref, name, F32)
 
 
+def test_rows_far_apart():
+    """A row stride from 2^26 elements on (beyond the lanes' 32-bit offsets), offsets past 2^32
+    bytes: the outputs of the packed input.  Both round the same sums once, and fp32 sums of the
+    same terms differ by 1e-5 of them at most, so they are a step of bf16 apart at most."""
+    import ssm_sequence_models_amd as ssm
+    L, C, row = 140, 66, 1 << 26
+    x, gate, dy, _, _ = _inputs(1, L, C, "sigmoid", BF16, False, seed=9)
+    wide = torch.empty(L * row, dtype=BF16, device="cuda").as_strided((1, L, C), (L * row, row, 1))
+    wide.copy_(x)
+    x, gate, dy = x.cuda(), gate.cuda(), dy.cuda()
+    want = ssm.gated_scan_fwd(x, gate, form="sigmoid")
+    got = ssm.gated_scan_fwd(wide, gate, form="sigmoid")
+    want += ssm.gated_scan_bwd(x, gate, dy, form="sigmoid")
+    got += ssm.gated_scan_bwd(wide, gate, dy, form="sigmoid")
+    for a, b in zip(want, got):
+        step = 2 * torch.finfo(a.dtype).eps / 2 if a.dtype == BF16 else 0.0
+        assert torch.allclose(a.double(), b.double(), rtol=1.01 * step + 1e-5, atol=1e-5)
+
+
 @pytest.mark.parametrize("C", [1, 7, 64, 300])
 @pytest.mark.parametrize("form", ["log", "sigmoid"])
 @pytest.mark.parametrize("dtype", [BF16, F32])

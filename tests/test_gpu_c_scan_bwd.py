@@ -96,6 +96,12 @@ def test_lengths(L, N):
         _compare(_inputs(1, L, 2, 1, 64, N, dtype, True, seed=L))
 
 
+@pytest.mark.parametrize("B,H,G,N", [(2, 48, 1, 64), (1, 95, 1, 64), (2, 50, 2, 128)])
+def test_many_heads(B, H, G, N):
+    """On both sides of the number of heads from which one block walks over a row's chunks."""
+    _compare(_inputs(B, 200, H, G, 64, N, BF16, True, seed=B * H))
+
+
 @pytest.mark.parametrize("kind", ["every", "edges", "back", "random"])
 @pytest.mark.parametrize("dtype,P,N", [(BF16, 64, 128), (BF16, 64, 64), (F32, 16, 16)])
 def test_packed(kind, dtype, P, N):

@@ -159,6 +159,15 @@ def test_gated_scan_workspace(lib):
     assert _gstep(lib, state=None) == 1
 
 
+def test_scan_bwd_widest_rows(lib):
+    """Rows beyond the matrix-core kernels' 32-bit offsets are laid out for the general ones (the
+    same for both types), the widest row within them is not."""
+    import ssm_sequence_models_amd as s
+    size = lambda H, dt: s.scan_bwd_workspace_size(1, 128, H, 64, 1, 64, dt)  # noqa: E731
+    assert size((1 << 17) + 1, torch.bfloat16) == size((1 << 17) + 1, torch.float32)
+    assert size(1 << 17, torch.bfloat16) != size(1 << 17, torch.float32)
+
+
 def test_gated_scan_binding_refusals():
     import ssm_sequence_models_amd as ssm
     x = torch.zeros(1, 4, 8)
