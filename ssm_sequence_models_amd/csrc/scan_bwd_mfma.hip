@@ -292,26 +292,40 @@ __global__ void __launch_bounds__(256, 2) sbf_states_kernel(ScanBwdArgs a) {
     const uint32_t vb = static_cast<uint32_t>((tid / BP) * b_row * 2 + 16 * (tid % BP));
     const uint32_t vo = static_cast<uint32_t>(w * 1024 + lane * 16);
 
+    // The next chunk's loads, none of them under a branch or used here: a use would wait for all
+    // of them, and behind a branch around some the wait for one is a wait for all.  Rows past the
+    // row's end are its last, set to 0 when they are staged.
     u4 rb[BL], rx[XL];
-    float rs = 0.0f;
+    float rs0, rs1, rth;
+    int nv;
     auto load = [&](int64_t c) __attribute__((always_inline)) {
         const int64_t t0 = c * kFQ;
-        const int nv = a.L - t0 < kFQ ? static_cast<int>(a.L - t0) : kFQ;
+        nv = a.L - t0 < kFQ ? static_cast<int>(a.L - t0) : kFQ;
+        const float* rec = a.decay + (bh * a.chunks + c) * 5 * kFQ + (tid & (kFQ - 1));
+        rs0 = rec[rev ? 2 * kFQ : 3 * kFQ];
+        rs1 = rec[4 * kFQ];
+        rth = a.through[bh * a.chunks + c];
         const char* xp = reinterpret_cast<const char*>(xs + t0 * x_row);
         const char* bp = reinterpret_cast<const char*>(bs + t0 * b_row);
+        if (nv == kFQ) {
+            const uint32_t ox = here(vx), ob = here(vb);
 #pragma unroll
-        for (int i = 0; i < XL; ++i) {
-            rx[i] = u4{0, 0, 0, 0};
-            if ((tid >> 3) + XR * i < nv) rx[i] = *reinterpret_cast<const u4any*>(xp + i * (2 * XR) * x_row + vx);
-        }
+            for (int i = 0; i < XL; ++i) rx[i] = *reinterpret_cast<const u4any*>(xp + i * (2 * XR) * x_row + ox);
 #pragma unroll
-        for (int i = 0; i < BL; ++i) {
-            rb[i] = u4{0, 0, 0, 0};
-            if (tid / BP + BR * i < nv) rb[i] = *reinterpret_cast<const u4any*>(bp + i * (2 * BR) * b_row + vb);
-        }
-        if (tid < kFQ) {
-            const float* rec = a.decay + (bh * a.chunks + c) * 5 * kFQ + tid;
-            rs = rev ? rec[2 * kFQ] : rec[3 * kFQ] * rec[4 * kFQ];
+            for (int i = 0; i < BL; ++i) rb[i] = *reinterpret_cast<const u4any*>(bp + i * (2 * BR) * b_row + ob);
+            asm volatile("");  // not merged with the other path
+        } else {
+            const int id = here(tid);
+#pragma unroll
+            for (int i = 0; i < XL; ++i) {
+                const int r = (id >> 3) + XR * i < nv ? (id >> 3) + XR * i : nv - 1;
+                rx[i] = *reinterpret_cast<const u4any*>(xp + 2 * r * x_row + 16 * (id & 7));
+            }
+#pragma unroll
+            for (int i = 0; i < BL; ++i) {
+                const int r = id / BP + BR * i < nv ? id / BP + BR * i : nv - 1;
+                rb[i] = *reinterpret_cast<const u4any*>(bp + 2 * r * b_row + 16 * (id % BP));
+            }
         }
     };
     const int64_t steps = SEQ ? a.chunks : 1;
@@ -333,6 +347,15 @@ __global__ void __launch_bounds__(256, 2) sbf_states_kernel(ScanBwdArgs a) {
     const int xo = down_off<128>(4 * g4, li) ^ (w << 5), bo = down_off<RB>(4 * g4, li);
     for (int64_t i = 0; i < steps; ++i) {
         const int64_t c = c0 + i * dc;
+        if (nv < kFQ) {
+#pragma unroll
+            for (int j = 0; j < XL; ++j)
+                if ((tid >> 3) + XR * j >= nv) rx[j] = u4{0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < BL; ++j)
+                if (tid / BP + BR * j >= nv) rb[j] = u4{0, 0, 0, 0};
+        }
+        const float th = rth;
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < XL; ++j)
@@ -340,12 +363,11 @@ __global__ void __launch_bounds__(256, 2) sbf_states_kernel(ScanBwdArgs a) {
 #pragma unroll
         for (int j = 0; j < BL; ++j)
             *reinterpret_cast<u4*>(sb + piece<RB>(tid / BP, tid % BP) + j * BR * RB) = rb[j];
-        if (tid < kFQ) scale[tid] = rs;
+        if (tid < kFQ) scale[tid] = rev ? rs0 : rs0 * rs1;
         __syncthreads();
-        if (i + 1 < steps) load(c + dc);
+        if (SEQ) load(i + 1 < steps ? c + dc : c);  // the last once more, not used
         if (SEQ) {
             store(c);
-            const float th = a.through[bh * a.chunks + c];
             if (th == 0.0f) {  // nothing passes a start, whatever the state was
 #pragma unroll
                 for (int n = 0; n < NT; ++n) acc[n] = f4{0, 0, 0, 0};
