@@ -571,7 +571,6 @@ __global__ void __launch_bounds__(kGThreads) gscan_bwd_kernel(GArgs a) {
         carry = fold_segments(a, p, sp[1], a.nseg - 1, -1, a.nseg - 1 - seg, 2, carry);
         __syncthreads();
     }
-    using T = typename S::T;
     // (A, H) of the segment's tokens before the tile
     auto before_tile = [&](int64_t tile) __attribute__((always_inline)) {
         const float* ck = a.ckpt + (p.b * a.tiles + tile) * 2 * a.C + p.c;

@@ -426,7 +426,8 @@ __global__ void __launch_bounds__(512) sb_grad_kernel(ScanBwdArgs a) {
 template <int Q>
 __global__ void __launch_bounds__(128 * kAnchor) sb_ddt_kernel(ScanBwdArgs a) {
     constexpr int K = Q / 64;
-    __shared__ double usum[2][kAnchor], vsum[2][kAnchor];
+    __shared__ double usum[2][kAnchor], vsum[2][kAnchor], most[2][kAnchor];
+    __shared__ float thr[2][kAnchor];
     const int64_t ranges = (a.chunks + kAnchor - 1) / kAnchor, br = a.B * ranges;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, hw = wave / kAnchor, ci = wave % kAnchor;
     const int64_t h = blockIdx.x / br * 2 + hw, b = blockIdx.x % br / ranges, range = blockIdx.x % ranges;
@@ -472,9 +473,24 @@ __global__ void __launch_bounds__(128 * kAnchor) sb_ddt_kernel(ScanBwdArgs a) {
             q[k] += s + before;
             before += __shfl(s + v[k], 63);
         }
+        // |f_last <G, S>| of this chunk is at most f_last |G| |S|
+        const float th = a.through[at];
+        double norms = 0.0;
+        if constexpr (Q != kQ) {
+            const int i = lane & 7;
+            float ns = i < a.N / 16 ? in[kSums * Q + 64 + i] : 0.0f, ng = i < a.N / 16 ? in[kSums * Q + 72 + i] : 0.0f;
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) {
+                ns += __shfl_xor(ns, o);
+                ng += __shfl_xor(ng, o);
+            }
+            norms = sqrt(static_cast<double>(ns)) * sqrt(static_cast<double>(ng));
+        }
         if (lane == 0) {
             usum[hw][ci] = after;
             vsum[hw][ci] = before;
+            thr[hw][ci] = th;
+            most[hw][ci] = 1.00001 * th * norms;
         }
     }
     __syncthreads();
@@ -482,27 +498,17 @@ __global__ void __launch_bounds__(128 * kAnchor) sb_ddt_kernel(ScanBwdArgs a) {
     // f_last <G, S> of this chunk: from the range's last chunk back (nothing across a start or a
     // decay to 0)
     double pass = 0.0;
-    for (int64_t d = Q == 64 ? c : last; d >= c; --d) {
-        const int64_t da = at + d - c;
-        const float th = a.through[da];
-        const float* tail = a.sums + da * (kSums * Q + kSumTail) + kSums * Q;
-        if (th == 0.0f) {
-            pass = 0.0;
-        } else if (Q == 64) {
-            pass = static_cast<double>(tail[64]) + tail[65];
-        } else if (d == last) {
-            pass = a.anchor[(b * a.H + h) * ranges + range];
-        } else {
-            float ns = 0.0f, ng = 0.0f;
-            for (int i = 0; i < a.N / 16; ++i) {
-                ns += tail[64 + i];
-                ng += tail[72 + i];
-            }
-            const double most = 1.00001 * th * sqrt(static_cast<double>(ns)) * sqrt(static_cast<double>(ng));
-            const int64_t k = d - range * kAnchor;
+    if constexpr (Q == kQ) {
+        if (thr[hw][ci] != 0.0f) pass = static_cast<double>(in[kSums * Q + 64]) + in[kSums * Q + 65];
+    } else {
+        const int end = static_cast<int>(last - range * kAnchor);
+        if (thr[hw][end] != 0.0f) pass = a.anchor[(b * a.H + h) * ranges + range];
+        for (int k = end - 1; k >= ci; --k) {
+            const double m = most[hw][k];
             pass += usum[hw][k + 1] - vsum[hw][k];
-            if (pass > most) pass = most;
-            if (pass < -most) pass = -most;
+            if (pass > m) pass = m;
+            if (pass < -m) pass = -m;
+            if (thr[hw][k] == 0.0f) pass = 0.0;
         }
     }
     const double A = a.A[h];

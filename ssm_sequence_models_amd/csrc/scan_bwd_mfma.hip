@@ -23,7 +23,7 @@
 //               far below u and v, |G| |S| f bounds it and with it the error
 // One kernel for dC and the rest together read S, G and dy once, but held 300 registers a lane:
 // at two wavefronts a SIMD (LDS) it spilled, and took 2318 us at 4 x 8192 tokens x 64 heads,
-// dstate 128, where the two take 168 + 486 us.
+// dstate 128, where the two take 168 + 478 us.
 //
 // Operands: x, dy, B and C are exact in bf16.  The fp32 operands S and G and the scaled x and dy
 // of sbf_states are taken in three bf16 parts (24 bits, nothing lost: ddt and dA are fp32
@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(256) sbf_anchor_kernel(ScanBwdArgs a) {
 //   0-7   s tile st (1, 2, .. and 7, 6, .. on one SIMD: nine pair tiles each): the pairs, W's sums, dx
 //   8-15  n tile nt: G's parts, dB from behind the chunk and v; the head before's sums
 // LDS holds one block a CU, so the roles are what hides one's LDS waits behind the other's
-// products: as eight wavefronts that did both in turn it took 541 us where this takes 486 (227
+// products: as eight wavefronts that did both in turn it took 541 us where this takes 478 (227
 // and 190 us at one row of 32768 tokens, 24 heads, dstate 64).  The t tiles are taken in pairs
 // from an even one on, so that the bodies a wavefront may start in are few and keep within 128
 // registers: from any one on they were 8, with 51 spilled registers where these spill 28
@@ -1032,6 +1032,7 @@ __global__ void __launch_bounds__(256) sbf_join_kernel(ScanBwdArgs a) {
     const float* p = (blockIdx.y ? a.dC_head : a.dB_head) + i;
     f4 s = *reinterpret_cast<const f4*>(p);
     const int64_t slabs = a.splits + (blockIdx.y ? a.dc_splits : 0);
+#pragma unroll 8
     for (int64_t j = 1; j < slabs; ++j) s += *reinterpret_cast<const f4*>(p + j * n);
     uint16_t* o = blockIdx.y ? static_cast<uint16_t*>(a.dC) + i / GN * a.dc_row
                              : static_cast<uint16_t*>(a.dB) + i / GN * a.db_row;
