@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(128 * kAnchor) sb_ddt_kernel(ScanBwdArgs a) {
         double u[K], v[K];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int t = lane + 64 * k, j = t >> 4;
+            const int t = lane + 64 * k;
             dts[k] = t0 + t < a.L ? (Q == 128 ? a.decay[(at * 5 + 4) * Q + t] : a.dt[(b * a.L + t0 + t) * a.H + h]) : 0.0f;
             const float coff = in[kSumColOff * Q + t], vt = in[kSumV * Q + t];
             u[k] = in[kSumU * Q + t];
@@ -458,8 +458,19 @@ __global__ void __launch_bounds__(128 * kAnchor) sb_ddt_kernel(ScanBwdArgs a) {
             direct[k] = ((coff + cdiag) + in[kSumDiag * Q + t]) + vt;
             q[k] = from_lane<16>(in[kSumRowOff * Q + t], lane) + before_lane<16>(static_cast<double>(coff) * dts[k], lane);
             q[k] += in[kSumRowDiag * Q + t];
-            for (int j2 = j + 1; j2 < Q / 16; ++j2)
-                for (int i = 0; i < j; ++i) q[k] += in[kSums * Q + 8 * j2 + i];
+        }
+        if constexpr (Q != kQ) {  // the tile pairs around the token's tile
+#pragma unroll
+            for (int j2 = 2; j2 < Q / 16; ++j2)
+#pragma unroll
+                for (int i = 0; i < j2 - 1; ++i) {
+                    const double w = in[kSums * Q + 8 * j2 + i];
+#pragma unroll
+                    for (int k = 0; k < K; ++k) {
+                        const int j = (lane >> 4) + 4 * k;
+                        q[k] += i < j && j < j2 ? w : 0.0;
+                    }
+                }
         }
 #pragma unroll
         for (int k = K - 1; k >= 0; --k) {
