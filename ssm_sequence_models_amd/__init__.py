@@ -9,7 +9,9 @@ import fails loudly if the library has not been built.
 Sources of the operations (page title and section): the length-generalization reading
 notes on arXiv:2507.02782v2, Sec. 2.1 Eq. (1), Sec. 2.5 Eq. (4), Sec. 2.6 (scan with
 initial / final state); the causal-conv1d tutorial ch. 7 (conv state S / F, decode update,
-cache_seqlens, conv_state_indices, seq_idx, and the backward with state gradients).
+cache_seqlens, conv_state_indices, seq_idx, and the backward with state gradients).  The
+scan's complete backward, the gated norm and the per-channel gated recurrence are formed from
+the same equations; their formulas stand with the declarations in the header.
 """
 from __future__ import annotations
 
