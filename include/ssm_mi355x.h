@@ -470,7 +470,8 @@ ssm_status_t ssm_scan_bwd(const void* x, const float* dt, const float* A, const 
  *                  into segments and, backward, the state before every 128th token
  * States and sums in fp32; outputs rounded once; deterministic.
  *
- * ssm_gated_scan_fwd   final_state may alias initial_state.  seqlen = 0: final = initial.
+ * ssm_gated_scan_fwd   final_state may be initial_state; outputs must not overlap inputs
+ *     otherwise (y in place of x or gate is not supported).  seqlen = 0: final = initial.
  * ssm_gated_scan_bwd   from dy and dfinal_state, with E_t the gradient token t hands to
  *     h_{t-1}:  D_t = dy_t + E_{t+1},  E_t = a_t D_t,  E_L = dfinal_state,  dx_t = i_t D_t,
  *     dinitial_state = E_0,  dgate_t = D_t a_t h_{t-1} (log form) or

@@ -746,7 +746,8 @@ def gated_scan_fwd(x, gate, form="sigmoid", initial_state=None, seq_idx=None,
     Sec. 2.1 Eq. (1), a state of one value per channel): a = exp(gate), i = 1 (form "log") or
     a = sigmoid(gate), i = 1 - a (form "sigmoid").  x, gate [b, L, C] (consecutive channels,
     tokens at any one stride); initial_state [b, C] fp32 (may be the same tensor as
-    final_state); seq_idx [b, L] int32.  Returns (y [b, L, C], final_state or None)."""
+    final_state; y must not overlap an input); seq_idx [b, L] int32.  Returns (y [b, L, C],
+    final_state or None)."""
     B, L, C, x_row, gate_row = _gated_args(x, gate, form)
     _need(initial_state, "initial_state", torch.float32, (B, C))
     _need(seq_idx, "seq_idx", torch.int32, (B, L))

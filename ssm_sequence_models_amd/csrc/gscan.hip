@@ -41,10 +41,18 @@
 // not reach the next.  Everything is fp32; outputs are rounded once.
 #include <type_traits>
 
+#include "gscan_groups.h"
 #include "internal.h"
 
 namespace ssm {
 namespace {
+
+constexpr bool g_splits_sound() {
+    for (int64_t C = 1; C <= 300; ++C)
+        if (!g_split_sound(C)) return false;
+    return true;
+}
+static_assert(g_splits_sound(), "a channel in two blocks");
 
 constexpr int kGW = 8;              // wavefronts a block
 constexpr int kGL = 8;              // tokens a lane and tile
@@ -120,8 +128,9 @@ struct GRaw {
 };
 
 // A lane's place: channels c0, c0 + 1 of the tokens 8 half .. 8 half + 7 of a wavefront's 16, and
-// one channel, c, of all that is joined over spans.  Past the last pair lanes take the last two
-// channels once more (of one channel, that one twice): the same values to the same places.
+// one channel, c, of all that is joined over spans.  Past the group's last pair lanes take its last
+// two channels once more (of one channel, that one twice): the same values to the same places, by
+// the same block (gscan_groups.h).
 struct GPos {
     int64_t b, c, c0;
     int lane, wave, half;
@@ -219,11 +228,12 @@ __device__ __forceinline__ GPos g_pos(const GArgs& a, int64_t row_group) {
     p.lane = threadIdx.x & 63;
     p.half = p.lane >> 5;
     p.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t groups = (a.C + 63) / 64;
+    const int64_t groups = g_groups(a.C);
     p.b = row_group / groups;
-    const int64_t c = (row_group % groups) * 64 + 2 * (p.lane & 31);
-    p.live = c + 1 < a.C || (c + 1 == a.C && p.half == 1);
-    p.c0 = c + 1 < a.C ? c : a.C > 1 ? a.C - 2 : 0;
+    const GChannels g = g_channels(a.C, row_group % groups);
+    const int64_t c = g.first + 2 * (p.lane & 31);
+    p.live = c + 1 < g.end || (c + 1 == g.end && p.half == 1);
+    p.c0 = g_pair(g, p.lane & 31);
     p.c = a.C > 1 ? p.c0 + p.half : 0;
     return p;
 }
@@ -418,7 +428,8 @@ __global__ void __launch_bounds__(kGThreads) gscan_fwd_kernel(GArgs a) {
         else if (a.h0) carry = a.h0[p.b * a.C + p.c];
         carry = fold_segments(a, p, sp[(first & 1) ^ 1], 0, 1, seg, 1, carry);
         // every wavefront has its initial state in hand before the first barrier, hence before
-        // wavefront 0 stores the final state
+        // wavefront 0 stores the final state, which may lie in the same place; no other block reads
+        // these channels' state (cut rows take it from the workspace)
         asm volatile("" : "+v"(carry));
     }
     auto step = [&](int64_t tile, const GRaw<S, false, SEQ>& cur, auto whole) __attribute__((always_inline)) {
@@ -720,7 +731,7 @@ __global__ void __launch_bounds__(256) gscan_step_kernel(GArgs a, float* pool, c
 //   1 x 1024 x 1024   20 / 22     one segment of 8 tiles: 15 / 31
 constexpr int64_t kFill = 256, kLeast = 4, kWhole = 8;
 void g_cut(GArgs& a, bool bwd) {
-    const int64_t blocks = a.B * ((a.C + 63) / 64);
+    const int64_t blocks = a.B * g_groups(a.C);
     a.tiles = (a.L + kGTile - 1) / kGTile;
     int64_t want = (kFill + blocks - 1) / blocks;
     if (!bwd && (2 * blocks >= kFill || a.tiles <= kWhole)) want = 1;
@@ -747,7 +758,7 @@ GArgs g_args(const GscanCall& c) {
 
 template <class S, bool SIG, bool SEQ>
 hipError_t fwd_typed(const GArgs& a, hipStream_t s) {
-    const int64_t groups = a.B * ((a.C + 63) / 64);
+    const int64_t groups = a.B * g_groups(a.C);
     if (a.nseg > 1) {
         gscan_fwd_kernel<S, SIG, SEQ, true><<<static_cast<uint32_t>(groups * (a.nseg - 1)), kGThreads, 0, s>>>(a);
         const hipError_t e = hipGetLastError();
@@ -758,7 +769,7 @@ hipError_t fwd_typed(const GArgs& a, hipStream_t s) {
 }
 template <class S, bool SIG, bool SEQ>
 hipError_t bwd_typed(const GArgs& a, hipStream_t s) {
-    const uint32_t grid = static_cast<uint32_t>(a.B * ((a.C + 63) / 64) * a.nseg);
+    const uint32_t grid = static_cast<uint32_t>(a.B * g_groups(a.C) * a.nseg);
     if (a.nseg > 1) gscan_bwd_states_kernel<S, SIG, SEQ, true><<<grid, kGThreads, 0, s>>>(a);
     else gscan_bwd_states_kernel<S, SIG, SEQ, false><<<grid, kGThreads, 0, s>>>(a);
     const hipError_t e = hipGetLastError();
@@ -790,7 +801,7 @@ int64_t gscan_blocks(int64_t B, int64_t L, int64_t C) {
     GArgs a{};
     a.B = B; a.L = L; a.C = C;
     g_cut(a, true);  // the forward has at most as many segments
-    return B * ((C + 63) / 64) * a.nseg;
+    return B * g_groups(C) * a.nseg;
 }
 
 size_t gscan_workspace_bytes(int64_t B, int64_t L, int64_t C, bool bwd) {
