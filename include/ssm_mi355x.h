@@ -437,7 +437,8 @@ ssm_status_t ssm_scan_bwd_initial_state(const float* dt, const float* A, const v
  * 32768); dt * A finite.  Sums and states in fp32 (sums of log decays in double); outputs
  * rounded once; deterministic.  Outputs must not overlap inputs (dinitial_state ==
  * dfinal_state is refused).  A non-finite value may reach every token of the 128-token chunks
- * (of the row, from its start) that its sequence reaches, other sequences' among them.
+ * (of the row, from its start) that its sequence has tokens in, other sequences' among them,
+ * and no token of other chunks.
  * seqlen = 0: dinitial_state = dfinal_state (or zeros), dA = 0.  batch = 0: dA = 0.
  * ------------------------------------------------------------------------------------- */
 size_t ssm_scan_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim,

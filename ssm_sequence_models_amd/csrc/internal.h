@@ -314,6 +314,7 @@ struct ScanBwdArgs {
     // matrix cores only
     float* decay;      // [B, H, chunks, 5, 128]: sums of log2 a (hi, lo), f, e, dt
     int32_t* starts;   // [B, chunks, 128]: sequence starts so far in the chunk
+    int2* bounds;      // [B, chunks]: tokens before the chunk's first start, and before its last
     int64_t splits, split_heads;  // ranges of a group's heads a chunk, heads in each
     int64_t dc_splits, dc_heads;  // the same for dC's part from before the chunk
     float* anchor;     // [B, H, ceil(chunks / kAnchor)]: f_last <G, S> of the last chunk of each

@@ -62,6 +62,7 @@ __device__ __forceinline__ f4 mfma4(const f4& a, const f4& b, f4 c) {
 struct ChunkDecay {
     double cs[kQ];   // sum of log2 a over the chunk's tokens 0 .. t
     int starts[kQ];  // sequence starts among tokens 0 .. t
+    int head, tail;  // tokens before the first start, and before the last
     float f[kQ];     // f_t
     float e[kQ];     // e_t
     float dt[kQ];    // dt_t (0 past the row's end)
@@ -94,6 +95,11 @@ __device__ __forceinline__ void chunk_decay(ChunkDecay& cd, const float* dt, int
         cd.e[t] = r == rend ? __builtin_amdgcn_exp2f(static_cast<float>(end - s)) : 0.0f;
         cd.dt[t] = d;
         if (t == 63) cd.through = cd.f[63];
+        const int head = __popcll(__ballot(r == 0)), tail = __popcll(__ballot(r != rend));
+        if (t == 0) {
+            cd.head = head;
+            cd.tail = tail;
+        }
     }
     __syncthreads();
 }
@@ -127,21 +133,23 @@ __device__ __forceinline__ f4 load4(const uint16_t* p) {
 }
 
 // A row-major view [tokens][cols] of the chunk's tokens: zeros outside.  What lies outside is read
-// from the last row and column instead and replaced, so no load is under a branch and waits for
-// another.  W: cols is a multiple of 16, so four consecutive columns are inside or outside.
+// from the last row and column instead (of no rows, the first) and replaced, so no load is under a
+// branch and waits for another.  W: cols is a multiple of 16, so four consecutive columns are inside
+// or outside.
 template <class S, bool W>
 struct View {
     const typename S::T* p;
     int64_t row;
     int rows, cols;
+    __device__ __forceinline__ int row_at(int r) const { return r < rows ? r : rows > 0 ? rows - 1 : 0; }
     __device__ __forceinline__ float at(int r, int c) const {
-        const float v = S::load(p, (r < rows ? r : rows - 1) * row + (c < cols ? c : cols - 1));
+        const float v = S::load(p, row_at(r) * row + (c < cols ? c : cols - 1));
         return r < rows && c < cols ? v : 0.0f;
     }
     // operand with the contraction along the row: row r, columns k .. k + 3
     __device__ __forceinline__ f4 along(int r, int k) const {
         if constexpr (W) {
-            const f4 v = load4(p + (r < rows ? r : rows - 1) * row + k);  // k < cols: called for 16 at a time
+            const f4 v = load4(p + row_at(r) * row + k);  // k < cols: called for 16 at a time
             return r < rows ? v : f4{0, 0, 0, 0};
         } else {
             return f4{at(r, k), at(r, k + 1), at(r, k + 2), at(r, k + 3)};
@@ -166,10 +174,14 @@ __global__ void __launch_bounds__(256) sb_local_kernel(ScanBwdArgs a) {
     using T = typename S::T;
     const int64_t tok = w.b * a.L + w.t0;
     const int P = static_cast<int>(a.P), N = static_cast<int>(a.N);
+    // Tokens across a start hand nothing on (forward those before the chunk's last start, in reverse
+    // those from its first on).  Their factor is 0, and so are both operands: a NaN or infinity of a
+    // sequence that ends in this chunk, times 0, would reach the chunks behind it.
+    const int lo = rev ? 0 : cd.tail, hi = rev && cd.head < w.nv ? cd.head : w.nv;
     const View<S, W> xv{static_cast<const T*>(rev ? a.dy : a.x) + tok * (rev ? a.dy_row : a.x_row) + w.h * P,
-                     rev ? a.dy_row : a.x_row, w.nv, P};
+                     rev ? a.dy_row : a.x_row, hi, P};
     const View<S, W> bv{static_cast<const T*>(rev ? a.C : a.Bm) + tok * (rev ? a.c_row : a.b_row) + w.g * N,
-                     rev ? a.c_row : a.b_row, w.nv, N};
+                     rev ? a.c_row : a.b_row, hi, N};
     float* out = (rev ? a.grads : a.states) + ((w.b * a.H + w.h) * a.chunks + w.c) * a.P * a.N;
     const int lane = threadIdx.x & 63, li = lane & 15, g4 = lane >> 4;
     if (!rev && threadIdx.x == 0) a.through[(w.b * a.H + w.h) * a.chunks + w.c] = cd.through;
@@ -192,6 +204,16 @@ __global__ void __launch_bounds__(256) sb_local_kernel(ScanBwdArgs a) {
             for (int i = 0; i < kLP; ++i) x[i] = xv.down(k + 4 * g4, p0 + 16 * i + li) * scale;
 #pragma unroll
             for (int i = 0; i < kLN; ++i) y[i] = bv.down(k + 4 * g4, n0 + 16 * i + li);
+            if (lo > 0) {  // the same for the whole block
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const bool in = k + 4 * g4 + j >= lo;
+#pragma unroll
+                    for (int i = 0; i < kLP; ++i) x[i][j] = in ? x[i][j] : 0.0f;
+#pragma unroll
+                    for (int i = 0; i < kLN; ++i) y[i][j] = in ? y[i][j] : 0.0f;
+                }
+            }
 #pragma unroll
             for (int i = 0; i < kLP; ++i)
 #pragma unroll

@@ -228,6 +228,10 @@ __global__ void __launch_bounds__(256) sbf_decay_kernel(ScanBwdArgs a) {
     if (h0 == 0 && threadIdx.x < 64) {
         a.starts[(b * a.chunks + c) * kFQ + lane] = r0;
         a.starts[(b * a.chunks + c) * kFQ + 64 + lane] = r1;
+        // (every lane counts: the ballots are the wavefront's)
+        const int head = __popcll(__ballot(r0 == 0)) + __popcll(__ballot(r1 == 0));
+        const int tail = __popcll(__ballot(r0 != rend)) + __popcll(__ballot(r1 != rend));
+        if (lane == 0) a.bounds[b * a.chunks + c] = int2{head, tail};
     }
     for (int j = 0; j < 4; ++j) {
         const int h = (threadIdx.x >> 6) + 4 * j;
@@ -297,6 +301,7 @@ __global__ void __launch_bounds__(256, 2) sbf_states_kernel(ScanBwdArgs a) {
     // row's end are its last, set to 0 when they are staged.
     u4 rb[BL], rx[XL];
     float rs0, rs1, rth;
+    int2 rbound;
     int nv;
     auto load = [&](int64_t c) __attribute__((always_inline)) {
         const int64_t t0 = c * kFQ;
@@ -305,6 +310,7 @@ __global__ void __launch_bounds__(256, 2) sbf_states_kernel(ScanBwdArgs a) {
         rs0 = rec[rev ? 2 * kFQ : 3 * kFQ];
         rs1 = rec[4 * kFQ];
         rth = a.through[bh * a.chunks + c];
+        rbound = a.bounds[b * a.chunks + c];
         const char* xp = reinterpret_cast<const char*>(xs + t0 * x_row);
         const char* bp = reinterpret_cast<const char*>(bs + t0 * b_row);
         if (nv == kFQ) {
@@ -347,13 +353,22 @@ __global__ void __launch_bounds__(256, 2) sbf_states_kernel(ScanBwdArgs a) {
     const int xo = down_off<128>(4 * g4, li) ^ (w << 5), bo = down_off<RB>(4 * g4, li);
     for (int64_t i = 0; i < steps; ++i) {
         const int64_t c = c0 + i * dc;
-        if (nv < kFQ) {
+        // tokens that hand nothing on: past the row's end, and across a start (forward those before
+        // the chunk's last start, in reverse those from its first on).  Their factor is 0, and so are
+        // both operands here: a NaN or infinity of a sequence that ends in this chunk, times 0, would
+        // reach the chunks behind it
+        const int lo = rev ? 0 : rbound.y, hi = rev && rbound.x < nv ? rbound.x : nv;
+        if (lo > 0 || hi < kFQ) {
 #pragma unroll
-            for (int j = 0; j < XL; ++j)
-                if ((tid >> 3) + XR * j >= nv) rx[j] = u4{0, 0, 0, 0};
+            for (int j = 0; j < XL; ++j) {
+                const int t = (tid >> 3) + XR * j;
+                if (t < lo || t >= hi) rx[j] = u4{0, 0, 0, 0};
+            }
 #pragma unroll
-            for (int j = 0; j < BL; ++j)
-                if (tid / BP + BR * j >= nv) rb[j] = u4{0, 0, 0, 0};
+            for (int j = 0; j < BL; ++j) {
+                const int t = tid / BP + BR * j;
+                if (t < lo || t >= hi) rb[j] = u4{0, 0, 0, 0};
+            }
         }
         const float th = rth;
         __syncthreads();
@@ -507,6 +522,7 @@ __global__ void __launch_bounds__(512, 4) sbf_dc_kernel(ScanBwdArgs a) {
     const int64_t t0 = c * kFQ, tok = b * a.L + t0;
     const int nv = a.L - t0 < kFQ ? static_cast<int>(a.L - t0) : kFQ;
     const int nt = wave % NT, th0 = NT == 8 ? 0 : (wave / NT) * TT;
+    const bool fresh = a.bounds[b * a.chunks + c].x == 0;  // a start on its first token: S is another sequence's
     const int row = tid >> 3;
     const uint32_t vdy = static_cast<uint32_t>(row * a.dy_row * 2 + 16 * (tid & 7));
     const uint32_t vs = static_cast<uint32_t>(nt * 4096 + (g4 >> 1) * 1024 + (g4 & 1) * 512 + li * 16);
@@ -559,7 +575,7 @@ __global__ void __launch_bounds__(512, 4) sbf_dc_kernel(ScanBwdArgs a) {
             float v[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                v[e] = rS[2 * kk + (e >> 2)][e & 3];
+                v[e] = fresh ? 0.0f : rS[2 * kk + (e >> 2)][e & 3];
                 norm += v[e] * v[e];
             }
             split(v, Sp[kk]);
@@ -597,7 +613,7 @@ __global__ void __launch_bounds__(512, 4) sbf_dc_kernel(ScanBwdArgs a) {
             }
             settle(acc[jj]);
             settle(w);
-            u[jj & 3] = w * ft;
+            u[jj & 3] = ft == 0.0f ? 0.0f : w * ft;  // of another sequence's dy, say, if it is no number
             if ((jj & 3) == 3) up[16 * (jj - 3)] = group_sums(u[0], u[1], u[2], u[3]);
         }
         sums += sum_step;
@@ -984,7 +1000,7 @@ __global__ void __launch_bounds__(1024) sbf_grad_kernel(ScanBwdArgs a) {
                 settle(acc[jj]);
                 settle(w);
                 if (jj == TT / 2 - 1 && h + 1 < heads) load_g();
-                v[jj & 3] = w * es;
+                v[jj & 3] = es == 0.0f ? 0.0f : w * es;
                 if ((jj & 3) == 3) *reinterpret_cast<float*>(sm + vt + 64 * (j - 3)) = group_sums(v[0], v[1], v[2], v[3]);
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -1075,6 +1091,7 @@ size_t lay_out(ScanBwdArgs& a, uint8_t* base) {
     part(a.through, bhc);
     part(a.decay, bhc * 5 * kFQ);
     part(a.starts, static_cast<size_t>(a.B * a.chunks) * kFQ);
+    part(a.bounds, static_cast<size_t>(a.B * a.chunks));
     part(a.sums, bhc * (kSums * kFQ + kSumTail));
     part(a.states, bhc * a.P * a.N);
     part(a.grads, bhc * a.P * a.N);
