@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import operator
 import os
 
 import torch  # must precede the library load: it binds the process's HIP runtime
@@ -840,6 +841,21 @@ def _norm_args(x, weight, bias, z, kind, ngroups):
     return C, rows, x_row, 0 if z is None else _rows(z, "z", C)[1]
 
 
+def _norm_limits(channels, ngroups, eps, rows, out_row):
+    """What ssm_norm_fwd itself refuses, refused before the call: a norm that follows a step on
+    state pools must not fail after the step has moved them."""
+    def refuse(status, detail):
+        raise SSMError("ssm_norm_fwd", status, detail)
+    if not ctypes.c_float(eps).value >= 0.0:
+        refuse(1, "eps must be >= 0")
+    if channels // operator.index(ngroups) > 16384:
+        refuse(2, "channels / ngroups must be <= 16384")
+    if ngroups > 0x7FFFFFFF or channels > 1 << 36:
+        refuse(2, "too many channels")
+    if rows > 1 and out_row < channels:
+        refuse(1, f"out row stride below {channels}")
+
+
 def _norm_plan(x, weight=None, bias=None, z=None, eps=1e-5, kind="rms", ngroups=1,
                norm_before_gate=False, out=None):
     """norm_fwd checked and its output allocated, not run: (out, the call)."""
@@ -848,9 +864,10 @@ def _norm_plan(x, weight=None, bias=None, z=None, eps=1e-5, kind="rms", ngroups=
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
     _need(out, "out", x.dtype, x.shape, contiguous=False)
     _need_device(x, weight=weight, bias=bias, z=z, out=out)
-    args = (_ptr(x), x_row, _ptr(z), z_row, _ptr(weight), _ptr(bias), _ptr(out),
-            _rows(out, "out", C)[1], rows, C, ngroups, eps, NORM[kind], int(norm_before_gate),
-            _dtype_code(x))
+    out_row = _rows(out, "out", C)[1]
+    _norm_limits(C, ngroups, eps, rows, out_row)
+    args = (_ptr(x), x_row, _ptr(z), z_row, _ptr(weight), _ptr(bias), _ptr(out), out_row, rows, C,
+            ngroups, eps, NORM[kind], int(norm_before_gate), _dtype_code(x))
 
     def run():
         with _on(x.device):
