@@ -332,6 +332,7 @@ enum { kSumU, kSumV, kSumRowOff, kSumRowDiag, kSumColOff, kSumColDiag, kSumDiag,
        kSumSpan = kSumRowOff, kSumSpanLow = kSumRowDiag, kSumULow = kSumColDiag };
 constexpr int kSumTail = 128;
 constexpr int kAnchor = 8;
+constexpr int kNormExp = 32;  // |S|^2 and |G|^2 are kept times 4^kNormExp
 size_t scan_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N,
                                 ssm_dtype_t dtype);
 int64_t scan_bwd_blocks(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N);

@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(128 * kAnchor) sb_ddt_kernel(ScanBwdArgs a) {
                 ns += __shfl_xor(ns, o);
                 ng += __shfl_xor(ng, o);
             }
-            norms = sqrt(static_cast<double>(ns)) * sqrt(static_cast<double>(ng));
+            norms = sqrt(static_cast<double>(ns)) * sqrt(static_cast<double>(ng)) / static_cast<double>(uint64_t{1} << (2 * kNormExp - 1)) / 2;
         }
         if (lane == 0) {
             usum[hw][ci] = after;

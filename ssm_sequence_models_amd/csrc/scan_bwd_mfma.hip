@@ -177,6 +177,18 @@ __device__ __forceinline__ float row_sums(const float (&v)[4], int li) {
     r += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(r), 0x124, 0xf, 0xf, true));         // rotated by 4
     return r + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(r), 0x128, 0xf, 0xf, true));   // by 8
 }
+// Sum of squares of a lane's 16 values, times 4^kNormExp, and never below it: a square of what is under
+// 2^-95 may be rounded to 0 (each by less than 2^-126), which the rest makes up for.  The gradients
+// are linear in dy, so a bound on their sums must not depend on how small they are.
+struct SquareSum {
+    float sum = 0.0f, most = 0.0f;
+    __device__ __forceinline__ void add(float v) {
+        const float q = v * static_cast<float>(uint64_t{1} << kNormExp);
+        sum += q * q;
+        most = __builtin_fmaxf(most, __builtin_fabsf(v));
+    }
+    __device__ __forceinline__ float bound() const { return sum + (most > 0.0f ? 0x1p-121f : 0.0f); }
+};
 // Makes an offset opaque: what is derived from it is computed where it is used instead of being
 // kept in registers over the whole loop over the heads.
 __device__ __forceinline__ int here(int v) {
@@ -569,18 +581,18 @@ __global__ void __launch_bounds__(512, 4) sbf_dc_kernel(ScanBwdArgs a) {
     for (int64_t h = hfirst; h < hend; ++h) {
         const int par = static_cast<int>(h - hfirst) & 1;
         bf8 Sp[2][3];
-        float norm = 0.0f;
+        SquareSum squares;
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
             float v[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 v[e] = fresh ? 0.0f : rS[2 * kk + (e >> 2)][e & 3];
-                norm += v[e] * v[e];
+                squares.add(v[e]);
             }
             split(v, Sp[kk]);
         }
-        norm = group_sum4(lane_sum16(norm));
+        const float norm = group_sum4(lane_sum16(squares.bound()));
         if (lane == 0 && wave < NT) sums[(kSums - kSumU) * kFQ + 64 + nt] = norm;
 #pragma unroll
         for (int i = 0; i < 2; ++i) *reinterpret_cast<u4*>(sdy[par] + piece<128>(row, tid & 7) + i * 64 * 128) = rdy[i];
@@ -943,18 +955,18 @@ __global__ void __launch_bounds__(1024) sbf_grad_kernel(ScanBwdArgs a) {
             const int hb = O::ROW + (h & 1) * O::HEAD;
             const int id = here(tid), ln = id & 63, li = ln & 15, g4 = ln >> 4;
             bf8 Gp[2][3];
-            float norm = 0.0f;
+            SquareSum squares;
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
                 float v[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     v[e] = rG[2 * kk + (e >> 2)][e & 3];
-                    norm += v[e] * v[e];
+                    squares.add(v[e]);
                 }
                 split(v, Gp[kk]);
             }
-            norm = group_sum4(lane_sum16(norm));
+            const float norm = group_sum4(lane_sum16(squares.bound()));
             if (ln == 0 && wave < NT) sums[kSums * kFQ + 72 + nt] = norm;
             __syncthreads();  // the previous head's x, dy and G have been read
             stage_x();
