@@ -332,6 +332,12 @@ enum { kSumU, kSumV, kSumRowOff, kSumRowDiag, kSumColOff, kSumColDiag, kSumDiag,
        kSumSpan = kSumRowOff, kSumSpanLow = kSumRowDiag, kSumULow = kSumColDiag };
 constexpr int kSumTail = 128;
 constexpr int kAnchor = 8;
+// 2^s of a sum held in double, within two steps of fp32 whatever s (2^float(s) alone is off by
+// |s| 2^-25)
+__device__ __forceinline__ float exp2_of(double s) {
+    const float hi = static_cast<float>(s);
+    return __builtin_amdgcn_exp2f(hi) * (1.0f + static_cast<float>(s - hi) * 0.6931471806f);
+}
 constexpr int kNormExp = 32;  // |S|^2 and |G|^2 are kept times 4^kNormExp
 size_t scan_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N,
                                 ssm_dtype_t dtype);

@@ -26,8 +26,10 @@
 // (here as a difference in double, on the bf16 matrix cores summed directly).  The part of ddt that does not pass through a_t is sum_t W_ts / dt_s + v_s / dt_s,
 // formed without the division.
 //
-// Decays: log a_t is summed in double over the chunk and each factor is the exponential of a
-// difference of two sums, so its relative error stays near 2^-24 however fast the decay.
+// Decays: log a_t is summed in double over the chunk and each factor is the exponential of a sum
+// or of a difference of two: f, e and f_last are within two steps of fp32 however fast the decay,
+// and here L too; on the bf16 matrix cores, where L's exponent is a difference of fp32 pairs, L is
+// within (2 + 1.4 |log2 L|) 2^-24 of itself (36 half-steps where it has fallen to 2^-24).
 // log2 a below -1500 (a = 0 in fp32 by far) counts as -1500: the sums keep what follows.
 //
 // This file: any headdim and dstate that the forward takes, fp32 or bf16 activations, products
@@ -91,8 +93,8 @@ __device__ __forceinline__ void chunk_decay(ChunkDecay& cd, const float* dt, int
         const int rend = __shfl(r, 63);
         cd.cs[t] = s;
         cd.starts[t] = r;
-        cd.f[t] = r == 0 ? __builtin_amdgcn_exp2f(static_cast<float>(s)) : 0.0f;
-        cd.e[t] = r == rend ? __builtin_amdgcn_exp2f(static_cast<float>(end - s)) : 0.0f;
+        cd.f[t] = r == 0 ? exp2_of(s) : 0.0f;
+        cd.e[t] = r == rend ? exp2_of(end - s) : 0.0f;
         cd.dt[t] = d;
         if (t == 63) cd.through = cd.f[63];
         const int head = __popcll(__ballot(r == 0)), tail = __popcll(__ballot(r != rend));

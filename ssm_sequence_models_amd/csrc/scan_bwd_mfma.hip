@@ -270,13 +270,13 @@ __global__ void __launch_bounds__(256) sbf_decay_kernel(ScanBwdArgs a) {
             const float hi = static_cast<float>(s);
             rec[t] = hi;
             rec[kFQ + t] = static_cast<float>(s - hi);
-            rec[2 * kFQ + t] = r == 0 ? __builtin_amdgcn_exp2f(hi) : 0.0f;
-            rec[3 * kFQ + t] = r == rend ? __builtin_amdgcn_exp2f(static_cast<float>(end - s)) : 0.0f;
+            rec[2 * kFQ + t] = r == 0 ? exp2_of(s) : 0.0f;
+            rec[3 * kFQ + t] = r == rend ? exp2_of(end - s) : 0.0f;
             rec[4 * kFQ + t] = d;
         };
         put(lane, s0, r0, d0);
         put(64 + lane, s1, r1, d1);
-        if (lane == 63) a.through[bh * a.chunks + c] = r1 == 0 ? __builtin_amdgcn_exp2f(static_cast<float>(s1)) : 0.0f;
+        if (lane == 63) a.through[bh * a.chunks + c] = r1 == 0 ? exp2_of(s1) : 0.0f;
     }
 }
 
