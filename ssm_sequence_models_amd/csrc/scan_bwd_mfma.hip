@@ -23,12 +23,13 @@
 //               far below u and v, |G| |S| f bounds it and with it the error
 // One kernel for dC and the rest together read S, G and dy once, but held 300 registers a lane:
 // at two wavefronts a SIMD (LDS) it spilled, and took 2318 us at 4 x 8192 tokens x 64 heads,
-// dstate 128, where the two take 168 + 478 us.
+// dstate 128, where the two take 168 + 515 us.
 //
-// Operands: x, dy, B and C are exact in bf16.  The fp32 operands S and G and the scaled x and dy
-// of sbf_states are taken in three bf16 parts (24 bits, nothing lost: ddt and dA are fp32
-// outputs formed from the same products); where only bf16 outputs depend on an operand (the
-// pairs of dx, G of dx, the pairs of dB and dC) two parts do (2^-17 of the operand).
+// Operands: x, dy, B and C are exact in bf16.  Every fp32 operand (S, G, the scaled x and dy of
+// sbf_states, the pairs of dx, the heads' summed pairs of dB and dC) is taken in three bf16 parts: 24
+// bits, nothing lost.  Two parts (2^-17 of the operand) for those that only bf16 outputs depend on
+// put 16 times as many of dx, dB and dC on the neighbour of the bf16 value that fp32 products give
+// (1.5 in a thousand at 4 x 8192 tokens x 64 heads, now 0.1), and took 1043 us where this takes 1081.
 //
 // Layouts of the 16 x 16 x 32 instruction: A lane (row li, k 8 g4 ..), B lane (column li, k
 // 8 g4 ..), result lane (column li, rows 4 g4 ..), li = lane % 16, g4 = lane / 16.  A result
@@ -473,26 +474,25 @@ struct GradLds {
     static constexpr int CB = B + kFQ * N * 2;         // C B^T, 36 tiles as results lie (at first and last: C)
     static constexpr int X = CB + 36 * 1024;           // [128 s][64] bf16
     static constexpr int DY = X + kFQ * 128;           // [128 t][64] bf16
-    static constexpr int G = DY + kFQ * 128;           // two parts of [N][64] bf16
-    static constexpr int LW = X;                       // at the end: two parts of [128 t][128 s] bf16
-    static constexpr int ROW = (G + 2 * N * 128 > LW + 2 * kFQ * 256 ? G + 2 * N * 128 : LW + 2 * kFQ * 256);
-    // per parity of the head: row sums of W by s tile [8][128], v by n tile [8][128], decays [5][128]
-    static constexpr int V = 8 * kFQ * 4, DEC = 16 * kFQ * 4;
-    static constexpr int HEAD = DEC + 5 * kFQ * 4;
-    static constexpr int START = ROW + 2 * HEAD;       // [128] int
-    static constexpr int TOTAL = START + kFQ * 4;
+    static constexpr int G = DY + kFQ * 128;           // three parts of [N][64] bf16
+    static constexpr int ROW = G + 3 * N * 128;        // row sums of W by s tile [8][128]
+    static constexpr int V = ROW + 8 * kFQ * 4;        // v by n tile [8][128]
+    static constexpr int DEC = V + 8 * kFQ * 4;        // decays [5][128]
+    static constexpr int START = DEC + 5 * kFQ * 4;    // [128] int
+    static constexpr int LW = CB + kFQ * N * 2;        // at the end, behind C: three parts of [128 t][128 s] bf16
+    static constexpr int TOTAL = START + kFQ * 4 > LW + 3 * kFQ * 256 ? START + kFQ * 4 : LW + 3 * kFQ * 256;
 };
 static_assert(GradLds<128>::TOTAL <= 160 * 1024, "LDS");
 
 // Joins one head's sums over wavefronts and writes them out for the ddt kernel: threads 0-127 v,
 // 128-255 the row sums, 256-319 the row sums' sums by tile.
 template <int N>
-__device__ __forceinline__ void head_sums(const uint8_t* sm, int hb, float* out, int tid) {
+__device__ __forceinline__ void head_sums(const uint8_t* sm, float* out, int tid) {
     using O = GradLds<N>;
     const int t = tid & 127, which = tid >> 7;
-    const float* row = reinterpret_cast<const float*>(sm + hb);
+    const float* row = reinterpret_cast<const float*>(sm + O::ROW);
     if (which == 0) {
-        const float* p = reinterpret_cast<const float*>(sm + hb + O::V) + t;
+        const float* p = reinterpret_cast<const float*>(sm + O::V) + t;
         float v = 0.0f;
 #pragma unroll
         for (int i = 0; i < N / 16; ++i) v += p[i * kFQ];
@@ -665,13 +665,15 @@ __global__ void __launch_bounds__(256) sbf_anchor_kernel(ScanBwdArgs a) {
 // 16 wavefronts, four a SIMD, in two roles that meet at the two barriers of a head and otherwise
 // run beside each other:
 //   0-7   s tile st (1, 2, .. and 7, 6, .. on one SIMD: nine pair tiles each): the pairs, W's sums, dx
-//   8-15  n tile nt: G's parts, dB from behind the chunk and v; the head before's sums
+//   8-15  n tile nt: G's parts, dB from behind the chunk and v; between the barriers the head
+//         before's sums
 // LDS holds one block a CU, so the roles are what hides one's LDS waits behind the other's
-// products: as eight wavefronts that did both in turn it took 541 us where this takes 478 (227
-// and 190 us at one row of 32768 tokens, 24 heads, dstate 64).  The t tiles are taken in pairs
-// from an even one on, so that the bodies a wavefront may start in are few and keep within 128
-// registers: from any one on they were 8, with 51 spilled registers where these spill 28
-// outside the pairs, and 510 us.
+// products: as eight wavefronts that did both in turn it took 541 us where the roles took 478 (227
+// and 190 us at one row of 32768 tokens, 24 heads, dstate 64), with two parts for the pairs and for
+// G of dx; with three of each it takes 515 and 212.  The third part of G fills the 160 KB, so the
+// heads' sums have one place, not two in turn, and are written out between the barriers.  The t
+// tiles are taken in pairs from an even one on, so that the bodies a wavefront may start in are few
+// and keep within 128 registers: from any one on they were 8, and 510 us where these took 478.
 template <int N>
 __global__ void __launch_bounds__(1024) sbf_grad_kernel(ScanBwdArgs a) {
     using O = GradLds<N>;
@@ -757,7 +759,6 @@ __global__ void __launch_bounds__(1024) sbf_grad_kernel(ScanBwdArgs a) {
         f4 lwd[2] = {}, lw[3][2] = {};
         char* dxp = reinterpret_cast<char*>(static_cast<uint16_t*>(a.dx) + tok * a.dx_row + hfirst * kFP);
         for (int h = 0; h < heads; ++h) {
-            const int hb = O::ROW + (h & 1) * O::HEAD;  // this head's part of LDS
             __syncthreads();  // the previous head's x, dy and G have been read
             stage_x();
             __syncthreads();
@@ -767,9 +768,9 @@ __global__ void __launch_bounds__(1024) sbf_grad_kernel(ScanBwdArgs a) {
             // LDS offsets of this head's reads
             const int xo = here(O::X + along_off<128>(li, g4));              // x, dy along rows
             const int yo = here(O::DY + down_off<128>(4 * g4, li));          // dy down rows
-            const int tl = here(hb + O::DEC + 4 * li);                       // decays of token li of a tile
-            const int t4 = here(hb + O::DEC + 16 * g4);                      // decays of tokens 4 g4 ..
-            const int rt = here(hb + st * LR + 16 * g4 + 4 * (li & 3));      // row sums
+            const int tl = here(O::DEC + 4 * li);                            // decays of token li of a tile
+            const int t4 = here(O::DEC + 16 * g4);                           // decays of tokens 4 g4 ..
+            const int rt = here(O::ROW + st * LR + 16 * g4 + 4 * (li & 3));  // row sums
             const int ct = here(cbt + 16 * ln);                              // C B^T
 
             // ---- pairs s <= t: W's sums, the pairs' part of dx ----
@@ -777,7 +778,7 @@ __global__ void __launch_bounds__(1024) sbf_grad_kernel(ScanBwdArgs a) {
             const float hi_s = lds<float>(sm + tl + 64 * st), lo_s = lds<float>(sm + tl + LR + 64 * st);
             const float dts = lds<float>(sm + tl + 4 * LR + 64 * st);
             float below = 0.0f, bdiag = 0.0f, diag = 0.0f;  // column sums of W / dt_s
-            u4 pw[2];  // two parts of the pairs of two t tiles, in token order
+            u4 pw[3];  // three parts of the pairs of two t tiles, in token order
             // the pairs of t tile j with s tile st, in half i of that operand
             auto tile = [&](int j, int i, f4& sum, auto on_diagonal) __attribute__((always_inline)) {
                 constexpr bool DIAG = decltype(on_diagonal)::value;
@@ -815,11 +816,16 @@ __global__ void __launch_bounds__(1024) sbf_grad_kernel(ScanBwdArgs a) {
                 settle(sum);
                 if (DIAG) spanning(rw, li, g4);
                 *reinterpret_cast<float*>(sm + rt + 64 * j) = row_sums(rw, li);  // the same from four lanes
-                const uint32_t q0 = pack_bf16x2(pv[0], pv[1]), q1 = pack_bf16x2(pv[2], pv[3]);
-                pw[0][2 * i] = q0;
-                pw[0][2 * i + 1] = q1;
-                pw[1][2 * i] = pack_bf16x2(pv[0] - __uint_as_float(q0 << 16), pv[1] - __uint_as_float(q0 & 0xFFFF0000u));
-                pw[1][2 * i + 1] = pack_bf16x2(pv[2] - __uint_as_float(q1 << 16), pv[3] - __uint_as_float(q1 & 0xFFFF0000u));
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    const uint32_t q0 = pack_bf16x2(pv[0], pv[1]), q1 = pack_bf16x2(pv[2], pv[3]);
+                    pw[k][2 * i] = q0;
+                    pw[k][2 * i + 1] = q1;
+                    pv[0] -= __uint_as_float(q0 << 16);
+                    pv[1] -= __uint_as_float(q0 & 0xFFFF0000u);
+                    pv[2] -= __uint_as_float(q1 << 16);
+                    pv[3] -= __uint_as_float(q1 & 0xFFFF0000u);
+                }
                 __builtin_amdgcn_sched_barrier(0);  // the registers of one tile at a time
             };
             // their part of dx, from t tile j on (even)
@@ -833,14 +839,14 @@ __global__ void __launch_bounds__(1024) sbf_grad_kernel(ScanBwdArgs a) {
                         y[p] = join(tr_read(q), tr_read(q + 16 * 128));
                     }
 #pragma unroll
-                    for (int k = 1; k >= 0; --k)
+                    for (int k = 2; k >= 0; --k)
 #pragma unroll
                         for (int p = 0; p < 2; ++p) dxa[p0 + p] = mfma(y[p], __builtin_bit_cast(bf8, pw[k]), dxa[p0 + p]);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             };
             if (st & 1) {
-                pw[0] = pw[1] = u4{0, 0, 0, 0};
+                pw[0] = pw[1] = pw[2] = u4{0, 0, 0, 0};
             } else {
                 tile(st, 0, lwd[0], std::true_type{});
             }
@@ -870,7 +876,7 @@ __global__ void __launch_bounds__(1024) sbf_grad_kernel(ScanBwdArgs a) {
             for (int kk = 0; kk < N / 32; ++kk) {
                 const bf8 bf = lds<bf8>(sm + (bst ^ (kk << 6)));
 #pragma unroll
-                for (int k = 1; k >= 0; --k)
+                for (int k = 2; k >= 0; --k)
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
                         const int o = k * PL + 32 * kk * 128;
@@ -890,18 +896,22 @@ __global__ void __launch_bounds__(1024) sbf_grad_kernel(ScanBwdArgs a) {
             dxp += kFP * 2;
         }
         __syncthreads();
-        // ---- the heads' summed pairs: two parts of [t][s] in LDS (zero above the diagonal) ----
+        __syncthreads();  // the last head's sums have been read
+        // ---- the heads' summed pairs: three parts of [t][s] in LDS (zero above the diagonal) ----
         const int s = 16 * st + li;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float v = j >> 1 == st >> 1 ? lwd[j & 1][e] : j > st ? lw[(j >> 1) > 0 ? (j >> 1) - 1 : 0][j & 1][e] : 0.0f;
+                float v = j >> 1 == st >> 1 ? lwd[j & 1][e] : j > st ? lw[(j >> 1) > 0 ? (j >> 1) - 1 : 0][j & 1][e] : 0.0f;
                 const int t = 16 * j + 4 * g4 + e;
-                const uint16_t hi = f32_to_bf16(v), lo = f32_to_bf16(v - bf16_to_f32(hi));
                 const int o = piece<256>(t, s >> 3) + 2 * (s & 7);
-                *reinterpret_cast<uint16_t*>(sm + O::LW + o) = hi;
-                *reinterpret_cast<uint16_t*>(sm + O::LW + kFQ * 256 + o) = lo;
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    const uint16_t part = f32_to_bf16(v);
+                    *reinterpret_cast<uint16_t*>(sm + O::LW + k * kFQ * 256 + o) = part;
+                    v -= bf16_to_f32(part);
+                }
             }
         __syncthreads();
         // ---- dC of n tile nt: sbf_dc's part (where this block alone has the pairs), then the pairs ----
@@ -920,8 +930,8 @@ __global__ void __launch_bounds__(1024) sbf_grad_kernel(ScanBwdArgs a) {
                 if (2 * k <= j) {  // s tiles 2 k, 2 k + 1
                     const uint8_t* p = sm + O::B + 32 * k * RB;
                     const bf8 f = join(tr_read(p + b0), tr_read(p + b1));
-                    acc = mfma(f, along<256>(sm + O::LW + kFQ * 256, lo_, 16 * j, k), acc);
-                    acc = mfma(f, along<256>(sm + O::LW, lo_, 16 * j, k), acc);
+#pragma unroll
+                    for (int i = 2; i >= 0; --i) acc = mfma(f, along<256>(sm + O::LW + i * kFQ * 256, lo_, 16 * j, k), acc);
                 }
             if (t >= nv) continue;
             if (a.splits == 1)
@@ -952,7 +962,6 @@ __global__ void __launch_bounds__(1024) sbf_grad_kernel(ScanBwdArgs a) {
         __syncthreads();  // the other role's of C B^T
         f4 acc[TT] = {};
         for (int h = 0; h < heads; ++h) {
-            const int hb = O::ROW + (h & 1) * O::HEAD;
             const int id = here(tid), ln = id & 63, li = ln & 15, g4 = ln >> 4;
             bf8 Gp[2][3];
             SquareSum squares;
@@ -975,21 +984,21 @@ __global__ void __launch_bounds__(1024) sbf_grad_kernel(ScanBwdArgs a) {
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) *reinterpret_cast<bf8*>(sm + k * PL + (q ^ (kk << 6))) = Gp[kk][k];
+                    for (int k = 0; k < 3; ++k) *reinterpret_cast<bf8*>(sm + k * PL + (q ^ (kk << 6))) = Gp[kk][k];
             }
             {
-                float* dec = reinterpret_cast<float*>(sm + hb + O::DEC);
+                float* dec = reinterpret_cast<float*>(sm + O::DEC);
                 dec[id] = rd[0];
                 if (id < kFQ) dec[4 * kFQ + id] = rd[1];
             }
+            if (h > 0) head_sums<N>(sm, sums - sum_step, here(id));
             __syncthreads();
             if (h + 1 < heads) load_x();
-            if (h > 0) head_sums<N>(sm, O::ROW + ((h & 1) ^ 1) * O::HEAD, sums - sum_step, here(id));
             sums += sum_step;
             const int xo = here(O::X + along_off<128>(li, g4));                      // x along rows
             const int cw = here(piece<RB>(li, 2 * nt + (g4 >> 1)) + 8 * (g4 & 1));   // B elements (n 4 g4 .., s li)
-            const int tl = here(hb + O::DEC + 4 * li);                               // decays of token li of a tile
-            const int vt = here(hb + O::V + nt * LR + 64 * group_of_row(g4) + 4 * li);  // v of n tile nt, four s tiles
+            const int tl = here(O::DEC + 4 * li);                                    // decays of token li of a tile
+            const int vt = here(O::V + nt * LR + 64 * group_of_row(g4) + 4 * li);  // v of n tile nt, four s tiles
             float v[4];
 #pragma unroll
             for (int jj = 0; jj < TT; ++jj) {
@@ -1018,7 +1027,8 @@ __global__ void __launch_bounds__(1024) sbf_grad_kernel(ScanBwdArgs a) {
             }
         }
         __syncthreads();
-        head_sums<N>(sm, O::ROW + ((heads - 1) & 1) * O::HEAD, sums - sum_step, tid);
+        head_sums<N>(sm, sums - sum_step, tid);
+        __syncthreads();
         {  // C again, in place of C B^T
             const uint16_t* cg = static_cast<const uint16_t*>(a.C) + tok * a.c_row + g * N;
             for (int q = tid; q < kFQ * BP; q += 512) {
@@ -1039,8 +1049,8 @@ __global__ void __launch_bounds__(1024) sbf_grad_kernel(ScanBwdArgs a) {
             for (int k = 0; k < 4; ++k)
                 if (2 * k + 1 >= j) {  // t tiles 2 k, 2 k + 1
                     const bf8 f = down<RB>(sm + O::CB, bo, 32 * k, 0);
-                    acc[jj] = mfma(f, down<256>(sm + O::LW + kFQ * 256, ld, 32 * k, j), acc[jj]);
-                    acc[jj] = mfma(f, down<256>(sm + O::LW, ld, 32 * k, j), acc[jj]);
+#pragma unroll
+                    for (int i = 2; i >= 0; --i) acc[jj] = mfma(f, down<256>(sm + O::LW + i * kFQ * 256, ld, 32 * k, j), acc[jj]);
                 }
             if (t >= nv) continue;
             if (a.splits == 1)
