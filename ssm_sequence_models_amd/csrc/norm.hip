@@ -14,6 +14,8 @@
 // weights are read once and the sums of dw and db stay in registers; each block writes one
 // partial row, and a second kernel adds the partial rows in a fixed order in double
 // (deterministic, no atomics).  All arithmetic is fp32; outputs are rounded once.
+#include <type_traits>
+
 #include "internal.h"
 
 namespace ssm {
@@ -410,19 +412,16 @@ int64_t norm_blocks(int64_t rows, int64_t m, int64_t groups, bool bwd) {
     return need < most ? need : most;
 }
 
-template <class S, bool TAIL, int NV, int TPR>
-void launch_one(const NormArgs& a, int gate, bool bwd, hipStream_t s) {
+template <bool BWD, class S, bool TAIL, int NV, int TPR>
+void launch_one(const NormArgs& a, int gate, hipStream_t s) {
     const dim3 grid(static_cast<uint32_t>(a.nb * a.groups)), block(TPR > 256 ? TPR : 256);
-#define SSM_NORM(G)                                                                    \
-    (bwd ? norm_bwd_kernel<S, TAIL, NV, TPR, G><<<grid, block, 0, s>>>(a)               \
-         : norm_fwd_kernel<S, TAIL, NV, TPR, G><<<grid, block, 0, s>>>(a))
-    if (gate == kGateNone)
-        SSM_NORM(kGateNone);
-    else if (gate == kGateBefore)
-        SSM_NORM(kGateBefore);
-    else
-        SSM_NORM(kGateAfter);
-#undef SSM_NORM
+    auto run = [&](auto g) {
+        if constexpr (BWD) norm_bwd_kernel<S, TAIL, NV, TPR, decltype(g)::value><<<grid, block, 0, s>>>(a);
+        else norm_fwd_kernel<S, TAIL, NV, TPR, decltype(g)::value><<<grid, block, 0, s>>>(a);
+    };
+    if (gate == kGateNone) run(std::integral_constant<int, kGateNone>{});
+    else if (gate == kGateBefore) run(std::integral_constant<int, kGateBefore>{});
+    else run(std::integral_constant<int, kGateAfter>{});
 }
 
 // Teams by the group's width m, bf16 with a gate at 32768 rows x 4096 channels (16384 x 8192),
@@ -431,21 +430,24 @@ void launch_one(const NormArgs& a, int gate, bool bwd, hipStream_t s) {
 //   m = 1024  one wavefront, two vectors 138 / 251          four wavefronts, half idle, 205 / 312
 //   m = 4096  four wavefronts, two vectors 146 / 260        eight, one vector 149 / 235
 //   m = 8192  16 wavefronts, one vector 138 / 279           eight, two vectors 151 / 350
-template <class S, bool TAIL>
-void launch_typed(const NormArgs& a, int gate, bool bwd, hipStream_t s) {
+template <bool BWD, class S, bool TAIL>
+void launch_typed(const NormArgs& a, int gate, hipStream_t s) {
     const int m = a.m;
-    if (m <= 512) launch_one<S, TAIL, 1, 64>(a, gate, bwd, s);
-    else if (m <= 1024) launch_one<S, TAIL, 2, 64>(a, gate, bwd, s);
-    else if (m <= 2048) launch_one<S, TAIL, 1, 256>(a, gate, bwd, s);
-    else if (m <= 4096 && !bwd) launch_one<S, TAIL, 2, 256>(a, gate, bwd, s);
-    else if (m <= 4096) launch_one<S, TAIL, 1, 512>(a, gate, bwd, s);
-    else if (m <= 8192) launch_one<S, TAIL, 1, 1024>(a, gate, bwd, s);
-    else launch_one<S, TAIL, 2, 1024>(a, gate, bwd, s);
+    if (m <= 512) return launch_one<BWD, S, TAIL, 1, 64>(a, gate, s);
+    if (m <= 1024) return launch_one<BWD, S, TAIL, 2, 64>(a, gate, s);
+    if (m <= 2048) return launch_one<BWD, S, TAIL, 1, 256>(a, gate, s);
+    if (m <= 4096) {
+        if constexpr (BWD) return launch_one<BWD, S, TAIL, 1, 512>(a, gate, s);
+        else return launch_one<BWD, S, TAIL, 2, 256>(a, gate, s);
+    }
+    if (m <= 8192) return launch_one<BWD, S, TAIL, 1, 1024>(a, gate, s);
+    launch_one<BWD, S, TAIL, 2, 1024>(a, gate, s);
 }
-void launch_norm(const NormArgs& a, ssm_dtype_t dtype, int gate, bool bwd, hipStream_t s) {
+template <bool BWD>
+void launch_norm(const NormArgs& a, ssm_dtype_t dtype, int gate, hipStream_t s) {
     const bool tail = a.m % kVec != 0;
-    if (dtype == SSM_BF16) tail ? launch_typed<BF16, true>(a, gate, bwd, s) : launch_typed<BF16, false>(a, gate, bwd, s);
-    else tail ? launch_typed<F32, true>(a, gate, bwd, s) : launch_typed<F32, false>(a, gate, bwd, s);
+    if (dtype == SSM_BF16) tail ? launch_typed<BWD, BF16, true>(a, gate, s) : launch_typed<BWD, BF16, false>(a, gate, s);
+    else tail ? launch_typed<BWD, F32, true>(a, gate, s) : launch_typed<BWD, F32, false>(a, gate, s);
 }
 
 }  // namespace
@@ -463,7 +465,7 @@ hipError_t launch_norm_fwd(const NormCall& c, hipStream_t s) {
     a.nb = norm_blocks(c.rows, a.m, c.groups, false);
     a.eps = c.eps; a.layer = c.layer;
     const int gate = c.z == nullptr ? kGateNone : c.gate_after ? kGateAfter : kGateBefore;
-    launch_norm(a, c.dtype, gate, false, s);
+    launch_norm<false>(a, c.dtype, gate, s);
     return hipGetLastError();
 }
 
@@ -484,7 +486,7 @@ hipError_t launch_norm_bwd(const NormCall& c, hipStream_t s) {
     a.want_db = c.db != nullptr;
     a.part = c.dw || c.db ? static_cast<float*>(c.workspace) : nullptr;
     const int gate = c.z == nullptr ? kGateNone : c.gate_after ? kGateAfter : kGateBefore;
-    launch_norm(a, c.dtype, gate, true, s);
+    launch_norm<true>(a, c.dtype, gate, s);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.part == nullptr) return e;
     const dim3 grid(static_cast<uint32_t>((c.channels + 63) / 64), c.db ? 2 : 1);
