@@ -231,6 +231,9 @@ def _workspace(ws, nbytes, device):
         return None, 0
     if ws is None:
         ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    # the kernels write nbytes from its first element on: repeated or skipped elements do not count
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {device}")
     if ws.numel() * ws.element_size() < nbytes:
         raise ValueError(f"workspace must hold {nbytes} bytes")
     return ws, ws.numel() * ws.element_size()
