@@ -456,7 +456,9 @@ ssm_status_t ssm_scan_bwd(const void* x, const float* dt, const float* A, const 
  * channel (A_t = diag(a_t), B = C = 1), for layers whose gates are data-dependent and whose
  * recurrence has no state dimension.  Per row b and channel c
  *     h_t = a_t h_{t-1} + i_t x_t,   y_t = h_t,   h_{-1} = initial_state (zeros when NULL)
- *   SSM_GATE_LOG:      a_t = exp(gate_t), i_t = 1         (gate <= 0 for a contraction)
+ *   SSM_GATE_LOG:      a_t = exp(gate_t), i_t = 1         (gate <= 0 for a contraction; gates
+ *                      above 0 as long as exp(their sum) over any consecutive tokens of a row is
+ *                      finite in fp32: beyond, results may be NaN also where the state is 0)
  *   SSM_GATE_SIGMOID:  a_t = sigmoid(gate_t), i_t = 1 - a_t
  * seq_idx: the state restarts from zero where seq_idx[b,t] != seq_idx[b,t-1] (a_t counts as 0
  * there, i_t does not change); a NaN or infinity of one sequence does not reach the next.

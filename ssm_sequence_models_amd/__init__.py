@@ -747,8 +747,9 @@ def gated_scan_bwd_workspace_size(batch, seqlen, channels) -> int:
 def gated_scan_fwd(x, gate, form="sigmoid", initial_state=None, seq_idx=None,
                    return_final_state=True, final_state=None, y=None, workspace=None):
     """The per-channel gated recurrence h_t = a_t h_{t-1} + i_t x_t (length-generalization notes
-    Sec. 2.1 Eq. (1), a state of one value per channel): a = exp(gate), i = 1 (form "log") or
-    a = sigmoid(gate), i = 1 - a (form "sigmoid").  x, gate [b, L, C] (consecutive channels,
+    Sec. 2.1 Eq. (1), a state of one value per channel): a = exp(gate), i = 1 (form "log"; exp of
+    the gates' sum over any consecutive tokens finite in fp32) or a = sigmoid(gate), i = 1 - a
+    (form "sigmoid").  x, gate [b, L, C] (consecutive channels,
     tokens at any one stride); initial_state [b, C] fp32 (may be the same tensor as
     final_state; y must not overlap an input); seq_idx [b, L] int32.  Returns (y [b, L, C],
     final_state or None)."""

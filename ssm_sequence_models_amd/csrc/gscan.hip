@@ -36,6 +36,9 @@
 // The backward needs h before each tile: its first kernel walks forward and stores (A, H) from
 // the segment's start to each tile's (8 bytes a channel and 128 tokens).
 //
+// A is a product of decays, so it must not leave fp32's range: gates of the log form above 0 are
+// served as long as e^(their sum) over consecutive tokens is finite (times a state of 0, infinity
+// would be NaN).
 // A span that holds a sequence start passes nothing on; it is marked by A = -1 (a product of
 // decays is never negative) and folded by a select, so a NaN or infinity of one sequence does
 // not reach the next.  Everything is fp32; outputs are rounded once.
@@ -74,8 +77,9 @@ struct GArgs {
     bool pairs;   // two channels and the lanes' 32-bit offsets serve whole tiles
 };
 
-// decay a and input factor i of a gate: e = exp(-g), a = 1 / (1 + e) and i = e a keep both to full
-// relative accuracy; e is held below 2^126, where 1 / (1 + e) is still a normal number
+// decay a and input factor i of a gate: e = exp(-g), a = 1 / (1 + e) and i = e a, neither a
+// difference, are within (6 + 1.3 |g|) 2^-24 of themselves (the exponent's rounding in e; one step
+// each of exp2 and rcp); e is held below 2^126, where 1 / (1 + e) is still a normal number
 template <bool SIG>
 __device__ __forceinline__ void gates(float g, float& a, float& i) {
     if constexpr (SIG) {
