@@ -945,7 +945,7 @@ ssm_status_t ssm_norm_fwd(const void* x, int64_t x_row, const void* z, int64_t z
 }
 
 size_t ssm_norm_bwd_workspace_size(int64_t rows, int64_t channels, int64_t ngroups) {
-    if (rows <= 0 || channels < 1 || ngroups < 1 || channels % ngroups != 0) return 0;
+    if (rows <= 0 || channels < 1 || ngroups < 1 || channels % ngroups != 0 || channels > (int64_t{1} << 36)) return 0;
     return static_cast<size_t>(2 * ssm::norm_partial_rows(rows, channels, ngroups) * channels) * 4;
 }
 
@@ -1011,10 +1011,18 @@ ssm_status_t ssm_norm_bwd(const void* x, int64_t x_row, const void* z, int64_t z
     return hip_status(ssm::launch_norm_bwd(c, reinterpret_cast<hipStream_t>(stream)), fn);
 }
 
+// sizes whose products do not leave 63 bits
+static bool scan_bwd_sizes_fit(int64_t batch, int64_t seqlen, int64_t nheads) {
+    const int64_t most = int64_t{1} << 31;
+    return batch < most && seqlen < most && nheads < most &&
+           (batch == 0 || seqlen == 0 || nheads <= (most << 20) / batch / seqlen);
+}
+
 size_t ssm_scan_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim,
                                    int64_t ngroups, int64_t dstate, ssm_dtype_t dtype) {
     if (batch <= 0 || seqlen <= 0 || nheads < 1 || headdim < 1 || ngroups < 1 || dstate < 1 ||
-        nheads % ngroups != 0 || !valid_dtype(dtype) || !ssm::recurrent_supported(headdim, dstate))
+        nheads % ngroups != 0 || !valid_dtype(dtype) || !ssm::recurrent_supported(headdim, dstate) ||
+        !scan_bwd_sizes_fit(batch, seqlen, nheads))
         return 0;
     return ssm::scan_bwd_workspace_bytes(batch, seqlen, nheads, headdim, ngroups, dstate, dtype);
 }
@@ -1031,9 +1039,7 @@ ssm_status_t ssm_scan_bwd(const void* x, const float* dt, const float* A, const 
     if (st != SSM_OK) return st;
     if (!ssm::recurrent_supported(headdim, dstate))
         return fail(SSM_ERR_UNSUPPORTED, "ssm_scan_bwd: headdim and dstate must be sizes that ssm_scan_fwd takes (dstate 4 * 2^k <= 256, headdim*dstate <= 32768)");
-    const int64_t most = int64_t{1} << 31;
-    if (batch >= most || seqlen >= most || nheads >= most ||
-        (batch > 0 && seqlen > 0 && nheads > (most << 20) / batch / seqlen))
+    if (!scan_bwd_sizes_fit(batch, seqlen, nheads))
         return fail(SSM_ERR_UNSUPPORTED, "ssm_scan_bwd: batch, seqlen or nheads too large");
     const size_t es = esize(dtype);
     const bool work = batch > 0 && seqlen > 0;
@@ -1095,6 +1101,12 @@ ssm_status_t ssm_scan_bwd(const void* x, const float* dt, const float* A, const 
 
 namespace {
 
+// sizes whose products below do not leave 63 bits, nor their grid 31
+bool gscan_sizes_fit(int64_t batch, int64_t seqlen, int64_t channels) {
+    const int64_t most = int64_t{1} << 31;
+    return batch < most && seqlen < most && channels < most && (batch == 0 || (channels + 63) / 64 <= most / batch);
+}
+
 ssm_status_t check_gscan_dims(const char* fn, int64_t batch, int64_t seqlen, int64_t channels,
                               int32_t form, int dtype) {
     if (!valid_dtype(dtype)) return fail(SSM_ERR_INVALID_ARG, std::string(fn) + ": bad dtype");
@@ -1102,10 +1114,7 @@ ssm_status_t check_gscan_dims(const char* fn, int64_t batch, int64_t seqlen, int
         return fail(SSM_ERR_INVALID_ARG, std::string(fn) + ": bad gate form");
     if (batch < 0 || seqlen < 0 || channels < 1)
         return fail(SSM_ERR_INVALID_ARG, std::string(fn) + ": need batch >= 0, tokens >= 0, channels >= 1");
-    // sizes whose products below could leave 63 bits, or their grid 31
-    const int64_t most = int64_t{1} << 31;
-    if (batch >= most || seqlen >= most || channels >= most ||
-        (batch > 0 && (channels + 63) / 64 > most / batch))
+    if (!gscan_sizes_fit(batch, seqlen, channels))
         return fail(SSM_ERR_UNSUPPORTED, std::string(fn) + ": batch, tokens or channels too large");
     return SSM_OK;
 }
@@ -1113,12 +1122,12 @@ ssm_status_t check_gscan_dims(const char* fn, int64_t batch, int64_t seqlen, int
 }  // namespace
 
 size_t ssm_gated_scan_fwd_workspace_size(int64_t batch, int64_t seqlen, int64_t channels) {
-    if (batch <= 0 || seqlen <= 0 || channels < 1) return 0;
+    if (batch <= 0 || seqlen <= 0 || channels < 1 || !gscan_sizes_fit(batch, seqlen, channels)) return 0;
     return ssm::gscan_workspace_bytes(batch, seqlen, channels, false);
 }
 
 size_t ssm_gated_scan_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t channels) {
-    if (batch <= 0 || seqlen <= 0 || channels < 1) return 0;
+    if (batch <= 0 || seqlen <= 0 || channels < 1 || !gscan_sizes_fit(batch, seqlen, channels)) return 0;
     return ssm::gscan_workspace_bytes(batch, seqlen, channels, true);
 }
 
