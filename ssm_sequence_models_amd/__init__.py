@@ -535,12 +535,13 @@ def conv_scan_fwd(xBC, conv_weight, conv_bias, dt, A, nheads, headdim, ngroups, 
     _need(final_state, "final_state", torch.float32, (bsz, H, P, N))
     ws, nbytes = _workspace(workspace, workspace_size(bsz, L, H, P, G, N, xBC.dtype), xBC.device)
     normed = None if norm is None else _norm_plan(y.view(bsz, L, H * P), **norm)[1]
-    _check("ssm_conv_scan_fwd", _lib.ssm_conv_scan_fwd(
-        _ptr(xBC), _ptr(conv_weight), _ptr(conv_bias), _ptr(conv_initial_state),
-        _ptr(conv_final_state), _ptr(dt), _ptr(A), _ptr(initial_state), _ptr(final_state),
-        _ptr(seq_idx), _ptr(y), bsz, L, H, P, G, N, K, _dtype_code(xBC), ACT[activation], _ptr(ws),
-        nbytes, _stream()))
-    return y if normed is None else normed(), conv_final_state, final_state
+    with _on(xBC.device):  # the norm reads y on the same stream
+        _check("ssm_conv_scan_fwd", _lib.ssm_conv_scan_fwd(
+            _ptr(xBC), _ptr(conv_weight), _ptr(conv_bias), _ptr(conv_initial_state),
+            _ptr(conv_final_state), _ptr(dt), _ptr(A), _ptr(initial_state), _ptr(final_state),
+            _ptr(seq_idx), _ptr(y), bsz, L, H, P, G, N, K, _dtype_code(xBC), ACT[activation],
+            _ptr(ws), nbytes, _stream()))
+        return y if normed is None else normed(), conv_final_state, final_state
 
 
 def noalloc_scratch_bytes() -> int:
@@ -655,12 +656,13 @@ def decode_step(x_new, conv_state, conv_weight, conv_bias, dt, A, ssm_state, nhe
         y = torch.empty((bsz, n_new, H, P), dtype=x_new.dtype, device=x_new.device)
     _need(y, "y", x_new.dtype, (bsz, n_new, H, P))
     normed = None if norm is None else _norm_plan(y.view(bsz, n_new, H * P), **norm)[1]
-    _check("ssm_decode_step", _lib.ssm_decode_step(
-        _ptr(x_new), _ptr(conv_state), _ptr(conv_weight), _ptr(conv_bias),
-        _ptr(conv_state_indices), _ptr(cache_seqlens), _ptr(dt), _ptr(A), _ptr(ssm_state),
-        _ptr(state_indices), _ptr(conv_out), _ptr(y), bsz, n_new, H, P, G, N, K, state_len,
-        n_cslots, ssm_state.shape[0], _dtype_code(x_new), ACT[activation], _stream()))
-    return y if normed is None else normed()
+    with _on(x_new.device):  # the norm reads y on the same stream
+        _check("ssm_decode_step", _lib.ssm_decode_step(
+            _ptr(x_new), _ptr(conv_state), _ptr(conv_weight), _ptr(conv_bias),
+            _ptr(conv_state_indices), _ptr(cache_seqlens), _ptr(dt), _ptr(A), _ptr(ssm_state),
+            _ptr(state_indices), _ptr(conv_out), _ptr(y), bsz, n_new, H, P, G, N, K, state_len,
+            n_cslots, ssm_state.shape[0], _dtype_code(x_new), ACT[activation], _stream()))
+        return y if normed is None else normed()
 
 
 def scan_bwd_workspace_size(batch, seqlen, nheads, headdim, ngroups, dstate,
