@@ -430,6 +430,9 @@ void launch_one(const NormArgs& a, int gate, hipStream_t s) {
 //   m = 1024  one wavefront, two vectors 138 / 251          four wavefronts, half idle, 205 / 312
 //   m = 4096  four wavefronts, two vectors 146 / 260        eight, one vector 149 / 235
 //   m = 8192  16 wavefronts, one vector 138 / 279           eight, two vectors 151 / 350
+// Far from the floor: m = 64, 128 and 256 (8, 16 and 32 lanes of a wavefront at work) 680 / 1030,
+// 347 / 533 and 185 / 294; m = 16384 171 / 551, gate before 164 / 995 (backward 17 to 125 registers are
+// spilled in the loop; at 8192 with the gate before 7).
 template <bool BWD, class S, bool TAIL>
 void launch_typed(const NormArgs& a, int gate, hipStream_t s) {
     const int m = a.m;
