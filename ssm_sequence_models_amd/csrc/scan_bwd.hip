@@ -134,7 +134,7 @@ __device__ __forceinline__ f4 load4(const uint16_t* p) {
               __uint_as_float(q[1] << 16), __uint_as_float(q[1] & 0xFFFF0000u)};
 }
 
-// A row-major view [tokens][cols] of the chunk's tokens: zeros outside.  What lies outside is read
+// A row-major view [tokens][cols] of the chunk's tokens lo .. rows - 1: zeros outside.  What lies outside is read
 // from the last row and column instead (of no rows, the first) and replaced, so no load is under a
 // branch and waits for another.  W: cols is a multiple of 16, so four consecutive columns are inside
 // or outside.
@@ -142,17 +142,18 @@ template <class S, bool W>
 struct View {
     const typename S::T* p;
     int64_t row;
-    int rows, cols;
+    int rows, cols, lo = 0;
+    __device__ __forceinline__ bool has(int r) const { return static_cast<unsigned>(r - lo) < static_cast<unsigned>(rows - lo); }
     __device__ __forceinline__ int row_at(int r) const { return r < rows ? r : rows > 0 ? rows - 1 : 0; }
     __device__ __forceinline__ float at(int r, int c) const {
         const float v = S::load(p, row_at(r) * row + (c < cols ? c : cols - 1));
-        return r < rows && c < cols ? v : 0.0f;
+        return has(r) && c < cols ? v : 0.0f;
     }
     // operand with the contraction along the row: row r, columns k .. k + 3
     __device__ __forceinline__ f4 along(int r, int k) const {
         if constexpr (W) {
             const f4 v = load4(p + row_at(r) * row + k);  // k < cols: called for 16 at a time
-            return r < rows ? v : f4{0, 0, 0, 0};
+            return has(r) ? v : f4{0, 0, 0, 0};
         } else {
             return f4{at(r, k), at(r, k + 1), at(r, k + 2), at(r, k + 3)};
         }
@@ -181,9 +182,9 @@ __global__ void __launch_bounds__(256) sb_local_kernel(ScanBwdArgs a) {
     // sequence that ends in this chunk, times 0, would reach the chunks behind it.
     const int lo = rev ? 0 : cd.tail, hi = rev && cd.head < w.nv ? cd.head : w.nv;
     const View<S, W> xv{static_cast<const T*>(rev ? a.dy : a.x) + tok * (rev ? a.dy_row : a.x_row) + w.h * P,
-                     rev ? a.dy_row : a.x_row, hi, P};
+                     rev ? a.dy_row : a.x_row, hi, P, lo};
     const View<S, W> bv{static_cast<const T*>(rev ? a.C : a.Bm) + tok * (rev ? a.c_row : a.b_row) + w.g * N,
-                     rev ? a.c_row : a.b_row, hi, N};
+                     rev ? a.c_row : a.b_row, hi, N, lo};
     float* out = (rev ? a.grads : a.states) + ((w.b * a.H + w.h) * a.chunks + w.c) * a.P * a.N;
     const int lane = threadIdx.x & 63, li = lane & 15, g4 = lane >> 4;
     if (!rev && threadIdx.x == 0) a.through[(w.b * a.H + w.h) * a.chunks + w.c] = cd.through;
@@ -206,16 +207,6 @@ __global__ void __launch_bounds__(256) sb_local_kernel(ScanBwdArgs a) {
             for (int i = 0; i < kLP; ++i) x[i] = xv.down(k + 4 * g4, p0 + 16 * i + li) * scale;
 #pragma unroll
             for (int i = 0; i < kLN; ++i) y[i] = bv.down(k + 4 * g4, n0 + 16 * i + li);
-            if (lo > 0) {  // the same for the whole block
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const bool in = k + 4 * g4 + j >= lo;
-#pragma unroll
-                    for (int i = 0; i < kLP; ++i) x[i][j] = in ? x[i][j] : 0.0f;
-#pragma unroll
-                    for (int i = 0; i < kLN; ++i) y[i][j] = in ? y[i][j] : 0.0f;
-                }
-            }
 #pragma unroll
             for (int i = 0; i < kLP; ++i)
 #pragma unroll
