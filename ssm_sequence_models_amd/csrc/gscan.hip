@@ -39,6 +39,7 @@
 // A is a product of decays, so it must not leave fp32's range: gates of the log form above 0 are
 // served as long as e^(their sum) over consecutive tokens is finite (times a state of 0, infinity
 // would be NaN).
+//
 // A span that holds a sequence start passes nothing on; it is marked by A = -1 (a product of
 // decays is never negative) and folded by a select, so a NaN or infinity of one sequence does
 // not reach the next.  Everything is fp32; outputs are rounded once.

@@ -134,10 +134,10 @@ __device__ __forceinline__ f4 load4(const uint16_t* p) {
               __uint_as_float(q[1] << 16), __uint_as_float(q[1] & 0xFFFF0000u)};
 }
 
-// A row-major view [tokens][cols] of the chunk's tokens lo .. rows - 1: zeros outside.  What lies outside is read
-// from the last row and column instead (of no rows, the first) and replaced, so no load is under a
-// branch and waits for another.  W: cols is a multiple of 16, so four consecutive columns are inside
-// or outside.
+// A row-major view [tokens][cols] of the chunk's tokens lo .. rows - 1: zeros outside.  What lies
+// outside is read from the last row and column instead (of no rows, the first) and replaced, so no
+// load is under a branch and waits for another.  W: cols is a multiple of 16, so four consecutive
+// columns are inside or outside.
 template <class S, bool W>
 struct View {
     const typename S::T* p;
