@@ -510,6 +510,68 @@ ssm_status_t ssm_gated_scan_step(const void* x, int64_t x_row, const void* gate,
                                  ssm_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------
+ * The gated delta rule: [LG] Sec. 2.1 Eq. (1) with a transition that also takes out what the state
+ * holds along the new token's key, h_t = a_t h_{t-1} (I - beta_t k_t k_t^T) + beta_t v_t k_t^T.  Per
+ * row b and head h (state h [headdim, dstate], key head h / (nheads / ngroups)):
+ *     e_t = v_t - a_t h_{t-1} k_t,   h_t = a_t h_{t-1} + beta_t e_t k_t^T,   y_t = scale h_t q_t
+ * a_t = exp(gate_t) (1 when gate is NULL), h_{-1} = initial_state (zeros when NULL); the state restarts
+ * from zero where seq_idx[b,t] != seq_idx[b,t-1] (a_t counts as 0 there).  The recurrence contracts
+ * for beta_t |k_t|^2 <= 2 and gates <= 0: keys are meant to be normed (ssm_qk_norm_fwd); outside that
+ * range states grow as the formula has them grow.  Gates above 0 are served while the products of
+ * decays of any 64 consecutive tokens are finite in fp32; gates below -1e4 count as -1e4.
+ *
+ *   q, k           [batch, seqlen, ngroups, dstate]  dtype; token t of row b at
+ *                  p + (b * seqlen + t) * p_row elements, its heads side by side (a channel range of
+ *                  a wider tensor).  The same for the other token tensors; input rows p_row >= 0,
+ *                  output rows at least the token's elements apart
+ *   v, y, dy, dv   [batch, seqlen, nheads, headdim]  dtype
+ *   beta, gate     [batch, seqlen, nheads] fp32; gate or NULL
+ *   initial_state, final_state, dfinal_state, dinitial_state   [batch, nheads, headdim, dstate] fp32,
+ *                  16-byte aligned, or NULL (zeros / not written)
+ *   seq_idx        [batch, seqlen] int32, or NULL
+ *   workspace      ..._workspace_size bytes, 256-byte aligned
+ * dstate a multiple of 4, at most 256; any headdim.  States and sums in fp32 (sums of gates in 64
+ * bits), products exact to fp32 for SSM_F32 and for everything that a fp32 output depends on; outputs
+ * rounded once.  Deterministic.
+ *
+ * ssm_delta_scan_fwd   final_state may be initial_state; no other output may overlap an input.
+ *     seqlen = 0: final = initial (or zeros).
+ * ssm_delta_scan_bwd   from dy and dfinal_state: dq, dk (summed over the heads of a key head), dv,
+ *     dbeta, dgate (NULL: not written), dinitial_state.  Nothing is kept from the forward.  Outputs
+ *     must not overlap inputs (dinitial_state == dfinal_state is refused).  seqlen = 0:
+ *     dinitial_state = dfinal_state (or zeros).
+ * ssm_delta_scan_step  n_new >= 1 tokens a request on pool slot s = state_indices[b] (b when NULL):
+ *     state [n_slots, nheads, headdim, dstate] fp32, in / out.  A row whose slot is outside
+ *     [0, n_slots) is skipped: its y is zero-filled, the pool is not touched.  Two rows on one slot:
+ *     undefined.
+ * ------------------------------------------------------------------------------------- */
+size_t ssm_delta_scan_fwd_workspace_size(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim,
+                                         int64_t ngroups, int64_t dstate, ssm_dtype_t dtype);
+ssm_status_t ssm_delta_scan_fwd(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v,
+                                int64_t v_row, const float* beta, const float* gate, float scale,
+                                const float* initial_state, float* final_state, const int32_t* seq_idx,
+                                void* y, int64_t y_row, int64_t batch, int64_t seqlen, int64_t nheads,
+                                int64_t headdim, int64_t ngroups, int64_t dstate, ssm_dtype_t dtype,
+                                void* workspace, size_t workspace_bytes, ssm_stream_t stream);
+size_t ssm_delta_scan_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim,
+                                         int64_t ngroups, int64_t dstate, ssm_dtype_t dtype);
+ssm_status_t ssm_delta_scan_bwd(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v,
+                                int64_t v_row, const float* beta, const float* gate, float scale,
+                                const void* dy, int64_t dy_row, const float* initial_state,
+                                const float* dfinal_state, const int32_t* seq_idx, void* dq, int64_t dq_row,
+                                void* dk, int64_t dk_row, void* dv, int64_t dv_row, float* dbeta,
+                                float* dgate, float* dinitial_state, int64_t batch, int64_t seqlen,
+                                int64_t nheads, int64_t headdim, int64_t ngroups, int64_t dstate,
+                                ssm_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                                ssm_stream_t stream);
+ssm_status_t ssm_delta_scan_step(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v,
+                                 int64_t v_row, const float* beta, const float* gate, float scale,
+                                 float* state, const int32_t* state_indices, void* y, int64_t y_row,
+                                 int64_t batch, int64_t n_new, int64_t nheads, int64_t headdim,
+                                 int64_t ngroups, int64_t dstate, int64_t n_slots, ssm_dtype_t dtype,
+                                 ssm_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
  * ssm_norm_fwd / ssm_norm_bwd -- RMS or layer norm of rows of channels with an optional SiLU
  * gate: the norm between a layer's scan and its output projection (gate before or after), or
  * a plain pre-norm (z NULL).  Per row and group of m = channels / ngroups channels:

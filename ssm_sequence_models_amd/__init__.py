@@ -127,6 +127,16 @@ def _load():
                                        fp, i64, i64, i64, ci, ci, vp, sz, vp]
     lib.ssm_gated_scan_step.argtypes = [vp, i64, vp, i64, fp, i32p, vp, i64, i64, i64, i64, i64,
                                         ci, ci, vp]
+    sizes = [i64, i64, i64, i64, i64, i64, ci]
+    for f in (lib.ssm_delta_scan_fwd_workspace_size, lib.ssm_delta_scan_bwd_workspace_size):
+        f.restype = sz
+        f.argtypes = sizes
+    qkv = [vp, i64, vp, i64, vp, i64, fp, fp, cf]
+    lib.ssm_delta_scan_fwd.argtypes = qkv + [fp, fp, i32p, vp, i64] + sizes + [vp, sz, vp]
+    lib.ssm_delta_scan_bwd.argtypes = qkv + [vp, i64, fp, fp, i32p, vp, i64, vp, i64, vp, i64, fp, fp,
+                                             fp] + sizes + [vp, sz, vp]
+    lib.ssm_delta_scan_step.argtypes = qkv + [fp, i32p, vp, i64, i64, i64, i64, i64, i64, i64, i64, ci,
+                                              vp]
     lib.ssm_stream_copy.argtypes = [vp, vp, i64, vp]
     lib.ssm_timing_enable.argtypes = [ci]
     lib.ssm_timing_read.argtypes = [ctypes.POINTER(ctypes.c_double),
@@ -136,6 +146,7 @@ def _load():
               "ssm_conv_scan_fwd_pooled", "ssm_state_stats_update", "ssm_scan_fwd_vector_decay",
               "ssm_initial_state_noise", "ssm_state_reset", "ssm_stream_copy", "ssm_norm_fwd",
               "ssm_norm_bwd", "ssm_scan_bwd", "ssm_gated_scan_fwd", "ssm_gated_scan_bwd", "ssm_gated_scan_step",
+              "ssm_delta_scan_fwd", "ssm_delta_scan_bwd", "ssm_delta_scan_step",
               "ssm_timing_enable", "ssm_timing_read"):
         getattr(lib, f).restype = ci
     return lib
@@ -824,6 +835,152 @@ def gated_scan_step(x, gate, state, form="sigmoid", state_indices=None, y=None):
         _check("ssm_gated_scan_step", _lib.ssm_gated_scan_step(
             _ptr(x), x_row, _ptr(gate), gate_row, _ptr(state), _ptr(state_indices), _ptr(y),
             _rows(y, "y", C)[1], B, T, C, state.shape[0], GATE[form], _dtype_code(x), _stream()))
+    return y
+
+
+def _token_row(t, name):
+    """Row stride of token tensor t [b, L, heads, dim]: a token's heads side by side, tokens at one
+    stride."""
+    b, L, heads, dim = t.shape
+    if t.is_contiguous():
+        return heads * dim
+    if (dim > 1 and t.stride(3) != 1) or (heads > 1 and t.stride(2) != dim):
+        raise ValueError(f"{name} must have a token's heads side by side")
+    row = t.stride(1) if L > 1 else t.stride(0) if b > 1 else heads * dim
+    if L > 1 and b > 1 and t.stride(0) != L * row:
+        raise ValueError(f"{name} must have its tokens at one stride")
+    return row
+
+
+def _delta_args(q, k, v, beta, gate, scale):
+    """Checks shared by the delta scans; returns (the leading arguments of the C calls, the sizes
+    batch, seqlen, nheads, headdim, ngroups, dstate)."""
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if t.dim() != 4:
+            raise ValueError(f"{name} must be [batch, tokens, heads, dim], got shape {tuple(t.shape)}")
+    b, L, H, P = v.shape
+    G, N = k.shape[2:]
+    if H < 1 or P < 1 or G < 1 or N < 1 or H % G != 0:
+        raise ValueError(f"v's {H} heads must be a positive multiple of k's {G}, and no dimension of a head 0")
+    _need(v, "v", contiguous=False)
+    _need(k, "k", v.dtype, (b, L, G, N), contiguous=False)
+    _need(q, "q", v.dtype, (b, L, G, N), contiguous=False)
+    _need(beta, "beta", torch.float32, (b, L, H))
+    _need(gate, "gate", torch.float32, (b, L, H))
+    _need_device(v, q=q, k=k, beta=beta, gate=gate)
+    return ((_ptr(q), _token_row(q, "q"), _ptr(k), _token_row(k, "k"), _ptr(v), _token_row(v, "v"),
+             _ptr(beta), _ptr(gate), scale), (b, L, H, P, G, N))
+
+
+def delta_scan_fwd_workspace_size(batch, seqlen, nheads, headdim, ngroups, dstate,
+                                  dtype=torch.bfloat16) -> int:
+    code = SSM_BF16 if dtype == torch.bfloat16 else SSM_F32
+    return int(_lib.ssm_delta_scan_fwd_workspace_size(batch, seqlen, nheads, headdim, ngroups, dstate,
+                                                      code))
+
+
+def delta_scan_bwd_workspace_size(batch, seqlen, nheads, headdim, ngroups, dstate,
+                                  dtype=torch.bfloat16) -> int:
+    code = SSM_BF16 if dtype == torch.bfloat16 else SSM_F32
+    return int(_lib.ssm_delta_scan_bwd_workspace_size(batch, seqlen, nheads, headdim, ngroups, dstate,
+                                                      code))
+
+
+def delta_scan_fwd(q, k, v, beta, gate=None, scale=1.0, initial_state=None, seq_idx=None,
+                   return_final_state=True, final_state=None, y=None, workspace=None):
+    """The gated delta rule (length-generalization notes Sec. 2.1 Eq. (1) with the transition
+    a_t (I - beta_t k_t k_t^T)): e_t = v_t - a_t h_{t-1} k_t, h_t = a_t h_{t-1} + beta_t e_t k_t^T,
+    y_t = scale h_t q_t, a_t = exp(gate_t).  q, k [b, L, G, N], v [b, L, H, P] (a token's heads side
+    by side, tokens at any one stride; H a multiple of G, N a multiple of 4 up to 256), beta, gate
+    [b, L, H] fp32 (gate None: 1 for every a); initial_state [b, H, P, N] fp32 (may be the same
+    tensor as final_state); seq_idx [b, L] int32.  Returns (y [b, L, H, P], final_state or None)."""
+    lead, sizes = _delta_args(q, k, v, beta, gate, scale)
+    b, L, H, P, G, N = sizes
+    _need(initial_state, "initial_state", torch.float32, (b, H, P, N))
+    _need(seq_idx, "seq_idx", torch.int32, (b, L))
+    if y is None:
+        y = torch.empty((b, L, H, P), dtype=v.dtype, device=v.device)
+    _need(y, "y", v.dtype, (b, L, H, P), contiguous=False)
+    if final_state is None and return_final_state:
+        final_state = torch.empty((b, H, P, N), dtype=torch.float32, device=v.device)
+    _need(final_state, "final_state", torch.float32, (b, H, P, N))
+    _need_device(v, initial_state=initial_state, seq_idx=seq_idx, y=y, final_state=final_state,
+                 workspace=workspace)
+    ws, wsb = _workspace(workspace, delta_scan_fwd_workspace_size(*sizes, v.dtype), v.device)
+    with _on(v.device):
+        _check("ssm_delta_scan_fwd", _lib.ssm_delta_scan_fwd(
+            *lead, _ptr(initial_state), _ptr(final_state), _ptr(seq_idx), _ptr(y),
+            _token_row(y, "y"), *sizes, _dtype_code(v), _ptr(ws), wsb, _stream()))
+    return y, final_state
+
+
+def delta_scan_bwd(q, k, v, beta, dy, gate=None, scale=1.0, initial_state=None, dfinal_state=None,
+                   seq_idx=None, dq=None, dk=None, dv=None, dbeta=None, dgate=None,
+                   dinitial_state=None, workspace=None):
+    """Backward of delta_scan_fwd from dy [b, L, H, P] and dfinal_state [b, H, P, N] fp32 (None =
+    zero); the other inputs as delta_scan_fwd's.  Returns (dq, dk [b, L, G, N], dv [b, L, H, P],
+    dbeta [b, L, H] fp32, dgate [b, L, H] fp32 or None without gate, dinitial_state
+    [b, H, P, N] fp32)."""
+    lead, sizes = _delta_args(q, k, v, beta, gate, scale)
+    b, L, H, P, G, N = sizes
+    dev = v.device
+    _need(dy, "dy", v.dtype, (b, L, H, P), contiguous=False)
+    _need(initial_state, "initial_state", torch.float32, (b, H, P, N))
+    _need(dfinal_state, "dfinal_state", torch.float32, (b, H, P, N))
+    _need(seq_idx, "seq_idx", torch.int32, (b, L))
+    if gate is None and dgate is not None:
+        raise ValueError("dgate given without gate")
+    if dq is None:
+        dq = torch.empty((b, L, G, N), dtype=v.dtype, device=dev)
+    if dk is None:
+        dk = torch.empty((b, L, G, N), dtype=v.dtype, device=dev)
+    if dv is None:
+        dv = torch.empty((b, L, H, P), dtype=v.dtype, device=dev)
+    if dbeta is None:
+        dbeta = torch.empty_like(beta)
+    if dgate is None and gate is not None:
+        dgate = torch.empty_like(gate)
+    if dinitial_state is None:
+        dinitial_state = torch.empty((b, H, P, N), dtype=torch.float32, device=dev)
+    _need(dq, "dq", v.dtype, (b, L, G, N), contiguous=False)
+    _need(dk, "dk", v.dtype, (b, L, G, N), contiguous=False)
+    _need(dv, "dv", v.dtype, (b, L, H, P), contiguous=False)
+    _need(dbeta, "dbeta", torch.float32, (b, L, H))
+    _need(dgate, "dgate", torch.float32, (b, L, H))
+    _need(dinitial_state, "dinitial_state", torch.float32, (b, H, P, N))
+    _need_device(v, dy=dy, initial_state=initial_state, dfinal_state=dfinal_state, seq_idx=seq_idx,
+                 dq=dq, dk=dk, dv=dv, dbeta=dbeta, dgate=dgate, dinitial_state=dinitial_state,
+                 workspace=workspace)
+    ws, wsb = _workspace(workspace, delta_scan_bwd_workspace_size(*sizes, v.dtype), dev)
+    with _on(dev):
+        _check("ssm_delta_scan_bwd", _lib.ssm_delta_scan_bwd(
+            *lead, _ptr(dy), _token_row(dy, "dy"), _ptr(initial_state), _ptr(dfinal_state),
+            _ptr(seq_idx), _ptr(dq), _token_row(dq, "dq"), _ptr(dk), _token_row(dk, "dk"), _ptr(dv),
+            _token_row(dv, "dv"), _ptr(dbeta), _ptr(dgate), _ptr(dinitial_state), *sizes,
+            _dtype_code(v), _ptr(ws), wsb, _stream()))
+    return dq, dk, dv, dbeta, dgate, dinitial_state
+
+
+def delta_scan_step(q, k, v, beta, state, gate=None, scale=1.0, state_indices=None, y=None):
+    """Decode update of a pool of delta_scan states: q, k [b, n_new, G, N], v [b, n_new, H, P], beta,
+    gate [b, n_new, H] fp32, state [n_slots, H, P, N] fp32 (updated in place), state_indices [b]
+    int32 (None: row b uses slot b).  Returns y [b, n_new, H, P]."""
+    lead, sizes = _delta_args(q, k, v, beta, gate, scale)
+    b, T, H, P, G, N = sizes
+    if state.dim() != 4 or tuple(state.shape[1:]) != (H, P, N):
+        raise ValueError(f"state must be [n_slots, {H}, {P}, {N}], got shape {tuple(state.shape)}")
+    _need(state, "state", torch.float32)
+    _need(state_indices, "state_indices", torch.int32, (b,))
+    if DEBUG_CHECKS:
+        check_distinct_slots(state_indices, state.shape[0], "state_indices")
+    if y is None:
+        y = torch.empty((b, T, H, P), dtype=v.dtype, device=v.device)
+    _need(y, "y", v.dtype, (b, T, H, P), contiguous=False)
+    _need_device(v, state=state, state_indices=state_indices, y=y)
+    with _on(v.device):
+        _check("ssm_delta_scan_step", _lib.ssm_delta_scan_step(
+            *lead, _ptr(state), _ptr(state_indices), _ptr(y), _token_row(y, "y"), *sizes,
+            state.shape[0], _dtype_code(v), _stream()))
     return y
 
 

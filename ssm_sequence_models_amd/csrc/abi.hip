@@ -7,6 +7,7 @@
 #include <utility>
 #include <vector>
 
+#include "delta.h"
 #include "internal.h"
 
 namespace {
@@ -1287,6 +1288,242 @@ ssm_status_t ssm_gated_scan_step(const void* x, int64_t x_row, const void* gate,
     return hip_status(ssm::launch_gscan_step(c, state, state_indices, n_slots,
                                              reinterpret_cast<hipStream_t>(stream)),
                       fn);
+}
+
+namespace {
+
+// what the three calls of the gated delta rule share: sizes, then the token rows' strides
+ssm_status_t check_delta_dims(const char* fn, int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim,
+                              int64_t ngroups, int64_t dstate, float scale, int dtype) {
+    ssm_status_t st = check_scan_dims(fn, batch, seqlen, nheads, headdim, ngroups, dstate, dtype);
+    if (st != SSM_OK) return st;
+    if (dstate % 4 != 0 || dstate > 256)
+        return fail(SSM_ERR_UNSUPPORTED, std::string(fn) + ": dstate must be a multiple of 4, at most 256");
+    if (headdim > 65536) return fail(SSM_ERR_UNSUPPORTED, std::string(fn) + ": headdim must be at most 65536");
+    if (!std::isfinite(scale)) return fail(SSM_ERR_INVALID_ARG, std::string(fn) + ": scale must be finite");
+    return SSM_OK;
+}
+// sizes whose products below do not leave 63 bits, nor their grids 31
+bool delta_sizes_fit(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim) {
+    const int64_t most = int64_t{1} << 31;
+    if (batch >= most || seqlen >= most || nheads >= most) return false;
+    if (batch == 0 || seqlen == 0) return true;
+    return nheads < most / batch && (seqlen + 31) / 32 < most / (batch * nheads) &&
+           (headdim + 15) / 16 < most / (batch * nheads);
+}
+
+}  // namespace
+
+size_t ssm_delta_scan_fwd_workspace_size(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim,
+                                         int64_t ngroups, int64_t dstate, ssm_dtype_t dtype) {
+    if (batch <= 0 || seqlen <= 0 ||
+        check_delta_dims("ssm_delta_scan_fwd_workspace_size", batch, seqlen, nheads, headdim, ngroups, dstate, 1.0f, dtype) != SSM_OK ||
+        !delta_sizes_fit(batch, seqlen, nheads, headdim))
+        return 0;
+    return ssm::delta_fwd_workspace_bytes(batch, seqlen, nheads, headdim, ngroups, dstate, dtype);
+}
+
+size_t ssm_delta_scan_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim,
+                                         int64_t ngroups, int64_t dstate, ssm_dtype_t dtype) {
+    if (batch <= 0 || seqlen <= 0 ||
+        check_delta_dims("ssm_delta_scan_bwd_workspace_size", batch, seqlen, nheads, headdim, ngroups, dstate, 1.0f, dtype) != SSM_OK ||
+        !delta_sizes_fit(batch, seqlen, nheads, headdim))
+        return 0;
+    return ssm::delta_bwd_workspace_bytes(batch, seqlen, nheads, headdim, ngroups, dstate, dtype);
+}
+
+ssm_status_t ssm_delta_scan_fwd(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v,
+                                int64_t v_row, const float* beta, const float* gate, float scale,
+                                const float* initial_state, float* final_state, const int32_t* seq_idx,
+                                void* y, int64_t y_row, int64_t batch, int64_t seqlen, int64_t nheads,
+                                int64_t headdim, int64_t ngroups, int64_t dstate, ssm_dtype_t dtype,
+                                void* workspace, size_t workspace_bytes, ssm_stream_t stream) {
+    const char* fn = "ssm_delta_scan_fwd";
+    ssm_status_t st = check_delta_dims(fn, batch, seqlen, nheads, headdim, ngroups, dstate, scale, dtype);
+    if (st != SSM_OK) return st;
+    if (!delta_sizes_fit(batch, seqlen, nheads, headdim))
+        return fail(SSM_ERR_UNSUPPORTED, std::string(fn) + ": batch, seqlen, nheads or headdim too large");
+    const size_t es = esize(dtype);
+    const bool work = batch > 0 && seqlen > 0;
+    const int64_t rows = batch * seqlen;
+    st = check_ptrs(fn, {{"q", q, work, es},
+                         {"k", k, work, es},
+                         {"v", v, work, es},
+                         {"beta", beta, work, 4},
+                         {"gate", gate, false, 4},
+                         {"initial_state", initial_state, false, 16},
+                         {"final_state", final_state, false, 16},
+                         {"seq_idx", seq_idx, false, 4},
+                         {"y", y, work, es}});
+    if (st == SSM_OK) st = check_row(fn, "q", q, q_row, rows, 0);
+    if (st == SSM_OK) st = check_row(fn, "k", k, k_row, rows, 0);
+    if (st == SSM_OK) st = check_row(fn, "v", v, v_row, rows, 0);
+    if (st == SSM_OK) st = check_row(fn, "y", y, y_row, rows, nheads * headdim);
+    if (st != SSM_OK) return st;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    if (!work)
+        return hip_status(ssm::launch_copy_or_zero_f32(final_state, initial_state, batch * nheads * headdim * dstate, s), fn);
+    const size_t need = ssm_delta_scan_fwd_workspace_size(batch, seqlen, nheads, headdim, ngroups, dstate, dtype);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 256)))
+        return fail(SSM_ERR_WORKSPACE, std::string(fn) + ": workspace must be >= " + std::to_string(need) +
+                                           " bytes, 256-byte aligned");
+    ssm::DeltaArgs a{};
+    a.q = q;
+    a.q_row = q_row;
+    a.k = k;
+    a.k_row = k_row;
+    a.v = v;
+    a.v_row = v_row;
+    a.beta = beta;
+    a.gate = gate;
+    a.scale = scale;
+    a.h0 = initial_state;
+    a.final_state = final_state;
+    a.seq = seq_idx;
+    a.y = y;
+    a.y_row = y_row;
+    a.B = batch;
+    a.L = seqlen;
+    a.H = nheads;
+    a.P = headdim;
+    a.G = ngroups;
+    a.N = dstate;
+    return hip_status(ssm::launch_delta_fwd(a, workspace, dtype, s), fn);
+}
+
+ssm_status_t ssm_delta_scan_bwd(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v,
+                                int64_t v_row, const float* beta, const float* gate, float scale,
+                                const void* dy, int64_t dy_row, const float* initial_state,
+                                const float* dfinal_state, const int32_t* seq_idx, void* dq, int64_t dq_row,
+                                void* dk, int64_t dk_row, void* dv, int64_t dv_row, float* dbeta,
+                                float* dgate, float* dinitial_state, int64_t batch, int64_t seqlen,
+                                int64_t nheads, int64_t headdim, int64_t ngroups, int64_t dstate,
+                                ssm_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                                ssm_stream_t stream) {
+    const char* fn = "ssm_delta_scan_bwd";
+    ssm_status_t st = check_delta_dims(fn, batch, seqlen, nheads, headdim, ngroups, dstate, scale, dtype);
+    if (st != SSM_OK) return st;
+    if (!delta_sizes_fit(batch, seqlen, nheads, headdim))
+        return fail(SSM_ERR_UNSUPPORTED, std::string(fn) + ": batch, seqlen, nheads or headdim too large");
+    const size_t es = esize(dtype);
+    const bool work = batch > 0 && seqlen > 0;
+    const int64_t rows = batch * seqlen;
+    st = check_ptrs(fn, {{"q", q, work, es},
+                         {"k", k, work, es},
+                         {"v", v, work, es},
+                         {"beta", beta, work, 4},
+                         {"gate", gate, false, 4},
+                         {"dy", dy, work, es},
+                         {"initial_state", initial_state, false, 16},
+                         {"dfinal_state", dfinal_state, false, 16},
+                         {"seq_idx", seq_idx, false, 4},
+                         {"dq", dq, work, es},
+                         {"dk", dk, work, es},
+                         {"dv", dv, work, es},
+                         {"dbeta", dbeta, work, 4},
+                         {"dgate", dgate, false, 4},
+                         {"dinitial_state", dinitial_state, false, 16}});
+    if (st == SSM_OK) st = check_row(fn, "q", q, q_row, rows, 0);
+    if (st == SSM_OK) st = check_row(fn, "k", k, k_row, rows, 0);
+    if (st == SSM_OK) st = check_row(fn, "v", v, v_row, rows, 0);
+    if (st == SSM_OK) st = check_row(fn, "dy", dy, dy_row, rows, 0);
+    if (st == SSM_OK) st = check_row(fn, "dq", dq, dq_row, rows, ngroups * dstate);
+    if (st == SSM_OK) st = check_row(fn, "dk", dk, dk_row, rows, ngroups * dstate);
+    if (st == SSM_OK) st = check_row(fn, "dv", dv, dv_row, rows, nheads * headdim);
+    if (st != SSM_OK) return st;
+    if (dinitial_state != nullptr && dinitial_state == dfinal_state)
+        return fail(SSM_ERR_INVALID_ARG, std::string(fn) + ": dinitial_state must not be dfinal_state");
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    if (!work)
+        return hip_status(ssm::launch_copy_or_zero_f32(dinitial_state, dfinal_state, batch * nheads * headdim * dstate, s), fn);
+    const size_t need = ssm_delta_scan_bwd_workspace_size(batch, seqlen, nheads, headdim, ngroups, dstate, dtype);
+    if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 256))
+        return fail(SSM_ERR_WORKSPACE, std::string(fn) + ": workspace must be >= " + std::to_string(need) +
+                                           " bytes, 256-byte aligned");
+    ssm::DeltaArgs a{};
+    a.q = q;
+    a.q_row = q_row;
+    a.k = k;
+    a.k_row = k_row;
+    a.v = v;
+    a.v_row = v_row;
+    a.beta = beta;
+    a.gate = gate;
+    a.scale = scale;
+    a.dy = dy;
+    a.dy_row = dy_row;
+    a.h0 = initial_state;
+    a.dhT = dfinal_state;
+    a.seq = seq_idx;
+    a.dq = dq;
+    a.dq_row = dq_row;
+    a.dk = dk;
+    a.dk_row = dk_row;
+    a.dv = dv;
+    a.dv_row = dv_row;
+    a.dbeta = dbeta;
+    a.dgate = dgate;
+    a.dh0 = dinitial_state;
+    a.B = batch;
+    a.L = seqlen;
+    a.H = nheads;
+    a.P = headdim;
+    a.G = ngroups;
+    a.N = dstate;
+    return hip_status(ssm::launch_delta_bwd(a, workspace, dtype, s), fn);
+}
+
+ssm_status_t ssm_delta_scan_step(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v,
+                                 int64_t v_row, const float* beta, const float* gate, float scale,
+                                 float* state, const int32_t* state_indices, void* y, int64_t y_row,
+                                 int64_t batch, int64_t n_new, int64_t nheads, int64_t headdim,
+                                 int64_t ngroups, int64_t dstate, int64_t n_slots, ssm_dtype_t dtype,
+                                 ssm_stream_t stream) {
+    const char* fn = "ssm_delta_scan_step";
+    ssm_status_t st = check_delta_dims(fn, batch, n_new, nheads, headdim, ngroups, dstate, scale, dtype);
+    if (st != SSM_OK) return st;
+    if (n_slots < 1) return fail(SSM_ERR_INVALID_ARG, std::string(fn) + ": n_slots must be >= 1");
+    if (!delta_sizes_fit(batch, n_new, nheads, headdim))
+        return fail(SSM_ERR_UNSUPPORTED, std::string(fn) + ": batch, n_new, nheads or headdim too large");
+    const size_t es = esize(dtype);
+    const bool work = batch > 0 && n_new > 0;
+    const int64_t rows = batch * n_new;
+    st = check_ptrs(fn, {{"q", q, work, es},
+                         {"k", k, work, es},
+                         {"v", v, work, es},
+                         {"beta", beta, work, 4},
+                         {"gate", gate, false, 4},
+                         {"state", state, work, 16},
+                         {"state_indices", state_indices, false, 4},
+                         {"y", y, work, es}});
+    if (st == SSM_OK) st = check_row(fn, "q", q, q_row, rows, 0);
+    if (st == SSM_OK) st = check_row(fn, "k", k, k_row, rows, 0);
+    if (st == SSM_OK) st = check_row(fn, "v", v, v_row, rows, 0);
+    if (st == SSM_OK) st = check_row(fn, "y", y, y_row, rows, nheads * headdim);
+    if (st != SSM_OK) return st;
+    if (!work) return ok();
+    ssm::DeltaStep d{};
+    d.a.q = q;
+    d.a.q_row = q_row;
+    d.a.k = k;
+    d.a.k_row = k_row;
+    d.a.v = v;
+    d.a.v_row = v_row;
+    d.a.beta = beta;
+    d.a.gate = gate;
+    d.a.scale = scale;
+    d.a.y = y;
+    d.a.y_row = y_row;
+    d.a.B = batch;
+    d.a.L = n_new;
+    d.a.H = nheads;
+    d.a.P = headdim;
+    d.a.G = ngroups;
+    d.a.N = dstate;
+    d.state_in = d.state_out = state;
+    d.slots = state_indices;
+    d.n_slots = n_slots;
+    return hip_status(ssm::launch_delta_step(d, dtype, reinterpret_cast<hipStream_t>(stream)), fn);
 }
 
 namespace {

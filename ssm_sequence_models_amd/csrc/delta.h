@@ -1,0 +1,342 @@
+// delta.h -- what the kernels of the gated delta rule share: the arguments, the two arithmetics
+// (bf16 matrix instructions on split operands, fp32 matrix instructions) and the workspace.
+//
+// Per head, with state h [P, N], a_t = e^gate_t and b_t = beta_t:
+//     e_t = v_t - a_t h_{t-1} k_t,   h_t = a_t h_{t-1} + b_t e_t k_t^T,   y_t = scale h_t q_t
+// Over a chunk of Q tokens that starts from h_0, with G_t the sum of the gates from the chunk's
+// start on and r_ts = e^(G_t - G_s) (0 where a packed sequence starts in (s, t]):
+//     D_ts = r_ts (k_t . k_s) b_s (s < t),   T = (I + D)^-1,   M_ts = scale r_ts q_t . k_s (s <= t)
+//     Z = V - e^G K h_0^T,   E = T Z,   U = b E
+//     Y = scale e^G Q h_0^T + M U,   h_Q = e^{G_Q} h_0 + U^T e^{G_Q - G} K
+// (E and b U keep apart so that b = 0 needs no division.)  T and M need no state: delta_prep forms
+// them for all chunks at once, and only the products with the state walk along the row.
+//
+// Layout of a walk: a wavefront owns 16 channels of one head for the whole row, with their state in
+// accumulators (rows: state dimension, columns: channels).  Every product's result has the tokens or
+// the state dimensions as rows and the wavefront's channels as columns, which is the next product's
+// right operand as it stands (mfma_tiles.h: "token order"), so no value passes between
+// wavefronts; K, Q, T and M are the left operands, shared in LDS.
+#pragma once
+
+#include "internal.h"
+#include "mfma_tiles.h"
+
+namespace ssm {
+
+struct DeltaArgs {
+    const void* q;  // [B, L, G, N], token rows q_row elements apart
+    const void* k;
+    const void* v;  // [B, L, H, P]
+    const void* dy;
+    const float* beta;  // [B, L, H]
+    const float* gate;  // [B, L, H] or NULL (= 0)
+    const float* h0;    // [B, H, P, N] or NULL
+    const float* dhT;   // [B, H, P, N] or NULL
+    const int32_t* seq;
+    void* y;
+    void* dq;
+    void* dk;
+    void* dv;
+    float* dbeta;
+    float* dgate;        // or NULL
+    float* dh0;          // or NULL
+    float* final_state;  // [B, H, P, N] or NULL
+    int64_t q_row, k_row, v_row, y_row, dy_row, dq_row, dk_row, dv_row;
+    int64_t B, L, H, P, G, N;
+    float scale;
+    // set by the launchers: the chunks' part of the workspace
+    int64_t chunks;
+    uint8_t* T;      // [B, H, chunks] images
+    uint8_t* M;
+    float* factors;  // [B, H, chunks, 3, Q]: e^G from the chunk's start, e^{G_Q - G}, beta
+};
+
+namespace delta {
+
+constexpr double kLog2e = 1.4426950408889634;
+
+// Sums of gates below this are as good as minus infinity (e^-1e4 = 0 in fp32), and finite: their
+// differences are no NaN.  A NaN stays one.
+constexpr float kLeastGate = -1e4f;
+__device__ __forceinline__ double gate_of(float g) { return g < kLeastGate ? kLeastGate : g; }
+
+// e^x of a sum kept in double
+__device__ __forceinline__ float exp_of(double x) { return exp2_of(x * kLog2e); }
+
+__device__ __forceinline__ float get(f4 v, int e) { return v[e]; }
+
+// ---------------------------------------------------------------------------------------
+// bf16: exact operands as they are, fp32 operands in bf16 parts (three hold all 24 bits)
+// ---------------------------------------------------------------------------------------
+struct ByBf16 {
+    using S = uint16_t;
+    static constexpr int Q = 64;   // tokens a chunk
+    static constexpr int KB = 32;  // contraction of one operand pair
+    static constexpr int R = 8;    // of it, values a lane
+    static constexpr int TP = 3;   // parts of T
+    template <int PARTS>
+    struct Frag {
+        bf8 p[PARTS];
+    };
+    template <int PARTS>
+    __device__ __forceinline__ static Frag<PARTS> parts(const float (&v)[8]) {
+        Frag<PARTS> f;
+        split<PARTS>(v, f.p);
+        return f;
+    }
+    // rows of the right operand's contraction block kk, from result tiles
+    template <int PARTS>
+    __device__ __forceinline__ static Frag<PARTS> of_tiles(const f4* tile, int kk) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = tile[2 * kk + (j >> 2)][j & 3];
+        return parts<PARTS>(v);
+    }
+    // products of parts whose orders sum below the more exact side's
+    template <int PA, int PB>
+    __device__ __forceinline__ static void mac(f4& c, const Frag<PA>& a, const Frag<PB>& b) {
+#pragma unroll
+        for (int i = PA - 1; i >= 0; --i)
+#pragma unroll
+            for (int j = PB - 1; j >= 0; --j)
+                if (i + j < (PA > PB ? PA : PB)) c = mfma(a.p[i], b.p[j], c);
+    }
+    __device__ __forceinline__ static float value(const S* p, int64_t i) { return bf16_to_f32(p[i]); }
+    __device__ __forceinline__ static void store(S* p, int64_t i, float v) { p[i] = f32_to_bf16(v); }
+
+    // LDS tiles of W columns: rows of 2 W bytes (128 or more) in swizzled 16-byte pieces
+    template <int W>
+    static constexpr int tile_bytes(int rows) { return rows * 2 * W; }
+    template <int W>
+    __device__ __forceinline__ static int piece_at(int row, int q) { return piece<2 * W>(row, q); }
+    // left operand, rows r0 + li, contraction block kk in token order
+    template <int W>
+    __device__ __forceinline__ static Frag<1> rows(const uint8_t* t, int r0, int kk, int li, int g4) {
+        const int at = (((g4 >> 1) ^ sw<2 * W>(li)) << 4 | (g4 & 1) << 3) ^ (kk << 6);
+        const uint8_t* p = t + (r0 + li) * (2 * W);
+        Frag<1> f;
+        f.p[0] = join(lds<s4>(p + at), lds<s4>(p + (at ^ 32)));
+        return f;
+    }
+    // the same in natural order
+    template <int W>
+    __device__ __forceinline__ static Frag<1> along(const uint8_t* t, int r0, int kk, int li, int g4) {
+        Frag<1> f;
+        f.p[0] = ssm::along<2 * W>(t, along_off<2 * W>(li, g4), r0, kk);
+        return f;
+    }
+    // left operand, columns 16 c + li as rows, contraction over the tile's rows r0 .. r0 + KB in token order
+    template <int W>
+    __device__ __forceinline__ static Frag<1> columns(const uint8_t* t, int r0, int c, int li, int g4) {
+        Frag<1> f;
+        f.p[0] = down<2 * W>(t, down_off<2 * W>(4 * g4, li), r0, c);
+        return f;
+    }
+    template <int W>
+    __device__ __forceinline__ static float at(const uint8_t* t, int row, int col) {
+        return bf16_to_f32(lds<uint16_t>(t + piece<2 * W>(row, col >> 3) + 2 * (col & 7)));
+    }
+    template <int W>
+    __device__ __forceinline__ static void put(uint8_t* t, int row, int col, bf8 v, int j) {
+        *reinterpret_cast<uint16_t*>(t + piece<2 * W>(row, col >> 3) + 2 * (col & 7)) = __builtin_bit_cast(uint16_t, v[j]);
+    }
+    // values n .. n + R of a row of N (a multiple of 4), zeros past its end
+    __device__ __forceinline__ static u4 load_run(const S* p, int n, int N) {
+        u4 v{0, 0, 0, 0};
+        if (n + 8 <= N) {
+            v = *reinterpret_cast<const u4any*>(p + n);
+        } else if (n < N) {
+            const u2 h = *reinterpret_cast<const u2any*>(p + n);
+            v[0] = h[0];
+            v[1] = h[1];
+        }
+        return v;
+    }
+    __device__ __forceinline__ static Frag<1> exact(u4 v) {
+        Frag<1> f;
+        f.p[0] = __builtin_bit_cast(bf8, v);
+        return f;
+    }
+};
+
+// ---------------------------------------------------------------------------------------
+// fp32: the same operands, whole (the number of parts says nothing here)
+// ---------------------------------------------------------------------------------------
+typedef uint32_t u4any4 __attribute__((ext_vector_type(4), aligned(4)));  // any fp32 address
+struct ByF32 {
+    using S = float;
+    static constexpr int Q = 32;
+    static constexpr int KB = 16;
+    static constexpr int R = 4;
+    static constexpr int TP = 1;
+    template <int PARTS>
+    struct Frag {
+        f4 v;
+    };
+    template <int PARTS>
+    __device__ __forceinline__ static Frag<PARTS> parts(const float (&v)[4]) {
+        return {f4{v[0], v[1], v[2], v[3]}};
+    }
+    template <int PARTS>
+    __device__ __forceinline__ static Frag<PARTS> of_tiles(const f4* tile, int kk) {
+        return {tile[kk]};
+    }
+    // one 16 x 16 x 4 instruction a value: lane groups g4 hold k = 4 g4 + e
+    template <int PA, int PB>
+    __device__ __forceinline__ static void mac(f4& c, const Frag<PA>& a, const Frag<PB>& b) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[e], b.v[e], c, 0, 0, 0);
+    }
+    __device__ __forceinline__ static float value(const S* p, int64_t i) { return p[i]; }
+    __device__ __forceinline__ static void store(S* p, int64_t i, float v) { p[i] = v; }
+
+    // LDS tiles of W columns: rows of W + 4 floats, so that 16 rows, and every fourth row, start at
+    // banks of their own
+    template <int W>
+    static constexpr int tile_bytes(int rows) { return rows * (W + 4) * 4; }
+    template <int W>
+    __device__ __forceinline__ static int piece_at(int row, int q) { return (row * (W + 4) + 4 * q) * 4; }
+    template <int W>
+    __device__ __forceinline__ static Frag<1> rows(const uint8_t* t, int r0, int kk, int li, int g4) {
+        return {lds<f4>(t + piece_at<W>(r0 + li, 4 * kk + g4))};
+    }
+    template <int W>
+    __device__ __forceinline__ static Frag<1> along(const uint8_t* t, int r0, int kk, int li, int g4) {
+        return rows<W>(t, r0, kk, li, g4);
+    }
+    template <int W>
+    __device__ __forceinline__ static Frag<1> columns(const uint8_t* t, int r0, int c, int li, int g4) {
+        Frag<1> f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f.v[e] = lds<float>(t + ((r0 + 4 * g4 + e) * (W + 4) + 16 * c + li) * 4);
+        return f;
+    }
+    template <int W>
+    __device__ __forceinline__ static float at(const uint8_t* t, int row, int col) {
+        return lds<float>(t + (row * (W + 4) + col) * 4);
+    }
+    __device__ __forceinline__ static u4 load_run(const S* p, int n, int N) {
+        u4 v{0, 0, 0, 0};
+        if (n < N) v = *reinterpret_cast<const u4any4*>(p + n);
+        return v;
+    }
+    __device__ __forceinline__ static Frag<1> exact(u4 v) { return {__builtin_bit_cast(f4, v)}; }
+};
+
+// T or M in the workspace: parts of Q x Q elements, row after row
+template <class MM>
+constexpr int image_bytes(int parts) { return parts * MM::Q * MM::Q * static_cast<int>(sizeof(typename MM::S)); }
+template <class MM>
+constexpr int m_parts(bool bwd) { return MM::TP == 1 ? 1 : bwd ? 3 : 2; }
+
+// one part of an operand kept as PARTS tiles behind each other
+template <class MM, int PARTS, class F>
+__device__ __forceinline__ typename MM::template Frag<PARTS> of_parts(F load) {
+    typename MM::template Frag<PARTS> f;
+    if constexpr (MM::TP == 1) {
+        f.v = load(0).v;
+    } else {
+#pragma unroll
+        for (int i = 0; i < PARTS; ++i) f.p[i] = load(i).p[0];
+    }
+    return f;
+}
+
+// Q rows of W columns from global memory (rows `row` elements apart, `valid` of them, N columns;
+// zeros elsewhere) into a tile
+template <class MM, int W, int THREADS>
+__device__ __forceinline__ void stage_rows(uint8_t* tile, const typename MM::S* src, int64_t row, int valid, int N) {
+    constexpr int E = 16 / sizeof(typename MM::S), PIECES = W / E;
+#pragma unroll
+    for (int i = threadIdx.x; i < MM::Q * PIECES; i += THREADS) {
+        const int r = i / PIECES, q = i % PIECES;
+        u4 v{0, 0, 0, 0};
+        if (r < valid) v = MM::load_run(src + r * row, q * E, N);
+        *reinterpret_cast<u4*>(tile + MM::template piece_at<W>(r, q)) = v;
+    }
+}
+// an image's parts into tiles behind each other
+template <class MM, int THREADS>
+__device__ __forceinline__ void stage_image(uint8_t* tiles, const uint8_t* src, int parts) {
+    constexpr int PIECES = MM::Q * sizeof(typename MM::S) / 16;
+    for (int i = threadIdx.x; i < parts * MM::Q * PIECES; i += THREADS) {
+        const int part = i / (MM::Q * PIECES), r = i / PIECES % MM::Q, q = i % PIECES;
+        *reinterpret_cast<u4*>(tiles + part * MM::template tile_bytes<MM::Q>(MM::Q) + MM::template piece_at<MM::Q>(r, q)) =
+            reinterpret_cast<const u4*>(src)[i];
+    }
+}
+
+// Blocks are dealt round-robin over the 8 XCDs: neighbours in the result run on one XCD and share
+// its L2.
+__device__ __forceinline__ int xcd_order(int block, int blocks) {
+    const int x = block & 7, per = blocks >> 3, more = blocks & 7;
+    return x * per + (x < more ? x : more) + (block >> 3);
+}
+
+// Of the chunk's token `lane`: the sum of its gates from the chunk's start on, the packed sequences
+// begun since then, and beta (tokens behind the row: gate 0, beta 0).  All 64 lanes call it.
+struct TokenSums {
+    double gates;
+    int starts;
+    float beta;
+};
+template <int Q>
+__device__ __forceinline__ TokenSums token_sums(const DeltaArgs& a, int64_t b, int64_t h, int64_t t0, int valid, int lane) {
+    TokenSums s{0.0, 0, 0.0f};
+    if (lane < valid) {
+        const int64_t t = b * a.L + t0 + lane;
+        if (a.gate) s.gates = gate_of(a.gate[t * a.H + h]);
+        s.beta = a.beta[t * a.H + h];
+        if (a.seq && t0 + lane > 0) s.starts = a.seq[t] != a.seq[t - 1];
+    }
+#pragma unroll
+    for (int d = 1; d < Q; d <<= 1) {
+        const double o = __shfl_up(s.gates, d);
+        const int r = __shfl_up(s.starts, d);
+        if (lane >= d) {
+            s.gates += o;
+            s.starts += r;
+        }
+    }
+    return s;
+}
+
+// the chunks' part of the workspace; returns its bytes
+template <class MM>
+size_t place_chunks(DeltaArgs& a, uint8_t* ws, bool bwd) {
+    a.chunks = (a.L + MM::Q - 1) / MM::Q;
+    const size_t n = static_cast<size_t>(a.B * a.H * a.chunks);
+    size_t at = 0;
+    a.T = ws;
+    at += n * image_bytes<MM>(MM::TP);
+    a.M = ws + at;
+    at += n * image_bytes<MM>(m_parts<MM>(bwd));
+    a.factors = reinterpret_cast<float*>(ws + at);
+    return at + n * 3 * MM::Q * 4;
+}
+
+}  // namespace delta
+
+// T, M and the factors of every chunk
+hipError_t launch_delta_prep(const DeltaArgs& a, ssm_dtype_t dtype, bool bwd, hipStream_t stream);
+// what the backward keeps of a walk: the state before every chunk, and E
+struct DeltaSaved {
+    float* states;  // [B, H, chunks, P, N]
+    float* e;       // [B, L, H, P]
+};
+hipError_t launch_delta_walk_saved(const DeltaArgs& a, const DeltaSaved& s, ssm_dtype_t dtype, hipStream_t stream);
+size_t delta_fwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N, ssm_dtype_t dtype);
+size_t delta_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N, ssm_dtype_t dtype);
+hipError_t launch_delta_fwd(DeltaArgs a, void* workspace, ssm_dtype_t dtype, hipStream_t stream);
+hipError_t launch_delta_bwd(DeltaArgs a, void* workspace, ssm_dtype_t dtype, hipStream_t stream);
+// token by token on state slots (row b's state at state_in / state_out + slot * P * N * H)
+struct DeltaStep {
+    DeltaArgs a;
+    const float* state_in;   // NULL: zeros
+    float* state_out;        // NULL: not written
+    const int32_t* slots;    // [B] or NULL (slot b)
+    int64_t n_slots;
+};
+hipError_t launch_delta_step(const DeltaStep& s, ssm_dtype_t dtype, hipStream_t stream);
+
+}  // namespace ssm

@@ -1,0 +1,637 @@
+// delta_bwd.hip -- the gated delta rule's backward.  With the chunk's quantities of delta.h, dh the
+// gradient of the state after the chunk and dY' = scale dY:
+//     dU = M^T dY + e^{G_Q - G} K dh^T,   dZ = T^T (b dU),   dV = dZ
+//     dh_0 = e^{G_Q} dh + (e^G dY')^T Q - (e^G dZ)^T K
+//     X_ts = r_ts scale (dY_t . U_s) (s <= t),   F_ts = -r_ts b_s (dZ_t . E_s) (s < t)
+//     dQ = e^G dY' h_0 + X K
+//     dK = e^{G_Q - G} U dh - e^G dZ h_0 + X^T Q + F^T K + F K
+//     db_s = dU_s . E_s - sum_t r_ts (k_t . k_s) (dZ_t . E_s)
+//     dgate_t: every product whose factor e^(..) spans token t, times itself: pairs s < t <= t',
+//              h_0 to t' >= t, s < t to the chunk's end, h_0 to the end
+//
+//   delta_walk   (delta.hip) along the rows again: the state before every chunk, and E
+//   delta_back   from the last chunk to the first: dh before every chunk, dZ, and of the channels'
+//                sums dU . E and e^{G_Q - G} (K dh^T) . U; laid out as the walk
+//   delta_grad   one block a chunk and key head (and range of its heads): the rest
+#include "delta.h"
+
+namespace ssm {
+namespace {
+
+using namespace delta;
+
+struct Buffers {
+    DeltaSaved saved;
+    float* grads;  // [B, H, chunks, P, N]: the gradient of the state after each chunk
+    float* dz;     // [B, L, H, P]
+    float* part;   // [B, H, chunks, 16-channel tiles, 2, Q]
+    float* dqk;    // [2, splits, B, L, G, N] where the heads of a key head are split
+    int64_t splits, heads;  // ranges of a key head's heads, and heads in each
+};
+
+__device__ __forceinline__ float sum16(float v) {  // over the 16 lanes that share g4
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xf, 0xf, true));
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xf, 0xf, true));
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xf, 0xf, true));
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 0xf, 0xf, true));
+    return v;
+}
+__device__ __forceinline__ float sum_groups(float v) {  // over the four lanes that share li
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+__device__ __forceinline__ f4 row4(const float* p) { return lds<f4>(reinterpret_cast<const uint8_t*>(p)); }
+
+template <class MM, int NT>
+__global__ __launch_bounds__(256) void delta_back_kernel(DeltaArgs a, Buffers u) {
+    using S = typename MM::S;
+    constexpr int Q = MM::Q, RT = Q / 16, KT = Q / MM::KB, W = 16 * NT, KN = W / MM::KB;
+    constexpr int MP = m_parts<MM>(true);
+    constexpr int QQ = MM::template tile_bytes<Q>(Q), QN = MM::template tile_bytes<W>(Q);
+    __shared__ __attribute__((aligned(16))) uint8_t sk[QN];
+    __shared__ __attribute__((aligned(16))) uint8_t sq[QN];
+    __shared__ __attribute__((aligned(16))) uint8_t st[MM::TP * QQ];
+    __shared__ __attribute__((aligned(16))) uint8_t sm[MP * QQ];
+    __shared__ __attribute__((aligned(16))) float sf[3 * Q];
+    const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g4 = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t pblocks = (a.P + 63) / 64, ptiles = (a.P + 15) / 16;
+    const int64_t unit = xcd_order(blockIdx.x, gridDim.x);
+    const int64_t pb = unit % pblocks, bh = unit / pblocks, h = bh % a.H, b = bh / a.H;
+    const int64_t g = h / (a.H / a.G);
+    const int64_t p0 = 64 * pb + 16 * w, p = p0 + li;
+    const bool mine = p0 < a.P, have = p < a.P;
+    const int N = static_cast<int>(a.N);
+    const int64_t state = (bh * a.P + p) * a.N;
+    f4 dh[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const int n = 16 * i + 4 * g4;
+        dh[i] = have && n < N && a.dhT ? *reinterpret_cast<const f4*>(a.dhT + state + n) : f4{0, 0, 0, 0};
+    }
+    for (int64_t c = a.chunks - 1; c >= 0; --c) {
+        const int64_t t0 = b * a.L + c * Q, image = bh * a.chunks + c;
+        const int valid = static_cast<int>(a.L - c * Q < Q ? a.L - c * Q : Q);
+        if (have) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                const int n = 16 * i + 4 * g4;
+                if (n < N) *reinterpret_cast<f4*>(u.grads + (image * a.P + p) * a.N + n) = dh[i];
+            }
+        }
+        __syncthreads();
+        stage_rows<MM, W, 256>(sk, static_cast<const S*>(a.k) + t0 * a.k_row + g * a.N, a.k_row, valid, N);
+        stage_rows<MM, W, 256>(sq, static_cast<const S*>(a.q) + t0 * a.q_row + g * a.N, a.q_row, valid, N);
+        stage_image<MM, 256>(st, a.T + image * image_bytes<MM>(MM::TP), MM::TP);
+        stage_image<MM, 256>(sm, a.M + image * image_bytes<MM>(MP), MP);
+        if (tid < 3 * Q) sf[tid] = a.factors[image * 3 * Q + tid];
+        __syncthreads();
+        if (!mine) continue;
+        f4 dy[RT], ev[RT], du[RT], dz[RT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            dy[i] = ev[i] = du[i] = dz[i] = f4{0, 0, 0, 0};
+            if (have) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = 16 * i + 4 * g4 + e;
+                    if (t < valid) {
+                        dy[i][e] = MM::value(static_cast<const S*>(a.dy) + (t0 + t) * a.dy_row + h * a.P, p);
+                        ev[i][e] = u.saved.e[((t0 + t) * a.H + h) * a.P + p];
+                    }
+                }
+            }
+        }
+        // e^{G_Q - G} K dh^T, and its products with U
+#pragma unroll
+        for (int kk = 0; kk < KN; ++kk) {
+            const auto s = MM::template of_tiles<3>(dh, kk);
+#pragma unroll
+            for (int i = 0; i < RT; ++i) MM::template mac<1, 3>(du[i], MM::template rows<W>(sk, 16 * i, kk, li, g4), s);
+        }
+        float* part = u.part + (image * ptiles + p0 / 16) * 2 * Q;
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            const f4 f = row4(sf + Q + 16 * i + 4 * g4), be = row4(sf + 2 * Q + 16 * i + 4 * g4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                du[i][e] = f[e] != 0.0f ? f[e] * du[i][e] : 0.0f;
+                const float v = sum16(du[i][e] * ev[i][e] * be[e]);
+                if (li == 0) part[Q + 16 * i + 4 * g4 + e] = v;
+            }
+        }
+        // dU += M^T dY
+#pragma unroll
+        for (int kk = 0; kk < KT; ++kk) {
+            const auto s = MM::template of_tiles<1>(dy, kk);
+#pragma unroll
+            for (int i = 0; i < (kk + 1) * MM::KB / 16; ++i) {
+                const auto l = of_parts<MM, MP>([&](int q) { return MM::template columns<Q>(sm + q * QQ, kk * MM::KB, i, li, g4); });
+                MM::template mac<MP, 1>(du[i], l, s);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            const f4 be = row4(sf + 2 * Q + 16 * i + 4 * g4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float v = sum16(du[i][e] * ev[i][e]);
+                if (li == 0) part[16 * i + 4 * g4 + e] = v;
+                du[i][e] *= be[e];
+            }
+        }
+        // dZ = T^T (b dU)
+#pragma unroll
+        for (int kk = 0; kk < KT; ++kk) {
+            const auto s = MM::template of_tiles<3>(du, kk);
+#pragma unroll
+            for (int i = 0; i < (kk + 1) * MM::KB / 16; ++i) {
+                const auto l = of_parts<MM, MM::TP>([&](int q) { return MM::template columns<Q>(st + q * QQ, kk * MM::KB, i, li, g4); });
+                MM::template mac<MM::TP, 3>(dz[i], l, s);
+            }
+        }
+        if (have) {
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = 16 * i + 4 * g4 + e;
+                    if (t < valid) {
+                        u.dz[((t0 + t) * a.H + h) * a.P + p] = dz[i][e];
+                        MM::store(static_cast<S*>(a.dv) + (t0 + t) * a.dv_row + h * a.P, p, dz[i][e]);
+                    }
+                }
+        }
+        // the gradient of the state before the chunk
+        const float through = sf[Q - 1];
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dh[i][e] = through != 0.0f ? through * dh[i][e] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            const f4 f = row4(sf + 16 * i + 4 * g4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                dy[i][e] = f[e] != 0.0f ? f[e] * a.scale * dy[i][e] : 0.0f;
+                dz[i][e] = f[e] != 0.0f ? -f[e] * dz[i][e] : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int kk = 0; kk < KT; ++kk) {
+            const auto sy = MM::template of_tiles<3>(dy, kk);
+            const auto sz = MM::template of_tiles<3>(dz, kk);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                MM::template mac<1, 3>(dh[i], MM::template columns<W>(sq, kk * MM::KB, i, li, g4), sy);
+                MM::template mac<1, 3>(dh[i], MM::template columns<W>(sk, kk * MM::KB, i, li, g4), sz);
+            }
+        }
+    }
+    if (a.dh0 && have) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const int n = 16 * i + 4 * g4;
+            if (n < N) *reinterpret_cast<f4*>(a.dh0 + state + n) = dh[i];
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------
+// delta_grad: eight wavefronts a block; a wavefront owns columns of dQ and dK (state dimensions) and
+// reads of h_0 and dh each element once, and takes tiles of the pairs in turn.  dY, dZ and E pass
+// through LDS in blocks of 64 channels; dQ and dK are summed over the heads of a key head in
+// accumulators.
+// ---------------------------------------------------------------------------------------
+template <class MM>
+__device__ __forceinline__ void load_values(const typename MM::S* p, int n, float (&v)[MM::R]) {
+    if (n >= MM::R) {
+        if constexpr (MM::R == 8) {
+            const u4 x = *reinterpret_cast<const u4any*>(p);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(j & 1 ? x[j >> 1] & 0xFFFF0000u : x[j >> 1] << 16);
+        } else {
+            const f4 x = __builtin_bit_cast(f4, *reinterpret_cast<const u4any4*>(p));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = x[j];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < MM::R; ++j) v[j] = j < n ? MM::value(p, j) : 0.0f;
+    }
+}
+template <int R>
+__device__ __forceinline__ void load_floats(const float* p, int n, float (&v)[R]) {
+    if (n >= R) {
+#pragma unroll
+        for (int i = 0; i < R / 4; ++i) {
+            const f4 x = __builtin_bit_cast(f4, *reinterpret_cast<const u4any4*>(p + 4 * i));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[4 * i + j] = x[j];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < R; ++j) v[j] = j < n ? p[j] : 0.0f;
+    }
+}
+// R values into PARTS tiles
+template <class MM, int W, int PARTS>
+__device__ __forceinline__ void put_parts(uint8_t* tiles, int bytes, int row, int q, const float (&v)[MM::R]) {
+    if constexpr (MM::TP == 1) {
+        *reinterpret_cast<f4*>(tiles + MM::template piece_at<W>(row, q)) = f4{v[0], v[1], v[2], v[3]};
+    } else {
+        const auto f = MM::template parts<PARTS>(v);
+#pragma unroll
+        for (int i = 0; i < PARTS; ++i) *reinterpret_cast<bf8*>(tiles + i * bytes + MM::template piece_at<W>(row, q)) = f.p[i];
+    }
+}
+// one value of a pair into PARTS tiles
+template <class MM, int PARTS>
+__device__ __forceinline__ void put_pair(uint8_t* tiles, int bytes, int row, int col, float v) {
+    if constexpr (MM::TP == 1) {
+        *reinterpret_cast<float*>(tiles + (row * (MM::Q + 4) + col) * 4) = v;
+    } else {
+        const int at = piece<2 * MM::Q>(row, col >> 3) + 2 * (col & 7);
+#pragma unroll
+        for (int i = 0; i < PARTS; ++i) {
+            const uint16_t h = f32_to_bf16(v);
+            *reinterpret_cast<uint16_t*>(tiles + i * bytes + at) = h;
+            v -= bf16_to_f32(h);
+        }
+    }
+}
+
+template <class MM, int NT>
+__global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a, Buffers u) {
+    using S = typename MM::S;
+    constexpr int Q = MM::Q, RT = Q / 16, KT = Q / MM::KB, W = 16 * NT, KN = W / MM::KB, KP = 64 / MM::KB, R = MM::R;
+    constexpr int CG = NT < 8 ? NT : 8, RG = 8 / CG;    // column and row groups of wavefronts
+    constexpr int CT = NT / CG, RW = RT / RG;           // a wavefront's column and row tiles
+    constexpr int TILES = RT * (RT + 1) / 2, MINE = (TILES + 7) / 8;
+    constexpr int TP = MM::TP, XP = TP == 1 ? 1 : 2;
+    constexpr int QN = MM::template tile_bytes<W>(Q), QP = MM::template tile_bytes<64>(Q), QQ = MM::template tile_bytes<Q>(Q);
+    constexpr int LOADS = (1 + 2 * TP) * QP, PAIRS = (2 * XP + TP) * QQ;
+    __shared__ __attribute__((aligned(16))) uint8_t sk[QN];
+    __shared__ __attribute__((aligned(16))) uint8_t sq[QN];
+    __shared__ __attribute__((aligned(16))) uint8_t pool[LOADS > PAIRS ? LOADS : PAIRS];
+    __shared__ __attribute__((aligned(16))) float sf[3 * Q];
+    __shared__ double sg[Q];
+    __shared__ int sr[Q];
+    __shared__ float sdb[RT][Q];    // sums over t of pairs, by row tiles
+    __shared__ float sc[CG][Q];     // products with h_0, by column groups
+    __shared__ float sspan[Q];
+    __shared__ float sdot[8];
+    uint8_t* const ty = pool;                   // dY
+    uint8_t* const tz = pool + QP;              // dZ
+    uint8_t* const te = pool + (1 + TP) * QP;   // E
+    uint8_t* const tx = pool;                   // X
+    uint8_t* const tf = pool + XP * QQ;         // F
+    uint8_t* const tw = pool + 2 * XP * QQ;     // the pairs' products themselves
+    const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g4 = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6), cg = w % CG, rg = w / CG;
+    int64_t unit = xcd_order(blockIdx.x, gridDim.x);
+    const int64_t split = unit % u.splits;
+    unit /= u.splits;
+    const int64_t g = unit % a.G;
+    unit /= a.G;
+    const int64_t c = unit % a.chunks, b = unit / a.chunks;
+    const int64_t rep = a.H / a.G, ptiles = (a.P + 15) / 16;
+    const int64_t h1 = g * rep + (rep < (split + 1) * u.heads ? rep : (split + 1) * u.heads);
+    const int valid = static_cast<int>(a.L - c * Q < Q ? a.L - c * Q : Q);
+    const int N = static_cast<int>(a.N), P = static_cast<int>(a.P);
+    const int64_t t0 = b * a.L + c * Q;
+
+    stage_rows<MM, W, 512>(sk, static_cast<const S*>(a.k) + t0 * a.k_row + g * a.N, a.k_row, valid, N);
+    stage_rows<MM, W, 512>(sq, static_cast<const S*>(a.q) + t0 * a.q_row + g * a.N, a.q_row, valid, N);
+    f4 dq[RW][CT], dk[RW][CT];
+#pragma unroll
+    for (int i = 0; i < RW; ++i)
+#pragma unroll
+        for (int j = 0; j < CT; ++j) dq[i][j] = dk[i][j] = f4{0, 0, 0, 0};
+
+    for (int64_t h = g * rep + split * u.heads; h < h1; ++h) {
+        const int64_t image = (b * a.H + h) * a.chunks + c;
+        const float* states = u.saved.states + image * a.P * a.N;
+        const float* grads = u.grads + image * a.P * a.N;
+        f4 qo[RW][CT], ko[RW][CT], ke[RW][CT], dm[MINE], db[MINE];
+#pragma unroll
+        for (int i = 0; i < RW; ++i)
+#pragma unroll
+            for (int j = 0; j < CT; ++j) qo[i][j] = ko[i][j] = ke[i][j] = f4{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < MINE; ++i) dm[i] = db[i] = f4{0, 0, 0, 0};
+        float dot = 0.0f;
+        for (int p0 = 0; p0 < P; p0 += 64) {
+            __syncthreads();
+            if (p0 == 0 && w == 0) {
+                const TokenSums s = token_sums<Q>(a, b, h, c * Q, valid, lane);
+                if (lane < Q) {
+                    sg[lane] = s.gates;
+                    sr[lane] = s.starts;
+                }
+            }
+            if (p0 == 0 && tid < 3 * Q) sf[tid] = a.factors[image * 3 * Q + tid];
+            for (int i = tid; i < Q * 64 / R; i += 512) {
+                const int r = i / (64 / R), q = i % (64 / R), left = r < valid ? P - p0 - R * q : 0;
+                float v[R];
+                load_values<MM>(static_cast<const S*>(a.dy) + (t0 + r) * a.dy_row + h * a.P + p0 + R * q, left, v);
+                put_parts<MM, 64, 1>(ty, QP, r, q, v);
+                const int64_t at = ((t0 + r) * a.H + h) * a.P + p0 + R * q;
+                load_floats<R>(u.dz + at, left, v);
+                put_parts<MM, 64, TP>(tz, QP, r, q, v);
+                load_floats<R>(u.saved.e + at, left, v);
+                put_parts<MM, 64, TP>(te, QP, r, q, v);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int kk = 0; kk < KP; ++kk) {
+#pragma unroll
+                for (int j = 0; j < CT; ++j) {
+                    const int n = 16 * (cg * CT + j) + li;
+                    float s[R], d[R];
+#pragma unroll
+                    for (int m = 0; m < R; ++m) {
+                        const int p = p0 + MM::KB * kk + R * g4 + m;
+                        s[m] = d[m] = 0.0f;
+                        if (p < P && n < N) {
+                            s[m] = states[static_cast<int64_t>(p) * N + n];
+                            d[m] = grads[static_cast<int64_t>(p) * N + n];
+                        }
+                        if (rg == 0) dot += s[m] * d[m];
+                    }
+                    const auto fs = MM::template parts<3>(s);
+                    const auto fd = MM::template parts<2>(d);
+#pragma unroll
+                    for (int i = 0; i < RW; ++i) {
+                        const int r0 = 16 * (rg * RW + i);
+                        MM::template mac<1, 3>(qo[i][j], MM::template along<64>(ty, r0, kk, li, g4), fs);
+                        const auto z = of_parts<MM, TP>([&](int q) { return MM::template along<64>(tz + q * QP, r0, kk, li, g4); });
+                        MM::template mac<TP, 3>(ko[i][j], z, fs);
+                        const auto e = of_parts<MM, XP>([&](int q) { return MM::template along<64>(te + q * QP, r0, kk, li, g4); });
+                        MM::template mac<XP, 2>(ke[i][j], e, fd);
+                    }
+                }
+#pragma unroll
+                for (int m = 0; m < MINE; ++m) {
+                    int tile = w + 8 * m, rt = 0;
+                    if (tile >= TILES) continue;
+                    while (tile > rt) tile -= ++rt;
+                    const auto e = of_parts<MM, TP>([&](int q) { return MM::template along<64>(te + q * QP, 16 * tile, kk, li, g4); });
+                    MM::template mac<1, TP>(dm[m], MM::template along<64>(ty, 16 * rt, kk, li, g4), e);
+                    const auto z = of_parts<MM, TP>([&](int q) { return MM::template along<64>(tz + q * QP, 16 * rt, kk, li, g4); });
+                    MM::template mac<TP, TP>(db[m], z, e);
+                }
+            }
+        }
+        __syncthreads();  // the loads' tiles become the pairs'
+#pragma unroll
+        for (int m = 0; m < MINE; ++m) {
+            int tile = w + 8 * m, rt = 0;
+            if (tile >= TILES) continue;
+            while (tile > rt) tile -= ++rt;
+            f4 kk{0, 0, 0, 0}, qk{0, 0, 0, 0};
+#pragma unroll
+            for (int x = 0; x < KN; ++x) {
+                const auto s = MM::template along<W>(sk, 16 * tile, x, li, g4);
+                MM::template mac<1, 1>(kk, MM::template along<W>(sk, 16 * rt, x, li, g4), s);
+                MM::template mac<1, 1>(qk, MM::template along<W>(sq, 16 * rt, x, li, g4), s);
+            }
+            const int s = 16 * tile + li;
+            const float be = sf[2 * Q + s];
+            float sum = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = 16 * rt + 4 * g4 + e;
+                const float r = s <= t && sr[s] == sr[t] ? exp_of(sg[t] - sg[s]) : 0.0f;
+                const bool on = r != 0.0f, below = on && s < t;
+                const float x = on ? r * a.scale * be * dm[m][e] : 0.0f;
+                const float f = below ? -r * db[m][e] : 0.0f;
+                const float pair = below ? x * qk[e] + f * be * kk[e] : 0.0f;
+                sum += below ? f * kk[e] : 0.0f;
+                put_pair<MM, XP>(tx, QQ, t, s, x);
+                put_pair<MM, XP>(tf, QQ, t, s, f * be);
+                put_pair<MM, TP>(tw, QQ, t, s, pair);
+                if (MM::KB == 32 && (rt & 1) && tile == rt - 1) {  // above the diagonal, in its contraction block
+                    put_pair<MM, XP>(tx, QQ, t - 16, s + 16, 0.0f);
+                    put_pair<MM, XP>(tf, QQ, t - 16, s + 16, 0.0f);
+                    put_pair<MM, TP>(tw, QQ, t - 16, s + 16, 0.0f);
+                }
+            }
+            sum = sum_groups(sum);
+            if (g4 == 0) sdb[rt][s] = sum;
+        }
+        // products with h_0, for dgate
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+            const int r0 = 16 * (rg * RW + i) + 4 * g4;
+            const f4 f = row4(sf + r0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int j = 0; j < CT; ++j) {
+                    const int n = 16 * (cg * CT + j) + li;
+                    qo[i][j][e] = f[e] != 0.0f ? f[e] * a.scale * qo[i][j][e] : 0.0f;
+                    ko[i][j][e] = f[e] != 0.0f ? -f[e] * ko[i][j][e] : 0.0f;
+                    sum += qo[i][j][e] * MM::template at<W>(sq, r0 + e, n) + ko[i][j][e] * MM::template at<W>(sk, r0 + e, n);
+                }
+                sum = sum16(sum);
+                if (li == 0) sc[cg][r0 + e] = sum;
+            }
+        }
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) dot += __shfl_xor(dot, d);
+        if (lane == 0) sdot[w] = dot;
+        __syncthreads();
+        if (w < RT) {  // pairs that span token t = 16 w + li
+            float span = 0.0f;
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                if (rt < w) continue;
+                f4 v{0, 0, 0, 0};
+#pragma unroll
+                for (int kk = 0; kk < KT; ++kk) {
+                    if (kk * MM::KB > 16 * w) continue;
+                    float one[R];
+#pragma unroll
+                    for (int j = 0; j < R; ++j)
+                        one[j] = MM::KB * kk + (j >> 2) * 16 + 4 * g4 + (j & 3) < 16 * w + li ? 1.0f : 0.0f;
+                    const auto l = of_parts<MM, TP>([&](int q) { return MM::template rows<Q>(tw + q * QQ, 16 * rt, kk, li, g4); });
+                    MM::template mac<TP, 1>(v, l, MM::template parts<1>(one));
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) span += 16 * rt + 4 * g4 + e >= 16 * w + li ? v[e] : 0.0f;
+            }
+            span = sum_groups(span);
+            if (g4 == 0) sspan[16 * w + li] = span;
+        }
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+            const int rt = rg * RW + i;
+            const f4 f = row4(sf + Q + 16 * rt + 4 * g4) * row4(sf + 2 * Q + 16 * rt + 4 * g4);
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+                const int ct = cg * CT + j;
+                dq[i][j] += qo[i][j];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dk[i][j][e] += ko[i][j][e] + (f[e] != 0.0f ? f[e] * ke[i][j][e] : 0.0f);
+#pragma unroll
+                for (int kk = 0; kk < KT; ++kk) {
+                    const auto fk = MM::template columns<W>(sk, kk * MM::KB, ct, li, g4);
+                    const auto fq = MM::template columns<W>(sq, kk * MM::KB, ct, li, g4);
+                    if (kk * MM::KB <= 16 * rt) {
+                        const auto x = of_parts<MM, XP>([&](int q) { return MM::template rows<Q>(tx + q * QQ, 16 * rt, kk, li, g4); });
+                        MM::template mac<XP, 1>(dq[i][j], x, fk);
+                        const auto y = of_parts<MM, XP>([&](int q) { return MM::template rows<Q>(tf + q * QQ, 16 * rt, kk, li, g4); });
+                        MM::template mac<XP, 1>(dk[i][j], y, fk);
+                    }
+                    if ((kk + 1) * MM::KB > 16 * rt) {
+                        const auto x = of_parts<MM, XP>([&](int q) { return MM::template columns<Q>(tx + q * QQ, kk * MM::KB, rt, li, g4); });
+                        MM::template mac<XP, 1>(dk[i][j], x, fq);
+                        const auto y = of_parts<MM, XP>([&](int q) { return MM::template columns<Q>(tf + q * QQ, kk * MM::KB, rt, li, g4); });
+                        MM::template mac<XP, 1>(dk[i][j], y, fk);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        if (w == 0) {
+            double from = 0.0, end = 0.0;
+            float be = 0.0f;
+            if (lane < Q) {
+#pragma unroll
+                for (int i = 0; i < CG; ++i) from += sc[i][lane];
+                const float* part = u.part + image * ptiles * 2 * Q;
+                for (int i = 0; i < ptiles; ++i) {
+                    be += part[i * 2 * Q + lane];
+                    end += part[i * 2 * Q + Q + lane];
+                }
+                for (int rt = lane / 16; rt < RT; ++rt) be += sdb[rt][lane];
+            }
+            const double own = end;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const double o = __shfl_down(from, d), e = __shfl_up(end, d);
+                if (lane + d < 64) from += o;
+                if (lane >= d) end += e;
+            }
+            float all = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) all += sdot[i];
+            if (lane < valid) {
+                const int64_t at = (t0 + lane) * a.H + h;
+                const float through = sf[Q - 1];
+                a.dbeta[at] = be;
+                if (a.dgate)
+                    a.dgate[at] = static_cast<float>(from + (end - own) + sspan[lane] + (through != 0.0f ? through * all : 0.0f));
+            }
+        }
+    }
+    const int64_t part = a.B * a.L * a.G * a.N;
+#pragma unroll
+    for (int i = 0; i < RW; ++i)
+#pragma unroll
+        for (int j = 0; j < CT; ++j) {
+            const int n = 16 * (cg * CT + j) + li;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = 16 * (rg * RW + i) + 4 * g4 + e;
+                if (t >= valid || n >= N) continue;
+                if (u.splits == 1) {
+                    MM::store(static_cast<S*>(a.dq) + (t0 + t) * a.dq_row + g * a.N, n, dq[i][j][e]);
+                    MM::store(static_cast<S*>(a.dk) + (t0 + t) * a.dk_row + g * a.N, n, dk[i][j][e]);
+                } else {
+                    float* to = u.dqk + split * part + ((t0 + t) * a.G + g) * a.N + n;
+                    to[0] = dq[i][j][e];
+                    to[u.splits * part] = dk[i][j][e];
+                }
+            }
+        }
+}
+
+// dQ and dK of key heads whose heads were split
+template <class MM>
+__global__ __launch_bounds__(256) void delta_join_kernel(DeltaArgs a, Buffers u) {
+    using S = typename MM::S;
+    const int64_t width = a.G * a.N, n = a.B * a.L * width;
+    for (int64_t i = blockIdx.x * int64_t{256} + threadIdx.x; i < 2 * n; i += gridDim.x * int64_t{256}) {
+        const bool k = i >= n;
+        const int64_t at = k ? i - n : i, row = at / width, col = at % width;
+        const float* from = u.dqk + (k ? u.splits * n : 0) + at;
+        float sum = 0.0f;
+        for (int64_t s = 0; s < u.splits; ++s) sum += from[s * n];
+        if (k) MM::store(static_cast<S*>(a.dk) + row * a.dk_row, col, sum);
+        else MM::store(static_cast<S*>(a.dq) + row * a.dq_row, col, sum);
+    }
+}
+
+// blocks that fill the GPU twice, where there are as many heads
+void split_heads(const DeltaArgs& a, Buffers& u) {
+    const int64_t rep = a.H / a.G, blocks = a.B * a.chunks * a.G;
+    int64_t splits = (512 + blocks - 1) / blocks;
+    if (splits > rep) splits = rep;
+    u.heads = (rep + splits - 1) / splits;
+    u.splits = (rep + u.heads - 1) / u.heads;
+}
+
+template <class MM>
+size_t place(DeltaArgs& a, Buffers& u, uint8_t* ws) {
+    size_t at = place_chunks<MM>(a, ws, true);
+    const auto take = [&](int64_t floats) {
+        float* p = reinterpret_cast<float*>(ws + at);
+        at += static_cast<size_t>((floats + 63) / 64 * 64) * 4;
+        return p;
+    };
+    split_heads(a, u);
+    const int64_t units = a.B * a.H * a.chunks, rows = a.B * a.L * a.H * a.P;
+    u.saved.states = take(units * a.P * a.N);
+    u.grads = take(units * a.P * a.N);
+    u.saved.e = take(rows);
+    u.dz = take(rows);
+    u.part = take(units * ((a.P + 15) / 16) * 2 * MM::Q);
+    u.dqk = take(u.splits > 1 ? 2 * u.splits * a.B * a.L * a.G * a.N : 0);
+    return at;
+}
+
+template <class MM, int NT>
+hipError_t kernels_of(const DeltaArgs& a, const Buffers& u, hipStream_t stream) {
+    delta_back_kernel<MM, NT><<<static_cast<unsigned>(a.B * a.H * ((a.P + 63) / 64)), 256, 0, stream>>>(a, u);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    delta_grad_kernel<MM, NT><<<static_cast<unsigned>(a.B * a.chunks * a.G * u.splits), 512, 0, stream>>>(a, u);
+    e = hipGetLastError();
+    if (e != hipSuccess || u.splits == 1) return e;
+    delta_join_kernel<MM><<<1024, 256, 0, stream>>>(a, u);
+    return hipGetLastError();
+}
+template <class MM>
+hipError_t bwd_of(DeltaArgs a, void* workspace, ssm_dtype_t dtype, hipStream_t stream) {
+    Buffers u{};
+    place<MM>(a, u, static_cast<uint8_t*>(workspace));
+    hipError_t e = launch_delta_prep(a, dtype, true, stream);
+    if (e == hipSuccess) e = launch_delta_walk_saved(a, u.saved, dtype, stream);
+    if (e != hipSuccess) return e;
+    if (a.N <= 64) return kernels_of<MM, 4>(a, u, stream);
+    if (a.N <= 128) return kernels_of<MM, 8>(a, u, stream);
+    return kernels_of<MM, 16>(a, u, stream);
+}
+
+}  // namespace
+
+size_t delta_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N, ssm_dtype_t dtype) {
+    DeltaArgs a{};
+    a.B = B;
+    a.L = L;
+    a.H = H;
+    a.P = P;
+    a.G = G;
+    a.N = N;
+    Buffers u{};
+    return dtype == SSM_BF16 ? place<ByBf16>(a, u, nullptr) : place<ByF32>(a, u, nullptr);
+}
+
+hipError_t launch_delta_bwd(DeltaArgs a, void* workspace, ssm_dtype_t dtype, hipStream_t stream) {
+    return dtype == SSM_BF16 ? bwd_of<ByBf16>(a, workspace, dtype, stream) : bwd_of<ByF32>(a, workspace, dtype, stream);
+}
+
+}  // namespace ssm
