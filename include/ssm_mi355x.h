@@ -532,7 +532,10 @@ ssm_status_t ssm_gated_scan_step(const void* x, int64_t x_row, const void* gate,
  *   workspace      ..._workspace_size bytes, 256-byte aligned
  * dstate a multiple of 4, at most 256; any headdim.  States and sums in fp32 (sums of gates in 64
  * bits), products exact to fp32 for SSM_F32 and for everything that a fp32 output depends on; outputs
- * rounded once.  Deterministic.
+ * rounded once.  Deterministic.  A NaN or infinity reaches the tokens of its own chunk (64 tokens for
+ * SSM_BF16, 32 for SSM_F32, from the row's start), forward its sequence's after them, and backward all
+ * chunks that its sequence has tokens in, other sequences' tokens in those among them; no token of
+ * other chunks, and no state that its sequence does not reach.
  *
  * ssm_delta_scan_fwd   final_state may be initial_state; no other output may overlap an input.
  *     seqlen = 0: final = initial (or zeros).
@@ -570,6 +573,52 @@ ssm_status_t ssm_delta_scan_step(const void* q, int64_t q_row, const void* k, in
                                  int64_t batch, int64_t n_new, int64_t nheads, int64_t headdim,
                                  int64_t ngroups, int64_t dstate, int64_t n_slots, ssm_dtype_t dtype,
                                  ssm_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * ssm_qk_norm_fwd / ssm_qk_norm_bwd -- the norm of every head of a layer's queries and keys, with the
+ * rotation of the head's first rotary_dim channels by the token's position, in one pass over both:
+ * what ssm_delta_scan_* takes as q and k.  Per token and head of headdim channels:
+ *     r = 1 / sqrt(sum x^2 + eps) (SSM_QK_NORM_L2) or 1 / sqrt(mean x^2 + eps) (SSM_QK_NORM_RMS)
+ *     m = weight r x
+ *     out: the pairs (m_i, m_{i + rotary_dim / 2}), or (m_2i, m_{2i+1}) if interleaved, turned by
+ *     the angle positions * inv_freq[i]; channels from rotary_dim on are m
+ * A head of zeros with eps = 0 gives 0 (and the gradient 0).  Statistics, angles' sines and sums in
+ * fp32, angles themselves in 64 bits (any int32 position, negative ones too); outputs rounded once.
+ * The backward recomputes the statistics and gives, from dq_out and dk_out, dq, dk and the sums over
+ * tokens and heads dq_weight, dk_weight (fixed order: deterministic).
+ *
+ *   q, dq_out, q_out, dq   [batch, seqlen, nheads_q, headdim] dtype; token t of row b at
+ *                  p + (b * seqlen + t) * p_row elements, its heads side by side (input rows
+ *                  p_row >= 0, output rows at least the token's elements apart).  k the same with
+ *                  nheads_k
+ *   q_weight, k_weight     [headdim] fp32, or NULL (ones)
+ *   inv_freq       [rotary_dim / 2] fp32 (rotary_dim = 0: no rotation)
+ *   positions      [batch, seqlen] int32, or NULL (token t of every row is at t)
+ *   dq_weight, dk_weight   [headdim] fp32, or NULL (not written)
+ *   workspace      ssm_qk_norm_bwd_workspace_size bytes, 4-byte aligned (not needed when both weight
+ *                  gradients are NULL)
+ * headdim <= 256.  q_out may be q, k_out k, dq dq_out and dk dk_out, with the same row stride; no
+ * other overlap of outputs.  No tokens: the weights' gradients are 0.
+ * ------------------------------------------------------------------------------------- */
+enum { SSM_QK_NORM_L2 = 0, SSM_QK_NORM_RMS = 1 };
+typedef int32_t ssm_qk_norm_t;
+ssm_status_t ssm_qk_norm_fwd(const void* q, int64_t q_row, const void* k, int64_t k_row,
+                             const float* q_weight, const float* k_weight, const float* inv_freq,
+                             const int32_t* positions, void* q_out, int64_t q_out_row, void* k_out,
+                             int64_t k_out_row, int64_t batch, int64_t seqlen, int64_t nheads_q,
+                             int64_t nheads_k, int64_t headdim, int64_t rotary_dim,
+                             int32_t interleaved, float eps, ssm_qk_norm_t kind, ssm_dtype_t dtype,
+                             ssm_stream_t stream);
+size_t ssm_qk_norm_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t headdim);
+ssm_status_t ssm_qk_norm_bwd(const void* q, int64_t q_row, const void* k, int64_t k_row,
+                             const float* q_weight, const float* k_weight, const float* inv_freq,
+                             const int32_t* positions, const void* dq_out, int64_t dq_out_row,
+                             const void* dk_out, int64_t dk_out_row, void* dq, int64_t dq_row,
+                             void* dk, int64_t dk_row, float* dq_weight, float* dk_weight,
+                             void* workspace, size_t workspace_bytes, int64_t batch, int64_t seqlen,
+                             int64_t nheads_q, int64_t nheads_k, int64_t headdim, int64_t rotary_dim,
+                             int32_t interleaved, float eps, ssm_qk_norm_t kind, ssm_dtype_t dtype,
+                             ssm_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------
  * ssm_norm_fwd / ssm_norm_bwd -- RMS or layer norm of rows of channels with an optional SiLU

@@ -137,6 +137,12 @@ def _load():
                                              fp] + sizes + [vp, sz, vp]
     lib.ssm_delta_scan_step.argtypes = qkv + [fp, i32p, vp, i64, i64, i64, i64, i64, i64, i64, i64, ci,
                                               vp]
+    qk = [vp, i64, vp, i64, fp, fp, fp, i32p]
+    how = [i64, i64, i64, i64, i64, i64, ci, cf, ci, ci, vp]
+    lib.ssm_qk_norm_fwd.argtypes = qk + [vp, i64, vp, i64] + how
+    lib.ssm_qk_norm_bwd_workspace_size.restype = sz
+    lib.ssm_qk_norm_bwd_workspace_size.argtypes = [i64, i64, i64]
+    lib.ssm_qk_norm_bwd.argtypes = qk + [vp, i64, vp, i64, vp, i64, vp, i64, fp, fp, vp, sz] + how
     lib.ssm_stream_copy.argtypes = [vp, vp, i64, vp]
     lib.ssm_timing_enable.argtypes = [ci]
     lib.ssm_timing_read.argtypes = [ctypes.POINTER(ctypes.c_double),
@@ -146,7 +152,8 @@ def _load():
               "ssm_conv_scan_fwd_pooled", "ssm_state_stats_update", "ssm_scan_fwd_vector_decay",
               "ssm_initial_state_noise", "ssm_state_reset", "ssm_stream_copy", "ssm_norm_fwd",
               "ssm_norm_bwd", "ssm_scan_bwd", "ssm_gated_scan_fwd", "ssm_gated_scan_bwd", "ssm_gated_scan_step",
-              "ssm_delta_scan_fwd", "ssm_delta_scan_bwd", "ssm_delta_scan_step",
+              "ssm_delta_scan_fwd", "ssm_delta_scan_bwd", "ssm_delta_scan_step", "ssm_qk_norm_fwd",
+              "ssm_qk_norm_bwd",
               "ssm_timing_enable", "ssm_timing_read"):
         getattr(lib, f).restype = ci
     return lib
@@ -982,6 +989,106 @@ def delta_scan_step(q, k, v, beta, state, gate=None, scale=1.0, state_indices=No
             *lead, _ptr(state), _ptr(state_indices), _ptr(y), _token_row(y, "y"), *sizes,
             state.shape[0], _dtype_code(v), _stream()))
     return y
+
+
+QK_NORM = {"l2": 0, "rms": 1}
+
+
+def _qk_args(q, k, q_weight, k_weight, inv_freq, positions, kind):
+    """Checks shared by qk_norm_fwd and qk_norm_bwd; returns (the leading arguments of the C calls,
+    the sizes batch, seqlen, nheads_q, nheads_k, headdim, rotary_dim)."""
+    if kind not in QK_NORM:
+        raise ValueError(f"kind must be one of {sorted(QK_NORM)}, got {kind!r}")
+    for t, name in ((q, "q"), (k, "k")):
+        if t.dim() != 4:
+            raise ValueError(f"{name} must be [batch, tokens, heads, dim], got shape {tuple(t.shape)}")
+    b, L, HQ, D = q.shape
+    HK = k.shape[2]
+    if HQ < 1 or HK < 1 or D < 1:
+        raise ValueError("q and k must have at least one head and channel")
+    _need(q, "q", contiguous=False)
+    _need(k, "k", q.dtype, (b, L, HK, D), contiguous=False)
+    _need(q_weight, "q_weight", torch.float32, (D,))
+    _need(k_weight, "k_weight", torch.float32, (D,))
+    if inv_freq is not None and inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [rotary_dim / 2]")
+    R = 0 if inv_freq is None else 2 * inv_freq.shape[0]
+    if R > D:
+        raise ValueError(f"inv_freq has {R // 2} pairs for {D} channels")
+    if positions is not None and inv_freq is None:
+        raise ValueError("positions given without inv_freq")
+    _need(inv_freq, "inv_freq", torch.float32)
+    _need(positions, "positions", torch.int32, (b, L))
+    _need_device(q, k=k, q_weight=q_weight, k_weight=k_weight, inv_freq=inv_freq, positions=positions)
+    return ((_ptr(q), _token_row(q, "q"), _ptr(k), _token_row(k, "k"), _ptr(q_weight), _ptr(k_weight),
+             _ptr(inv_freq), _ptr(positions)), (b, L, HQ, HK, D, R))
+
+
+def qk_norm_fwd(q, k, q_weight=None, k_weight=None, eps=1e-6, kind="l2", inv_freq=None,
+                positions=None, interleaved=False, q_out=None, k_out=None):
+    """Norm of every head of q [b, L, HQ, D] and k [b, L, HK, D] (a token's heads side by side, tokens
+    at any one stride; D up to 256): x / sqrt(sum x^2 + eps) (kind "l2") or x / sqrt(mean x^2 + eps)
+    ("rms"), times q_weight / k_weight [D] fp32; with inv_freq [R/2] fp32 the first R channels are
+    turned in pairs (i, i + R/2), or (2i, 2i + 1) if interleaved, by positions * inv_freq[i]
+    (positions [b, L] int32, None: token t of every row is at t).  q_out may be q, k_out may be k.
+    Returns (q_out, k_out)."""
+    lead, sizes = _qk_args(q, k, q_weight, k_weight, inv_freq, positions, kind)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+    _need(q_out, "q_out", q.dtype, q.shape, contiguous=False)
+    _need(k_out, "k_out", q.dtype, k.shape, contiguous=False)
+    _need_device(q, q_out=q_out, k_out=k_out)
+    with _on(q.device):
+        _check("ssm_qk_norm_fwd", _lib.ssm_qk_norm_fwd(
+            *lead, _ptr(q_out), _token_row(q_out, "q_out"), _ptr(k_out), _token_row(k_out, "k_out"),
+            *sizes, int(interleaved), eps, QK_NORM[kind], _dtype_code(q), _stream()))
+    return q_out, k_out
+
+
+def qk_norm_bwd_workspace_size(batch, seqlen, headdim) -> int:
+    return int(_lib.ssm_qk_norm_bwd_workspace_size(batch, seqlen, headdim))
+
+
+def qk_norm_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, eps=1e-6, kind="l2",
+                inv_freq=None, positions=None, interleaved=False, dq=None, dk=None, dq_weight=None,
+                dk_weight=None, workspace=None):
+    """Backward of qk_norm_fwd from dq_out [b, L, HQ, D] and dk_out [b, L, HK, D]: the statistics are
+    recomputed from q and k.  dq may be dq_out, dk may be dk_out.  Returns (dq, dk, dq_weight [D] fp32
+    or None without q_weight, dk_weight likewise)."""
+    lead, sizes = _qk_args(q, k, q_weight, k_weight, inv_freq, positions, kind)
+    D = q.shape[3]
+    _need(dq_out, "dq_out", q.dtype, q.shape, contiguous=False)
+    _need(dk_out, "dk_out", q.dtype, k.shape, contiguous=False)
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if dk is None:
+        dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+    for w, dw, name in ((q_weight, dq_weight, "q"), (k_weight, dk_weight, "k")):
+        if w is None and dw is not None:
+            raise ValueError(f"d{name}_weight given without {name}_weight")
+    if q_weight is not None and dq_weight is None:
+        dq_weight = torch.empty(D, dtype=torch.float32, device=q.device)
+    if k_weight is not None and dk_weight is None:
+        dk_weight = torch.empty(D, dtype=torch.float32, device=q.device)
+    _need(dq, "dq", q.dtype, q.shape, contiguous=False)
+    _need(dk, "dk", q.dtype, k.shape, contiguous=False)
+    _need(dq_weight, "dq_weight", torch.float32, (D,))
+    _need(dk_weight, "dk_weight", torch.float32, (D,))
+    _need_device(q, dq_out=dq_out, dk_out=dk_out, dq=dq, dk=dk, dq_weight=dq_weight, dk_weight=dk_weight,
+                 workspace=workspace)
+    need = 0
+    if dq_weight is not None or dk_weight is not None:
+        need = qk_norm_bwd_workspace_size(*q.shape[:2], D)
+    ws, wsb = _workspace(workspace, need, q.device)
+    with _on(q.device):
+        _check("ssm_qk_norm_bwd", _lib.ssm_qk_norm_bwd(
+            *lead, _ptr(dq_out), _token_row(dq_out, "dq_out"), _ptr(dk_out),
+            _token_row(dk_out, "dk_out"), _ptr(dq), _token_row(dq, "dq"), _ptr(dk),
+            _token_row(dk, "dk"), _ptr(dq_weight), _ptr(dk_weight), _ptr(ws), wsb, *sizes,
+            int(interleaved), eps, QK_NORM[kind], _dtype_code(q), _stream()))
+    return dq, dk, dq_weight, dk_weight
 
 
 NORM = {"rms": 0, "layer": 1}

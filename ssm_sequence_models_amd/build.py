@@ -14,7 +14,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libssm_mi355x.so")
-SOURCES = ["abi.hip", "bwd.hip", "conv.hip", "delta.hip", "delta_bwd.hip", "gscan.hip", "init_state.hip", "norm.hip", "pool.hip", "recurrent.hip", "scan_bwd.hip", "scan_bwd_mfma.hip",
+SOURCES = ["abi.hip", "bwd.hip", "conv.hip", "delta.hip", "delta_bwd.hip", "gscan.hip", "init_state.hip", "norm.hip", "pool.hip", "qk_norm.hip", "recurrent.hip", "scan_bwd.hip", "scan_bwd_mfma.hip",
            "ssd.hip", "vchunk.hip", "vdecay.hip"]
 ARCH = "gfx950"
 

@@ -1527,6 +1527,163 @@ ssm_status_t ssm_delta_scan_step(const void* q, int64_t q_row, const void* k, in
 }
 
 namespace {
+
+ssm_status_t check_qk_norm_dims(const char* fn, int64_t batch, int64_t seqlen, int64_t nheads_q, int64_t nheads_k,
+                                int64_t headdim, int64_t rotary_dim, const float* inv_freq, float eps,
+                                int32_t kind, int dtype) {
+    if (!valid_dtype(dtype)) return fail(SSM_ERR_INVALID_ARG, std::string(fn) + ": bad dtype");
+    if (kind != SSM_QK_NORM_L2 && kind != SSM_QK_NORM_RMS)
+        return fail(SSM_ERR_INVALID_ARG, std::string(fn) + ": bad norm kind");
+    if (batch < 0 || seqlen < 0 || nheads_q < 1 || nheads_k < 1 || headdim < 1)
+        return fail(SSM_ERR_INVALID_ARG, std::string(fn) + ": need batch >= 0, seqlen >= 0, heads and headdim >= 1");
+    if (rotary_dim < 0 || rotary_dim % 2 != 0 || rotary_dim > headdim)
+        return fail(SSM_ERR_INVALID_ARG, std::string(fn) + ": rotary_dim must be even and at most headdim");
+    if (rotary_dim > 0 && inv_freq == nullptr)
+        return fail(SSM_ERR_INVALID_ARG, std::string(fn) + ": inv_freq is NULL");
+    if (!(eps >= 0.0f)) return fail(SSM_ERR_INVALID_ARG, std::string(fn) + ": eps must be >= 0");
+    if (headdim > 256) return fail(SSM_ERR_UNSUPPORTED, std::string(fn) + ": headdim must be at most 256");
+    const int64_t most = int64_t{1} << 31;
+    if (batch >= most || seqlen >= most || (batch > 0 && seqlen >= most / batch) || nheads_q >= most / 256 || nheads_k >= most / 256)
+        return fail(SSM_ERR_UNSUPPORTED, std::string(fn) + ": too many tokens or heads");
+    return SSM_OK;
+}
+
+}  // namespace
+
+ssm_status_t ssm_qk_norm_fwd(const void* q, int64_t q_row, const void* k, int64_t k_row, const float* q_weight,
+                             const float* k_weight, const float* inv_freq, const int32_t* positions,
+                             void* q_out, int64_t q_out_row, void* k_out, int64_t k_out_row, int64_t batch,
+                             int64_t seqlen, int64_t nheads_q, int64_t nheads_k, int64_t headdim,
+                             int64_t rotary_dim, int32_t interleaved, float eps, ssm_qk_norm_t kind,
+                             ssm_dtype_t dtype, ssm_stream_t stream) {
+    const char* fn = "ssm_qk_norm_fwd";
+    ssm_status_t st = check_qk_norm_dims(fn, batch, seqlen, nheads_q, nheads_k, headdim, rotary_dim, inv_freq, eps, kind, dtype);
+    if (st != SSM_OK) return st;
+    const size_t es = esize(dtype);
+    const int64_t rows = batch * seqlen;
+    const bool work = rows > 0;
+    st = check_ptrs(fn, {{"q", q, work, es},
+                         {"k", k, work, es},
+                         {"q_weight", q_weight, false, 4},
+                         {"k_weight", k_weight, false, 4},
+                         {"inv_freq", inv_freq, false, 4},
+                         {"positions", positions, false, 4},
+                         {"q_out", q_out, work, es},
+                         {"k_out", k_out, work, es}});
+    if (st == SSM_OK) st = check_row(fn, "q", q, q_row, rows, 0);
+    if (st == SSM_OK) st = check_row(fn, "k", k, k_row, rows, 0);
+    if (st == SSM_OK) st = check_row(fn, "q_out", q_out, q_out_row, rows, nheads_q * headdim);
+    if (st == SSM_OK) st = check_row(fn, "k_out", k_out, k_out_row, rows, nheads_k * headdim);
+    if (st != SSM_OK) return st;
+    if (!work) return ok();
+    ssm::QkNormCall c{};
+    c.x[0] = q;
+    c.x[1] = k;
+    c.x_row[0] = q_row;
+    c.x_row[1] = k_row;
+    c.out[0] = q_out;
+    c.out[1] = k_out;
+    c.out_row[0] = q_out_row;
+    c.out_row[1] = k_out_row;
+    c.w[0] = q_weight;
+    c.w[1] = k_weight;
+    c.heads[0] = nheads_q;
+    c.heads[1] = nheads_k;
+    c.tokens = rows;
+    c.L = seqlen;
+    c.D = headdim;
+    c.R = rotary_dim;
+    c.inv_freq = inv_freq;
+    c.positions = positions;
+    c.eps = eps;
+    c.l2 = kind == SSM_QK_NORM_L2;
+    c.interleaved = interleaved != 0;
+    c.dtype = dtype;
+    return hip_status(ssm::launch_qk_norm_fwd(c, reinterpret_cast<hipStream_t>(stream)), fn);
+}
+
+size_t ssm_qk_norm_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t headdim) {
+    const int64_t most = int64_t{1} << 31;
+    if (batch <= 0 || seqlen <= 0 || headdim < 1 || headdim > 256 || batch >= most || seqlen >= most / batch) return 0;
+    return static_cast<size_t>(ssm::qk_norm_partial_rows(batch * seqlen) * 2 * headdim) * 4;
+}
+
+ssm_status_t ssm_qk_norm_bwd(const void* q, int64_t q_row, const void* k, int64_t k_row, const float* q_weight,
+                             const float* k_weight, const float* inv_freq, const int32_t* positions,
+                             const void* dq_out, int64_t dq_out_row, const void* dk_out, int64_t dk_out_row,
+                             void* dq, int64_t dq_row, void* dk, int64_t dk_row, float* dq_weight,
+                             float* dk_weight, void* workspace, size_t workspace_bytes, int64_t batch,
+                             int64_t seqlen, int64_t nheads_q, int64_t nheads_k, int64_t headdim,
+                             int64_t rotary_dim, int32_t interleaved, float eps, ssm_qk_norm_t kind,
+                             ssm_dtype_t dtype, ssm_stream_t stream) {
+    const char* fn = "ssm_qk_norm_bwd";
+    ssm_status_t st = check_qk_norm_dims(fn, batch, seqlen, nheads_q, nheads_k, headdim, rotary_dim, inv_freq, eps, kind, dtype);
+    if (st != SSM_OK) return st;
+    const size_t es = esize(dtype);
+    const int64_t rows = batch * seqlen;
+    const bool work = rows > 0;
+    st = check_ptrs(fn, {{"q", q, work, es},
+                         {"k", k, work, es},
+                         {"q_weight", q_weight, false, 4},
+                         {"k_weight", k_weight, false, 4},
+                         {"inv_freq", inv_freq, false, 4},
+                         {"positions", positions, false, 4},
+                         {"dq_out", dq_out, work, es},
+                         {"dk_out", dk_out, work, es},
+                         {"dq", dq, work, es},
+                         {"dk", dk, work, es},
+                         {"dq_weight", dq_weight, false, 4},
+                         {"dk_weight", dk_weight, false, 4},
+                         {"workspace", workspace, false, 4}});
+    if (st == SSM_OK) st = check_row(fn, "q", q, q_row, rows, 0);
+    if (st == SSM_OK) st = check_row(fn, "k", k, k_row, rows, 0);
+    if (st == SSM_OK) st = check_row(fn, "dq_out", dq_out, dq_out_row, rows, 0);
+    if (st == SSM_OK) st = check_row(fn, "dk_out", dk_out, dk_out_row, rows, 0);
+    if (st == SSM_OK) st = check_row(fn, "dq", dq, dq_row, rows, nheads_q * headdim);
+    if (st == SSM_OK) st = check_row(fn, "dk", dk, dk_row, rows, nheads_k * headdim);
+    if (st != SSM_OK) return st;
+    const bool sums = dq_weight != nullptr || dk_weight != nullptr;
+    if (work && sums) {
+        const size_t need = ssm_qk_norm_bwd_workspace_size(batch, seqlen, headdim);
+        if (workspace == nullptr || workspace_bytes < need)
+            return fail(SSM_ERR_WORKSPACE, std::string(fn) + ": workspace missing or smaller than "
+                                           "ssm_qk_norm_bwd_workspace_size");
+    }
+    if (!work && !sums) return ok();
+    ssm::QkNormCall c{};
+    c.x[0] = q;
+    c.x[1] = k;
+    c.x_row[0] = q_row;
+    c.x_row[1] = k_row;
+    c.dy[0] = dq_out;
+    c.dy[1] = dk_out;
+    c.dy_row[0] = dq_out_row;
+    c.dy_row[1] = dk_out_row;
+    c.out[0] = dq;
+    c.out[1] = dk;
+    c.out_row[0] = dq_row;
+    c.out_row[1] = dk_row;
+    c.w[0] = q_weight;
+    c.w[1] = k_weight;
+    c.dw[0] = dq_weight;
+    c.dw[1] = dk_weight;
+    c.partial = sums ? static_cast<float*>(workspace) : nullptr;
+    c.heads[0] = nheads_q;
+    c.heads[1] = nheads_k;
+    c.tokens = rows;
+    c.L = seqlen;
+    c.D = headdim;
+    c.R = rotary_dim;
+    c.inv_freq = inv_freq;
+    c.positions = positions;
+    c.eps = eps;
+    c.l2 = kind == SSM_QK_NORM_L2;
+    c.interleaved = interleaved != 0;
+    c.dtype = dtype;
+    return hip_status(ssm::launch_qk_norm_bwd(c, reinterpret_cast<hipStream_t>(stream)), fn);
+}
+
+namespace {
 ssm_status_t check_state_dims(const char* fn, int64_t batch, int64_t nheads, int64_t headdim,
                               int64_t dstate) {
     if (batch < 0) return fail(SSM_ERR_INVALID_ARG, std::string(fn) + ": negative batch");

@@ -48,11 +48,14 @@ struct DeltaArgs {
     int64_t chunks;
     uint8_t* T;      // [B, H, chunks] images
     uint8_t* M;
-    float* factors;  // [B, H, chunks, 3, Q]: e^G from the chunk's start, e^{G_Q - G}, beta
+    float* factors;  // [B, H, chunks, kFactors, Q]: e^G from the chunk's start, e^{G_Q - G}, beta, sequences begun
 };
 
 namespace delta {
 
+constexpr int kFactors = 4;
+// added to the sequences begun of a chunk's tokens where its keys or queries are not all finite
+constexpr float kNotFinite = 1024.0f;
 constexpr double kLog2e = 1.4426950408889634;
 
 // Sums of gates below this are as good as minus infinity (e^-1e4 = 0 in fp32), and finite: their
@@ -157,6 +160,13 @@ struct ByBf16 {
         f.p[0] = __builtin_bit_cast(bf8, v);
         return f;
     }
+    __device__ __forceinline__ static bool not_finite(const Frag<1>& f) {
+        const u4 v = __builtin_bit_cast(u4, f.p[0]);
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bad = bad || (v[i] & 0x7F800000u) == 0x7F800000u || (v[i] & 0x7F80u) == 0x7F80u;
+        return bad;
+    }
 };
 
 // ---------------------------------------------------------------------------------------
@@ -221,6 +231,12 @@ struct ByF32 {
         return v;
     }
     __device__ __forceinline__ static Frag<1> exact(u4 v) { return {__builtin_bit_cast(f4, v)}; }
+    __device__ __forceinline__ static bool not_finite(const Frag<1>& f) {
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bad = bad || !__builtin_isfinite(f.v[i]);
+        return bad;
+    }
 };
 
 // T or M in the workspace: parts of Q x Q elements, row after row
@@ -264,6 +280,57 @@ __device__ __forceinline__ void stage_image(uint8_t* tiles, const uint8_t* src, 
         *reinterpret_cast<u4*>(tiles + part * MM::template tile_bytes<MM::Q>(MM::Q) + MM::template piece_at<MM::Q>(r, q)) =
             reinterpret_cast<const u4*>(src)[i];
     }
+}
+
+// A NaN or infinity of one packed sequence times the 0 that keeps the sequences apart would reach the
+// others, and with the state the chunks that those go on in.  Products that sum over tokens therefore
+// take the sequences one by one where a chunk holds several and an operand is not finite, and rows
+// of K and Q whose factor is 0 are cleared before they enter the state.
+template <int RT>
+__device__ __forceinline__ bool all_finite(const f4 (&v)[RT]) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s += v[i][e] * 0.0f;
+    return __all(s == 0.0f);
+}
+// out = product(in), by sequences where that is needed; begun: of the chunk's tokens
+template <int RT, class F>
+__device__ __forceinline__ void by_sequences(f4 (&out)[RT], const f4 (&in)[RT], const float* begun, int last, int g4, F product) {
+    const bool one = last == 0 || all_finite(in);
+    for (int r = 0; r <= (one ? 0 : last); ++r) {
+        f4 some[RT], sum[RT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            some[i] = in[i];
+            sum[i] = out[i];
+        }
+        if (!one) {
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (static_cast<int>(begun[16 * i + 4 * g4 + e]) % 1024 != r) some[i][e] = 0.0f;
+        }
+        product(sum, some);
+        if (!one) {
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (static_cast<int>(begun[16 * i + 4 * g4 + e]) % 1024 != r) sum[i][e] = out[i][e];
+        }
+#pragma unroll
+        for (int i = 0; i < RT; ++i) out[i] = sum[i];
+    }
+}
+// rows of a tile whose factor is 0
+template <class MM, int W>
+__device__ __forceinline__ void clear_rows(uint8_t* tile, const float* factor) {
+    constexpr int PIECES = W * sizeof(typename MM::S) / 16;
+    for (int i = threadIdx.x; i < MM::Q * PIECES; i += 256)
+        if (factor[i / PIECES] == 0.0f) *reinterpret_cast<u4*>(tile + MM::template piece_at<W>(i / PIECES, i % PIECES)) = u4{0, 0, 0, 0};
 }
 
 // Blocks are dealt round-robin over the 8 XCDs: neighbours in the result run on one XCD and share
@@ -312,7 +379,7 @@ size_t place_chunks(DeltaArgs& a, uint8_t* ws, bool bwd) {
     a.M = ws + at;
     at += n * image_bytes<MM>(m_parts<MM>(bwd));
     a.factors = reinterpret_cast<float*>(ws + at);
-    return at + n * 3 * MM::Q * 4;
+    return at + n * kFactors * MM::Q * 4;
 }
 
 }  // namespace delta

@@ -29,6 +29,7 @@ __global__ __launch_bounds__(MM::Q * 4) void delta_prep_kernel(DeltaArgs a, int 
     __shared__ double sg[Q];
     __shared__ int sr[Q];
     __shared__ float sbeta[Q];
+    __shared__ int sbad;
     const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g4 = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t unit = xcd_order(blockIdx.x, gridDim.x);  // (b, chunk, h): the heads of a key head are neighbours
@@ -37,6 +38,7 @@ __global__ __launch_bounds__(MM::Q * 4) void delta_prep_kernel(DeltaArgs a, int 
     const int valid = static_cast<int>(a.L - t0 < Q ? a.L - t0 : Q), N = static_cast<int>(a.N);
     const int64_t image = (b * a.H + h) * a.chunks + c;
 
+    if (tid == 0) sbad = 0;
     if (w == 0) {
         const TokenSums s = token_sums<Q>(a, b, h, t0, valid, lane);
         const double end = __shfl(s.gates, Q - 1);
@@ -45,10 +47,11 @@ __global__ __launch_bounds__(MM::Q * 4) void delta_prep_kernel(DeltaArgs a, int 
             sg[lane] = s.gates;
             sr[lane] = s.starts;
             sbeta[lane] = s.beta;
-            float* f = a.factors + image * 3 * Q;
+            float* f = a.factors + image * kFactors * Q;
             f[lane] = s.starts == 0 ? exp_of(s.gates) : 0.0f;
             f[Q + lane] = s.starts == rend ? exp_of(end - s.gates) : 0.0f;
             f[2 * Q + lane] = s.beta;
+            f[3 * Q + lane] = static_cast<float>(s.starts);
         }
     }
     for (int i = tid; i < Q * LD; i += Q * 4) st[i] = sm[i] = 0.0f;
@@ -60,9 +63,11 @@ __global__ __launch_bounds__(MM::Q * 4) void delta_prep_kernel(DeltaArgs a, int 
     const S* qp = static_cast<const S*>(a.q) + (b * a.L + t0) * a.q_row + g * a.N;
     const int rows = 16 * w + li;
     const u4 none{0, 0, 0, 0};
+    bool bad = false;
     for (int n = MM::R * g4; n < N + MM::R * g4; n += MM::KB) {  // the same number of steps in every lane
         const auto fk = MM::exact(rows < valid ? MM::load_run(kp + rows * a.k_row, n, N) : none);
         const auto fq = MM::exact(rows < valid ? MM::load_run(qp + rows * a.q_row, n, N) : none);
+        bad = bad || MM::not_finite(fk) || MM::not_finite(fq);
 #pragma unroll
         for (int j = 0; j < RT; ++j) {
             if (j > w) continue;
@@ -73,6 +78,8 @@ __global__ __launch_bounds__(MM::Q * 4) void delta_prep_kernel(DeltaArgs a, int 
         }
     }
     __syncthreads();
+    const bool several = sr[Q - 1] != 0;
+    if (bad && several) sbad = 1;
 #pragma unroll
     for (int j = 0; j < RT; ++j) {
         if (j > w) continue;
@@ -94,7 +101,7 @@ __global__ __launch_bounds__(MM::Q * 4) void delta_prep_kernel(DeltaArgs a, int 
             float v = i == li ? 1.0f : 0.0f;
 #pragma unroll
             for (int m = 0; m < i; ++m) v -= sd[(16 * w + i) * LD + 16 * w + m] * x[m];
-            x[i] = v;
+            x[i] = v = i < li ? 0.0f : v;  // nothing above the diagonal, whatever D holds
             if (g4 == 0) sii[w][i * 20 + li] = st[(16 * w + i) * LD + 16 * w + li] = v;
         }
     }
@@ -113,6 +120,11 @@ __global__ __launch_bounds__(MM::Q * 4) void delta_prep_kernel(DeltaArgs a, int 
                 const f4 l = *reinterpret_cast<const f4*>(&sd[(16 * i + li) * LD + 16 * (w + m) + 4 * g4]);
                 ByF32::mac<1, 1>(sum, ByF32::Frag<1>{l}, ByF32::Frag<1>{x[m]});
             }
+            if (several) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (sr[16 * i + 4 * g4 + e] != sr[16 * w + li]) sum[e] = 0.0f;
+            }
             f4 out{0, 0, 0, 0};
             const f4 l = *reinterpret_cast<const f4*>(&sii[i][li * 20 + 4 * g4]);
             ByF32::mac<1, 1>(out, ByF32::Frag<1>{l}, ByF32::Frag<1>{sum});
@@ -122,6 +134,7 @@ __global__ __launch_bounds__(MM::Q * 4) void delta_prep_kernel(DeltaArgs a, int 
         }
     }
     __syncthreads();
+    if (sbad && tid < Q) a.factors[image * kFactors * Q + 3 * Q + tid] = static_cast<float>(sr[tid]) + kNotFinite;
     // out in parts, R values a piece
     uint8_t* T = a.T + image * image_bytes<MM>(MM::TP);
     uint8_t* M = a.M + image * image_bytes<MM>(mparts);
@@ -164,7 +177,7 @@ __global__ __launch_bounds__(256) void delta_walk_kernel(DeltaArgs a, DeltaSaved
     __shared__ __attribute__((aligned(16))) uint8_t sq[SAVE ? 16 : QN];
     __shared__ __attribute__((aligned(16))) uint8_t st[MM::TP * QQ];
     __shared__ __attribute__((aligned(16))) uint8_t sm[SAVE ? 16 : MP * QQ];
-    __shared__ __attribute__((aligned(16))) float sf[3 * Q];
+    __shared__ __attribute__((aligned(16))) float sf[kFactors * Q];
     const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g4 = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t pblocks = (a.P + 63) / 64;
@@ -196,9 +209,11 @@ __global__ __launch_bounds__(256) void delta_walk_kernel(DeltaArgs a, DeltaSaved
         if (!SAVE) stage_rows<MM, W, 256>(sq, static_cast<const S*>(a.q) + t0 * a.q_row + g * a.N, a.q_row, valid, N);
         stage_image<MM, 256>(st, a.T + image * image_bytes<MM>(MM::TP), MM::TP);
         if (!SAVE) stage_image<MM, 256>(sm, a.M + image * image_bytes<MM>(MP), MP);
-        if (tid < 3 * Q) sf[tid] = a.factors[image * 3 * Q + tid];
+        if (tid < kFactors * Q) sf[tid] = a.factors[image * kFactors * Q + tid];
         __syncthreads();
-        if (!mine) continue;
+        const int begun = static_cast<int>(sf[4 * Q - 1]) % 1024;
+        const bool clean = sf[4 * Q - 1] < kNotFinite;
+        if (clean && !mine) continue;
         f4 z[RT], y[RT], x[RT];
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
@@ -232,15 +247,17 @@ __global__ __launch_bounds__(256) void delta_walk_kernel(DeltaArgs a, DeltaSaved
             }
             x[i] = f4{0, 0, 0, 0};
         }
+        by_sequences(x, z, sf + 3 * Q, begun, g4, [&](f4 (&out)[RT], const f4 (&in)[RT]) {
 #pragma unroll
-        for (int kk = 0; kk < KT; ++kk) {
-            const auto s = MM::template of_tiles<3>(z, kk);
+            for (int kk = 0; kk < KT; ++kk) {
+                const auto s = MM::template of_tiles<3>(in, kk);
 #pragma unroll
-            for (int i = kk * MM::KB / 16; i < RT; ++i) {
-                const auto l = of_parts<MM, MM::TP>([&](int q) { return MM::template rows<Q>(st + q * QQ, 16 * i, kk, li, g4); });
-                MM::template mac<MM::TP, 3>(x[i], l, s);
+                for (int i = kk * MM::KB / 16; i < RT; ++i) {
+                    const auto l = of_parts<MM, MM::TP>([&](int q) { return MM::template rows<Q>(st + q * QQ, 16 * i, kk, li, g4); });
+                    MM::template mac<MM::TP, 3>(out[i], l, s);
+                }
             }
-        }
+        });
         if (SAVE && have) {
 #pragma unroll
             for (int i = 0; i < RT; ++i)
@@ -272,6 +289,11 @@ __global__ __launch_bounds__(256) void delta_walk_kernel(DeltaArgs a, DeltaSaved
                 }
         }
         // the state after the chunk
+        if (!clean) {
+            __syncthreads();
+            clear_rows<MM, W>(sk, sf + Q);
+            __syncthreads();
+        }
         const float through = sf[Q - 1];
 #pragma unroll
         for (int i = 0; i < NT; ++i)

@@ -52,7 +52,7 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaArgs a, Buffers u)
     __shared__ __attribute__((aligned(16))) uint8_t sq[QN];
     __shared__ __attribute__((aligned(16))) uint8_t st[MM::TP * QQ];
     __shared__ __attribute__((aligned(16))) uint8_t sm[MP * QQ];
-    __shared__ __attribute__((aligned(16))) float sf[3 * Q];
+    __shared__ __attribute__((aligned(16))) float sf[kFactors * Q];
     const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g4 = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t pblocks = (a.P + 63) / 64, ptiles = (a.P + 15) / 16;
@@ -84,9 +84,11 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaArgs a, Buffers u)
         stage_rows<MM, W, 256>(sq, static_cast<const S*>(a.q) + t0 * a.q_row + g * a.N, a.q_row, valid, N);
         stage_image<MM, 256>(st, a.T + image * image_bytes<MM>(MM::TP), MM::TP);
         stage_image<MM, 256>(sm, a.M + image * image_bytes<MM>(MP), MP);
-        if (tid < 3 * Q) sf[tid] = a.factors[image * 3 * Q + tid];
+        if (tid < kFactors * Q) sf[tid] = a.factors[image * kFactors * Q + tid];
         __syncthreads();
-        if (!mine) continue;
+        const int begun = static_cast<int>(sf[4 * Q - 1]) % 1024;
+        const bool clean = sf[4 * Q - 1] < kNotFinite;
+        if (clean && !mine) continue;
         f4 dy[RT], ev[RT], du[RT], dz[RT];
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
@@ -117,39 +119,43 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaArgs a, Buffers u)
             for (int e = 0; e < 4; ++e) {
                 du[i][e] = f[e] != 0.0f ? f[e] * du[i][e] : 0.0f;
                 const float v = sum16(du[i][e] * ev[i][e] * be[e]);
-                if (li == 0) part[Q + 16 * i + 4 * g4 + e] = v;
+                if (mine && li == 0) part[Q + 16 * i + 4 * g4 + e] = v;
             }
         }
         // dU += M^T dY
+        by_sequences(du, dy, sf + 3 * Q, begun, g4, [&](f4 (&out)[RT], const f4 (&in)[RT]) {
 #pragma unroll
-        for (int kk = 0; kk < KT; ++kk) {
-            const auto s = MM::template of_tiles<1>(dy, kk);
+            for (int kk = 0; kk < KT; ++kk) {
+                const auto s = MM::template of_tiles<1>(in, kk);
 #pragma unroll
-            for (int i = 0; i < (kk + 1) * MM::KB / 16; ++i) {
-                const auto l = of_parts<MM, MP>([&](int q) { return MM::template columns<Q>(sm + q * QQ, kk * MM::KB, i, li, g4); });
-                MM::template mac<MP, 1>(du[i], l, s);
+                for (int i = 0; i < (kk + 1) * MM::KB / 16; ++i) {
+                    const auto l = of_parts<MM, MP>([&](int q) { return MM::template columns<Q>(sm + q * QQ, kk * MM::KB, i, li, g4); });
+                    MM::template mac<MP, 1>(out[i], l, s);
+                }
             }
-        }
+        });
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
             const f4 be = row4(sf + 2 * Q + 16 * i + 4 * g4);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float v = sum16(du[i][e] * ev[i][e]);
-                if (li == 0) part[16 * i + 4 * g4 + e] = v;
+                if (mine && li == 0) part[16 * i + 4 * g4 + e] = v;
                 du[i][e] *= be[e];
             }
         }
         // dZ = T^T (b dU)
+        by_sequences(dz, du, sf + 3 * Q, begun, g4, [&](f4 (&out)[RT], const f4 (&in)[RT]) {
 #pragma unroll
-        for (int kk = 0; kk < KT; ++kk) {
-            const auto s = MM::template of_tiles<3>(du, kk);
+            for (int kk = 0; kk < KT; ++kk) {
+                const auto s = MM::template of_tiles<3>(in, kk);
 #pragma unroll
-            for (int i = 0; i < (kk + 1) * MM::KB / 16; ++i) {
-                const auto l = of_parts<MM, MM::TP>([&](int q) { return MM::template columns<Q>(st + q * QQ, kk * MM::KB, i, li, g4); });
-                MM::template mac<MM::TP, 3>(dz[i], l, s);
+                for (int i = 0; i < (kk + 1) * MM::KB / 16; ++i) {
+                    const auto l = of_parts<MM, MM::TP>([&](int q) { return MM::template columns<Q>(st + q * QQ, kk * MM::KB, i, li, g4); });
+                    MM::template mac<MM::TP, 3>(out[i], l, s);
+                }
             }
-        }
+        });
         if (have) {
 #pragma unroll
             for (int i = 0; i < RT; ++i)
@@ -163,6 +169,12 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaArgs a, Buffers u)
                 }
         }
         // the gradient of the state before the chunk
+        if (!clean) {
+            __syncthreads();
+            clear_rows<MM, W>(sk, sf);
+            clear_rows<MM, W>(sq, sf);
+            __syncthreads();
+        }
         const float through = sf[Q - 1];
 #pragma unroll
         for (int i = 0; i < NT; ++i)
@@ -274,7 +286,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a, Buffers u)
     __shared__ __attribute__((aligned(16))) uint8_t sk[QN];
     __shared__ __attribute__((aligned(16))) uint8_t sq[QN];
     __shared__ __attribute__((aligned(16))) uint8_t pool[LOADS > PAIRS ? LOADS : PAIRS];
-    __shared__ __attribute__((aligned(16))) float sf[3 * Q];
+    __shared__ __attribute__((aligned(16))) float sf[kFactors * Q];
     __shared__ double sg[Q];
     __shared__ int sr[Q];
     __shared__ float sdb[RT][Q];    // sums over t of pairs, by row tiles
@@ -330,7 +342,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a, Buffers u)
                     sr[lane] = s.starts;
                 }
             }
-            if (p0 == 0 && tid < 3 * Q) sf[tid] = a.factors[image * 3 * Q + tid];
+            if (p0 == 0 && tid < kFactors * Q) sf[tid] = a.factors[image * kFactors * Q + tid];
             for (int i = tid; i < Q * 64 / R; i += 512) {
                 const int r = i / (64 / R), q = i % (64 / R), left = r < valid ? P - p0 - R * q : 0;
                 float v[R];

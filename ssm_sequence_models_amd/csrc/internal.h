@@ -258,6 +258,25 @@ struct NormCall {
 int64_t norm_partial_rows(int64_t rows, int64_t channels, int64_t groups);
 hipError_t launch_norm_fwd(const NormCall& c, hipStream_t stream);
 hipError_t launch_norm_bwd(const NormCall& c, hipStream_t stream);
+// norm of the heads of queries (0) and keys (1) with the rotation by position
+struct QkNormCall {
+    const void* x[2];
+    const void* dy[2];
+    void* out[2];        // the outputs; backward dq and dk
+    const float* w[2];   // NULL: ones
+    float* dw[2];        // NULL: not written
+    float* partial;      // [qk_norm_partial_rows, 2, D], NULL without dw
+    int64_t x_row[2], dy_row[2], out_row[2], heads[2];
+    int64_t tokens, L, D, R;  // tokens: all rows'; R: rotated channels
+    const float* inv_freq;
+    const int32_t* positions;  // NULL: the token's index in its row
+    float eps;
+    int l2, interleaved;
+    ssm_dtype_t dtype;
+};
+int64_t qk_norm_partial_rows(int64_t tokens);
+hipError_t launch_qk_norm_fwd(const QkNormCall& c, hipStream_t stream);
+hipError_t launch_qk_norm_bwd(const QkNormCall& c, hipStream_t stream);
 // the per-channel gated recurrence; token rows of C elements at the given strides
 struct GscanCall {
     const void* x;
