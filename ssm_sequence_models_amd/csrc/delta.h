@@ -44,10 +44,13 @@ struct DeltaArgs {
     int64_t q_row, k_row, v_row, y_row, dy_row, dq_row, dk_row, dv_row;
     int64_t B, L, H, P, G, N;
     float scale;
-    // set by the launchers: the chunks' part of the workspace
+    // set by the launchers: whether q and k go straight into LDS (16-byte aligned rows, dstate whole pieces)
+    // and a chunk's rows of every token tensor lie within 31 bits of bytes; the chunks' part of the workspace
+    bool direct;
     int64_t chunks;
     uint8_t* T;      // [B, H, chunks] images
     uint8_t* M;
+    uint8_t* Tt;     // transposed, backward only (M is transposed there)
     float* factors;  // [B, H, chunks, kFactors, Q]: e^G from the chunk's start, e^{G_Q - G}, beta, sequences begun
 };
 
@@ -112,6 +115,9 @@ struct ByBf16 {
     static constexpr int tile_bytes(int rows) { return rows * 2 * W; }
     template <int W>
     __device__ __forceinline__ static int piece_at(int row, int q) { return piece<2 * W>(row, q); }
+    // first column of the 16 bytes that lie at slot `s` of a row
+    template <int W>
+    __device__ __forceinline__ static int column_of(int row, int s) { return 8 * (s ^ sw<2 * W>(row)); }
     // left operand, rows r0 + li, contraction block kk in token order
     template <int W>
     __device__ __forceinline__ static Frag<1> rows(const uint8_t* t, int r0, int kk, int li, int g4) {
@@ -207,6 +213,8 @@ struct ByF32 {
     template <int W>
     __device__ __forceinline__ static int piece_at(int row, int q) { return (row * (W + 4) + 4 * q) * 4; }
     template <int W>
+    __device__ __forceinline__ static int column_of(int, int s) { return 4 * s; }
+    template <int W>
     __device__ __forceinline__ static Frag<1> rows(const uint8_t* t, int r0, int kk, int li, int g4) {
         return {lds<f4>(t + piece_at<W>(r0 + li, 4 * kk + g4))};
     }
@@ -239,9 +247,24 @@ struct ByF32 {
     }
 };
 
-// T or M in the workspace: parts of Q x Q elements, row after row
+// T and M in the workspace and in LDS: left operands as the instruction takes them, 64 lanes x 16 bytes
+// a part, of the 16-row tiles rt and contraction blocks kk that are not all 0, rt slowest.  As they
+// are: rows t, contraction over s <= t.  Transposed: rows s, contraction over t >= s.
 template <class MM>
-constexpr int image_bytes(int parts) { return parts * MM::Q * MM::Q * static_cast<int>(sizeof(typename MM::S)); }
+constexpr int first_frag(int rt, bool transposed) {
+    int n = 0;
+    for (int r = 0; r < rt; ++r)
+        n += transposed ? MM::Q / MM::KB - 16 * r / MM::KB : 16 * r / MM::KB + 1;
+    return n;
+}
+template <class MM>
+constexpr int frag_count() { return first_frag<MM>(MM::Q / 16, false); }
+template <class MM>
+constexpr int frag_at(int rt, int kk, bool transposed) {
+    return first_frag<MM>(rt, transposed) + kk - (transposed ? 16 * rt / MM::KB : 0);
+}
+template <class MM>
+constexpr int image_bytes(int parts) { return parts * frag_count<MM>() * 1024; }
 template <class MM>
 constexpr int m_parts(bool bwd) { return MM::TP == 1 ? 1 : bwd ? 3 : 2; }
 
@@ -257,13 +280,68 @@ __device__ __forceinline__ typename MM::template Frag<PARTS> of_parts(F load) {
     }
     return f;
 }
+template <class MM, int PARTS>
+__device__ __forceinline__ typename MM::template Frag<PARTS> frag(const uint8_t* image, int at, int lane) {
+    return of_parts<MM, PARTS>([&](int q) { return MM::exact(lds<u4>(image + (at * PARTS + q) * 1024 + lane * 16)); });
+}
+
+// Raw buffers: loads past the end give 0, stores past it are dropped.
+typedef __amdgpu_buffer_rsrc_t Buffer;
+constexpr int kOutside = 0x7FFFFFF0;
+__device__ __forceinline__ Buffer buffer(const void* p, int64_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, static_cast<int>(bytes), 0x00020000);
+}
+// token rows from t0 on that a chunk has, of `width` elements; rows times stride within 31 bits (DeltaArgs::direct)
+template <class S>
+__device__ __forceinline__ Buffer token_buffer(const void* p, int64_t t0, int64_t row, int64_t col, int valid, int64_t width) {
+    return buffer(static_cast<const S*>(p) + t0 * row + col, ((valid - 1) * row + width) * sizeof(S));
+}
+// 64 x 16 bytes straight into 1 KB of LDS, lane l at byte 16 l
+__device__ __forceinline__ void to_lds(Buffer r, uint32_t at, uint8_t* lds) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, at, 0, 0, 0);
+}
+__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }  // vmcnt(0)
+// an element as it lies in memory; value_of where it is used, which is where the load is waited for
+template <class S>
+__device__ __forceinline__ S load_at(Buffer r, uint32_t at) {
+    if constexpr (sizeof(S) == 2) return __builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0);
+    else return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0));
+}
+__device__ __forceinline__ float value_of(uint16_t v) { return bf16_to_f32(v); }
+__device__ __forceinline__ float value_of(float v) { return v; }
+template <class S>
+__device__ __forceinline__ void store_at(Buffer r, uint32_t at, float v) {
+    if constexpr (sizeof(S) == 2) __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(v), r, at, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, at, 0, 0);
+}
+
+// LDS of a staged tile of W columns: whole rounds of four wavefronts' loads
+template <class MM, int W>
+constexpr int staged_bytes() { return (MM::template tile_bytes<W>(MM::Q) + 4095) / 4096 * 4096; }
+// a tile's rows straight into LDS by four wavefronts (w of them): N columns, zeros past them and past the rows
+template <class MM, int W>
+__device__ __forceinline__ void direct_rows(uint8_t* tile, Buffer r, int row, int N, int w, int lane) {
+    constexpr int ES = sizeof(typename MM::S), SLOTS = MM::template tile_bytes<W>(MM::Q) / MM::Q / 16;
+#pragma unroll
+    for (int i = 0; i < staged_bytes<MM, W>() / 4096; ++i) {
+        const int slot = (4 * i + w) * 64 + lane, t = slot / SLOTS, n = MM::template column_of<W>(t, slot % SLOTS);
+        to_lds(r, t < MM::Q && n < N ? (t * row + n) * ES : kOutside, tile + (4 * i + w) * 1024);
+    }
+}
+// an image's kilobytes
+template <int BYTES>
+__device__ __forceinline__ void direct_image(uint8_t* to, const uint8_t* from, int w, int lane) {
+    const Buffer r = buffer(from, BYTES);
+#pragma unroll
+    for (int i = 0; i < (BYTES + 1023) / 1024; i += 4)
+        if (i + w < (BYTES + 1023) / 1024) to_lds(r, (i + w) * 1024 + lane * 16, to + (i + w) * 1024);
+}
 
 // Q rows of W columns from global memory (rows `row` elements apart, `valid` of them, N columns;
 // zeros elsewhere) into a tile
 template <class MM, int W, int THREADS>
 __device__ __forceinline__ void stage_rows(uint8_t* tile, const typename MM::S* src, int64_t row, int valid, int N) {
     constexpr int E = 16 / sizeof(typename MM::S), PIECES = W / E;
-#pragma unroll
     for (int i = threadIdx.x; i < MM::Q * PIECES; i += THREADS) {
         const int r = i / PIECES, q = i % PIECES;
         u4 v{0, 0, 0, 0};
@@ -271,21 +349,11 @@ __device__ __forceinline__ void stage_rows(uint8_t* tile, const typename MM::S* 
         *reinterpret_cast<u4*>(tile + MM::template piece_at<W>(r, q)) = v;
     }
 }
-// an image's parts into tiles behind each other
-template <class MM, int THREADS>
-__device__ __forceinline__ void stage_image(uint8_t* tiles, const uint8_t* src, int parts) {
-    constexpr int PIECES = MM::Q * sizeof(typename MM::S) / 16;
-    for (int i = threadIdx.x; i < parts * MM::Q * PIECES; i += THREADS) {
-        const int part = i / (MM::Q * PIECES), r = i / PIECES % MM::Q, q = i % PIECES;
-        *reinterpret_cast<u4*>(tiles + part * MM::template tile_bytes<MM::Q>(MM::Q) + MM::template piece_at<MM::Q>(r, q)) =
-            reinterpret_cast<const u4*>(src)[i];
-    }
-}
-
 // A NaN or infinity of one packed sequence times the 0 that keeps the sequences apart would reach the
-// others, and with the state the chunks that those go on in.  Products that sum over tokens therefore
-// take the sequences one by one where a chunk holds several and an operand is not finite, and rows
-// of K and Q whose factor is 0 are cleared before they enter the state.
+// others, and with the state the chunks that those go on in.  So where a chunk holds several sequences
+// and an operand of a product over its tokens is not finite, only the rows of the sequence whose state
+// goes on enter it, the other rows of the result are NaN, and rows of K and Q whose factor is 0 are
+// cleared before they enter the state.
 template <int RT>
 __device__ __forceinline__ bool all_finite(const f4 (&v)[RT]) {
     float s = 0.0f;
@@ -295,35 +363,22 @@ __device__ __forceinline__ bool all_finite(const f4 (&v)[RT]) {
         for (int e = 0; e < 4; ++e) s += v[i][e] * 0.0f;
     return __all(s == 0.0f);
 }
-// out = product(in), by sequences where that is needed; begun: of the chunk's tokens
+// v's rows outside sequence `only` (begun: of the chunk's tokens)
+template <int RT>
+__device__ __forceinline__ void fill_others(f4 (&v)[RT], const float* begun, int only, int g4, float with) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (static_cast<int>(begun[16 * i + 4 * g4 + e]) % static_cast<int>(kNotFinite) != only) v[i][e] = with;
+}
+// out += product(in), with in's rows outside `only` taken out where that is needed
 template <int RT, class F>
-__device__ __forceinline__ void by_sequences(f4 (&out)[RT], const f4 (&in)[RT], const float* begun, int last, int g4, F product) {
-    const bool one = last == 0 || all_finite(in);
-    for (int r = 0; r <= (one ? 0 : last); ++r) {
-        f4 some[RT], sum[RT];
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            some[i] = in[i];
-            sum[i] = out[i];
-        }
-        if (!one) {
-#pragma unroll
-            for (int i = 0; i < RT; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (static_cast<int>(begun[16 * i + 4 * g4 + e]) % 1024 != r) some[i][e] = 0.0f;
-        }
-        product(sum, some);
-        if (!one) {
-#pragma unroll
-            for (int i = 0; i < RT; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (static_cast<int>(begun[16 * i + 4 * g4 + e]) % 1024 != r) sum[i][e] = out[i][e];
-        }
-#pragma unroll
-        for (int i = 0; i < RT; ++i) out[i] = sum[i];
-    }
+__device__ __forceinline__ void kept_apart(f4 (&out)[RT], f4 (&in)[RT], const float* begun, int last, int only, int g4, F product) {
+    const bool apart = last != 0 && !all_finite(in);
+    if (apart) fill_others(in, begun, only, g4, 0.0f);
+    product();
+    if (apart) fill_others(out, begun, only, g4, __builtin_nanf(""));
 }
 // rows of a tile whose factor is 0
 template <class MM, int W>
@@ -368,6 +423,11 @@ __device__ __forceinline__ TokenSums token_sums(const DeltaArgs& a, int64_t b, i
     return s;
 }
 
+inline bool direct_rows_fit(const void* p, int64_t row, size_t es, bool whole) {
+    return row < (int64_t{1} << 30) / 64 / static_cast<int64_t>(es) &&
+           (!whole || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && row * es % 16 == 0));
+}
+
 // the chunks' part of the workspace; returns its bytes
 template <class MM>
 size_t place_chunks(DeltaArgs& a, uint8_t* ws, bool bwd) {
@@ -378,6 +438,8 @@ size_t place_chunks(DeltaArgs& a, uint8_t* ws, bool bwd) {
     at += n * image_bytes<MM>(MM::TP);
     a.M = ws + at;
     at += n * image_bytes<MM>(m_parts<MM>(bwd));
+    a.Tt = ws + at;
+    if (bwd) at += n * image_bytes<MM>(MM::TP);
     a.factors = reinterpret_cast<float*>(ws + at);
     return at + n * kFactors * MM::Q * 4;
 }

@@ -10,36 +10,39 @@ using namespace delta;
 // ---------------------------------------------------------------------------------------
 // delta_prep: T, M and the factors of one chunk of one head, a block of Q / 16 wavefronts
 //
-// Wavefront w forms the rows 16 w .. of k . k and q . k (exact products, fp32 sums) and the
-// factors r of its pairs from differences of double sums, each pair by its own exponential: no
-// factor leaves the range that the pair's own decay has.  T by blocks of 16: the diagonal blocks
-// by forward substitution, one column a lane; then wavefront j takes the blocks below (j, j)
-// down its column, T_ij = -T_ii sum_m D_im T_mj, whose results are the next products' operands
-// where they lie.  (A product form of the inverse, (I - D)(I + D^2) .., loses everything where
-// keys repeat: the powers of D grow as binomials while T itself stays small.)
+// Wavefront w forms the rows t = 16 w .. of k . k and q . k (exact products, fp32 sums) with the keys
+// s as the instruction's rows, so that lane (li, g4) holds the pairs of t = 16 w + li with four
+// neighbouring s: the order of the left operands that T and M are for the walk, which leave
+// from registers.  The factors r of the pairs come from differences of double sums, each by its
+// own exponential: no factor leaves the range that the pair's own decay has.  T (I + D) = I by
+// blocks of 16, from a row's diagonal block to the left: the diagonal block by substitution, a row
+// a lane; then T_ij = -(sum_m T_im D_mj) T_jj, transposed, so that results are the next
+// products' operands where they lie.  (A product form of the inverse, (I - D)(I + D^2) .., loses
+// everything where keys repeat: the powers of D grow as binomials while T itself stays small.)
 // ---------------------------------------------------------------------------------------
-template <class MM>
-__global__ __launch_bounds__(MM::Q * 4) void delta_prep_kernel(DeltaArgs a, int mparts) {
+template <class MM, bool BWD>
+__global__ __launch_bounds__(MM::Q * 4) void delta_prep_kernel(DeltaArgs a) {
     using S = typename MM::S;
-    constexpr int Q = MM::Q, RT = Q / 16, LD = Q + 4;
-    __shared__ __attribute__((aligned(16))) float sd[Q * LD];       // D
-    __shared__ __attribute__((aligned(16))) float st[Q * LD];       // T
-    __shared__ __attribute__((aligned(16))) float sm[Q * LD];       // M
-    __shared__ __attribute__((aligned(16))) float sii[RT][16 * 20];  // T's diagonal blocks
-    __shared__ double sg[Q];
-    __shared__ int sr[Q];
-    __shared__ float sbeta[Q];
+    constexpr int Q = MM::Q, RT = Q / 16, KT = Q / MM::KB, LD = Q + 4, R = MM::R;
+    constexpr int MP = m_parts<MM>(BWD);
+    __shared__ __attribute__((aligned(16))) float sd[Q * LD];        // D transposed: [s][t]
+    __shared__ __attribute__((aligned(16))) float sii[RT][16 * 20];  // T's diagonal blocks, transposed
+    __shared__ __attribute__((aligned(16))) float so[BWD ? Q * LD : 4];
+    __shared__ __attribute__((aligned(16))) double sg[Q];
+    __shared__ __attribute__((aligned(16))) int sr[Q];
+    __shared__ __attribute__((aligned(16))) float sbeta[Q];
     __shared__ int sbad;
     const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g4 = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t unit = xcd_order(blockIdx.x, gridDim.x);  // (b, chunk, h): the heads of a key head are neighbours
-    const int64_t h = unit % a.H, bc = unit / a.H, c = bc % a.chunks, b = bc / a.chunks;
-    const int64_t g = h / (a.H / a.G), t0 = c * Q;
+    const int unit = xcd_order(blockIdx.x, gridDim.x);  // (b, chunk, h): the heads of a key head are neighbours
+    const int H = static_cast<int>(a.H), h = unit % H, bc = unit / H;
+    const int c = bc % static_cast<int>(a.chunks), b = bc / static_cast<int>(a.chunks);
+    const int64_t g = h / (H / static_cast<int>(a.G)), t0 = static_cast<int64_t>(c) * Q;
     const int valid = static_cast<int>(a.L - t0 < Q ? a.L - t0 : Q), N = static_cast<int>(a.N);
-    const int64_t image = (b * a.H + h) * a.chunks + c;
+    const int64_t image = (static_cast<int64_t>(b) * H + h) * a.chunks + c;
 
     if (tid == 0) sbad = 0;
-    if (w == 0) {
+    if (w == RT - 1) {
         const TokenSums s = token_sums<Q>(a, b, h, t0, valid, lane);
         const double end = __shfl(s.gates, Q - 1);
         const int rend = __shfl(s.starts, Q - 1);
@@ -54,178 +57,247 @@ __global__ __launch_bounds__(MM::Q * 4) void delta_prep_kernel(DeltaArgs a, int 
             f[3 * Q + lane] = static_cast<float>(s.starts);
         }
     }
-    for (int i = tid; i < Q * LD; i += Q * 4) st[i] = sm[i] = 0.0f;
-    // products of the rows 16 w ..
+    // products of the rows 16 w ..; rows behind the sequence's end count as its last one and have no
+    // factor other than 0
     f4 kk[RT], qk[RT];
 #pragma unroll
     for (int j = 0; j < RT; ++j) kk[j] = qk[j] = f4{0, 0, 0, 0};
     const S* kp = static_cast<const S*>(a.k) + (b * a.L + t0) * a.k_row + g * a.N;
     const S* qp = static_cast<const S*>(a.q) + (b * a.L + t0) * a.q_row + g * a.N;
-    const int rows = 16 * w + li;
-    const u4 none{0, 0, 0, 0};
+    const int last = valid - 1, own = 16 * w + li < last ? 16 * w + li : last;
     bool bad = false;
-    for (int n = MM::R * g4; n < N + MM::R * g4; n += MM::KB) {  // the same number of steps in every lane
-        const auto fk = MM::exact(rows < valid ? MM::load_run(kp + rows * a.k_row, n, N) : none);
-        const auto fq = MM::exact(rows < valid ? MM::load_run(qp + rows * a.q_row, n, N) : none);
+    for (int n = R * g4; n < N + R * g4; n += MM::KB) {  // the same number of steps in every lane
+        const auto fk = MM::exact(MM::load_run(kp + own * a.k_row, n, N));
+        const auto fq = MM::exact(MM::load_run(qp + own * a.q_row, n, N));
         bad = bad || MM::not_finite(fk) || MM::not_finite(fq);
 #pragma unroll
         for (int j = 0; j < RT; ++j) {
             if (j > w) continue;
-            const int s = 16 * j + li;
-            const auto fs = j == w ? fk : MM::exact(s < valid ? MM::load_run(kp + s * a.k_row, n, N) : none);
-            MM::template mac<1, 1>(kk[j], fk, fs);
-            MM::template mac<1, 1>(qk[j], fq, fs);
+            const int s = 16 * j + li < last ? 16 * j + li : last;
+            const auto fs = j == w ? fk : MM::exact(MM::load_run(kp + s * a.k_row, n, N));
+            MM::template mac<1, 1>(kk[j], fs, fk);
+            MM::template mac<1, 1>(qk[j], fs, fq);
         }
     }
     __syncthreads();
     const bool several = sr[Q - 1] != 0;
     if (bad && several) sbad = 1;
+    const int t = 16 * w + li;
+    const double gt = sg[t];
+    const int rt = sr[t];
 #pragma unroll
     for (int j = 0; j < RT; ++j) {
         if (j > w) continue;
-        const int s = 16 * j + li;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int t = 16 * w + 4 * g4 + e;
-            const float r = s <= t && sr[s] == sr[t] ? exp_of(sg[t] - sg[s]) : 0.0f;
+            const int s = 16 * j + 4 * g4 + e;
+            const float r = s <= t && t < valid && sr[s] == rt ? exp_of(gt - sg[s]) : 0.0f;
             // a factor of 0 leaves nothing of what is not finite either
-            sd[t * LD + s] = s < t && r != 0.0f ? r * kk[j][e] * sbeta[s] : 0.0f;
-            sm[t * LD + s] = r != 0.0f ? r * qk[j][e] * a.scale : 0.0f;
+            sd[s * LD + t] = s < t && r != 0.0f ? r * kk[j][e] * sbeta[s] : 0.0f;
+            qk[j][e] = r != 0.0f ? r * qk[j][e] * a.scale : 0.0f;
         }
     }
     __syncthreads();
-    {  // T_ww, column li
-        float x[16];
+    f4 x[RT];  // T's rows t: x[j][e] is T_ts of s = 16 j + 4 g4 + e
+    {          // the diagonal block, row li of it in every g4
+        float v[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float v = i == li ? 1.0f : 0.0f;
+        for (int j = 15; j >= 0; --j) {
+            float sum = j == li ? 1.0f : 0.0f;
 #pragma unroll
-            for (int m = 0; m < i; ++m) v -= sd[(16 * w + i) * LD + 16 * w + m] * x[m];
-            x[i] = v = i < li ? 0.0f : v;  // nothing above the diagonal, whatever D holds
-            if (g4 == 0) sii[w][i * 20 + li] = st[(16 * w + i) * LD + 16 * w + li] = v;
+            for (int m = j + 1; m < 16; ++m) sum -= v[m] * sd[(16 * w + j) * LD + 16 * w + m];
+            v[j] = j > li ? 0.0f : sum;  // nothing above the diagonal, whatever D holds
         }
+        f4 d;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            d[e] = g4 == 0 ? v[e] : g4 == 1 ? v[4 + e] : g4 == 2 ? v[8 + e] : v[12 + e];
+            sii[w][(4 * g4 + e) * 20 + li] = d[e];
+        }
+#pragma unroll
+        for (int j = 0; j < RT; ++j) x[j] = j == w ? d : f4{0, 0, 0, 0};
     }
     __syncthreads();
-    {  // the blocks below (w, w)
-        f4 x[RT];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[0][e] = sii[w][(4 * g4 + e) * 20 + li];
+    for (int j = RT - 2; j >= 0; --j) {
+        if (j >= w) continue;
+        f4 sum{0, 0, 0, 0}, out{0, 0, 0, 0};
 #pragma unroll
-        for (int d = 1; d < RT; ++d) {
-            if (w + d >= RT) continue;
-            const int i = w + d;
-            f4 sum{0, 0, 0, 0};
-#pragma unroll
-            for (int m = 0; m < d; ++m) {
-                const f4 l = *reinterpret_cast<const f4*>(&sd[(16 * i + li) * LD + 16 * (w + m) + 4 * g4]);
-                ByF32::mac<1, 1>(sum, ByF32::Frag<1>{l}, ByF32::Frag<1>{x[m]});
-            }
-            if (several) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (sr[16 * i + 4 * g4 + e] != sr[16 * w + li]) sum[e] = 0.0f;
-            }
-            f4 out{0, 0, 0, 0};
-            const f4 l = *reinterpret_cast<const f4*>(&sii[i][li * 20 + 4 * g4]);
-            ByF32::mac<1, 1>(out, ByF32::Frag<1>{l}, ByF32::Frag<1>{sum});
-            x[d] = -out;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) st[(16 * i + 4 * g4 + e) * LD + 16 * w + li] = x[d][e];
+        for (int m = j + 1; m < RT; ++m) {
+            if (m > w) continue;
+            const f4 l = *reinterpret_cast<const f4*>(&sd[(16 * j + li) * LD + 16 * m + 4 * g4]);
+            ByF32::mac<1, 1>(sum, ByF32::Frag<1>{l}, ByF32::Frag<1>{x[m]});
         }
+        if (several) {  // sequences apart: a 0 of another's is not one times what is not finite
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (sr[16 * j + 4 * g4 + e] != rt) sum[e] = 0.0f;
+        }
+        const f4 l = *reinterpret_cast<const f4*>(&sii[j][li * 20 + 4 * g4]);
+        ByF32::mac<1, 1>(out, ByF32::Frag<1>{l}, ByF32::Frag<1>{sum});
+        x[j] = -out;
     }
-    __syncthreads();
+    if (several) {
+#pragma unroll
+        for (int j = 0; j < RT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (sr[16 * j + 4 * g4 + e] != rt) x[j][e] = 0.0f;
+    }
     if (sbad && tid < Q) a.factors[image * kFactors * Q + 3 * Q + tid] = static_cast<float>(sr[tid]) + kNotFinite;
-    // out in parts, R values a piece
     uint8_t* T = a.T + image * image_bytes<MM>(MM::TP);
-    uint8_t* M = a.M + image * image_bytes<MM>(mparts);
-    constexpr int PIECES = Q / MM::R;
-    for (int i = tid; i < Q * PIECES; i += Q * 4) {
-        const int r = i / PIECES, q = i % PIECES;
-        float v[MM::R], m[MM::R];
+    uint8_t* M = a.M + image * image_bytes<MM>(MP);
+    const auto put = [&](uint8_t* to, const auto& f, auto parts) {
 #pragma unroll
-        for (int j = 0; j < MM::R; ++j) {
-            const int s = MM::R * q + j;
-            v[j] = sr[s] == sr[r] ? st[r * LD + s] : 0.0f;
-            m[j] = sm[r * LD + s];
+        for (int p = 0; p < parts(); ++p) {
+            if constexpr (MM::TP == 1) *reinterpret_cast<f4*>(to + lane * 16) = f.v;
+            else *reinterpret_cast<bf8*>(to + p * 1024 + lane * 16) = f.p[p];
         }
-        if constexpr (MM::TP == 1) {
-            reinterpret_cast<f4*>(T)[i] = f4{v[0], v[1], v[2], v[3]};
-            reinterpret_cast<f4*>(M)[i] = f4{m[0], m[1], m[2], m[3]};
-        } else {
-            const auto ft = MM::template parts<3>(v);
-            const auto fm = MM::template parts<3>(m);
+    };
 #pragma unroll
-            for (int p = 0; p < 3; ++p) {
-                reinterpret_cast<bf8*>(T)[p * Q * PIECES + i] = ft.p[p];
-                if (p < mparts) reinterpret_cast<bf8*>(M)[p * Q * PIECES + i] = fm.p[p];
+    for (int i = 0; i < RT; ++i) {
+        if (i != w) continue;
+#pragma unroll
+        for (int kb = 0; kb <= 16 * i / MM::KB; ++kb) {
+            put(T + frag_at<MM>(i, kb, false) * MM::TP * 1024, MM::template of_tiles<MM::TP>(x, kb), [] { return MM::TP; });
+            if (!BWD) put(M + frag_at<MM>(i, kb, false) * MP * 1024, MM::template of_tiles<MP>(qk, kb), [] { return MP; });
+        }
+    }
+    if constexpr (BWD) {  // T and M once more with rows s: their columns through LDS
+        uint8_t* Tt = a.Tt + image * image_bytes<MM>(MM::TP);
+#pragma unroll
+        for (int pass = 0; pass < 2; ++pass) {
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < RT; ++j) *reinterpret_cast<f4*>(&so[t * LD + 16 * j + 4 * g4]) = pass ? qk[j] : x[j];
+            __syncthreads();
+#pragma unroll
+            for (int kb = 0; kb < KT; ++kb) {
+                if ((kb + 1) * MM::KB <= 16 * w) continue;
+                float v[R];
+#pragma unroll
+                for (int m = 0; m < R; ++m) v[m] = so[(MM::KB * kb + (m >> 2) * 16 + 4 * g4 + (m & 3)) * LD + t];
+                const auto f = MM::template parts<MM::TP>(v);
+                uint8_t* to = pass ? M : Tt;
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+                    if (i == w) put(to + frag_at<MM>(i, kb, true) * MM::TP * 1024, f, [] { return MM::TP; });
             }
         }
     }
 }
 
 // ---------------------------------------------------------------------------------------
-// The walk: 16 channels of a head a wavefront, four wavefronts a block
-// ---------------------------------------------------------------------------------------
+// The walk: 16 channels of a head a wavefront, four wavefronts a block.  The next chunk's K, Q, T, M and
+// factors go straight into the other half of LDS, and its values into registers, while this
+// chunk's products run (one half only where dstate is over 128).
 // SAVE: for the backward, the states and E in place of y
+// ---------------------------------------------------------------------------------------
 template <class MM, int NT, bool SAVE>
+struct WalkLds {
+    static constexpr int W = 16 * NT, MP = m_parts<MM>(false);
+    static constexpr int K = 0, T = K + staged_bytes<MM, W>(), F = T + image_bytes<MM>(MM::TP), Qq = F + 1024,
+                         M = Qq + (SAVE ? 0 : staged_bytes<MM, W>()), BYTES = M + (SAVE ? 0 : image_bytes<MM>(MP));
+    static constexpr int HALVES = NT <= 8 ? 2 : 1;
+};
+
+// DIRECT: see DeltaArgs; without it q and k pass through registers
+template <class MM, int NT, bool SAVE, bool DIRECT>
 __global__ __launch_bounds__(256) void delta_walk_kernel(DeltaArgs a, DeltaSaved keep) {
     using S = typename MM::S;
-    constexpr int Q = MM::Q, RT = Q / 16, KT = Q / MM::KB, W = 16 * NT, KN = W / MM::KB;
-    constexpr int MP = m_parts<MM>(false);
-    constexpr int QQ = MM::template tile_bytes<Q>(Q), QN = MM::template tile_bytes<W>(Q);
-    __shared__ __attribute__((aligned(16))) uint8_t sk[QN];
-    __shared__ __attribute__((aligned(16))) uint8_t sq[SAVE ? 16 : QN];
-    __shared__ __attribute__((aligned(16))) uint8_t st[MM::TP * QQ];
-    __shared__ __attribute__((aligned(16))) uint8_t sm[SAVE ? 16 : MP * QQ];
-    __shared__ __attribute__((aligned(16))) float sf[kFactors * Q];
+    using O = WalkLds<MM, NT, SAVE>;
+    constexpr int Q = MM::Q, RT = Q / 16, KT = Q / MM::KB, W = 16 * NT, KN = W / MM::KB, MP = O::MP, ES = sizeof(S);
+    __shared__ __attribute__((aligned(1024))) uint8_t sm[O::HALVES * O::BYTES];
     const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g4 = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t pblocks = (a.P + 63) / 64;
-    const int64_t unit = xcd_order(blockIdx.x, gridDim.x);
-    const int64_t pb = unit % pblocks, bh = unit / pblocks, h = bh % a.H, b = bh / a.H;
-    const int64_t g = h / (a.H / a.G);
-    const int64_t p0 = 64 * pb + 16 * w, p = p0 + li;
-    const bool mine = p0 < a.P, have = p < a.P;
-    const int N = static_cast<int>(a.N);
-    const int64_t state = (bh * a.P + p) * a.N;
+    const int H = static_cast<int>(a.H), P = static_cast<int>(a.P), N = static_cast<int>(a.N);
+    const int pblocks = (P + 63) / 64;
+    const int unit = xcd_order(blockIdx.x, gridDim.x);
+    const int pb = unit % pblocks, bh = unit / pblocks, h = bh % H, b = bh / H;
+    const int g = h / (H / static_cast<int>(a.G));
+    const int p0 = 64 * pb + 16 * w, p = p0 + li;
+    const bool mine = p0 < P, have = p < P;
+    const int chunks = static_cast<int>(a.chunks);
+    const int64_t state = (static_cast<int64_t>(bh) * P + p) * N;
+    // byte offsets of this lane's token 4 g4 and channel (DIRECT)
+    const uint32_t vat = have ? 4 * g4 * static_cast<uint32_t>(a.v_row) * ES + p * ES : kOutside;
+    const uint32_t yat = have ? 4 * g4 * static_cast<uint32_t>(a.y_row) * ES + p * ES : kOutside;
+    const auto fetch = [&](int c, uint8_t* half) {
+        const int64_t t0 = b * a.L + static_cast<int64_t>(c) * Q, image = static_cast<int64_t>(bh) * chunks + c;
+        const int valid = static_cast<int>(a.L - static_cast<int64_t>(c) * Q < Q ? a.L - static_cast<int64_t>(c) * Q : Q);
+        if (DIRECT) {
+            direct_rows<MM, W>(half + O::K, token_buffer<S>(a.k, t0, a.k_row, g * N, valid, N), static_cast<int>(a.k_row), N, w, lane);
+            if (!SAVE) direct_rows<MM, W>(half + O::Qq, token_buffer<S>(a.q, t0, a.q_row, g * N, valid, N), static_cast<int>(a.q_row), N, w, lane);
+        } else {
+            stage_rows<MM, W, 256>(half + O::K, static_cast<const S*>(a.k) + t0 * a.k_row + g * N, a.k_row, valid, N);
+            if (!SAVE) stage_rows<MM, W, 256>(half + O::Qq, static_cast<const S*>(a.q) + t0 * a.q_row + g * N, a.q_row, valid, N);
+        }
+        direct_image<image_bytes<MM>(MM::TP)>(half + O::T, a.T + image * image_bytes<MM>(MM::TP), w, lane);
+        if (!SAVE) direct_image<image_bytes<MM>(MP)>(half + O::M, a.M + image * image_bytes<MM>(MP), w, lane);
+        direct_image<kFactors * Q * 4>(half + O::F, reinterpret_cast<const uint8_t*>(a.factors + image * kFactors * Q), w, lane);
+    };
+    S vn[RT][4];  // the next chunk's values
+    const auto fetch_values = [&](int c) {
+        const int64_t t0 = b * a.L + static_cast<int64_t>(c) * Q;
+        const int valid = static_cast<int>(a.L - static_cast<int64_t>(c) * Q < Q ? a.L - static_cast<int64_t>(c) * Q : Q);
+        const Buffer r = token_buffer<S>(a.v, t0, a.v_row, static_cast<int64_t>(h) * P, DIRECT ? valid : 1, P);
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (DIRECT) {
+                    vn[i][e] = load_at<S>(r, vat + (16 * i + e) * static_cast<uint32_t>(a.v_row) * ES);
+                } else {
+                    const int t = 16 * i + 4 * g4 + e;
+                    vn[i][e] = S{0};
+                    if (have && t < valid) vn[i][e] = static_cast<const S*>(a.v)[(t0 + t) * a.v_row + static_cast<int64_t>(h) * P + p];
+                }
+            }
+    };
     f4 hs[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
         const int n = 16 * i + 4 * g4;
         hs[i] = have && n < N && a.h0 ? *reinterpret_cast<const f4*>(a.h0 + state + n) : f4{0, 0, 0, 0};
     }
-    for (int64_t c = 0; c < a.chunks; ++c) {
-        const int64_t t0 = b * a.L + c * Q, image = bh * a.chunks + c;
-        const int valid = static_cast<int>(a.L - c * Q < Q ? a.L - c * Q : Q);
-        if (SAVE && have) {
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                const int n = 16 * i + 4 * g4;
-                if (n < N) *reinterpret_cast<f4*>(keep.states + (image * a.P + p) * a.N + n) = hs[i];
-            }
+    if (O::HALVES == 2) fetch(0, sm);
+    fetch_values(0);
+    for (int c = 0; c < chunks; ++c) {
+        const int64_t t0 = b * a.L + static_cast<int64_t>(c) * Q;
+        const int valid = static_cast<int>(a.L - static_cast<int64_t>(c) * Q < Q ? a.L - static_cast<int64_t>(c) * Q : Q);
+        uint8_t* const half = O::HALVES == 2 ? sm + (c & 1) * O::BYTES : sm;
+        if (O::HALVES == 1) {
+            __syncthreads();
+            fetch(c, half);
         }
+        wait_loads();
         __syncthreads();
-        stage_rows<MM, W, 256>(sk, static_cast<const S*>(a.k) + t0 * a.k_row + g * a.N, a.k_row, valid, N);
-        if (!SAVE) stage_rows<MM, W, 256>(sq, static_cast<const S*>(a.q) + t0 * a.q_row + g * a.N, a.q_row, valid, N);
-        stage_image<MM, 256>(st, a.T + image * image_bytes<MM>(MM::TP), MM::TP);
-        if (!SAVE) stage_image<MM, 256>(sm, a.M + image * image_bytes<MM>(MP), MP);
-        if (tid < kFactors * Q) sf[tid] = a.factors[image * kFactors * Q + tid];
-        __syncthreads();
-        const int begun = static_cast<int>(sf[4 * Q - 1]) % 1024;
-        const bool clean = sf[4 * Q - 1] < kNotFinite;
-        if (clean && !mine) continue;
-        f4 z[RT], y[RT], x[RT];
+        f4 z[RT], y[RT], x[RT], v[RT];
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
             z[i] = y[i] = x[i] = f4{0, 0, 0, 0};
-            if (have) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int t = 16 * i + 4 * g4 + e;
-                    if (t < valid) x[i][e] = MM::value(static_cast<const S*>(a.v) + (t0 + t) * a.v_row + h * a.P, p);
-                }
+            for (int e = 0; e < 4; ++e) v[i][e] = value_of(vn[i][e]);
+        }
+        if (c + 1 < chunks) {
+            if (O::HALVES == 2) fetch(c + 1, sm + ((c + 1) & 1) * O::BYTES);
+            fetch_values(c + 1);
+        }
+        uint8_t* const sk = half + O::K;
+        const uint8_t* const sq = half + O::Qq;
+        const uint8_t* const st = half + O::T;
+        const float* const sf = reinterpret_cast<const float*>(half + O::F);
+        if (SAVE && have) {
+            float* to = keep.states + (static_cast<int64_t>(bh) * chunks + c) * P * N + static_cast<int64_t>(p) * N;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                const int n = 16 * i + 4 * g4;
+                if (n < N) *reinterpret_cast<f4*>(to + n) = hs[i];
             }
         }
+        const int begun = static_cast<int>(sf[4 * Q - 1]) % static_cast<int>(kNotFinite);
+        const bool clean = sf[4 * Q - 1] < kNotFinite;
+        if (clean && !mine) continue;
         // K h^T and Q h^T
 #pragma unroll
         for (int kk = 0; kk < KN; ++kk) {
@@ -239,23 +311,20 @@ __global__ __launch_bounds__(256) void delta_walk_kernel(DeltaArgs a, DeltaSaved
         // Z = V - e^G K h^T, E = T Z
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
-            const f4 f = lds<f4>(reinterpret_cast<const uint8_t*>(sf + 16 * i + 4 * g4));
+            const f4 f = *reinterpret_cast<const f4*>(sf + 16 * i + 4 * g4);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {  // nothing of a state that a start has cut off
-                z[i][e] = x[i][e] - (f[e] != 0.0f ? f[e] * z[i][e] : 0.0f);
+                z[i][e] = v[i][e] - (f[e] != 0.0f ? f[e] * z[i][e] : 0.0f);
                 y[i][e] = f[e] != 0.0f ? f[e] * a.scale * y[i][e] : 0.0f;
             }
-            x[i] = f4{0, 0, 0, 0};
         }
-        by_sequences(x, z, sf + 3 * Q, begun, g4, [&](f4 (&out)[RT], const f4 (&in)[RT]) {
+        kept_apart(x, z, sf + 3 * Q, begun, begun, g4, [&] {
 #pragma unroll
             for (int kk = 0; kk < KT; ++kk) {
-                const auto s = MM::template of_tiles<3>(in, kk);
+                const auto s = MM::template of_tiles<3>(z, kk);
 #pragma unroll
-                for (int i = kk * MM::KB / 16; i < RT; ++i) {
-                    const auto l = of_parts<MM, MM::TP>([&](int q) { return MM::template rows<Q>(st + q * QQ, 16 * i, kk, li, g4); });
-                    MM::template mac<MM::TP, 3>(out[i], l, s);
-                }
+                for (int i = kk * MM::KB / 16; i < RT; ++i)
+                    MM::template mac<MM::TP, 3>(x[i], frag<MM, MM::TP>(st, frag_at<MM>(i, kk, false), lane), s);
             }
         });
         if (SAVE && have) {
@@ -264,28 +333,28 @@ __global__ __launch_bounds__(256) void delta_walk_kernel(DeltaArgs a, DeltaSaved
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int t = 16 * i + 4 * g4 + e;
-                    if (t < valid) keep.e[((t0 + t) * a.H + h) * a.P + p] = x[i][e];
+                    if (t < valid) keep.e[((t0 + t) * H + h) * P + p] = x[i][e];
                 }
         }
         // U = b E, Y += M U
 #pragma unroll
-        for (int i = 0; i < RT; ++i) x[i] *= lds<f4>(reinterpret_cast<const uint8_t*>(sf + 2 * Q + 16 * i + 4 * g4));
+        for (int i = 0; i < RT; ++i) x[i] *= *reinterpret_cast<const f4*>(sf + 2 * Q + 16 * i + 4 * g4);
+        if (!SAVE) {
 #pragma unroll
-        for (int kk = 0; kk < (SAVE ? 0 : KT); ++kk) {
-            const auto s = MM::template of_tiles<MP>(x, kk);
+            for (int kk = 0; kk < KT; ++kk) {
+                const auto s = MM::template of_tiles<MP>(x, kk);
 #pragma unroll
-            for (int i = kk * MM::KB / 16; i < RT; ++i) {
-                const auto l = of_parts<MM, MP>([&](int q) { return MM::template rows<Q>(sm + q * QQ, 16 * i, kk, li, g4); });
-                MM::template mac<MP, MP>(y[i], l, s);
+                for (int i = kk * MM::KB / 16; i < RT; ++i)
+                    MM::template mac<MP, MP>(y[i], frag<MM, MP>(half + O::M, frag_at<MM>(i, kk, false), lane), s);
             }
-        }
-        if (!SAVE && have) {
+            const Buffer r = token_buffer<S>(a.y, t0, a.y_row, static_cast<int64_t>(h) * P, DIRECT ? valid : 1, P);
 #pragma unroll
             for (int i = 0; i < RT; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int t = 16 * i + 4 * g4 + e;
-                    if (t < valid) MM::store(static_cast<S*>(a.y) + (t0 + t) * a.y_row + h * a.P, p, y[i][e]);
+                    if (DIRECT) store_at<S>(r, yat + (16 * i + e) * static_cast<uint32_t>(a.y_row) * ES, y[i][e]);
+                    else if (have && t < valid) MM::store(static_cast<S*>(a.y) + (t0 + t) * a.y_row + static_cast<int64_t>(h) * P, p, y[i][e]);
                 }
         }
         // the state after the chunk
@@ -301,7 +370,7 @@ __global__ __launch_bounds__(256) void delta_walk_kernel(DeltaArgs a, DeltaSaved
             for (int e = 0; e < 4; ++e) hs[i][e] = through != 0.0f ? through * hs[i][e] : 0.0f;
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
-            const f4 f = lds<f4>(reinterpret_cast<const uint8_t*>(sf + Q + 16 * i + 4 * g4));
+            const f4 f = *reinterpret_cast<const f4*>(sf + Q + 16 * i + 4 * g4);
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[i][e] = f[e] != 0.0f ? f[e] * x[i][e] : 0.0f;
         }
@@ -449,7 +518,8 @@ hipError_t step_by_width(const DeltaStep& s, hipStream_t stream) {
 template <class MM, int NT, bool SAVE>
 hipError_t walk_of(const DeltaArgs& a, const DeltaSaved& keep, hipStream_t stream) {
     const int64_t blocks = a.B * a.H * ((a.P + 63) / 64);
-    delta_walk_kernel<MM, NT, SAVE><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a, keep);
+    if (a.direct) delta_walk_kernel<MM, NT, SAVE, true><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a, keep);
+    else delta_walk_kernel<MM, NT, SAVE, false><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a, keep);
     return hipGetLastError();
 }
 template <class MM, bool SAVE>
@@ -461,6 +531,9 @@ hipError_t walk_by_width(const DeltaArgs& a, const DeltaSaved& keep, hipStream_t
 template <class MM>
 hipError_t fwd_of(DeltaArgs a, void* workspace, ssm_dtype_t dtype, hipStream_t stream) {
     place_chunks<MM>(a, static_cast<uint8_t*>(workspace), false);
+    constexpr size_t es = sizeof(typename MM::S);
+    a.direct = a.N % (16 / es) == 0 && direct_rows_fit(a.q, a.q_row, es, true) && direct_rows_fit(a.k, a.k_row, es, true) &&
+               direct_rows_fit(a.v, a.v_row, es, false) && direct_rows_fit(a.y, a.y_row, es, false);
     const hipError_t e = launch_delta_prep(a, dtype, false, stream);
     return e != hipSuccess ? e : walk_by_width<MM, false>(a, DeltaSaved{}, stream);
 }
@@ -469,8 +542,10 @@ hipError_t fwd_of(DeltaArgs a, void* workspace, ssm_dtype_t dtype, hipStream_t s
 
 hipError_t launch_delta_prep(const DeltaArgs& a, ssm_dtype_t dtype, bool bwd, hipStream_t stream) {
     const unsigned blocks = static_cast<unsigned>(a.B * a.H * a.chunks);
-    if (dtype == SSM_BF16) delta_prep_kernel<ByBf16><<<blocks, 256, 0, stream>>>(a, m_parts<ByBf16>(bwd));
-    else delta_prep_kernel<ByF32><<<blocks, 128, 0, stream>>>(a, m_parts<ByF32>(bwd));
+    if (dtype == SSM_BF16 && bwd) delta_prep_kernel<ByBf16, true><<<blocks, 256, 0, stream>>>(a);
+    else if (dtype == SSM_BF16) delta_prep_kernel<ByBf16, false><<<blocks, 256, 0, stream>>>(a);
+    else if (bwd) delta_prep_kernel<ByF32, true><<<blocks, 128, 0, stream>>>(a);
+    else delta_prep_kernel<ByF32, false><<<blocks, 128, 0, stream>>>(a);
     return hipGetLastError();
 }
 

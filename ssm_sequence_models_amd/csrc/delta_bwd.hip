@@ -43,67 +43,124 @@ __device__ __forceinline__ float sum_groups(float v) {  // over the four lanes t
 __device__ __forceinline__ f4 row4(const float* p) { return lds<f4>(reinterpret_cast<const uint8_t*>(p)); }
 
 template <class MM, int NT>
+struct BackLds {
+    static constexpr int W = 16 * NT, MP = m_parts<MM>(true);
+    static constexpr int K = 0, T = K + staged_bytes<MM, W>(), F = T + image_bytes<MM>(MM::TP), Qq = F + 1024,
+                         M = Qq + staged_bytes<MM, W>(), BYTES = M + image_bytes<MM>(MP);
+    static constexpr int HALVES = NT <= 8 ? 2 : 1;
+};
+
+// Laid out, fetched and, with and without DIRECT, addressed as the walk (delta.hip), from the last chunk
+// to the first.
+template <class MM, int NT, bool DIRECT>
 __global__ __launch_bounds__(256) void delta_back_kernel(DeltaArgs a, Buffers u) {
     using S = typename MM::S;
-    constexpr int Q = MM::Q, RT = Q / 16, KT = Q / MM::KB, W = 16 * NT, KN = W / MM::KB;
-    constexpr int MP = m_parts<MM>(true);
-    constexpr int QQ = MM::template tile_bytes<Q>(Q), QN = MM::template tile_bytes<W>(Q);
-    __shared__ __attribute__((aligned(16))) uint8_t sk[QN];
-    __shared__ __attribute__((aligned(16))) uint8_t sq[QN];
-    __shared__ __attribute__((aligned(16))) uint8_t st[MM::TP * QQ];
-    __shared__ __attribute__((aligned(16))) uint8_t sm[MP * QQ];
-    __shared__ __attribute__((aligned(16))) float sf[kFactors * Q];
+    using O = BackLds<MM, NT>;
+    constexpr int Q = MM::Q, RT = Q / 16, KT = Q / MM::KB, W = 16 * NT, KN = W / MM::KB, MP = O::MP, ES = sizeof(S);
+    __shared__ __attribute__((aligned(1024))) uint8_t sm[O::HALVES * O::BYTES];
     const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g4 = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t pblocks = (a.P + 63) / 64, ptiles = (a.P + 15) / 16;
-    const int64_t unit = xcd_order(blockIdx.x, gridDim.x);
-    const int64_t pb = unit % pblocks, bh = unit / pblocks, h = bh % a.H, b = bh / a.H;
-    const int64_t g = h / (a.H / a.G);
-    const int64_t p0 = 64 * pb + 16 * w, p = p0 + li;
-    const bool mine = p0 < a.P, have = p < a.P;
-    const int N = static_cast<int>(a.N);
-    const int64_t state = (bh * a.P + p) * a.N;
+    const int H = static_cast<int>(a.H), P = static_cast<int>(a.P), N = static_cast<int>(a.N);
+    const int pblocks = (P + 63) / 64, ptiles = (P + 15) / 16;
+    const int unit = xcd_order(blockIdx.x, gridDim.x);
+    const int pb = unit % pblocks, bh = unit / pblocks, h = bh % H, b = bh / H;
+    const int g = h / (H / static_cast<int>(a.G));
+    const int p0 = 64 * pb + 16 * w, p = p0 + li;
+    const bool mine = p0 < P, have = p < P;
+    const int chunks = static_cast<int>(a.chunks);
+    const int64_t state = (static_cast<int64_t>(bh) * P + p) * N, erow = static_cast<int64_t>(H) * P;
+    const uint32_t dyat = have ? 4 * g4 * static_cast<uint32_t>(a.dy_row) * ES + p * ES : kOutside;
+    const uint32_t dvat = have ? 4 * g4 * static_cast<uint32_t>(a.dv_row) * ES + p * ES : kOutside;
+    const uint32_t eat = have ? 4 * g4 * static_cast<uint32_t>(erow) * 4 + p * 4 : kOutside;
+    const auto rows_of = [&](int c) {
+        const int64_t left = a.L - static_cast<int64_t>(c) * Q;
+        return static_cast<int>(left < Q ? left : Q);
+    };
+    const auto fetch = [&](int c, uint8_t* half) {
+        const int64_t t0 = b * a.L + static_cast<int64_t>(c) * Q, image = static_cast<int64_t>(bh) * chunks + c;
+        const int valid = rows_of(c);
+        if (DIRECT) {
+            direct_rows<MM, W>(half + O::K, token_buffer<S>(a.k, t0, a.k_row, g * N, valid, N), static_cast<int>(a.k_row), N, w, lane);
+            direct_rows<MM, W>(half + O::Qq, token_buffer<S>(a.q, t0, a.q_row, g * N, valid, N), static_cast<int>(a.q_row), N, w, lane);
+        } else {
+            stage_rows<MM, W, 256>(half + O::K, static_cast<const S*>(a.k) + t0 * a.k_row + g * N, a.k_row, valid, N);
+            stage_rows<MM, W, 256>(half + O::Qq, static_cast<const S*>(a.q) + t0 * a.q_row + g * N, a.q_row, valid, N);
+        }
+        direct_image<image_bytes<MM>(MM::TP)>(half + O::T, a.Tt + image * image_bytes<MM>(MM::TP), w, lane);
+        direct_image<image_bytes<MM>(MP)>(half + O::M, a.M + image * image_bytes<MM>(MP), w, lane);
+        direct_image<kFactors * Q * 4>(half + O::F, reinterpret_cast<const uint8_t*>(a.factors + image * kFactors * Q), w, lane);
+    };
+    S dyn[RT][4];  // the next chunk's dY and E
+    float en[RT][4];
+    const auto fetch_values = [&](int c) {
+        const int64_t t0 = b * a.L + static_cast<int64_t>(c) * Q;
+        const int valid = rows_of(c);
+        const Buffer ry = token_buffer<S>(a.dy, t0, a.dy_row, static_cast<int64_t>(h) * P, DIRECT ? valid : 1, P);
+        const Buffer re = token_buffer<float>(u.saved.e, t0, erow, static_cast<int64_t>(h) * P, DIRECT ? valid : 1, P);
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (DIRECT) {
+                    dyn[i][e] = load_at<S>(ry, dyat + (16 * i + e) * static_cast<uint32_t>(a.dy_row) * ES);
+                    en[i][e] = load_at<float>(re, eat + (16 * i + e) * static_cast<uint32_t>(erow) * 4);
+                } else {
+                    const int t = 16 * i + 4 * g4 + e;
+                    dyn[i][e] = S{0};
+                    en[i][e] = 0.0f;
+                    if (have && t < valid) {
+                        dyn[i][e] = static_cast<const S*>(a.dy)[(t0 + t) * a.dy_row + static_cast<int64_t>(h) * P + p];
+                        en[i][e] = u.saved.e[(t0 + t) * erow + static_cast<int64_t>(h) * P + p];
+                    }
+                }
+            }
+    };
     f4 dh[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
         const int n = 16 * i + 4 * g4;
         dh[i] = have && n < N && a.dhT ? *reinterpret_cast<const f4*>(a.dhT + state + n) : f4{0, 0, 0, 0};
     }
-    for (int64_t c = a.chunks - 1; c >= 0; --c) {
-        const int64_t t0 = b * a.L + c * Q, image = bh * a.chunks + c;
-        const int valid = static_cast<int>(a.L - c * Q < Q ? a.L - c * Q : Q);
-        if (have) {
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                const int n = 16 * i + 4 * g4;
-                if (n < N) *reinterpret_cast<f4*>(u.grads + (image * a.P + p) * a.N + n) = dh[i];
-            }
+    if (O::HALVES == 2) fetch(chunks - 1, sm + ((chunks - 1) & 1) * O::BYTES);
+    fetch_values(chunks - 1);
+    for (int c = chunks - 1; c >= 0; --c) {
+        const int64_t t0 = b * a.L + static_cast<int64_t>(c) * Q, image = static_cast<int64_t>(bh) * chunks + c;
+        const int valid = rows_of(c);
+        uint8_t* const half = O::HALVES == 2 ? sm + (c & 1) * O::BYTES : sm;
+        if (O::HALVES == 1) {
+            __syncthreads();
+            fetch(c, half);
         }
+        wait_loads();
         __syncthreads();
-        stage_rows<MM, W, 256>(sk, static_cast<const S*>(a.k) + t0 * a.k_row + g * a.N, a.k_row, valid, N);
-        stage_rows<MM, W, 256>(sq, static_cast<const S*>(a.q) + t0 * a.q_row + g * a.N, a.q_row, valid, N);
-        stage_image<MM, 256>(st, a.T + image * image_bytes<MM>(MM::TP), MM::TP);
-        stage_image<MM, 256>(sm, a.M + image * image_bytes<MM>(MP), MP);
-        if (tid < kFactors * Q) sf[tid] = a.factors[image * kFactors * Q + tid];
-        __syncthreads();
-        const int begun = static_cast<int>(sf[4 * Q - 1]) % 1024;
-        const bool clean = sf[4 * Q - 1] < kNotFinite;
-        if (clean && !mine) continue;
         f4 dy[RT], ev[RT], du[RT], dz[RT];
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
-            dy[i] = ev[i] = du[i] = dz[i] = f4{0, 0, 0, 0};
-            if (have) {
+            du[i] = dz[i] = f4{0, 0, 0, 0};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int t = 16 * i + 4 * g4 + e;
-                    if (t < valid) {
-                        dy[i][e] = MM::value(static_cast<const S*>(a.dy) + (t0 + t) * a.dy_row + h * a.P, p);
-                        ev[i][e] = u.saved.e[((t0 + t) * a.H + h) * a.P + p];
-                    }
-                }
+            for (int e = 0; e < 4; ++e) {
+                dy[i][e] = value_of(dyn[i][e]);
+                ev[i][e] = en[i][e];
             }
         }
+        if (c > 0) {
+            if (O::HALVES == 2) fetch(c - 1, sm + ((c - 1) & 1) * O::BYTES);
+            fetch_values(c - 1);
+        }
+        if (have) {
+            float* to = u.grads + image * P * N + static_cast<int64_t>(p) * N;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                const int n = 16 * i + 4 * g4;
+                if (n < N) *reinterpret_cast<f4*>(to + n) = dh[i];
+            }
+        }
+        uint8_t* const sk = half + O::K;
+        uint8_t* const sq = half + O::Qq;
+        const float* const sf = reinterpret_cast<const float*>(half + O::F);
+        const int begun = static_cast<int>(sf[4 * Q - 1]) % static_cast<int>(kNotFinite);
+        const bool clean = sf[4 * Q - 1] < kNotFinite;
+        if (clean && !mine) continue;
         // e^{G_Q - G} K dh^T, and its products with U
 #pragma unroll
         for (int kk = 0; kk < KN; ++kk) {
@@ -115,56 +172,59 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaArgs a, Buffers u)
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
             const f4 f = row4(sf + Q + 16 * i + 4 * g4), be = row4(sf + 2 * Q + 16 * i + 4 * g4);
+            f4 v;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 du[i][e] = f[e] != 0.0f ? f[e] * du[i][e] : 0.0f;
-                const float v = sum16(du[i][e] * ev[i][e] * be[e]);
-                if (mine && li == 0) part[Q + 16 * i + 4 * g4 + e] = v;
+                v[e] = sum16(du[i][e] * ev[i][e] * be[e]);
             }
+            if (mine && li == 0) *reinterpret_cast<f4*>(part + Q + 16 * i + 4 * g4) = v;
         }
         // dU += M^T dY
-        by_sequences(du, dy, sf + 3 * Q, begun, g4, [&](f4 (&out)[RT], const f4 (&in)[RT]) {
+        kept_apart(du, dy, sf + 3 * Q, begun, 0, g4, [&] {
 #pragma unroll
             for (int kk = 0; kk < KT; ++kk) {
-                const auto s = MM::template of_tiles<1>(in, kk);
+                const auto s = MM::template of_tiles<1>(dy, kk);
 #pragma unroll
-                for (int i = 0; i < (kk + 1) * MM::KB / 16; ++i) {
-                    const auto l = of_parts<MM, MP>([&](int q) { return MM::template columns<Q>(sm + q * QQ, kk * MM::KB, i, li, g4); });
-                    MM::template mac<MP, 1>(out[i], l, s);
-                }
+                for (int i = 0; i < (kk + 1) * MM::KB / 16; ++i)
+                    MM::template mac<MP, 1>(du[i], frag<MM, MP>(half + O::M, frag_at<MM>(i, kk, true), lane), s);
             }
         });
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
             const f4 be = row4(sf + 2 * Q + 16 * i + 4 * g4);
+            f4 v;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float v = sum16(du[i][e] * ev[i][e]);
-                if (mine && li == 0) part[16 * i + 4 * g4 + e] = v;
+                v[e] = sum16(du[i][e] * ev[i][e]);
                 du[i][e] *= be[e];
             }
+            if (mine && li == 0) *reinterpret_cast<f4*>(part + 16 * i + 4 * g4) = v;
         }
         // dZ = T^T (b dU)
-        by_sequences(dz, du, sf + 3 * Q, begun, g4, [&](f4 (&out)[RT], const f4 (&in)[RT]) {
+        kept_apart(dz, du, sf + 3 * Q, begun, 0, g4, [&] {
 #pragma unroll
             for (int kk = 0; kk < KT; ++kk) {
-                const auto s = MM::template of_tiles<3>(in, kk);
+                const auto s = MM::template of_tiles<3>(du, kk);
 #pragma unroll
-                for (int i = 0; i < (kk + 1) * MM::KB / 16; ++i) {
-                    const auto l = of_parts<MM, MM::TP>([&](int q) { return MM::template columns<Q>(st + q * QQ, kk * MM::KB, i, li, g4); });
-                    MM::template mac<MM::TP, 3>(out[i], l, s);
-                }
+                for (int i = 0; i < (kk + 1) * MM::KB / 16; ++i)
+                    MM::template mac<MM::TP, 3>(dz[i], frag<MM, MM::TP>(half + O::T, frag_at<MM>(i, kk, true), lane), s);
             }
         });
-        if (have) {
+        {
+            const Buffer rz = token_buffer<float>(u.dz, t0, erow, static_cast<int64_t>(h) * P, DIRECT ? valid : 1, P);
+            const Buffer rv = token_buffer<S>(a.dv, t0, a.dv_row, static_cast<int64_t>(h) * P, DIRECT ? valid : 1, P);
 #pragma unroll
             for (int i = 0; i < RT; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int t = 16 * i + 4 * g4 + e;
-                    if (t < valid) {
-                        u.dz[((t0 + t) * a.H + h) * a.P + p] = dz[i][e];
-                        MM::store(static_cast<S*>(a.dv) + (t0 + t) * a.dv_row + h * a.P, p, dz[i][e]);
+                    if (DIRECT) {
+                        store_at<float>(rz, eat + (16 * i + e) * static_cast<uint32_t>(erow) * 4, dz[i][e]);
+                        store_at<S>(rv, dvat + (16 * i + e) * static_cast<uint32_t>(a.dv_row) * ES, dz[i][e]);
+                    } else if (have && t < valid) {
+                        u.dz[(t0 + t) * erow + static_cast<int64_t>(h) * P + p] = dz[i][e];
+                        MM::store(static_cast<S*>(a.dv) + (t0 + t) * a.dv_row + static_cast<int64_t>(h) * P, p, dz[i][e]);
                     }
                 }
         }
@@ -607,7 +667,9 @@ size_t place(DeltaArgs& a, Buffers& u, uint8_t* ws) {
 
 template <class MM, int NT>
 hipError_t kernels_of(const DeltaArgs& a, const Buffers& u, hipStream_t stream) {
-    delta_back_kernel<MM, NT><<<static_cast<unsigned>(a.B * a.H * ((a.P + 63) / 64)), 256, 0, stream>>>(a, u);
+    const unsigned blocks = static_cast<unsigned>(a.B * a.H * ((a.P + 63) / 64));
+    if (a.direct) delta_back_kernel<MM, NT, true><<<blocks, 256, 0, stream>>>(a, u);
+    else delta_back_kernel<MM, NT, false><<<blocks, 256, 0, stream>>>(a, u);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     delta_grad_kernel<MM, NT><<<static_cast<unsigned>(a.B * a.chunks * a.G * u.splits), 512, 0, stream>>>(a, u);
@@ -620,6 +682,10 @@ template <class MM>
 hipError_t bwd_of(DeltaArgs a, void* workspace, ssm_dtype_t dtype, hipStream_t stream) {
     Buffers u{};
     place<MM>(a, u, static_cast<uint8_t*>(workspace));
+    constexpr size_t es = sizeof(typename MM::S);
+    a.direct = a.N % (16 / es) == 0 && direct_rows_fit(a.q, a.q_row, es, true) && direct_rows_fit(a.k, a.k_row, es, true) &&
+               direct_rows_fit(a.v, a.v_row, es, false) && direct_rows_fit(a.dy, a.dy_row, es, false) &&
+               direct_rows_fit(a.dv, a.dv_row, es, false) && direct_rows_fit(nullptr, a.H * a.P, 4, false);
     hipError_t e = launch_delta_prep(a, dtype, true, stream);
     if (e == hipSuccess) e = launch_delta_walk_saved(a, u.saved, dtype, stream);
     if (e != hipSuccess) return e;
