@@ -44,8 +44,8 @@ struct DeltaArgs {
     int64_t q_row, k_row, v_row, y_row, dy_row, dq_row, dk_row, dv_row;
     int64_t B, L, H, P, G, N;
     float scale;
-    // set by the launchers: whether q and k go straight into LDS (16-byte aligned rows, dstate whole pieces)
-    // and a chunk's rows of every token tensor lie within 31 bits of bytes; the chunks' part of the workspace
+    // set by the launchers: whether tokens go straight into LDS (16-byte aligned rows, dstate and headdim whole
+    // pieces, a chunk's rows of every token tensor within 31 bits of bytes); the chunks' part of the workspace
     bool direct;
     int64_t chunks;
     uint8_t* T;      // [B, H, chunks] images
@@ -115,9 +115,6 @@ struct ByBf16 {
     static constexpr int tile_bytes(int rows) { return rows * 2 * W; }
     template <int W>
     __device__ __forceinline__ static int piece_at(int row, int q) { return piece<2 * W>(row, q); }
-    // first column of the 16 bytes that lie at slot `s` of a row
-    template <int W>
-    __device__ __forceinline__ static int column_of(int row, int s) { return 8 * (s ^ sw<2 * W>(row)); }
     // left operand, rows r0 + li, contraction block kk in token order
     template <int W>
     __device__ __forceinline__ static Frag<1> rows(const uint8_t* t, int r0, int kk, int li, int g4) {
@@ -134,6 +131,48 @@ struct ByBf16 {
         f.p[0] = ssm::along<2 * W>(t, along_off<2 * W>(li, g4), r0, kk);
         return f;
     }
+    // first column of the 16 bytes that lie at slot `s` of a row
+    template <int W>
+    __device__ __forceinline__ static int column_of(int row, int s) { return 8 * (s ^ sw<2 * W>(row)); }
+    // Tiles that a state is multiplied with: the same pieces under a swizzle of their own (rows 0 - 7
+    // and 8 - 15 apart but for its bit 1), for the operand along rows in natural order and a
+    // transposing read whose four columns a lane are half b ^ (j & 1) of piece j: 32 lanes at 64 banks.
+    // A state's tile i holds, in lane group g4, the dimensions state_row(i, g4) .. + 3.
+    template <int W>
+    __device__ __forceinline__ static int state_sw(int row) {
+        const int b0 = row & 1, b1 = (row >> 1) & 1, b2 = (row >> 2) & 1, b3 = (row >> 3) & 1;
+        return W == 64 ? b1 << 2 | b3 << 1 | b2 : b0 << 3 | b1 << 2 | b3 << 1 | b2;
+    }
+    template <int W>
+    __device__ __forceinline__ static int state_piece(int row, int q) { return row * (2 * W) + ((q ^ state_sw<W>(row)) << 4); }
+    template <int W>
+    __device__ __forceinline__ static int state_column(int row, int slot) { return 8 * (slot ^ state_sw<W>(row)); }
+    __device__ __forceinline__ static int state_row(int i, int g4) { return 32 * (i >> 1) + 8 * g4 + 4 * ((i & 1) ^ (g4 & 1)); }
+    template <int W>
+    __device__ __forceinline__ static Frag<1> state_rows(const uint8_t* t, int r0, int kk, int li, int g4) {
+        Frag<1> f;
+        f.p[0] = lds<bf8>(t + r0 * (2 * W) + (state_piece<W>(li, g4) ^ (kk << 6)));
+        return f;
+    }
+    template <int W>
+    __device__ __forceinline__ static Frag<1> state_columns(const uint8_t* t, int r0, int i, int li, int g4) {
+        const int j = li & 3, row = 4 * g4 + (li >> 2);
+        const uint8_t* p = t + r0 * (2 * W) + ((state_piece<W>(row, j) + 8 * (j & 1)) ^ ((i >> 1) << 6) ^ ((i & 1) << 3));
+        Frag<1> f;
+        f.p[0] = join(tr_read(p), tr_read(p + 16 * 2 * W));
+        return f;
+    }
+    template <int PARTS>
+    __device__ __forceinline__ static Frag<PARTS> of_state(const f4* tile, int kk, int g4) {
+        const f4 lo = tile[2 * kk], hi = tile[2 * kk + 1];
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[e] = g4 & 1 ? hi[e] : lo[e];
+            v[4 + e] = g4 & 1 ? lo[e] : hi[e];
+        }
+        return parts<PARTS>(v);
+    }
     // left operand, columns 16 c + li as rows, contraction over the tile's rows r0 .. r0 + KB in token order
     template <int W>
     __device__ __forceinline__ static Frag<1> columns(const uint8_t* t, int r0, int c, int li, int g4) {
@@ -145,9 +184,16 @@ struct ByBf16 {
     __device__ __forceinline__ static float at(const uint8_t* t, int row, int col) {
         return bf16_to_f32(lds<uint16_t>(t + piece<2 * W>(row, col >> 3) + 2 * (col & 7)));
     }
+    // rows r0 + 4 g4 .. + 3 of column 16 c + li
     template <int W>
-    __device__ __forceinline__ static void put(uint8_t* t, int row, int col, bf8 v, int j) {
-        *reinterpret_cast<uint16_t*>(t + piece<2 * W>(row, col >> 3) + 2 * (col & 7)) = __builtin_bit_cast(uint16_t, v[j]);
+    __device__ __forceinline__ static f4 four_rows(const uint8_t* t, int r0, int c, int li, int g4) {
+        const u2 v = __builtin_bit_cast(u2, tr_read(t + r0 * (2 * W) + (down_off<2 * W>(4 * g4, li) ^ (c << 5))));
+        return f4{__uint_as_float(v[0] << 16), __uint_as_float(v[0] & 0xFFFF0000u), __uint_as_float(v[1] << 16),
+                  __uint_as_float(v[1] & 0xFFFF0000u)};
+    }
+    template <int W>
+    __device__ __forceinline__ static void put(uint8_t* t, int row, int col, float v) {
+        *reinterpret_cast<uint16_t*>(t + piece<2 * W>(row, col >> 3) + 2 * (col & 7)) = f32_to_bf16(v);
     }
     // values n .. n + R of a row of N (a multiple of 4), zeros past its end
     __device__ __forceinline__ static u4 load_run(const S* p, int n, int N) {
@@ -213,8 +259,6 @@ struct ByF32 {
     template <int W>
     __device__ __forceinline__ static int piece_at(int row, int q) { return (row * (W + 4) + 4 * q) * 4; }
     template <int W>
-    __device__ __forceinline__ static int column_of(int, int s) { return 4 * s; }
-    template <int W>
     __device__ __forceinline__ static Frag<1> rows(const uint8_t* t, int r0, int kk, int li, int g4) {
         return {lds<f4>(t + piece_at<W>(r0 + li, 4 * kk + g4))};
     }
@@ -232,6 +276,33 @@ struct ByF32 {
     template <int W>
     __device__ __forceinline__ static float at(const uint8_t* t, int row, int col) {
         return lds<float>(t + (row * (W + 4) + col) * 4);
+    }
+    template <int W>
+    __device__ __forceinline__ static f4 four_rows(const uint8_t* t, int r0, int c, int li, int g4) {
+        return columns<W>(t, r0, c, li, g4).v;
+    }
+    template <int W>
+    __device__ __forceinline__ static void put(uint8_t* t, int row, int col, float v) {
+        *reinterpret_cast<float*>(t + (row * (W + 4) + col) * 4) = v;
+    }
+    template <int W>
+    __device__ __forceinline__ static int column_of(int, int s) { return 4 * s; }
+    template <int W>
+    __device__ __forceinline__ static int state_piece(int row, int q) { return piece_at<W>(row, q); }
+    template <int W>
+    __device__ __forceinline__ static int state_column(int, int slot) { return 4 * slot; }
+    __device__ __forceinline__ static int state_row(int i, int g4) { return 16 * i + 4 * g4; }
+    template <int W>
+    __device__ __forceinline__ static Frag<1> state_rows(const uint8_t* t, int r0, int kk, int li, int g4) {
+        return rows<W>(t, r0, kk, li, g4);
+    }
+    template <int W>
+    __device__ __forceinline__ static Frag<1> state_columns(const uint8_t* t, int r0, int i, int li, int g4) {
+        return columns<W>(t, r0, i, li, g4);
+    }
+    template <int PARTS>
+    __device__ __forceinline__ static Frag<PARTS> of_state(const f4* tile, int kk, int) {
+        return {tile[kk]};
     }
     __device__ __forceinline__ static u4 load_run(const S* p, int n, int N) {
         u4 v{0, 0, 0, 0};
@@ -315,40 +386,47 @@ __device__ __forceinline__ void store_at(Buffer r, uint32_t at, float v) {
     else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, at, 0, 0);
 }
 
-// LDS of a staged tile of W columns: whole rounds of four wavefronts' loads
+// LDS of a tile of W columns that one wavefront stages: whole kilobytes
 template <class MM, int W>
-constexpr int staged_bytes() { return (MM::template tile_bytes<W>(MM::Q) + 4095) / 4096 * 4096; }
-// a tile's rows straight into LDS by four wavefronts (w of them): N columns, zeros past them and past the rows
-template <class MM, int W>
-__device__ __forceinline__ void direct_rows(uint8_t* tile, Buffer r, int row, int N, int w, int lane) {
+constexpr int staged_bytes() { return (MM::template tile_bytes<W>(MM::Q) + 1023) / 1024 * 1024; }
+// a tile's rows straight into LDS by one wavefront: N columns, zeros past them and past the rows
+template <class MM, int W, bool STATE>
+__device__ __forceinline__ void direct_rows(uint8_t* tile, Buffer r, int row, int N, int lane) {
     constexpr int ES = sizeof(typename MM::S), SLOTS = MM::template tile_bytes<W>(MM::Q) / MM::Q / 16;
 #pragma unroll
-    for (int i = 0; i < staged_bytes<MM, W>() / 4096; ++i) {
-        const int slot = (4 * i + w) * 64 + lane, t = slot / SLOTS, n = MM::template column_of<W>(t, slot % SLOTS);
-        to_lds(r, t < MM::Q && n < N ? (t * row + n) * ES : kOutside, tile + (4 * i + w) * 1024);
+    for (int i = 0; i < staged_bytes<MM, W>() / 1024; ++i) {
+        const int slot = 64 * i + lane, t = slot / SLOTS;
+        const int n = STATE ? MM::template state_column<W>(t, slot % SLOTS) : MM::template column_of<W>(t, slot % SLOTS);
+        to_lds(r, t < MM::Q && n < N ? (t * row + n) * ES : kOutside, tile + 1024 * i);
     }
 }
-// an image's kilobytes
+// an image's kilobytes by one wavefront
 template <int BYTES>
-__device__ __forceinline__ void direct_image(uint8_t* to, const uint8_t* from, int w, int lane) {
+__device__ __forceinline__ void direct_image(uint8_t* to, const uint8_t* from, int lane) {
     const Buffer r = buffer(from, BYTES);
 #pragma unroll
-    for (int i = 0; i < (BYTES + 1023) / 1024; i += 4)
-        if (i + w < (BYTES + 1023) / 1024) to_lds(r, (i + w) * 1024 + lane * 16, to + (i + w) * 1024);
+    for (int i = 0; i < (BYTES + 1023) / 1024; ++i) to_lds(r, i * 1024 + lane * 16, to + i * 1024);
 }
 
 // Q rows of W columns from global memory (rows `row` elements apart, `valid` of them, N columns;
-// zeros elsewhere) into a tile
-template <class MM, int W, int THREADS>
+// zeros elsewhere) into a tile, or one that a state is multiplied with
+template <class MM, int W, int THREADS, bool STATE>
 __device__ __forceinline__ void stage_rows(uint8_t* tile, const typename MM::S* src, int64_t row, int valid, int N) {
     constexpr int E = 16 / sizeof(typename MM::S), PIECES = W / E;
-    for (int i = threadIdx.x; i < MM::Q * PIECES; i += THREADS) {
+    for (int i = threadIdx.x % THREADS; i < MM::Q * PIECES; i += THREADS) {
         const int r = i / PIECES, q = i % PIECES;
         u4 v{0, 0, 0, 0};
         if (r < valid) v = MM::load_run(src + r * row, q * E, N);
-        *reinterpret_cast<u4*>(tile + MM::template piece_at<W>(r, q)) = v;
+        *reinterpret_cast<u4*>(tile + (STATE ? MM::template state_piece<W>(r, q) : MM::template piece_at<W>(r, q))) = v;
     }
 }
+// Q rows of 64 columns, `have` of them, element by element (rows that are not whole pieces)
+template <class MM, int THREADS>
+__device__ __forceinline__ void stage_elements(uint8_t* tile, const typename MM::S* src, int64_t row, int valid, int have) {
+    for (int i = threadIdx.x % THREADS; i < MM::Q * 64; i += THREADS)
+        MM::template put<64>(tile, i / 64, i % 64, i / 64 < valid && i % 64 < have ? MM::value(src + (i / 64) * row, i % 64) : 0.0f);
+}
+
 // A NaN or infinity of one packed sequence times the 0 that keeps the sequences apart would reach the
 // others, and with the state the chunks that those go on in.  So where a chunk holds several sequences
 // and an operand of a product over its tokens is not finite, only the rows of the sequence whose state
@@ -373,19 +451,44 @@ __device__ __forceinline__ void fill_others(f4 (&v)[RT], const float* begun, int
             if (static_cast<int>(begun[16 * i + 4 * g4 + e]) % static_cast<int>(kNotFinite) != only) v[i][e] = with;
 }
 // out += product(in), with in's rows outside `only` taken out where that is needed
-template <int RT, class F>
-__device__ __forceinline__ void kept_apart(f4 (&out)[RT], f4 (&in)[RT], const float* begun, int last, int only, int g4, F product) {
-    const bool apart = last != 0 && !all_finite(in);
-    if (apart) fill_others(in, begun, only, g4, 0.0f);
-    product();
-    if (apart) fill_others(out, begun, only, g4, __builtin_nanf(""));
+template <bool STARTS, int RT, class F>
+__device__ __forceinline__ void kept_apart(f4 (&out)[RT], f4 (&in)[RT], const float* begun, int only, int g4, F product) {
+    if constexpr (STARTS) {
+        const bool apart = !all_finite(in);
+        if (apart) fill_others(in, begun, only, g4, 0.0f);
+        product();
+        if (apart) fill_others(out, begun, only, g4, __builtin_nanf(""));
+    } else {
+        product();
+    }
 }
-// rows of a tile whose factor is 0
+// Products with the factors of a chunk's tokens.  Only where a sequence starts within the chunk (STARTS) is
+// a factor 0 by more than underflow: there it leaves nothing of what is not finite either.
+template <bool STARTS, int RT>
+__device__ __forceinline__ void scale_rows(f4 (&v)[RT], const float* factor, float more, int g4) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        const f4 f = lds<f4>(reinterpret_cast<const uint8_t*>(factor + 16 * i + 4 * g4));
+        v[i] *= f * more;
+        if (STARTS) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[i][e] = f[e] != 0.0f ? v[i][e] : 0.0f;
+        }
+    }
+}
+// (with a start the state before the chunk does not reach its end)
+template <bool STARTS, int NT>
+__device__ __forceinline__ void scale_state(f4 (&v)[NT], float through) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) v[i] = STARTS && through == 0.0f ? f4{0, 0, 0, 0} : v[i] * through;
+}
+
+// rows of a tile whose factor is 0, by the four wavefronts that walk
 template <class MM, int W>
 __device__ __forceinline__ void clear_rows(uint8_t* tile, const float* factor) {
     constexpr int PIECES = W * sizeof(typename MM::S) / 16;
     for (int i = threadIdx.x; i < MM::Q * PIECES; i += 256)
-        if (factor[i / PIECES] == 0.0f) *reinterpret_cast<u4*>(tile + MM::template piece_at<W>(i / PIECES, i % PIECES)) = u4{0, 0, 0, 0};
+        if (factor[i / PIECES] == 0.0f) *reinterpret_cast<u4*>(tile + MM::template state_piece<W>(i / PIECES, i % PIECES)) = u4{0, 0, 0, 0};
 }
 
 // Blocks are dealt round-robin over the 8 XCDs: neighbours in the result run on one XCD and share
@@ -423,9 +526,8 @@ __device__ __forceinline__ TokenSums token_sums(const DeltaArgs& a, int64_t b, i
     return s;
 }
 
-inline bool direct_rows_fit(const void* p, int64_t row, size_t es, bool whole) {
-    return row < (int64_t{1} << 30) / 64 / static_cast<int64_t>(es) &&
-           (!whole || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && row * es % 16 == 0));
+inline bool direct_rows_fit(const void* p, int64_t row, size_t es) {
+    return row < (int64_t{1} << 30) / 64 / static_cast<int64_t>(es) && reinterpret_cast<uintptr_t>(p) % 16 == 0 && row * es % 16 == 0;
 }
 
 // the chunks' part of the workspace; returns its bytes
@@ -446,9 +548,7 @@ size_t place_chunks(DeltaArgs& a, uint8_t* ws, bool bwd) {
 
 }  // namespace delta
 
-// T, M and the factors of every chunk
-hipError_t launch_delta_prep(const DeltaArgs& a, ssm_dtype_t dtype, bool bwd, hipStream_t stream);
-// what the backward keeps of a walk: the state before every chunk, and E
+// what the backward keeps of a walk: the state before every chunk, and E (and T and M transposed)
 struct DeltaSaved {
     float* states;  // [B, H, chunks, P, N]
     float* e;       // [B, L, H, P]

@@ -1,5 +1,7 @@
 // delta.hip -- the gated delta rule forward (formulas in delta.h): delta_prep, the walk along the
 // rows, and the token-by-token form on state slots.
+#include <type_traits>
+
 #include "delta.h"
 
 namespace ssm {
@@ -20,10 +22,10 @@ using namespace delta;
 // products' operands where they lie.  (A product form of the inverse, (I - D)(I + D^2) .., loses
 // everything where keys repeat: the powers of D grow as binomials while T itself stays small.)
 // ---------------------------------------------------------------------------------------
-template <class MM, bool BWD>
+template <class MM, int NT, bool BWD, bool DIRECT>
 __global__ __launch_bounds__(MM::Q * 4) void delta_prep_kernel(DeltaArgs a) {
     using S = typename MM::S;
-    constexpr int Q = MM::Q, RT = Q / 16, KT = Q / MM::KB, LD = Q + 4, R = MM::R;
+    constexpr int Q = MM::Q, RT = Q / 16, KT = Q / MM::KB, LD = Q + 4, R = MM::R, KN = 16 * NT / MM::KB;
     constexpr int MP = m_parts<MM>(BWD);
     __shared__ __attribute__((aligned(16))) float sd[Q * LD];        // D transposed: [s][t]
     __shared__ __attribute__((aligned(16))) float sii[RT][16 * 20];  // T's diagonal blocks, transposed
@@ -57,28 +59,42 @@ __global__ __launch_bounds__(MM::Q * 4) void delta_prep_kernel(DeltaArgs a) {
             f[3 * Q + lane] = static_cast<float>(s.starts);
         }
     }
-    // products of the rows 16 w ..; rows behind the sequence's end count as its last one and have no
-    // factor other than 0
+    // products of the rows 16 w ..; rows behind the row's end are 0
     f4 kk[RT], qk[RT];
 #pragma unroll
     for (int j = 0; j < RT; ++j) kk[j] = qk[j] = f4{0, 0, 0, 0};
-    const S* kp = static_cast<const S*>(a.k) + (b * a.L + t0) * a.k_row + g * a.N;
-    const S* qp = static_cast<const S*>(a.q) + (b * a.L + t0) * a.q_row + g * a.N;
-    const int last = valid - 1, own = 16 * w + li < last ? 16 * w + li : last;
+    const int64_t first = b * a.L + t0;
+    const S* kp = static_cast<const S*>(a.k) + first * a.k_row + g * a.N;
+    const S* qp = static_cast<const S*>(a.q) + first * a.q_row + g * a.N;
+    const Buffer rk = token_buffer<S>(a.k, first, a.k_row, g * a.N, DIRECT ? valid : 1, a.N);
+    const Buffer rq = token_buffer<S>(a.q, first, a.q_row, g * a.N, DIRECT ? valid : 1, a.N);
+    const auto load = [&](Buffer r, const S* p, int64_t row, int t, int kb) {
+        const int n = MM::KB * kb + R * g4;
+        if (DIRECT)
+            return __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(
+                                              r, n < N ? (t * static_cast<uint32_t>(row) + n) * sizeof(S) : kOutside, 0, 0));
+        return t < valid ? MM::load_run(p + t * row, n, N) : u4{0, 0, 0, 0};
+    };
     bool bad = false;
-    for (int n = R * g4; n < N + R * g4; n += MM::KB) {  // the same number of steps in every lane
-        const auto fk = MM::exact(MM::load_run(kp + own * a.k_row, n, N));
-        const auto fq = MM::exact(MM::load_run(qp + own * a.q_row, n, N));
-        bad = bad || MM::not_finite(fk) || MM::not_finite(fq);
+    u4 fk[KN], fq[KN];
 #pragma unroll
-        for (int j = 0; j < RT; ++j) {
-            if (j > w) continue;
-            const int s = 16 * j + li < last ? 16 * j + li : last;
-            const auto fs = j == w ? fk : MM::exact(MM::load_run(kp + s * a.k_row, n, N));
-            MM::template mac<1, 1>(kk[j], fs, fk);
-            MM::template mac<1, 1>(qk[j], fs, fq);
+    for (int kb = 0; kb < KN; ++kb) fk[kb] = load(rk, kp, a.k_row, 16 * w + li, kb);
+#pragma unroll
+    for (int kb = 0; kb < KN; ++kb) fq[kb] = load(rq, qp, a.q_row, 16 * w + li, kb);
+#pragma unroll
+    for (int j = 0; j < RT; ++j) {
+        if (j > w) continue;
+        u4 fs[KN];
+#pragma unroll
+        for (int kb = 0; kb < KN; ++kb) fs[kb] = j == w ? fk[kb] : load(rk, kp, a.k_row, 16 * j + li, kb);
+#pragma unroll
+        for (int kb = 0; kb < KN; ++kb) {
+            MM::template mac<1, 1>(kk[j], MM::exact(fs[kb]), MM::exact(fk[kb]));
+            MM::template mac<1, 1>(qk[j], MM::exact(fs[kb]), MM::exact(fq[kb]));
         }
     }
+#pragma unroll
+    for (int kb = 0; kb < KN; ++kb) bad = bad || MM::not_finite(MM::exact(fk[kb])) || MM::not_finite(MM::exact(fq[kb]));
     __syncthreads();
     const bool several = sr[Q - 1] != 0;
     if (bad && several) sbad = 1;
@@ -188,204 +204,216 @@ __global__ __launch_bounds__(MM::Q * 4) void delta_prep_kernel(DeltaArgs a) {
 }
 
 // ---------------------------------------------------------------------------------------
-// The walk: 16 channels of a head a wavefront, four wavefronts a block.  The next chunk's K, Q, T, M and
-// factors go straight into the other half of LDS, and its values into registers, while this
-// chunk's products run (one half only where dstate is over 128).
+// The walk: 16 channels of a head a wavefront, four such wavefronts a block, and a fifth that moves memory:
+// the next chunk's K, Q, T, M, factors and values straight into the other half of LDS (one half only
+// where dstate is over 128), and the last chunk's y out of it.  (Fetched by the four themselves, the
+// loads' issue was a third of a chunk's time.)
 // SAVE: for the backward, the states and E in place of y
+// DIRECT: see DeltaArgs; without it tokens pass through registers
 // ---------------------------------------------------------------------------------------
 template <class MM, int NT, bool SAVE>
 struct WalkLds {
-    static constexpr int W = 16 * NT, MP = m_parts<MM>(false);
-    static constexpr int K = 0, T = K + staged_bytes<MM, W>(), F = T + image_bytes<MM>(MM::TP), Qq = F + 1024,
-                         M = Qq + (SAVE ? 0 : staged_bytes<MM, W>()), BYTES = M + (SAVE ? 0 : image_bytes<MM>(MP));
-    static constexpr int HALVES = NT <= 8 ? 2 : 1;
+    static constexpr int W = 16 * NT, MP = m_parts<MM>(false), HALVES = NT <= 8 ? 2 : 1;
+    static constexpr int V = 0, K = V + staged_bytes<MM, 64>(), T = K + staged_bytes<MM, W>(), F = T + image_bytes<MM>(MM::TP),
+                         Qq = F + 1024, M = Qq + (SAVE ? 0 : staged_bytes<MM, W>()), HALF = M + (SAVE ? 0 : image_bytes<MM>(MP));
+    static constexpr int Y = HALVES * HALF, BYTES = Y + (SAVE ? 0 : 2 * MM::template tile_bytes<64>(MM::Q));
 };
 
-// DIRECT: see DeltaArgs; without it q and k pass through registers
 template <class MM, int NT, bool SAVE, bool DIRECT>
-__global__ __launch_bounds__(256) void delta_walk_kernel(DeltaArgs a, DeltaSaved keep) {
+__global__ __launch_bounds__(320) void delta_walk_kernel(DeltaArgs a, DeltaSaved keep) {
     using S = typename MM::S;
     using O = WalkLds<MM, NT, SAVE>;
     constexpr int Q = MM::Q, RT = Q / 16, KT = Q / MM::KB, W = 16 * NT, KN = W / MM::KB, MP = O::MP, ES = sizeof(S);
-    __shared__ __attribute__((aligned(1024))) uint8_t sm[O::HALVES * O::BYTES];
-    const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g4 = lane >> 4;
-    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    constexpr int YB = MM::template tile_bytes<64>(Q);
+    __shared__ __attribute__((aligned(1024))) uint8_t sm[O::BYTES];
+    const int lane = threadIdx.x & 63, li = lane & 15, g4 = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int H = static_cast<int>(a.H), P = static_cast<int>(a.P), N = static_cast<int>(a.N);
     const int pblocks = (P + 63) / 64;
     const int unit = xcd_order(blockIdx.x, gridDim.x);
     const int pb = unit % pblocks, bh = unit / pblocks, h = bh % H, b = bh / H;
     const int g = h / (H / static_cast<int>(a.G));
+    const int chunks = static_cast<int>(a.chunks);
+    const auto rows_of = [&](int c) {
+        const int64_t left = a.L - static_cast<int64_t>(c) * Q;
+        return static_cast<int>(left < Q ? left : Q);
+    };
+    const auto half_of = [&](int c) { return sm + (O::HALVES == 2 ? (c & 1) * O::HALF : 0); };
+    // what the chunk's last token says: sequences begun, and whether all keys and queries are finite
+    const auto marks_of = [&](const uint8_t* half) {
+        return __builtin_amdgcn_readfirstlane(static_cast<int>(reinterpret_cast<const float*>(half + O::F)[4 * Q - 1]));
+    };
+
+    if (w == 4) {
+        const int64_t col = static_cast<int64_t>(h) * P + 64 * pb;
+        const int width = P - 64 * pb < 64 ? P - 64 * pb : 64;
+        const auto fetch = [&](int c) {
+            uint8_t* const half = half_of(c);
+            const int64_t t0 = b * a.L + static_cast<int64_t>(c) * Q, image = static_cast<int64_t>(bh) * chunks + c;
+            const int valid = rows_of(c);
+            if (DIRECT) {
+                direct_rows<MM, W, true>(half + O::K, token_buffer<S>(a.k, t0, a.k_row, g * N, valid, N), static_cast<int>(a.k_row), N, lane);
+                if (!SAVE) direct_rows<MM, W, true>(half + O::Qq, token_buffer<S>(a.q, t0, a.q_row, g * N, valid, N), static_cast<int>(a.q_row), N, lane);
+                direct_rows<MM, 64, false>(half + O::V, token_buffer<S>(a.v, t0, a.v_row, col, valid, width), static_cast<int>(a.v_row), width, lane);
+            } else {
+                stage_rows<MM, W, 64, true>(half + O::K, static_cast<const S*>(a.k) + t0 * a.k_row + g * N, a.k_row, valid, N);
+                if (!SAVE) stage_rows<MM, W, 64, true>(half + O::Qq, static_cast<const S*>(a.q) + t0 * a.q_row + g * N, a.q_row, valid, N);
+                stage_elements<MM, 64>(half + O::V, static_cast<const S*>(a.v) + t0 * a.v_row + col, a.v_row, valid, width);
+            }
+            direct_image<image_bytes<MM>(MM::TP)>(half + O::T, a.T + image * image_bytes<MM>(MM::TP), lane);
+            if (!SAVE) direct_image<image_bytes<MM>(MP)>(half + O::M, a.M + image * image_bytes<MM>(MP), lane);
+            direct_image<kFactors * Q * 4>(half + O::F, reinterpret_cast<const uint8_t*>(a.factors + image * kFactors * Q), lane);
+        };
+        const auto store = [&](int c) {
+            if (SAVE || c < 0) return;
+            const uint8_t* y = sm + O::Y + (c & 1) * YB;
+            const int64_t t0 = b * a.L + static_cast<int64_t>(c) * Q;
+            const int valid = rows_of(c);
+            if (DIRECT) {
+                constexpr int PIECES = 64 * ES / 16;
+                const Buffer r = token_buffer<S>(a.y, t0, a.y_row, col, valid, width);
+#pragma unroll
+                for (int i = 0; i < Q * PIECES / 64; ++i) {
+                    const int t = (64 * i + lane) / PIECES, q = lane % PIECES, n = q * (16 / ES);
+                    __builtin_amdgcn_raw_buffer_store_b128(lds<u4>(y + MM::template piece_at<64>(t, q)), r,
+                                                           n < width ? (t * static_cast<int>(a.y_row) + n) * ES : kOutside, 0, 0);
+                }
+            } else {
+                for (int i = lane; i < valid * 64; i += 64)
+                    if (lane < width)
+                        MM::store(static_cast<S*>(a.y) + (t0 + i / 64) * a.y_row + col, lane, MM::template at<64>(y, i / 64, lane));
+            }
+        };
+        if (O::HALVES == 2) fetch(0);
+        for (int c = 0; c < chunks; ++c) {
+            if (O::HALVES == 1) {
+                __syncthreads();
+                fetch(c);
+            }
+            wait_loads();
+            __syncthreads();
+            if (O::HALVES == 2 && c + 1 < chunks) fetch(c + 1);
+            store(c - 1);
+            if (marks_of(half_of(c)) >= static_cast<int>(kNotFinite)) {
+                __syncthreads();
+                __syncthreads();
+            }
+        }
+        __syncthreads();
+        store(chunks - 1);
+        return;
+    }
+
     const int p0 = 64 * pb + 16 * w, p = p0 + li;
     const bool mine = p0 < P, have = p < P;
-    const int chunks = static_cast<int>(a.chunks);
     const int64_t state = (static_cast<int64_t>(bh) * P + p) * N;
-    // byte offsets of this lane's token 4 g4 and channel (DIRECT)
-    const uint32_t vat = have ? 4 * g4 * static_cast<uint32_t>(a.v_row) * ES + p * ES : kOutside;
-    const uint32_t yat = have ? 4 * g4 * static_cast<uint32_t>(a.y_row) * ES + p * ES : kOutside;
-    const auto fetch = [&](int c, uint8_t* half) {
-        const int64_t t0 = b * a.L + static_cast<int64_t>(c) * Q, image = static_cast<int64_t>(bh) * chunks + c;
-        const int valid = static_cast<int>(a.L - static_cast<int64_t>(c) * Q < Q ? a.L - static_cast<int64_t>(c) * Q : Q);
-        if (DIRECT) {
-            direct_rows<MM, W>(half + O::K, token_buffer<S>(a.k, t0, a.k_row, g * N, valid, N), static_cast<int>(a.k_row), N, w, lane);
-            if (!SAVE) direct_rows<MM, W>(half + O::Qq, token_buffer<S>(a.q, t0, a.q_row, g * N, valid, N), static_cast<int>(a.q_row), N, w, lane);
-        } else {
-            stage_rows<MM, W, 256>(half + O::K, static_cast<const S*>(a.k) + t0 * a.k_row + g * N, a.k_row, valid, N);
-            if (!SAVE) stage_rows<MM, W, 256>(half + O::Qq, static_cast<const S*>(a.q) + t0 * a.q_row + g * N, a.q_row, valid, N);
-        }
-        direct_image<image_bytes<MM>(MM::TP)>(half + O::T, a.T + image * image_bytes<MM>(MM::TP), w, lane);
-        if (!SAVE) direct_image<image_bytes<MM>(MP)>(half + O::M, a.M + image * image_bytes<MM>(MP), w, lane);
-        direct_image<kFactors * Q * 4>(half + O::F, reinterpret_cast<const uint8_t*>(a.factors + image * kFactors * Q), w, lane);
-    };
-    S vn[RT][4];  // the next chunk's values
-    const auto fetch_values = [&](int c) {
-        const int64_t t0 = b * a.L + static_cast<int64_t>(c) * Q;
-        const int valid = static_cast<int>(a.L - static_cast<int64_t>(c) * Q < Q ? a.L - static_cast<int64_t>(c) * Q : Q);
-        const Buffer r = token_buffer<S>(a.v, t0, a.v_row, static_cast<int64_t>(h) * P, DIRECT ? valid : 1, P);
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (DIRECT) {
-                    vn[i][e] = load_at<S>(r, vat + (16 * i + e) * static_cast<uint32_t>(a.v_row) * ES);
-                } else {
-                    const int t = 16 * i + 4 * g4 + e;
-                    vn[i][e] = S{0};
-                    if (have && t < valid) vn[i][e] = static_cast<const S*>(a.v)[(t0 + t) * a.v_row + static_cast<int64_t>(h) * P + p];
-                }
-            }
-    };
+    const uint32_t eat = have ? 4 * g4 * static_cast<uint32_t>(H * P) * 4 + p * 4 : kOutside;
     f4 hs[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-        const int n = 16 * i + 4 * g4;
+        const int n = MM::state_row(i, g4);
         hs[i] = have && n < N && a.h0 ? *reinterpret_cast<const f4*>(a.h0 + state + n) : f4{0, 0, 0, 0};
     }
-    if (O::HALVES == 2) fetch(0, sm);
-    fetch_values(0);
     for (int c = 0; c < chunks; ++c) {
         const int64_t t0 = b * a.L + static_cast<int64_t>(c) * Q;
-        const int valid = static_cast<int>(a.L - static_cast<int64_t>(c) * Q < Q ? a.L - static_cast<int64_t>(c) * Q : Q);
-        uint8_t* const half = O::HALVES == 2 ? sm + (c & 1) * O::BYTES : sm;
-        if (O::HALVES == 1) {
-            __syncthreads();
-            fetch(c, half);
-        }
-        wait_loads();
+        const int valid = rows_of(c);
+        uint8_t* const half = half_of(c);
+        if (O::HALVES == 1) __syncthreads();
         __syncthreads();
-        f4 z[RT], y[RT], x[RT], v[RT];
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            z[i] = y[i] = x[i] = f4{0, 0, 0, 0};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[i][e] = value_of(vn[i][e]);
-        }
-        if (c + 1 < chunks) {
-            if (O::HALVES == 2) fetch(c + 1, sm + ((c + 1) & 1) * O::BYTES);
-            fetch_values(c + 1);
-        }
         uint8_t* const sk = half + O::K;
-        const uint8_t* const sq = half + O::Qq;
-        const uint8_t* const st = half + O::T;
         const float* const sf = reinterpret_cast<const float*>(half + O::F);
         if (SAVE && have) {
             float* to = keep.states + (static_cast<int64_t>(bh) * chunks + c) * P * N + static_cast<int64_t>(p) * N;
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                const int n = 16 * i + 4 * g4;
+                const int n = MM::state_row(i, g4);
                 if (n < N) *reinterpret_cast<f4*>(to + n) = hs[i];
             }
         }
-        const int begun = static_cast<int>(sf[4 * Q - 1]) % static_cast<int>(kNotFinite);
-        const bool clean = sf[4 * Q - 1] < kNotFinite;
+        const int marks = marks_of(half);
+        const bool clean = marks < static_cast<int>(kNotFinite);
         if (clean && !mine) continue;
-        // K h^T and Q h^T
+        // straight on without branches, or with what chunks with starts need
+        const auto chunk = [&](auto with_starts) __attribute__((always_inline)) {
+            constexpr bool STARTS = decltype(with_starts)::value;
+            f4 z[RT], y[RT], x[RT];
 #pragma unroll
-        for (int kk = 0; kk < KN; ++kk) {
-            const auto s = MM::template of_tiles<3>(hs, kk);
+            for (int i = 0; i < RT; ++i) z[i] = y[i] = x[i] = f4{0, 0, 0, 0};
+            // K h^T and Q h^T
 #pragma unroll
-            for (int i = 0; i < RT; ++i) {
-                MM::template mac<1, 3>(z[i], MM::template rows<W>(sk, 16 * i, kk, li, g4), s);
-                if (!SAVE) MM::template mac<1, 3>(y[i], MM::template rows<W>(sq, 16 * i, kk, li, g4), s);
+            for (int kk = 0; kk < KN; ++kk) {
+                const auto s = MM::template of_state<3>(hs, kk, g4);
+#pragma unroll
+                for (int i = 0; i < RT; ++i) {
+                    MM::template mac<1, 3>(z[i], MM::template state_rows<W>(sk, 16 * i, kk, li, g4), s);
+                    if (!SAVE) MM::template mac<1, 3>(y[i], MM::template state_rows<W>(half + O::Qq, 16 * i, kk, li, g4), s);
+                }
             }
-        }
-        // Z = V - e^G K h^T, E = T Z
+            // Z = V - e^G K h^T, E = T Z
+            scale_rows<STARTS>(z, sf, 1.0f, g4);
+            if (!SAVE) scale_rows<STARTS>(y, sf, a.scale, g4);
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            const f4 f = *reinterpret_cast<const f4*>(sf + 16 * i + 4 * g4);
+            for (int i = 0; i < RT; ++i) z[i] = MM::template four_rows<64>(half + O::V, 16 * i, w, li, g4) - z[i];
+            kept_apart<STARTS>(x, z, sf + 3 * Q, marks % static_cast<int>(kNotFinite), g4, [&] {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {  // nothing of a state that a start has cut off
-                z[i][e] = v[i][e] - (f[e] != 0.0f ? f[e] * z[i][e] : 0.0f);
-                y[i][e] = f[e] != 0.0f ? f[e] * a.scale * y[i][e] : 0.0f;
+                for (int kk = 0; kk < KT; ++kk) {
+                    const auto s = MM::template of_tiles<3>(z, kk);
+#pragma unroll
+                    for (int i = kk * MM::KB / 16; i < RT; ++i)
+                        MM::template mac<MM::TP, 3>(x[i], frag<MM, MM::TP>(half + O::T, frag_at<MM>(i, kk, false), lane), s);
+                }
+            });
+            if (SAVE) {
+                const Buffer r = token_buffer<float>(keep.e, t0, static_cast<int64_t>(H) * P, static_cast<int64_t>(h) * P, DIRECT ? valid : 1, P);
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int t = 16 * i + 4 * g4 + e;
+                        if (DIRECT) store_at<float>(r, eat + (16 * i + e) * static_cast<uint32_t>(H * P) * 4, x[i][e]);
+                        else if (have && t < valid) keep.e[((t0 + t) * H + h) * P + p] = x[i][e];
+                    }
             }
-        }
-        kept_apart(x, z, sf + 3 * Q, begun, begun, g4, [&] {
+            // U = b E, Y += M U
+            scale_rows<false>(x, sf + 2 * Q, 1.0f, g4);
+            if (!SAVE) {
+#pragma unroll
+                for (int kk = 0; kk < KT; ++kk) {
+                    const auto s = MM::template of_tiles<MP>(x, kk);
+#pragma unroll
+                    for (int i = kk * MM::KB / 16; i < RT; ++i)
+                        MM::template mac<MP, MP>(y[i], frag<MM, MP>(half + O::M, frag_at<MM>(i, kk, false), lane), s);
+                }
+                uint8_t* const to = sm + O::Y + (c & 1) * YB;
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) MM::template put<64>(to, 16 * i + 4 * g4 + e, 16 * w + li, y[i][e]);
+            }
+            // the state after the chunk
+            if (STARTS && !clean) {
+                __syncthreads();
+                clear_rows<MM, W>(sk, sf + Q);
+                __syncthreads();
+            }
+            scale_state<STARTS>(hs, sf[Q - 1]);
+            scale_rows<STARTS>(x, sf + Q, 1.0f, g4);
 #pragma unroll
             for (int kk = 0; kk < KT; ++kk) {
-                const auto s = MM::template of_tiles<3>(z, kk);
+                const auto s = MM::template of_tiles<3>(x, kk);
 #pragma unroll
-                for (int i = kk * MM::KB / 16; i < RT; ++i)
-                    MM::template mac<MM::TP, 3>(x[i], frag<MM, MM::TP>(st, frag_at<MM>(i, kk, false), lane), s);
+                for (int i = 0; i < NT; ++i)
+                    MM::template mac<1, 3>(hs[i], MM::template state_columns<W>(sk, kk * MM::KB, i, li, g4), s);
             }
-        });
-        if (SAVE && have) {
-#pragma unroll
-            for (int i = 0; i < RT; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int t = 16 * i + 4 * g4 + e;
-                    if (t < valid) keep.e[((t0 + t) * H + h) * P + p] = x[i][e];
-                }
-        }
-        // U = b E, Y += M U
-#pragma unroll
-        for (int i = 0; i < RT; ++i) x[i] *= *reinterpret_cast<const f4*>(sf + 2 * Q + 16 * i + 4 * g4);
-        if (!SAVE) {
-#pragma unroll
-            for (int kk = 0; kk < KT; ++kk) {
-                const auto s = MM::template of_tiles<MP>(x, kk);
-#pragma unroll
-                for (int i = kk * MM::KB / 16; i < RT; ++i)
-                    MM::template mac<MP, MP>(y[i], frag<MM, MP>(half + O::M, frag_at<MM>(i, kk, false), lane), s);
-            }
-            const Buffer r = token_buffer<S>(a.y, t0, a.y_row, static_cast<int64_t>(h) * P, DIRECT ? valid : 1, P);
-#pragma unroll
-            for (int i = 0; i < RT; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int t = 16 * i + 4 * g4 + e;
-                    if (DIRECT) store_at<S>(r, yat + (16 * i + e) * static_cast<uint32_t>(a.y_row) * ES, y[i][e]);
-                    else if (have && t < valid) MM::store(static_cast<S*>(a.y) + (t0 + t) * a.y_row + static_cast<int64_t>(h) * P, p, y[i][e]);
-                }
-        }
-        // the state after the chunk
-        if (!clean) {
-            __syncthreads();
-            clear_rows<MM, W>(sk, sf + Q);
-            __syncthreads();
-        }
-        const float through = sf[Q - 1];
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) hs[i][e] = through != 0.0f ? through * hs[i][e] : 0.0f;
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            const f4 f = *reinterpret_cast<const f4*>(sf + Q + 16 * i + 4 * g4);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[i][e] = f[e] != 0.0f ? f[e] * x[i][e] : 0.0f;
-        }
-#pragma unroll
-        for (int kk = 0; kk < KT; ++kk) {
-            const auto s = MM::template of_tiles<3>(x, kk);
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-                MM::template mac<1, 3>(hs[i], MM::template columns<W>(sk, kk * MM::KB, i, li, g4), s);
-        }
+        };
+        if (marks != 0) chunk(std::true_type{});
+        else chunk(std::false_type{});
     }
+    __syncthreads();
     if (!SAVE && a.final_state && have) {
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-            const int n = 16 * i + 4 * g4;
+            const int n = MM::state_row(i, g4);
             if (n < N) *reinterpret_cast<f4*>(a.final_state + state + n) = hs[i];
         }
     }
@@ -515,11 +543,22 @@ hipError_t step_by_width(const DeltaStep& s, hipStream_t stream) {
     return step_of<D, 8, 2>(s, stream);
 }
 
+template <class MM, int NT>
+void prep_of(const DeltaArgs& a, bool bwd, hipStream_t stream) {
+    const unsigned blocks = static_cast<unsigned>(a.B * a.H * a.chunks);
+    if (bwd && a.direct) delta_prep_kernel<MM, NT, true, true><<<blocks, MM::Q * 4, 0, stream>>>(a);
+    else if (bwd) delta_prep_kernel<MM, NT, true, false><<<blocks, MM::Q * 4, 0, stream>>>(a);
+    else if (a.direct) delta_prep_kernel<MM, NT, false, true><<<blocks, MM::Q * 4, 0, stream>>>(a);
+    else delta_prep_kernel<MM, NT, false, false><<<blocks, MM::Q * 4, 0, stream>>>(a);
+}
 template <class MM, int NT, bool SAVE>
 hipError_t walk_of(const DeltaArgs& a, const DeltaSaved& keep, hipStream_t stream) {
+    prep_of<MM, NT>(a, SAVE, stream);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
     const int64_t blocks = a.B * a.H * ((a.P + 63) / 64);
-    if (a.direct) delta_walk_kernel<MM, NT, SAVE, true><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a, keep);
-    else delta_walk_kernel<MM, NT, SAVE, false><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a, keep);
+    if (a.direct) delta_walk_kernel<MM, NT, SAVE, true><<<static_cast<unsigned>(blocks), 320, 0, stream>>>(a, keep);
+    else delta_walk_kernel<MM, NT, SAVE, false><<<static_cast<unsigned>(blocks), 320, 0, stream>>>(a, keep);
     return hipGetLastError();
 }
 template <class MM, bool SAVE>
@@ -529,25 +568,15 @@ hipError_t walk_by_width(const DeltaArgs& a, const DeltaSaved& keep, hipStream_t
     return walk_of<MM, 16, SAVE>(a, keep, stream);
 }
 template <class MM>
-hipError_t fwd_of(DeltaArgs a, void* workspace, ssm_dtype_t dtype, hipStream_t stream) {
+hipError_t fwd_of(DeltaArgs a, void* workspace, hipStream_t stream) {
     place_chunks<MM>(a, static_cast<uint8_t*>(workspace), false);
     constexpr size_t es = sizeof(typename MM::S);
-    a.direct = a.N % (16 / es) == 0 && direct_rows_fit(a.q, a.q_row, es, true) && direct_rows_fit(a.k, a.k_row, es, true) &&
-               direct_rows_fit(a.v, a.v_row, es, false) && direct_rows_fit(a.y, a.y_row, es, false);
-    const hipError_t e = launch_delta_prep(a, dtype, false, stream);
-    return e != hipSuccess ? e : walk_by_width<MM, false>(a, DeltaSaved{}, stream);
+    a.direct = a.N % (16 / es) == 0 && a.P % (16 / es) == 0 && direct_rows_fit(a.q, a.q_row, es) &&
+               direct_rows_fit(a.k, a.k_row, es) && direct_rows_fit(a.v, a.v_row, es) && direct_rows_fit(a.y, a.y_row, es);
+    return walk_by_width<MM, false>(a, DeltaSaved{}, stream);
 }
 
 }  // namespace
-
-hipError_t launch_delta_prep(const DeltaArgs& a, ssm_dtype_t dtype, bool bwd, hipStream_t stream) {
-    const unsigned blocks = static_cast<unsigned>(a.B * a.H * a.chunks);
-    if (dtype == SSM_BF16 && bwd) delta_prep_kernel<ByBf16, true><<<blocks, 256, 0, stream>>>(a);
-    else if (dtype == SSM_BF16) delta_prep_kernel<ByBf16, false><<<blocks, 256, 0, stream>>>(a);
-    else if (bwd) delta_prep_kernel<ByF32, true><<<blocks, 128, 0, stream>>>(a);
-    else delta_prep_kernel<ByF32, false><<<blocks, 128, 0, stream>>>(a);
-    return hipGetLastError();
-}
 
 hipError_t launch_delta_walk_saved(const DeltaArgs& a, const DeltaSaved& s, ssm_dtype_t dtype, hipStream_t stream) {
     return dtype == SSM_BF16 ? walk_by_width<ByBf16, true>(a, s, stream) : walk_by_width<ByF32, true>(a, s, stream);
@@ -562,7 +591,7 @@ size_t delta_fwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t P, int
 }
 
 hipError_t launch_delta_fwd(DeltaArgs a, void* workspace, ssm_dtype_t dtype, hipStream_t stream) {
-    return dtype == SSM_BF16 ? fwd_of<ByBf16>(a, workspace, dtype, stream) : fwd_of<ByF32>(a, workspace, dtype, stream);
+    return dtype == SSM_BF16 ? fwd_of<ByBf16>(a, workspace, stream) : fwd_of<ByF32>(a, workspace, stream);
 }
 
 hipError_t launch_delta_step(const DeltaStep& s, ssm_dtype_t dtype, hipStream_t stream) {

@@ -13,6 +13,8 @@
 //   delta_back   from the last chunk to the first: dh before every chunk, dZ, and of the channels'
 //                sums dU . E and e^{G_Q - G} (K dh^T) . U; laid out as the walk
 //   delta_grad   one block a chunk and key head (and range of its heads): the rest
+#include <type_traits>
+
 #include "delta.h"
 
 namespace ssm {
@@ -42,228 +44,213 @@ __device__ __forceinline__ float sum_groups(float v) {  // over the four lanes t
 }
 __device__ __forceinline__ f4 row4(const float* p) { return lds<f4>(reinterpret_cast<const uint8_t*>(p)); }
 
+// Laid out as the walk (delta.hip), from the last chunk to the first; E comes and dZ goes by the wavefronts
+// that use them (LDS is full).
 template <class MM, int NT>
 struct BackLds {
-    static constexpr int W = 16 * NT, MP = m_parts<MM>(true);
-    static constexpr int K = 0, T = K + staged_bytes<MM, W>(), F = T + image_bytes<MM>(MM::TP), Qq = F + 1024,
-                         M = Qq + staged_bytes<MM, W>(), BYTES = M + image_bytes<MM>(MP);
-    static constexpr int HALVES = NT <= 8 ? 2 : 1;
+    static constexpr int W = 16 * NT, MP = m_parts<MM>(true), HALVES = NT <= 8 ? 2 : 1;
+    static constexpr int V = 0, K = V + staged_bytes<MM, 64>(), T = K + staged_bytes<MM, W>(), F = T + image_bytes<MM>(MM::TP),
+                         Qq = F + 1024, M = Qq + staged_bytes<MM, W>(), HALF = M + image_bytes<MM>(MP);
 };
 
-// Laid out, fetched and, with and without DIRECT, addressed as the walk (delta.hip), from the last chunk
-// to the first.
 template <class MM, int NT, bool DIRECT>
-__global__ __launch_bounds__(256) void delta_back_kernel(DeltaArgs a, Buffers u) {
+__global__ __launch_bounds__(320) void delta_back_kernel(DeltaArgs a, Buffers u) {
     using S = typename MM::S;
     using O = BackLds<MM, NT>;
-    constexpr int Q = MM::Q, RT = Q / 16, KT = Q / MM::KB, W = 16 * NT, KN = W / MM::KB, MP = O::MP, ES = sizeof(S);
-    __shared__ __attribute__((aligned(1024))) uint8_t sm[O::HALVES * O::BYTES];
-    const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g4 = lane >> 4;
-    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    constexpr int Q = MM::Q, RT = Q / 16, KT = Q / MM::KB, W = 16 * NT, KN = W / MM::KB, MP = O::MP;
+    __shared__ __attribute__((aligned(1024))) uint8_t sm[O::HALVES * O::HALF];
+    const int lane = threadIdx.x & 63, li = lane & 15, g4 = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int H = static_cast<int>(a.H), P = static_cast<int>(a.P), N = static_cast<int>(a.N);
     const int pblocks = (P + 63) / 64, ptiles = (P + 15) / 16;
     const int unit = xcd_order(blockIdx.x, gridDim.x);
     const int pb = unit % pblocks, bh = unit / pblocks, h = bh % H, b = bh / H;
     const int g = h / (H / static_cast<int>(a.G));
-    const int p0 = 64 * pb + 16 * w, p = p0 + li;
-    const bool mine = p0 < P, have = p < P;
     const int chunks = static_cast<int>(a.chunks);
-    const int64_t state = (static_cast<int64_t>(bh) * P + p) * N, erow = static_cast<int64_t>(H) * P;
-    const uint32_t dyat = have ? 4 * g4 * static_cast<uint32_t>(a.dy_row) * ES + p * ES : kOutside;
-    const uint32_t dvat = have ? 4 * g4 * static_cast<uint32_t>(a.dv_row) * ES + p * ES : kOutside;
-    const uint32_t eat = have ? 4 * g4 * static_cast<uint32_t>(erow) * 4 + p * 4 : kOutside;
     const auto rows_of = [&](int c) {
         const int64_t left = a.L - static_cast<int64_t>(c) * Q;
         return static_cast<int>(left < Q ? left : Q);
     };
-    const auto fetch = [&](int c, uint8_t* half) {
-        const int64_t t0 = b * a.L + static_cast<int64_t>(c) * Q, image = static_cast<int64_t>(bh) * chunks + c;
-        const int valid = rows_of(c);
-        if (DIRECT) {
-            direct_rows<MM, W>(half + O::K, token_buffer<S>(a.k, t0, a.k_row, g * N, valid, N), static_cast<int>(a.k_row), N, w, lane);
-            direct_rows<MM, W>(half + O::Qq, token_buffer<S>(a.q, t0, a.q_row, g * N, valid, N), static_cast<int>(a.q_row), N, w, lane);
-        } else {
-            stage_rows<MM, W, 256>(half + O::K, static_cast<const S*>(a.k) + t0 * a.k_row + g * N, a.k_row, valid, N);
-            stage_rows<MM, W, 256>(half + O::Qq, static_cast<const S*>(a.q) + t0 * a.q_row + g * N, a.q_row, valid, N);
-        }
-        direct_image<image_bytes<MM>(MM::TP)>(half + O::T, a.Tt + image * image_bytes<MM>(MM::TP), w, lane);
-        direct_image<image_bytes<MM>(MP)>(half + O::M, a.M + image * image_bytes<MM>(MP), w, lane);
-        direct_image<kFactors * Q * 4>(half + O::F, reinterpret_cast<const uint8_t*>(a.factors + image * kFactors * Q), w, lane);
+    const auto half_of = [&](int c) { return sm + (O::HALVES == 2 ? (c & 1) * O::HALF : 0); };
+    const auto marks_of = [&](const uint8_t* half) {
+        return __builtin_amdgcn_readfirstlane(static_cast<int>(reinterpret_cast<const float*>(half + O::F)[4 * Q - 1]));
     };
-    S dyn[RT][4];  // the next chunk's dY and E
-    float en[RT][4];
-    const auto fetch_values = [&](int c) {
+
+    if (w == 4) {
+        const int64_t col = static_cast<int64_t>(h) * P + 64 * pb;
+        const int width = P - 64 * pb < 64 ? P - 64 * pb : 64;
+        const auto fetch = [&](int c) {
+            uint8_t* const half = half_of(c);
+            const int64_t t0 = b * a.L + static_cast<int64_t>(c) * Q, image = static_cast<int64_t>(bh) * chunks + c;
+            const int valid = rows_of(c);
+            if (DIRECT) {
+                direct_rows<MM, W, true>(half + O::K, token_buffer<S>(a.k, t0, a.k_row, g * N, valid, N), static_cast<int>(a.k_row), N, lane);
+                direct_rows<MM, W, true>(half + O::Qq, token_buffer<S>(a.q, t0, a.q_row, g * N, valid, N), static_cast<int>(a.q_row), N, lane);
+                direct_rows<MM, 64, false>(half + O::V, token_buffer<S>(a.dy, t0, a.dy_row, col, valid, width), static_cast<int>(a.dy_row), width, lane);
+            } else {
+                stage_rows<MM, W, 64, true>(half + O::K, static_cast<const S*>(a.k) + t0 * a.k_row + g * N, a.k_row, valid, N);
+                stage_rows<MM, W, 64, true>(half + O::Qq, static_cast<const S*>(a.q) + t0 * a.q_row + g * N, a.q_row, valid, N);
+                stage_elements<MM, 64>(half + O::V, static_cast<const S*>(a.dy) + t0 * a.dy_row + col, a.dy_row, valid, width);
+            }
+            direct_image<image_bytes<MM>(MM::TP)>(half + O::T, a.Tt + image * image_bytes<MM>(MM::TP), lane);
+            direct_image<image_bytes<MM>(MP)>(half + O::M, a.M + image * image_bytes<MM>(MP), lane);
+            direct_image<kFactors * Q * 4>(half + O::F, reinterpret_cast<const uint8_t*>(a.factors + image * kFactors * Q), lane);
+        };
+        if (O::HALVES == 2) fetch(chunks - 1);
+        for (int c = chunks - 1; c >= 0; --c) {
+            if (O::HALVES == 1) {
+                __syncthreads();
+                fetch(c);
+            }
+            wait_loads();
+            __syncthreads();
+            if (O::HALVES == 2 && c > 0) fetch(c - 1);
+            if (marks_of(half_of(c)) >= static_cast<int>(kNotFinite)) {
+                __syncthreads();
+                __syncthreads();
+            }
+        }
+        return;
+    }
+
+    const int p0 = 64 * pb + 16 * w, p = p0 + li;
+    const bool mine = p0 < P, have = p < P;
+    const int64_t state = (static_cast<int64_t>(bh) * P + p) * N, erow = static_cast<int64_t>(H) * P;
+    const uint32_t eat = have ? 4 * g4 * static_cast<uint32_t>(erow) * 4 + p * 4 : kOutside;
+    float en[RT][4];  // the next chunk's E
+    const auto fetch_e = [&](int c) {
         const int64_t t0 = b * a.L + static_cast<int64_t>(c) * Q;
         const int valid = rows_of(c);
-        const Buffer ry = token_buffer<S>(a.dy, t0, a.dy_row, static_cast<int64_t>(h) * P, DIRECT ? valid : 1, P);
         const Buffer re = token_buffer<float>(u.saved.e, t0, erow, static_cast<int64_t>(h) * P, DIRECT ? valid : 1, P);
 #pragma unroll
         for (int i = 0; i < RT; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                if (DIRECT) {
-                    dyn[i][e] = load_at<S>(ry, dyat + (16 * i + e) * static_cast<uint32_t>(a.dy_row) * ES);
-                    en[i][e] = load_at<float>(re, eat + (16 * i + e) * static_cast<uint32_t>(erow) * 4);
-                } else {
-                    const int t = 16 * i + 4 * g4 + e;
-                    dyn[i][e] = S{0};
-                    en[i][e] = 0.0f;
-                    if (have && t < valid) {
-                        dyn[i][e] = static_cast<const S*>(a.dy)[(t0 + t) * a.dy_row + static_cast<int64_t>(h) * P + p];
-                        en[i][e] = u.saved.e[(t0 + t) * erow + static_cast<int64_t>(h) * P + p];
-                    }
-                }
+                const int t = 16 * i + 4 * g4 + e;
+                if (DIRECT) en[i][e] = load_at<float>(re, eat + (16 * i + e) * static_cast<uint32_t>(erow) * 4);
+                else en[i][e] = have && t < valid ? u.saved.e[(t0 + t) * erow + static_cast<int64_t>(h) * P + p] : 0.0f;
             }
     };
     f4 dh[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-        const int n = 16 * i + 4 * g4;
+        const int n = MM::state_row(i, g4);
         dh[i] = have && n < N && a.dhT ? *reinterpret_cast<const f4*>(a.dhT + state + n) : f4{0, 0, 0, 0};
     }
-    if (O::HALVES == 2) fetch(chunks - 1, sm + ((chunks - 1) & 1) * O::BYTES);
-    fetch_values(chunks - 1);
+    fetch_e(chunks - 1);
     for (int c = chunks - 1; c >= 0; --c) {
         const int64_t t0 = b * a.L + static_cast<int64_t>(c) * Q, image = static_cast<int64_t>(bh) * chunks + c;
         const int valid = rows_of(c);
-        uint8_t* const half = O::HALVES == 2 ? sm + (c & 1) * O::BYTES : sm;
-        if (O::HALVES == 1) {
-            __syncthreads();
-            fetch(c, half);
-        }
-        wait_loads();
+        uint8_t* const half = half_of(c);
+        if (O::HALVES == 1) __syncthreads();
         __syncthreads();
-        f4 dy[RT], ev[RT], du[RT], dz[RT];
+        f4 ev[RT];
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            du[i] = dz[i] = f4{0, 0, 0, 0};
+        for (int i = 0; i < RT; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                dy[i][e] = value_of(dyn[i][e]);
-                ev[i][e] = en[i][e];
-            }
-        }
-        if (c > 0) {
-            if (O::HALVES == 2) fetch(c - 1, sm + ((c - 1) & 1) * O::BYTES);
-            fetch_values(c - 1);
-        }
+            for (int e = 0; e < 4; ++e) ev[i][e] = en[i][e];
+        if (c > 0) fetch_e(c - 1);
         if (have) {
             float* to = u.grads + image * P * N + static_cast<int64_t>(p) * N;
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                const int n = 16 * i + 4 * g4;
+                const int n = MM::state_row(i, g4);
                 if (n < N) *reinterpret_cast<f4*>(to + n) = dh[i];
             }
         }
         uint8_t* const sk = half + O::K;
         uint8_t* const sq = half + O::Qq;
         const float* const sf = reinterpret_cast<const float*>(half + O::F);
-        const int begun = static_cast<int>(sf[4 * Q - 1]) % static_cast<int>(kNotFinite);
-        const bool clean = sf[4 * Q - 1] < kNotFinite;
+        const int marks = marks_of(half);
+        const bool clean = marks < static_cast<int>(kNotFinite);
         if (clean && !mine) continue;
-        // e^{G_Q - G} K dh^T, and its products with U
+        const auto chunk = [&](auto with_starts) __attribute__((always_inline)) {
+            constexpr bool STARTS = decltype(with_starts)::value;
+            f4 du[RT], dz[RT], dy[RT];
 #pragma unroll
-        for (int kk = 0; kk < KN; ++kk) {
-            const auto s = MM::template of_tiles<3>(dh, kk);
-#pragma unroll
-            for (int i = 0; i < RT; ++i) MM::template mac<1, 3>(du[i], MM::template rows<W>(sk, 16 * i, kk, li, g4), s);
-        }
-        float* part = u.part + (image * ptiles + p0 / 16) * 2 * Q;
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            const f4 f = row4(sf + Q + 16 * i + 4 * g4), be = row4(sf + 2 * Q + 16 * i + 4 * g4);
-            f4 v;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                du[i][e] = f[e] != 0.0f ? f[e] * du[i][e] : 0.0f;
-                v[e] = sum16(du[i][e] * ev[i][e] * be[e]);
+            for (int i = 0; i < RT; ++i) {
+                du[i] = dz[i] = f4{0, 0, 0, 0};
+                dy[i] = MM::template four_rows<64>(half + O::V, 16 * i, w, li, g4);
             }
-            if (mine && li == 0) *reinterpret_cast<f4*>(part + Q + 16 * i + 4 * g4) = v;
-        }
-        // dU += M^T dY
-        kept_apart(du, dy, sf + 3 * Q, begun, 0, g4, [&] {
+            // e^{G_Q - G} K dh^T, and its products with U
 #pragma unroll
-            for (int kk = 0; kk < KT; ++kk) {
-                const auto s = MM::template of_tiles<1>(dy, kk);
+            for (int kk = 0; kk < KN; ++kk) {
+                const auto s = MM::template of_state<3>(dh, kk, g4);
 #pragma unroll
-                for (int i = 0; i < (kk + 1) * MM::KB / 16; ++i)
-                    MM::template mac<MP, 1>(du[i], frag<MM, MP>(half + O::M, frag_at<MM>(i, kk, true), lane), s);
+                for (int i = 0; i < RT; ++i) MM::template mac<1, 3>(du[i], MM::template state_rows<W>(sk, 16 * i, kk, li, g4), s);
             }
-        });
+            float* part = u.part + (image * ptiles + p0 / 16) * 2 * Q + 4 * g4 + li;
+            scale_rows<STARTS>(du, sf + Q, 1.0f, g4);
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            const f4 be = row4(sf + 2 * Q + 16 * i + 4 * g4);
-            f4 v;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[e] = sum16(du[i][e] * ev[i][e]);
-                du[i][e] *= be[e];
+            for (int i = 0; i < RT; ++i) {
+                const f4 v = du[i] * ev[i] * row4(sf + 2 * Q + 16 * i + 4 * g4);
+                const float s = row_sums({v[0], v[1], v[2], v[3]}, li);
+                if (mine && li < 4) part[Q + 16 * i] = s;
             }
-            if (mine && li == 0) *reinterpret_cast<f4*>(part + 16 * i + 4 * g4) = v;
-        }
-        // dZ = T^T (b dU)
-        kept_apart(dz, du, sf + 3 * Q, begun, 0, g4, [&] {
+            // dU += M^T dY
+            kept_apart<STARTS>(du, dy, sf + 3 * Q, 0, g4, [&] {
 #pragma unroll
-            for (int kk = 0; kk < KT; ++kk) {
-                const auto s = MM::template of_tiles<3>(du, kk);
+                for (int kk = 0; kk < KT; ++kk) {
+                    const auto s = MM::template of_tiles<1>(dy, kk);
 #pragma unroll
-                for (int i = 0; i < (kk + 1) * MM::KB / 16; ++i)
-                    MM::template mac<MM::TP, 3>(dz[i], frag<MM, MM::TP>(half + O::T, frag_at<MM>(i, kk, true), lane), s);
+                    for (int i = 0; i < (kk + 1) * MM::KB / 16; ++i)
+                        MM::template mac<MP, 1>(du[i], frag<MM, MP>(half + O::M, frag_at<MM>(i, kk, true), lane), s);
+                }
+            });
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                const f4 v = du[i] * ev[i];
+                const float s = row_sums({v[0], v[1], v[2], v[3]}, li);
+                if (mine && li < 4) part[16 * i] = s;
             }
-        });
-        {
+            // dZ = T^T (b dU)
+            scale_rows<false>(du, sf + 2 * Q, 1.0f, g4);
+            kept_apart<STARTS>(dz, du, sf + 3 * Q, 0, g4, [&] {
+#pragma unroll
+                for (int kk = 0; kk < KT; ++kk) {
+                    const auto s = MM::template of_tiles<3>(du, kk);
+#pragma unroll
+                    for (int i = 0; i < (kk + 1) * MM::KB / 16; ++i)
+                        MM::template mac<MM::TP, 3>(dz[i], frag<MM, MM::TP>(half + O::T, frag_at<MM>(i, kk, true), lane), s);
+                }
+            });
             const Buffer rz = token_buffer<float>(u.dz, t0, erow, static_cast<int64_t>(h) * P, DIRECT ? valid : 1, P);
-            const Buffer rv = token_buffer<S>(a.dv, t0, a.dv_row, static_cast<int64_t>(h) * P, DIRECT ? valid : 1, P);
 #pragma unroll
             for (int i = 0; i < RT; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int t = 16 * i + 4 * g4 + e;
-                    if (DIRECT) {
-                        store_at<float>(rz, eat + (16 * i + e) * static_cast<uint32_t>(erow) * 4, dz[i][e]);
-                        store_at<S>(rv, dvat + (16 * i + e) * static_cast<uint32_t>(a.dv_row) * ES, dz[i][e]);
-                    } else if (have && t < valid) {
-                        u.dz[(t0 + t) * erow + static_cast<int64_t>(h) * P + p] = dz[i][e];
-                        MM::store(static_cast<S*>(a.dv) + (t0 + t) * a.dv_row + static_cast<int64_t>(h) * P, p, dz[i][e]);
-                    }
+                    if (DIRECT) store_at<float>(rz, eat + (16 * i + e) * static_cast<uint32_t>(erow) * 4, dz[i][e]);
+                    else if (have && t < valid) u.dz[(t0 + t) * erow + static_cast<int64_t>(h) * P + p] = dz[i][e];
                 }
-        }
-        // the gradient of the state before the chunk
-        if (!clean) {
-            __syncthreads();
-            clear_rows<MM, W>(sk, sf);
-            clear_rows<MM, W>(sq, sf);
-            __syncthreads();
-        }
-        const float through = sf[Q - 1];
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) dh[i][e] = through != 0.0f ? through * dh[i][e] : 0.0f;
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            const f4 f = row4(sf + 16 * i + 4 * g4);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                dy[i][e] = f[e] != 0.0f ? f[e] * a.scale * dy[i][e] : 0.0f;
-                dz[i][e] = f[e] != 0.0f ? -f[e] * dz[i][e] : 0.0f;
+            // the gradient of the state before the chunk
+            if (STARTS && !clean) {
+                __syncthreads();
+                clear_rows<MM, W>(sk, sf);
+                clear_rows<MM, W>(sq, sf);
+                __syncthreads();
             }
-        }
+            scale_state<STARTS>(dh, sf[Q - 1]);
+            scale_rows<STARTS>(dy, sf, a.scale, g4);
+            scale_rows<STARTS>(dz, sf, -1.0f, g4);
 #pragma unroll
-        for (int kk = 0; kk < KT; ++kk) {
-            const auto sy = MM::template of_tiles<3>(dy, kk);
-            const auto sz = MM::template of_tiles<3>(dz, kk);
+            for (int kk = 0; kk < KT; ++kk) {
+                const auto sy = MM::template of_tiles<3>(dy, kk);
+                const auto sz = MM::template of_tiles<3>(dz, kk);
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                MM::template mac<1, 3>(dh[i], MM::template columns<W>(sq, kk * MM::KB, i, li, g4), sy);
-                MM::template mac<1, 3>(dh[i], MM::template columns<W>(sk, kk * MM::KB, i, li, g4), sz);
+                for (int i = 0; i < NT; ++i) {
+                    MM::template mac<1, 3>(dh[i], MM::template state_columns<W>(sq, kk * MM::KB, i, li, g4), sy);
+                    MM::template mac<1, 3>(dh[i], MM::template state_columns<W>(sk, kk * MM::KB, i, li, g4), sz);
+                }
             }
-        }
+        };
+        if (marks != 0) chunk(std::true_type{});
+        else chunk(std::false_type{});
     }
     if (a.dh0 && have) {
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-            const int n = 16 * i + 4 * g4;
+            const int n = MM::state_row(i, g4);
             if (n < N) *reinterpret_cast<f4*>(a.dh0 + state + n) = dh[i];
         }
     }
@@ -290,6 +277,19 @@ __device__ __forceinline__ void load_values(const typename MM::S* p, int n, floa
     } else {
 #pragma unroll
         for (int j = 0; j < MM::R; ++j) v[j] = j < n ? MM::value(p, j) : 0.0f;
+    }
+}
+template <class MM>
+__device__ __forceinline__ void store_values(typename MM::S* p, int n, const float (&v)[MM::R]) {
+    if (n >= MM::R) {
+        if constexpr (MM::R == 8)
+            *reinterpret_cast<u4any*>(p) = u4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+        else
+            *reinterpret_cast<u4any4*>(p) = __builtin_bit_cast(u4, f4{v[0], v[1], v[2], v[3]});
+    } else {
+#pragma unroll
+        for (int j = 0; j < MM::R; ++j)
+            if (j < n) MM::store(p, j, v[j]);
     }
 }
 template <int R>
@@ -373,8 +373,8 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a, Buffers u)
     const int N = static_cast<int>(a.N), P = static_cast<int>(a.P);
     const int64_t t0 = b * a.L + c * Q;
 
-    stage_rows<MM, W, 512>(sk, static_cast<const S*>(a.k) + t0 * a.k_row + g * a.N, a.k_row, valid, N);
-    stage_rows<MM, W, 512>(sq, static_cast<const S*>(a.q) + t0 * a.q_row + g * a.N, a.q_row, valid, N);
+    stage_rows<MM, W, 512, false>(sk, static_cast<const S*>(a.k) + t0 * a.k_row + g * a.N, a.k_row, valid, N);
+    stage_rows<MM, W, 512, false>(sq, static_cast<const S*>(a.q) + t0 * a.q_row + g * a.N, a.q_row, valid, N);
     f4 dq[RW][CT], dk[RW][CT];
 #pragma unroll
     for (int i = 0; i < RW; ++i)
@@ -411,6 +411,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a, Buffers u)
                 const int64_t at = ((t0 + r) * a.H + h) * a.P + p0 + R * q;
                 load_floats<R>(u.dz + at, left, v);
                 put_parts<MM, 64, TP>(tz, QP, r, q, v);
+                store_values<MM>(static_cast<S*>(a.dv) + (t0 + r) * a.dv_row + h * a.P + p0 + R * q, left, v);
                 load_floats<R>(u.saved.e + at, left, v);
                 put_parts<MM, 64, TP>(te, QP, r, q, v);
             }
@@ -668,8 +669,8 @@ size_t place(DeltaArgs& a, Buffers& u, uint8_t* ws) {
 template <class MM, int NT>
 hipError_t kernels_of(const DeltaArgs& a, const Buffers& u, hipStream_t stream) {
     const unsigned blocks = static_cast<unsigned>(a.B * a.H * ((a.P + 63) / 64));
-    if (a.direct) delta_back_kernel<MM, NT, true><<<blocks, 256, 0, stream>>>(a, u);
-    else delta_back_kernel<MM, NT, false><<<blocks, 256, 0, stream>>>(a, u);
+    if (a.direct) delta_back_kernel<MM, NT, true><<<blocks, 320, 0, stream>>>(a, u);
+    else delta_back_kernel<MM, NT, false><<<blocks, 320, 0, stream>>>(a, u);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     delta_grad_kernel<MM, NT><<<static_cast<unsigned>(a.B * a.chunks * a.G * u.splits), 512, 0, stream>>>(a, u);
@@ -683,11 +684,10 @@ hipError_t bwd_of(DeltaArgs a, void* workspace, ssm_dtype_t dtype, hipStream_t s
     Buffers u{};
     place<MM>(a, u, static_cast<uint8_t*>(workspace));
     constexpr size_t es = sizeof(typename MM::S);
-    a.direct = a.N % (16 / es) == 0 && direct_rows_fit(a.q, a.q_row, es, true) && direct_rows_fit(a.k, a.k_row, es, true) &&
-               direct_rows_fit(a.v, a.v_row, es, false) && direct_rows_fit(a.dy, a.dy_row, es, false) &&
-               direct_rows_fit(a.dv, a.dv_row, es, false) && direct_rows_fit(nullptr, a.H * a.P, 4, false);
-    hipError_t e = launch_delta_prep(a, dtype, true, stream);
-    if (e == hipSuccess) e = launch_delta_walk_saved(a, u.saved, dtype, stream);
+    a.direct = a.N % (16 / es) == 0 && a.P % (16 / es) == 0 && direct_rows_fit(a.q, a.q_row, es) &&
+               direct_rows_fit(a.k, a.k_row, es) && direct_rows_fit(a.v, a.v_row, es) && direct_rows_fit(a.dy, a.dy_row, es) &&
+               direct_rows_fit(nullptr, a.H * a.P, 4);
+    const hipError_t e = launch_delta_walk_saved(a, u.saved, dtype, stream);
     if (e != hipSuccess) return e;
     if (a.N <= 64) return kernels_of<MM, 4>(a, u, stream);
     if (a.N <= 128) return kernels_of<MM, 8>(a, u, stream);

@@ -91,5 +91,17 @@ __device__ __forceinline__ bf8 down(const uint8_t* tile, int lane_off, int r0, i
     return join(tr_read(p), tr_read(p + 16 * RB));
 }
 
+// Sums over the 16 lanes that share g4, of four values at once: lane li holds that of v[li % 4].
+__device__ __forceinline__ float row_sums(const float (&v)[4], int li) {
+    const float k01 = li & 1 ? v[1] : v[0], s01 = li & 1 ? v[0] : v[1];
+    const float k23 = li & 1 ? v[3] : v[2], s23 = li & 1 ? v[2] : v[3];
+    const float a = k01 + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(s01), 0xB1, 0xf, 0xf, true));
+    const float b = k23 + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(s23), 0xB1, 0xf, 0xf, true));
+    const float k = li & 2 ? b : a, o = li & 2 ? a : b;
+    float r = k + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(o), 0x4E, 0xf, 0xf, true));
+    r += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(r), 0x124, 0xf, 0xf, true));         // rotated by 4
+    return r + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(r), 0x128, 0xf, 0xf, true));   // by 8
+}
+
 }  // namespace
 }  // namespace ssm
