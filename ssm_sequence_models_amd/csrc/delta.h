@@ -51,6 +51,7 @@ struct DeltaArgs {
     uint8_t* T;      // [B, H, chunks] images
     uint8_t* M;
     uint8_t* Tt;     // transposed, backward only (M is transposed there)
+    double* gates;   // [B, H, chunks, Q]: sums of gates from the chunk's start on, backward only
     float* factors;  // [B, H, chunks, kFactors, Q]: e^G from the chunk's start, e^{G_Q - G}, beta, sequences begun
 };
 
@@ -543,7 +544,9 @@ size_t place_chunks(DeltaArgs& a, uint8_t* ws, bool bwd) {
     a.Tt = ws + at;
     if (bwd) at += n * image_bytes<MM>(MM::TP);
     a.factors = reinterpret_cast<float*>(ws + at);
-    return at + n * kFactors * MM::Q * 4;
+    at += n * kFactors * MM::Q * 4;
+    a.gates = reinterpret_cast<double*>(ws + at);
+    return at + (bwd ? n * MM::Q * 8 : 0);
 }
 
 }  // namespace delta

@@ -57,6 +57,7 @@ __global__ __launch_bounds__(MM::Q * 4) void delta_prep_kernel(DeltaArgs a) {
             f[Q + lane] = s.starts == rend ? exp_of(end - s.gates) : 0.0f;
             f[2 * Q + lane] = s.beta;
             f[3 * Q + lane] = static_cast<float>(s.starts);
+            if (BWD) a.gates[image * Q + lane] = s.gates;
         }
     }
     // products of the rows 16 w ..; rows behind the row's end are 0

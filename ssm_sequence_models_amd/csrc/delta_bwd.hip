@@ -12,7 +12,9 @@
 //   delta_walk   (delta.hip) along the rows again: the state before every chunk, and E
 //   delta_back   from the last chunk to the first: dh before every chunk, dZ, and of the channels'
 //                sums dU . E and e^{G_Q - G} (K dh^T) . U; laid out as the walk
-//   delta_grad   one block a chunk and key head (and range of its heads): the rest
+//   delta_grad   one block a chunk and key head (and range of its heads): dQ, dK, and of dbeta and dgate
+//                what the pairs and the states give
+//   delta_gate   a wavefront a chunk and head: dbeta, and dgate's sums along the chunk
 #include <type_traits>
 
 #include "delta.h"
@@ -27,6 +29,7 @@ struct Buffers {
     float* grads;  // [B, H, chunks, P, N]: the gradient of the state after each chunk
     float* dz;     // [B, L, H, P]
     float* part;   // [B, H, chunks, 16-channel tiles, 2, Q]
+    float* gate;   // [B, H, chunks, 4, Q]: for dgate and dbeta, what delta_gate sums over a chunk's tokens
     float* dqk;    // [2, splits, B, L, G, N] where the heads of a key head are split
     int64_t splits, heads;  // ranges of a key head's heads, and heads in each
 };
@@ -346,9 +349,8 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a, Buffers u)
     __shared__ __attribute__((aligned(16))) uint8_t sk[QN];
     __shared__ __attribute__((aligned(16))) uint8_t sq[QN];
     __shared__ __attribute__((aligned(16))) uint8_t pool[LOADS > PAIRS ? LOADS : PAIRS];
-    __shared__ __attribute__((aligned(16))) float sf[kFactors * Q];
+    __shared__ __attribute__((aligned(16))) float sf[kFactors * Q];  // plane 3: sequences begun
     __shared__ double sg[Q];
-    __shared__ int sr[Q];
     __shared__ float sdb[RT][Q];    // sums over t of pairs, by row tiles
     __shared__ float sc[CG][Q];     // products with h_0, by column groups
     __shared__ float sspan[Q];
@@ -381,10 +383,49 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a, Buffers u)
 #pragma unroll
         for (int j = 0; j < CT; ++j) dq[i][j] = dk[i][j] = f4{0, 0, 0, 0};
 
-    for (int64_t h = g * rep + split * u.heads; h < h1; ++h) {
+    // what a thread stages of 64 channels of a head, and what a lane takes of h_0 and dh, are loaded
+    // one block of channels ahead
+    const int srow = static_cast<int>(threadIdx.x) / (64 / R), sq8 = threadIdx.x % (64 / R);
+    static_assert(Q * 64 / R == 512, "one piece a thread");
+    float ny[R], nz[R], ne[R];
+    float ns[KP][CT][R], nd[KP][CT][R];
+    const auto load_tokens = [&](int64_t h, int p0) {
+        const int left = srow < valid ? P - p0 - R * sq8 : 0;
+        const int64_t at = ((t0 + srow) * a.H + h) * a.P + p0 + R * sq8;
+        load_values<MM>(static_cast<const S*>(a.dy) + (t0 + srow) * a.dy_row + h * a.P + p0 + R * sq8, left, ny);
+        load_floats<R>(u.dz + at, left, nz);
+        load_floats<R>(u.saved.e + at, left, ne);
+    };
+    const auto load_states = [&](int64_t h, int p0) {
         const int64_t image = (b * a.H + h) * a.chunks + c;
-        const float* states = u.saved.states + image * a.P * a.N;
-        const float* grads = u.grads + image * a.P * a.N;
+        const Buffer rs = buffer(u.saved.states + image * P * N, static_cast<int64_t>(P) * N * 4);
+        const Buffer rd = buffer(u.grads + image * P * N, static_cast<int64_t>(P) * N * 4);
+#pragma unroll
+        for (int kk = 0; kk < KP; ++kk)
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+                const int n = 16 * (cg * CT + j) + li;
+                const uint32_t at = n < N ? ((p0 + MM::KB * kk + R * g4) * N + n) * 4 : kOutside;
+#pragma unroll
+                for (int m = 0; m < R; ++m) {
+                    ns[kk][j][m] = load_at<float>(rs, at + m * N * 4);
+                    nd[kk][j][m] = load_at<float>(rd, at + m * N * 4);
+                }
+            }
+    };
+    float nf = 0.0f;
+    double ng = 0.0;
+    const auto load_factors = [&](int64_t h) {
+        const int64_t image = (b * a.H + h) * a.chunks + c;
+        if (tid < kFactors * Q) nf = a.factors[image * kFactors * Q + tid];
+        if (tid < Q) ng = a.gates[image * Q + tid];
+    };
+    const int64_t h0 = g * rep + split * u.heads;
+    load_factors(h0);
+    load_tokens(h0, 0);
+    load_states(h0, 0);
+    for (int64_t h = h0; h < h1; ++h) {
+        const int64_t image = (b * a.H + h) * a.chunks + c;
         f4 qo[RW][CT], ko[RW][CT], ke[RW][CT], dm[MINE], db[MINE];
 #pragma unroll
         for (int i = 0; i < RW; ++i)
@@ -395,45 +436,31 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a, Buffers u)
         float dot = 0.0f;
         for (int p0 = 0; p0 < P; p0 += 64) {
             __syncthreads();
-            if (p0 == 0 && w == 0) {
-                const TokenSums s = token_sums<Q>(a, b, h, c * Q, valid, lane);
-                if (lane < Q) {
-                    sg[lane] = s.gates;
-                    sr[lane] = s.starts;
-                }
+            if (p0 == 0) {
+                if (tid < kFactors * Q) sf[tid] = nf;
+                if (tid < Q) sg[tid] = ng;
             }
-            if (p0 == 0 && tid < kFactors * Q) sf[tid] = a.factors[image * kFactors * Q + tid];
-            for (int i = tid; i < Q * 64 / R; i += 512) {
-                const int r = i / (64 / R), q = i % (64 / R), left = r < valid ? P - p0 - R * q : 0;
-                float v[R];
-                load_values<MM>(static_cast<const S*>(a.dy) + (t0 + r) * a.dy_row + h * a.P + p0 + R * q, left, v);
-                put_parts<MM, 64, 1>(ty, QP, r, q, v);
-                const int64_t at = ((t0 + r) * a.H + h) * a.P + p0 + R * q;
-                load_floats<R>(u.dz + at, left, v);
-                put_parts<MM, 64, TP>(tz, QP, r, q, v);
-                store_values<MM>(static_cast<S*>(a.dv) + (t0 + r) * a.dv_row + h * a.P + p0 + R * q, left, v);
-                load_floats<R>(u.saved.e + at, left, v);
-                put_parts<MM, 64, TP>(te, QP, r, q, v);
+            put_parts<MM, 64, 1>(ty, QP, srow, sq8, ny);
+            put_parts<MM, 64, TP>(tz, QP, srow, sq8, nz);
+            put_parts<MM, 64, TP>(te, QP, srow, sq8, ne);
+            store_values<MM>(static_cast<S*>(a.dv) + (t0 + srow) * a.dv_row + h * a.P + p0 + R * sq8, srow < valid ? P - p0 - R * sq8 : 0, nz);
+            const bool same = p0 + 64 < P;
+            const int64_t hn = same ? h : h + 1;
+            if (hn < h1) {
+                load_tokens(hn, same ? p0 + 64 : 0);
+                if (!same) load_factors(hn);
             }
             __syncthreads();
 #pragma unroll
             for (int kk = 0; kk < KP; ++kk) {
 #pragma unroll
                 for (int j = 0; j < CT; ++j) {
-                    const int n = 16 * (cg * CT + j) + li;
-                    float s[R], d[R];
+                    if (rg == 0) {
 #pragma unroll
-                    for (int m = 0; m < R; ++m) {
-                        const int p = p0 + MM::KB * kk + R * g4 + m;
-                        s[m] = d[m] = 0.0f;
-                        if (p < P && n < N) {
-                            s[m] = states[static_cast<int64_t>(p) * N + n];
-                            d[m] = grads[static_cast<int64_t>(p) * N + n];
-                        }
-                        if (rg == 0) dot += s[m] * d[m];
+                        for (int m = 0; m < R; ++m) dot += ns[kk][j][m] * nd[kk][j][m];
                     }
-                    const auto fs = MM::template parts<3>(s);
-                    const auto fd = MM::template parts<2>(d);
+                    const auto fs = MM::template parts<3>(ns[kk][j]);
+                    const auto fd = MM::template parts<2>(nd[kk][j]);
 #pragma unroll
                     for (int i = 0; i < RW; ++i) {
                         const int r0 = 16 * (rg * RW + i);
@@ -444,6 +471,10 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a, Buffers u)
                         MM::template mac<XP, 2>(ke[i][j], e, fd);
                     }
                 }
+            }
+            if (hn < h1) load_states(hn, same ? p0 + 64 : 0);
+#pragma unroll
+            for (int kk = 0; kk < KP; ++kk) {
 #pragma unroll
                 for (int m = 0; m < MINE; ++m) {
                     int tile = w + 8 * m, rt = 0;
@@ -475,7 +506,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a, Buffers u)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int t = 16 * rt + 4 * g4 + e;
-                const float r = s <= t && sr[s] == sr[t] ? exp_of(sg[t] - sg[s]) : 0.0f;
+                const float r = s <= t && sf[3 * Q + s] == sf[3 * Q + t] ? exp_of(sg[t] - sg[s]) : 0.0f;
                 const bool on = r != 0.0f, below = on && s < t;
                 const float x = on ? r * a.scale * be * dm[m][e] : 0.0f;
                 const float f = below ? -r * db[m][e] : 0.0f;
@@ -568,36 +599,20 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a, Buffers u)
             }
         }
         __syncthreads();
-        if (w == 0) {
-            double from = 0.0, end = 0.0;
-            float be = 0.0f;
-            if (lane < Q) {
+        if (tid < Q) {
+            float from = 0.0f, be = 0.0f, all = 0.0f;
 #pragma unroll
-                for (int i = 0; i < CG; ++i) from += sc[i][lane];
-                const float* part = u.part + image * ptiles * 2 * Q;
-                for (int i = 0; i < ptiles; ++i) {
-                    be += part[i * 2 * Q + lane];
-                    end += part[i * 2 * Q + Q + lane];
-                }
-                for (int rt = lane / 16; rt < RT; ++rt) be += sdb[rt][lane];
-            }
-            const double own = end;
+            for (int i = 0; i < CG; ++i) from += sc[i][tid];
 #pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const double o = __shfl_down(from, d), e = __shfl_up(end, d);
-                if (lane + d < 64) from += o;
-                if (lane >= d) end += e;
-            }
-            float all = 0.0f;
+            for (int rt = 0; rt < RT; ++rt) be += rt >= tid / 16 ? sdb[rt][tid] : 0.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) all += sdot[i];
-            if (lane < valid) {
-                const int64_t at = (t0 + lane) * a.H + h;
-                const float through = sf[Q - 1];
-                a.dbeta[at] = be;
-                if (a.dgate)
-                    a.dgate[at] = static_cast<float>(from + (end - own) + sspan[lane] + (through != 0.0f ? through * all : 0.0f));
-            }
+            const float through = sf[Q - 1];
+            float* to = u.gate + image * 4 * Q + tid;
+            to[0] = from;
+            to[Q] = sspan[tid];
+            to[2 * Q] = be;
+            to[3 * Q] = through != 0.0f ? through * all : 0.0f;
         }
     }
     const int64_t part = a.B * a.L * a.G * a.N;
@@ -620,6 +635,44 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a, Buffers u)
                 }
             }
         }
+}
+
+// dbeta, and dgate_t = sum of the products with h_0 of t and later tokens + the pairs that span t + sum of
+// the products with dh of tokens before t + the states' own product
+template <int Q>
+__global__ __launch_bounds__(256) void delta_gate_kernel(DeltaArgs a, Buffers u) {
+    const int lane = threadIdx.x & 63;
+    const int64_t image = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+    if (image >= a.B * a.H * a.chunks) return;
+    const int64_t c = image % a.chunks, bh = image / a.chunks, h = bh % a.H, b = bh / a.H;
+    const int64_t t = c * Q + lane, ptiles = (a.P + 15) / 16;
+    const bool have = lane < Q && t < a.L;
+    double from = 0.0, end = 0.0;
+    float be = 0.0f, rest = 0.0f;
+    if (have) {
+        const float* part = u.part + image * ptiles * 2 * Q + lane;
+        const float* g = u.gate + image * 4 * Q + lane;
+        from = g[0];
+        rest = g[Q] + g[3 * Q];
+        be = g[2 * Q];
+#pragma unroll 8
+        for (int i = 0; i < ptiles; ++i) {
+            be += part[i * 2 * Q];
+            end += part[i * 2 * Q + Q];
+        }
+    }
+    const double own = end;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const double o = __shfl_down(from, d), e = __shfl_up(end, d);
+        if (lane + d < 64) from += o;
+        if (lane >= d) end += e;
+    }
+    if (have) {
+        const int64_t at = (b * a.L + t) * a.H + h;
+        a.dbeta[at] = be;
+        if (a.dgate) a.dgate[at] = static_cast<float>(from + (end - own) + rest);
+    }
 }
 
 // dQ and dK of key heads whose heads were split
@@ -662,6 +715,7 @@ size_t place(DeltaArgs& a, Buffers& u, uint8_t* ws) {
     u.saved.e = take(rows);
     u.dz = take(rows);
     u.part = take(units * ((a.P + 15) / 16) * 2 * MM::Q);
+    u.gate = take(units * 4 * MM::Q);
     u.dqk = take(u.splits > 1 ? 2 * u.splits * a.B * a.L * a.G * a.N : 0);
     return at;
 }
@@ -674,6 +728,9 @@ hipError_t kernels_of(const DeltaArgs& a, const Buffers& u, hipStream_t stream) 
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     delta_grad_kernel<MM, NT><<<static_cast<unsigned>(a.B * a.chunks * a.G * u.splits), 512, 0, stream>>>(a, u);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    delta_gate_kernel<MM::Q><<<static_cast<unsigned>((a.B * a.H * a.chunks + 3) / 4), 256, 0, stream>>>(a, u);
     e = hipGetLastError();
     if (e != hipSuccess || u.splits == 1) return e;
     delta_join_kernel<MM><<<1024, 256, 0, stream>>>(a, u);
