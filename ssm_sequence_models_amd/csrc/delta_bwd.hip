@@ -24,6 +24,8 @@ namespace {
 
 using namespace delta;
 
+constexpr int kGradWaves = 8;
+
 struct Buffers {
     DeltaSaved saved;
     float* grads;  // [B, H, chunks, P, N]: the gradient of the state after each chunk
@@ -266,23 +268,6 @@ __global__ __launch_bounds__(320) void delta_back_kernel(DeltaArgs a, Buffers u)
 // accumulators.
 // ---------------------------------------------------------------------------------------
 template <class MM>
-__device__ __forceinline__ void load_values(const typename MM::S* p, int n, float (&v)[MM::R]) {
-    if (n >= MM::R) {
-        if constexpr (MM::R == 8) {
-            const u4 x = *reinterpret_cast<const u4any*>(p);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(j & 1 ? x[j >> 1] & 0xFFFF0000u : x[j >> 1] << 16);
-        } else {
-            const f4 x = __builtin_bit_cast(f4, *reinterpret_cast<const u4any4*>(p));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = x[j];
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < MM::R; ++j) v[j] = j < n ? MM::value(p, j) : 0.0f;
-    }
-}
-template <class MM>
 __device__ __forceinline__ void store_values(typename MM::S* p, int n, const float (&v)[MM::R]) {
     if (n >= MM::R) {
         if constexpr (MM::R == 8)
@@ -293,20 +278,6 @@ __device__ __forceinline__ void store_values(typename MM::S* p, int n, const flo
 #pragma unroll
         for (int j = 0; j < MM::R; ++j)
             if (j < n) MM::store(p, j, v[j]);
-    }
-}
-template <int R>
-__device__ __forceinline__ void load_floats(const float* p, int n, float (&v)[R]) {
-    if (n >= R) {
-#pragma unroll
-        for (int i = 0; i < R / 4; ++i) {
-            const f4 x = __builtin_bit_cast(f4, *reinterpret_cast<const u4any4*>(p + 4 * i));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[4 * i + j] = x[j];
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < R; ++j) v[j] = j < n ? p[j] : 0.0f;
     }
 }
 // R values into PARTS tiles
@@ -336,13 +307,13 @@ __device__ __forceinline__ void put_pair(uint8_t* tiles, int bytes, int row, int
     }
 }
 
-template <class MM, int NT>
-__global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a, Buffers u) {
+template <class MM, int NT, bool DIRECT>
+__global__ __launch_bounds__(64 * kGradWaves) void delta_grad_kernel(DeltaArgs a, Buffers u) {
     using S = typename MM::S;
     constexpr int Q = MM::Q, RT = Q / 16, KT = Q / MM::KB, W = 16 * NT, KN = W / MM::KB, KP = 64 / MM::KB, R = MM::R;
-    constexpr int CG = NT < 8 ? NT : 8, RG = 8 / CG;    // column and row groups of wavefronts
+    constexpr int WV = kGradWaves, CG = NT < WV ? NT : WV, RG = WV / CG;  // column and row groups of wavefronts
     constexpr int CT = NT / CG, RW = RT / RG;           // a wavefront's column and row tiles
-    constexpr int TILES = RT * (RT + 1) / 2, MINE = (TILES + 7) / 8;
+    constexpr int TILES = RT * (RT + 1) / 2, MINE = (TILES + WV - 1) / WV;
     constexpr int TP = MM::TP, XP = TP == 1 ? 1 : 2;
     constexpr int QN = MM::template tile_bytes<W>(Q), QP = MM::template tile_bytes<64>(Q), QQ = MM::template tile_bytes<Q>(Q);
     constexpr int LOADS = (1 + 2 * TP) * QP, PAIRS = (2 * XP + TP) * QQ;
@@ -354,15 +325,15 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a, Buffers u)
     __shared__ float sdb[RT][Q];    // sums over t of pairs, by row tiles
     __shared__ float sc[CG][Q];     // products with h_0, by column groups
     __shared__ float sspan[Q];
-    __shared__ float sdot[8];
+    __shared__ float sdot[WV];
     uint8_t* const ty = pool;                   // dY
     uint8_t* const tz = pool + QP;              // dZ
     uint8_t* const te = pool + (1 + TP) * QP;   // E
     uint8_t* const tx = pool;                   // X
     uint8_t* const tf = pool + XP * QQ;         // F
     uint8_t* const tw = pool + 2 * XP * QQ;     // the pairs' products themselves
-    const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g4 = lane >> 4;
-    const int w = __builtin_amdgcn_readfirstlane(tid >> 6), cg = w % CG, rg = w / CG;
+    const int tid = threadIdx.x, lane = tid & 63, li_ = lane & 15, g4_ = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6), cg = w % CG, rg = RG == 1 ? 0 : w / CG;
     int64_t unit = xcd_order(blockIdx.x, gridDim.x);
     const int64_t split = unit % u.splits;
     unit /= u.splits;
@@ -375,8 +346,8 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a, Buffers u)
     const int N = static_cast<int>(a.N), P = static_cast<int>(a.P);
     const int64_t t0 = b * a.L + c * Q;
 
-    stage_rows<MM, W, 512, false>(sk, static_cast<const S*>(a.k) + t0 * a.k_row + g * a.N, a.k_row, valid, N);
-    stage_rows<MM, W, 512, false>(sq, static_cast<const S*>(a.q) + t0 * a.q_row + g * a.N, a.q_row, valid, N);
+    stage_rows<MM, W, 64 * WV, false>(sk, static_cast<const S*>(a.k) + t0 * a.k_row + g * a.N, a.k_row, valid, N);
+    stage_rows<MM, W, 64 * WV, false>(sq, static_cast<const S*>(a.q) + t0 * a.q_row + g * a.N, a.q_row, valid, N);
     f4 dq[RW][CT], dk[RW][CT];
 #pragma unroll
     for (int i = 0; i < RW; ++i)
@@ -385,18 +356,46 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a, Buffers u)
 
     // what a thread stages of 64 channels of a head, and what a lane takes of h_0 and dh, are loaded
     // one block of channels ahead
-    const int srow = static_cast<int>(threadIdx.x) / (64 / R), sq8 = threadIdx.x % (64 / R);
-    static_assert(Q * 64 / R == 512, "one piece a thread");
-    float ny[R], nz[R], ne[R];
+    constexpr int PT = Q * 64 / R / (64 * WV);  // pieces of the tokens' tiles a thread
+    const int sq8 = tid % (64 / R);
+    const auto srow = [&](int i) { return (tid + 64 * WV * i) / (64 / R); };
+    u4 ny[PT];
+    f4 nz[PT][R / 4], ne[PT][R / 4];
     float ns[KP][CT][R], nd[KP][CT][R];
     const auto load_tokens = [&](int64_t h, int p0) {
-        const int left = srow < valid ? P - p0 - R * sq8 : 0;
-        const int64_t at = ((t0 + srow) * a.H + h) * a.P + p0 + R * sq8;
-        load_values<MM>(static_cast<const S*>(a.dy) + (t0 + srow) * a.dy_row + h * a.P + p0 + R * sq8, left, ny);
-        load_floats<R>(u.dz + at, left, nz);
-        load_floats<R>(u.saved.e + at, left, ne);
+        const int p = p0 + R * sq8;
+        const Buffer ry = token_buffer<S>(a.dy, t0, a.dy_row, h * a.P, DIRECT ? valid : 1, a.P);
+        const Buffer rz = token_buffer<float>(u.dz, t0, a.H * a.P, h * a.P, DIRECT ? valid : 1, a.P);
+        const Buffer re = token_buffer<float>(u.saved.e, t0, a.H * a.P, h * a.P, DIRECT ? valid : 1, a.P);
+#pragma unroll
+        for (int x = 0; x < PT; ++x) {
+            const int row = srow(x);
+            if constexpr (DIRECT) {
+                const uint32_t ya = p < P ? (row * static_cast<uint32_t>(a.dy_row) + p) * sizeof(S) : kOutside;
+                const uint32_t za = p < P ? (row * static_cast<uint32_t>(a.H * a.P) + p) * 4 : kOutside;
+                ny[x] = __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(ry, ya, 0, 0));
+#pragma unroll
+                for (int i = 0; i < R / 4; ++i) {
+                    nz[x][i] = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(rz, za + 16 * i, 0, 0));
+                    ne[x][i] = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(re, za + 16 * i, 0, 0));
+                }
+            } else {
+                const int left = row < valid ? P - p : 0;
+                const int64_t at = ((t0 + row) * a.H + h) * a.P + p;
+                const S* y = static_cast<const S*>(a.dy) + (t0 + row) * a.dy_row + h * a.P + p;
+                S v[R];
+#pragma unroll
+                for (int j = 0; j < R; ++j) {
+                    v[j] = j < left ? y[j] : S{0};
+                    nz[x][j >> 2][j & 3] = j < left ? u.dz[at + j] : 0.0f;
+                    ne[x][j >> 2][j & 3] = j < left ? u.saved.e[at + j] : 0.0f;
+                }
+                __builtin_memcpy(&ny[x], v, 16);
+            }
+        }
     };
     const auto load_states = [&](int64_t h, int p0) {
+        const int li = here(li_), g4 = here(g4_);
         const int64_t image = (b * a.H + h) * a.chunks + c;
         const Buffer rs = buffer(u.saved.states + image * P * N, static_cast<int64_t>(P) * N * 4);
         const Buffer rd = buffer(u.grads + image * P * N, static_cast<int64_t>(P) * N * 4);
@@ -420,6 +419,13 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a, Buffers u)
         if (tid < kFactors * Q) nf = a.factors[image * kFactors * Q + tid];
         if (tid < Q) ng = a.gates[image * Q + tid];
     };
+    int trow[MINE], tcol[MINE];  // this wavefront's tiles of the pairs, row tiles from the first on
+#pragma unroll
+    for (int m = 0; m < MINE; ++m) {
+        tcol[m] = w + WV * m;
+        trow[m] = 0;
+        while (tcol[m] > trow[m]) tcol[m] -= ++trow[m];
+    }
     const int64_t h0 = g * rep + split * u.heads;
     load_factors(h0);
     load_tokens(h0, 0);
@@ -440,10 +446,24 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a, Buffers u)
                 if (tid < kFactors * Q) sf[tid] = nf;
                 if (tid < Q) sg[tid] = ng;
             }
-            put_parts<MM, 64, 1>(ty, QP, srow, sq8, ny);
-            put_parts<MM, 64, TP>(tz, QP, srow, sq8, nz);
-            put_parts<MM, 64, TP>(te, QP, srow, sq8, ne);
-            store_values<MM>(static_cast<S*>(a.dv) + (t0 + srow) * a.dv_row + h * a.P + p0 + R * sq8, srow < valid ? P - p0 - R * sq8 : 0, nz);
+#pragma unroll
+            for (int x = 0; x < PT; ++x) {
+                const int row = srow(x);
+                *reinterpret_cast<u4*>(ty + MM::template piece_at<64>(row, sq8)) = ny[x];
+                float z[R], e[R];
+#pragma unroll
+                for (int j = 0; j < R; ++j) {
+                    z[j] = nz[x][j >> 2][j & 3];
+                    e[j] = ne[x][j >> 2][j & 3];
+                }
+                put_parts<MM, 64, TP>(tz, QP, row, sq8, z);
+                put_parts<MM, 64, TP>(te, QP, row, sq8, e);
+                if (DIRECT) {
+                    if (row < valid && p0 + R * sq8 < P) store_values<MM>(static_cast<S*>(a.dv) + (t0 + row) * a.dv_row + h * a.P + p0 + R * sq8, R, z);
+                } else {
+                    store_values<MM>(static_cast<S*>(a.dv) + (t0 + row) * a.dv_row + h * a.P + p0 + R * sq8, row < valid ? P - p0 - R * sq8 : 0, z);
+                }
+            }
             const bool same = p0 + 64 < P;
             const int64_t hn = same ? h : h + 1;
             if (hn < h1) {
@@ -453,33 +473,40 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a, Buffers u)
             __syncthreads();
 #pragma unroll
             for (int kk = 0; kk < KP; ++kk) {
+                const int li = here(li_), g4 = here(g4_);
+                typename MM::template Frag<3> fs[CT];
+                typename MM::template Frag<2> fd[CT];
 #pragma unroll
                 for (int j = 0; j < CT; ++j) {
                     if (rg == 0) {
 #pragma unroll
                         for (int m = 0; m < R; ++m) dot += ns[kk][j][m] * nd[kk][j][m];
                     }
-                    const auto fs = MM::template parts<3>(ns[kk][j]);
-                    const auto fd = MM::template parts<2>(nd[kk][j]);
+                    fs[j] = MM::template parts<3>(ns[kk][j]);
+                    fd[j] = MM::template parts<2>(nd[kk][j]);
+                }
 #pragma unroll
-                    for (int i = 0; i < RW; ++i) {
-                        const int r0 = 16 * (rg * RW + i);
-                        MM::template mac<1, 3>(qo[i][j], MM::template along<64>(ty, r0, kk, li, g4), fs);
-                        const auto z = of_parts<MM, TP>([&](int q) { return MM::template along<64>(tz + q * QP, r0, kk, li, g4); });
-                        MM::template mac<TP, 3>(ko[i][j], z, fs);
-                        const auto e = of_parts<MM, XP>([&](int q) { return MM::template along<64>(te + q * QP, r0, kk, li, g4); });
-                        MM::template mac<XP, 2>(ke[i][j], e, fd);
+                for (int i = 0; i < RW; ++i) {
+                    const int r0 = 16 * (rg * RW + i);
+                    const auto y = MM::template along<64>(ty, r0, kk, li, g4);
+                    const auto z = of_parts<MM, TP>([&](int q) { return MM::template along<64>(tz + q * QP, r0, kk, li, g4); });
+                    const auto e = of_parts<MM, XP>([&](int q) { return MM::template along<64>(te + q * QP, r0, kk, li, g4); });
+#pragma unroll
+                    for (int j = 0; j < CT; ++j) {
+                        MM::template mac<1, 3>(qo[i][j], y, fs[j]);
+                        MM::template mac<TP, 3>(ko[i][j], z, fs[j]);
+                        MM::template mac<XP, 2>(ke[i][j], e, fd[j]);
                     }
                 }
             }
             if (hn < h1) load_states(hn, same ? p0 + 64 : 0);
 #pragma unroll
-            for (int kk = 0; kk < KP; ++kk) {
+            for (int m = 0; m < MINE; ++m) {
+                if (w + WV * m >= TILES) continue;
+                const int tile = tcol[m], rt = trow[m];
+                const int li = here(li_), g4 = here(g4_);
 #pragma unroll
-                for (int m = 0; m < MINE; ++m) {
-                    int tile = w + 8 * m, rt = 0;
-                    if (tile >= TILES) continue;
-                    while (tile > rt) tile -= ++rt;
+                for (int kk = 0; kk < KP; ++kk) {
                     const auto e = of_parts<MM, TP>([&](int q) { return MM::template along<64>(te + q * QP, 16 * tile, kk, li, g4); });
                     MM::template mac<1, TP>(dm[m], MM::template along<64>(ty, 16 * rt, kk, li, g4), e);
                     const auto z = of_parts<MM, TP>([&](int q) { return MM::template along<64>(tz + q * QP, 16 * rt, kk, li, g4); });
@@ -490,9 +517,9 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a, Buffers u)
         __syncthreads();  // the loads' tiles become the pairs'
 #pragma unroll
         for (int m = 0; m < MINE; ++m) {
-            int tile = w + 8 * m, rt = 0;
-            if (tile >= TILES) continue;
-            while (tile > rt) tile -= ++rt;
+            if (w + WV * m >= TILES) continue;
+            const int tile = tcol[m], rt = trow[m];
+            const int li = here(li_), g4 = here(g4_);
             f4 kk{0, 0, 0, 0}, qk{0, 0, 0, 0};
 #pragma unroll
             for (int x = 0; x < KN; ++x) {
@@ -527,6 +554,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a, Buffers u)
         // products with h_0, for dgate
 #pragma unroll
         for (int i = 0; i < RW; ++i) {
+            const int li = here(li_), g4 = here(g4_);
             const int r0 = 16 * (rg * RW + i) + 4 * g4;
             const f4 f = row4(sf + r0);
 #pragma unroll
@@ -548,6 +576,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a, Buffers u)
         if (lane == 0) sdot[w] = dot;
         __syncthreads();
         if (w < RT) {  // pairs that span token t = 16 w + li
+            const int li = here(li_), g4 = here(g4_);
             float span = 0.0f;
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
@@ -571,6 +600,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a, Buffers u)
         }
 #pragma unroll
         for (int i = 0; i < RW; ++i) {
+            const int li = here(li_), g4 = here(g4_);
             const int rt = rg * RW + i;
             const f4 f = row4(sf + Q + 16 * rt + 4 * g4) * row4(sf + 2 * Q + 16 * rt + 4 * g4);
 #pragma unroll
@@ -606,7 +636,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a, Buffers u)
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) be += rt >= tid / 16 ? sdb[rt][tid] : 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) all += sdot[i];
+            for (int i = 0; i < WV; ++i) all += sdot[i];
             const float through = sf[Q - 1];
             float* to = u.gate + image * 4 * Q + tid;
             to[0] = from;
@@ -615,26 +645,44 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs a, Buffers u)
             to[3 * Q] = through != 0.0f ? through * all : 0.0f;
         }
     }
-    const int64_t part = a.B * a.L * a.G * a.N;
+    const int li = li_, g4 = g4_;
+    if (u.splits == 1) {
+        const Buffer rq = token_buffer<S>(a.dq, t0, a.dq_row, g * a.N, DIRECT ? valid : 1, a.N);
+        const Buffer rk = token_buffer<S>(a.dk, t0, a.dk_row, g * a.N, DIRECT ? valid : 1, a.N);
 #pragma unroll
-    for (int i = 0; i < RW; ++i)
+        for (int i = 0; i < RW; ++i)
 #pragma unroll
-        for (int j = 0; j < CT; ++j) {
-            const int n = 16 * (cg * CT + j) + li;
+            for (int j = 0; j < CT; ++j) {
+                const int n = 16 * (cg * CT + j) + li;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int t = 16 * (rg * RW + i) + 4 * g4 + e;
-                if (t >= valid || n >= N) continue;
-                if (u.splits == 1) {
-                    MM::store(static_cast<S*>(a.dq) + (t0 + t) * a.dq_row + g * a.N, n, dq[i][j][e]);
-                    MM::store(static_cast<S*>(a.dk) + (t0 + t) * a.dk_row + g * a.N, n, dk[i][j][e]);
-                } else {
+                for (int e = 0; e < 4; ++e) {
+                    const int t = 16 * (rg * RW + i) + 4 * g4 + e;
+                    if (DIRECT) {
+                        store_at<S>(rq, n < N ? (t * static_cast<uint32_t>(a.dq_row) + n) * sizeof(S) : kOutside, dq[i][j][e]);
+                        store_at<S>(rk, n < N ? (t * static_cast<uint32_t>(a.dk_row) + n) * sizeof(S) : kOutside, dk[i][j][e]);
+                    } else if (t < valid && n < N) {
+                        MM::store(static_cast<S*>(a.dq) + (t0 + t) * a.dq_row + g * a.N, n, dq[i][j][e]);
+                        MM::store(static_cast<S*>(a.dk) + (t0 + t) * a.dk_row + g * a.N, n, dk[i][j][e]);
+                    }
+                }
+            }
+    } else {
+        const int64_t part = a.B * a.L * a.G * a.N;
+#pragma unroll
+        for (int i = 0; i < RW; ++i)
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+                const int n = 16 * (cg * CT + j) + li;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = 16 * (rg * RW + i) + 4 * g4 + e;
+                    if (t >= valid || n >= N) continue;
                     float* to = u.dqk + split * part + ((t0 + t) * a.G + g) * a.N + n;
                     to[0] = dq[i][j][e];
                     to[u.splits * part] = dk[i][j][e];
                 }
             }
-        }
+    }
 }
 
 // dbeta, and dgate_t = sum of the products with h_0 of t and later tokens + the pairs that span t + sum of
@@ -727,7 +775,9 @@ hipError_t kernels_of(const DeltaArgs& a, const Buffers& u, hipStream_t stream) 
     else delta_back_kernel<MM, NT, false><<<blocks, 320, 0, stream>>>(a, u);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    delta_grad_kernel<MM, NT><<<static_cast<unsigned>(a.B * a.chunks * a.G * u.splits), 512, 0, stream>>>(a, u);
+    const unsigned grads = static_cast<unsigned>(a.B * a.chunks * a.G * u.splits);
+    if (a.direct) delta_grad_kernel<MM, NT, true><<<grads, 64 * kGradWaves, 0, stream>>>(a, u);
+    else delta_grad_kernel<MM, NT, false><<<grads, 64 * kGradWaves, 0, stream>>>(a, u);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     delta_gate_kernel<MM::Q><<<static_cast<unsigned>((a.B * a.H * a.chunks + 3) / 4), 256, 0, stream>>>(a, u);
@@ -743,7 +793,7 @@ hipError_t bwd_of(DeltaArgs a, void* workspace, ssm_dtype_t dtype, hipStream_t s
     constexpr size_t es = sizeof(typename MM::S);
     a.direct = a.N % (16 / es) == 0 && a.P % (16 / es) == 0 && direct_rows_fit(a.q, a.q_row, es) &&
                direct_rows_fit(a.k, a.k_row, es) && direct_rows_fit(a.v, a.v_row, es) && direct_rows_fit(a.dy, a.dy_row, es) &&
-               direct_rows_fit(nullptr, a.H * a.P, 4);
+               direct_rows_fit(a.dq, a.dq_row, es) && direct_rows_fit(a.dk, a.dk_row, es) && direct_rows_fit(nullptr, a.H * a.P, 4);
     const hipError_t e = launch_delta_walk_saved(a, u.saved, dtype, stream);
     if (e != hipSuccess) return e;
     if (a.N <= 64) return kernels_of<MM, 4>(a, u, stream);

@@ -102,6 +102,12 @@ __device__ __forceinline__ float row_sums(const float (&v)[4], int li) {
     r += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(r), 0x124, 0xf, 0xf, true));         // rotated by 4
     return r + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(r), 0x128, 0xf, 0xf, true));   // by 8
 }
+// Makes an offset opaque: what is derived from it is computed where it is used instead of being
+// kept in registers over the whole loop over the heads.
+__device__ __forceinline__ int here(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
 
 }  // namespace
 }  // namespace ssm

@@ -101,12 +101,6 @@ struct SquareSum {
     }
     __device__ __forceinline__ float bound() const { return sum + (most > 0.0f ? 0x1p-121f : 0.0f); }
 };
-// Makes an offset opaque: what is derived from it is computed where it is used instead of being
-// kept in registers over the whole loop over the heads.
-__device__ __forceinline__ int here(int v) {
-    asm volatile("" : "+v"(v));
-    return v;
-}
 // keeps a sum where it is computed (moved to the loop's end it would keep its terms in registers)
 __device__ __forceinline__ void settle(float& v) { asm volatile("" : "+v"(v)); }
 __device__ __forceinline__ void settle(f4& v) {
