@@ -51,6 +51,11 @@ struct DeltaArgs {
     uint8_t* T;      // [B, H, chunks] images
     uint8_t* M;
     uint8_t* Tt;     // transposed, backward only (M is transposed there)
+    // rows cut into `segs` segments of seg_chunks chunks where there are few (delta_join in delta.hip)
+    int64_t segs, seg_chunks;
+    float* phi;      // [B, H, segs, N, N]: what a segment makes of the state before it, from the right
+    float* gain;     // [B, H, segs, P, N]: what its own tokens bring
+    float* entry;    // [B, H, segs, P, N]: the state before it (backward: the gradient of the state after it)
     double* gates;   // [B, H, chunks, Q]: sums of gates from the chunk's start on, backward only
     float* factors;  // [B, H, chunks, kFactors, Q]: e^G from the chunk's start, e^{G_Q - G}, beta, sequences begun
 };
@@ -531,6 +536,31 @@ inline bool direct_rows_fit(const void* p, int64_t row, size_t es) {
     return row < (int64_t{1} << 30) / 64 / static_cast<int64_t>(es) && reinterpret_cast<uintptr_t>(p) % 16 == 0 && row * es % 16 == 0;
 }
 
+// Rows are cut into segments where their walks do not fill the 256 CUs: all segments from zero, with the
+// N unit rows as further channels that give what a segment makes of the state before it; the states
+// before the segments from those; then the walk proper, all segments side by side.  The cut is the
+// one with the shortest sum of its walks' rounds, in measured microseconds a chunk: 2.0 (from zero)
+// and 2.9 forward, 2.0, 3.0 (from zero) and 3.7 backward, 2 a segment for the states between, 10
+// for the launches.
+inline void plan_segments(DeltaArgs& a, bool bwd) {
+    const int64_t units = a.B * a.H, own = (a.P + 63) / 64, all = own + (a.N + 63) / 64;
+    const auto rounds = [](int64_t blocks) { return static_cast<double>((blocks + 255) / 256); };
+    a.segs = 1;
+    a.seg_chunks = a.chunks;
+    double best = rounds(units * own) * a.chunks * (bwd ? 5.7 : 2.9) * 0.85;
+    for (int64_t n = 2; n <= 64 && n * 4 <= a.chunks; ++n) {
+        const int64_t each = (a.chunks + n - 1) / n;
+        if ((a.chunks + each - 1) / each != n) continue;
+        const double t = rounds(units * all * n) * each * 2.0 + rounds(units * own * n) * each * (bwd ? 8.7 : 2.9) +
+                         n * (bwd ? 4.0 : 2.0) + (bwd ? 20.0 : 10.0);
+        if (t < best) {
+            best = t;
+            a.segs = n;
+            a.seg_chunks = each;
+        }
+    }
+}
+
 // the chunks' part of the workspace; returns its bytes
 template <class MM>
 size_t place_chunks(DeltaArgs& a, uint8_t* ws, bool bwd) {
@@ -546,7 +576,16 @@ size_t place_chunks(DeltaArgs& a, uint8_t* ws, bool bwd) {
     a.factors = reinterpret_cast<float*>(ws + at);
     at += n * kFactors * MM::Q * 4;
     a.gates = reinterpret_cast<double*>(ws + at);
-    return at + (bwd ? n * MM::Q * 8 : 0);
+    at += bwd ? n * MM::Q * 8 : 0;
+    plan_segments(a, bwd);
+    const size_t states = a.segs > 1 ? static_cast<size_t>(a.B * a.H * a.segs) : 0;
+    a.phi = reinterpret_cast<float*>(ws + at);
+    at += states * a.N * a.N * 4;
+    a.gain = reinterpret_cast<float*>(ws + at);
+    at += states * a.P * a.N * 4;
+    a.entry = reinterpret_cast<float*>(ws + at);
+    at += states * a.P * a.N * 4;
+    return (at + 255) / 256 * 256;
 }
 
 }  // namespace delta
@@ -557,6 +596,8 @@ struct DeltaSaved {
     float* e;       // [B, L, H, P]
 };
 hipError_t launch_delta_walk_saved(const DeltaArgs& a, const DeltaSaved& s, ssm_dtype_t dtype, hipStream_t stream);
+// the gradients of the states after the segments
+hipError_t launch_delta_join_back(const DeltaArgs& a, ssm_dtype_t dtype, hipStream_t stream);
 size_t delta_fwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N, ssm_dtype_t dtype);
 size_t delta_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N, ssm_dtype_t dtype);
 hipError_t launch_delta_fwd(DeltaArgs a, void* workspace, ssm_dtype_t dtype, hipStream_t stream);

@@ -209,32 +209,36 @@ __global__ __launch_bounds__(MM::Q * 4) void delta_prep_kernel(DeltaArgs a) {
 // the next chunk's K, Q, T, M, factors and values straight into the other half of LDS (one half only
 // where dstate is over 128), and the last chunk's y out of it.  (Fetched by the four themselves, the
 // loads' issue was a third of a chunk's time.)
-// SAVE: for the backward, the states and E in place of y
+// kSave: for the backward, the states and E in place of y.  kSpan: a segment from zero, and behind the
+// channels the N unit rows without values; only the state after it.
 // DIRECT: see DeltaArgs; without it tokens pass through registers
 // ---------------------------------------------------------------------------------------
-template <class MM, int NT, bool SAVE>
+enum { kOut, kSave, kSpan };
+template <class MM, int NT, int MODE>
 struct WalkLds {
     static constexpr int W = 16 * NT, MP = m_parts<MM>(false), HALVES = NT <= 8 ? 2 : 1;
     static constexpr int V = 0, K = V + staged_bytes<MM, 64>(), T = K + staged_bytes<MM, W>(), F = T + image_bytes<MM>(MM::TP),
-                         Qq = F + 1024, M = Qq + (SAVE ? 0 : staged_bytes<MM, W>()), HALF = M + (SAVE ? 0 : image_bytes<MM>(MP));
-    static constexpr int Y = HALVES * HALF, BYTES = Y + (SAVE ? 0 : 2 * MM::template tile_bytes<64>(MM::Q));
+                         Qq = F + 1024, M = Qq + (MODE != kOut ? 0 : staged_bytes<MM, W>()), HALF = M + (MODE != kOut ? 0 : image_bytes<MM>(MP));
+    static constexpr int Y = HALVES * HALF, BYTES = Y + (MODE != kOut ? 0 : 2 * MM::template tile_bytes<64>(MM::Q));
 };
 
-template <class MM, int NT, bool SAVE, bool DIRECT>
+template <class MM, int NT, int MODE, bool DIRECT>
 __global__ __launch_bounds__(320) void delta_walk_kernel(DeltaArgs a, DeltaSaved keep) {
     using S = typename MM::S;
-    using O = WalkLds<MM, NT, SAVE>;
+    using O = WalkLds<MM, NT, MODE>;
     constexpr int Q = MM::Q, RT = Q / 16, KT = Q / MM::KB, W = 16 * NT, KN = W / MM::KB, MP = O::MP, ES = sizeof(S);
     constexpr int YB = MM::template tile_bytes<64>(Q);
     __shared__ __attribute__((aligned(1024))) uint8_t sm[O::BYTES];
     const int lane = threadIdx.x & 63, li = lane & 15, g4 = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int H = static_cast<int>(a.H), P = static_cast<int>(a.P), N = static_cast<int>(a.N);
-    const int pblocks = (P + 63) / 64;
+    const int pblocks = (P + 63) / 64, all = pblocks + (MODE == kSpan ? (N + 63) / 64 : 0), segs = static_cast<int>(a.segs);
     const int unit = xcd_order(blockIdx.x, gridDim.x);
-    const int pb = unit % pblocks, bh = unit / pblocks, h = bh % H, b = bh / H;
+    const int pb = unit % all, seg = unit / all % segs, bh = unit / all / segs, h = bh % H, b = bh / H;
     const int g = h / (H / static_cast<int>(a.G));
-    const int chunks = static_cast<int>(a.chunks);
+    const bool rows = MODE == kSpan && pb >= pblocks;  // unit rows
+    const int chunks = static_cast<int>(a.chunks), c0 = seg * static_cast<int>(a.seg_chunks);
+    const int c1 = c0 + static_cast<int>(a.seg_chunks) < chunks ? c0 + static_cast<int>(a.seg_chunks) : chunks;
     const auto rows_of = [&](int c) {
         const int64_t left = a.L - static_cast<int64_t>(c) * Q;
         return static_cast<int>(left < Q ? left : Q);
@@ -254,19 +258,19 @@ __global__ __launch_bounds__(320) void delta_walk_kernel(DeltaArgs a, DeltaSaved
             const int valid = rows_of(c);
             if (DIRECT) {
                 direct_rows<MM, W, true>(half + O::K, token_buffer<S>(a.k, t0, a.k_row, g * N, valid, N), static_cast<int>(a.k_row), N, lane);
-                if (!SAVE) direct_rows<MM, W, true>(half + O::Qq, token_buffer<S>(a.q, t0, a.q_row, g * N, valid, N), static_cast<int>(a.q_row), N, lane);
-                direct_rows<MM, 64, false>(half + O::V, token_buffer<S>(a.v, t0, a.v_row, col, valid, width), static_cast<int>(a.v_row), width, lane);
+                if (MODE == kOut) direct_rows<MM, W, true>(half + O::Qq, token_buffer<S>(a.q, t0, a.q_row, g * N, valid, N), static_cast<int>(a.q_row), N, lane);
+                if (!rows) direct_rows<MM, 64, false>(half + O::V, token_buffer<S>(a.v, t0, a.v_row, col, valid, width), static_cast<int>(a.v_row), width, lane);
             } else {
                 stage_rows<MM, W, 64, true>(half + O::K, static_cast<const S*>(a.k) + t0 * a.k_row + g * N, a.k_row, valid, N);
-                if (!SAVE) stage_rows<MM, W, 64, true>(half + O::Qq, static_cast<const S*>(a.q) + t0 * a.q_row + g * N, a.q_row, valid, N);
-                stage_elements<MM, 64>(half + O::V, static_cast<const S*>(a.v) + t0 * a.v_row + col, a.v_row, valid, width);
+                if (MODE == kOut) stage_rows<MM, W, 64, true>(half + O::Qq, static_cast<const S*>(a.q) + t0 * a.q_row + g * N, a.q_row, valid, N);
+                if (!rows) stage_elements<MM, 64>(half + O::V, static_cast<const S*>(a.v) + t0 * a.v_row + col, a.v_row, valid, width);
             }
             direct_image<image_bytes<MM>(MM::TP)>(half + O::T, a.T + image * image_bytes<MM>(MM::TP), lane);
-            if (!SAVE) direct_image<image_bytes<MM>(MP)>(half + O::M, a.M + image * image_bytes<MM>(MP), lane);
+            if (MODE == kOut) direct_image<image_bytes<MM>(MP)>(half + O::M, a.M + image * image_bytes<MM>(MP), lane);
             direct_image<kFactors * Q * 4>(half + O::F, reinterpret_cast<const uint8_t*>(a.factors + image * kFactors * Q), lane);
         };
         const auto store = [&](int c) {
-            if (SAVE || c < 0) return;
+            if (MODE != kOut || c < c0) return;
             const uint8_t* y = sm + O::Y + (c & 1) * YB;
             const int64_t t0 = b * a.L + static_cast<int64_t>(c) * Q;
             const int valid = rows_of(c);
@@ -285,15 +289,15 @@ __global__ __launch_bounds__(320) void delta_walk_kernel(DeltaArgs a, DeltaSaved
                         MM::store(static_cast<S*>(a.y) + (t0 + i / 64) * a.y_row + col, lane, MM::template at<64>(y, i / 64, lane));
             }
         };
-        if (O::HALVES == 2) fetch(0);
-        for (int c = 0; c < chunks; ++c) {
+        if (O::HALVES == 2) fetch(c0);
+        for (int c = c0; c < c1; ++c) {
             if (O::HALVES == 1) {
                 __syncthreads();
                 fetch(c);
             }
             wait_loads();
             __syncthreads();
-            if (O::HALVES == 2 && c + 1 < chunks) fetch(c + 1);
+            if (O::HALVES == 2 && c + 1 < c1) fetch(c + 1);
             store(c - 1);
             if (marks_of(half_of(c)) >= static_cast<int>(kNotFinite)) {
                 __syncthreads();
@@ -301,21 +305,28 @@ __global__ __launch_bounds__(320) void delta_walk_kernel(DeltaArgs a, DeltaSaved
             }
         }
         __syncthreads();
-        store(chunks - 1);
+        store(c1 - 1);
         return;
     }
 
-    const int p0 = 64 * pb + 16 * w, p = p0 + li;
-    const bool mine = p0 < P, have = p < P;
-    const int64_t state = (static_cast<int64_t>(bh) * P + p) * N;
+    const int p0 = 64 * (rows ? pb - pblocks : pb) + 16 * w, p = p0 + li, most = rows ? N : P;
+    const bool mine = p0 < most, have = p < most;
+    const int64_t bhs = static_cast<int64_t>(bh) * segs + seg;
+    const float* const from = MODE == kSpan ? nullptr : segs > 1 ? a.entry + (bhs * P + p) * N : a.h0 ? a.h0 + (static_cast<int64_t>(bh) * P + p) * N : nullptr;
+    float* const to = MODE == kSpan ? (rows ? a.phi + (bhs * N + p) * N : a.gain + (bhs * P + p) * N)
+                      : MODE == kOut && a.final_state && seg == segs - 1 ? a.final_state + (static_cast<int64_t>(bh) * P + p) * N : nullptr;
     const uint32_t eat = have ? 4 * g4 * static_cast<uint32_t>(H * P) * 4 + p * 4 : kOutside;
     f4 hs[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
         const int n = MM::state_row(i, g4);
-        hs[i] = have && n < N && a.h0 ? *reinterpret_cast<const f4*>(a.h0 + state + n) : f4{0, 0, 0, 0};
+        hs[i] = have && n < N && from ? *reinterpret_cast<const f4*>(from + n) : f4{0, 0, 0, 0};
+        if (rows) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) hs[i][e] = n + e == p ? 1.0f : 0.0f;
+        }
     }
-    for (int c = 0; c < chunks; ++c) {
+    for (int c = c0; c < c1; ++c) {
         const int64_t t0 = b * a.L + static_cast<int64_t>(c) * Q;
         const int valid = rows_of(c);
         uint8_t* const half = half_of(c);
@@ -323,7 +334,7 @@ __global__ __launch_bounds__(320) void delta_walk_kernel(DeltaArgs a, DeltaSaved
         __syncthreads();
         uint8_t* const sk = half + O::K;
         const float* const sf = reinterpret_cast<const float*>(half + O::F);
-        if (SAVE && have) {
+        if (MODE == kSave && have) {
             float* to = keep.states + (static_cast<int64_t>(bh) * chunks + c) * P * N + static_cast<int64_t>(p) * N;
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
@@ -347,14 +358,14 @@ __global__ __launch_bounds__(320) void delta_walk_kernel(DeltaArgs a, DeltaSaved
 #pragma unroll
                 for (int i = 0; i < RT; ++i) {
                     MM::template mac<1, 3>(z[i], MM::template state_rows<W>(sk, 16 * i, kk, li, g4), s);
-                    if (!SAVE) MM::template mac<1, 3>(y[i], MM::template state_rows<W>(half + O::Qq, 16 * i, kk, li, g4), s);
+                    if (MODE == kOut) MM::template mac<1, 3>(y[i], MM::template state_rows<W>(half + O::Qq, 16 * i, kk, li, g4), s);
                 }
             }
             // Z = V - e^G K h^T, E = T Z
             scale_rows<STARTS>(z, sf, 1.0f, g4);
-            if (!SAVE) scale_rows<STARTS>(y, sf, a.scale, g4);
+            if (MODE == kOut) scale_rows<STARTS>(y, sf, a.scale, g4);
 #pragma unroll
-            for (int i = 0; i < RT; ++i) z[i] = MM::template four_rows<64>(half + O::V, 16 * i, w, li, g4) - z[i];
+            for (int i = 0; i < RT; ++i) z[i] = (rows ? f4{0, 0, 0, 0} : MM::template four_rows<64>(half + O::V, 16 * i, w, li, g4)) - z[i];
             kept_apart<STARTS>(x, z, sf + 3 * Q, marks % static_cast<int>(kNotFinite), g4, [&] {
 #pragma unroll
                 for (int kk = 0; kk < KT; ++kk) {
@@ -364,7 +375,7 @@ __global__ __launch_bounds__(320) void delta_walk_kernel(DeltaArgs a, DeltaSaved
                         MM::template mac<MM::TP, 3>(x[i], frag<MM, MM::TP>(half + O::T, frag_at<MM>(i, kk, false), lane), s);
                 }
             });
-            if (SAVE) {
+            if (MODE == kSave) {
                 const Buffer r = token_buffer<float>(keep.e, t0, static_cast<int64_t>(H) * P, static_cast<int64_t>(h) * P, DIRECT ? valid : 1, P);
 #pragma unroll
                 for (int i = 0; i < RT; ++i)
@@ -377,7 +388,7 @@ __global__ __launch_bounds__(320) void delta_walk_kernel(DeltaArgs a, DeltaSaved
             }
             // U = b E, Y += M U
             scale_rows<false>(x, sf + 2 * Q, 1.0f, g4);
-            if (!SAVE) {
+            if (MODE == kOut) {
 #pragma unroll
                 for (int kk = 0; kk < KT; ++kk) {
                     const auto s = MM::template of_tiles<MP>(x, kk);
@@ -411,12 +422,92 @@ __global__ __launch_bounds__(320) void delta_walk_kernel(DeltaArgs a, DeltaSaved
         else chunk(std::false_type{});
     }
     __syncthreads();
-    if (!SAVE && a.final_state && have) {
+    if (to && have) {
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             const int n = MM::state_row(i, g4);
-            if (n < N) *reinterpret_cast<f4*>(a.final_state + state + n) = hs[i];
+            if (n < N) *reinterpret_cast<f4*>(to + n) = hs[i];
         }
+    }
+}
+
+// ---------------------------------------------------------------------------------------
+// The states before the segments, h = h phi + gain from the first on (BACK: the gradients after them,
+// g = g phi^T + gain from the last on): 16 channels of a head a block, a wavefront 16 columns a
+// product of the fp32 instruction, the next segment's phi loaded meanwhile.
+// ---------------------------------------------------------------------------------------
+template <int Q, int NT, bool BACK>
+__global__ __launch_bounds__(NT < 8 ? 64 * NT : 512) void delta_join_states_kernel(DeltaArgs a) {
+    constexpr int WV = NT < 8 ? NT : 8, CT = NT / WV, LD = 16 * NT + 4;
+    __shared__ __attribute__((aligned(16))) float sh[16 * LD];
+    const int lane = threadIdx.x & 63, li = lane & 15, g4 = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int P = static_cast<int>(a.P), N = static_cast<int>(a.N), segs = static_cast<int>(a.segs);
+    const int ptiles = (P + 15) / 16, p0 = blockIdx.x % ptiles * 16;
+    const int64_t bh = blockIdx.x / ptiles;
+    const float* const first = BACK ? a.dhT : a.h0;
+    const int s0 = BACK ? segs - 1 : 0, step = BACK ? -1 : 1;
+    f4 h[CT];  // rows p0 + 4 g4 .., columns 16 (w + WV j) + li
+    const auto each = [&](auto f) {
+#pragma unroll
+        for (int j = 0; j < CT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int p = p0 + 4 * g4 + e, n = 16 * (w + WV * j) + li;
+                f(j, e, p, n, p < P && n < N);
+            }
+    };
+    each([&](int j, int e, int p, int n, bool in) { h[j][e] = in && first ? first[(bh * P + p) * N + n] : 0.0f; });
+    f4 next[CT][NT];
+    const auto load = [&](int s) {
+        const Buffer r = buffer(a.phi + (bh * segs + s) * N * N, static_cast<int64_t>(N) * N * 4);
+#pragma unroll
+        for (int j = 0; j < CT; ++j)
+#pragma unroll
+            for (int kk = 0; kk < NT; ++kk) {
+                const int n = 16 * (w + WV * j) + li, m = 16 * kk + 4 * g4;
+                if (BACK) {
+                    next[j][kk] = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(r, n < N && m < N ? (n * N + m) * 4 : kOutside, 0, 0));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) next[j][kk][e] = load_at<float>(r, n < N ? ((m + e) * N + n) * 4 : kOutside);
+                }
+            }
+    };
+    load(s0);
+    for (int i = 0; i < segs; ++i) {
+        const int s = s0 + step * i;
+        const int64_t at = (bh * segs + s) * P;
+        __syncthreads();
+        f4 gain[CT];
+        each([&](int j, int e, int p, int n, bool in) {
+            sh[(4 * g4 + e) * LD + n] = h[j][e];
+            gain[j][e] = 0.0f;
+            if (in) {
+                a.entry[(at + p) * N + n] = h[j][e];
+                if (i + 1 < segs) gain[j][e] = a.gain[(at + p) * N + n];
+            }
+        });
+        __syncthreads();
+        if (i + 1 == segs) break;
+        // with a start in the segment nothing of the state before it is left, finite or not
+        bool starts = false;
+        for (int64_t c = s * a.seg_chunks + lane; c < (s + 1) * a.seg_chunks && c < a.chunks; c += 64)
+            starts = starts || a.factors[((bh * a.chunks + c) * kFactors + 4) * Q - 1] != 0.0f;
+        const bool cut = __any(starts);
+        f4 sum[CT];
+#pragma unroll
+        for (int j = 0; j < CT; ++j) {
+            sum[j] = f4{0, 0, 0, 0};
+#pragma unroll
+            for (int kk = 0; kk < NT; ++kk) {
+                const f4 l = *reinterpret_cast<const f4*>(&sh[li * LD + 16 * kk + 4 * g4]);
+                ByF32::mac<1, 1>(sum[j], ByF32::Frag<1>{l}, ByF32::Frag<1>{next[j][kk]});
+            }
+        }
+        if (i + 2 < segs) load(s + step);
+#pragma unroll
+        for (int j = 0; j < CT; ++j) h[j] = cut ? gain[j] : sum[j] + gain[j];
     }
 }
 
@@ -552,21 +643,40 @@ void prep_of(const DeltaArgs& a, bool bwd, hipStream_t stream) {
     else if (a.direct) delta_prep_kernel<MM, NT, false, true><<<blocks, MM::Q * 4, 0, stream>>>(a);
     else delta_prep_kernel<MM, NT, false, false><<<blocks, MM::Q * 4, 0, stream>>>(a);
 }
-template <class MM, int NT, bool SAVE>
+template <class MM, int NT, int MODE>
 hipError_t walk_of(const DeltaArgs& a, const DeltaSaved& keep, hipStream_t stream) {
-    prep_of<MM, NT>(a, SAVE, stream);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const int64_t blocks = a.B * a.H * ((a.P + 63) / 64);
-    if (a.direct) delta_walk_kernel<MM, NT, SAVE, true><<<static_cast<unsigned>(blocks), 320, 0, stream>>>(a, keep);
-    else delta_walk_kernel<MM, NT, SAVE, false><<<static_cast<unsigned>(blocks), 320, 0, stream>>>(a, keep);
+    const int64_t all = (a.P + 63) / 64 + (MODE == kSpan ? (a.N + 63) / 64 : 0);
+    const unsigned blocks = static_cast<unsigned>(a.B * a.H * a.segs * all);
+    if (a.direct) delta_walk_kernel<MM, NT, MODE, true><<<blocks, 320, 0, stream>>>(a, keep);
+    else delta_walk_kernel<MM, NT, MODE, false><<<blocks, 320, 0, stream>>>(a, keep);
     return hipGetLastError();
+}
+template <class MM, int NT, bool BACK>
+hipError_t join_of(const DeltaArgs& a, hipStream_t stream) {
+    const unsigned blocks = static_cast<unsigned>(a.B * a.H * ((a.P + 15) / 16));
+    delta_join_states_kernel<MM::Q, NT, BACK><<<blocks, NT < 8 ? 64 * NT : 512, 0, stream>>>(a);
+    return hipGetLastError();
+}
+template <class MM>
+hipError_t join_back(const DeltaArgs& a, hipStream_t stream) {
+    if (a.N <= 64) return join_of<MM, 4, true>(a, stream);
+    if (a.N <= 128) return join_of<MM, 8, true>(a, stream);
+    return join_of<MM, 16, true>(a, stream);
+}
+template <class MM, int NT, bool SAVE>
+hipError_t rows_of_width(const DeltaArgs& a, const DeltaSaved& keep, hipStream_t stream) {
+    prep_of<MM, NT>(a, SAVE, stream);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && a.segs > 1) e = walk_of<MM, NT, kSpan>(a, keep, stream);
+    if (e == hipSuccess && a.segs > 1) e = join_of<MM, NT, false>(a, stream);
+    if (e == hipSuccess) e = walk_of<MM, NT, SAVE ? kSave : kOut>(a, keep, stream);
+    return e;
 }
 template <class MM, bool SAVE>
 hipError_t walk_by_width(const DeltaArgs& a, const DeltaSaved& keep, hipStream_t stream) {
-    if (a.N <= 64) return walk_of<MM, 4, SAVE>(a, keep, stream);
-    if (a.N <= 128) return walk_of<MM, 8, SAVE>(a, keep, stream);
-    return walk_of<MM, 16, SAVE>(a, keep, stream);
+    if (a.N <= 64) return rows_of_width<MM, 4, SAVE>(a, keep, stream);
+    if (a.N <= 128) return rows_of_width<MM, 8, SAVE>(a, keep, stream);
+    return rows_of_width<MM, 16, SAVE>(a, keep, stream);
 }
 template <class MM>
 hipError_t fwd_of(DeltaArgs a, void* workspace, hipStream_t stream) {
@@ -583,11 +693,18 @@ hipError_t launch_delta_walk_saved(const DeltaArgs& a, const DeltaSaved& s, ssm_
     return dtype == SSM_BF16 ? walk_by_width<ByBf16, true>(a, s, stream) : walk_by_width<ByF32, true>(a, s, stream);
 }
 
+hipError_t launch_delta_join_back(const DeltaArgs& a, ssm_dtype_t dtype, hipStream_t stream) {
+    return dtype == SSM_BF16 ? join_back<ByBf16>(a, stream) : join_back<ByF32>(a, stream);
+}
+
 size_t delta_fwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N, ssm_dtype_t dtype) {
     DeltaArgs a{};
     a.B = B;
     a.L = L;
     a.H = H;
+    a.P = P;
+    a.G = G;
+    a.N = N;
     return dtype == SSM_BF16 ? place_chunks<ByBf16>(a, nullptr, false) : place_chunks<ByF32>(a, nullptr, false);
 }
 

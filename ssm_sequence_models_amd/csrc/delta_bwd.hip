@@ -58,7 +58,8 @@ struct BackLds {
                          Qq = F + 1024, M = Qq + staged_bytes<MM, W>(), HALF = M + image_bytes<MM>(MP);
 };
 
-template <class MM, int NT, bool DIRECT>
+// SPAN: a segment from zero, only the gradient of the state before it
+template <class MM, int NT, bool SPAN, bool DIRECT>
 __global__ __launch_bounds__(320) void delta_back_kernel(DeltaArgs a, Buffers u) {
     using S = typename MM::S;
     using O = BackLds<MM, NT>;
@@ -69,9 +70,10 @@ __global__ __launch_bounds__(320) void delta_back_kernel(DeltaArgs a, Buffers u)
     const int H = static_cast<int>(a.H), P = static_cast<int>(a.P), N = static_cast<int>(a.N);
     const int pblocks = (P + 63) / 64, ptiles = (P + 15) / 16;
     const int unit = xcd_order(blockIdx.x, gridDim.x);
-    const int pb = unit % pblocks, bh = unit / pblocks, h = bh % H, b = bh / H;
-    const int g = h / (H / static_cast<int>(a.G));
-    const int chunks = static_cast<int>(a.chunks);
+    const int segs = static_cast<int>(a.segs), pb = unit % pblocks, seg = unit / pblocks % segs, bh = unit / pblocks / segs;
+    const int h = bh % H, b = bh / H, g = h / (H / static_cast<int>(a.G));
+    const int chunks = static_cast<int>(a.chunks), c0 = seg * static_cast<int>(a.seg_chunks);
+    const int c1 = c0 + static_cast<int>(a.seg_chunks) < chunks ? c0 + static_cast<int>(a.seg_chunks) : chunks;
     const auto rows_of = [&](int c) {
         const int64_t left = a.L - static_cast<int64_t>(c) * Q;
         return static_cast<int>(left < Q ? left : Q);
@@ -101,15 +103,15 @@ __global__ __launch_bounds__(320) void delta_back_kernel(DeltaArgs a, Buffers u)
             direct_image<image_bytes<MM>(MP)>(half + O::M, a.M + image * image_bytes<MM>(MP), lane);
             direct_image<kFactors * Q * 4>(half + O::F, reinterpret_cast<const uint8_t*>(a.factors + image * kFactors * Q), lane);
         };
-        if (O::HALVES == 2) fetch(chunks - 1);
-        for (int c = chunks - 1; c >= 0; --c) {
+        if (O::HALVES == 2) fetch(c1 - 1);
+        for (int c = c1 - 1; c >= c0; --c) {
             if (O::HALVES == 1) {
                 __syncthreads();
                 fetch(c);
             }
             wait_loads();
             __syncthreads();
-            if (O::HALVES == 2 && c > 0) fetch(c - 1);
+            if (O::HALVES == 2 && c > c0) fetch(c - 1);
             if (marks_of(half_of(c)) >= static_cast<int>(kNotFinite)) {
                 __syncthreads();
                 __syncthreads();
@@ -120,7 +122,9 @@ __global__ __launch_bounds__(320) void delta_back_kernel(DeltaArgs a, Buffers u)
 
     const int p0 = 64 * pb + 16 * w, p = p0 + li;
     const bool mine = p0 < P, have = p < P;
-    const int64_t state = (static_cast<int64_t>(bh) * P + p) * N, erow = static_cast<int64_t>(H) * P;
+    const int64_t erow = static_cast<int64_t>(H) * P, bhs = static_cast<int64_t>(bh) * segs + seg;
+    const float* const from = SPAN ? nullptr : segs > 1 ? a.entry + (bhs * P + p) * N : a.dhT ? a.dhT + (static_cast<int64_t>(bh) * P + p) * N : nullptr;
+    float* const dest = SPAN ? a.gain + (bhs * P + p) * N : a.dh0 && seg == 0 ? a.dh0 + (static_cast<int64_t>(bh) * P + p) * N : nullptr;
     const uint32_t eat = have ? 4 * g4 * static_cast<uint32_t>(erow) * 4 + p * 4 : kOutside;
     float en[RT][4];  // the next chunk's E
     const auto fetch_e = [&](int c) {
@@ -140,10 +144,10 @@ __global__ __launch_bounds__(320) void delta_back_kernel(DeltaArgs a, Buffers u)
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
         const int n = MM::state_row(i, g4);
-        dh[i] = have && n < N && a.dhT ? *reinterpret_cast<const f4*>(a.dhT + state + n) : f4{0, 0, 0, 0};
+        dh[i] = have && n < N && from ? *reinterpret_cast<const f4*>(from + n) : f4{0, 0, 0, 0};
     }
-    fetch_e(chunks - 1);
-    for (int c = chunks - 1; c >= 0; --c) {
+    if (!SPAN) fetch_e(c1 - 1);
+    for (int c = c1 - 1; c >= c0; --c) {
         const int64_t t0 = b * a.L + static_cast<int64_t>(c) * Q, image = static_cast<int64_t>(bh) * chunks + c;
         const int valid = rows_of(c);
         uint8_t* const half = half_of(c);
@@ -153,9 +157,9 @@ __global__ __launch_bounds__(320) void delta_back_kernel(DeltaArgs a, Buffers u)
 #pragma unroll
         for (int i = 0; i < RT; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) ev[i][e] = en[i][e];
-        if (c > 0) fetch_e(c - 1);
-        if (have) {
+            for (int e = 0; e < 4; ++e) ev[i][e] = SPAN ? 0.0f : en[i][e];
+        if (!SPAN && c > c0) fetch_e(c - 1);
+        if (!SPAN && have) {
             float* to = u.grads + image * P * N + static_cast<int64_t>(p) * N;
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
@@ -187,7 +191,7 @@ __global__ __launch_bounds__(320) void delta_back_kernel(DeltaArgs a, Buffers u)
             float* part = u.part + (image * ptiles + p0 / 16) * 2 * Q + 4 * g4 + li;
             scale_rows<STARTS>(du, sf + Q, 1.0f, g4);
 #pragma unroll
-            for (int i = 0; i < RT; ++i) {
+            for (int i = 0; i < (SPAN ? 0 : RT); ++i) {
                 const f4 v = du[i] * ev[i] * row4(sf + 2 * Q + 16 * i + 4 * g4);
                 const float s = row_sums({v[0], v[1], v[2], v[3]}, li);
                 if (mine && li < 4) part[Q + 16 * i] = s;
@@ -203,7 +207,7 @@ __global__ __launch_bounds__(320) void delta_back_kernel(DeltaArgs a, Buffers u)
                 }
             });
 #pragma unroll
-            for (int i = 0; i < RT; ++i) {
+            for (int i = 0; i < (SPAN ? 0 : RT); ++i) {
                 const f4 v = du[i] * ev[i];
                 const float s = row_sums({v[0], v[1], v[2], v[3]}, li);
                 if (mine && li < 4) part[16 * i] = s;
@@ -221,7 +225,7 @@ __global__ __launch_bounds__(320) void delta_back_kernel(DeltaArgs a, Buffers u)
             });
             const Buffer rz = token_buffer<float>(u.dz, t0, erow, static_cast<int64_t>(h) * P, DIRECT ? valid : 1, P);
 #pragma unroll
-            for (int i = 0; i < RT; ++i)
+            for (int i = 0; i < (SPAN ? 0 : RT); ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int t = 16 * i + 4 * g4 + e;
@@ -252,11 +256,11 @@ __global__ __launch_bounds__(320) void delta_back_kernel(DeltaArgs a, Buffers u)
         if (marks != 0) chunk(std::true_type{});
         else chunk(std::false_type{});
     }
-    if (a.dh0 && have) {
+    if (dest && have) {
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             const int n = MM::state_row(i, g4);
-            if (n < N) *reinterpret_cast<f4*>(a.dh0 + state + n) = dh[i];
+            if (n < N) *reinterpret_cast<f4*>(dest + n) = dh[i];
         }
     }
 }
@@ -768,12 +772,21 @@ size_t place(DeltaArgs& a, Buffers& u, uint8_t* ws) {
     return at;
 }
 
+template <class MM, int NT, bool SPAN>
+hipError_t back_of(const DeltaArgs& a, const Buffers& u, hipStream_t stream) {
+    const unsigned blocks = static_cast<unsigned>(a.B * a.H * a.segs * ((a.P + 63) / 64));
+    if (a.direct) delta_back_kernel<MM, NT, SPAN, true><<<blocks, 320, 0, stream>>>(a, u);
+    else delta_back_kernel<MM, NT, SPAN, false><<<blocks, 320, 0, stream>>>(a, u);
+    return hipGetLastError();
+}
 template <class MM, int NT>
 hipError_t kernels_of(const DeltaArgs& a, const Buffers& u, hipStream_t stream) {
-    const unsigned blocks = static_cast<unsigned>(a.B * a.H * ((a.P + 63) / 64));
-    if (a.direct) delta_back_kernel<MM, NT, true><<<blocks, 320, 0, stream>>>(a, u);
-    else delta_back_kernel<MM, NT, false><<<blocks, 320, 0, stream>>>(a, u);
-    hipError_t e = hipGetLastError();
+    hipError_t e = hipSuccess;
+    if (a.segs > 1) {
+        e = back_of<MM, NT, true>(a, u, stream);
+        if (e == hipSuccess) e = launch_delta_join_back(a, MM::TP == 1 ? SSM_F32 : SSM_BF16, stream);
+    }
+    if (e == hipSuccess) e = back_of<MM, NT, false>(a, u, stream);
     if (e != hipSuccess) return e;
     const unsigned grads = static_cast<unsigned>(a.B * a.chunks * a.G * u.splits);
     if (a.direct) delta_grad_kernel<MM, NT, true><<<grads, 64 * kGradWaves, 0, stream>>>(a, u);

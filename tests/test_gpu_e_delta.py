@@ -134,6 +134,40 @@ def test_long_row():
     _compare(_inputs(1, 1500, 2, 1, 64, 64, BF16, seed=6), seq=_seq(1, 1500, "random"))
 
 
+@pytest.mark.parametrize("dtype,B,L,H,G,P,N", [(BF16, 1, 2100, 1, 1, 64, 128), (BF16, 1, 1030, 3, 3, 80, 64), (F32, 1, 1100, 2, 1, 40, 48),
+                                               (BF16, 2, 1100, 1, 1, 16, 200), (F32, 1, 900, 1, 1, 32, 256)])
+def test_cut_rows(dtype, B, L, H, G, P, N):
+    """Few heads: rows in segments side by side, joined through what each makes of the state before it."""
+    _compare(_inputs(B, L, H, G, P, N, dtype, seed=L), scale=1.0)
+    s = _inputs(B, L, H, G, P, N, dtype, gate=False, states=False, seed=L + 1)
+    seq = torch.zeros(B, L, dtype=torch.int32)
+    seq[:, L // 3:] = 1
+    seq[0, L // 2 + 1:] = 2
+    _compare(s, scale=1.0, seq=seq)
+
+
+def test_cut_rows_stay_apart():
+    """A NaN in the first of two sequences leaves the segments behind its end as they are, and in the
+    second those before its start."""
+    s = _inputs(1, 2100, 1, 1, 64, 64, BF16, seed=18)
+    seq = torch.zeros(1, 2100, dtype=torch.int32)
+    seq[:, 1000:] = 1
+    clean = _run(s, 1.0, seq)
+    for name, at in (("v", 300), ("k", 999), ("dy", 1500), ("q", 1001)):
+        bad = dict(s, **{name: s[name].clone()})
+        bad[name].view(1, 2100, -1)[0, at, 0] = float("nan")
+        got = _run(bad, 1.0, seq)
+        for n, t in got.items():
+            if n == "final":
+                assert at >= 1000 or torch.equal(t, clean[n]), (name, n)
+            elif n == "dh0":
+                assert at < 1000 or torch.equal(t, clean[n]), (name, n)
+            elif at < 1000:
+                assert torch.equal(t[:, 1024:], clean[n][:, 1024:]), (name, n)
+            else:
+                assert torch.equal(t[:, :960], clean[n][:, :960]), (name, n)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_repeat_is_equal(dtype):
     s = _inputs(2, 300, 4, 1, 64, 128, dtype, seed=7)
