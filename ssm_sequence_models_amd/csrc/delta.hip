@@ -49,7 +49,7 @@ __global__ __launch_bounds__(MM::Q * 4) void delta_prep_kernel(DeltaArgs a) {
         const double end = __shfl(s.gates, Q - 1);
         const int rend = __shfl(s.starts, Q - 1);
         if (lane < Q) {
-            sg[lane] = s.gates;
+            sg[lane] = s.gates * kLog2e;
             sr[lane] = s.starts;
             sbeta[lane] = s.beta;
             float* f = a.factors + image * kFactors * Q;
@@ -105,14 +105,32 @@ __global__ __launch_bounds__(MM::Q * 4) void delta_prep_kernel(DeltaArgs a) {
 #pragma unroll
     for (int j = 0; j < RT; ++j) {
         if (j > w) continue;
+        const f4 be = *reinterpret_cast<const f4*>(&sbeta[16 * j + 4 * g4]);
+        f4 r;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int s = 16 * j + 4 * g4 + e;
-            const float r = s <= t && t < valid && sr[s] == rt ? exp_of(gt - sg[s]) : 0.0f;
-            // a factor of 0 leaves nothing of what is not finite either
-            sd[s * LD + t] = s < t && r != 0.0f ? r * kk[j][e] * sbeta[s] : 0.0f;
-            qk[j][e] = r != 0.0f ? r * qk[j][e] * a.scale : 0.0f;
+        for (int e = 0; e < 4; ++e) r[e] = exp2_of(gt - sg[16 * j + 4 * g4 + e]);
+        if (several) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) r[e] = sr[16 * j + 4 * g4 + e] == rt ? r[e] : 0.0f;
         }
+        f4 dd = r * kk[j] * be, mm = r * qk[j] * a.scale;
+        if (several) {  // another sequence's factor leaves nothing of what is not finite either
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                dd[e] = r[e] != 0.0f ? dd[e] : 0.0f;
+                mm[e] = r[e] != 0.0f ? mm[e] : 0.0f;
+            }
+        }
+        if (j == w) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                dd[e] = 4 * g4 + e < li ? dd[e] : 0.0f;
+                mm[e] = 4 * g4 + e <= li ? mm[e] : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sd[(16 * j + 4 * g4 + e) * LD + t] = dd[e];
+        qk[j] = mm;
     }
     __syncthreads();
     f4 x[RT];  // T's rows t: x[j][e] is T_ts of s = 16 j + 4 g4 + e

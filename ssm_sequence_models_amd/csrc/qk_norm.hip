@@ -29,42 +29,46 @@ struct Piece;
 template <>
 struct Piece<BF16> {
     static constexpr int V = 8;
-    __device__ __forceinline__ static void load(const uint16_t* p, float (&v)[8]) {
-        const u4e2 x = *reinterpret_cast<const u4e2*>(p);
+    __device__ __forceinline__ static u32x4_t raw(const uint16_t* p) { return *reinterpret_cast<const u4e2*>(p); }
+    __device__ __forceinline__ static u32x4_t pack(const float (&v)[8]) {  // of values that are bf16
+        return u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+    }
+    __device__ __forceinline__ static void values(u32x4_t x, float (&v)[8]) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(j & 1 ? x[j >> 1] & 0xFFFF0000u : x[j >> 1] << 16);
     }
     __device__ __forceinline__ static void store(uint16_t* p, const float (&v)[8]) {
-        u4e2 x;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-        *reinterpret_cast<u4e2*>(p) = x;
+        *reinterpret_cast<u4e2*>(p) = pack(v);
     }
 };
 template <>
 struct Piece<F32> {
     static constexpr int V = 4;
-    __device__ __forceinline__ static void load(const float* p, float (&v)[4]) {
-        const u4e4 x = *reinterpret_cast<const u4e4*>(p);
+    __device__ __forceinline__ static u32x4_t raw(const float* p) { return *reinterpret_cast<const u4e4*>(p); }
+    __device__ __forceinline__ static u32x4_t pack(const float (&v)[4]) {
+        return u32x4_t{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+    }
+    __device__ __forceinline__ static void values(u32x4_t x, float (&v)[4]) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(x[j]);
     }
     __device__ __forceinline__ static void store(float* p, const float (&v)[4]) {
-        u4e4 x;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = __float_as_uint(v[j]);
-        *reinterpret_cast<u4e4*>(p) = x;
+        *reinterpret_cast<u4e4*>(p) = pack(v);
     }
 };
 
-// a lane's piece of a head: channels i0 .. i0 + V of D, and how it takes part in the rotation
-template <class D>
+// How a call's heads lie in pieces: whole ones without rotation, with the partners of a piece in a piece
+// of their own (kHalves) or beside each other in it (kInterleaved), or any channels (kAny).
+enum { kPlain, kHalves, kInterleaved, kAny };
+
+// a lane's piece of a head: channels i0 .. i0 + have, and how it takes part in the rotation
+template <class D, int ROT>
 struct Lane {
     static constexpr int V = Piece<D>::V;
-    int i0, have;     // channels of the piece (V, fewer at the end of an odd D, 0 behind it)
-    bool turned;      // some of them are rotated
-    bool whole;       // partners are a piece of their own (or the same, interleaved)
-    int R, interleaved;
+    using T = typename D::T;
+    using Raw = decltype(Piece<D>::raw(nullptr));
+    int i0, have, R;
+    bool turned, interleaved;
 
     __device__ __forceinline__ Lane(const QkNormCall& c, int l) {
         i0 = l * V;
@@ -72,8 +76,7 @@ struct Lane {
         have = left < 0 ? 0 : left < V ? left : V;
         R = static_cast<int>(c.R);
         interleaved = c.interleaved;
-        turned = have > 0 && i0 < R;
-        whole = have == V && R % (interleaved ? V : 2 * V) == 0;
+        turned = ROT != kPlain && have > 0 && i0 < R;
     }
     __device__ __forceinline__ int partner(int i) const {
         return i >= R ? i : interleaved ? i ^ 1 : i < R / 2 ? i + R / 2 : i - R / 2;
@@ -81,32 +84,42 @@ struct Lane {
     __device__ __forceinline__ bool first(int i) const { return interleaved ? !(i & 1) : i < R / 2; }
     __device__ __forceinline__ int pair(int i) const { return interleaved ? i >> 1 : i < R / 2 ? i : i - R / 2; }
 
-    __device__ __forceinline__ void load(const typename D::T* p, float (&v)[V]) const {
-        if (have == V) {
-            Piece<D>::load(p + i0, v);
+    // a head's piece, and its partners', as loads in flight (kAny: values)
+    __device__ __forceinline__ Raw load(const T* p) const {
+        if constexpr (ROT != kAny) {
+            return have ? Piece<D>::raw(p + i0) : Raw{};
         } else {
+            float v[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) v[j] = j < have ? D::load(p, i0 + j) : 0.0f;
+            return Piece<D>::pack(v);
         }
     }
-    __device__ __forceinline__ void store(typename D::T* p, const float (&v)[V]) const {
+    __device__ __forceinline__ Raw load_partners(const T* p, Raw own) const {
+        if constexpr (ROT == kHalves) {
+            return turned ? Piece<D>::raw(p + (i0 < R / 2 ? i0 + R / 2 : i0 - R / 2)) : Raw{};
+        } else if constexpr (ROT == kAny) {
+            float v[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[j] = j < have ? D::load(p, partner(i0 + j)) : 0.0f;
+            return Piece<D>::pack(v);
+        } else {
+            return own;
+        }
+    }
+    __device__ __forceinline__ void partners(Raw r, float (&v)[V]) const {
+        float u[V];
+        Piece<D>::values(r, u);
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = ROT == kInterleaved ? u[j ^ 1] : u[j];
+    }
+    __device__ __forceinline__ void store(T* p, const float (&v)[V]) const {
         if (have == V) {
             Piece<D>::store(p + i0, v);
-        } else {
+        } else if (ROT == kAny) {
 #pragma unroll
             for (int j = 0; j < V; ++j)
                 if (j < have) D::store(p, i0 + j, v[j]);
-        }
-    }
-    __device__ __forceinline__ void load_partners(const typename D::T* p, const float (&own)[V], float (&v)[V]) const {
-        if (whole && interleaved) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) v[j] = own[j ^ 1];
-        } else if (whole) {
-            Piece<D>::load(p + partner(i0), v);
-        } else {
-#pragma unroll
-            for (int j = 0; j < V; ++j) v[j] = j < have ? D::load(p, partner(i0 + j)) : 0.0f;
         }
     }
     __device__ __forceinline__ void weights(const float* w, float (&own)[V], float (&other)[V]) const {
@@ -118,15 +131,36 @@ struct Lane {
     }
     // v turned by the token's angles (dir 1) or back (dir -1); `other` holds the partners
     __device__ __forceinline__ void turn(const float2* cs, float dir, float (&v)[V], const float (&other)[V]) const {
+        if constexpr (ROT == kInterleaved) {
+            const float2* a = cs + i0 / 2;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int i = i0 + j;
-            if (i >= R) continue;
-            const float2 a = cs[pair(i)];
-            v[j] = v[j] * a.x + other[j] * (first(i) ? -dir : dir) * a.y;
+            for (int j = 0; j < V; ++j) v[j] = v[j] * a[j / 2].x + other[j] * (j & 1 ? dir : -dir) * a[j / 2].y;
+        } else if constexpr (ROT == kHalves) {
+            const float2* a = cs + (i0 < R / 2 ? i0 : i0 - R / 2);
+            const float sign = i0 < R / 2 ? -dir : dir;
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[j] = v[j] * a[j].x + other[j] * sign * a[j].y;
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int i = i0 + j;
+                if (i >= R) continue;
+                const float2 a = cs[pair(i)];
+                v[j] = v[j] * a.x + other[j] * (first(i) ? -dir : dir) * a.y;
+            }
         }
     }
 };
+
+// the next head of a block's tokens that a head's lanes take
+__device__ __forceinline__ void next_head(int& token, int& head, int heads, int tokens_on, int heads_on) {
+    token += tokens_on;
+    head += heads_on;
+    if (head >= heads) {
+        head -= heads;
+        ++token;
+    }
+}
 
 template <int LPH>
 __device__ __forceinline__ float sum_lanes(float v) {  // over a head's lanes
@@ -156,30 +190,45 @@ __device__ __forceinline__ float inverse(float squares, const QkNormCall& c) {
     return v > 0.0f ? 1.0f / sqrtf(v) : v == 0.0f ? 0.0f : v;  // NaN stays one
 }
 
-template <class D, int LPH>
+// The next head's loads are in flight while one is computed.
+template <class D, int LPH, int ROT>
 __global__ __launch_bounds__(kThreads) void qk_norm_fwd_kernel(QkNormCall c, int tokens) {
     using T = typename D::T;
-    constexpr int V = Piece<D>::V;
-    __shared__ float2 cs[kMostTokens * 128];
+    using L = Lane<D, ROT>;
+    constexpr int V = L::V;
+    __shared__ __attribute__((aligned(16))) float2 cs[kMostTokens * 128];
     const int64_t first = static_cast<int64_t>(blockIdx.x) * tokens;
     if (c.tokens - first < tokens) tokens = static_cast<int>(c.tokens - first);
     if (c.R) {
         angles(c, cs, first, tokens);
         __syncthreads();
     }
-    const Lane<D> lane(c, threadIdx.x % LPH);
-    const int half = static_cast<int>(c.R / 2);
+    const L lane(c, threadIdx.x % LPH);
+    const int half = static_cast<int>(c.R / 2), D_ = static_cast<int>(c.D);
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
         const int heads = static_cast<int>(c.heads[side]);
+        const T* const xs = static_cast<const T*>(c.x[side]) + first * c.x_row[side];
+        T* const outs = static_cast<T*>(c.out[side]) + first * c.out_row[side];
         float w[V], wo[V];
         lane.weights(c.w[side], w, wo);
-        for (int u = threadIdx.x / LPH; u < tokens * heads; u += kThreads / LPH) {
-            const int token = u / heads, head = u % heads;
-            const T* x = static_cast<const T*>(c.x[side]) + (first + token) * c.x_row[side] + head * c.D;
-            float v[V], o[V];
-            lane.load(x, v);
-            if (lane.turned) lane.load_partners(x, v, o);
+        int token = threadIdx.x / LPH / heads, head = threadIdx.x / LPH % heads;
+        const int tokens_on = kThreads / LPH / heads, heads_on = kThreads / LPH % heads;
+        typename L::Raw x{}, o{};
+        const auto load = [&] {
+            if (token >= tokens) return;
+            const T* p = xs + token * c.x_row[side] + head * D_;
+            x = lane.load(p);
+            o = lane.load_partners(p, x);
+        };
+        load();
+        while (token < tokens) {
+            const int t = token, h = head;
+            float v[V], u[V];
+            Piece<D>::values(x, v);
+            lane.partners(o, u);
+            next_head(token, head, heads, tokens_on, heads_on);
+            load();
             float sum = 0.0f;
 #pragma unroll
             for (int j = 0; j < V; ++j) sum += v[j] * v[j];
@@ -188,52 +237,67 @@ __global__ __launch_bounds__(kThreads) void qk_norm_fwd_kernel(QkNormCall c, int
             for (int j = 0; j < V; ++j) v[j] *= r * w[j];
             if (lane.turned) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) o[j] *= r * wo[j];
-                lane.turn(cs + token * half, 1.0f, v, o);
+                for (int j = 0; j < V; ++j) u[j] *= r * wo[j];
+                lane.turn(cs + t * half, 1.0f, v, u);
             }
-            lane.store(static_cast<T*>(c.out[side]) + (first + token) * c.out_row[side] + head * c.D, v);
+            lane.store(outs + t * c.out_row[side] + h * D_, v);
         }
     }
 }
 
-// Blocks walk over the tokens; the sums for dw stay in the lanes of their channels to the end, are
-// added over a block's heads in LDS, and go out as a row a block (qk_norm_weights_kernel adds those).
-template <class D, int LPH>
+// Blocks walk over the tokens, queries first; the sums for dw stay in the lanes of their channels to the
+// end, are added over a block's heads in LDS, and go out as a row a block (qk_norm_weights_kernel adds
+// those).
+template <class D, int LPH, int ROT>
 __global__ __launch_bounds__(kThreads) void qk_norm_bwd_kernel(QkNormCall c, int most) {
     using T = typename D::T;
-    constexpr int V = Piece<D>::V, HEADS = kThreads / LPH;
-    __shared__ float2 cs[kMostTokens * 128];
+    using L = Lane<D, ROT>;
+    constexpr int V = L::V, HEADS = kThreads / LPH;
+    __shared__ __attribute__((aligned(16))) float2 cs[kMostTokens * 128];
     __shared__ float sums[HEADS][LPH * V];
-    const Lane<D> lane(c, threadIdx.x % LPH);
-    const int half = static_cast<int>(c.R / 2), hd = threadIdx.x / LPH;
+    const L lane(c, threadIdx.x % LPH);
+    const int half = static_cast<int>(c.R / 2), hd = threadIdx.x / LPH, D_ = static_cast<int>(c.D);
     const float per = c.l2 ? 1.0f : 1.0f / static_cast<float>(c.D);
-    float dw[2][V];
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side) {
+        const int heads = static_cast<int>(side ? c.heads[1] : c.heads[0]);
+        const int64_t x_row = side ? c.x_row[1] : c.x_row[0], dy_row = side ? c.dy_row[1] : c.dy_row[0],
+                      out_row = side ? c.out_row[1] : c.out_row[0];
+        const T* const xs = static_cast<const T*>(side ? c.x[1] : c.x[0]);
+        const T* const dys = static_cast<const T*>(side ? c.dy[1] : c.dy[0]);
+        T* const outs = static_cast<T*>(side ? c.out[1] : c.out[0]);
+        float w[V], unused[V], dw[V];
+        lane.weights(side ? c.w[1] : c.w[0], w, unused);
 #pragma unroll
-    for (int j = 0; j < V; ++j) dw[0][j] = dw[1][j] = 0.0f;
-    for (int64_t first = static_cast<int64_t>(blockIdx.x) * most; first < c.tokens;
-         first += static_cast<int64_t>(gridDim.x) * most) {
-        const int tokens = c.tokens - first < most ? static_cast<int>(c.tokens - first) : most;
-        if (c.R) {
-            __syncthreads();
-            angles(c, cs, first, tokens);
-            __syncthreads();
-        }
-#pragma unroll
-        for (int side = 0; side < 2; ++side) {
-            const int heads = static_cast<int>(c.heads[side]);
-            float w[V], unused[V];
-            lane.weights(c.w[side], w, unused);
-            for (int u = hd; u < tokens * heads; u += HEADS) {
-                const int token = u / heads, head = u % heads;
-                const T* x = static_cast<const T*>(c.x[side]) + (first + token) * c.x_row[side] + head * c.D;
-                const T* dy = static_cast<const T*>(c.dy[side]) + (first + token) * c.dy_row[side] + head * c.D;
-                float v[V], d[V], o[V];
-                lane.load(x, v);
-                lane.load(dy, d);
-                if (lane.turned) {
-                    lane.load_partners(dy, d, o);
-                    lane.turn(cs + token * half, -1.0f, d, o);
-                }
+        for (int j = 0; j < V; ++j) dw[j] = 0.0f;
+        const int tokens_on = HEADS / heads, heads_on = HEADS % heads;
+        for (int64_t first = static_cast<int64_t>(blockIdx.x) * most; first < c.tokens;
+             first += static_cast<int64_t>(gridDim.x) * most) {
+            const int tokens = c.tokens - first < most ? static_cast<int>(c.tokens - first) : most;
+            int token = hd / heads, head = hd % heads;
+            typename L::Raw x{}, y{}, o{};
+            const auto load = [&] {
+                if (token >= tokens) return;
+                const T* p = dys + (first + token) * dy_row + head * D_;
+                x = lane.load(xs + (first + token) * x_row + head * D_);
+                y = lane.load(p);
+                o = lane.load_partners(p, y);
+            };
+            load();
+            if (c.R) {
+                __syncthreads();
+                angles(c, cs, first, tokens);
+                __syncthreads();
+            }
+            while (token < tokens) {
+                const int t = token, h = head;
+                float v[V], d[V], u[V];
+                Piece<D>::values(x, v);
+                Piece<D>::values(y, d);
+                lane.partners(o, u);
+                next_head(token, head, heads, tokens_on, heads_on);
+                load();
+                if (lane.turned) lane.turn(cs + t * half, -1.0f, d, u);
                 float sum = 0.0f;
 #pragma unroll
                 for (int j = 0; j < V; ++j) sum += v[j] * v[j];
@@ -242,24 +306,20 @@ __global__ __launch_bounds__(kThreads) void qk_norm_bwd_kernel(QkNormCall c, int
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     v[j] *= r;
-                    dw[side][j] += d[j] * v[j];
+                    dw[j] += d[j] * v[j];
                     d[j] *= w[j];
                     dot += d[j] * v[j];
                 }
                 dot = sum_lanes<LPH>(dot) * per;
 #pragma unroll
                 for (int j = 0; j < V; ++j) d[j] = r * (d[j] - v[j] * dot);
-                lane.store(static_cast<T*>(c.out[side]) + (first + token) * c.out_row[side] + head * c.D, d);
+                lane.store(outs + (first + t) * out_row + h * D_, d);
             }
         }
-    }
-    if (!c.partial) return;
-    const int D_ = static_cast<int>(c.D);
-#pragma unroll
-    for (int side = 0; side < 2; ++side) {
+        if (!c.partial) continue;
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < V; ++j) sums[hd][lane.i0 + j] = dw[side][j];
+        for (int j = 0; j < V; ++j) sums[hd][lane.i0 + j] = dw[j];
         __syncthreads();
         if (static_cast<int>(threadIdx.x) < D_) {
             float s = 0.0f;
@@ -292,25 +352,29 @@ int tokens_a_block(int64_t tokens) {
     return n < 1 ? 1 : n > kMostTokens ? kMostTokens : static_cast<int>(n);
 }
 
-template <class D, int LPH>
-hipError_t fwd_of(const QkNormCall& c, hipStream_t s) {
+template <class D, int LPH, int ROT>
+void run(const QkNormCall& c, bool bwd, hipStream_t s) {
     const int n = tokens_a_block(c.tokens);
-    qk_norm_fwd_kernel<D, LPH><<<static_cast<unsigned>((c.tokens + n - 1) / n), kThreads, 0, s>>>(c, n);
-    return hipGetLastError();
+    if (bwd) qk_norm_bwd_kernel<D, LPH, ROT><<<static_cast<unsigned>(qk_norm_partial_rows(c.tokens)), kThreads, 0, s>>>(c, n);
+    else qk_norm_fwd_kernel<D, LPH, ROT><<<static_cast<unsigned>((c.tokens + n - 1) / n), kThreads, 0, s>>>(c, n);
 }
 template <class D, int LPH>
-hipError_t bwd_of(const QkNormCall& c, hipStream_t s) {
-    qk_norm_bwd_kernel<D, LPH><<<static_cast<unsigned>(qk_norm_partial_rows(c.tokens)), kThreads, 0, s>>>(
-        c, tokens_a_block(c.tokens));
+hipError_t by_rotation(const QkNormCall& c, bool bwd, hipStream_t s) {
+    constexpr int V = Piece<D>::V;
+    if (c.D % V != 0) run<D, LPH, kAny>(c, bwd, s);
+    else if (c.R == 0) run<D, LPH, kPlain>(c, bwd, s);
+    else if (c.interleaved && c.R % V == 0) run<D, LPH, kInterleaved>(c, bwd, s);
+    else if (!c.interleaved && c.R % (2 * V) == 0) run<D, LPH, kHalves>(c, bwd, s);
+    else run<D, LPH, kAny>(c, bwd, s);
     return hipGetLastError();
 }
 template <class D>
 hipError_t by_width(const QkNormCall& c, bool bwd, hipStream_t s) {
     const int64_t pieces = (c.D + Piece<D>::V - 1) / Piece<D>::V;
-    if (pieces <= 8) return bwd ? bwd_of<D, 8>(c, s) : fwd_of<D, 8>(c, s);
-    if (pieces <= 16) return bwd ? bwd_of<D, 16>(c, s) : fwd_of<D, 16>(c, s);
-    if (pieces <= 32) return bwd ? bwd_of<D, 32>(c, s) : fwd_of<D, 32>(c, s);
-    return bwd ? bwd_of<F32, 64>(c, s) : fwd_of<F32, 64>(c, s);  // fp32 only: D is at most 256
+    if (pieces <= 8) return by_rotation<D, 8>(c, bwd, s);
+    if (pieces <= 16) return by_rotation<D, 16>(c, bwd, s);
+    if (pieces <= 32 || Piece<D>::V == 8) return by_rotation<D, 32>(c, bwd, s);
+    return by_rotation<F32, 64>(c, bwd, s);  // fp32 only: D is at most 256
 }
 
 }  // namespace
