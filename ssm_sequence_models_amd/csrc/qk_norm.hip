@@ -122,11 +122,32 @@ struct Lane {
                 if (j < have) D::store(p, i0 + j, v[j]);
         }
     }
+    __device__ __forceinline__ static void floats(const float* p, float (&v)[V]) {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+            const u4e4 x = *reinterpret_cast<const u4e4*>(p + 4 * i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[4 * i + j] = __uint_as_float(x[j]);
+        }
+    }
     __device__ __forceinline__ void weights(const float* w, float (&own)[V], float (&other)[V]) const {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            own[j] = w && j < have ? w[i0 + j] : 1.0f;
-            other[j] = w && j < have ? w[partner(i0 + j)] : 1.0f;
+        for (int j = 0; j < V; ++j) own[j] = other[j] = 1.0f;
+        if (!w) return;
+        if constexpr (ROT == kAny) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                own[j] = j < have ? w[i0 + j] : 1.0f;
+                other[j] = j < have ? w[partner(i0 + j)] : 1.0f;
+            }
+        } else {  // lanes behind the head read its first piece
+            floats(w + (have ? i0 : 0), own);
+            if constexpr (ROT == kHalves) {
+                floats(w + (turned ? partner(i0) : 0), other);
+            } else if constexpr (ROT == kInterleaved) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) other[j] = own[j ^ 1];
+            }
         }
     }
     // v turned by the token's angles (dir 1) or back (dir -1); `other` holds the partners
@@ -346,15 +367,17 @@ __global__ __launch_bounds__(kThreads) void qk_norm_weights_kernel(QkNormCall c,
     if (threadIdx.x == 0) c.dw[side][i] = static_cast<float>(sums[0]);
 }
 
-// tokens a block: enough blocks for every CU before a block takes more than one
-int tokens_a_block(int64_t tokens) {
-    const int64_t n = tokens / 2048;
+// tokens a block at a time: enough blocks for every CU before a block takes more than one; backward
+// few partial rows and one round of blocks (3 x 1027 tokens x 8 heads x 80: 19 us for one token at a
+// time in three rounds)
+int tokens_a_block(int64_t tokens, bool bwd) {
+    const int64_t n = bwd ? (tokens + 1023) / 1024 : tokens / 2048;
     return n < 1 ? 1 : n > kMostTokens ? kMostTokens : static_cast<int>(n);
 }
 
 template <class D, int LPH, int ROT>
 void run(const QkNormCall& c, bool bwd, hipStream_t s) {
-    const int n = tokens_a_block(c.tokens);
+    const int n = tokens_a_block(c.tokens, bwd);
     if (bwd) qk_norm_bwd_kernel<D, LPH, ROT><<<static_cast<unsigned>(qk_norm_partial_rows(c.tokens)), kThreads, 0, s>>>(c, n);
     else qk_norm_fwd_kernel<D, LPH, ROT><<<static_cast<unsigned>((c.tokens + n - 1) / n), kThreads, 0, s>>>(c, n);
 }
@@ -380,7 +403,7 @@ hipError_t by_width(const QkNormCall& c, bool bwd, hipStream_t s) {
 }  // namespace
 
 int64_t qk_norm_partial_rows(int64_t tokens) {
-    const int64_t n = tokens_a_block(tokens), blocks = (tokens + n - 1) / n;
+    const int64_t n = tokens_a_block(tokens, true), blocks = (tokens + n - 1) / n;
     return blocks < 1024 ? blocks : 1024;
 }
 hipError_t launch_qk_norm_fwd(const QkNormCall& c, hipStream_t s) {
