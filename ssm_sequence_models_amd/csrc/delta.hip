@@ -23,40 +23,40 @@ using namespace delta;
 // everything where keys repeat: the powers of D grow as binomials while T itself stays small.)
 // ---------------------------------------------------------------------------------------
 template <class MM, int NT, bool BWD, bool DIRECT>
-__global__ __launch_bounds__(MM::Q * 4) void delta_prep_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(MM::Q * 4, NT <= 8 ? 4 : 1) void delta_prep_kernel(DeltaArgs a, int heads) {
     using S = typename MM::S;
     constexpr int Q = MM::Q, RT = Q / 16, KT = Q / MM::KB, LD = Q + 4, R = MM::R, KN = 16 * NT / MM::KB;
     constexpr int MP = m_parts<MM>(BWD);
     __shared__ __attribute__((aligned(16))) float sd[Q * LD];        // D transposed: [s][t]
     __shared__ __attribute__((aligned(16))) float sii[RT][16 * 20];  // T's diagonal blocks, transposed
-    __shared__ __attribute__((aligned(16))) float so[BWD ? Q * LD : 4];
-    __shared__ __attribute__((aligned(16))) double sg[Q];
+    float* const so = sd;  // T and M on the way out, once D is used up
+    __shared__ __attribute__((aligned(16))) double sgs[RT][Q];
     __shared__ __attribute__((aligned(16))) int sr[Q];
-    __shared__ __attribute__((aligned(16))) float sbeta[Q];
+    __shared__ __attribute__((aligned(16))) float sbetas[RT][Q];
     __shared__ int sbad;
-    const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g4 = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, li_ = lane & 15, g4_ = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int unit = xcd_order(blockIdx.x, gridDim.x);  // (b, chunk, h): the heads of a key head are neighbours
-    const int H = static_cast<int>(a.H), h = unit % H, bc = unit / H;
+    const int unit = xcd_order(blockIdx.x, gridDim.x);  // (b, chunk, heads): those of a key head are neighbours
+    const int H = static_cast<int>(a.H), ranges = H / heads, h0 = unit % ranges * heads, bc = unit / ranges;
     const int c = bc % static_cast<int>(a.chunks), b = bc / static_cast<int>(a.chunks);
-    const int64_t g = h / (H / static_cast<int>(a.G)), t0 = static_cast<int64_t>(c) * Q;
+    const int64_t g = h0 / (H / static_cast<int>(a.G)), t0 = static_cast<int64_t>(c) * Q;
     const int valid = static_cast<int>(a.L - t0 < Q ? a.L - t0 : Q), N = static_cast<int>(a.N);
-    const int64_t image = (static_cast<int64_t>(b) * H + h) * a.chunks + c;
+    const int64_t first_image = (static_cast<int64_t>(b) * H + h0) * a.chunks + c;
 
     if (tid == 0) sbad = 0;
-    if (w == RT - 1) {
-        const TokenSums s = token_sums<Q>(a, b, h, t0, valid, lane);
+    if (w < heads) {
+        const TokenSums s = token_sums<Q>(a, b, h0 + w, t0, valid, lane);
         const double end = __shfl(s.gates, Q - 1);
         const int rend = __shfl(s.starts, Q - 1);
         if (lane < Q) {
-            sg[lane] = s.gates * kLog2e;
-            sr[lane] = s.starts;
-            sbeta[lane] = s.beta;
+            const int64_t image = first_image + w * a.chunks;
+            sgs[w][lane] = s.gates * kLog2e;
+            sbetas[w][lane] = s.beta;
+            if (w == 0) sr[lane] = s.starts;
             float* f = a.factors + image * kFactors * Q;
             f[lane] = s.starts == 0 ? exp_of(s.gates) : 0.0f;
             f[Q + lane] = s.starts == rend ? exp_of(end - s.gates) : 0.0f;
             f[2 * Q + lane] = s.beta;
-            f[3 * Q + lane] = static_cast<float>(s.starts);
             if (BWD) a.gates[image * Q + lane] = s.gates;
         }
     }
@@ -70,7 +70,7 @@ __global__ __launch_bounds__(MM::Q * 4) void delta_prep_kernel(DeltaArgs a) {
     const Buffer rk = token_buffer<S>(a.k, first, a.k_row, g * a.N, DIRECT ? valid : 1, a.N);
     const Buffer rq = token_buffer<S>(a.q, first, a.q_row, g * a.N, DIRECT ? valid : 1, a.N);
     const auto load = [&](Buffer r, const S* p, int64_t row, int t, int kb) {
-        const int n = MM::KB * kb + R * g4;
+        const int n = MM::KB * kb + R * g4_;
         if (DIRECT)
             return __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(
                                               r, n < N ? (t * static_cast<uint32_t>(row) + n) * sizeof(S) : kOutside, 0, 0));
@@ -79,15 +79,15 @@ __global__ __launch_bounds__(MM::Q * 4) void delta_prep_kernel(DeltaArgs a) {
     bool bad = false;
     u4 fk[KN], fq[KN];
 #pragma unroll
-    for (int kb = 0; kb < KN; ++kb) fk[kb] = load(rk, kp, a.k_row, 16 * w + li, kb);
+    for (int kb = 0; kb < KN; ++kb) fk[kb] = load(rk, kp, a.k_row, 16 * w + li_, kb);
 #pragma unroll
-    for (int kb = 0; kb < KN; ++kb) fq[kb] = load(rq, qp, a.q_row, 16 * w + li, kb);
+    for (int kb = 0; kb < KN; ++kb) fq[kb] = load(rq, qp, a.q_row, 16 * w + li_, kb);
 #pragma unroll
     for (int j = 0; j < RT; ++j) {
         if (j > w) continue;
         u4 fs[KN];
 #pragma unroll
-        for (int kb = 0; kb < KN; ++kb) fs[kb] = j == w ? fk[kb] : load(rk, kp, a.k_row, 16 * j + li, kb);
+        for (int kb = 0; kb < KN; ++kb) fs[kb] = j == w ? fk[kb] : load(rk, kp, a.k_row, 16 * j + li_, kb);
 #pragma unroll
         for (int kb = 0; kb < KN; ++kb) {
             MM::template mac<1, 1>(kk[j], MM::exact(fs[kb]), MM::exact(fk[kb]));
@@ -99,124 +99,133 @@ __global__ __launch_bounds__(MM::Q * 4) void delta_prep_kernel(DeltaArgs a) {
     __syncthreads();
     const bool several = sr[Q - 1] != 0;
     if (bad && several) sbad = 1;
-    const int t = 16 * w + li;
-    const double gt = sg[t];
-    const int rt = sr[t];
+    for (int hh = 0; hh < heads; ++hh) {
+        const int li = here(li_), g4 = here(g4_);  // addresses are formed where they are used, not kept over the loop
+        const int t = 16 * w + li, rt = sr[t];
+        const int64_t image = first_image + hh * a.chunks;
+        const double* const sg = sgs[hh];
+        const float* const sbeta = sbetas[hh];
+        const double gt = sg[t];
+        f4 md[RT];  // M's rows t
 #pragma unroll
-    for (int j = 0; j < RT; ++j) {
-        if (j > w) continue;
-        const f4 be = *reinterpret_cast<const f4*>(&sbeta[16 * j + 4 * g4]);
-        f4 r;
+        for (int j = 0; j < RT; ++j) md[j] = f4{0, 0, 0, 0};
+        if (hh > 0) __syncthreads();  // D's place
 #pragma unroll
-        for (int e = 0; e < 4; ++e) r[e] = exp2_of(gt - sg[16 * j + 4 * g4 + e]);
+        for (int j = 0; j < RT; ++j) {
+            if (j > w) continue;
+            const f4 be = *reinterpret_cast<const f4*>(&sbeta[16 * j + 4 * g4]);
+            f4 r;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) r[e] = exp2_of(gt - sg[16 * j + 4 * g4 + e]);
+            if (several) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) r[e] = sr[16 * j + 4 * g4 + e] == rt ? r[e] : 0.0f;
+            }
+            f4 dd = r * kk[j] * be, mm = r * qk[j] * a.scale;
+            if (several) {  // another sequence's factor leaves nothing of what is not finite either
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    dd[e] = r[e] != 0.0f ? dd[e] : 0.0f;
+                    mm[e] = r[e] != 0.0f ? mm[e] : 0.0f;
+                }
+            }
+            if (j == w) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    dd[e] = 4 * g4 + e < li ? dd[e] : 0.0f;
+                    mm[e] = 4 * g4 + e <= li ? mm[e] : 0.0f;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sd[(16 * j + 4 * g4 + e) * LD + t] = dd[e];
+            md[j] = mm;
+        }
+        __syncthreads();
+        f4 x[RT];  // T's rows t: x[j][e] is T_ts of s = 16 j + 4 g4 + e
+        {          // the diagonal block, row li of it in every g4
+            float v[16];
+#pragma unroll
+            for (int j = 15; j >= 0; --j) {
+                float sum = j == li ? 1.0f : 0.0f;
+#pragma unroll
+                for (int m = j + 1; m < 16; ++m) sum -= v[m] * sd[(16 * w + j) * LD + 16 * w + m];
+                v[j] = j > li ? 0.0f : sum;  // nothing above the diagonal, whatever D holds
+            }
+            f4 d;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                d[e] = g4 == 0 ? v[e] : g4 == 1 ? v[4 + e] : g4 == 2 ? v[8 + e] : v[12 + e];
+                sii[w][(4 * g4 + e) * 20 + li] = d[e];
+            }
+#pragma unroll
+            for (int j = 0; j < RT; ++j) x[j] = j == w ? d : f4{0, 0, 0, 0};
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = RT - 2; j >= 0; --j) {
+            if (j >= w) continue;
+            f4 sum{0, 0, 0, 0}, out{0, 0, 0, 0};
+#pragma unroll
+            for (int m = j + 1; m < RT; ++m) {
+                if (m > w) continue;
+                const f4 l = *reinterpret_cast<const f4*>(&sd[(16 * j + li) * LD + 16 * m + 4 * g4]);
+                ByF32::mac<1, 1>(sum, ByF32::Frag<1>{l}, ByF32::Frag<1>{x[m]});
+            }
+            if (several) {  // sequences apart: a 0 of another's is not one times what is not finite
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (sr[16 * j + 4 * g4 + e] != rt) sum[e] = 0.0f;
+            }
+            const f4 l = *reinterpret_cast<const f4*>(&sii[j][li * 20 + 4 * g4]);
+            ByF32::mac<1, 1>(out, ByF32::Frag<1>{l}, ByF32::Frag<1>{sum});
+            x[j] = -out;
+        }
         if (several) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) r[e] = sr[16 * j + 4 * g4 + e] == rt ? r[e] : 0.0f;
-        }
-        f4 dd = r * kk[j] * be, mm = r * qk[j] * a.scale;
-        if (several) {  // another sequence's factor leaves nothing of what is not finite either
+            for (int j = 0; j < RT; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                dd[e] = r[e] != 0.0f ? dd[e] : 0.0f;
-                mm[e] = r[e] != 0.0f ? mm[e] : 0.0f;
+                for (int e = 0; e < 4; ++e)
+                    if (sr[16 * j + 4 * g4 + e] != rt) x[j][e] = 0.0f;
+        }
+        if (tid < Q) a.factors[image * kFactors * Q + 3 * Q + tid] = static_cast<float>(sr[tid]) + (sbad ? kNotFinite : 0.0f);
+        uint8_t* T = a.T + image * image_bytes<MM>(MM::TP);
+        uint8_t* M = a.M + image * image_bytes<MM>(MP);
+        const auto put = [&](uint8_t* to, const auto& f, auto parts) {
+#pragma unroll
+            for (int p = 0; p < parts(); ++p) {
+                if constexpr (MM::TP == 1) *reinterpret_cast<f4*>(to + lane * 16) = f.v;
+                else *reinterpret_cast<bf8*>(to + p * 1024 + lane * 16) = f.p[p];
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            if (i != w) continue;
+#pragma unroll
+            for (int kb = 0; kb <= 16 * i / MM::KB; ++kb) {
+                put(T + frag_at<MM>(i, kb, false) * MM::TP * 1024, MM::template of_tiles<MM::TP>(x, kb), [] { return MM::TP; });
+                if (!BWD) put(M + frag_at<MM>(i, kb, false) * MP * 1024, MM::template of_tiles<MP>(md, kb), [] { return MP; });
             }
         }
-        if (j == w) {
+        if constexpr (BWD) {  // T and M once more with rows s: their columns through LDS
+            uint8_t* Tt = a.Tt + image * image_bytes<MM>(MM::TP);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                dd[e] = 4 * g4 + e < li ? dd[e] : 0.0f;
-                mm[e] = 4 * g4 + e <= li ? mm[e] : 0.0f;
-            }
-        }
+            for (int pass = 0; pass < 2; ++pass) {
+                __syncthreads();
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sd[(16 * j + 4 * g4 + e) * LD + t] = dd[e];
-        qk[j] = mm;
-    }
-    __syncthreads();
-    f4 x[RT];  // T's rows t: x[j][e] is T_ts of s = 16 j + 4 g4 + e
-    {          // the diagonal block, row li of it in every g4
-        float v[16];
+                for (int j = 0; j < RT; ++j) *reinterpret_cast<f4*>(&so[t * LD + 16 * j + 4 * g4]) = pass ? md[j] : x[j];
+                __syncthreads();
 #pragma unroll
-        for (int j = 15; j >= 0; --j) {
-            float sum = j == li ? 1.0f : 0.0f;
+                for (int kb = 0; kb < KT; ++kb) {
+                    if ((kb + 1) * MM::KB <= 16 * w) continue;
+                    float v[R];
 #pragma unroll
-            for (int m = j + 1; m < 16; ++m) sum -= v[m] * sd[(16 * w + j) * LD + 16 * w + m];
-            v[j] = j > li ? 0.0f : sum;  // nothing above the diagonal, whatever D holds
-        }
-        f4 d;
+                    for (int m = 0; m < R; ++m) v[m] = so[(MM::KB * kb + (m >> 2) * 16 + 4 * g4 + (m & 3)) * LD + t];
+                    const auto f = MM::template parts<MM::TP>(v);
+                    uint8_t* to = pass ? M : Tt;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            d[e] = g4 == 0 ? v[e] : g4 == 1 ? v[4 + e] : g4 == 2 ? v[8 + e] : v[12 + e];
-            sii[w][(4 * g4 + e) * 20 + li] = d[e];
-        }
-#pragma unroll
-        for (int j = 0; j < RT; ++j) x[j] = j == w ? d : f4{0, 0, 0, 0};
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = RT - 2; j >= 0; --j) {
-        if (j >= w) continue;
-        f4 sum{0, 0, 0, 0}, out{0, 0, 0, 0};
-#pragma unroll
-        for (int m = j + 1; m < RT; ++m) {
-            if (m > w) continue;
-            const f4 l = *reinterpret_cast<const f4*>(&sd[(16 * j + li) * LD + 16 * m + 4 * g4]);
-            ByF32::mac<1, 1>(sum, ByF32::Frag<1>{l}, ByF32::Frag<1>{x[m]});
-        }
-        if (several) {  // sequences apart: a 0 of another's is not one times what is not finite
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (sr[16 * j + 4 * g4 + e] != rt) sum[e] = 0.0f;
-        }
-        const f4 l = *reinterpret_cast<const f4*>(&sii[j][li * 20 + 4 * g4]);
-        ByF32::mac<1, 1>(out, ByF32::Frag<1>{l}, ByF32::Frag<1>{sum});
-        x[j] = -out;
-    }
-    if (several) {
-#pragma unroll
-        for (int j = 0; j < RT; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (sr[16 * j + 4 * g4 + e] != rt) x[j][e] = 0.0f;
-    }
-    if (sbad && tid < Q) a.factors[image * kFactors * Q + 3 * Q + tid] = static_cast<float>(sr[tid]) + kNotFinite;
-    uint8_t* T = a.T + image * image_bytes<MM>(MM::TP);
-    uint8_t* M = a.M + image * image_bytes<MM>(MP);
-    const auto put = [&](uint8_t* to, const auto& f, auto parts) {
-#pragma unroll
-        for (int p = 0; p < parts(); ++p) {
-            if constexpr (MM::TP == 1) *reinterpret_cast<f4*>(to + lane * 16) = f.v;
-            else *reinterpret_cast<bf8*>(to + p * 1024 + lane * 16) = f.p[p];
-        }
-    };
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-        if (i != w) continue;
-#pragma unroll
-        for (int kb = 0; kb <= 16 * i / MM::KB; ++kb) {
-            put(T + frag_at<MM>(i, kb, false) * MM::TP * 1024, MM::template of_tiles<MM::TP>(x, kb), [] { return MM::TP; });
-            if (!BWD) put(M + frag_at<MM>(i, kb, false) * MP * 1024, MM::template of_tiles<MP>(qk, kb), [] { return MP; });
-        }
-    }
-    if constexpr (BWD) {  // T and M once more with rows s: their columns through LDS
-        uint8_t* Tt = a.Tt + image * image_bytes<MM>(MM::TP);
-#pragma unroll
-        for (int pass = 0; pass < 2; ++pass) {
-            __syncthreads();
-#pragma unroll
-            for (int j = 0; j < RT; ++j) *reinterpret_cast<f4*>(&so[t * LD + 16 * j + 4 * g4]) = pass ? qk[j] : x[j];
-            __syncthreads();
-#pragma unroll
-            for (int kb = 0; kb < KT; ++kb) {
-                if ((kb + 1) * MM::KB <= 16 * w) continue;
-                float v[R];
-#pragma unroll
-                for (int m = 0; m < R; ++m) v[m] = so[(MM::KB * kb + (m >> 2) * 16 + 4 * g4 + (m & 3)) * LD + t];
-                const auto f = MM::template parts<MM::TP>(v);
-                uint8_t* to = pass ? M : Tt;
-#pragma unroll
-                for (int i = 0; i < RT; ++i)
-                    if (i == w) put(to + frag_at<MM>(i, kb, true) * MM::TP * 1024, f, [] { return MM::TP; });
+                    for (int i = 0; i < RT; ++i)
+                        if (i == w) put(to + frag_at<MM>(i, kb, true) * MM::TP * 1024, f, [] { return MM::TP; });
+                }
             }
         }
     }
@@ -655,11 +664,14 @@ hipError_t step_by_width(const DeltaStep& s, hipStream_t stream) {
 
 template <class MM, int NT>
 void prep_of(const DeltaArgs& a, bool bwd, hipStream_t stream) {
-    const unsigned blocks = static_cast<unsigned>(a.B * a.H * a.chunks);
-    if (bwd && a.direct) delta_prep_kernel<MM, NT, true, true><<<blocks, MM::Q * 4, 0, stream>>>(a);
-    else if (bwd) delta_prep_kernel<MM, NT, true, false><<<blocks, MM::Q * 4, 0, stream>>>(a);
-    else if (a.direct) delta_prep_kernel<MM, NT, false, true><<<blocks, MM::Q * 4, 0, stream>>>(a);
-    else delta_prep_kernel<MM, NT, false, false><<<blocks, MM::Q * 4, 0, stream>>>(a);
+    // a key head's heads share the products: up to one a wavefront, as long as there are blocks for all CUs
+    int heads = 1;
+    while (2 * heads <= MM::Q / 16 && a.H / a.G % (2 * heads) == 0 && a.B * a.chunks * a.H / (2 * heads) >= 1024) heads *= 2;
+    const unsigned blocks = static_cast<unsigned>(a.B * a.chunks * (a.H / heads));
+    if (bwd && a.direct) delta_prep_kernel<MM, NT, true, true><<<blocks, MM::Q * 4, 0, stream>>>(a, heads);
+    else if (bwd) delta_prep_kernel<MM, NT, true, false><<<blocks, MM::Q * 4, 0, stream>>>(a, heads);
+    else if (a.direct) delta_prep_kernel<MM, NT, false, true><<<blocks, MM::Q * 4, 0, stream>>>(a, heads);
+    else delta_prep_kernel<MM, NT, false, false><<<blocks, MM::Q * 4, 0, stream>>>(a, heads);
 }
 template <class MM, int NT, int MODE>
 hipError_t walk_of(const DeltaArgs& a, const DeltaSaved& keep, hipStream_t stream) {
