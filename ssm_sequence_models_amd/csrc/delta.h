@@ -395,12 +395,14 @@ __device__ __forceinline__ void store_at(Buffer r, uint32_t at, float v) {
 // LDS of a tile of W columns that one wavefront stages: whole kilobytes
 template <class MM, int W>
 constexpr int staged_bytes() { return (MM::template tile_bytes<W>(MM::Q) + 1023) / 1024 * 1024; }
-// a tile's rows straight into LDS by one wavefront: N columns, zeros past them and past the rows
-template <class MM, int W, bool STATE>
-__device__ __forceinline__ void direct_rows(uint8_t* tile, Buffer r, int row, int N, int lane) {
+// a tile's rows straight into LDS by WAVES wavefronts (w of them): N columns, zeros past them and past the rows
+template <class MM, int W, bool STATE, int WAVES = 1>
+__device__ __forceinline__ void direct_rows(uint8_t* tile, Buffer r, int row, int N, int lane, int w = 0) {
     constexpr int ES = sizeof(typename MM::S), SLOTS = MM::template tile_bytes<W>(MM::Q) / MM::Q / 16;
 #pragma unroll
-    for (int i = 0; i < staged_bytes<MM, W>() / 1024; ++i) {
+    for (int at = 0; at < staged_bytes<MM, W>() / 1024; at += WAVES) {
+        const int i = at + w;
+        if (WAVES > 1 && i >= staged_bytes<MM, W>() / 1024) continue;
         const int slot = 64 * i + lane, t = slot / SLOTS;
         const int n = STATE ? MM::template state_column<W>(t, slot % SLOTS) : MM::template column_of<W>(t, slot % SLOTS);
         to_lds(r, t < MM::Q && n < N ? (t * row + n) * ES : kOutside, tile + 1024 * i);

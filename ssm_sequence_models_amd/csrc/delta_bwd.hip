@@ -36,13 +36,6 @@ struct Buffers {
     int64_t splits, heads;  // ranges of a key head's heads, and heads in each
 };
 
-__device__ __forceinline__ float sum16(float v) {  // over the 16 lanes that share g4
-    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xf, 0xf, true));
-    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xf, 0xf, true));
-    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xf, 0xf, true));
-    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 0xf, 0xf, true));
-    return v;
-}
 __device__ __forceinline__ float sum_groups(float v) {  // over the four lanes that share li
     v += __shfl_xor(v, 16);
     return v + __shfl_xor(v, 32);
@@ -319,7 +312,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void delta_grad_kernel(DeltaArgs a
     constexpr int CT = NT / CG, RW = RT / RG;           // a wavefront's column and row tiles
     constexpr int TILES = RT * (RT + 1) / 2, MINE = (TILES + WV - 1) / WV;
     constexpr int TP = MM::TP, XP = TP == 1 ? 1 : 2;
-    constexpr int QN = MM::template tile_bytes<W>(Q), QP = MM::template tile_bytes<64>(Q), QQ = MM::template tile_bytes<Q>(Q);
+    constexpr int QN = staged_bytes<MM, W>(), QP = MM::template tile_bytes<64>(Q), QQ = MM::template tile_bytes<Q>(Q);
     constexpr int LOADS = (1 + 2 * TP) * QP, PAIRS = (2 * XP + TP) * QQ;
     __shared__ __attribute__((aligned(16))) uint8_t sk[QN];
     __shared__ __attribute__((aligned(16))) uint8_t sq[QN];
@@ -350,8 +343,13 @@ __global__ __launch_bounds__(64 * kGradWaves) void delta_grad_kernel(DeltaArgs a
     const int N = static_cast<int>(a.N), P = static_cast<int>(a.P);
     const int64_t t0 = b * a.L + c * Q;
 
-    stage_rows<MM, W, 64 * WV, false>(sk, static_cast<const S*>(a.k) + t0 * a.k_row + g * a.N, a.k_row, valid, N);
-    stage_rows<MM, W, 64 * WV, false>(sq, static_cast<const S*>(a.q) + t0 * a.q_row + g * a.N, a.q_row, valid, N);
+    if (DIRECT) {  // on their way while the first loads below are issued; waited for at the head's first barrier
+        direct_rows<MM, W, false, WV>(sk, token_buffer<S>(a.k, t0, a.k_row, g * a.N, valid, N), static_cast<int>(a.k_row), N, lane, w);
+        direct_rows<MM, W, false, WV>(sq, token_buffer<S>(a.q, t0, a.q_row, g * a.N, valid, N), static_cast<int>(a.q_row), N, lane, w);
+    } else {
+        stage_rows<MM, W, 64 * WV, false>(sk, static_cast<const S*>(a.k) + t0 * a.k_row + g * a.N, a.k_row, valid, N);
+        stage_rows<MM, W, 64 * WV, false>(sq, static_cast<const S*>(a.q) + t0 * a.q_row + g * a.N, a.q_row, valid, N);
+    }
     f4 dq[RW][CT], dk[RW][CT];
 #pragma unroll
     for (int i = 0; i < RW; ++i)
@@ -434,6 +432,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void delta_grad_kernel(DeltaArgs a
     load_factors(h0);
     load_tokens(h0, 0);
     load_states(h0, 0);
+    if (DIRECT) wait_loads();
     for (int64_t h = h0; h < h1; ++h) {
         const int64_t image = (b * a.H + h) * a.chunks + c;
         f4 qo[RW][CT], ko[RW][CT], ke[RW][CT], dm[MINE], db[MINE];
@@ -537,8 +536,8 @@ __global__ __launch_bounds__(64 * kGradWaves) void delta_grad_kernel(DeltaArgs a
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int t = 16 * rt + 4 * g4 + e;
-                const float r = s <= t && sf[3 * Q + s] == sf[3 * Q + t] ? exp_of(sg[t] - sg[s]) : 0.0f;
-                const bool on = r != 0.0f, below = on && s < t;
+                const bool one = sf[3 * Q + s] == sf[3 * Q + t], on = one && s <= t, below = one && s < t;
+                const float r = exp_of(sg[t] - sg[s]);
                 const float x = on ? r * a.scale * be * dm[m][e] : 0.0f;
                 const float f = below ? -r * db[m][e] : 0.0f;
                 const float pair = below ? x * qk[e] + f * be * kk[e] : 0.0f;
@@ -556,24 +555,32 @@ __global__ __launch_bounds__(64 * kGradWaves) void delta_grad_kernel(DeltaArgs a
             if (g4 == 0) sdb[rt][s] = sum;
         }
         // products with h_0, for dgate
+        const bool several = sf[4 * Q - 1] != 0.0f;
 #pragma unroll
         for (int i = 0; i < RW; ++i) {
             const int li = here(li_), g4 = here(g4_);
             const int r0 = 16 * (rg * RW + i) + 4 * g4;
             const f4 f = row4(sf + r0);
+float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float sum = 0.0f;
+            for (int j = 0; j < CT; ++j) {
+                const int n = 16 * (cg * CT + j) + li;
+                qo[i][j] *= f * a.scale;
+                ko[i][j] *= -f;
+                if (several) {
 #pragma unroll
-                for (int j = 0; j < CT; ++j) {
-                    const int n = 16 * (cg * CT + j) + li;
-                    qo[i][j][e] = f[e] != 0.0f ? f[e] * a.scale * qo[i][j][e] : 0.0f;
-                    ko[i][j][e] = f[e] != 0.0f ? -f[e] * ko[i][j][e] : 0.0f;
-                    sum += qo[i][j][e] * MM::template at<W>(sq, r0 + e, n) + ko[i][j][e] * MM::template at<W>(sk, r0 + e, n);
+                    for (int e = 0; e < 4; ++e) {
+                        qo[i][j][e] = f[e] != 0.0f ? qo[i][j][e] : 0.0f;
+                        ko[i][j][e] = f[e] != 0.0f ? ko[i][j][e] : 0.0f;
+                    }
                 }
-                sum = sum16(sum);
-                if (li == 0) sc[cg][r0 + e] = sum;
+                const f4 q4 = MM::template four_rows<W>(sq, 16 * (rg * RW + i), cg * CT + j, li, g4);
+                const f4 k4 = MM::template four_rows<W>(sk, 16 * (rg * RW + i), cg * CT + j, li, g4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] += qo[i][j][e] * q4[e] + ko[i][j][e] * k4[e];
             }
+            const float sum = row_sums(v, li);
+            if (li < 4) sc[cg][r0 + li] = sum;
         }
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) dot += __shfl_xor(dot, d);
@@ -612,7 +619,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void delta_grad_kernel(DeltaArgs a
                 const int ct = cg * CT + j;
                 dq[i][j] += qo[i][j];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) dk[i][j][e] += ko[i][j][e] + (f[e] != 0.0f ? f[e] * ke[i][j][e] : 0.0f);
+                for (int e = 0; e < 4; ++e) dk[i][j][e] += ko[i][j][e] + (several && f[e] == 0.0f ? 0.0f : f[e] * ke[i][j][e]);
 #pragma unroll
                 for (int kk = 0; kk < KT; ++kk) {
                     const auto fk = MM::template columns<W>(sk, kk * MM::KB, ct, li, g4);
