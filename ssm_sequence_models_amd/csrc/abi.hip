@@ -1520,7 +1520,7 @@ ssm_status_t ssm_delta_scan_step(const void* q, int64_t q_row, const void* k, in
     d.a.P = headdim;
     d.a.G = ngroups;
     d.a.N = dstate;
-    d.state_in = d.state_out = state;
+    d.state = state;
     d.slots = state_indices;
     d.n_slots = n_slots;
     return hip_status(ssm::launch_delta_step(d, dtype, reinterpret_cast<hipStream_t>(stream)), fn);

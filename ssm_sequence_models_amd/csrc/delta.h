@@ -44,14 +44,15 @@ struct DeltaArgs {
     int64_t q_row, k_row, v_row, y_row, dy_row, dq_row, dk_row, dv_row;
     int64_t B, L, H, P, G, N;
     float scale;
-    // set by the launchers: whether tokens go straight into LDS (16-byte aligned rows, dstate and headdim whole
-    // pieces, a chunk's rows of every token tensor within 31 bits of bytes); the chunks' part of the workspace
+    // set by the launchers: whether tokens go straight into LDS (16-byte aligned rows that do not overlap, dstate
+    // and headdim whole pieces, a chunk's rows of every token tensor within 30 bits of bytes); the chunks' part
+    // of the workspace
     bool direct;
     int64_t chunks;
     uint8_t* T;      // [B, H, chunks] images
     uint8_t* M;
     uint8_t* Tt;     // transposed, backward only (M is transposed there)
-    // rows cut into `segs` segments of seg_chunks chunks where there are few (delta_join in delta.hip)
+    // rows cut into `segs` segments of seg_chunks chunks where there are few (plan_segments)
     int64_t segs, seg_chunks;
     float* phi;      // [B, H, segs, N, N]: what a segment makes of the state before it, from the right
     float* gain;     // [B, H, segs, P, N]: what its own tokens bring
@@ -74,8 +75,6 @@ __device__ __forceinline__ double gate_of(float g) { return g < kLeastGate ? kLe
 
 // e^x of a sum kept in double
 __device__ __forceinline__ float exp_of(double x) { return exp2_of(x * kLog2e); }
-
-__device__ __forceinline__ float get(f4 v, int e) { return v[e]; }
 
 // ---------------------------------------------------------------------------------------
 // bf16: exact operands as they are, fp32 operands in bf16 parts (three hold all 24 bits)
@@ -534,8 +533,10 @@ __device__ __forceinline__ TokenSums token_sums(const DeltaArgs& a, int64_t b, i
     return s;
 }
 
-inline bool direct_rows_fit(const void* p, int64_t row, size_t es) {
-    return row < (int64_t{1} << 30) / 64 / static_cast<int64_t>(es) && reinterpret_cast<uintptr_t>(p) % 16 == 0 && row * es % 16 == 0;
+// (rows that overlap, a token that stands for all of them say, do not end where a buffer of them ends)
+inline bool direct_rows_fit(const void* p, int64_t row, int64_t width, size_t es) {
+    return row >= width && row < (int64_t{1} << 30) / 64 / static_cast<int64_t>(es) &&
+           reinterpret_cast<uintptr_t>(p) % 16 == 0 && row * es % 16 == 0;
 }
 
 // Rows are cut into segments where their walks do not fill the 256 CUs: all segments from zero, with the
@@ -604,12 +605,11 @@ size_t delta_fwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t P, int
 size_t delta_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N, ssm_dtype_t dtype);
 hipError_t launch_delta_fwd(DeltaArgs a, void* workspace, ssm_dtype_t dtype, hipStream_t stream);
 hipError_t launch_delta_bwd(DeltaArgs a, void* workspace, ssm_dtype_t dtype, hipStream_t stream);
-// token by token on state slots (row b's state at state_in / state_out + slot * P * N * H)
+// token by token on state slots (row b's state at state + slot * H * P * N)
 struct DeltaStep {
     DeltaArgs a;
-    const float* state_in;   // NULL: zeros
-    float* state_out;        // NULL: not written
-    const int32_t* slots;    // [B] or NULL (slot b)
+    float* state;
+    const int32_t* slots;  // [B] or NULL (slot b)
     int64_t n_slots;
 };
 hipError_t launch_delta_step(const DeltaStep& s, ssm_dtype_t dtype, hipStream_t stream);

@@ -588,9 +588,9 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaStep s, int64_t un
         for (int i = 0; i < NI; ++i) {
             const int n = 32 * i + 4 * l8;
             hs[r][i] = f4{0, 0, 0, 0};
-            if (s.state_in && n < N && p0 + 8 * r < a.P)
+            if (n < N && p0 + 8 * r < a.P)
                 hs[r][i] = __builtin_nontemporal_load(
-                    reinterpret_cast<const f4*>(s.state_in + ((slot * a.H + h) * a.P + p0 + 8 * r) * a.N + n));
+                    reinterpret_cast<const f4*>(s.state + ((slot * a.H + h) * a.P + p0 + 8 * r) * a.N + n));
         }
     for (int64_t t = 0; t < a.L; ++t) {
         const int64_t row = b * a.L + t;
@@ -611,8 +611,7 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaStep s, int64_t un
         for (int r = 0; r < RG; ++r)
             v[r] = p0 + 8 * r < a.P ? D::load(static_cast<const S*>(a.v) + row * a.v_row + h * a.P, p0 + 8 * r) : 0.0f;
         const float be = a.beta[row * a.H + h];
-        float f = a.gate ? exp_of(gate_of(a.gate[row * a.H + h])) : 1.0f;
-        const bool cut = a.seq && t > 0 && a.seq[row] != a.seq[row - 1];
+        const float f = a.gate ? exp_of(gate_of(a.gate[row * a.H + h])) : 1.0f;
 #pragma unroll
         for (int r = 0; r < RG; ++r) {
             float kh = 0.0f, y = 0.0f;
@@ -620,7 +619,7 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaStep s, int64_t un
             for (int i = 0; i < NI; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    hs[r][i][e] = cut ? 0.0f : f * hs[r][i][e];
+                    hs[r][i][e] *= f;
                     kh += hs[r][i][e] * k[i][e];
                 }
             const float u = be * (v[r] - sum8(kh));
@@ -635,17 +634,15 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaStep s, int64_t un
             if (l8 == 0 && p0 + 8 * r < a.P) D::store(static_cast<S*>(a.y) + row * a.y_row + h * a.P, p0 + 8 * r, a.scale * y);
         }
     }
-    if (s.state_out) {
 #pragma unroll
-        for (int r = 0; r < RG; ++r)
+    for (int r = 0; r < RG; ++r)
 #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const int n = 32 * i + 4 * l8;
-                if (n < N && p0 + 8 * r < a.P)
-                    __builtin_nontemporal_store(
-                        hs[r][i], reinterpret_cast<f4*>(s.state_out + ((slot * a.H + h) * a.P + p0 + 8 * r) * a.N + n));
-            }
-    }
+        for (int i = 0; i < NI; ++i) {
+            const int n = 32 * i + 4 * l8;
+            if (n < N && p0 + 8 * r < a.P)
+                __builtin_nontemporal_store(
+                    hs[r][i], reinterpret_cast<f4*>(s.state + ((slot * a.H + h) * a.P + p0 + 8 * r) * a.N + n));
+        }
 }
 
 template <class D, int NI, int RG>
@@ -712,8 +709,10 @@ template <class MM>
 hipError_t fwd_of(DeltaArgs a, void* workspace, hipStream_t stream) {
     place_chunks<MM>(a, static_cast<uint8_t*>(workspace), false);
     constexpr size_t es = sizeof(typename MM::S);
-    a.direct = a.N % (16 / es) == 0 && a.P % (16 / es) == 0 && direct_rows_fit(a.q, a.q_row, es) &&
-               direct_rows_fit(a.k, a.k_row, es) && direct_rows_fit(a.v, a.v_row, es) && direct_rows_fit(a.y, a.y_row, es);
+    const int64_t keys = a.G * a.N, values = a.H * a.P;
+    a.direct = a.N % (16 / es) == 0 && a.P % (16 / es) == 0 && direct_rows_fit(a.q, a.q_row, keys, es) &&
+               direct_rows_fit(a.k, a.k_row, keys, es) && direct_rows_fit(a.v, a.v_row, values, es) &&
+               direct_rows_fit(a.y, a.y_row, values, es);
     return walk_by_width<MM, false>(a, DeltaSaved{}, stream);
 }
 

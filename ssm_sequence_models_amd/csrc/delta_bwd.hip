@@ -561,7 +561,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void delta_grad_kernel(DeltaArgs a
             const int li = here(li_), g4 = here(g4_);
             const int r0 = 16 * (rg * RW + i) + 4 * g4;
             const f4 f = row4(sf + r0);
-float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int j = 0; j < CT; ++j) {
                 const int n = 16 * (cg * CT + j) + li;
@@ -811,9 +811,11 @@ hipError_t bwd_of(DeltaArgs a, void* workspace, ssm_dtype_t dtype, hipStream_t s
     Buffers u{};
     place<MM>(a, u, static_cast<uint8_t*>(workspace));
     constexpr size_t es = sizeof(typename MM::S);
-    a.direct = a.N % (16 / es) == 0 && a.P % (16 / es) == 0 && direct_rows_fit(a.q, a.q_row, es) &&
-               direct_rows_fit(a.k, a.k_row, es) && direct_rows_fit(a.v, a.v_row, es) && direct_rows_fit(a.dy, a.dy_row, es) &&
-               direct_rows_fit(a.dq, a.dq_row, es) && direct_rows_fit(a.dk, a.dk_row, es) && direct_rows_fit(nullptr, a.H * a.P, 4);
+    const int64_t keys = a.G * a.N, values = a.H * a.P;
+    a.direct = a.N % (16 / es) == 0 && a.P % (16 / es) == 0 && direct_rows_fit(a.q, a.q_row, keys, es) &&
+               direct_rows_fit(a.k, a.k_row, keys, es) && direct_rows_fit(a.v, a.v_row, values, es) &&
+               direct_rows_fit(a.dy, a.dy_row, values, es) && direct_rows_fit(a.dq, a.dq_row, keys, es) &&
+               direct_rows_fit(a.dk, a.dk_row, keys, es) && direct_rows_fit(nullptr, values, values, 4);
     const hipError_t e = launch_delta_walk_saved(a, u.saved, dtype, stream);
     if (e != hipSuccess) return e;
     if (a.N <= 64) return kernels_of<MM, 4>(a, u, stream);

@@ -214,6 +214,25 @@ def test_strided_tokens_and_outputs(dtype):
     assert bool((wide[..., width:] == 5.0).all())
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_one_token_for_all(dtype):
+    """A token that stands for all of a row (stride 0), with lengths that end inside a chunk: the same
+    bits as its copies, in every operand and in all of them."""
+    import ssm_sequence_models_amd as ssm
+    s = {n: _cuda(t) for n, t in _inputs(1, 77, 4, 2, 32, 32, dtype, seed=18).items()}
+    names = ("q", "k", "v", "dy")
+    for which in (*((n,) for n in names), ("q", "dy"), names):
+        one = {n: s[n][:, :1].expand_as(s[n]) if n in which else s[n] for n in names}
+
+        def run(c):
+            how = dict(gate=s["gate"], initial_state=s["h0"])
+            return (*ssm.delta_scan_fwd(c["q"], c["k"], c["v"], s["beta"], **how),
+                    *ssm.delta_scan_bwd(c["q"], c["k"], c["v"], s["beta"], c["dy"], dfinal_state=s["dhT"], **how))
+        assert one[which[0]].stride(1) == 0
+        for a, b in zip(run(one), run({n: t.contiguous() for n, t in one.items()})):
+            assert torch.equal(a, b), which
+
+
 def test_no_tokens():
     import ssm_sequence_models_amd as ssm
     z = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
