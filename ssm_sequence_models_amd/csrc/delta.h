@@ -542,15 +542,16 @@ inline bool direct_rows_fit(const void* p, int64_t row, int64_t width, size_t es
 // Rows are cut into segments where their walks do not fill the 256 CUs: all segments from zero, with the
 // N unit rows as further channels that give what a segment makes of the state before it; the states
 // before the segments from those; then the walk proper, all segments side by side.  The cut is the
-// one with the shortest sum of its walks' rounds, in measured microseconds a chunk: 2.0 (from zero)
-// and 2.9 forward, 2.0, 3.0 (from zero) and 3.7 backward, 2 a segment for the states between, 10
-// for the launches.
+// one with the smallest sum of its walks' rounds, in units fitted to calls of 512 to 32845 tokens: a chunk
+// 2.5 uncut, 2.0 (from zero) and 2.9 forward; 5.7 uncut, 2.0 (from zero) and 8.7 (three walks) backward; 2 a
+// segment and walk for the states between, 10 a direction for the launches.  (bf16, 1024 tokens of 8 heads x
+// 64 x 128 backward: 131 us cut, 166 uncut; of 8 rows of 4 heads forward: 70 us cut, 65 uncut.)
 inline void plan_segments(DeltaArgs& a, bool bwd) {
     const int64_t units = a.B * a.H, own = (a.P + 63) / 64, all = own + (a.N + 63) / 64;
     const auto rounds = [](int64_t blocks) { return static_cast<double>((blocks + 255) / 256); };
     a.segs = 1;
     a.seg_chunks = a.chunks;
-    double best = rounds(units * own) * a.chunks * (bwd ? 5.7 : 2.9) * 0.85;
+    double best = rounds(units * own) * a.chunks * (bwd ? 5.7 : 2.5);
     for (int64_t n = 2; n <= 64 && n * 4 <= a.chunks; ++n) {
         const int64_t each = (a.chunks + n - 1) / n;
         if ((a.chunks + each - 1) / each != n) continue;

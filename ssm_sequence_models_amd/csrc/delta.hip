@@ -461,80 +461,73 @@ __global__ __launch_bounds__(320) void delta_walk_kernel(DeltaArgs a, DeltaSaved
 // ---------------------------------------------------------------------------------------
 // The states before the segments, h = h phi + gain from the first on (BACK: the gradients after them,
 // g = g phi^T + gain from the last on): 16 channels of a head a block, a wavefront 16 columns a
-// product of the fp32 instruction, the next segment's phi loaded meanwhile.
+// product of the fp32 instruction, the next segments' phi and gain loaded meanwhile.
 // ---------------------------------------------------------------------------------------
 template <int Q, int NT, bool BACK>
-__global__ __launch_bounds__(NT < 8 ? 64 * NT : 512) void delta_join_states_kernel(DeltaArgs a) {
-    constexpr int WV = NT < 8 ? NT : 8, CT = NT / WV, LD = 16 * NT + 4;
+__global__ __launch_bounds__(64 * NT) void delta_join_states_kernel(DeltaArgs a) {
+    constexpr int LD = 16 * NT + 4, AHEAD = NT < 16 ? 2 : 1;  // segments whose phi and gain are on their way (registers)
     __shared__ __attribute__((aligned(16))) float sh[16 * LD];
+    __shared__ bool cut[64];
     const int lane = threadIdx.x & 63, li = lane & 15, g4 = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int P = static_cast<int>(a.P), N = static_cast<int>(a.N), segs = static_cast<int>(a.segs);
-    const int ptiles = (P + 15) / 16, p0 = blockIdx.x % ptiles * 16;
+    const int ptiles = (P + 15) / 16, p0 = blockIdx.x % ptiles * 16 + 4 * g4, n = 16 * w + li;  // rows p0 .., column n
     const int64_t bh = blockIdx.x / ptiles;
     const float* const first = BACK ? a.dhT : a.h0;
     const int s0 = BACK ? segs - 1 : 0, step = BACK ? -1 : 1;
-    f4 h[CT];  // rows p0 + 4 g4 .., columns 16 (w + WV j) + li
-    const auto each = [&](auto f) {
+    f4 h{0, 0, 0, 0};
 #pragma unroll
-        for (int j = 0; j < CT; ++j)
+    for (int e = 0; e < 4; ++e)
+        if (first && p0 + e < P && n < N) h[e] = first[(bh * P + p0 + e) * N + n];
+    // with a start in a segment nothing of the state before it is left, finite or not
+    for (int s = threadIdx.x; s < segs; s += 64 * NT) cut[s] = false;
+    __syncthreads();
+    for (int c = threadIdx.x; c < static_cast<int>(a.chunks); c += 64 * NT)
+        if (a.factors[((bh * a.chunks + c) * kFactors + 4) * Q - 1] != 0.0f) cut[c / static_cast<int>(a.seg_chunks)] = true;
+    f4 phi[AHEAD][NT], gain[AHEAD];
+    const auto load = [&](int i, f4 (&ph)[NT], f4& gn) {
+        if (i + 1 >= segs) return;
+        const int64_t at = bh * segs + s0 + step * i;
+        const Buffer r = buffer(a.phi + at * N * N, static_cast<int64_t>(N) * N * 4);
+        const Buffer rg = buffer(a.gain + at * P * N, static_cast<int64_t>(P) * N * 4);
+#pragma unroll
+        for (int kk = 0; kk < NT; ++kk) {
+            const int m = 16 * kk + 4 * g4;
+            if (BACK) {
+                ph[kk] = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(r, n < N && m < N ? (n * N + m) * 4 : kOutside, 0, 0));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) ph[kk][e] = load_at<float>(r, n < N ? ((m + e) * N + n) * 4 : kOutside);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) gn[e] = load_at<float>(rg, n < N ? ((p0 + e) * N + n) * 4 : kOutside);
+    };
+#pragma unroll
+    for (int d = 0; d < AHEAD; ++d) load(d, phi[d], gain[d]);
+    for (int i0 = 0; i0 < segs; i0 += AHEAD) {
+#pragma unroll
+        for (int d = 0; d < AHEAD; ++d) {
+            const int i = i0 + d, s = s0 + step * i;
+            if (i >= segs) continue;
+            __syncthreads();
+            float* const entry = a.entry + (bh * segs + s) * P * N;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int p = p0 + 4 * g4 + e, n = 16 * (w + WV * j) + li;
-                f(j, e, p, n, p < P && n < N);
+                sh[(4 * g4 + e) * LD + n] = h[e];
+                if (p0 + e < P && n < N) entry[static_cast<int64_t>(p0 + e) * N + n] = h[e];
             }
-    };
-    each([&](int j, int e, int p, int n, bool in) { h[j][e] = in && first ? first[(bh * P + p) * N + n] : 0.0f; });
-    f4 next[CT][NT];
-    const auto load = [&](int s) {
-        const Buffer r = buffer(a.phi + (bh * segs + s) * N * N, static_cast<int64_t>(N) * N * 4);
-#pragma unroll
-        for (int j = 0; j < CT; ++j)
-#pragma unroll
-            for (int kk = 0; kk < NT; ++kk) {
-                const int n = 16 * (w + WV * j) + li, m = 16 * kk + 4 * g4;
-                if (BACK) {
-                    next[j][kk] = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(r, n < N && m < N ? (n * N + m) * 4 : kOutside, 0, 0));
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) next[j][kk][e] = load_at<float>(r, n < N ? ((m + e) * N + n) * 4 : kOutside);
-                }
-            }
-    };
-    load(s0);
-    for (int i = 0; i < segs; ++i) {
-        const int s = s0 + step * i;
-        const int64_t at = (bh * segs + s) * P;
-        __syncthreads();
-        f4 gain[CT];
-        each([&](int j, int e, int p, int n, bool in) {
-            sh[(4 * g4 + e) * LD + n] = h[j][e];
-            gain[j][e] = 0.0f;
-            if (in) {
-                a.entry[(at + p) * N + n] = h[j][e];
-                if (i + 1 < segs) gain[j][e] = a.gain[(at + p) * N + n];
-            }
-        });
-        __syncthreads();
-        if (i + 1 == segs) break;
-        // with a start in the segment nothing of the state before it is left, finite or not
-        bool starts = false;
-        for (int64_t c = s * a.seg_chunks + lane; c < (s + 1) * a.seg_chunks && c < a.chunks; c += 64)
-            starts = starts || a.factors[((bh * a.chunks + c) * kFactors + 4) * Q - 1] != 0.0f;
-        const bool cut = __any(starts);
-        f4 sum[CT];
-#pragma unroll
-        for (int j = 0; j < CT; ++j) {
-            sum[j] = f4{0, 0, 0, 0};
+            __syncthreads();
+            if (i + 1 == segs) continue;
+            f4 sum{0, 0, 0, 0};
 #pragma unroll
             for (int kk = 0; kk < NT; ++kk) {
                 const f4 l = *reinterpret_cast<const f4*>(&sh[li * LD + 16 * kk + 4 * g4]);
-                ByF32::mac<1, 1>(sum[j], ByF32::Frag<1>{l}, ByF32::Frag<1>{next[j][kk]});
+                ByF32::mac<1, 1>(sum, ByF32::Frag<1>{l}, ByF32::Frag<1>{phi[d][kk]});
             }
+            h = cut[s] ? gain[d] : sum + gain[d];
+            load(i + AHEAD, phi[d], gain[d]);
         }
-        if (i + 2 < segs) load(s + step);
-#pragma unroll
-        for (int j = 0; j < CT; ++j) h[j] = cut ? gain[j] : sum[j] + gain[j];
     }
 }
 
@@ -681,7 +674,7 @@ hipError_t walk_of(const DeltaArgs& a, const DeltaSaved& keep, hipStream_t strea
 template <class MM, int NT, bool BACK>
 hipError_t join_of(const DeltaArgs& a, hipStream_t stream) {
     const unsigned blocks = static_cast<unsigned>(a.B * a.H * ((a.P + 15) / 16));
-    delta_join_states_kernel<MM::Q, NT, BACK><<<blocks, NT < 8 ? 64 * NT : 512, 0, stream>>>(a);
+    delta_join_states_kernel<MM::Q, NT, BACK><<<blocks, 64 * NT, 0, stream>>>(a);
     return hipGetLastError();
 }
 template <class MM>
