@@ -21,6 +21,10 @@ using namespace delta;
 // a lane; then T_ij = -(sum_m T_im D_mj) T_jj, transposed, so that results are the next
 // products' operands where they lie.  (A product form of the inverse, (I - D)(I + D^2) .., loses
 // everything where keys repeat: the powers of D grow as binomials while T itself stays small.)
+// The heads of a key head go through the products once, up to a wavefront's worth of them a block (4 x 8192 x
+// 32 heads of 16 key heads, dstate 128: 242 us a head a block, 180 so; for the backward 300 and 246).  What
+// bounds it: the chain of a row's substitution and its three syncs at four wavefronts a SIMD; its
+// matrix instructions are busy 7 % of the time, its vector ones 34 %.  (Six wavefronts a SIMD: spills, 273.)
 // ---------------------------------------------------------------------------------------
 template <class MM, int NT, bool BWD, bool DIRECT>
 __global__ __launch_bounds__(MM::Q * 4, NT <= 8 ? 4 : 1) void delta_prep_kernel(DeltaArgs a, int heads) {
@@ -236,6 +240,9 @@ __global__ __launch_bounds__(MM::Q * 4, NT <= 8 ? 4 : 1) void delta_prep_kernel(
 // the next chunk's K, Q, T, M, factors and values straight into the other half of LDS (one half only
 // where dstate is over 128), and the last chunk's y out of it.  (Fetched by the four themselves, the
 // loads' issue was a third of a chunk's time.)
+// A block has all of a CU's LDS, so a SIMD has one of the four: the chain of a chunk's five products is what
+// bounds the walk (matrix instructions busy 27 % of it, vector ones 35 %, splits and scalings; 3.7 to 4.9 us a
+// chunk by the clock).  4 x 8192 x 32 heads x 128 x 128, bf16, 256 blocks of 128 chunks: 470 to 630 us.
 // kSave: for the backward, the states and E in place of y.  kSpan: a segment from zero, and behind the
 // channels the N unit rows without values; only the state after it.
 // DIRECT: see DeltaArgs; without it tokens pass through registers
@@ -462,6 +469,8 @@ __global__ __launch_bounds__(320) void delta_walk_kernel(DeltaArgs a, DeltaSaved
 // The states before the segments, h = h phi + gain from the first on (BACK: the gradients after them,
 // g = g phi^T + gain from the last on): 16 channels of a head a block, a wavefront 16 columns a
 // product of the fp32 instruction, the next segments' phi and gain loaded meanwhile.
+// 2 us a segment at dstate 128, 1.1 at 64 (one segment's loads ahead, and the starts read by the way: 4.3
+// and 2.9).
 // ---------------------------------------------------------------------------------------
 template <int Q, int NT, bool BACK>
 __global__ __launch_bounds__(64 * NT) void delta_join_states_kernel(DeltaArgs a) {
@@ -534,7 +543,8 @@ __global__ __launch_bounds__(64 * NT) void delta_join_states_kernel(DeltaArgs a)
 // ---------------------------------------------------------------------------------------
 // Token by token: the decode step.  Eight lanes hold a channel's state, 128 bytes side by side
 // of it a load, RG channels eight apart a lane; a wavefront is a unit of its own.  The state's
-// one read and one write are the whole cost (256 requests of 32 heads x 128 x 128: 1 GiB).
+// one read and one write are the whole cost (256 requests of 32 heads x 128 x 128: 1.07 GB in 199 us,
+// 5.4 TB/s).
 // ---------------------------------------------------------------------------------------
 __device__ __forceinline__ float sum8(float v) {  // over the eight lanes of a channel
     v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xf, 0xf, true));          // i ^ 1
@@ -654,7 +664,8 @@ hipError_t step_by_width(const DeltaStep& s, hipStream_t stream) {
 
 template <class MM, int NT>
 void prep_of(const DeltaArgs& a, bool bwd, hipStream_t stream) {
-    // a key head's heads share the products: up to one a wavefront, as long as there are blocks for all CUs
+    // a key head's heads share the products: up to one a wavefront, as long as the blocks fill the GPU (fewer:
+    // 1024 tokens of 32 heads of 8 x 128 x 128 forward 77 us, 69 with a head a block)
     int heads = 1;
     while (2 * heads <= MM::Q / 16 && a.H / a.G % (2 * heads) == 0 && a.B * a.chunks * a.H / (2 * heads) >= 1024) heads *= 2;
     const unsigned blocks = static_cast<unsigned>(a.B * a.chunks * (a.H / heads));

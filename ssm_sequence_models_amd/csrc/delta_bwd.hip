@@ -44,6 +44,8 @@ __device__ __forceinline__ f4 row4(const float* p) { return lds<f4>(reinterpret_
 
 // Laid out as the walk (delta.hip), from the last chunk to the first; E comes and dZ goes by the wavefronts
 // that use them (LDS is full).
+// Bound as the walk is, by the chain of a chunk's products with one such wavefront a SIMD (matrix instructions
+// busy 25 % of it, vector ones 32 %): 4 x 8192 x 32 heads x 128 x 128, bf16, 830 to 870 us for 128 chunks.
 template <class MM, int NT>
 struct BackLds {
     static constexpr int W = 16 * NT, MP = m_parts<MM>(true), HALVES = NT <= 8 ? 2 : 1;
@@ -263,6 +265,12 @@ __global__ __launch_bounds__(320) void delta_back_kernel(DeltaArgs a, Buffers u)
 // reads of h_0 and dh each element once, and takes tiles of the pairs in turn.  dY, dZ and E pass
 // through LDS in blocks of 64 channels; dQ and dK are summed over the heads of a key head in
 // accumulators.
+// fp32 operands go in three bf16 parts where dbeta and dgate, which are fp32, depend on them, and in two where only
+// dQ and dK do: these are rounded to bf16 (two parts leave 2^-17 of a term), and for fp32 the parts are whole.
+// Bound by its waits and vector work: 1300 to 1400 us at 4 x 8192 x 32 heads of 16 key heads x 128 x 128, bf16 (matrix
+// instructions busy 20 %, vector ones 45 %; h_0, dh, E and dZ, 3.2 GB, would take 520 us at the copy's rate).
+// Four wavefronts a block: 1900.  LDS addresses are formed where they are used (`here`): kept over the loops
+// they cost 2650 us in spilled registers.
 // ---------------------------------------------------------------------------------------
 template <class MM>
 __device__ __forceinline__ void store_values(typename MM::S* p, int n, const float (&v)[MM::R]) {
@@ -750,10 +758,13 @@ __global__ __launch_bounds__(256) void delta_join_kernel(DeltaArgs a, Buffers u)
     }
 }
 
-// blocks that fill the GPU twice, where there are as many heads
+// Ranges of a key head's heads where key heads and chunks alone leave CUs idle; they cost a pass over their partial
+// sums.  The whole backward: 256 tokens of 16 heads of one key head x 64 x 64 64 us (unsplit 185), 1024 of 32 heads of
+// 8 x 128 x 128 202 (unsplit 215; in blocks for twice the CUs 218), 2 x 4096 of 8 of 2 x 64 x 128, 256 blocks unsplit,
+// 277 (split 301).
 void split_heads(const DeltaArgs& a, Buffers& u) {
     const int64_t rep = a.H / a.G, blocks = a.B * a.chunks * a.G;
-    int64_t splits = (512 + blocks - 1) / blocks;
+    int64_t splits = (256 + blocks - 1) / blocks;
     if (splits > rep) splits = rep;
     u.heads = (rep + splits - 1) / splits;
     u.splits = (rep + u.heads - 1) / u.heads;
