@@ -22,9 +22,10 @@ using namespace delta;
 // products' operands where they lie.  (A product form of the inverse, (I - D)(I + D^2) .., loses
 // everything where keys repeat: the powers of D grow as binomials while T itself stays small.)
 // The heads of a key head go through the products once, up to a wavefront's worth of them a block (4 x 8192 x
-// 32 heads of 16 key heads, dstate 128: 242 us a head a block, 180 so; for the backward 300 and 246).  What
-// bounds it: the chain of a row's substitution and its three syncs at four wavefronts a SIMD; its
-// matrix instructions are busy 7 % of the time, its vector ones 34 %.  (Six wavefronts a SIMD: spills, 273.)
+// 32 heads of 16 key heads, dstate 128: 242 us a head a block, 180 so; for the backward 300 and 235).  What
+// bounds it: the chain of a row's substitution and its syncs at four wavefronts a SIMD (vector instructions busy
+// half of the time, matrix ones a tenth), and 0.52 GB of images written (backward 0.93).  (Six wavefronts a
+// SIMD: spills, 273.)
 // ---------------------------------------------------------------------------------------
 template <class MM, int NT, bool BWD, bool DIRECT>
 __global__ __launch_bounds__(MM::Q * 4, NT <= 8 ? 4 : 1) void delta_prep_kernel(DeltaArgs a, int heads) {
@@ -241,8 +242,9 @@ __global__ __launch_bounds__(MM::Q * 4, NT <= 8 ? 4 : 1) void delta_prep_kernel(
 // where dstate is over 128), and the last chunk's y out of it.  (Fetched by the four themselves, the
 // loads' issue was a third of a chunk's time.)
 // A block has all of a CU's LDS, so a SIMD has one of the four: the chain of a chunk's five products is what
-// bounds the walk (matrix instructions busy 27 % of it, vector ones 35 %, splits and scalings; 3.7 to 4.9 us a
-// chunk by the clock).  4 x 8192 x 32 heads x 128 x 128, bf16, 256 blocks of 128 chunks: 470 to 630 us.
+// bounds the walk (matrix instructions busy 45 % of it, vector ones 47 %, splits and scalings; 3.7 to 4.9 us a
+// chunk by the clock).  4 x 8192 x 32 heads x 128 x 128, bf16, 256 blocks of 128 chunks: 470 to 630 us.  As kSave
+// 525, 29 % and 37 %: it moves 2.3 GB, half of them the states, at 4.4 TB/s.
 // kSave: for the backward, the states and E in place of y.  kSpan: a segment from zero, and behind the
 // channels the N unit rows without values; only the state after it.
 // DIRECT: see DeltaArgs; without it tokens pass through registers

@@ -44,8 +44,9 @@ __device__ __forceinline__ f4 row4(const float* p) { return lds<f4>(reinterpret_
 
 // Laid out as the walk (delta.hip), from the last chunk to the first; E comes and dZ goes by the wavefronts
 // that use them (LDS is full).
-// Bound as the walk is, by the chain of a chunk's products with one such wavefront a SIMD (matrix instructions
-// busy 25 % of it, vector ones 32 %): 4 x 8192 x 32 heads x 128 x 128, bf16, 830 to 870 us for 128 chunks.
+// Bound by the chain of a chunk's products with one such wavefront a SIMD (matrix instructions busy 24 % of it,
+// vector ones 32 %) and by the 3.4 GB that it moves, dh and dZ out, E and the images of T and M in, at 4.2 TB/s:
+// 4 x 8192 x 32 heads x 128 x 128, bf16, 790 to 870 us for 128 chunks.
 template <class MM, int NT>
 struct BackLds {
     static constexpr int W = 16 * NT, MP = m_parts<MM>(true), HALVES = NT <= 8 ? 2 : 1;
@@ -267,8 +268,8 @@ __global__ __launch_bounds__(320) void delta_back_kernel(DeltaArgs a, Buffers u)
 // accumulators.
 // fp32 operands go in three bf16 parts where dbeta and dgate, which are fp32, depend on them, and in two where only
 // dQ and dK do: these are rounded to bf16 (two parts leave 2^-17 of a term), and for fp32 the parts are whole.
-// Bound by its waits and vector work: 1300 to 1400 us at 4 x 8192 x 32 heads of 16 key heads x 128 x 128, bf16 (matrix
-// instructions busy 20 %, vector ones 45 %; h_0, dh, E and dZ, 3.2 GB, would take 520 us at the copy's rate).
+// Bound by its waits and vector work: 1250 to 1400 us at 4 x 8192 x 32 heads of 16 key heads x 128 x 128, bf16 (matrix
+// instructions busy 23 %, vector ones 46 %; it moves 4.3 GB, h_0, dh, E and dZ the most of them, at 3.3 TB/s).
 // Four wavefronts a block: 1900.  LDS addresses are formed where they are used (`here`): kept over the loops
 // they cost 2650 us in spilled registers.
 // ---------------------------------------------------------------------------------------
