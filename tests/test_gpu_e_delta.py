@@ -89,6 +89,23 @@ def test_heads(B, H, G):
     _compare(_inputs(B, 50, H, G, 16, 32, F32, seed=H))
 
 
+@pytest.mark.parametrize("dtype,H,G", [(BF16, 128, 32), (BF16, 96, 16), (F32, 64, 16)])
+def test_many_heads_of_a_key_head(dtype, H, G):
+    """Enough heads that a block forms a key head's products for several: the bits of heads with keys of
+    their own, and the 64-bit form in two rows."""
+    B, L, P, N = 16, 150, 8, 16
+    s = _inputs(B, L, H, G, P, N, dtype, seed=H)
+    seq = _seq(B, L, "random")
+    got = _run(s, 0.5, seq)
+    own = _run(dict(s, **{n: s[n].repeat_interleave(H // G, 2) for n in ("q", "k")}), 0.5, seq)
+    for n in ("y", "final", "dv", "dbeta", "dgate", "dh0"):
+        assert torch.equal(got[n], own[n]), n
+    two = {n: None if t is None else t[:2].contiguous() for n, t in s.items()}
+    ref = delta64(two["q"], two["k"], two["v"], two["beta"], two["gate"], 0.5, two["h0"], seq[:2], two["dy"], two["dhT"])
+    for n, t in got.items():
+        check_delta(t[:2], ref, n, F32 if n in STATE else dtype, N + P + 256, -(-L // 32))
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("kind", ["every", "edges", "random"])
 def test_packed(kind, dtype):
@@ -380,6 +397,21 @@ def test_rows_far_apart():
         p.copy_(c[n])
     y2, final2 = ssm.delta_scan_fwd(*parts, c["beta"], gate=c["gate"], initial_state=c["h0"])
     assert torch.equal(y, y2) and torch.equal(final, final2)
+
+
+def test_step_slots_far_apart():
+    """A slot behind 2^31 elements of the pool: the bits of a pool of its own."""
+    import ssm_sequence_models_amd as ssm
+    H, P, N, slots = 32, 128, 128, 4100
+    c = {n: _cuda(t) for n, t in _inputs(2, 1, H, 16, P, N, BF16, seed=19).items()}
+    small = c["h0"].clone()
+    pool = torch.empty(slots, H, P, N, device="cuda")
+    at = torch.tensor([slots - 1, 3], dtype=torch.int32, device="cuda")
+    pool[slots - 1], pool[3] = small[0], small[1]
+    args = (c["q"], c["k"], c["v"], c["beta"])
+    y = ssm.delta_scan_step(*args, pool, gate=c["gate"], state_indices=at)
+    assert torch.equal(y, ssm.delta_scan_step(*args, small, gate=c["gate"]))
+    assert torch.equal(pool[slots - 1], small[0]) and torch.equal(pool[3], small[1])
 
 
 def test_graph_replay_and_streams():
