@@ -531,8 +531,8 @@ ssm_status_t ssm_gated_scan_step(const void* x, int64_t x_row, const void* gate,
  *   seq_idx        [batch, seqlen] int32, or NULL
  *   workspace      ..._workspace_size bytes, 256-byte aligned
  * dstate a multiple of 4, at most 256; any headdim.  States and sums in fp32 (sums of gates in 64
- * bits), products exact to fp32 for SSM_F32 and for everything that a fp32 output depends on; outputs
- * rounded once.  Deterministic.  A NaN or infinity reaches the tokens of its own chunk (64 tokens for
+ * bits), products of operands that hold 24 bits in either dtype; outputs rounded once.
+ * Deterministic.  A NaN or infinity reaches the tokens of its own chunk (64 tokens for
  * SSM_BF16, 32 for SSM_F32, from the row's start), forward its sequence's after them, and backward all
  * chunks that its sequence has tokens in, other sequences' tokens in those among them; no token of
  * other chunks, and no state that its sequence does not reach.

@@ -84,7 +84,7 @@ struct ByBf16 {
     static constexpr int Q = 64;   // tokens a chunk
     static constexpr int KB = 32;  // contraction of one operand pair
     static constexpr int R = 8;    // of it, values a lane
-    static constexpr int TP = 3;   // parts of T
+    static constexpr int TP = 3;   // parts of T, M and every other fp32 operand that is kept
     template <int PARTS>
     struct Frag {
         bf8 p[PARTS];
@@ -341,8 +341,6 @@ constexpr int frag_at(int rt, int kk, bool transposed) {
 }
 template <class MM>
 constexpr int image_bytes(int parts) { return parts * frag_count<MM>() * 1024; }
-template <class MM>
-constexpr int m_parts(bool bwd) { return MM::TP == 1 ? 1 : bwd ? 3 : 2; }
 
 // one part of an operand kept as PARTS tiles behind each other
 template <class MM, int PARTS, class F>
@@ -377,6 +375,8 @@ __device__ __forceinline__ void to_lds(Buffer r, uint32_t at, uint8_t* lds) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, at, 0, 0, 0);
 }
 __device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }  // vmcnt(0)
+// LDS reads are done before anything behind this (direct loads into LDS do not wait for them)
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 // an element as it lies in memory; value_of where it is used, which is where the load is waited for
 template <class S>
 __device__ __forceinline__ S load_at(Buffer r, uint32_t at) {
@@ -574,7 +574,7 @@ size_t place_chunks(DeltaArgs& a, uint8_t* ws, bool bwd) {
     a.T = ws;
     at += n * image_bytes<MM>(MM::TP);
     a.M = ws + at;
-    at += n * image_bytes<MM>(m_parts<MM>(bwd));
+    at += n * image_bytes<MM>(MM::TP);
     a.Tt = ws + at;
     if (bwd) at += n * image_bytes<MM>(MM::TP);
     a.factors = reinterpret_cast<float*>(ws + at);

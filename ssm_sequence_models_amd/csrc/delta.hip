@@ -31,7 +31,6 @@ template <class MM, int NT, bool BWD, bool DIRECT>
 __global__ __launch_bounds__(MM::Q * 4, NT <= 8 ? 4 : 1) void delta_prep_kernel(DeltaArgs a, int heads) {
     using S = typename MM::S;
     constexpr int Q = MM::Q, RT = Q / 16, KT = Q / MM::KB, LD = Q + 4, R = MM::R, KN = 16 * NT / MM::KB;
-    constexpr int MP = m_parts<MM>(BWD);
     __shared__ __attribute__((aligned(16))) float sd[Q * LD];        // D transposed: [s][t]
     __shared__ __attribute__((aligned(16))) float sii[RT][16 * 20];  // T's diagonal blocks, transposed
     float* const so = sd;  // T and M on the way out, once D is used up
@@ -194,10 +193,10 @@ __global__ __launch_bounds__(MM::Q * 4, NT <= 8 ? 4 : 1) void delta_prep_kernel(
         }
         if (tid < Q) a.factors[image * kFactors * Q + 3 * Q + tid] = static_cast<float>(sr[tid]) + (sbad ? kNotFinite : 0.0f);
         uint8_t* T = a.T + image * image_bytes<MM>(MM::TP);
-        uint8_t* M = a.M + image * image_bytes<MM>(MP);
-        const auto put = [&](uint8_t* to, const auto& f, auto parts) {
+        uint8_t* M = a.M + image * image_bytes<MM>(MM::TP);
+        const auto put = [&](uint8_t* to, const auto& f) {
 #pragma unroll
-            for (int p = 0; p < parts(); ++p) {
+            for (int p = 0; p < MM::TP; ++p) {
                 if constexpr (MM::TP == 1) *reinterpret_cast<f4*>(to + lane * 16) = f.v;
                 else *reinterpret_cast<bf8*>(to + p * 1024 + lane * 16) = f.p[p];
             }
@@ -207,8 +206,8 @@ __global__ __launch_bounds__(MM::Q * 4, NT <= 8 ? 4 : 1) void delta_prep_kernel(
             if (i != w) continue;
 #pragma unroll
             for (int kb = 0; kb <= 16 * i / MM::KB; ++kb) {
-                put(T + frag_at<MM>(i, kb, false) * MM::TP * 1024, MM::template of_tiles<MM::TP>(x, kb), [] { return MM::TP; });
-                if (!BWD) put(M + frag_at<MM>(i, kb, false) * MP * 1024, MM::template of_tiles<MP>(md, kb), [] { return MP; });
+                put(T + frag_at<MM>(i, kb, false) * MM::TP * 1024, MM::template of_tiles<MM::TP>(x, kb));
+                if (!BWD) put(M + frag_at<MM>(i, kb, false) * MM::TP * 1024, MM::template of_tiles<MM::TP>(md, kb));
             }
         }
         if constexpr (BWD) {  // T and M once more with rows s: their columns through LDS
@@ -229,7 +228,7 @@ __global__ __launch_bounds__(MM::Q * 4, NT <= 8 ? 4 : 1) void delta_prep_kernel(
                     uint8_t* to = pass ? M : Tt;
 #pragma unroll
                     for (int i = 0; i < RT; ++i)
-                        if (i == w) put(to + frag_at<MM>(i, kb, true) * MM::TP * 1024, f, [] { return MM::TP; });
+                        if (i == w) put(to + frag_at<MM>(i, kb, true) * MM::TP * 1024, f);
                 }
             }
         }
@@ -252,18 +251,18 @@ __global__ __launch_bounds__(MM::Q * 4, NT <= 8 ? 4 : 1) void delta_prep_kernel(
 enum { kOut, kSave, kSpan };
 template <class MM, int NT, int MODE>
 struct WalkLds {
-    static constexpr int W = 16 * NT, MP = m_parts<MM>(false), HALVES = NT <= 8 ? 2 : 1;
+    static constexpr int W = 16 * NT, HALVES = NT <= 8 ? 2 : 1;
     static constexpr int V = 0, K = V + staged_bytes<MM, 64>(), T = K + staged_bytes<MM, W>(), F = T + image_bytes<MM>(MM::TP),
-                         Qq = F + 1024, M = Qq + (MODE != kOut ? 0 : staged_bytes<MM, W>()), HALF = M + (MODE != kOut ? 0 : image_bytes<MM>(MP));
-    static constexpr int Y = HALVES * HALF, BYTES = Y + (MODE != kOut ? 0 : 2 * MM::template tile_bytes<64>(MM::Q));
+                         Qq = F + 1024, M = Qq + (MODE != kOut ? 0 : staged_bytes<MM, W>()), HALF = M + (MODE != kOut ? 0 : image_bytes<MM>(MM::TP));
+    // a chunk's y: in place of its values, or (one half) in two places of its own
+    static constexpr int YB = MODE == kOut && HALVES == 1 ? MM::template tile_bytes<64>(MM::Q) : 0, BYTES = HALVES * HALF + 2 * YB;
 };
 
 template <class MM, int NT, int MODE, bool DIRECT>
 __global__ __launch_bounds__(320) void delta_walk_kernel(DeltaArgs a, DeltaSaved keep) {
     using S = typename MM::S;
     using O = WalkLds<MM, NT, MODE>;
-    constexpr int Q = MM::Q, RT = Q / 16, KT = Q / MM::KB, W = 16 * NT, KN = W / MM::KB, MP = O::MP, ES = sizeof(S);
-    constexpr int YB = MM::template tile_bytes<64>(Q);
+    constexpr int Q = MM::Q, RT = Q / 16, KT = Q / MM::KB, W = 16 * NT, KN = W / MM::KB, TP = MM::TP, ES = sizeof(S);
     __shared__ __attribute__((aligned(1024))) uint8_t sm[O::BYTES];
     const int lane = threadIdx.x & 63, li = lane & 15, g4 = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -280,6 +279,7 @@ __global__ __launch_bounds__(320) void delta_walk_kernel(DeltaArgs a, DeltaSaved
         return static_cast<int>(left < Q ? left : Q);
     };
     const auto half_of = [&](int c) { return sm + (O::HALVES == 2 ? (c & 1) * O::HALF : 0); };
+    const auto y_of = [&](int c) { return O::YB ? sm + O::HALF + (c & 1) * O::YB : half_of(c) + O::V; };
     // what the chunk's last token says: sequences begun, and whether all keys and queries are finite
     const auto marks_of = [&](const uint8_t* half) {
         return __builtin_amdgcn_readfirstlane(static_cast<int>(reinterpret_cast<const float*>(half + O::F)[4 * Q - 1]));
@@ -295,19 +295,25 @@ __global__ __launch_bounds__(320) void delta_walk_kernel(DeltaArgs a, DeltaSaved
             if (DIRECT) {
                 direct_rows<MM, W, true>(half + O::K, token_buffer<S>(a.k, t0, a.k_row, g * N, valid, N), static_cast<int>(a.k_row), N, lane);
                 if (MODE == kOut) direct_rows<MM, W, true>(half + O::Qq, token_buffer<S>(a.q, t0, a.q_row, g * N, valid, N), static_cast<int>(a.q_row), N, lane);
-                if (!rows) direct_rows<MM, 64, false>(half + O::V, token_buffer<S>(a.v, t0, a.v_row, col, valid, width), static_cast<int>(a.v_row), width, lane);
             } else {
                 stage_rows<MM, W, 64, true>(half + O::K, static_cast<const S*>(a.k) + t0 * a.k_row + g * N, a.k_row, valid, N);
                 if (MODE == kOut) stage_rows<MM, W, 64, true>(half + O::Qq, static_cast<const S*>(a.q) + t0 * a.q_row + g * N, a.q_row, valid, N);
-                if (!rows) stage_elements<MM, 64>(half + O::V, static_cast<const S*>(a.v) + t0 * a.v_row + col, a.v_row, valid, width);
             }
-            direct_image<image_bytes<MM>(MM::TP)>(half + O::T, a.T + image * image_bytes<MM>(MM::TP), lane);
-            if (MODE == kOut) direct_image<image_bytes<MM>(MP)>(half + O::M, a.M + image * image_bytes<MM>(MP), lane);
+            direct_image<image_bytes<MM>(TP)>(half + O::T, a.T + image * image_bytes<MM>(TP), lane);
+            if (MODE == kOut) direct_image<image_bytes<MM>(TP)>(half + O::M, a.M + image * image_bytes<MM>(TP), lane);
             direct_image<kFactors * Q * 4>(half + O::F, reinterpret_cast<const uint8_t*>(a.factors + image * kFactors * Q), lane);
+        };
+        const auto fetch_values = [&](int c) {
+            uint8_t* const half = half_of(c);
+            const int64_t t0 = b * a.L + static_cast<int64_t>(c) * Q;
+            const int valid = rows_of(c);
+            if (rows) return;
+            if (DIRECT) direct_rows<MM, 64, false>(half + O::V, token_buffer<S>(a.v, t0, a.v_row, col, valid, width), static_cast<int>(a.v_row), width, lane);
+            else stage_elements<MM, 64>(half + O::V, static_cast<const S*>(a.v) + t0 * a.v_row + col, a.v_row, valid, width);
         };
         const auto store = [&](int c) {
             if (MODE != kOut || c < c0) return;
-            const uint8_t* y = sm + O::Y + (c & 1) * YB;
+            const uint8_t* y = y_of(c);
             const int64_t t0 = b * a.L + static_cast<int64_t>(c) * Q;
             const int valid = rows_of(c);
             if (DIRECT) {
@@ -325,16 +331,24 @@ __global__ __launch_bounds__(320) void delta_walk_kernel(DeltaArgs a, DeltaSaved
                         MM::store(static_cast<S*>(a.y) + (t0 + i / 64) * a.y_row + col, lane, MM::template at<64>(y, i / 64, lane));
             }
         };
-        if (O::HALVES == 2) fetch(c0);
+        if (O::HALVES == 2) {
+            fetch(c0);
+            fetch_values(c0);
+        }
         for (int c = c0; c < c1; ++c) {
             if (O::HALVES == 1) {
                 __syncthreads();
                 fetch(c);
+                fetch_values(c);
             }
             wait_loads();
             __syncthreads();
             if (O::HALVES == 2 && c + 1 < c1) fetch(c + 1);
             store(c - 1);
+            if (O::HALVES == 2 && c + 1 < c1) {
+                wait_lds();  // y leaves before the next values come into its place
+                fetch_values(c + 1);
+            }
             if (marks_of(half_of(c)) >= static_cast<int>(kNotFinite)) {
                 __syncthreads();
                 __syncthreads();
@@ -408,7 +422,7 @@ __global__ __launch_bounds__(320) void delta_walk_kernel(DeltaArgs a, DeltaSaved
                     const auto s = MM::template of_tiles<3>(z, kk);
 #pragma unroll
                     for (int i = kk * MM::KB / 16; i < RT; ++i)
-                        MM::template mac<MM::TP, 3>(x[i], frag<MM, MM::TP>(half + O::T, frag_at<MM>(i, kk, false), lane), s);
+                        MM::template mac<TP, 3>(x[i], frag<MM, TP>(half + O::T, frag_at<MM>(i, kk, false), lane), s);
                 }
             });
             if (MODE == kSave) {
@@ -427,12 +441,12 @@ __global__ __launch_bounds__(320) void delta_walk_kernel(DeltaArgs a, DeltaSaved
             if (MODE == kOut) {
 #pragma unroll
                 for (int kk = 0; kk < KT; ++kk) {
-                    const auto s = MM::template of_tiles<MP>(x, kk);
+                    const auto s = MM::template of_tiles<TP>(x, kk);
 #pragma unroll
                     for (int i = kk * MM::KB / 16; i < RT; ++i)
-                        MM::template mac<MP, MP>(y[i], frag<MM, MP>(half + O::M, frag_at<MM>(i, kk, false), lane), s);
+                        MM::template mac<TP, TP>(y[i], frag<MM, TP>(half + O::M, frag_at<MM>(i, kk, false), lane), s);
                 }
-                uint8_t* const to = sm + O::Y + (c & 1) * YB;
+                uint8_t* const to = y_of(c);  // (this wavefront's columns, whose values it has read)
 #pragma unroll
                 for (int i = 0; i < RT; ++i)
 #pragma unroll

@@ -49,9 +49,9 @@ __device__ __forceinline__ f4 row4(const float* p) { return lds<f4>(reinterpret_
 // 4 x 8192 x 32 heads x 128 x 128, bf16, 790 to 870 us for 128 chunks.
 template <class MM, int NT>
 struct BackLds {
-    static constexpr int W = 16 * NT, MP = m_parts<MM>(true), HALVES = NT <= 8 ? 2 : 1;
+    static constexpr int W = 16 * NT, HALVES = NT <= 8 ? 2 : 1;
     static constexpr int V = 0, K = V + staged_bytes<MM, 64>(), T = K + staged_bytes<MM, W>(), F = T + image_bytes<MM>(MM::TP),
-                         Qq = F + 1024, M = Qq + staged_bytes<MM, W>(), HALF = M + image_bytes<MM>(MP);
+                         Qq = F + 1024, M = Qq + staged_bytes<MM, W>(), HALF = M + image_bytes<MM>(MM::TP);
 };
 
 // SPAN: a segment from zero, only the gradient of the state before it
@@ -59,7 +59,7 @@ template <class MM, int NT, bool SPAN, bool DIRECT>
 __global__ __launch_bounds__(320) void delta_back_kernel(DeltaArgs a, Buffers u) {
     using S = typename MM::S;
     using O = BackLds<MM, NT>;
-    constexpr int Q = MM::Q, RT = Q / 16, KT = Q / MM::KB, W = 16 * NT, KN = W / MM::KB, MP = O::MP;
+    constexpr int Q = MM::Q, RT = Q / 16, KT = Q / MM::KB, W = 16 * NT, KN = W / MM::KB, TP = MM::TP;
     __shared__ __attribute__((aligned(1024))) uint8_t sm[O::HALVES * O::HALF];
     const int lane = threadIdx.x & 63, li = lane & 15, g4 = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -96,7 +96,7 @@ __global__ __launch_bounds__(320) void delta_back_kernel(DeltaArgs a, Buffers u)
                 stage_elements<MM, 64>(half + O::V, static_cast<const S*>(a.dy) + t0 * a.dy_row + col, a.dy_row, valid, width);
             }
             direct_image<image_bytes<MM>(MM::TP)>(half + O::T, a.Tt + image * image_bytes<MM>(MM::TP), lane);
-            direct_image<image_bytes<MM>(MP)>(half + O::M, a.M + image * image_bytes<MM>(MP), lane);
+            direct_image<image_bytes<MM>(MM::TP)>(half + O::M, a.M + image * image_bytes<MM>(MM::TP), lane);
             direct_image<kFactors * Q * 4>(half + O::F, reinterpret_cast<const uint8_t*>(a.factors + image * kFactors * Q), lane);
         };
         if (O::HALVES == 2) fetch(c1 - 1);
@@ -199,7 +199,7 @@ __global__ __launch_bounds__(320) void delta_back_kernel(DeltaArgs a, Buffers u)
                     const auto s = MM::template of_tiles<1>(dy, kk);
 #pragma unroll
                     for (int i = 0; i < (kk + 1) * MM::KB / 16; ++i)
-                        MM::template mac<MP, 1>(du[i], frag<MM, MP>(half + O::M, frag_at<MM>(i, kk, true), lane), s);
+                        MM::template mac<TP, 1>(du[i], frag<MM, TP>(half + O::M, frag_at<MM>(i, kk, true), lane), s);
                 }
             });
 #pragma unroll
@@ -216,7 +216,7 @@ __global__ __launch_bounds__(320) void delta_back_kernel(DeltaArgs a, Buffers u)
                     const auto s = MM::template of_tiles<3>(du, kk);
 #pragma unroll
                     for (int i = 0; i < (kk + 1) * MM::KB / 16; ++i)
-                        MM::template mac<MM::TP, 3>(dz[i], frag<MM, MM::TP>(half + O::T, frag_at<MM>(i, kk, true), lane), s);
+                        MM::template mac<TP, 3>(dz[i], frag<MM, TP>(half + O::T, frag_at<MM>(i, kk, true), lane), s);
                 }
             });
             const Buffer rz = token_buffer<float>(u.dz, t0, erow, static_cast<int64_t>(h) * P, DIRECT ? valid : 1, P);
@@ -266,8 +266,7 @@ __global__ __launch_bounds__(320) void delta_back_kernel(DeltaArgs a, Buffers u)
 // reads of h_0 and dh each element once, and takes tiles of the pairs in turn.  dY, dZ and E pass
 // through LDS in blocks of 64 channels; dQ and dK are summed over the heads of a key head in
 // accumulators.
-// fp32 operands go in three bf16 parts where dbeta and dgate, which are fp32, depend on them, and in two where only
-// dQ and dK do: these are rounded to bf16 (two parts leave 2^-17 of a term), and for fp32 the parts are whole.
+// fp32 operands go in three bf16 parts, which hold all of their 24 bits, or whole.
 // Bound by its waits and vector work: 1250 to 1400 us at 4 x 8192 x 32 heads of 16 key heads x 128 x 128, bf16 (matrix
 // instructions busy 23 %, vector ones 46 %; it moves 4.3 GB, h_0, dh, E and dZ the most of them, at 3.3 TB/s).
 // Four wavefronts a block: 1900.  LDS addresses are formed where they are used (`here`): kept over the loops
@@ -320,9 +319,9 @@ __global__ __launch_bounds__(64 * kGradWaves) void delta_grad_kernel(DeltaArgs a
     constexpr int WV = kGradWaves, CG = NT < WV ? NT : WV, RG = WV / CG;  // column and row groups of wavefronts
     constexpr int CT = NT / CG, RW = RT / RG;           // a wavefront's column and row tiles
     constexpr int TILES = RT * (RT + 1) / 2, MINE = (TILES + WV - 1) / WV;
-    constexpr int TP = MM::TP, XP = TP == 1 ? 1 : 2;
+    constexpr int TP = MM::TP;
     constexpr int QN = staged_bytes<MM, W>(), QP = MM::template tile_bytes<64>(Q), QQ = MM::template tile_bytes<Q>(Q);
-    constexpr int LOADS = (1 + 2 * TP) * QP, PAIRS = (2 * XP + TP) * QQ;
+    constexpr int LOADS = (1 + 2 * TP) * QP, PAIRS = 3 * TP * QQ;
     __shared__ __attribute__((aligned(16))) uint8_t sk[QN];
     __shared__ __attribute__((aligned(16))) uint8_t sq[QN];
     __shared__ __attribute__((aligned(16))) uint8_t pool[LOADS > PAIRS ? LOADS : PAIRS];
@@ -336,8 +335,8 @@ __global__ __launch_bounds__(64 * kGradWaves) void delta_grad_kernel(DeltaArgs a
     uint8_t* const tz = pool + QP;              // dZ
     uint8_t* const te = pool + (1 + TP) * QP;   // E
     uint8_t* const tx = pool;                   // X
-    uint8_t* const tf = pool + XP * QQ;         // F
-    uint8_t* const tw = pool + 2 * XP * QQ;     // the pairs' products themselves
+    uint8_t* const tf = pool + TP * QQ;         // F
+    uint8_t* const tw = pool + 2 * TP * QQ;     // the pairs' products themselves
     const int tid = threadIdx.x, lane = tid & 63, li_ = lane & 15, g4_ = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6), cg = w % CG, rg = RG == 1 ? 0 : w / CG;
     int64_t unit = xcd_order(blockIdx.x, gridDim.x);
@@ -487,7 +486,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void delta_grad_kernel(DeltaArgs a
             for (int kk = 0; kk < KP; ++kk) {
                 const int li = here(li_), g4 = here(g4_);
                 typename MM::template Frag<3> fs[CT];
-                typename MM::template Frag<2> fd[CT];
+                typename MM::template Frag<3> fd[CT];
 #pragma unroll
                 for (int j = 0; j < CT; ++j) {
                     if (rg == 0) {
@@ -495,19 +494,19 @@ __global__ __launch_bounds__(64 * kGradWaves) void delta_grad_kernel(DeltaArgs a
                         for (int m = 0; m < R; ++m) dot += ns[kk][j][m] * nd[kk][j][m];
                     }
                     fs[j] = MM::template parts<3>(ns[kk][j]);
-                    fd[j] = MM::template parts<2>(nd[kk][j]);
+                    fd[j] = MM::template parts<3>(nd[kk][j]);
                 }
 #pragma unroll
                 for (int i = 0; i < RW; ++i) {
                     const int r0 = 16 * (rg * RW + i);
                     const auto y = MM::template along<64>(ty, r0, kk, li, g4);
                     const auto z = of_parts<MM, TP>([&](int q) { return MM::template along<64>(tz + q * QP, r0, kk, li, g4); });
-                    const auto e = of_parts<MM, XP>([&](int q) { return MM::template along<64>(te + q * QP, r0, kk, li, g4); });
+                    const auto e = of_parts<MM, TP>([&](int q) { return MM::template along<64>(te + q * QP, r0, kk, li, g4); });
 #pragma unroll
                     for (int j = 0; j < CT; ++j) {
                         MM::template mac<1, 3>(qo[i][j], y, fs[j]);
                         MM::template mac<TP, 3>(ko[i][j], z, fs[j]);
-                        MM::template mac<XP, 2>(ke[i][j], e, fd[j]);
+                        MM::template mac<TP, 3>(ke[i][j], e, fd[j]);
                     }
                 }
             }
@@ -551,12 +550,12 @@ __global__ __launch_bounds__(64 * kGradWaves) void delta_grad_kernel(DeltaArgs a
                 const float f = below ? -r * db[m][e] : 0.0f;
                 const float pair = below ? x * qk[e] + f * be * kk[e] : 0.0f;
                 sum += below ? f * kk[e] : 0.0f;
-                put_pair<MM, XP>(tx, QQ, t, s, x);
-                put_pair<MM, XP>(tf, QQ, t, s, f * be);
+                put_pair<MM, TP>(tx, QQ, t, s, x);
+                put_pair<MM, TP>(tf, QQ, t, s, f * be);
                 put_pair<MM, TP>(tw, QQ, t, s, pair);
                 if (MM::KB == 32 && (rt & 1) && tile == rt - 1) {  // above the diagonal, in its contraction block
-                    put_pair<MM, XP>(tx, QQ, t - 16, s + 16, 0.0f);
-                    put_pair<MM, XP>(tf, QQ, t - 16, s + 16, 0.0f);
+                    put_pair<MM, TP>(tx, QQ, t - 16, s + 16, 0.0f);
+                    put_pair<MM, TP>(tf, QQ, t - 16, s + 16, 0.0f);
                     put_pair<MM, TP>(tw, QQ, t - 16, s + 16, 0.0f);
                 }
             }
@@ -634,16 +633,16 @@ __global__ __launch_bounds__(64 * kGradWaves) void delta_grad_kernel(DeltaArgs a
                     const auto fk = MM::template columns<W>(sk, kk * MM::KB, ct, li, g4);
                     const auto fq = MM::template columns<W>(sq, kk * MM::KB, ct, li, g4);
                     if (kk * MM::KB <= 16 * rt) {
-                        const auto x = of_parts<MM, XP>([&](int q) { return MM::template rows<Q>(tx + q * QQ, 16 * rt, kk, li, g4); });
-                        MM::template mac<XP, 1>(dq[i][j], x, fk);
-                        const auto y = of_parts<MM, XP>([&](int q) { return MM::template rows<Q>(tf + q * QQ, 16 * rt, kk, li, g4); });
-                        MM::template mac<XP, 1>(dk[i][j], y, fk);
+                        const auto x = of_parts<MM, TP>([&](int q) { return MM::template rows<Q>(tx + q * QQ, 16 * rt, kk, li, g4); });
+                        MM::template mac<TP, 1>(dq[i][j], x, fk);
+                        const auto y = of_parts<MM, TP>([&](int q) { return MM::template rows<Q>(tf + q * QQ, 16 * rt, kk, li, g4); });
+                        MM::template mac<TP, 1>(dk[i][j], y, fk);
                     }
                     if ((kk + 1) * MM::KB > 16 * rt) {
-                        const auto x = of_parts<MM, XP>([&](int q) { return MM::template columns<Q>(tx + q * QQ, kk * MM::KB, rt, li, g4); });
-                        MM::template mac<XP, 1>(dk[i][j], x, fq);
-                        const auto y = of_parts<MM, XP>([&](int q) { return MM::template columns<Q>(tf + q * QQ, kk * MM::KB, rt, li, g4); });
-                        MM::template mac<XP, 1>(dk[i][j], y, fk);
+                        const auto x = of_parts<MM, TP>([&](int q) { return MM::template columns<Q>(tx + q * QQ, kk * MM::KB, rt, li, g4); });
+                        MM::template mac<TP, 1>(dk[i][j], x, fq);
+                        const auto y = of_parts<MM, TP>([&](int q) { return MM::template columns<Q>(tf + q * QQ, kk * MM::KB, rt, li, g4); });
+                        MM::template mac<TP, 1>(dk[i][j], y, fk);
                     }
                 }
             }
