@@ -4,7 +4,8 @@
 // Per head, with state h [P, N], a_t = e^gate_t and b_t = beta_t:
 //     e_t = v_t - a_t h_{t-1} k_t,   h_t = a_t h_{t-1} + b_t e_t k_t^T,   y_t = scale h_t q_t
 // Over a chunk of Q tokens that starts from h_0, with G_t the sum of the gates from the chunk's
-// start on and r_ts = e^(G_t - G_s) (0 where a packed sequence starts in (s, t]):
+// start on (from a packed sequence's where that starts later) and r_ts = e^(G_t - G_s) (0 where a
+// packed sequence starts in (s, t]):
 //     D_ts = r_ts (k_t . k_s) b_s (s < t),   T = (I + D)^-1,   M_ts = scale r_ts q_t . k_s (s <= t)
 //     Z = V - e^G K h_0^T,   E = T Z,   U = b E
 //     Y = scale e^G Q h_0^T + M U,   h_Q = e^{G_Q} h_0 + U^T e^{G_Q - G} K
@@ -57,7 +58,7 @@ struct DeltaArgs {
     float* phi;      // [B, H, segs, N, N]: what a segment makes of the state before it, from the right
     float* gain;     // [B, H, segs, P, N]: what its own tokens bring
     float* entry;    // [B, H, segs, P, N]: the state before it (backward: the gradient of the state after it)
-    double* gates;   // [B, H, chunks, Q]: sums of gates from the chunk's start on, backward only
+    double* gates;   // [B, H, chunks, Q]: sums of gates (TokenSums), backward only
     float* factors;  // [B, H, chunks, kFactors, Q]: e^G from the chunk's start, e^{G_Q - G}, beta, sequences begun
 };
 
@@ -505,8 +506,10 @@ __device__ __forceinline__ int xcd_order(int block, int blocks) {
     return x * per + (x < more ? x : more) + (block >> 3);
 }
 
-// Of the chunk's token `lane`: the sum of its gates from the chunk's start on, the packed sequences
-// begun since then, and beta (tokens behind the row: gate 0, beta 0).  All 64 lanes call it.
+// Of the chunk's token `lane`: the sum of the gates from the chunk's start on, or from its sequence's where that
+// starts within the chunk (a first token's gate counts for nothing), the packed sequences begun since the chunk's
+// start, and beta (tokens behind the row: gate 0, beta 0).  Sums of two tokens are compared within a sequence only,
+// and what one sequence's gates hold is not in the next one's.  All 64 lanes call it.
 struct TokenSums {
     double gates;
     int starts;
@@ -517,16 +520,16 @@ __device__ __forceinline__ TokenSums token_sums(const DeltaArgs& a, int64_t b, i
     TokenSums s{0.0, 0, 0.0f};
     if (lane < valid) {
         const int64_t t = b * a.L + t0 + lane;
-        if (a.gate) s.gates = gate_of(a.gate[t * a.H + h]);
         s.beta = a.beta[t * a.H + h];
         if (a.seq && t0 + lane > 0) s.starts = a.seq[t] != a.seq[t - 1];
+        if (a.gate && s.starts == 0) s.gates = gate_of(a.gate[t * a.H + h]);
     }
 #pragma unroll
     for (int d = 1; d < Q; d <<= 1) {
         const double o = __shfl_up(s.gates, d);
         const int r = __shfl_up(s.starts, d);
         if (lane >= d) {
-            s.gates += o;
+            s.gates += s.starts == 0 ? o : 0.0;  // (starts among the d tokens up to this one)
             s.starts += r;
         }
     }
