@@ -517,8 +517,9 @@ ssm_status_t ssm_gated_scan_step(const void* x, int64_t x_row, const void* gate,
  * a_t = exp(gate_t) (1 when gate is NULL), h_{-1} = initial_state (zeros when NULL); the state restarts
  * from zero where seq_idx[b,t] != seq_idx[b,t-1] (a_t counts as 0 there).  The recurrence contracts
  * for beta_t |k_t|^2 <= 2 and gates <= 0: keys are meant to be normed (ssm_qk_norm_fwd); outside that
- * range states grow as the formula has them grow.  Gates above 0 are served while the products of
- * decays of any 64 consecutive tokens are finite in fp32; gates below -1e4 count as -1e4.
+ * range states grow as the formula has them grow.  Gates above 0 are served while the states and the
+ * products of decays of any 64 consecutive tokens are finite in fp32 (a rounding error grows by such
+ * a product); gates below -1e4 count as -1e4.
  *
  *   q, k           [batch, seqlen, ngroups, dstate]  dtype; token t of row b at
  *                  p + (b * seqlen + t) * p_row elements, its heads side by side (a channel range of

@@ -55,7 +55,8 @@ struct DeltaArgs {
     uint8_t* Tt;     // transposed, backward only (M is transposed there)
     // rows cut into `segs` segments of seg_chunks chunks where there are few (plan_segments)
     int64_t segs, seg_chunks;
-    float* phi;      // [B, H, segs, N, N]: what a segment makes of the state before it, from the right
+    float* phi;      // [B, H, segs, N, N]: what a segment makes of the state before it, from the right; row m
+    int32_t* power;  // [B, H, segs, N]: times 2^power[m]
     float* gain;     // [B, H, segs, P, N]: what its own tokens bring
     float* entry;    // [B, H, segs, P, N]: the state before it (backward: the gradient of the state after it)
     double* gates;   // [B, H, chunks, Q]: sums of gates (TokenSums), backward only
@@ -491,6 +492,27 @@ __device__ __forceinline__ void scale_state(f4 (&v)[NT], float through) {
     for (int i = 0; i < NT; ++i) v[i] = STARTS && through == 0.0f ? f4{0, 0, 0, 0} : v[i] * through;
 }
 
+// A unit row's walk through a segment of gates above 0 may pass fp32's range where the state that it is multiplied
+// with is 0 or small.  So the row keeps a power of 2, from 0 on, that holds its largest value below 2.
+template <int NT>
+__device__ __forceinline__ void keep_in_range(f4 (&row)[NT], int& power) {
+    float most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) most = fmaxf(most, fabsf(row[i][e]));
+    most = fmaxf(most, __shfl_xor(most, 16));
+    most = fmaxf(most, __shfl_xor(most, 32));
+    // (a row that is 0 or not finite stays as it is)
+    const int want = most > 0.0f && most < __builtin_inff() ? max(power + __builtin_amdgcn_frexp_expf(most) - 1, 0) : power;
+    if (__all(want == power)) return;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) row[i][e] = __builtin_ldexpf(row[i][e], power - want);
+    power = want;
+}
+
 // rows of a tile whose factor is 0, by the four wavefronts that walk
 template <class MM, int W>
 __device__ __forceinline__ void clear_rows(uint8_t* tile, const float* factor) {
@@ -588,6 +610,8 @@ size_t place_chunks(DeltaArgs& a, uint8_t* ws, bool bwd) {
     const size_t states = a.segs > 1 ? static_cast<size_t>(a.B * a.H * a.segs) : 0;
     a.phi = reinterpret_cast<float*>(ws + at);
     at += states * a.N * a.N * 4;
+    a.power = reinterpret_cast<int32_t*>(ws + at);
+    at += states * a.N * 4;
     a.gain = reinterpret_cast<float*>(ws + at);
     at += states * a.P * a.N * 4;
     a.entry = reinterpret_cast<float*>(ws + at);

@@ -376,6 +376,7 @@ __global__ __launch_bounds__(320) void delta_walk_kernel(DeltaArgs a, DeltaSaved
             for (int e = 0; e < 4; ++e) hs[i][e] = n + e == p ? 1.0f : 0.0f;
         }
     }
+    int power = 0;
     for (int c = c0; c < c1; ++c) {
         const int64_t t0 = b * a.L + static_cast<int64_t>(c) * Q;
         const int valid = rows_of(c);
@@ -470,8 +471,10 @@ __global__ __launch_bounds__(320) void delta_walk_kernel(DeltaArgs a, DeltaSaved
         };
         if (marks != 0) chunk(std::true_type{});
         else chunk(std::false_type{});
+        if (MODE == kSpan && rows) keep_in_range(hs, power);
     }
     __syncthreads();
+    if (MODE == kSpan && rows && have && g4 == 0) a.power[bhs * N + p] = power;
     if (to && have) {
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
@@ -483,7 +486,7 @@ __global__ __launch_bounds__(320) void delta_walk_kernel(DeltaArgs a, DeltaSaved
 
 // ---------------------------------------------------------------------------------------
 // The states before the segments, h = h phi + gain from the first on (BACK: the gradients after them,
-// g = g phi^T + gain from the last on): 16 channels of a head a block, a wavefront 16 columns a
+// g = g phi^T + gain from the last on), with the powers of phi's rows m put to h (BACK: to the product): 16 channels of a head a block, a wavefront 16 columns a
 // product of the fp32 instruction, the next segments' phi and gain loaded meanwhile.
 // 2 us a segment at dstate 128, 1.1 at 64 (one segment's loads ahead, and the starts read by the way: 4.3
 // and 2.9).
@@ -510,9 +513,11 @@ __global__ __launch_bounds__(64 * NT) void delta_join_states_kernel(DeltaArgs a)
     for (int c = threadIdx.x; c < static_cast<int>(a.chunks); c += 64 * NT)
         if (a.factors[((bh * a.chunks + c) * kFactors + 4) * Q - 1] != 0.0f) cut[c / static_cast<int>(a.seg_chunks)] = true;
     f4 phi[AHEAD][NT], gain[AHEAD];
-    const auto load = [&](int i, f4 (&ph)[NT], f4& gn) {
+    int power[AHEAD];  // of row n
+    const auto load = [&](int i, f4 (&ph)[NT], f4& gn, int& pw) {
         if (i + 1 >= segs) return;
         const int64_t at = bh * segs + s0 + step * i;
+        pw = n < N ? a.power[at * N + n] : 0;
         const Buffer r = buffer(a.phi + at * N * N, static_cast<int64_t>(N) * N * 4);
         const Buffer rg = buffer(a.gain + at * P * N, static_cast<int64_t>(P) * N * 4);
 #pragma unroll
@@ -529,7 +534,7 @@ __global__ __launch_bounds__(64 * NT) void delta_join_states_kernel(DeltaArgs a)
         for (int e = 0; e < 4; ++e) gn[e] = load_at<float>(rg, n < N ? ((p0 + e) * N + n) * 4 : kOutside);
     };
 #pragma unroll
-    for (int d = 0; d < AHEAD; ++d) load(d, phi[d], gain[d]);
+    for (int d = 0; d < AHEAD; ++d) load(d, phi[d], gain[d], power[d]);
     for (int i0 = 0; i0 < segs; i0 += AHEAD) {
 #pragma unroll
         for (int d = 0; d < AHEAD; ++d) {
@@ -539,7 +544,7 @@ __global__ __launch_bounds__(64 * NT) void delta_join_states_kernel(DeltaArgs a)
             float* const entry = a.entry + (bh * segs + s) * P * N;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                sh[(4 * g4 + e) * LD + n] = h[e];
+                sh[(4 * g4 + e) * LD + n] = BACK || i + 1 == segs ? h[e] : __builtin_ldexpf(h[e], power[d]);
                 if (p0 + e < P && n < N) entry[static_cast<int64_t>(p0 + e) * N + n] = h[e];
             }
             __syncthreads();
@@ -550,8 +555,12 @@ __global__ __launch_bounds__(64 * NT) void delta_join_states_kernel(DeltaArgs a)
                 const f4 l = *reinterpret_cast<const f4*>(&sh[li * LD + 16 * kk + 4 * g4]);
                 ByF32::mac<1, 1>(sum, ByF32::Frag<1>{l}, ByF32::Frag<1>{phi[d][kk]});
             }
+            if (BACK) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[e] = __builtin_ldexpf(sum[e], power[d]);
+            }
             h = cut[s] ? gain[d] : sum + gain[d];
-            load(i + AHEAD, phi[d], gain[d]);
+            load(i + AHEAD, phi[d], gain[d], power[d]);
         }
     }
 }
