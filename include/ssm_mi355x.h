@@ -533,10 +533,11 @@ ssm_status_t ssm_gated_scan_step(const void* x, int64_t x_row, const void* gate,
  *   workspace      ..._workspace_size bytes, 256-byte aligned
  * dstate a multiple of 4, at most 256; any headdim.  States and sums in fp32 (sums of gates in 64
  * bits), products of operands that hold 24 bits in either dtype; outputs rounded once.
- * Deterministic.  A NaN or infinity reaches the tokens of its own chunk (64 tokens for
- * SSM_BF16, 32 for SSM_F32, from the row's start), forward its sequence's after them, and backward all
- * chunks that its sequence has tokens in, other sequences' tokens in those among them; no token of
- * other chunks, and no state that its sequence does not reach.
+ * Deterministic.  A NaN or infinity reaches, forward, its own sequence only:
+ * its tokens from its chunk's first on (chunks of 64 tokens for SSM_BF16, 32 for SSM_F32, from the
+ * row's start), and its final state; backward all chunks that its sequence has tokens in, other
+ * sequences' tokens in those among them, no token of other chunks, and no state that its sequence
+ * does not reach.  The gate of a token that restarts the state reaches nothing.
  *
  * ssm_delta_scan_fwd   final_state may be initial_state; no other output may overlap an input.
  *     seqlen = 0: final = initial (or zeros).

@@ -438,9 +438,9 @@ __device__ __forceinline__ void stage_elements(uint8_t* tile, const typename MM:
 
 // A NaN or infinity of one packed sequence times the 0 that keeps the sequences apart would reach the
 // others, and with the state the chunks that those go on in.  So where a chunk holds several sequences
-// and an operand of a product over its tokens is not finite, only the rows of the sequence whose state
-// goes on enter it, the other rows of the result are NaN, and rows of K and Q whose factor is 0 are
-// cleared before they enter the state.
+// and an operand of a product over its tokens is not finite, such values are 0 in the product and the
+// rows of their sequences NaN in its result, and rows of K and Q whose factor is 0 are cleared before
+// they enter the state.
 template <int RT>
 __device__ __forceinline__ bool all_finite(const f4 (&v)[RT]) {
     float s = 0.0f;
@@ -450,26 +450,53 @@ __device__ __forceinline__ bool all_finite(const f4 (&v)[RT]) {
         for (int e = 0; e < 4; ++e) s += v[i][e] * 0.0f;
     return __all(s == 0.0f);
 }
-// v's rows outside sequence `only` (begun: of the chunk's tokens)
-template <int RT>
-__device__ __forceinline__ void fill_others(f4 (&v)[RT], const float* begun, int only, int g4, float with) {
+// MM::of_tiles of finite values, 0 for the others
+template <class MM, int PARTS, bool FINITE, int RT>
+__device__ __forceinline__ typename MM::template Frag<PARTS> finite_tiles(const f4 (&v)[RT], int kk) {
+    if constexpr (!FINITE) {
+        return MM::template of_tiles<PARTS>(v, kk);
+    } else {
+        constexpr int N = MM::KB / 16;
+        f4 t[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t[i][e] = __builtin_isfinite(v[N * kk + i][e]) ? v[N * kk + i][e] : 0.0f;
+        return MM::template of_tiles<PARTS>(t, 0);
+    }
+}
+// all rows of the sequences that have one of `rows` (starts: a bit for each sequence's first row but the chunk's)
+__device__ __forceinline__ uint64_t whole_sequences(uint64_t rows, uint64_t starts) {
+    uint64_t all = 0;
+    for (int from = 0; from < 64;) {  // as many rounds as sequences
+        const int to = starts ? __builtin_ctzll(starts) : 64;
+        starts &= starts - 1;
+        const uint64_t own = (~0ull >> (64 - (to - from))) << from;
+        all |= rows & own ? own : 0;
+        from = to;
+    }
+    return all;
+}
+// After out += product of in's finite values: the rows of the sequences (begun: of the chunk's Q tokens) that have
+// others in the lane's column
+template <bool STARTS, int Q, int RT>
+__device__ __forceinline__ void mark_sequences(f4 (&out)[RT], const f4 (&in)[RT], const float* begun, int lane) {
+    if (!STARTS || all_finite(in)) return;
+    const int g4 = lane >> 4;
+    unsigned long long rows = 0;
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (static_cast<int>(begun[16 * i + 4 * g4 + e]) % static_cast<int>(kNotFinite) != only) v[i][e] = with;
-}
-// out += product(in), with in's rows outside `only` taken out where that is needed
-template <bool STARTS, int RT, class F>
-__device__ __forceinline__ void kept_apart(f4 (&out)[RT], f4 (&in)[RT], const float* begun, int only, int g4, F product) {
-    if constexpr (STARTS) {
-        const bool apart = !all_finite(in);
-        if (apart) fill_others(in, begun, only, g4, 0.0f);
-        product();
-        if (apart) fill_others(out, begun, only, g4, __builtin_nanf(""));
-    } else {
-        product();
-    }
+        for (int e = 0; e < 4; ++e) rows |= static_cast<unsigned long long>(!__builtin_isfinite(in[i][e])) << (16 * i + e);
+    rows <<= 4 * g4;
+    rows |= __shfl_xor(rows, 16);
+    rows |= __shfl_xor(rows, 32);
+    const uint64_t starts = __ballot(lane > 0 && lane < Q && begun[lane < Q ? lane : 0] != begun[lane > 0 && lane < Q ? lane - 1 : 0]);
+    rows = whole_sequences(rows, starts) >> (4 * g4);
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[i][e] = rows >> (16 * i + e) & 1 ? __builtin_nanf("") : out[i][e];
 }
 // Products with the factors of a chunk's tokens.  Only where a sequence starts within the chunk (STARTS) is
 // a factor 0 by more than underflow: there it leaves nothing of what is not finite either.

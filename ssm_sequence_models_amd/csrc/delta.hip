@@ -247,6 +247,7 @@ __global__ __launch_bounds__(MM::Q * 4, NT <= 8 ? 4 : 1) void delta_prep_kernel(
 // kSave: for the backward, the states and E in place of y.  kSpan: a segment from zero, and behind the
 // channels the N unit rows without values; only the state after it.
 // DIRECT: see DeltaArgs; without it tokens pass through registers
+// (Registers for two blocks a CU where LDS has the place, dstate up to 64.)
 // ---------------------------------------------------------------------------------------
 enum { kOut, kSave, kSpan };
 template <class MM, int NT, int MODE>
@@ -259,7 +260,7 @@ struct WalkLds {
 };
 
 template <class MM, int NT, int MODE, bool DIRECT>
-__global__ __launch_bounds__(320) void delta_walk_kernel(DeltaArgs a, DeltaSaved keep) {
+__global__ __launch_bounds__(320, NT <= 4 && (MODE == kSpan || (MODE == kSave && DIRECT)) ? 3 : 1) void delta_walk_kernel(DeltaArgs a, DeltaSaved keep) {
     using S = typename MM::S;
     using O = WalkLds<MM, NT, MODE>;
     constexpr int Q = MM::Q, RT = Q / 16, KT = Q / MM::KB, W = 16 * NT, KN = W / MM::KB, TP = MM::TP, ES = sizeof(S);
@@ -417,15 +418,14 @@ __global__ __launch_bounds__(320) void delta_walk_kernel(DeltaArgs a, DeltaSaved
             if (MODE == kOut) scale_rows<STARTS>(y, sf, a.scale, g4);
 #pragma unroll
             for (int i = 0; i < RT; ++i) z[i] = (rows ? f4{0, 0, 0, 0} : MM::template four_rows<64>(half + O::V, 16 * i, w, li, g4)) - z[i];
-            kept_apart<STARTS>(x, z, sf + 3 * Q, marks % static_cast<int>(kNotFinite), g4, [&] {
 #pragma unroll
-                for (int kk = 0; kk < KT; ++kk) {
-                    const auto s = MM::template of_tiles<3>(z, kk);
+            for (int kk = 0; kk < KT; ++kk) {
+                const auto s = finite_tiles<MM, 3, STARTS>(z, kk);
 #pragma unroll
-                    for (int i = kk * MM::KB / 16; i < RT; ++i)
-                        MM::template mac<TP, 3>(x[i], frag<MM, TP>(half + O::T, frag_at<MM>(i, kk, false), lane), s);
-                }
-            });
+                for (int i = kk * MM::KB / 16; i < RT; ++i)
+                    MM::template mac<TP, 3>(x[i], frag<MM, TP>(half + O::T, frag_at<MM>(i, kk, false), lane), s);
+            }
+            mark_sequences<STARTS, Q>(x, z, sf + 3 * Q, lane);
             if (MODE == kSave) {
                 const Buffer r = token_buffer<float>(keep.e, t0, static_cast<int64_t>(H) * P, static_cast<int64_t>(h) * P, DIRECT ? valid : 1, P);
 #pragma unroll
@@ -442,11 +442,12 @@ __global__ __launch_bounds__(320) void delta_walk_kernel(DeltaArgs a, DeltaSaved
             if (MODE == kOut) {
 #pragma unroll
                 for (int kk = 0; kk < KT; ++kk) {
-                    const auto s = MM::template of_tiles<TP>(x, kk);
+                    const auto s = finite_tiles<MM, TP, STARTS>(x, kk);
 #pragma unroll
                     for (int i = kk * MM::KB / 16; i < RT; ++i)
                         MM::template mac<TP, TP>(y[i], frag<MM, TP>(half + O::M, frag_at<MM>(i, kk, false), lane), s);
                 }
+                mark_sequences<STARTS, Q>(y, x, sf + 3 * Q, lane);
                 uint8_t* const to = y_of(c);  // (this wavefront's columns, whose values it has read)
 #pragma unroll
                 for (int i = 0; i < RT; ++i)

@@ -193,15 +193,14 @@ __global__ __launch_bounds__(320) void delta_back_kernel(DeltaArgs a, Buffers u)
                 if (mine && li < 4) part[Q + 16 * i] = s;
             }
             // dU += M^T dY
-            kept_apart<STARTS>(du, dy, sf + 3 * Q, 0, g4, [&] {
 #pragma unroll
-                for (int kk = 0; kk < KT; ++kk) {
-                    const auto s = MM::template of_tiles<1>(dy, kk);
+            for (int kk = 0; kk < KT; ++kk) {
+                const auto s = finite_tiles<MM, 1, STARTS>(dy, kk);
 #pragma unroll
-                    for (int i = 0; i < (kk + 1) * MM::KB / 16; ++i)
-                        MM::template mac<TP, 1>(du[i], frag<MM, TP>(half + O::M, frag_at<MM>(i, kk, true), lane), s);
-                }
-            });
+                for (int i = 0; i < (kk + 1) * MM::KB / 16; ++i)
+                    MM::template mac<TP, 1>(du[i], frag<MM, TP>(half + O::M, frag_at<MM>(i, kk, true), lane), s);
+            }
+            mark_sequences<STARTS, Q>(du, dy, sf + 3 * Q, lane);
 #pragma unroll
             for (int i = 0; i < (SPAN ? 0 : RT); ++i) {
                 const f4 v = du[i] * ev[i];
@@ -210,15 +209,14 @@ __global__ __launch_bounds__(320) void delta_back_kernel(DeltaArgs a, Buffers u)
             }
             // dZ = T^T (b dU)
             scale_rows<false>(du, sf + 2 * Q, 1.0f, g4);
-            kept_apart<STARTS>(dz, du, sf + 3 * Q, 0, g4, [&] {
 #pragma unroll
-                for (int kk = 0; kk < KT; ++kk) {
-                    const auto s = MM::template of_tiles<3>(du, kk);
+            for (int kk = 0; kk < KT; ++kk) {
+                const auto s = finite_tiles<MM, 3, STARTS>(du, kk);
 #pragma unroll
-                    for (int i = 0; i < (kk + 1) * MM::KB / 16; ++i)
-                        MM::template mac<TP, 3>(dz[i], frag<MM, TP>(half + O::T, frag_at<MM>(i, kk, true), lane), s);
-                }
-            });
+                for (int i = 0; i < (kk + 1) * MM::KB / 16; ++i)
+                    MM::template mac<TP, 3>(dz[i], frag<MM, TP>(half + O::T, frag_at<MM>(i, kk, true), lane), s);
+            }
+            mark_sequences<STARTS, Q>(dz, du, sf + 3 * Q, lane);
             const Buffer rz = token_buffer<float>(u.dz, t0, erow, static_cast<int64_t>(h) * P, DIRECT ? valid : 1, P);
 #pragma unroll
             for (int i = 0; i < (SPAN ? 0 : RT); ++i)
