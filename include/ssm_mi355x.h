@@ -584,7 +584,8 @@ ssm_status_t ssm_delta_scan_step(const void* q, int64_t q_row, const void* k, in
  *     m = weight r x
  *     out: the pairs (m_i, m_{i + rotary_dim / 2}), or (m_2i, m_{2i+1}) if interleaved, turned by
  *     the angle positions * inv_freq[i]; channels from rotary_dim on are m
- * A head of zeros with eps = 0 gives 0 (and the gradient 0).  Statistics, angles' sines and sums in
+ * A head of zeros with eps = 0 gives 0 (and the gradient 0); any other finite values are normed, also
+ * where their squares leave fp32's range.  Statistics, angles' sines and sums in
  * fp32, angles themselves in 64 bits (any int32 position, negative ones too); outputs rounded once.
  * The backward recomputes the statistics and gives, from dq_out and dk_out, dq, dk and the sums over
  * tokens and heads dq_weight, dk_weight (fixed order: deterministic).

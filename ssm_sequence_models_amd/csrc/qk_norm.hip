@@ -209,10 +209,37 @@ __device__ __forceinline__ void angles(const QkNormCall& c, float2* cs, int64_t 
     }
 }
 
-// sum of squares -> 1 / norm; 0 for a head of zeros without eps
-__device__ __forceinline__ float inverse(float squares, const QkNormCall& c) {
-    const float v = squares * (c.l2 ? 1.0f : 1.0f / static_cast<float>(c.D)) + c.eps;
-    return v > 0.0f ? 1.0f / sqrtf(v) : v == 0.0f ? 0.0f : v;  // NaN stays one
+// A head's 1 / norm (0 for a head of zeros without eps).  Where the squares leave fp32's range, or come near its
+// ends, the values and the norm are taken in units of 2^up instead of 1: v is divided by it, and what is formed of
+// 1 / norm without v is to be.
+template <int LPH, int V>
+__device__ __forceinline__ float inverse(float (&v)[V], const QkNormCall& c, int& up) {
+    const float per = c.l2 ? 1.0f : 1.0f / static_cast<float>(c.D);
+    const auto squares = [&] {
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) sum += v[j] * v[j];
+        return sum_lanes<LPH>(sum) * per;
+    };
+    float s = squares() + c.eps;
+    up = 0;
+    if (__float_as_uint(s) - 0x17800000u > 0x38800000u) {  // not within 2^-80 .. 2^80, for a head's lanes alike
+        float most = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) most = fmaxf(most, fabsf(v[j]));
+#pragma unroll
+        for (int d = 1; d < LPH; d <<= 1) most = fmaxf(most, __shfl_xor(most, d));
+        if (s != s) return s;  // NaN stays one
+        if (s == 0.0f && most == 0.0f) return 0.0f;
+        if (most < __builtin_inff() && c.eps < __builtin_inff()) {
+            const int of_eps = c.eps > 0.0f ? (__builtin_amdgcn_frexp_expf(c.eps) >> 1) + 1 : -1000;
+            up = max(most > 0.0f ? __builtin_amdgcn_frexp_expf(most) : -1000, of_eps);
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[j] = __builtin_ldexpf(v[j], -up);
+            s = squares() + __builtin_ldexpf(c.eps, -2 * up);
+        }
+    }
+    return 1.0f / sqrtf(s);
 }
 
 // The next head's loads are in flight while one is computed.
@@ -254,10 +281,12 @@ __global__ __launch_bounds__(kThreads) void qk_norm_fwd_kernel(QkNormCall c, int
             lane.partners(o, u);
             next_head(token, head, heads, tokens_on, heads_on);
             load();
-            float sum = 0.0f;
+            int up;
+            const float r = inverse<LPH>(v, c, up);
+            if (up != 0) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) sum += v[j] * v[j];
-            const float r = inverse(sum_lanes<LPH>(sum), c);
+                for (int j = 0; j < V; ++j) u[j] = __builtin_ldexpf(u[j], -up);
+            }
 #pragma unroll
             for (int j = 0; j < V; ++j) v[j] *= r * w[j];
             if (lane.turned) {
@@ -323,10 +352,8 @@ __global__ __launch_bounds__(kThreads) void qk_norm_bwd_kernel(QkNormCall c, int
                 next_head(token, head, heads, tokens_on, heads_on);
                 load();
                 if (lane.turned) lane.turn(cs + t * half, -1.0f, d, u);
-                float sum = 0.0f;
-#pragma unroll
-                for (int j = 0; j < V; ++j) sum += v[j] * v[j];
-                const float r = inverse(sum_lanes<LPH>(sum), c);
+                int up;
+                const float r = inverse<LPH>(v, c, up);
                 float dot = 0.0f;
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
@@ -338,6 +365,10 @@ __global__ __launch_bounds__(kThreads) void qk_norm_bwd_kernel(QkNormCall c, int
                 dot = sum_lanes<LPH>(dot) * per;
 #pragma unroll
                 for (int j = 0; j < V; ++j) d[j] = r * (d[j] - v[j] * dot);
+                if (up != 0) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) d[j] = __builtin_ldexpf(d[j], -up);
+                }
                 lane.store(outs + (first + t) * out_row + h * D_, d);
             }
         }
