@@ -1303,13 +1303,19 @@ ssm_status_t check_delta_dims(const char* fn, int64_t batch, int64_t seqlen, int
     if (!std::isfinite(scale)) return fail(SSM_ERR_INVALID_ARG, std::string(fn) + ": scale must be finite");
     return SSM_OK;
 }
-// sizes whose products below do not leave 63 bits, nor their grids 31
+// sizes whose products below do not leave 63 bits, nor their numbers of blocks 31
 bool delta_sizes_fit(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim) {
     const int64_t most = int64_t{1} << 31;
     if (batch >= most || seqlen >= most || nheads >= most) return false;
-    if (batch == 0 || seqlen == 0) return true;
+    if (batch == 0) return true;
     return nheads < most / batch && (seqlen + 31) / 32 < most / (batch * nheads) &&
            (headdim + 15) / 16 < most / (batch * nheads);
+}
+// the same for the calls over long rows, and grids that can be launched
+bool delta_rows_fit(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim, int64_t ngroups, int64_t dstate,
+                    ssm_dtype_t dtype, bool bwd) {
+    return delta_sizes_fit(batch, seqlen, nheads, headdim) &&
+           (batch == 0 || seqlen == 0 || ssm::delta_launches_fit(batch, seqlen, nheads, headdim, ngroups, dstate, dtype, bwd));
 }
 
 }  // namespace
@@ -1318,7 +1324,7 @@ size_t ssm_delta_scan_fwd_workspace_size(int64_t batch, int64_t seqlen, int64_t 
                                          int64_t ngroups, int64_t dstate, ssm_dtype_t dtype) {
     if (batch <= 0 || seqlen <= 0 ||
         check_delta_dims("ssm_delta_scan_fwd_workspace_size", batch, seqlen, nheads, headdim, ngroups, dstate, 1.0f, dtype) != SSM_OK ||
-        !delta_sizes_fit(batch, seqlen, nheads, headdim))
+        !delta_rows_fit(batch, seqlen, nheads, headdim, ngroups, dstate, dtype, false))
         return 0;
     return ssm::delta_fwd_workspace_bytes(batch, seqlen, nheads, headdim, ngroups, dstate, dtype);
 }
@@ -1327,7 +1333,7 @@ size_t ssm_delta_scan_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t 
                                          int64_t ngroups, int64_t dstate, ssm_dtype_t dtype) {
     if (batch <= 0 || seqlen <= 0 ||
         check_delta_dims("ssm_delta_scan_bwd_workspace_size", batch, seqlen, nheads, headdim, ngroups, dstate, 1.0f, dtype) != SSM_OK ||
-        !delta_sizes_fit(batch, seqlen, nheads, headdim))
+        !delta_rows_fit(batch, seqlen, nheads, headdim, ngroups, dstate, dtype, true))
         return 0;
     return ssm::delta_bwd_workspace_bytes(batch, seqlen, nheads, headdim, ngroups, dstate, dtype);
 }
@@ -1341,7 +1347,7 @@ ssm_status_t ssm_delta_scan_fwd(const void* q, int64_t q_row, const void* k, int
     const char* fn = "ssm_delta_scan_fwd";
     ssm_status_t st = check_delta_dims(fn, batch, seqlen, nheads, headdim, ngroups, dstate, scale, dtype);
     if (st != SSM_OK) return st;
-    if (!delta_sizes_fit(batch, seqlen, nheads, headdim))
+    if (!delta_rows_fit(batch, seqlen, nheads, headdim, ngroups, dstate, dtype, false))
         return fail(SSM_ERR_UNSUPPORTED, std::string(fn) + ": batch, seqlen, nheads or headdim too large");
     const size_t es = esize(dtype);
     const bool work = batch > 0 && seqlen > 0;
@@ -1403,7 +1409,7 @@ ssm_status_t ssm_delta_scan_bwd(const void* q, int64_t q_row, const void* k, int
     const char* fn = "ssm_delta_scan_bwd";
     ssm_status_t st = check_delta_dims(fn, batch, seqlen, nheads, headdim, ngroups, dstate, scale, dtype);
     if (st != SSM_OK) return st;
-    if (!delta_sizes_fit(batch, seqlen, nheads, headdim))
+    if (!delta_rows_fit(batch, seqlen, nheads, headdim, ngroups, dstate, dtype, true))
         return fail(SSM_ERR_UNSUPPORTED, std::string(fn) + ": batch, seqlen, nheads or headdim too large");
     const size_t es = esize(dtype);
     const bool work = batch > 0 && seqlen > 0;

@@ -656,6 +656,8 @@ struct DeltaSaved {
 hipError_t launch_delta_walk_saved(const DeltaArgs& a, const DeltaSaved& s, ssm_dtype_t dtype, hipStream_t stream);
 // the gradients of the states after the segments
 hipError_t launch_delta_join_back(const DeltaArgs& a, ssm_dtype_t dtype, hipStream_t stream);
+// of sizes whose products stay within 63 bits
+bool delta_launches_fit(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N, ssm_dtype_t dtype, bool bwd);
 size_t delta_fwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N, ssm_dtype_t dtype);
 size_t delta_bwd_workspace_bytes(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N, ssm_dtype_t dtype);
 hipError_t launch_delta_fwd(DeltaArgs a, void* workspace, ssm_dtype_t dtype, hipStream_t stream);

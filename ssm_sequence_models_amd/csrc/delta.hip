@@ -596,7 +596,7 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaStep s, int64_t un
     using S = typename D::T;
     const DeltaArgs& a = s.a;
     const int lane = threadIdx.x & 63, l8 = lane & 7;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+    const int64_t unit = long_block() * 4 + (threadIdx.x >> 6);
     if (unit >= units) return;
     const int64_t slabs = (a.P + 8 * RG - 1) / (8 * RG);
     const int64_t slab = unit % slabs, bh = unit / slabs, h = bh % a.H, b = bh / a.H, g = h / (a.H / a.G);
@@ -677,7 +677,7 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaStep s, int64_t un
 template <class D, int NI, int RG>
 hipError_t step_of(const DeltaStep& s, hipStream_t stream) {
     const int64_t units = s.a.B * s.a.H * ((s.a.P + 8 * RG - 1) / (8 * RG));
-    delta_step_kernel<D, NI, RG><<<static_cast<unsigned>((units + 3) / 4), 256, 0, stream>>>(s, units);
+    delta_step_kernel<D, NI, RG><<<long_grid((units + 3) / 4), 256, 0, stream>>>(s, units);
     return hipGetLastError();
 }
 template <class D>
@@ -688,12 +688,17 @@ hipError_t step_by_width(const DeltaStep& s, hipStream_t stream) {
     return step_of<D, 8, 2>(s, stream);
 }
 
-template <class MM, int NT>
-void prep_of(const DeltaArgs& a, bool bwd, hipStream_t stream) {
-    // a key head's heads share the products: up to one a wavefront, as long as the blocks fill the GPU (fewer:
-    // 1024 tokens of 32 heads of 8 x 128 x 128 forward 77 us, 69 with a head a block)
+// a key head's heads share the products of prep: up to one a wavefront, as long as the blocks fill the GPU (fewer:
+// 1024 tokens of 32 heads of 8 x 128 x 128 forward 77 us, 69 with a head a block)
+template <class MM>
+int prep_heads(const DeltaArgs& a) {
     int heads = 1;
     while (2 * heads <= MM::Q / 16 && a.H / a.G % (2 * heads) == 0 && a.B * a.chunks * a.H / (2 * heads) >= 1024) heads *= 2;
+    return heads;
+}
+template <class MM, int NT>
+void prep_of(const DeltaArgs& a, bool bwd, hipStream_t stream) {
+    const int heads = prep_heads<MM>(a);
     const unsigned blocks = static_cast<unsigned>(a.B * a.chunks * (a.H / heads));
     if (bwd && a.direct) delta_prep_kernel<MM, NT, true, true><<<blocks, MM::Q * 4, 0, stream>>>(a, heads);
     else if (bwd) delta_prep_kernel<MM, NT, true, false><<<blocks, MM::Q * 4, 0, stream>>>(a, heads);
@@ -746,7 +751,27 @@ hipError_t fwd_of(DeltaArgs a, void* workspace, hipStream_t stream) {
     return walk_by_width<MM, false>(a, DeltaSaved{}, stream);
 }
 
+// whether each launch has less than 2^32 threads
+template <class MM>
+bool launches_fit(DeltaArgs a, bool bwd) {
+    place_chunks<MM>(a, nullptr, bwd);
+    const int64_t most = int64_t{1} << 32, walk = (a.P + 63) / 64 + (a.segs > 1 ? (a.N + 63) / 64 : 0);
+    return a.B * a.chunks * (a.H / prep_heads<MM>(a)) < most / (MM::Q * 4) && a.B * a.H * a.segs * walk < most / 320 &&
+           (!bwd || a.B * a.chunks * a.G < most / 512);
+}
+
 }  // namespace
+
+bool delta_launches_fit(int64_t B, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N, ssm_dtype_t dtype, bool bwd) {
+    DeltaArgs a{};
+    a.B = B;
+    a.L = L;
+    a.H = H;
+    a.P = P;
+    a.G = G;
+    a.N = N;
+    return dtype == SSM_BF16 ? launches_fit<ByBf16>(a, bwd) : launches_fit<ByF32>(a, bwd);
+}
 
 hipError_t launch_delta_walk_saved(const DeltaArgs& a, const DeltaSaved& s, ssm_dtype_t dtype, hipStream_t stream) {
     return dtype == SSM_BF16 ? walk_by_width<ByBf16, true>(a, s, stream) : walk_by_width<ByF32, true>(a, s, stream);

@@ -258,6 +258,13 @@ struct NormCall {
 int64_t norm_partial_rows(int64_t rows, int64_t channels, int64_t groups);
 hipError_t launch_norm_fwd(const NormCall& c, hipStream_t stream);
 hipError_t launch_norm_bwd(const NormCall& c, hipStream_t stream);
+// A grid for any number of blocks of up to 1024 threads (a launch's first dimension holds less than 2^32 threads);
+// its blocks go by long_block, those past the end return.
+inline dim3 long_grid(int64_t blocks) {
+    const int64_t x = blocks < (int64_t{1} << 21) ? blocks : int64_t{1} << 21;
+    return dim3(static_cast<unsigned>(x), static_cast<unsigned>((blocks + x - 1) / x));
+}
+__device__ __forceinline__ int64_t long_block() { return static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x; }
 // norm of the heads of queries (0) and keys (1) with the rotation by position
 struct QkNormCall {
     const void* x[2];

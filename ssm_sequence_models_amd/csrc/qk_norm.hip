@@ -249,7 +249,8 @@ __global__ __launch_bounds__(kThreads) void qk_norm_fwd_kernel(QkNormCall c, int
     using L = Lane<D, ROT>;
     constexpr int V = L::V;
     __shared__ __attribute__((aligned(16))) float2 cs[kMostTokens * 128];
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * tokens;
+    const int64_t first = long_block() * tokens;
+    if (first >= c.tokens) return;
     if (c.tokens - first < tokens) tokens = static_cast<int>(c.tokens - first);
     if (c.R) {
         angles(c, cs, first, tokens);
@@ -414,7 +415,7 @@ template <class D, int LPH, int ROT>
 void run(const QkNormCall& c, bool bwd, hipStream_t s) {
     const int n = tokens_a_block(c.tokens, bwd);
     if (bwd) qk_norm_bwd_kernel<D, LPH, ROT><<<static_cast<unsigned>(qk_norm_partial_rows(c.tokens)), kThreads, 0, s>>>(c, n);
-    else qk_norm_fwd_kernel<D, LPH, ROT><<<static_cast<unsigned>((c.tokens + n - 1) / n), kThreads, 0, s>>>(c, n);
+    else qk_norm_fwd_kernel<D, LPH, ROT><<<long_grid((c.tokens + n - 1) / n), kThreads, 0, s>>>(c, n);
 }
 template <class D, int LPH>
 hipError_t by_rotation(const QkNormCall& c, bool bwd, hipStream_t s) {
