@@ -528,11 +528,11 @@ __device__ __forceinline__ void keep_in_range(f4 (&row)[NT], int& power) {
     for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) most = fmaxf(most, fabsf(row[i][e]));
+    if (!__any(most >= 2.0f || power > 0)) return;
     most = fmaxf(most, __shfl_xor(most, 16));
     most = fmaxf(most, __shfl_xor(most, 32));
     // (a row that is 0 or not finite stays as it is)
     const int want = most > 0.0f && most < __builtin_inff() ? max(power + __builtin_amdgcn_frexp_expf(most) - 1, 0) : power;
-    if (__all(want == power)) return;
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll

@@ -518,9 +518,9 @@ __global__ __launch_bounds__(64 * NT) void delta_join_states_kernel(DeltaArgs a)
     const auto load = [&](int i, f4 (&ph)[NT], f4& gn, int& pw) {
         if (i + 1 >= segs) return;
         const int64_t at = bh * segs + s0 + step * i;
-        pw = n < N ? a.power[at * N + n] : 0;
         const Buffer r = buffer(a.phi + at * N * N, static_cast<int64_t>(N) * N * 4);
         const Buffer rg = buffer(a.gain + at * P * N, static_cast<int64_t>(P) * N * 4);
+        pw = __builtin_amdgcn_raw_buffer_load_b32(buffer(a.power + at * N, N * 4), 4 * n, 0, 0);
 #pragma unroll
         for (int kk = 0; kk < NT; ++kk) {
             const int m = 16 * kk + 4 * g4;
