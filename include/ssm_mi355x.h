@@ -530,7 +530,9 @@ ssm_status_t ssm_gated_scan_step(const void* x, int64_t x_row, const void* gate,
  *   initial_state, final_state, dfinal_state, dinitial_state   [batch, nheads, headdim, dstate] fp32,
  *                  16-byte aligned, or NULL (zeros / not written)
  *   seq_idx        [batch, seqlen] int32, or NULL
- *   workspace      ..._workspace_size bytes, 256-byte aligned
+ *   workspace      ..._workspace_size bytes, 256-byte aligned (4 x 8192 tokens x 32 heads x 128 x 128 in
+ *                  bf16: 0.62 GB forward; 4.24 GB backward, of them the states and their gradients
+ *                  before each chunk, 2.1, and T and M, 0.9)
  * dstate a multiple of 4, at most 256; any headdim.  States and sums in fp32 (sums of gates in 64
  * bits), products of operands that hold 24 bits in either dtype; outputs rounded once.
  * Deterministic.  A NaN or infinity reaches, forward, its own sequence only:

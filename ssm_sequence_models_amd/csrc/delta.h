@@ -594,7 +594,8 @@ inline bool direct_rows_fit(const void* p, int64_t row, int64_t width, size_t es
 // Rows are cut into segments where their walks do not fill the 256 CUs: all segments from zero, with the
 // N unit rows as further channels that give what a segment makes of the state before it; the states
 // before the segments from those; then the walk proper, all segments side by side.  The cut is the
-// one with the smallest sum of its walks' rounds, in units fitted to calls of 512 to 32845 tokens: a chunk
+// one with the smallest sum of its walks' rounds, in units fitted to calls in bf16 of 512 to 32845 tokens, dstate 64
+// and 128 (a choice between cuts, not microseconds; fp32 and other widths take it as it is): a chunk
 // 2.5 uncut, 2.0 (from zero) and 2.9 forward; 5.7 uncut, 2.0 (from zero) and 8.7 (three walks) backward; 2 a
 // segment and walk for the states between, 10 a direction for the launches.  (bf16, 1024 tokens of 8 heads x
 // 64 x 128 backward: 131 us cut, 166 uncut; of 8 rows of 4 heads forward: 70 us cut, 65 uncut.)

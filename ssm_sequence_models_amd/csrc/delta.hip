@@ -22,10 +22,10 @@ using namespace delta;
 // products' operands where they lie.  (A product form of the inverse, (I - D)(I + D^2) .., loses
 // everything where keys repeat: the powers of D grow as binomials while T itself stays small.)
 // The heads of a key head go through the products once, up to a wavefront's worth of them a block (4 x 8192 x
-// 32 heads of 16 key heads, dstate 128: 242 us a head a block, 180 so; for the backward 300 and 235).  What
+// 32 heads of 16 key heads, dstate 128: 195 to 220 us, backward 240 to 250; a head a block took 62 and 65 more).  What
 // bounds it: the chain of a row's substitution and its syncs at four wavefronts a SIMD (vector instructions busy
-// half of the time, matrix ones a tenth), and 0.52 GB of images written (backward 0.93).  (Six wavefronts a
-// SIMD: spills, 273.)
+// half of the time, matrix ones a tenth), and 0.62 GB of images written (backward 0.93).  (Six wavefronts a
+// SIMD: spills, slower.)
 // ---------------------------------------------------------------------------------------
 template <class MM, int NT, bool BWD, bool DIRECT>
 __global__ __launch_bounds__(MM::Q * 4, NT <= 8 ? 4 : 1) void delta_prep_kernel(DeltaArgs a, int heads) {
@@ -239,11 +239,12 @@ __global__ __launch_bounds__(MM::Q * 4, NT <= 8 ? 4 : 1) void delta_prep_kernel(
 // The walk: 16 channels of a head a wavefront, four such wavefronts a block, and a fifth that moves memory:
 // the next chunk's K, Q, T, M, factors and values straight into the other half of LDS (one half only
 // where dstate is over 128), and the last chunk's y out of it.  (Fetched by the four themselves, the
-// loads' issue was a third of a chunk's time.)
+// loads' issue was a third of a chunk's time.)  A chunk's y goes into its values' place in LDS, which the fifth
+// empties before the next values come; with one half, where LDS has room, into a place of its own.
 // A block has all of a CU's LDS, so a SIMD has one of the four: the chain of a chunk's five products is what
-// bounds the walk (matrix instructions busy 45 % of it, vector ones 47 %, splits and scalings; 3.7 to 4.9 us a
-// chunk by the clock).  4 x 8192 x 32 heads x 128 x 128, bf16, 256 blocks of 128 chunks: 470 to 630 us.  As kSave
-// 525, 29 % and 37 %: it moves 2.3 GB, half of them the states, at 4.4 TB/s.
+// bounds the walk (matrix instructions busy 45 % of it, vector ones 47 %, splits and scalings; 4.0 to 5.0 us a
+// chunk by the clock).  4 x 8192 x 32 heads x 128 x 128, bf16, 256 blocks of 128 chunks: 510 to 645 us.  As kSave
+// 510 to 530, 29 % and 36 %: it moves 2.3 GB, half of them the states, at 4.4 TB/s.
 // kSave: for the backward, the states and E in place of y.  kSpan: a segment from zero, and behind the
 // channels the N unit rows without values; only the state after it.
 // DIRECT: see DeltaArgs; without it tokens pass through registers
@@ -489,8 +490,7 @@ __global__ __launch_bounds__(320, NT <= 4 && (MODE == kSpan || (MODE == kSave &&
 // The states before the segments, h = h phi + gain from the first on (BACK: the gradients after them,
 // g = g phi^T + gain from the last on), with the powers of phi's rows m put to h (BACK: to the product): 16 channels of a head a block, a wavefront 16 columns a
 // product of the fp32 instruction, the next segments' phi and gain loaded meanwhile.
-// 2 us a segment at dstate 128, 1.1 at 64 (one segment's loads ahead, and the starts read by the way: 4.3
-// and 2.9).
+// 2.1 us a segment at dstate 128, 1.1 at 64 (one segment's loads ahead, and the starts read by the way: twice that).
 // ---------------------------------------------------------------------------------------
 template <int Q, int NT, bool BACK>
 __global__ __launch_bounds__(64 * NT) void delta_join_states_kernel(DeltaArgs a) {

@@ -46,7 +46,7 @@ __device__ __forceinline__ f4 row4(const float* p) { return lds<f4>(reinterpret_
 // that use them (LDS is full).
 // Bound by the chain of a chunk's products with one such wavefront a SIMD (matrix instructions busy 24 % of it,
 // vector ones 32 %) and by the 3.4 GB that it moves, dh and dZ out, E and the images of T and M in, at 4.2 TB/s:
-// 4 x 8192 x 32 heads x 128 x 128, bf16, 790 to 870 us for 128 chunks.
+// 4 x 8192 x 32 heads x 128 x 128, bf16, 800 to 840 us for 128 chunks.
 template <class MM, int NT>
 struct BackLds {
     static constexpr int W = 16 * NT, HALVES = NT <= 8 ? 2 : 1;
@@ -265,10 +265,11 @@ __global__ __launch_bounds__(320) void delta_back_kernel(DeltaArgs a, Buffers u)
 // through LDS in blocks of 64 channels; dQ and dK are summed over the heads of a key head in
 // accumulators.
 // fp32 operands go in three bf16 parts, which hold all of their 24 bits, or whole.
-// Bound by its waits and vector work: 1250 to 1400 us at 4 x 8192 x 32 heads of 16 key heads x 128 x 128, bf16 (matrix
-// instructions busy 23 %, vector ones 46 %; it moves 4.3 GB, h_0, dh, E and dZ the most of them, at 3.3 TB/s).
-// Four wavefronts a block: 1900.  LDS addresses are formed where they are used (`here`): kept over the loops
-// they cost 2650 us in spilled registers.
+// Bound by its waits and vector work: 1370 to 1470 us at 4 x 8192 x 32 heads of 16 key heads x 128 x 128, bf16 (matrix
+// instructions busy 25 %, vector ones 46 %; it moves 4.3 GB, h_0, dh, E and dZ the most of them, at 3.0 TB/s).  With
+// X, F, E and dh of dk in two parts, which lose what bf16's rounding does not hide where terms cancel, 1250 to 1400.
+// Four wavefronts a block: 1.3 times slower.  LDS addresses are formed where they are used (`here`): kept over the
+// loops they cost as much again in spilled registers.
 // ---------------------------------------------------------------------------------------
 template <class MM>
 __device__ __forceinline__ void store_values(typename MM::S* p, int n, const float (&v)[MM::R]) {
@@ -343,7 +344,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void delta_grad_kernel(DeltaArgs a
     const int64_t g = unit % a.G;
     unit /= a.G;
     const int64_t c = unit % a.chunks, b = unit / a.chunks;
-    const int64_t rep = a.H / a.G, ptiles = (a.P + 15) / 16;
+    const int64_t rep = a.H / a.G;
     const int64_t h1 = g * rep + (rep < (split + 1) * u.heads ? rep : (split + 1) * u.heads);
     const int valid = static_cast<int>(a.L - c * Q < Q ? a.L - c * Q : Q);
     const int N = static_cast<int>(a.N), P = static_cast<int>(a.P);
@@ -570,7 +571,6 @@ __global__ __launch_bounds__(64 * kGradWaves) void delta_grad_kernel(DeltaArgs a
             float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int j = 0; j < CT; ++j) {
-                const int n = 16 * (cg * CT + j) + li;
                 qo[i][j] *= f * a.scale;
                 ko[i][j] *= -f;
                 if (several) {
@@ -757,9 +757,9 @@ __global__ __launch_bounds__(256) void delta_join_kernel(DeltaArgs a, Buffers u)
 }
 
 // Ranges of a key head's heads where key heads and chunks alone leave CUs idle; they cost a pass over their partial
-// sums.  The whole backward: 256 tokens of 16 heads of one key head x 64 x 64 64 us (unsplit 185), 1024 of 32 heads of
-// 8 x 128 x 128 202 (unsplit 215; in blocks for twice the CUs 218), 2 x 4096 of 8 of 2 x 64 x 128, 256 blocks unsplit,
-// 277 (split 301).
+// sums.  The whole backward, with the pairs in two parts: 256 tokens of 16 heads of one key head x 64 x 64 64 us
+// (unsplit 185), 1024 of 32 heads of 8 x 128 x 128 202 (unsplit 215; in blocks for twice the CUs 218), 2 x 4096 of 8 of
+// 2 x 64 x 128, 256 blocks unsplit, 277 (split 301).
 void split_heads(const DeltaArgs& a, Buffers& u) {
     const int64_t rep = a.H / a.G, blocks = a.B * a.chunks * a.G;
     int64_t splits = (256 + blocks - 1) / blocks;

@@ -13,9 +13,10 @@
 // An angle is a product in double, its whole turns taken off there: positions of any int32 size
 // keep the accuracy of position 0.
 //
-// 4 x 8192 tokens x 32 heads x 128 bf16, rotation 64, weights: forward 102 to 108 us (0.54 GB, 5.1 TB/s), backward
-// 157 + 5 (0.81 GB, 5.1 TB/s).  Without the rotation's layout as a template and the next head's loads in flight these
-// were 177 and 231.  Up to 8 tokens a block (16: no gain; streaming stores: none either).
+// 4 x 8192 tokens x 32 heads x 128 bf16, rotation 64, weights: forward 105 us (0.54 GB, 5.1 TB/s), backward 153 to
+// 158 + 5 (0.81 GB, 5.2 TB/s).  Without the rotation's layout as a template and the next head's loads in flight these
+// were 177 and 231.  In fp32, 128 channels: 213 and 315 (5.0 and 5.1 TB/s).  Layouts of the rotation outside whole
+// pieces go channel by channel: 16 + 16 heads x 80, rotation 40, bf16 322 us and 417 (1.0 and 1.2 TB/s).  Up to 8 tokens a block (16: no gain; streaming stores: none either).
 #include "internal.h"
 
 namespace ssm {
